@@ -1,0 +1,448 @@
+// Appending to the paged 8-bit KV cache, and the bookkeeping of its pages:
+// forking, freeing and compacting sequences.
+//
+// A step's accepted rows (the lookahead window's winners, "The Verification
+// Branch" of the paper-graph-ui page, section 3.4) enter the cache here as
+// e4m3 bytes; the pages say nothing of 8-bit or paged caches.
+#include <algorithm>
+
+#include "kv8.h"
+
+namespace la {
+
+// ------------------------------------------------------------------ scans
+// Exclusive prefix of v over the block in thread order; the block's sum in *tot.
+__device__ __forceinline__ int block_scan(int v, int *warp_tot, int *tot) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_tot[w] = incl;
+    __syncthreads();
+    if (w == 0) {
+        int x = lane < nw ? warp_tot[lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        warp_tot[lane] = x;
+    }
+    __syncthreads();
+    *tot = warp_tot[nw - 1];
+    const int r = incl - v + (w ? warp_tot[w - 1] : 0);
+    __syncthreads();
+    return r;
+}
+
+// ------------------------------------------------------------------ append: pages
+constexpr int kPlanThreads = 1024;
+
+// One CTA decides for every sequence which pages its new rows need, before
+// any byte moves.  Whether a page is free or shared is taken from refs as
+// they stand at the start, so a page that one sequence copies away from is
+// neither written nor handed out again within the call, and the answer does
+// not depend on the order in which threads run.
+//   ws: take[n_seqs] pages wanted (bit 30: the last page is copied),
+//       base[n_seqs] first of them in the list, src[n_seqs] page that holds
+//       the stored tokens of the first touched page, list[] free pages.
+__global__ void __launch_bounds__(kPlanThreads) k_kv8_plan(la_kv8_cache c, const int *row_start, int n_rows,
+                                                           int max_rows, int *stored, int *ws) {
+    pdl_trigger();
+    pdl_wait();
+    constexpr int kCopy = 1 << 30;
+    __shared__ int warp_tot[32];
+    int *take = ws, *base = ws + c.n_seqs, *src = ws + 2 * c.n_seqs, *list = ws + 3 * c.n_seqs;
+    const int tid = threadIdx.x;
+    // What each sequence wants; base: its place in the list if all fit.
+    int wanted = 0;
+    for (int s0 = 0; s0 < c.n_seqs; s0 += kPlanThreads) {
+        const int s = s0 + tid;
+        int need = 0, copy = 0;
+        if (s < c.n_seqs) {
+            int first, from = -1;
+            int n = kv8_rows(c, row_start, n_rows, s, &first);
+            const int len = kv8_len(c, s);
+            if (n > max_rows || (c.lens[s] != len)) {
+                atomicOr(c.status, LA_KV8_BAD);
+                n = 0;
+            }
+            if (n > 0) {
+                const long long held = (len + c.page - 1) / c.page, want = (static_cast<long long>(len) + n + c.page - 1) / c.page;
+                if (want > c.max_pages) {
+                    atomicOr(c.status, LA_KV8_FULL);
+                    n = 0;
+                } else {
+                    need = static_cast<int>(want - held);
+                    if (len % c.page) {
+                        from = kv8_page(c, s, len / c.page);
+                        if (from < 0) n = need = 0;
+                        else if (c.refs[from] > 1) copy = 1;
+                    }
+                }
+            }
+            stored[s] = n;
+            src[s] = from;
+        }
+        int tot;
+        const int at = block_scan(need + copy, warp_tot, &tot);
+        if (s < c.n_seqs) {
+            take[s] = (need + copy) | (copy ? kCopy : 0);
+            base[s] = wanted + at;
+        }
+        wanted += tot;
+    }
+    // The lowest free pages, as many as are wanted.
+    int found = 0;
+    for (int p0 = 0; p0 < c.n_pages && found < wanted; p0 += 4 * kPlanThreads) {
+        int free4 = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int p = p0 + 4 * tid + i;
+            if (p < c.n_pages && c.refs[p] == 0) free4 |= 1 << i;
+        }
+        int tot;
+        int at = found + block_scan(__popc(free4), warp_tot, &tot);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((free4 >> i) & 1) {
+                if (at < wanted) list[at] = p0 + 4 * tid + i;
+                ++at;
+            }
+        found += tot;
+    }
+    __syncthreads();
+    // Too few: in the order of the slots, those that still fit.
+    if (found < wanted && tid == 0) {
+        int used = 0;
+        for (int s = 0; s < c.n_seqs; ++s) {
+            const int t = take[s] & ~kCopy;
+            if (!stored[s]) continue;
+            if (t > found - used) {
+                stored[s] = 0;
+                atomicOr(c.status, LA_KV8_FULL);
+                continue;
+            }
+            base[s] = used;
+            used += t;
+        }
+    }
+    __syncthreads();
+    // Table, references and lengths: one warp per sequence.
+    const int lane = tid & 31;
+    for (int s = tid >> 5; s < c.n_seqs; s += kPlanThreads / 32) {
+        const int n = stored[s];
+        if (!n) continue;
+        const int t = take[s] & ~kCopy, len = c.lens[s];
+        const bool copy = take[s] & kCopy;
+        const int begin = copy ? len / c.page : (len + c.page - 1) / c.page;
+        int *row = c.table + static_cast<long long>(s) * c.max_pages;
+        for (int i = lane; i < t; i += 32) {
+            const int p = list[base[s] + i];
+            row[begin + i] = p;
+            c.refs[p] = 1;
+        }
+        if (lane == 0) {
+            if (copy) atomicSub(&c.refs[src[s]], 1);
+            c.lens[s] = len + n;
+        }
+        __syncwarp();
+    }
+}
+
+// ------------------------------------------------------------------ append: bytes
+__device__ __forceinline__ int kv8_exponent(float amax) {
+    const unsigned b = __float_as_uint(amax);
+    const int e = static_cast<int>(b >> 23) - ((b & 0x7fffffu) <= 0x600000u ? 135 : 134);   // amax <= 448 * 2^e
+    return min(max(e, kKv8MinExp), kKv8MaxExp);
+}
+__device__ __forceinline__ int kv8_scale_exponent(float scale) {
+    const int e = static_cast<int>((__float_as_uint(scale) >> 23) & 255u) - 127;
+    return min(max(e, kKv8MinExp), kKv8MaxExp);
+}
+__device__ __forceinline__ float kv8_power(int e) { return __uint_as_float(static_cast<unsigned>(e + 127) << 23); }
+__device__ __forceinline__ bool finite_f(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+// Nearest e4m3 (ties to even); magnitudes past 448 clamp, NaN and infinities become NaN.
+__device__ __forceinline__ uint32_t kv8_byte(float x) {
+    return finite_f(x) ? static_cast<uint32_t>(__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3)) : 0x7fu;
+}
+__device__ __forceinline__ float kv8_value(uint32_t b) {
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(b), __NV_E4M3)));
+}
+// A stored byte at a scale 2^-shift of what it was, shift >= 0.
+__device__ __forceinline__ uint32_t kv8_shrink(uint32_t b, float f) {
+    return (b & 0x7fu) == 0x7fu ? b : kv8_byte(kv8_value(b) * f);
+}
+
+constexpr int kStoreThreads = 256;
+
+// One CTA per (sequence, touched page, KV head, layer, K or V): the page's
+// new rows go through shared memory once, for the largest magnitude and then
+// for the bytes (V is transposed on the way).
+template <int HD>
+__global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_kv8_rows r, const int *src, int touched) {
+    pdl_trigger();
+    pdl_wait();
+    __shared__ __align__(16) __nv_bfloat16 sm[128 * HD + 8 * 8];   // 8 elements more after every 16 rows: see V below
+    __shared__ float red[kStoreThreads / 32];
+    const int s = blockIdx.x / touched, j = blockIdx.x % touched;
+    const int head = blockIdx.y, layer = blockIdx.z >> 1, isv = blockIdx.z & 1;
+    const int n = r.stored[s];
+    if (n <= 0) return;
+    const int len = c.lens[s] - n;
+    const int pj = len / c.page + j;
+    const int a = j == 0 ? len % c.page : 0;                       // tokens of this page that are stored already
+    const long long left = static_cast<long long>(len) + n - static_cast<long long>(pj) * c.page;
+    if (left <= 0) return;
+    const int b = static_cast<int>(min(left, static_cast<long long>(c.page)));
+    const int to = kv8_page(c, s, pj), from = a > 0 ? src[s] : -1;
+    if (to < 0) return;
+    const int row0 = (r.row_start ? r.row_start[s] : s) + pj * c.page + a - len;
+    const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(isv ? r.v : r.k) +
+                             layer * (isv ? r.v_layer_stride : r.k_layer_stride) + static_cast<long long>(head) * HD;
+    const long long stride = isv ? r.v_stride : r.k_stride;
+    const int tid = threadIdx.x, n_src = r.n_src;
+    auto place = [](int t, int d) { return t * HD + (t >> 4) * 8 + d; };
+
+    float amax = 0.f;
+    constexpr int C = HD / 8;                                      // 16-byte pieces of a row
+    for (int i = tid; i < (b - a) * C; i += kStoreThreads) {
+        const int t = i / C, d = (i % C) * 8;
+        const int row = r.row_idx ? r.row_idx[row0 + t] : row0 + t;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (static_cast<unsigned>(row) < static_cast<unsigned>(n_src)) w = *reinterpret_cast<const uint4 *>(x + row * stride + d);
+        else atomicOr(c.status, LA_KV8_BAD);                       // stored as zeros
+        *reinterpret_cast<uint4 *>(sm + place(a + t, d)) = w;
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float lo = __uint_as_float(u[k] << 16), hi = __uint_as_float(u[k] & 0xffff0000u);
+            if (finite_f(lo)) amax = fmaxf(amax, fabsf(lo));
+            if (finite_f(hi)) amax = fmaxf(amax, fabsf(hi));
+        }
+    }
+    amax = warp_max(amax);
+    if ((tid & 31) == 0) red[tid >> 5] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kStoreThreads / 32; ++w) amax = fmaxf(amax, red[w]);
+
+    float *scales = isv ? c.v_scale : c.k_scale;
+    uint8_t *pool = static_cast<uint8_t *>(isv ? c.v : c.k);
+    const long long blk = kv8_block(c, layer, to, head), old = from >= 0 ? kv8_block(c, layer, from, head) : 0;
+    const int e_old = from >= 0 ? kv8_scale_exponent(scales[old]) : kKv8MinExp;
+    const int e = max(e_old, kv8_exponent(amax));
+    const long long bytes = static_cast<long long>(c.page) * HD;
+    uint8_t *out = pool + blk * bytes;
+    __syncthreads();                                               // every thread has read the old scale
+    if (tid == 0) scales[blk] = kv8_power(e);
+    // Stored tokens: in a new place, or at a grown scale.
+    if (from >= 0 && (e > e_old || from != to)) {
+        const uint8_t *was = pool + old * bytes;
+        const float f = kv8_power(e_old - e < -126 ? -126 : e_old - e);
+        for (int i = tid; i < a * HD; i += kStoreThreads) {
+            const int at = isv ? (i / a) * c.page + i % a : i;
+            out[at] = static_cast<uint8_t>(kv8_shrink(was[at], f));
+        }
+    }
+    // New tokens.
+    const float f = kv8_power(-e);
+    if (!isv) {
+        for (int i = tid; i < (b - a) * (HD / 16); i += kStoreThreads) {
+            const int t = a + i / (HD / 16), d = (i % (HD / 16)) * 16;
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                w[k] = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[k] |= kv8_byte(__bfloat162float(sm[place(t, d + 4 * k + q)]) * f) << (8 * q);
+            }
+            *reinterpret_cast<uint4 *>(out + static_cast<long long>(t) * HD + d) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+        // A warp writes 16-token pieces of neighbouring dims; the padding
+        // keeps its reads of one dim's tokens in different banks.
+        const int pieces = c.page / 16;
+        for (int i = tid; i < HD * pieces; i += kStoreThreads) {
+            const int d = i / pieces, t0 = (i % pieces) * 16;
+            uint8_t *dst = out + static_cast<long long>(d) * c.page + t0;
+            if (t0 >= a && t0 + 16 <= b) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    w[k] = 0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) w[k] |= kv8_byte(__bfloat162float(sm[place(t0 + 4 * k + q, d)]) * f) << (8 * q);
+                }
+                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+                for (int t = max(t0, a); t < min(t0 + 16, b); ++t)
+                    dst[t - t0] = static_cast<uint8_t>(kv8_byte(__bfloat162float(sm[place(t, d)]) * f));
+            }
+        }
+    }
+}
+
+cudaError_t kv8_append_launch(const la_kv8_cache &c, const la_kv8_rows &r, int *ws, cudaStream_t s) {
+    cudaError_t e = launch_k(k_kv8_plan, dim3(1), dim3(kPlanThreads), 0, s, c, r.row_start, r.n_rows, r.max_rows, r.stored, ws);
+    if (e != cudaSuccess) return e;
+    const int touched = (r.max_rows - 1) / c.page + 2;
+    const dim3 grid(static_cast<unsigned>(c.n_seqs) * touched, c.n_kv_heads, 2 * c.n_layers);
+    const int *src = ws + 2 * c.n_seqs;
+    if (c.head_dim == 128) return launch_k(k_kv8_store<128>, grid, dim3(kStoreThreads), 0, s, c, r, src, touched);
+    return launch_k(k_kv8_store<64>, grid, dim3(kStoreThreads), 0, s, c, r, src, touched);
+}
+
+// ------------------------------------------------------------------ fork, free
+// One CTA per pair.  Pairs are judged by the call's start: a dst that is some
+// pair's src, or that an earlier pair names, is refused, so no CTA reads what
+// another writes but refs, which only grow, atomically.
+__global__ void __launch_bounds__(256) k_kv8_fork(la_kv8_cache c, const int *src, const int *dst, int n) {
+    pdl_trigger();
+    pdl_wait();
+    const int i = blockIdx.x, tid = threadIdx.x;
+    const int a = src[i], b = dst[i];
+    bool clash = false;
+    for (int k = tid; k < n; k += 256) clash |= src[k] == b || (k < i && dst[k] == b) || dst[k] == a;
+    clash = __syncthreads_or(clash);
+    const bool ok = !clash && static_cast<unsigned>(a) < static_cast<unsigned>(c.n_seqs) &&
+                    static_cast<unsigned>(b) < static_cast<unsigned>(c.n_seqs);
+    const int lb = ok ? c.lens[b] : 0;
+    const int len = ok ? kv8_len(c, a) : 0;
+    __syncthreads();                                               // lens[b] is read before it is written below
+    if (!ok || lb != 0 || len != c.lens[a]) {
+        if (tid == 0) atomicOr(c.status, LA_KV8_BAD);
+        return;
+    }
+    const int *ra = c.table + static_cast<long long>(a) * c.max_pages;
+    int *rb = c.table + static_cast<long long>(b) * c.max_pages;
+    for (int k = tid; k < c.max_pages; k += 256) {
+        const int p = ra[k];
+        const bool real = static_cast<unsigned>(p) < static_cast<unsigned>(c.n_pages);
+        if (real) atomicAdd(&c.refs[p], 1);
+        rb[k] = real ? p : -1;
+    }
+    if (tid == 0) c.lens[b] = len;
+}
+
+// One CTA per entry of slots.  The exchange gives each table entry to one CTA,
+// so a slot that occurs twice loses every reference once.
+__global__ void __launch_bounds__(256) k_kv8_free(la_kv8_cache c, const int *slots, const int *keep) {
+    pdl_trigger();
+    pdl_wait();
+    const int s = slots[blockIdx.x], tid = threadIdx.x;
+    if (static_cast<unsigned>(s) >= static_cast<unsigned>(c.n_seqs)) {
+        if (tid == 0) atomicOr(c.status, LA_KV8_BAD);
+        return;
+    }
+    const int k = keep ? max(keep[blockIdx.x], 0) : 0;
+    int *row = c.table + static_cast<long long>(s) * c.max_pages;
+    const int first = k / c.page + (k % c.page ? 1 : 0);
+    for (int j = first + tid; j < c.max_pages; j += 256) {
+        const int p = atomicExch(&row[j], -1);
+        if (static_cast<unsigned>(p) < static_cast<unsigned>(c.n_pages)) atomicSub(&c.refs[p], 1);
+    }
+    if (tid == 0) atomicMin(&c.lens[s], k);
+}
+
+cudaError_t kv8_fork_launch(const la_kv8_cache &c, const int *src, const int *dst, int n, cudaStream_t s) {
+    return n > 0 ? launch_k(k_kv8_fork, dim3(n), dim3(256), 0, s, c, src, dst, n) : cudaSuccess;
+}
+cudaError_t kv8_free_launch(const la_kv8_cache &c, const int *slots, const int *keep, int n, cudaStream_t s) {
+    return n > 0 ? launch_k(k_kv8_free, dim3(n), dim3(256), 0, s, c, slots, keep) : cudaSuccess;
+}
+
+// ------------------------------------------------------------------ compact
+// One CTA counts the used pages and pairs the used ones above that count with
+// the free ones below it, in ascending order.
+//   ws: [0] pairs, [1] used pages, then src[n_pages], dst[n_pages] and
+//       count[n_pages] (references) of the pairs, ascending, and to[n_pages],
+//       the new number of each used page.
+__global__ void __launch_bounds__(kPlanThreads) k_kv8_pair(la_kv8_cache c, int *n_live, int *ws) {
+    pdl_trigger();
+    pdl_wait();
+    __shared__ int warp_tot[32];
+    const int tid = threadIdx.x;
+    int *src = ws + 4, *dst = src + c.n_pages, *count = dst + c.n_pages, *to = count + c.n_pages;
+    int live = 0;
+    for (int p0 = 0; p0 < c.n_pages; p0 += kPlanThreads) {
+        const int p = p0 + tid;
+        int tot;
+        block_scan(p < c.n_pages && c.refs[p] > 0, warp_tot, &tot);
+        live += tot;
+    }
+    int holes = 0, movers = 0;
+    for (int p0 = 0; p0 < c.n_pages; p0 += kPlanThreads) {
+        const int p = p0 + tid;
+        const bool in = p < c.n_pages, used = in && c.refs[p] > 0;
+        const bool hole = in && !used && p < live, mover = used && p >= live;
+        int tot;                                                   // a chunk's holes and movers in one scan of two halves
+        const int at = block_scan((hole ? 1 : 0) | (mover ? 1 << 16 : 0), warp_tot, &tot);
+        if (hole) dst[holes + (at & 0xffff)] = p;
+        if (mover) {
+            src[movers + (at >> 16)] = p;
+            count[movers + (at >> 16)] = c.refs[p];
+        }
+        if (in) to[p] = p;
+        holes += tot & 0xffff;
+        movers += tot >> 16;
+    }
+    __syncthreads();
+    for (int i = tid; i < movers; i += kPlanThreads) to[src[i]] = dst[i];
+    if (tid == 0) {
+        ws[0] = movers;
+        ws[1] = live;
+        if (n_live) *n_live = live;
+    }
+}
+
+constexpr int kMoveThreads = 256;
+
+// Copies the pairs' pages, layer by layer, and rewrites the table and refs.
+// A (layer, page)'s K (or V) is one run of n_kv_heads * page * head_dim bytes.
+__global__ void __launch_bounds__(kMoveThreads) k_kv8_move(la_kv8_cache c, int *table_out, int *refs_out, const int *ws) {
+    pdl_trigger();
+    pdl_wait();
+    const int movers = ws[0], live = ws[1];
+    const int *src = ws + 4, *dst = src + c.n_pages, *count = dst + c.n_pages, *to = count + c.n_pages;
+    const long long thread = static_cast<long long>(blockIdx.x) * kMoveThreads + threadIdx.x;
+    const long long threads = static_cast<long long>(gridDim.x) * kMoveThreads;
+    const long long cells = static_cast<long long>(c.n_seqs) * c.max_pages;
+    for (long long i = thread; i < cells; i += threads) {
+        const int p = c.table[i];
+        table_out[i] = static_cast<unsigned>(p) < static_cast<unsigned>(c.n_pages) ? to[p] : -1;
+    }
+    // refs_out may be refs: a page moved into (0 there, or its new count
+    // already) and a page moved away from are told apart by number alone.
+    for (long long i = thread; i < c.n_pages; i += threads) {
+        const int n = c.refs[i];
+        if (i >= live) refs_out[i] = 0;
+        else if (n > 0) refs_out[i] = n;
+    }
+    for (long long i = thread; i < movers; i += threads) refs_out[dst[i]] = count[i];
+    const int run = c.n_kv_heads * c.page * c.head_dim;            // bytes, a multiple of 2048
+    const long long items = 2ll * movers * c.n_layers;
+    for (long long i = blockIdx.x; i < items; i += gridDim.x) {
+        const int pair = static_cast<int>(i >> 1) % movers, layer = static_cast<int>((i >> 1) / movers);
+        uint8_t *pool = static_cast<uint8_t *>(i & 1 ? c.v : c.k);
+        float *scales = i & 1 ? c.v_scale : c.k_scale;
+        const long long a = kv8_block(c, layer, src[pair], 0), b = kv8_block(c, layer, dst[pair], 0);
+        const long long bytes = static_cast<long long>(c.page) * c.head_dim;
+        const uint4 *x = reinterpret_cast<const uint4 *>(pool + a * bytes);
+        uint4 *y = reinterpret_cast<uint4 *>(pool + b * bytes);
+        for (int k = threadIdx.x; k < run / 16; k += kMoveThreads) y[k] = x[k];
+        for (int k = threadIdx.x; k < c.n_kv_heads; k += kMoveThreads) scales[b + k] = scales[a + k];
+    }
+}
+
+cudaError_t kv8_compact_launch(const la_kv8_cache &c, int *table_out, int *refs_out, int *n_live, int *ws, int nsm,
+                               cudaStream_t s) {
+    cudaError_t e = launch_k(k_kv8_pair, dim3(1), dim3(kPlanThreads), 0, s, c, n_live, ws);
+    if (e != cudaSuccess) return e;
+    return launch_k(k_kv8_move, dim3(8 * nsm), dim3(kMoveThreads), 0, s, c, table_out, refs_out, ws);
+}
+
+}  // namespace la

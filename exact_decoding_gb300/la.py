@@ -70,6 +70,30 @@ class la_state_t(ctypes.Structure):
                 ("records", _I32P), ("uses", _I32P)]
 
 
+class la_kv8_cache(ctypes.Structure):
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("status", ctypes.c_void_p)]
+
+
+class la_kv8_attn(ctypes.Structure):
+    _fields_ = [("layer", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("n_rows", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32), ("max_len", ctypes.c_int32), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("row_start", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("vis", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("scale", ctypes.c_float)]
+
+
+class la_kv8_rows(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int32), ("n_src", ctypes.c_int32), ("max_rows", ctypes.c_int32),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("k_layer_stride", ctypes.c_int64),
+                ("v_layer_stride", ctypes.c_int64), ("row_start", ctypes.c_void_p), ("row_idx", ctypes.c_void_p),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("stored", ctypes.c_void_p)]
+
+
 def load_library():
     """Load libla.so; raises if it has not been built (no fallback exists)."""
     global _lib
@@ -99,6 +123,15 @@ def load_library():
                                    ctypes.POINTER(ctypes.c_uint32), _I32P, ctypes.c_int32, _I32P, _I32P]
     lib.la_gemm_schedule.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _I32P,
                                      ctypes.c_int32, _I32P, _I32P, _I32P, _I32P]
+    KV8 = ctypes.POINTER(la_kv8_cache)
+    lib.la_kv8_workspace.argtypes = [KV8, ctypes.POINTER(ctypes.c_int64)]
+    lib.la_kv8_attention.argtypes = [KV8, ctypes.POINTER(la_kv8_attn), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]
+    lib.la_kv8_append.argtypes = [KV8, ctypes.POINTER(la_kv8_rows), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]
+    lib.la_kv8_fork.argtypes = [KV8, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]
+    lib.la_kv8_free.argtypes = [KV8, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]
+    lib.la_kv8_compact.argtypes = [KV8, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                   ctypes.c_int64, ctypes.c_void_p]
+    lib.la_kv8_status.argtypes = [KV8, ctypes.POINTER(ctypes.c_uint32), ctypes.c_void_p]
     lib.la_destroy.argtypes = [H]
     lib.la_destroy.restype = None
     lib.la_strerror.argtypes = [ctypes.c_int]
@@ -107,7 +140,8 @@ def load_library():
     lib.la_last_error.restype = ctypes.c_char_p
     for name in ("la_create", "la_prefill", "la_step", "la_ar_step", "la_generate", "la_stats", "la_export_state",
                  "la_import_state", "la_debug_logits", "la_gemm_bf16", "la_gemm_bf16_noalloc", "la_gemm_status",
-                 "la_selftest_timeout", "la_gemm_schedule", "la_step_tables"):
+                 "la_selftest_timeout", "la_gemm_schedule", "la_step_tables", "la_kv8_workspace", "la_kv8_attention",
+                 "la_kv8_append", "la_kv8_fork", "la_kv8_free", "la_kv8_compact", "la_kv8_status"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -276,6 +310,43 @@ def la_gemm_schedule(tiles: int, n_kb: int, ctas: int, whole_first: bool):
         return segs[:nseg[0]].copy(), first[:used[0] + 1].copy(), planes
 
 
+def la_kv8_workspace(cache: la_kv8_cache) -> int:
+    n = ctypes.c_int64()
+    _check(load_library().la_kv8_workspace(cache, ctypes.byref(n)), "la_kv8_workspace")
+    return n.value
+
+
+def la_kv8_attention(cache: la_kv8_cache, args: la_kv8_attn, workspace_ptr: int, workspace_bytes: int,
+                     stream: Optional[int] = None) -> None:
+    _check(load_library().la_kv8_attention(cache, args, workspace_ptr, workspace_bytes, stream), "la_kv8_attention")
+
+
+def la_kv8_append(cache: la_kv8_cache, rows: la_kv8_rows, workspace_ptr: int, workspace_bytes: int,
+                  stream: Optional[int] = None) -> None:
+    _check(load_library().la_kv8_append(cache, rows, workspace_ptr, workspace_bytes, stream), "la_kv8_append")
+
+
+def la_kv8_fork(cache: la_kv8_cache, src_ptr: int, dst_ptr: int, n: int, stream: Optional[int] = None) -> None:
+    _check(load_library().la_kv8_fork(cache, src_ptr, dst_ptr, n, stream), "la_kv8_fork")
+
+
+def la_kv8_free(cache: la_kv8_cache, slots_ptr: int, keep_ptr: Optional[int], n: int,
+                stream: Optional[int] = None) -> None:
+    _check(load_library().la_kv8_free(cache, slots_ptr, keep_ptr, n, stream), "la_kv8_free")
+
+
+def la_kv8_compact(cache: la_kv8_cache, table_out_ptr: int, refs_out_ptr: int, n_live_ptr: Optional[int],
+                   workspace_ptr: int, workspace_bytes: int, stream: Optional[int] = None) -> None:
+    _check(load_library().la_kv8_compact(cache, table_out_ptr, refs_out_ptr, n_live_ptr, workspace_ptr, workspace_bytes,
+                                         stream), "la_kv8_compact")
+
+
+def la_kv8_status(cache: la_kv8_cache, stream: Optional[int] = None) -> None:
+    """Raise LaError if a call on this cache met no free page (-3), something
+    outside the cache (-6) or a wait that gave up (-5); clears the status."""
+    _check(load_library().la_kv8_status(cache, None, stream), "la_kv8_status")
+
+
 def la_destroy(h) -> None:
     if h:
         load_library().la_destroy(h)
@@ -318,6 +389,171 @@ class DeviceWeights:
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in self._keep if hasattr(t, "numel"))
+
+
+class Kv8Cache:
+    """A paged 8-bit KV cache (la_kv8_*): the pool, its scales, the sequences'
+    table and lengths, and a workspace, all as torch tensors on one device.
+
+    k, v        uint8 (e4m3) [layers, pages, kv heads, page, dim] and, V
+                transposed, [layers, pages, kv heads, dim, page]
+    k_scale, v_scale   float32 [layers, pages, kv heads], powers of two
+    table, lens, refs  int32 [seqs, max_pages], [seqs], [pages]
+
+    `tensors` adopts existing tensors by those names.  Calls run on `stream`
+    (default: torch's current stream of the cache's device) and do not
+    synchronise; status() does, and raises what they met.  Calls that overlap
+    (streams, captured graphs) need a `workspace` of their own (workspace())."""
+
+    def __init__(self, n_layers: int, n_pages: int, page: int, n_kv_heads: int, head_dim: int, n_seqs: int,
+                 max_pages: int, device="cuda", tensors: Optional[dict] = None):
+        import torch
+        self._torch = torch
+        tensors = dict(tensors or {})
+        given = next(iter(tensors.values()), None)
+        dev = torch.device(given.device if given is not None else device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+        pool = (n_layers, n_pages, n_kv_heads)
+        shapes = {"k": (*pool, page, head_dim), "v": (*pool, head_dim, page), "k_scale": pool, "v_scale": pool,
+                  "table": (n_seqs, max_pages), "lens": (n_seqs,), "refs": (n_pages,), "status": (1,)}
+        types = {"k": torch.uint8, "v": torch.uint8, "k_scale": torch.float32, "v_scale": torch.float32}
+        for name, shape in shapes.items():
+            t = tensors.pop(name, None)
+            if t is None:
+                t = torch.zeros(shape, dtype=types.get(name, torch.int32), device=dev)
+                if name == "table":
+                    t.fill_(-1)
+                elif name.endswith("scale"):
+                    t.fill_(1.0)
+            self._checked(t, name, types.get(name, torch.int32), shape)
+            setattr(self, "status_word" if name == "status" else name, t)
+        if tensors:
+            raise ValueError(f"unknown tensors: {sorted(tensors)}")
+        self.n_layers, self.n_pages, self.page, self.n_kv_heads = n_layers, n_pages, page, n_kv_heads
+        self.head_dim, self.n_seqs, self.max_pages = head_dim, n_seqs, max_pages
+        self.struct = la_kv8_cache(n_layers, n_pages, page, n_kv_heads, head_dim, n_seqs, max_pages,
+                                   *[getattr(self, "status_word" if n == "status" else n).data_ptr()
+                                     for n in shapes])
+        with torch.cuda.device(dev):
+            self._ws = self.workspace()
+        self._stored = torch.zeros(n_seqs, dtype=torch.int32, device=dev)
+        self._live = torch.zeros(1, dtype=torch.int32, device=dev)
+
+    def workspace(self):
+        """A workspace for calls that overlap with others on this cache."""
+        with self._torch.cuda.device(self.device):
+            return self._torch.empty(la_kv8_workspace(self.struct), dtype=self._torch.uint8, device=self.device)
+
+    # -------------------------------------------------------------- checks
+    def _checked(self, t, name, dtype, shape):
+        if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != self.device:
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {self.device}, not "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
+
+    def _ints(self, t, name, n):
+        """int32 device vector of n values, or None."""
+        return None if t is None else self._checked(t, name, self._torch.int32, (n,))
+
+    def _heads(self, t, name, heads, lead):
+        """bf16 [*lead, rows, heads, dim] with dense (heads, dim); returns rows, row stride."""
+        if t.dtype != self._torch.bfloat16 or t.device != self.device or t.dim() != lead + 3 or t.shape[-1] != self.head_dim \
+                or (heads and t.shape[-2] != heads) or t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != self.head_dim):
+            raise ValueError(f"{name} must be a bfloat16 tensor [{'layers, ' if lead else ''}rows, {heads or 'heads'}, "
+                             f"{self.head_dim}] on {self.device} with dense heads, not {t.dtype} {tuple(t.shape)} strides "
+                             f"{t.stride()} on {t.device}")
+        rows = t.shape[-3]
+        return rows, t.stride(-3) if rows > 1 else t.shape[-2] * self.head_dim
+
+    def _call(self, fn, *args, stream=None):
+        """fn(self.struct, *args, stream) with the cache's device current."""
+        cuda = self._torch.cuda
+        idx = self.device.index
+        if cuda.current_device() == idx:
+            fn(self.struct, *args, stream.cuda_stream if stream is not None else cuda.current_stream(idx).cuda_stream)
+        else:
+            with cuda.device(idx):
+                fn(self.struct, *args, stream.cuda_stream if stream is not None else cuda.current_stream(idx).cuda_stream)
+
+    # -------------------------------------------------------------- calls
+    def attention(self, q, k=None, v=None, row_start=None, layer: int = 0, vis=None, out=None, scale: float = 0.0,
+                  max_rows: int = 0, max_len: int = 0, workspace=None, stream=None):
+        """Attention of the rows q [rows, heads, dim] over their sequences'
+        cached tokens and the visible new rows k, v [rows, kv heads, dim];
+        see la_kv8_attention.  max_rows and max_len are bounds that the host
+        knows (0: none); they steer the split of the work only.  Returns out."""
+        rows, qs = self._heads(q, "q", 0, 0)
+        if out is None:
+            out = self._torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        n, os_ = self._heads(out, "out", q.shape[1], 0)
+        ks = vs = 0
+        kp = vp = None
+        if k is not None or v is not None:
+            if k is None or v is None:
+                raise ValueError("k and v come together")
+            nk, ks = self._heads(k, "k", self.n_kv_heads, 0)
+            nv, vs = self._heads(v, "v", self.n_kv_heads, 0)
+            if nk != rows or nv != rows:
+                raise ValueError(f"k and v must have q's {rows} rows, not {nk} and {nv}")
+            kp, vp = k.data_ptr(), v.data_ptr()
+        if n != rows:
+            raise ValueError(f"out must have q's {rows} rows, not {n}")
+        a = la_kv8_attn(layer, q.shape[1], rows, max_rows, max_len, qs, ks, vs, os_,
+                        self._ints(row_start, "row_start", self.n_seqs + 1), q.data_ptr(), kp, vp,
+                        None if vis is None else self._checked(vis, "vis", self._torch.int32, (rows, 8)), out.data_ptr(),
+                        scale)
+        ws = self._ws if workspace is None else workspace
+        self._call(la_kv8_attention, a, ws.data_ptr(), ws.numel() * ws.element_size(), stream=stream)
+        return out
+
+    def append(self, k, v, row_start=None, row_idx=None, stored=None, max_rows: int = 0, workspace=None, stream=None):
+        """Append the rows of k, v [layers, rows, kv heads, dim] (or the rows
+        row_idx of them) behind the sequences; see la_kv8_append.  Returns
+        stored [seqs], the rows stored for each sequence (without `stored`, a
+        tensor that the next append overwrites)."""
+        n, ks = self._heads(k, "k", self.n_kv_heads, 1)
+        nv, vs = self._heads(v, "v", self.n_kv_heads, 1)
+        if k.shape[0] != self.n_layers or v.shape[0] != self.n_layers or nv != n:
+            raise ValueError(f"k and v must be [{self.n_layers} layers, rows, ...], not {tuple(k.shape)} and {tuple(v.shape)}")
+        if row_idx is not None:
+            self._ints(row_idx, "row_idx", row_idx.numel())
+        stored = self._stored if stored is None else stored
+        r = la_kv8_rows(n if row_idx is None else row_idx.numel(), n, max_rows, ks, vs, k.stride(0), v.stride(0),
+                        self._ints(row_start, "row_start", self.n_seqs + 1),
+                        None if row_idx is None else row_idx.data_ptr(), k.data_ptr(), v.data_ptr(),
+                        self._ints(stored, "stored", self.n_seqs))
+        ws = self._ws if workspace is None else workspace
+        self._call(la_kv8_append, r, ws.data_ptr(), ws.numel() * ws.element_size(), stream=stream)
+        return stored
+
+    def fork(self, src, dst, stream=None) -> None:
+        """The empty slots dst continue the sequences src (int32 device vectors); see la_kv8_fork."""
+        self._call(la_kv8_fork, self._ints(src, "src", src.numel()), self._ints(dst, "dst", src.numel()), src.numel(),
+                   stream=stream)
+
+    def free(self, slots, keep=None, stream=None) -> None:
+        """Shorten the sequences in slots to keep tokens (None: 0); see la_kv8_free."""
+        self._call(la_kv8_free, self._ints(slots, "slots", slots.numel()), self._ints(keep, "keep", slots.numel()),
+                   slots.numel(), stream=stream)
+
+    def compact(self, table_out=None, refs_out=None, n_live=None, workspace=None, stream=None):
+        """Move the used pages to the pool's front; see la_kv8_compact.  The new
+        table and counts go to table_out, refs_out (default: in place).
+        Returns n_live, an int32 tensor with the number of used pages."""
+        table_out = self.table if table_out is None else table_out
+        refs_out = self.refs if refs_out is None else refs_out
+        n_live = self._live if n_live is None else n_live
+        ws = self._ws if workspace is None else workspace
+        self._call(la_kv8_compact, self._checked(table_out, "table_out", self._torch.int32, self.table.shape),
+                   self._ints(refs_out, "refs_out", self.n_pages), self._ints(n_live, "n_live", 1), ws.data_ptr(),
+                   ws.numel() * ws.element_size(), stream=stream)
+        return n_live
+
+    def status(self, stream=None) -> None:
+        """Wait for the stream and raise LaError for what earlier calls met; see la_kv8_status."""
+        self._call(la_kv8_status, stream=stream)
 
 
 class Decoder:

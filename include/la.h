@@ -342,6 +342,151 @@ int la_step_tables(int32_t N, int32_t W, int32_t G, int32_t *depth, uint32_t *vi
 int la_gemm_schedule(int32_t tiles, int32_t n_kb, int32_t ctas, int32_t whole_first, int32_t *segs,
                      int32_t max_segs, int32_t *nseg, int32_t *cta_first, int32_t *ctas_used, int32_t *planes);
 
+/* ------------------------------------------------------------------------
+ * Paged 8-bit KV cache.
+ *
+ * K and V of many sequences in pages of `page` tokens, one byte per element
+ * (e4m3: 4 exponent bits, 3 fraction bits, largest value 448), with one scale
+ * for each (layer, page, KV head) of K and of V: element = byte value * scale.
+ * Scales are powers of two.  A sequence is a slot: a row of page numbers in
+ * `table` and a length in `lens`; token p of slot s lies in page
+ * table[s][p / page] at offset p % page, in every layer.  A page may belong
+ * to several sequences (la_kv8_fork); refs counts the table entries that name
+ * it, and a page with refs 0 is free.  The caller owns all memory; before the
+ * first call table holds -1, and lens, refs and *status hold 0.
+ *
+ * All calls are asynchronous on their stream (cudaStream_t or NULL), allocate
+ * nothing and can be captured into a CUDA graph.  What only the device knows
+ * (no free page, a page number or slot outside the cache) sets a bit in
+ * *status, which la_kv8_status reads; such pages, slots and rows are skipped,
+ * never read.  Calls on one cache that change it must not overlap with any
+ * other call on it; la_kv8_attention calls may overlap with one another when
+ * each has a workspace of its own (that holds for captured graphs too).
+ * The pages name 8-bit caches nowhere: a library extension with no passage. */
+#define LA_KV8_MAX_SEQS 4096
+
+/* Bits of la_kv8_cache.status. */
+#define LA_KV8_FULL     1u   /* append: no free page or table entry left; that sequence's rows were not stored */
+#define LA_KV8_BAD      2u   /* a page number, slot, length or row outside the cache, or a refused fork; skipped */
+#define LA_KV8_TIMEOUT  4u   /* a bounded wait in the attention gave up; that call's output is void */
+
+typedef struct la_kv8_cache {
+    int32_t n_layers;
+    int32_t n_pages;      /* 1 .. 2^24 */
+    int32_t page;         /* tokens per page: 32, 64 or 128 */
+    int32_t n_kv_heads;
+    int32_t head_dim;     /* 64 or 128 */
+    int32_t n_seqs;       /* slots, 1 .. LA_KV8_MAX_SEQS */
+    int32_t max_pages;    /* table entries per slot */
+    void     *k;          /* device, e4m3 [n_layers][n_pages][n_kv_heads][page][head_dim], 16-byte aligned */
+    void     *v;          /* device, e4m3 [n_layers][n_pages][n_kv_heads][head_dim][page], 16-byte aligned */
+    float    *k_scale;    /* device [n_layers][n_pages][n_kv_heads] */
+    float    *v_scale;    /* device [n_layers][n_pages][n_kv_heads] */
+    int32_t  *table;      /* device [n_seqs][max_pages], page number or -1 */
+    int32_t  *lens;       /* device [n_seqs] tokens stored */
+    int32_t  *refs;       /* device [n_pages] */
+    uint32_t *status;     /* device [1] */
+} la_kv8_cache;
+
+/* New rows of every sequence: their queries, and their own K and V at 16 bits,
+ * which they attend to besides the cache.  Strides are in elements between
+ * consecutive rows, multiples of 8 and at least the row's width; q, k, v and
+ * out are 16-byte aligned (columns of one fused projection are fine). */
+typedef struct la_kv8_attn {
+    int32_t layer;
+    int32_t n_heads;          /* query heads, a multiple of n_kv_heads, at most 256 per KV head; head i reads KV head
+                                 i / (n_heads / n_kv_heads) */
+    int32_t n_rows;           /* rows of all sequences together */
+    int32_t max_rows;         /* most rows of one sequence (a hint: it picks the kernel, never the result); <= 0: n_rows */
+    int32_t max_len;          /* most tokens of one sequence (a hint likewise); <= 0: max_pages * page */
+    int64_t q_stride, k_stride, v_stride, out_stride;
+    const int32_t *row_start; /* device [n_seqs + 1]: slot s has rows row_start[s] .. row_start[s + 1] - 1, rising from
+                                 row_start[0] >= 0 to row_start[n_seqs] <= n_rows; NULL: n_rows == n_seqs, one row each.
+                                 Rows of no slot are left as they are */
+    const void *q;            /* device bf16 [n_rows][n_heads * head_dim] */
+    const void *k;            /* device bf16 [n_rows][n_kv_heads * head_dim], or NULL with v: rows see the cache alone */
+    const void *v;
+    const uint32_t *vis;      /* device [n_rows][8] or NULL.  Bit i % 32 of word i / 32: the row attends to row i of
+                                 its own sequence (rows past 255 are never seen); NULL: rows 0 .. itself */
+    void *out;                /* device bf16 [n_rows][n_heads * head_dim]; must not overlap the inputs */
+    float scale;              /* factor on q . k; 0: 1 / sqrt(head_dim) */
+} la_kv8_attn;
+
+/* Bytes of workspace that la_kv8_attention, la_kv8_append and la_kv8_compact
+ * need for this cache on the current device (16-byte aligned device memory,
+ * any contents; calls that overlap need one each).  Errors: INVALID_ARG, CUDA. */
+int la_kv8_workspace(const la_kv8_cache *c, int64_t *bytes);
+
+/* out[r] = sum over the keys j that row r sees of softmax_j(scale * q[r] . K_j) V_j,
+ * where the keys are the lens[s] cached tokens of its sequence and its visible
+ * new rows.  Sums and the softmax are fp32; the products' operands are fp16
+ * with power-of-two factors (e4m3 and bf16 values are exact in them, the
+ * softmax weights rounded to 11 bits); out is rounded once to bf16.  A row
+ * that sees nothing gives 0.  Values of keys that a row does not see, and
+ * bytes behind a sequence's last token, never reach it, NaN and infinities
+ * included.  Results do not depend on other sequences' contents but may
+ * differ in the last bits with the split of the keys (max_len, n_seqs).
+ * Errors: INVALID_ARG, UNSUPPORTED, CAPACITY (workspace too small), CUDA. */
+int la_kv8_attention(const la_kv8_cache *c, const la_kv8_attn *a, void *workspace, int64_t workspace_bytes,
+                     void *stream);
+
+/* Rows to append, all layers at once. */
+typedef struct la_kv8_rows {
+    int32_t n_rows;           /* entries of row_idx, or (row_idx NULL) rows of k and v */
+    int32_t n_src;            /* rows of k and v; <= 0: n_rows */
+    int32_t max_rows;         /* most rows of one sequence (a bound; rows past it are refused as BAD); <= 0: n_rows */
+    int64_t k_stride, v_stride;               /* elements between rows, multiples of 8 */
+    int64_t k_layer_stride, v_layer_stride;   /* elements between layers, multiples of 8 */
+    const int32_t *row_start; /* device [n_seqs + 1] as in la_kv8_attn, or NULL: one row for every slot */
+    const int32_t *row_idx;   /* device [n_rows] or NULL: appended row i is row row_idx[i] of k and v (the accepted
+                                 rows of a step, in order) */
+    const void *k;            /* device bf16 [n_layers][n_src][n_kv_heads * head_dim], 16-byte aligned */
+    const void *v;
+    int32_t *stored;          /* device [n_seqs]: rows stored for each slot (all of its rows, or 0) */
+} la_kv8_rows;
+
+/* Append rows behind the sequences' tokens and advance lens.  Pages come from
+ * the free ones, lowest number first, in the order of the slots; a partly
+ * filled last page that other entries name too is first replaced by a copy,
+ * so sharers never see the new rows.  The scale of a (layer, page, head) is
+ * 2^e with the least e in [-60, 60] for which every finite element is at most
+ * 448 * 2^e, and never less than the page had; stored tokens of a page whose
+ * scale grows are rounded again at the new scale (exact unless they become
+ * subnormal).  Elements are rounded to nearest even; beyond 448 * 2^60 they
+ * are clamped, and NaN and infinities are stored as NaN.  A sequence for which
+ * pages or table entries run out stores nothing (stored 0, LA_KV8_FULL); later
+ * ones may still fit.  Errors: INVALID_ARG, CAPACITY (workspace), CUDA. */
+int la_kv8_append(const la_kv8_cache *c, const la_kv8_rows *r, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Make slot dst[i] (empty) a continuation of slot src[i]: it names the same
+ * pages and has the same length.  No page is copied here.  src, dst: device
+ * int32[n].  A pair whose dst is not empty, occurs earlier in dst or is some
+ * pair's src is refused (LA_KV8_BAD).  Errors: INVALID_ARG, CUDA. */
+int la_kv8_fork(const la_kv8_cache *c, const int32_t *src, const int32_t *dst, int32_t n, void *stream);
+
+/* Shorten the sequences in slots[i] to their first keep[i] tokens (keep NULL:
+ * 0, the slot becomes empty; a keep past the length changes nothing) and drop
+ * their references to the pages behind them.  slots, keep: device int32[n];
+ * a slot may occur twice (the least keep counts).  Errors: INVALID_ARG, CUDA. */
+int la_kv8_free(const la_kv8_cache *c, const int32_t *slots, const int32_t *keep, int32_t n, void *stream);
+
+/* Move the pages in use into page numbers 0 .. *n_live - 1: each used page
+ * with a number >= the count of used pages moves (K, V and scales of every
+ * layer) into a free page below it, lowest into lowest.  table_out
+ * [n_seqs][max_pages] and refs_out [n_pages] (device) receive the new table
+ * and counts; they may be the cache's own.  Given other arrays, the old table
+ * and refs stay valid until the next append: the pages' old bytes are left in
+ * place.  n_live: device int32[1] or NULL.  Errors: INVALID_ARG, CAPACITY
+ * (workspace), CUDA. */
+int la_kv8_compact(const la_kv8_cache *c, int32_t *table_out, int32_t *refs_out, int32_t *n_live, void *workspace,
+                   int64_t workspace_bytes, void *stream);
+
+/* Synchronise `stream`, read and clear *status.  LA_ERR_DEVICE_TIMEOUT,
+ * LA_ERR_STATE (LA_KV8_BAD) or LA_ERR_CAPACITY (LA_KV8_FULL), in this order,
+ * if the bit was set since the last status call, else LA_OK; *bits (host, or
+ * NULL) receives the word.  Errors: those and INVALID_ARG, CUDA. */
+int la_kv8_status(const la_kv8_cache *c, uint32_t *bits, void *stream);
+
 void la_destroy(la_handle *h);
 const char *la_strerror(int code);
 const char *la_last_error(void);
