@@ -11,7 +11,7 @@
 // fp16's range, whatever the pages' scales are.
 //
 // The work is the list of (sequence, KV head, tile of query vectors) units,
-// each a run of key tiles: the cached tokens, then the sequence's new rows.
+// each a run of key tiles: the sequence's new rows, then its cached tokens.
 // Every worker (CTA) takes an equal share of the flattened key tiles of all
 // units, read off the device-side lengths, so ragged batches and single long
 // sequences fill the GPU alike.  A unit that one worker does not cover leaves
@@ -30,7 +30,7 @@ struct Kv8Args {
     la_kv8_attn a;
     int gq;            // query heads per KV head
     int q_tile;        // query vectors per unit
-    int k_tile;        // keys per tile
+    int k_tile, n_tile;   // cached tokens, new rows per key tile
     int whole;         // 1: worker w runs units w, w + workers, ... whole, and nothing is joined
     int workers;
     float scale_log2;  // scale * log2(e)
@@ -39,12 +39,17 @@ struct Kv8Args {
 };
 
 // ------------------------------------------------------------------ work list
+constexpr int kUnitCost = 4;
+
 struct Kv8Seq {
     int first, rows;         // rows of the slot
     int len;                 // cached tokens
     int qtiles;              // tiles of query vectors
     int ctiles, ntiles;      // key tiles of the cache and of the new rows
-    __device__ int ktiles() const { return max(ctiles + ntiles, 1); }
+    // A unit's length in the flattened list: its key tiles behind kUnitCost
+    // empty ones, which stand for what a unit costs beside its tiles (its
+    // queries, the first copies' latency, the join of the warps).
+    __device__ int ktiles() const { return kUnitCost + ctiles + ntiles; }
 };
 
 __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Args &p, int s) {
@@ -53,7 +58,7 @@ __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Args &p, int s) {
     q.len = kv8_len(p.c, s);
     q.qtiles = static_cast<int>((static_cast<long long>(q.rows) * p.gq + p.q_tile - 1) / p.q_tile);
     q.ctiles = (q.len + p.k_tile - 1) / p.k_tile;
-    q.ntiles = p.a.k ? (q.rows + p.k_tile - 1) / p.k_tile : 0;
+    q.ntiles = p.a.k ? (q.rows + p.n_tile - 1) / p.n_tile : 0;
     return q;
 }
 
@@ -108,7 +113,7 @@ __device__ __forceinline__ long long kv8_share(long long total, int w, int worke
 // ------------------------------------------------------------------ mma
 // D (16 x 8, fp32) += A (16 x 16, fp16) * B (16 x 8, fp16).
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -132,67 +137,181 @@ __device__ __forceinline__ int fit_f16(float amax) { return max(exponent_of(amax
 
 // ------------------------------------------------------------------ few query vectors per KV head
 // k_kv8_rows: 16 query vectors per unit (all heads of a KV head's group for
-// one row, or some rows), 8 warps that take the unit's 64-key tiles in turn,
-// each with its own running softmax; joined through shared memory at the end
-// of the unit.  No tile is shared, so nothing waits on a barrier inside a
-// unit.  K and V bytes go from global memory to registers in the order in
-// which mma.m16n8k16 wants its B operand: the products are sums over dims
-// (keys), so any order will do as long as q (the weights) has the same one.
-//   K: column n of product j is key 16 (n >> 1) + 2 j + (n & 1); lane (n, t)
-//      reads HD / 4 consecutive bytes of that key's row from byte t HD / 4.
-//   V: lane (n, t) reads keys 16 t .. 16 t + 15 of dim 8 i + n: one 16-byte load.
+// one row, or some rows).  Bound by the cache's bytes: every byte is read
+// once and meets 16 query vectors.  The warps of a CTA take the unit's tiles
+// (one page each) in turn, each with its own running softmax and its own ring
+// of page blocks in shared memory, so no barrier is met inside a unit; they
+// are joined through shared memory at the unit's end.  A block of K or V of
+// one (page, KV head) is one run of page * head_dim bytes: one bulk copy.
+//
+// From shared memory the bytes go to the B operand of mma.m16n8k16 without a
+// transpose: the products are sums over dims (keys), so any order will do as
+// long as q (the weights) has the same one.
+//   K: column n of product j is key KT/4 (n >> 1) + 2 j + (n & 1) of the piece;
+//      lane (n, t) reads HD / 4 consecutive bytes of that key's row.
+//   V: lane (n, t) reads its KT / 4 consecutive keys of dim 8 i + n.
 // Then the weights of product j's columns 2 t, 2 t + 1 are this lane's keys
-// 16 t + 2 j, + 1: already the A operand of the second product.
-constexpr int kRowsWarps = 8;
-constexpr int kRowsQ = 16, kRowsK = 64;
+// KT/4 t + 2 j, + 1: already the A operand of the second product.
+constexpr int kRowsWarps = 4;
+constexpr int kRowsQ = 16;
+constexpr int kRowsNew = 64;     // new rows per tile
 
-template <int HD>
-struct RowsShared {
-    long long tiles[LA_KV8_MAX_SEQS + 1];
-    long long warp_sum[kRowsWarps];
-    float m[kRowsWarps][kRowsQ], l[kRowsWarps][kRowsQ];
-    alignas(16) float o[kRowsWarps][kRowsQ][HD + 4];   // read as float4
+template <int HD, int PAGE>
+struct Rows {
+    static constexpr int block = HD * PAGE;                                     // bytes of one page's K (or V) of a head
+    static constexpr int slots = block >= 8192 ? 3 : 6;                         // of a warp's ring; K and V alternate
+    static constexpr int ring = block * slots * kRowsWarps;
+    static constexpr int join = kRowsWarps * kRowsQ * (HD + 4) * 4;             // over the ring, at the end of a unit
+    static constexpr int ml_off = ring > join ? ring : join;
+    static constexpr int bar_off = ml_off + kRowsWarps * kRowsQ * 2 * 4;
+    static constexpr int meta_off = bar_off + kRowsWarps * slots * 8;           // [warp][slot] factor of K, exponent of V
+    static constexpr int sum_off = meta_off + kRowsWarps * slots * 8;
+    static constexpr int tiles_off = sum_off + kRowsWarps * 8;                  // (n_seqs + 1) prefix sums follow
+    static constexpr int per_sm = block > 8192 ? 1 : block < 4096 ? 3 : 2;         // CTAs per SM that registers and the ring allow
+    static size_t bytes(int n_seqs) { return tiles_off + (static_cast<size_t>(n_seqs) + 1) * 8; }
 };
 
-template <int HD>
-__global__ void __launch_bounds__(32 * kRowsWarps, 1) k_kv8_rows(const __grid_constant__ Kv8Args p) {
-    constexpr int NI = HD / 8;    // 8-dim groups of the output
-    constexpr int KS = HD / 16;   // steps of the first product
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    RowsShared<HD> &sh = *reinterpret_cast<RowsShared<HD> *>(smem_raw);
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Untiled bulk copy global -> shared, completing `bytes` on mbarrier `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// Online softmax of one piece: scores sc (columns: this lane's keys) to the
+// fp16 weights w16, with the running maximum m, the sum l and O's factor.
+template <int NJ, int NI>
+__device__ __forceinline__ void rows_softmax(float (&sc)[NJ][4], const uint32_t (&see)[2], float kf, const float (&qf)[2], int vx,
+                                             float (&m)[2], float (&l)[2], float (&o)[NI][4], uint32_t (&w16)[NJ][2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {   // rows g (elements 0, 1 of a product) and g + 8 (2, 3)
+        const float f = kf * qf[h], add = static_cast<float>(vx);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float &x = sc[j][2 * h + e];
+                x = (see[h] >> (2 * j + e)) & 1u ? fmaf(x, f, add) : -INFINITY;
+                mx = fmaxf(mx, x);
+            }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[h], mx), base = mn == -INFINITY ? 0.f : mn;
+        const float alpha = ex2(m[h] - base);
+        m[h] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const float a = ex2(sc[j][2 * h] - base), b = ex2(sc[j][2 * h + 1] - base);
+            sum += a + b;
+            w16[j][h] = pack_f16(a, b);
+        }
+        l[h] = l[h] * alpha + sum * power_of(-vx);
+        if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                o[i][2 * h] *= alpha;
+                o[i][2 * h + 1] *= alpha;
+            }
+        }
+    }
+}
+
+template <int HD, int PAGE>
+__global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8_rows(const __grid_constant__ Kv8Args p) {
+    using Lay = Rows<HD, PAGE>;
+    constexpr int NI = HD / 8;                    // 8-dim groups of the output
+    constexpr int KS = HD / 16;                   // steps of the first product
+    constexpr int KT = PAGE < 64 ? PAGE : 64;     // keys per piece
+    constexpr int CH = KT / 4;                    // of them, one lane's
+    constexpr int NS = Lay::slots;
+    extern __shared__ __align__(128) uint8_t smem[];
+    float *sh_ml = reinterpret_cast<float *>(smem + Lay::ml_off);   // [warp][16][m, l]
+    float *sh_o = reinterpret_cast<float *>(smem);                  // [warp][16][HD + 4], over the ring
+    long long *tiles = reinterpret_cast<long long *>(smem + Lay::tiles_off);
     pdl_trigger();
-    pdl_wait();
     const la_kv8_cache &c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-    kv8_plan(p, sh.tiles, sh.warp_sum);
-    const long long total = sh.tiles[c.n_seqs];
+    const uint32_t ring = smem_u32(smem) + warp * NS * Lay::block, bars = smem_u32(smem + Lay::bar_off) + warp * NS * 8;
+    const uint8_t *my_ring = smem + warp * NS * Lay::block;
+    int2 *meta = reinterpret_cast<int2 *>(smem + Lay::meta_off) + warp * NS;
+    if (lane < NS) mbar_init(bars + lane * 8, 1);
+    fence_barrier_init();
+    pdl_wait();
+    kv8_plan(p, tiles, reinterpret_cast<long long *>(smem + Lay::sum_off));
+    const long long total = tiles[c.n_seqs];
     const int workers = kv8_workers(p, total);
     if (!p.whole && static_cast<int>(blockIdx.x) >= workers) return;
     long long at = p.whole ? 0 : kv8_share(total, blockIdx.x, workers);
     const long long end = p.whole ? total : kv8_share(total, blockIdx.x + 1, workers);
     long long skip = blockIdx.x;   // whole: units to pass over
-    const uint8_t *kp = static_cast<const uint8_t *>(c.k), *vp = static_cast<const uint8_t *>(c.v);
-    const long long bytes = static_cast<long long>(c.page) * HD;
+    int in_slot = 0, out_slot = 0;   // ring positions: the next block to load, the next to read
+    uint32_t out_phase = 0;
+    bool ok = true;                  // false once a wait gave up: this warp loads nothing more
 
     while (at < end) {
-        const int s = kv8_find(sh.tiles, c.n_seqs, at);
+        const int s = kv8_find(tiles, c.n_seqs, at);
         const Kv8Seq sq = kv8_seq(p, s);
         const int kt = sq.ktiles();
         if (p.whole) {
-            // units of this slot from `at` on
-            const long long units = (sh.tiles[s + 1] - at) / kt;
+            const long long units = (tiles[s + 1] - at) / kt;   // of this slot from `at` on
             if (skip >= units) {
                 skip -= units;
-                at = sh.tiles[s + 1];
+                at = tiles[s + 1];
                 continue;
             }
             at += skip * kt;
             skip = p.workers - 1;
         }
-        const int unit = static_cast<int>((at - sh.tiles[s]) / kt), k0 = static_cast<int>((at - sh.tiles[s]) % kt);
-        const int k1 = static_cast<int>(min(static_cast<long long>(kt), k0 + (end - at)));
+        const int unit = static_cast<int>((at - tiles[s]) / kt), v0 = static_cast<int>((at - tiles[s]) % kt);
+        const int v1 = static_cast<int>(min(static_cast<long long>(kt), v0 + (end - at)));
+        const int k0 = max(v0 - kUnitCost, 0), k_end = max(v1 - kUnitCost, 0);   // key tiles of this piece
         const int head = unit / sq.qtiles, qv0 = (unit % sq.qtiles) * kRowsQ;
         const int nqv = min(kRowsQ, sq.rows * p.gq - qv0);
+
+        // This warp's tiles: k0 + warp, + 4, ...; the new rows' come first in
+        // the unit.  Cached ones are numbered i = 0 .. nc - 1, page first + 4 i.
+        int kt0 = k0 + warp, first = kt0;
+        while (first < sq.ntiles) first += kRowsWarps;
+        const int nc = ok && first < k_end ? (k_end - first + kRowsWarps - 1) / kRowsWarps : 0;
+        const int page0 = first - sq.ntiles;
+        // Block 2 i is K of tile i, block 2 i + 1 its V.  Page numbers and
+        // scales are looked up 32 tiles at a time, lane i for tile 32 n + i.
+        int my_page = -1, my_vx = 0, issued = 0;
+        float my_kf = 0.f;
+        auto issue = [&]() {
+            const int i = issued >> 1;
+            if ((issued & 63) == 0) {
+                my_page = i + lane < nc ? kv8_page(c, s, page0 + kRowsWarps * (i + lane)) : -1;
+                if (my_page >= 0) {
+                    const long long blk = kv8_block(c, p.a.layer, my_page, head);
+                    my_kf = c.k_scale[blk];
+                    my_vx = exponent_of(c.v_scale[blk]);
+                }
+            }
+            const int pg = __shfl_sync(0xffffffffu, my_page, i & 31);
+            if (lane == (i & 31)) meta[in_slot] = make_int2(pg < 0 ? -1 : __float_as_int(my_kf), my_vx);
+            if (lane == 0) {
+                const uint32_t bar = bars + in_slot * 8;
+                if (pg >= 0) {
+                    mbar_arrive_expect_tx(bar, Lay::block);
+                    bulk_load(ring + in_slot * Lay::block,
+                              static_cast<const uint8_t *>(issued & 1 ? c.v : c.k) + kv8_block(c, p.a.layer, pg, head) * Lay::block, Lay::block, bar);
+                } else {
+                    mbar_arrive_expect_tx(bar, 0);   // a page number outside the cache: nothing is loaded, no key counts
+                }
+            }
+            __syncwarp();
+            in_slot = in_slot + 1 == NS ? 0 : in_slot + 1;
+            ++issued;
+        };
+        while (issued < min(NS, 2 * nc)) issue();
 
         // q as fp16 A operands, each vector scaled by a power of two to fit.
         uint32_t q[KS][4];
@@ -227,9 +346,8 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 1) k_kv8_rows(const __grid_co
             for (int i = 0; i < KS / 2; ++i) {
                 const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {   // word k: dims 2k, 2k + 1 of 8; step 2 i + k / 2, half k & 1
+                for (int k = 0; k < 4; ++k)   // word k: dims 2k, 2k + 1 of 8; step 2 i + k / 2, half k & 1
                     q[2 * i + (k >> 1)][h + 2 * (k & 1)] = pack_f16(bf16_bits(u[k] & 0xffffu) * f, bf16_bits(u[k] >> 16) * f);
-                }
             }
         }
 
@@ -238,219 +356,228 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 1) k_kv8_rows(const __grid_co
 #pragma unroll
         for (int i = 0; i < NI; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-        const int k_end = min(k1, sq.ctiles + sq.ntiles);   // a unit without keys has one empty tile
-        for (int kt0 = k0 + warp; kt0 < k_end; kt0 += kRowsWarps) {
-            float sc[8][4];
+        // ---- new rows: bf16, scaled by a power of two for the whole tile
+        for (; kt0 < min(k_end, sq.ntiles); kt0 += kRowsWarps) {
+            constexpr int NJ = kRowsNew / 8;
+            const int key0 = kt0 * kRowsNew, nkeys = min(kRowsNew, sq.rows - key0);
+            const __nv_bfloat16 *kn = static_cast<const __nv_bfloat16 *>(p.a.k) + (sq.first + key0) * p.a.k_stride + head * HD;
+            const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + head * HD;
+            float ak = 0.f, av = 0.f;
+            for (int i = lane; i < nkeys * (HD / 2); i += 32) {
+                const int r = i / (HD / 2), d = 2 * (i % (HD / 2));
+                const uint32_t a = *reinterpret_cast<const uint32_t *>(kn + r * p.a.k_stride + d);
+                const uint32_t b = *reinterpret_cast<const uint32_t *>(vn + r * p.a.v_stride + d);
+                const float x[4] = {bf16_bits(a & 0xffffu), bf16_bits(a >> 16), bf16_bits(b & 0xffffu), bf16_bits(b >> 16)};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
-            float kf;      // factor on this lane's scores (columns: keys of its 16-key piece t)
-            int vx;        // exponent of V's scale for those keys
-            uint32_t see[2];   // bit 2 j + e: key 16 t + 2 j + e is seen by row h
-            const bool cached = kt0 < sq.ctiles;
-            const int key0 = (cached ? kt0 : kt0 - sq.ctiles) * kRowsK;
-            long long vblk = 0;
-            int vlive = 0;     // keys of this lane's piece that count
-            int nx = 0;
-            if (cached) {
-                const int ck = key0 + 16 * (g >> 1), cv = key0 + 16 * t;   // first keys of the pieces this lane reads
-                const int pk = ck < sq.len ? kv8_page(c, s, ck / c.page) : -1, kk = ck % c.page;
-                const int pv = cv < sq.len ? kv8_page(c, s, cv / c.page) : -1;
-                const long long kblk = kv8_block(c, p.a.layer, max(pk, 0), head);
-                vblk = kv8_block(c, p.a.layer, max(pv, 0), head);
-                kf = c.k_scale[vblk];
-                vx = exponent_of(c.v_scale[vblk]);
-                vlive = pv < 0 ? 0 : min(max(sq.len - key0 - 16 * t, 0), 16);
-                see[0] = see[1] = vlive == 16 ? 0xffffu : (1u << vlive) - 1u;
-                const uint8_t *row = kp + kblk * bytes + static_cast<long long>(kk + (g & 1)) * HD + t * (HD / 4);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    uint4 w[HD / 64];
-#pragma unroll
-                    for (int i = 0; i < HD / 64; ++i) w[i] = __ldcg(reinterpret_cast<const uint4 *>(row + 2 * j * HD) + i);
-#pragma unroll
-                    for (int i = 0; i < HD / 64; ++i) {
-                        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            uint32_t b0, b1;
-                            e4m3x4_f16(u[k], b0, b1);
-                            mma_f16(sc[j], q[4 * i + k], b0, b1);
-                        }
-                    }
-                }
-            } else {
-                // New rows: bf16, scaled by a power of two for the whole tile.
-                const int nkeys = min(kRowsK, sq.rows - key0);
-                const __nv_bfloat16 *kn = static_cast<const __nv_bfloat16 *>(p.a.k) + (sq.first + key0) * p.a.k_stride + head * HD;
-                const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + head * HD;
-                float ak = 0.f, av = 0.f;
-                for (int i = lane; i < nkeys * (HD / 2); i += 32) {
-                    const int r = i / (HD / 2), d = 2 * (i % (HD / 2));
-                    const uint32_t a = *reinterpret_cast<const uint32_t *>(kn + r * p.a.k_stride + d);
-                    const uint32_t b = *reinterpret_cast<const uint32_t *>(vn + r * p.a.v_stride + d);
-                    const float x[4] = {bf16_bits(a & 0xffffu), bf16_bits(a >> 16), bf16_bits(b & 0xffffu), bf16_bits(b >> 16)};
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        if (is_finite(x[k])) ak = fmaxf(ak, fabsf(x[k]));
-                        if (is_finite(x[2 + k])) av = fmaxf(av, fabsf(x[2 + k]));
-                    }
-                }
-                ak = warp_max(ak);
-                av = warp_max(av);
-                const int kx = fit_f16(ak);
-                nx = fit_f16(av);
-                kf = power_of(kx);
-                vx = nx;
-                vlive = min(max(nkeys - 16 * t, 0), 16);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int first = key0 + 16 * t;   // this lane's keys, as rows of the sequence
-                    if (myrow[h] < 0 || first >= sq.rows) see[h] = 0;
-                    else if (p.a.vis)
-                        see[h] = first < 256 ? p.a.vis[(static_cast<long long>(sq.first) + myrow[h]) * 8 + first / 32] >> (first % 32) & 0xffffu : 0;
-                    else see[h] = myrow[h] >= first + 15 ? 0xffffu : myrow[h] < first ? 0u : (2u << (myrow[h] - first)) - 1u;
-                    if (vlive < 16) see[h] &= (1u << vlive) - 1u;
-                }
-                const float f = power_of(-kx);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int r = 16 * (g >> 1) + 2 * j + (g & 1);
-                    const __nv_bfloat16 *row = kn + r * p.a.k_stride + t * (HD / 4);
-#pragma unroll
-                    for (int i = 0; i < KS; ++i) {
-                        const uint2 w = r < nkeys ? *reinterpret_cast<const uint2 *>(row + 4 * i) : make_uint2(0, 0);
-                        mma_f16(sc[j], q[i], pack_f16(bf16_bits(w.x & 0xffffu) * f, bf16_bits(w.x >> 16) * f),
-                                pack_f16(bf16_bits(w.y & 0xffffu) * f, bf16_bits(w.y >> 16) * f));
-                    }
+                for (int k = 0; k < 2; ++k) {
+                    if (is_finite(x[k])) ak = fmaxf(ak, fabsf(x[k]));
+                    if (is_finite(x[2 + k])) av = fmaxf(av, fabsf(x[2 + k]));
                 }
             }
-            // Softmax: rows g (elements 0, 1 of a product) and g + 8 (2, 3).
-            uint32_t w16[8][2];
+            const int kx = fit_f16(warp_max(ak)), vx = fit_f16(warp_max(av));
+            const int live = min(max(nkeys - 16 * t, 0), 16);
+            uint32_t see[2];   // bit 2 j + e: this lane's key 16 t + 2 j + e is seen by row h
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float f = kf * qf[h], add = static_cast<float>(vx);
-                float mx = -INFINITY;
+                const int k = key0 + 16 * t;
+                if (myrow[h] < 0) see[h] = 0;
+                else if (p.a.vis)
+                    see[h] = k < 256 ? p.a.vis[(static_cast<long long>(sq.first) + myrow[h]) * 8 + k / 32] >> (k % 32) & 0xffffu : 0;
+                else see[h] = myrow[h] >= k + 15 ? 0xffffu : myrow[h] < k ? 0u : (2u << (myrow[h] - k)) - 1u;
+                if (live < 16) see[h] &= (1u << live) - 1u;
+            }
+            float sc[NJ][4];
+            const float f = power_of(-kx);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < NJ; ++j) {
+                sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
+                if (2 * j >= nkeys) continue;
+                const int r = 16 * (g >> 1) + 2 * j + (g & 1);
+                const __nv_bfloat16 *row = kn + r * p.a.k_stride + t * (HD / 4);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float &x = sc[j][2 * h + e];
-                        x = (see[h] >> (2 * j + e)) & 1u ? fmaf(x, f, add) : -INFINITY;
-                        mx = fmaxf(mx, x);
-                    }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float mn = fmaxf(m[h], mx), base = mn == -INFINITY ? 0.f : mn;
-                const float alpha = exp2f(m[h] - base);
-                m[h] = mn;
-                float sum = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float a = exp2f(sc[j][2 * h] - base), b = exp2f(sc[j][2 * h + 1] - base);
-                    sum += a + b;
-                    w16[j][h] = pack_f16(a, b);
+                for (int i = 0; i < KS; ++i) {
+                    const uint2 w = r < nkeys ? *reinterpret_cast<const uint2 *>(row + 4 * i) : make_uint2(0, 0);
+                    mma_f16(sc[j], q[i], pack_f16(bf16_bits(w.x & 0xffffu) * f, bf16_bits(w.x >> 16) * f),
+                            pack_f16(bf16_bits(w.y & 0xffffu) * f, bf16_bits(w.y >> 16) * f));
                 }
-                l[h] = l[h] * alpha + sum * power_of(-vx);
-                if (__any_sync(0xffffffffu, alpha != 1.f)) {
+            }
+            uint32_t w16[NJ][2];
+            rows_softmax<NJ, NI>(sc, see, power_of(kx), qf, vx, m, l, o, w16);
+            // A NaN or infinity of V counts 0 in the product (0 * inf would
+            // reach rows that do not see it) and is added for the rows that do.
+            const float fv = power_of(-vx);
+            bool odd = false;
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) {
-                        o[i][2 * h] *= alpha;
-                        o[i][2 * h + 1] *= alpha;
+            for (int i = 0; i < NI; ++i) {
+#pragma unroll
+                for (int k = 0; k < NJ / 2; ++k) {
+                    if (4 * k >= nkeys) continue;
+                    float x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = 16 * t + 4 * k + e;
+                        x[e] = r < nkeys ? __bfloat162float(vn[r * p.a.v_stride + 8 * i + g]) : 0.f;
+                        odd |= !is_finite(x[e]);
+                        x[e] = is_finite(x[e]) ? x[e] * fv : 0.f;
+                    }
+                    const uint32_t a[4] = {w16[2 * k][0], w16[2 * k][1], w16[2 * k + 1][0], w16[2 * k + 1][1]};
+                    mma_f16(o[i], a, pack_f16(x[0], x[1]), pack_f16(x[2], x[3]));
+                }
+            }
+            if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    for (int r = 0; r < nkeys; ++r) {
+                        const uint32_t b0 = __shfl_sync(0xffffffffu, see[0], 4 * g + (r >> 4)), b1 = __shfl_sync(0xffffffffu, see[1], 4 * g + (r >> 4));
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float x = __bfloat162float(vn[r * p.a.v_stride + 8 * i + 2 * t + e]);
+                            if (is_finite(x)) continue;
+                            if ((b0 >> (r & 15)) & 1u) o[i][e] += x;
+                            if ((b1 >> (r & 15)) & 1u) o[i][2 + e] += x;
+                        }
+                    }
+            }
+        }
+
+        // ---- cached tokens
+        auto landed = [&]() {   // the next block to read is there
+            ok = __all_sync(0xffffffffu, mbar_wait(bars + out_slot * 8, out_phase, c.status, LA_KV8_TIMEOUT));
+            return ok;
+        };
+        auto next = [&]() {     // it has been read: its slot takes the next block to load
+            __syncwarp();
+            if (++out_slot == NS) {
+                out_slot = 0;
+                out_phase ^= 1;
+            }
+            if (issued < 2 * nc) issue();
+        };
+        int read = 0;           // blocks read
+        for (int i = 0; i < nc; ++i) {
+            if (!landed()) break;
+            const int2 mt = meta[out_slot];
+            const float kf = __int_as_float(mt.x);
+            const int vx = mt.y;
+            const int left = mt.x == -1 ? 0 : sq.len - (page0 + kRowsWarps * i) * PAGE;   // keys of this page that count
+            constexpr int NJ = KT / 8;
+            float sc[PAGE / KT][NJ][4];
+            const uint8_t *kblk = my_ring + out_slot * Lay::block;
+#pragma unroll
+            for (int piece = 0; piece < PAGE / KT; ++piece) {
+                const uint8_t *row = kblk + (piece * KT + CH * (g >> 1) + (g & 1)) * HD + t * (HD / 4);
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) sc[piece][j][0] = sc[piece][j][1] = sc[piece][j][2] = sc[piece][j][3] = 0.f;
+#pragma unroll
+                for (int x = 0; x < HD / 64; ++x) {   // steps outside, products inside: their sums do not wait on one another
+                    uint4 w[NJ];
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) w[j] = *reinterpret_cast<const uint4 *>(row + 2 * j * HD + 16 * x);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j) {
+                            uint32_t b0, b1;
+                            e4m3x4_f16(k == 0 ? w[j].x : k == 1 ? w[j].y : k == 2 ? w[j].z : w[j].w, b0, b1);
+                            mma_f16(sc[piece][j], q[4 * x + k], b0, b1);
+                        }
+                }
+            }
+            next();
+            ++read;
+            if (!landed()) break;
+            const uint8_t *vblk = my_ring + out_slot * Lay::block;
+#pragma unroll
+            for (int piece = 0; piece < PAGE / KT; ++piece) {
+                const int live = min(max(left - piece * KT - CH * t, 0), CH);
+                const uint32_t see1 = (1u << live) - 1u;
+                const uint32_t see[2] = {see1, see1};
+                uint32_t w16[NJ][2];
+                rows_softmax<NJ, NI>(sc[piece], see, kf, qf, vx, m, l, o, w16);
+                const uint8_t *col = vblk + g * PAGE + piece * KT + CH * t;
+                const bool whole = left >= PAGE;
+                constexpr int NG = 4;   // output groups in flight together
+#pragma unroll
+                for (int n0 = 0; n0 < NI; n0 += NG) {
+                    uint32_t u[NG][CH / 4];
+#pragma unroll
+                    for (int n = 0; n < NG; ++n) {
+                        if constexpr (CH == 16) {
+                            const uint4 w = *reinterpret_cast<const uint4 *>(col + 8 * (n0 + n) * PAGE);
+                            u[n][0] = w.x, u[n][1] = w.y, u[n][2] = w.z, u[n][3] = w.w;
+                        } else {
+                            const uint2 w = *reinterpret_cast<const uint2 *>(col + 8 * (n0 + n) * PAGE);
+                            u[n][0] = w.x, u[n][1] = w.y;
+                        }
+                    }
+                    if (!whole) {   // bytes behind the last token may be anything
+#pragma unroll
+                        for (int k = 0; k < CH / 4; ++k) {
+                            const int b = live - 4 * k;
+                            const uint32_t mask = b >= 4 ? 0xffffffffu : b <= 0 ? 0u : (1u << (8 * b)) - 1u;
+#pragma unroll
+                            for (int n = 0; n < NG; ++n) u[n][k] &= mask;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < CH / 4; ++k) {
+                        const uint32_t a[4] = {w16[2 * k][0], w16[2 * k][1], w16[2 * k + 1][0], w16[2 * k + 1][1]};
+#pragma unroll
+                        for (int n = 0; n < NG; ++n) {
+                            uint32_t b0, b1;
+                            e4m3x4_f16(u[n][k], b0, b1);
+                            mma_f16(o[n0 + n], a, b0, b1);
+                        }
                     }
                 }
             }
-            // O += w V
-            if (cached) {
-                const uint8_t *col = vp + vblk * bytes + static_cast<long long>(g) * c.page + (key0 + 16 * t) % c.page;
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    uint4 w = __ldcg(reinterpret_cast<const uint4 *>(col + static_cast<long long>(8 * i) * c.page));
-                    uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                    if (vlive < 16) {   // bytes behind the last token may be anything
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int n = vlive - 4 * k;
-                            u[k] = n >= 4 ? u[k] : n <= 0 ? 0u : u[k] & ((1u << (8 * n)) - 1u);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t b0, b1;
-                        e4m3x4_f16(u[k], b0, b1);
-                        const uint32_t a[4] = {w16[2 * k][0], w16[2 * k][1], w16[2 * k + 1][0], w16[2 * k + 1][1]};
-                        mma_f16(o[i], a, b0, b1);
-                    }
-                }
-            } else {
-                // V of the new rows.  A NaN or infinity counts 0 in the product
-                // (0 * inf would reach rows that do not see it) and is added
-                // for the rows that do.
-                const int nkeys = min(kRowsK, sq.rows - key0);
-                const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + head * HD;
-                const float f = power_of(-nx);
-                bool odd = false;
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float x[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int r = 16 * t + 4 * k + e;
-                            x[e] = r < nkeys ? __bfloat162float(vn[r * p.a.v_stride + 8 * i + g]) : 0.f;
-                            odd |= !is_finite(x[e]);
-                            x[e] = is_finite(x[e]) ? x[e] * f : 0.f;
-                        }
-                        const uint32_t a[4] = {w16[2 * k][0], w16[2 * k][1], w16[2 * k + 1][0], w16[2 * k + 1][1]};
-                        mma_f16(o[i], a, pack_f16(x[0], x[1]), pack_f16(x[2], x[3]));
-                    }
-                }
-                if (__any_sync(0xffffffffu, odd)) {
-#pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        for (int r = 0; r < nkeys; ++r) {
-                            const uint32_t b0 = __shfl_sync(0xffffffffu, see[0], 4 * g + (r >> 4)), b1 = __shfl_sync(0xffffffffu, see[1], 4 * g + (r >> 4));
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float x = __bfloat162float(vn[r * p.a.v_stride + 8 * i + 2 * t + e]);
-                                if (is_finite(x)) continue;
-                                if ((b0 >> (r & 15)) & 1u) o[i][e] += x;
-                                if ((b1 >> (r & 15)) & 1u) o[i][2 + e] += x;
-                            }
-                        }
+            next();
+            ++read;
+        }
+        if (!ok) {   // void: wait (bounded) for what is still in flight
+            for (; read < issued; ++read) {
+                mbar_wait(bars + out_slot * 8, out_phase, c.status, LA_KV8_TIMEOUT);
+                if (++out_slot == NS) {
+                    out_slot = 0;
+                    out_phase ^= 1;
                 }
             }
         }
 
-        // Join the warps: weights 2^(m_w - M), then the sum in warp order.
+        // ---- join the warps: weights 2^(m_w - M), then the sum in warp order
+        __syncthreads();   // the rings are free
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            const int r = warp * kRowsQ + g + 8 * h;
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            if (t == 0) {
-                sh.m[warp][g + 8 * h] = m[h];
-                sh.l[warp][g + 8 * h] = l[h];
-            }
+            if (t == 0) *reinterpret_cast<float2 *>(sh_ml + 2 * r) = make_float2(m[h], l[h]);
+            if (g + 8 * h < nqv) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
-                *reinterpret_cast<float2 *>(&sh.o[warp][g + 8 * h][8 * i + 2 * t]) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+                for (int i = 0; i < NI; ++i)
+                    *reinterpret_cast<float2 *>(sh_o + r * (HD + 4) + 8 * i + 2 * t) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+            }
         }
         __syncthreads();
-        const bool all = k0 == 0 && k1 == kt;
-        const int slot = 2 * blockIdx.x + (k0 == 0 ? 1 : 0);
+        const bool all = v0 == 0 && v1 == kt;
+        const int slot = 2 * blockIdx.x + (v0 == 0 ? 1 : 0);
         for (int i = tid; i < nqv * (HD / 4); i += 32 * kRowsWarps) {
             const int r = i / (HD / 4), d = 4 * (i % (HD / 4));
+            float2 ml[kRowsWarps];
             float mx = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kRowsWarps; ++w) mx = fmaxf(mx, sh.m[w][r]);
+            for (int w = 0; w < kRowsWarps; ++w) {
+                ml[w] = *reinterpret_cast<const float2 *>(sh_ml + 2 * (w * kRowsQ + r));
+                mx = fmaxf(mx, ml[w].x);
+            }
             float L = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kRowsWarps; ++w) {
-                if (sh.l[w][r] == 0.f) continue;   // saw no key
-                const float f = exp2f(sh.m[w][r] - mx);
-                const float4 x = *reinterpret_cast<const float4 *>(&sh.o[w][r][d]);
-                L += f * sh.l[w][r];
+                if (ml[w].y == 0.f) continue;   // saw no key
+                const float f = ex2(ml[w].x - mx);
+                const float4 x = *reinterpret_cast<const float4 *>(sh_o + (w * kRowsQ + r) * (HD + 4) + d);
+                L += f * ml[w].y;
                 acc.x += f * x.x;
                 acc.y += f * x.y;
                 acc.z += f * x.z;
@@ -468,68 +595,67 @@ __global__ void __launch_bounds__(32 * kRowsWarps, 1) k_kv8_rows(const __grid_co
                 if (d == 0) *reinterpret_cast<float2 *>(p.part_ml + (static_cast<long long>(slot) * kRowsQ + r) * 2) = make_float2(mx, L);
             }
         }
+        fence_proxy_async_smem();   // these accesses before the next unit's bulk copies into the same bytes
         __syncthreads();
-        at += k1 - k0;
+        at += v1 - v0;
     }
 }
 
 // ------------------------------------------------------------------ join
 // A unit that several workers share: worker ranges are contiguous, so the
 // unit's pieces are those of consecutive workers, the first in its slot 1
-// (the piece begins the unit), the others in their slot 0.  One CTA per unit,
-// pieces added in key order.
-constexpr int kJoinThreads = 128;
+// (the piece begins the unit), the others in their slot 0.  One CTA per border
+// between workers; the first border inside a unit adds its pieces, in order.
+constexpr int kJoinThreads = 512, kJoinBatch = 8;
 
 template <int HD>
 __global__ void __launch_bounds__(kJoinThreads) k_kv8_join(const __grid_constant__ Kv8Args p) {
-    __shared__ long long tiles[LA_KV8_MAX_SEQS + 1];
+    extern __shared__ long long join_tiles[];   // [n_seqs + 1]
     __shared__ long long warp_sum[kJoinThreads / 32];
     pdl_trigger();
     pdl_wait();
+    long long *tiles = join_tiles;
     kv8_plan(p, tiles, warp_sum);
     const long long total = tiles[p.c.n_seqs];
-    // unit blockIdx.x: its slot by walking the slots' unit counts
-    long long u = blockIdx.x;
-    int s = 0;
-    Kv8Seq sq;
-    for (;; ++s) {
-        if (s == p.c.n_seqs) return;
-        if (tiles[s + 1] == tiles[s]) continue;
-        sq = kv8_seq(p, s);
-        const long long units = static_cast<long long>(sq.qtiles) * p.c.n_kv_heads;
-        if (u < units) break;
-        u -= units;
-    }
+    const int workers = kv8_workers(p, total), border = blockIdx.x + 1;
+    if (border >= workers) return;
+    const long long cut = kv8_share(total, border, workers);
+    const int s = kv8_find(tiles, p.c.n_seqs, cut);
+    const Kv8Seq sq = kv8_seq(p, s);
     const int kt = sq.ktiles();
-    const long long t0 = tiles[s] + u * kt, t1 = t0 + kt;
-    // first and last worker: the largest w with share(w) <= tile
-    const int workers = kv8_workers(p, total);
-    auto owner = [&](long long tile) {
-        long long w = tile * workers / total;
-        while (w + 1 < workers && kv8_share(total, static_cast<int>(w) + 1, workers) <= tile) ++w;
-        while (w > 0 && kv8_share(total, static_cast<int>(w), workers) > tile) --w;
-        return static_cast<int>(w);
-    };
-    const int w0 = owner(t0), w1 = owner(t1 - 1);
-    if (w0 == w1) return;
+    const long long u = (cut - tiles[s]) / kt, t0 = tiles[s] + u * kt, t1 = t0 + kt;
+    if (cut == t0 || kv8_share(total, border - 1, workers) > t0) return;
+    const int w0 = border - 1;
+    int w1 = border;   // the last worker with a piece
+    while (w1 + 1 < workers && kv8_share(total, w1 + 1, workers) < t1) ++w1;
     const int head = static_cast<int>(u) / sq.qtiles, qv0 = (static_cast<int>(u) % sq.qtiles) * p.q_tile;
     const int nqv = min(p.q_tile, sq.rows * p.gq - qv0);
     for (int i = threadIdx.x; i < nqv * (HD / 4); i += kJoinThreads) {
         const int r = i / (HD / 4), d = 4 * (i % (HD / 4));
+        // pieces kJoinBatch at a time, so that their loads are in flight together
         float mx = -INFINITY, L = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = w0; w <= w1; ++w) {
-            const long long rec = static_cast<long long>(2 * w + (w == w0 ? 1 : 0)) * p.q_tile + r;
-            const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + rec * 2);
-            if (ml.y == 0.f) continue;
-            const float4 x = *reinterpret_cast<const float4 *>(p.part + rec * HD + d);
-            const float mn = fmaxf(mx, ml.x), a = exp2f(mx - mn), b = exp2f(ml.x - mn);
-            L = L * a + ml.y * b;
-            acc.x = acc.x * a + x.x * b;
-            acc.y = acc.y * a + x.y * b;
-            acc.z = acc.z * a + x.z * b;
-            acc.w = acc.w * a + x.w * b;
-            mx = mn;
+        for (int w = w0; w <= w1; w += kJoinBatch) {
+            float2 ml[kJoinBatch];
+            float4 x[kJoinBatch];
+#pragma unroll
+            for (int b = 0; b < kJoinBatch; ++b) {
+                const int ww = min(w + b, w1);
+                const long long rec = static_cast<long long>(2 * ww + (ww == w0 ? 1 : 0)) * p.q_tile + r;
+                ml[b] = *reinterpret_cast<const float2 *>(p.part_ml + rec * 2);
+                x[b] = *reinterpret_cast<const float4 *>(p.part + rec * HD + d);
+            }
+#pragma unroll
+            for (int b = 0; b < kJoinBatch; ++b) {
+                if (w + b > w1 || ml[b].y == 0.f) continue;   // a piece that saw no key
+                const float mn = fmaxf(mx, ml[b].x), f0 = exp2f(mx - mn), f1 = exp2f(ml[b].x - mn);
+                L = L * f0 + ml[b].y * f1;
+                acc.x = acc.x * f0 + x[b].x * f1;
+                acc.y = acc.y * f0 + x[b].y * f1;
+                acc.z = acc.z * f0 + x[b].z * f1;
+                acc.w = acc.w * f0 + x[b].w * f1;
+                mx = mn;
+            }
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
         const int qv = qv0 + r;
@@ -540,7 +666,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv8_join(const __grid_constant
 }
 
 // ------------------------------------------------------------------ launch
-constexpr int kRowsPerSm = 1;
+constexpr int kRowsPerSm = 4;   // most CTAs of k_kv8_rows per SM
 
 int64_t kv8_workspace_bytes(const la_kv8_cache &c, int nsm) {
     const int64_t part = static_cast<int64_t>(nsm) * kRowsPerSm * 2 * kRowsQ * (c.head_dim + 2) * 4;
@@ -559,29 +685,40 @@ static bool attrs_needed(const std::atomic<unsigned long long> &mask, unsigned l
     return !(mask.load() & *bit);
 }
 
-template <int HD>
+template <int HD, int PAGE>
 static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
+    using Lay = Rows<HD, PAGE>;
+    static_assert(Lay::per_sm <= kRowsPerSm, "workspace");
     p.q_tile = kRowsQ;
-    p.k_tile = kRowsK;
+    p.k_tile = PAGE;
+    p.n_tile = kRowsNew;
     const long long units = ((static_cast<long long>(p.a.n_rows) * p.gq) / kRowsQ + p.c.n_seqs) * p.c.n_kv_heads;   // at most
-    const long long tiles = (p.a.max_len + kRowsK - 1) / kRowsK + (p.a.k ? (p.a.max_rows + kRowsK - 1) / kRowsK : 0);
+    const long long tiles = (p.a.max_len + PAGE - 1) / PAGE + (p.a.k ? (p.a.max_rows + kRowsNew - 1) / kRowsNew : 0);
     // A unit of at most two tiles per warp is not worth splitting: its pieces
     // would cost a second kernel.
     p.whole = tiles <= 2 * kRowsWarps;
-    p.workers = p.whole ? static_cast<int>(std::min<long long>(units, 1 << 20)) : nsm * kRowsPerSm;
+    p.workers = p.whole ? static_cast<int>(std::min<long long>(units, 1 << 20)) : nsm * Lay::per_sm;
     p.part = static_cast<float *>(ws);
     p.part_ml = p.part + static_cast<long long>(nsm) * kRowsPerSm * 2 * kRowsQ * HD;
     static std::atomic<unsigned long long> configured{0};
     unsigned long long bit = 0;
-    const size_t smem = sizeof(RowsShared<HD>);
     if (attrs_needed(configured, &bit)) {
-        cudaError_t e = cudaFuncSetAttribute(k_kv8_rows<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        cudaError_t e = cudaFuncSetAttribute(k_kv8_rows<HD, PAGE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(Lay::bytes(LA_KV8_MAX_SEQS)));
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
-    cudaError_t e = launch_k(k_kv8_rows<HD>, dim3(p.workers), dim3(32 * kRowsWarps), smem, s, p);
+    cudaError_t e = launch_k(k_kv8_rows<HD, PAGE>, dim3(p.workers), dim3(32 * kRowsWarps), Lay::bytes(p.c.n_seqs), s, p);
     if (e != cudaSuccess || p.whole) return e;
-    return launch_k(k_kv8_join<HD>, dim3(static_cast<unsigned>(units)), dim3(kJoinThreads), 0, s, p);
+    if (p.workers < 2) return cudaSuccess;
+    return launch_k(k_kv8_join<HD>, dim3(p.workers - 1), dim3(kJoinThreads), (static_cast<size_t>(p.c.n_seqs) + 1) * 8, s, p);
+}
+
+template <int HD>
+static cudaError_t attention_launch_hd(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
+    if (p.c.page == 32) return rows_launch<HD, 32>(p, nsm, ws, s);
+    if (p.c.page == 64) return rows_launch<HD, 64>(p, nsm, ws, s);
+    return rows_launch<HD, 128>(p, nsm, ws, s);
 }
 
 cudaError_t kv8_attention_launch(const la_kv8_cache &c, const la_kv8_attn &a, void *ws, int nsm, cudaStream_t s) {
@@ -591,7 +728,7 @@ cudaError_t kv8_attention_launch(const la_kv8_cache &c, const la_kv8_attn &a, vo
     p.a = a;
     p.gq = a.n_heads / c.n_kv_heads;
     p.scale_log2 = a.scale * kKv8Log2e;
-    return c.head_dim == 128 ? rows_launch<128>(p, nsm, ws, s) : rows_launch<64>(p, nsm, ws, s);
+    return c.head_dim == 128 ? attention_launch_hd<128>(p, nsm, ws, s) : attention_launch_hd<64>(p, nsm, ws, s);
 }
 
 }  // namespace la
