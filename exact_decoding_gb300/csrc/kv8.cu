@@ -46,16 +46,19 @@ constexpr int kPlanThreads = 1024;
 // they stand at the start, so a page that one sequence copies away from is
 // neither written nor handed out again within the call, and the answer does
 // not depend on the order in which threads run.
-//   ws: take[n_seqs] pages wanted (bit 30: the last page is copied),
-//       base[n_seqs] first of them in the list, src[n_seqs] page that holds
-//       the stored tokens of the first touched page, list[] free pages.
+//   ws: record[n_seqs] for the kernels that write the bytes (rows, length
+//       before them, page that holds the stored tokens of the first touched
+//       page or -1, that page's new place), take[n_seqs] pages wanted (bit 30:
+//       the last page is copied), base[n_seqs] first of them in the list,
+//       list[] free pages.
 __global__ void __launch_bounds__(kPlanThreads) k_kv8_plan(la_kv8_cache c, const int *row_start, int n_rows,
                                                            int max_rows, int *stored, int *ws) {
     pdl_trigger();
     pdl_wait();
     constexpr int kCopy = 1 << 30;
     __shared__ int warp_tot[32];
-    int *take = ws, *base = ws + c.n_seqs, *src = ws + 2 * c.n_seqs, *list = ws + 3 * c.n_seqs;
+    int4 *record = reinterpret_cast<int4 *>(ws);
+    int *take = ws + 4 * c.n_seqs, *base = take + c.n_seqs, *list = base + c.n_seqs;
     const int tid = threadIdx.x;
     // What each sequence wants; base: its place in the list if all fit.
     int wanted = 0;
@@ -66,7 +69,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv8_plan(la_kv8_cache c, const
             int first, from = -1;
             int n = kv8_rows(c, row_start, n_rows, s, &first);
             const int len = kv8_len(c, s);
-            if (n > max_rows || (c.lens[s] != len)) {
+            if (n > max_rows || c.lens[s] != len) {
                 atomicOr(c.status, LA_KV8_BAD);
                 n = 0;
             }
@@ -85,7 +88,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv8_plan(la_kv8_cache c, const
                 }
             }
             stored[s] = n;
-            src[s] = from;
+            record[s] = make_int4(n, len, from, -1);
         }
         int tot;
         const int at = block_scan(need + copy, warp_tot, &tot);
@@ -135,8 +138,11 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv8_plan(la_kv8_cache c, const
     const int lane = tid & 31;
     for (int s = tid >> 5; s < c.n_seqs; s += kPlanThreads / 32) {
         const int n = stored[s];
-        if (!n) continue;
-        const int t = take[s] & ~kCopy, len = c.lens[s];
+        if (!n) {
+            if (lane == 0) record[s].x = 0;
+            continue;
+        }
+        const int t = take[s] & ~kCopy, len = record[s].y, from = record[s].z;
         const bool copy = take[s] & kCopy;
         const int begin = copy ? len / c.page : (len + c.page - 1) / c.page;
         int *row = c.table + static_cast<long long>(s) * c.max_pages;
@@ -146,7 +152,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv8_plan(la_kv8_cache c, const
             c.refs[p] = 1;
         }
         if (lane == 0) {
-            if (copy) atomicSub(&c.refs[src[s]], 1);
+            if (copy) atomicSub(&c.refs[from], 1);
+            record[s].w = copy || from < 0 ? list[base[s]] : from;
             c.lens[s] = len + n;
         }
         __syncwarp();
@@ -183,22 +190,22 @@ constexpr int kStoreThreads = 256;
 // new rows go through shared memory once, for the largest magnitude and then
 // for the bytes (V is transposed on the way).
 template <int HD>
-__global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_kv8_rows r, const int *src, int touched) {
+__global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_kv8_rows r, const int4 *record, int touched) {
     pdl_trigger();
     pdl_wait();
-    __shared__ __align__(16) __nv_bfloat16 sm[128 * HD + 8 * 8];   // 8 elements more after every 16 rows: see V below
+    extern __shared__ __align__(16) __nv_bfloat16 sm[];            // [page] rows, 8 elements more after every 16: see V below
     __shared__ float red[kStoreThreads / 32];
     const int s = blockIdx.x / touched, j = blockIdx.x % touched;
     const int head = blockIdx.y, layer = blockIdx.z >> 1, isv = blockIdx.z & 1;
-    const int n = r.stored[s];
+    const int4 rec = record[s];
+    const int n = rec.x, len = rec.y;
     if (n <= 0) return;
-    const int len = c.lens[s] - n;
     const int pj = len / c.page + j;
     const int a = j == 0 ? len % c.page : 0;                       // tokens of this page that are stored already
     const long long left = static_cast<long long>(len) + n - static_cast<long long>(pj) * c.page;
     if (left <= 0) return;
     const int b = static_cast<int>(min(left, static_cast<long long>(c.page)));
-    const int to = kv8_page(c, s, pj), from = a > 0 ? src[s] : -1;
+    const int to = j == 0 ? rec.w : kv8_page(c, s, pj), from = a > 0 ? rec.z : -1;
     if (to < 0) return;
     const int row0 = (r.row_start ? r.row_start[s] : s) + pj * c.page + a - len;
     const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(isv ? r.v : r.k) +
@@ -208,20 +215,29 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_
     auto place = [](int t, int d) { return t * HD + (t >> 4) * 8 + d; };
 
     float amax = 0.f;
-    constexpr int C = HD / 8;                                      // 16-byte pieces of a row
-    for (int i = tid; i < (b - a) * C; i += kStoreThreads) {
-        const int t = i / C, d = (i % C) * 8;
-        const int row = r.row_idx ? r.row_idx[row0 + t] : row0 + t;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (static_cast<unsigned>(row) < static_cast<unsigned>(n_src)) w = *reinterpret_cast<const uint4 *>(x + row * stride + d);
-        else atomicOr(c.status, LA_KV8_BAD);                       // stored as zeros
-        *reinterpret_cast<uint4 *>(sm + place(a + t, d)) = w;
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    constexpr int C = HD / 8, B = 4;                               // 16-byte pieces of a row; loads in flight
+    for (int i0 = tid; i0 < (b - a) * C; i0 += B * kStoreThreads) {
+        uint4 w[B];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float lo = __uint_as_float(u[k] << 16), hi = __uint_as_float(u[k] & 0xffff0000u);
-            if (finite_f(lo)) amax = fmaxf(amax, fabsf(lo));
-            if (finite_f(hi)) amax = fmaxf(amax, fabsf(hi));
+        for (int k = 0; k < B; ++k) {
+            const int i = i0 + k * kStoreThreads, t = i / C, d = (i % C) * 8;
+            w[k] = make_uint4(0, 0, 0, 0);
+            if (t >= b - a) continue;
+            const int row = r.row_idx ? r.row_idx[row0 + t] : row0 + t;
+            if (static_cast<unsigned>(row) < static_cast<unsigned>(n_src)) w[k] = *reinterpret_cast<const uint4 *>(x + row * stride + d);
+            else atomicOr(c.status, LA_KV8_BAD);                   // stored as zeros
+        }
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const int i = i0 + k * kStoreThreads, t = i / C, d = (i % C) * 8;
+            if (t < b - a) *reinterpret_cast<uint4 *>(sm + place(a + t, d)) = w[k];
+            const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float lo = __uint_as_float(u[q] << 16), hi = __uint_as_float(u[q] & 0xffff0000u);
+                if (finite_f(lo)) amax = fmaxf(amax, fabsf(lo));
+                if (finite_f(hi)) amax = fmaxf(amax, fabsf(hi));
+            }
         }
     }
     amax = warp_max(amax);
@@ -286,14 +302,149 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_
     }
 }
 
+// A decoding step appends a row or a few to each sequence: one warp per
+// (sequence, touched page, KV head, layer) writes both K and V.  A CTA per
+// item, as above, spends its time on launching and barriers for 512 bytes of
+// input (64 sequences x 32 layers x 8 heads: 129 us against this kernel's).
+constexpr int kFewRows = 8, kFewWarps = 4;
+
+template <int HD>
+__global__ void __launch_bounds__(32 * kFewWarps) k_kv8_store_few(la_kv8_cache c, la_kv8_rows r, const int4 *record, int touched,
+                                                                  long long items) {
+    constexpr int E = HD / 32;                                     // a lane's elements of a row
+    pdl_trigger();
+    pdl_wait();
+    const long long item = static_cast<long long>(blockIdx.x) * kFewWarps + (threadIdx.x >> 5);
+    if (item >= items) return;
+    const int lane = threadIdx.x & 31;
+    const int head = static_cast<int>(item % c.n_kv_heads);
+    const long long up = item / c.n_kv_heads;
+    const int isv = static_cast<int>(up & 1), layer = static_cast<int>((up >> 1) % c.n_layers);
+    const int sj = static_cast<int>((up >> 1) / c.n_layers), s = sj / touched, j = sj % touched;
+    const int4 rec = record[s];
+    const int first = r.row_start ? r.row_start[s] : s;
+    const int n = rec.x, len = rec.y;
+    if (n <= 0) return;
+    const int pj = len / c.page + j;
+    const int a = j == 0 ? len % c.page : 0;
+    const long long left = static_cast<long long>(len) + n - static_cast<long long>(pj) * c.page;
+    if (left <= 0) return;
+    const int b = static_cast<int>(min(left, static_cast<long long>(c.page)));
+    const int to = j == 0 ? rec.w : kv8_page(c, s, pj), from = a > 0 ? rec.z : -1;
+    if (to < 0) return;
+    const int row0 = first + pj * c.page + a - len;
+    const long long blk = kv8_block(c, layer, to, head), old = from >= 0 ? kv8_block(c, layer, from, head) : 0;
+    const long long bytes = static_cast<long long>(c.page) * HD;
+    float *scales = isv ? c.v_scale : c.k_scale;
+    uint8_t *pool = static_cast<uint8_t *>(isv ? c.v : c.k), *out = pool + blk * bytes;
+    const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(isv ? r.v : r.k) + layer * (isv ? r.v_layer_stride : r.k_layer_stride) +
+                             static_cast<long long>(head) * HD + lane * E;
+    const long long stride = isv ? r.v_stride : r.k_stride;
+    const float was = from >= 0 ? scales[old] : 0.f;
+    // This lane's elements of row i, as bf16 pairs.
+    uint32_t w[E / 2];
+    auto load = [&](int i) {
+        const int row = r.row_idx ? r.row_idx[row0 + i] : row0 + i;
+        const bool in = static_cast<unsigned>(row) < static_cast<unsigned>(r.n_src);
+        if (!in && lane == 0) atomicOr(c.status, LA_KV8_BAD);      // stored as zeros
+        if constexpr (E == 4) {
+            const uint2 u = in ? *reinterpret_cast<const uint2 *>(x + row * stride) : make_uint2(0, 0);
+            w[0] = u.x;
+            w[1] = u.y;
+        } else {
+            w[0] = in ? *reinterpret_cast<const uint32_t *>(x + row * stride) : 0u;
+        }
+    };
+    float amax = 0.f;
+    for (int i = 0; i < b - a; ++i) {
+        load(i);
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) {
+            const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xffff0000u);
+            if (finite_f(lo)) amax = fmaxf(amax, fabsf(lo));
+            if (finite_f(hi)) amax = fmaxf(amax, fabsf(hi));
+        }
+    }
+    const int e_old = from >= 0 ? kv8_scale_exponent(was) : kKv8MinExp;
+    const int e = max(e_old, kv8_exponent(warp_max(amax)));
+    __syncwarp();                                                  // every lane has the old scale
+    if (lane == 0) scales[blk] = kv8_power(e);
+    if (from >= 0 && (e > e_old || from != to)) {                  // stored tokens: a grown scale, or a copy
+        const uint8_t *in = pool + old * bytes;
+        const float f = kv8_power(e_old - e);
+        // 16 bytes at a time: of K from token t0's dims, of V's dim d from
+        // token t0.  A piece that ends behind the stored tokens keeps the
+        // bytes there (this warp alone writes the block).
+        const int pieces = isv ? (a + 15) / 16 : a * (HD / 16), total = isv ? HD * pieces : pieces;
+        constexpr int B = 4;
+        for (int i0 = lane; i0 < total; i0 += 32 * B) {
+            uint4 o[B], v[B];
+            long long at[B];
+            int keep[B];                                           // bytes of the piece that belong to stored tokens
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                const int i = i0 + 32 * k;
+                if (i >= total) {
+                    keep[k] = 0;
+                    continue;
+                }
+                const int d = isv ? i / pieces : 0, t0 = isv ? (i % pieces) * 16 : 16 * i;
+                at[k] = isv ? static_cast<long long>(d) * c.page + t0 : static_cast<long long>(t0);
+                keep[k] = isv ? min(a - t0, 16) : 16;
+                v[k] = *reinterpret_cast<const uint4 *>(in + at[k]);
+                if (keep[k] < 16) o[k] = *reinterpret_cast<const uint4 *>(out + at[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < B; ++k) {
+                if (keep[k] == 0) continue;
+                uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                const uint32_t q[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    if (e > e_old)
+                        u[y] = kv8_shrink(u[y] & 255u, f) | kv8_shrink(u[y] >> 8 & 255u, f) << 8 | kv8_shrink(u[y] >> 16 & 255u, f) << 16 |
+                               kv8_shrink(u[y] >> 24, f) << 24;
+                    const int m = keep[k] - 4 * y;
+                    const uint32_t mask = m >= 4 ? 0xffffffffu : m <= 0 ? 0u : (1u << (8 * m)) - 1u;
+                    u[y] = keep[k] < 16 ? (u[y] & mask) | (q[y] & ~mask) : u[y];
+                }
+                *reinterpret_cast<uint4 *>(out + at[k]) = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+        }
+        __syncwarp();                                              // a kept piece may hold bytes that new tokens replace
+    }
+    const float f = kv8_power(-e);
+    for (int i = 0; i < b - a; ++i) {
+        if (b - a > 1) load(i);                                    // a single row is still in registers
+        uint32_t q[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) q[k] = kv8_byte(__uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16) * f);
+        if (!isv) {
+            uint8_t *dst = out + static_cast<long long>(a + i) * HD + lane * E;
+            if constexpr (E == 4) *reinterpret_cast<uint32_t *>(dst) = q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24;
+            else *reinterpret_cast<uint16_t *>(dst) = static_cast<uint16_t>(q[0] | q[1] << 8);
+        } else {
+#pragma unroll
+            for (int k = 0; k < E; ++k) out[static_cast<long long>(lane * E + k) * c.page + a + i] = static_cast<uint8_t>(q[k]);
+        }
+    }
+}
+
 cudaError_t kv8_append_launch(const la_kv8_cache &c, const la_kv8_rows &r, int *ws, cudaStream_t s) {
     cudaError_t e = launch_k(k_kv8_plan, dim3(1), dim3(kPlanThreads), 0, s, c, r.row_start, r.n_rows, r.max_rows, r.stored, ws);
     if (e != cudaSuccess) return e;
-    const int touched = (r.max_rows - 1) / c.page + 2;
+    const int touched = kv8_touched(r.max_rows, c.page);
+    const int4 *record = reinterpret_cast<const int4 *>(ws);
+    const long long items = 2ll * c.n_seqs * touched * c.n_kv_heads * c.n_layers;
+    if (r.max_rows <= kFewRows && items / kFewWarps < 0x7fffffffll) {
+        const dim3 g(static_cast<unsigned>((items + kFewWarps - 1) / kFewWarps));
+        if (c.head_dim == 128) return launch_k(k_kv8_store_few<128>, g, dim3(32 * kFewWarps), 0, s, c, r, record, touched, items);
+        return launch_k(k_kv8_store_few<64>, g, dim3(32 * kFewWarps), 0, s, c, r, record, touched, items);
+    }
     const dim3 grid(static_cast<unsigned>(c.n_seqs) * touched, c.n_kv_heads, 2 * c.n_layers);
-    const int *src = ws + 2 * c.n_seqs;
-    if (c.head_dim == 128) return launch_k(k_kv8_store<128>, grid, dim3(kStoreThreads), 0, s, c, r, src, touched);
-    return launch_k(k_kv8_store<64>, grid, dim3(kStoreThreads), 0, s, c, r, src, touched);
+    const size_t smem = (static_cast<size_t>(c.page) * c.head_dim + c.page / 16 * 8) * 2;
+    if (c.head_dim == 128) return launch_k(k_kv8_store<128>, grid, dim3(kStoreThreads), smem, s, c, r, record, touched);
+    return launch_k(k_kv8_store<64>, grid, dim3(kStoreThreads), smem, s, c, r, record, touched);
 }
 
 // ------------------------------------------------------------------ fork, free

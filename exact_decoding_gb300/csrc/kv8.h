@@ -44,6 +44,9 @@ __device__ __forceinline__ long long kv8_block(const la_kv8_cache &c, int layer,
     return (static_cast<long long>(layer) * c.n_pages + page) * c.n_kv_heads + head;
 }
 
+// Pages that m >= 1 consecutive tokens can touch.
+__host__ __device__ inline int kv8_touched(int m, int page) { return m == 1 ? 1 : (m - 2) / page + 2; }
+
 // Workspace of one cache: the attention's partial results, or the plans of
 // append and compact (calls that overlap need a workspace each).
 int64_t kv8_workspace_bytes(const la_kv8_cache &c, int nsm);

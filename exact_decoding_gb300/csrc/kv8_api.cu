@@ -121,7 +121,7 @@ int append_body(const la_kv8_cache *c, const la_kv8_rows *rows, void *ws, int64_
     if (!r.row_start) r.max_rows = 1;
     if (r.max_rows <= 0 || r.max_rows > r.n_rows) r.max_rows = r.n_rows;
     if (r.max_rows < 1) r.max_rows = 1;
-    if (static_cast<int64_t>(c->n_seqs) * ((r.max_rows - 1) / c->page + 2) > 0x7fffffffll)
+    if (static_cast<int64_t>(c->n_seqs) * kv8_touched(r.max_rows, c->page) > 0x7fffffffll)
         return bad(where, "n_seqs * max_rows too large for one call");
     int nsm = 0;
     if ((rc = check_workspace(c, ws, ws_bytes, &nsm, where)) != LA_OK) return rc;

@@ -670,7 +670,7 @@ constexpr int kRowsPerSm = 4;   // most CTAs of k_kv8_rows per SM
 
 int64_t kv8_workspace_bytes(const la_kv8_cache &c, int nsm) {
     const int64_t part = static_cast<int64_t>(nsm) * kRowsPerSm * 2 * kRowsQ * (c.head_dim + 2) * 4;
-    const int64_t plans = (std::max<int64_t>(3ll * c.n_seqs + c.n_pages, 4ll * c.n_pages) + 16) * 4;
+    const int64_t plans = (std::max<int64_t>(6ll * c.n_seqs + c.n_pages, 4ll * c.n_pages) + 16) * 4;
     return (std::max(part, plans) + 255) / 256 * 256;
 }
 
