@@ -184,6 +184,25 @@ __device__ __forceinline__ uint32_t kv8_shrink(uint32_t b, float f) {
     return (b & 0x7fu) == 0x7fu ? b : kv8_byte(kv8_value(b) * f);
 }
 
+// Two elements to two bytes, both finite (e4m3 of lo in the low byte).
+__device__ __forceinline__ uint32_t kv8_pair(float lo, float hi) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+// Largest magnitude of bf16 pairs, NaN if any is NaN.
+__device__ __forceinline__ uint32_t kv8_max2(uint32_t m, uint32_t x) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x & 0x7fff7fffu));
+    return r;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// The same among finite elements only, where the fast maximum met others.
+__device__ __forceinline__ float kv8_finite_max(float m, uint32_t w) {
+    if (finite_f(bf16_lo(w))) m = fmaxf(m, fabsf(bf16_lo(w)));
+    if (finite_f(bf16_hi(w))) m = fmaxf(m, fabsf(bf16_hi(w)));
+    return m;
+}
+
 constexpr int kStoreThreads = 256;
 
 // One CTA per (sequence, touched page, KV head, layer, K or V): the page's
@@ -193,11 +212,12 @@ template <int HD>
 __global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_kv8_rows r, const int4 *record, int touched) {
     pdl_trigger();
     pdl_wait();
-    extern __shared__ __align__(16) __nv_bfloat16 sm[];            // [page] rows, 8 elements more after every 16: see V below
+    extern __shared__ __align__(16) __nv_bfloat16 sm[];            // [page] rows, 16 elements more after every 16: see V below
     __shared__ float red[kStoreThreads / 32];
     const int s = blockIdx.x / touched, j = blockIdx.x % touched;
     const int head = blockIdx.y, layer = blockIdx.z >> 1, isv = blockIdx.z & 1;
     const int4 rec = record[s];
+    const int first = r.row_start ? r.row_start[s] : s;
     const int n = rec.x, len = rec.y;
     if (n <= 0) return;
     const int pj = len / c.page + j;
@@ -207,14 +227,14 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_
     const int b = static_cast<int>(min(left, static_cast<long long>(c.page)));
     const int to = j == 0 ? rec.w : kv8_page(c, s, pj), from = a > 0 ? rec.z : -1;
     if (to < 0) return;
-    const int row0 = (r.row_start ? r.row_start[s] : s) + pj * c.page + a - len;
+    const int row0 = first + pj * c.page + a - len;
     const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(isv ? r.v : r.k) +
                              layer * (isv ? r.v_layer_stride : r.k_layer_stride) + static_cast<long long>(head) * HD;
     const long long stride = isv ? r.v_stride : r.k_stride;
     const int tid = threadIdx.x, n_src = r.n_src;
-    auto place = [](int t, int d) { return t * HD + (t >> 4) * 8 + d; };
+    auto place = [](int t, int d) { return t * HD + (t >> 4) * 16 + d; };
 
-    float amax = 0.f;
+    uint32_t top = 0;
     constexpr int C = HD / 8, B = 4;                               // 16-byte pieces of a row; loads in flight
     for (int i0 = tid; i0 < (b - a) * C; i0 += B * kStoreThreads) {
         uint4 w[B];
@@ -231,14 +251,16 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_
         for (int k = 0; k < B; ++k) {
             const int i = i0 + k * kStoreThreads, t = i / C, d = (i % C) * 8;
             if (t < b - a) *reinterpret_cast<uint4 *>(sm + place(a + t, d)) = w[k];
-            const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float lo = __uint_as_float(u[q] << 16), hi = __uint_as_float(u[q] & 0xffff0000u);
-                if (finite_f(lo)) amax = fmaxf(amax, fabsf(lo));
-                if (finite_f(hi)) amax = fmaxf(amax, fabsf(hi));
-            }
+            top = kv8_max2(kv8_max2(kv8_max2(kv8_max2(top, w[k].x), w[k].y), w[k].z), w[k].w);
         }
+    }
+    // Every element finite?  Else the maximum is taken again among those that are.
+    float amax = fmaxf(bf16_lo(top), bf16_hi(top));
+    const bool odd = __syncthreads_or(!finite_f(bf16_lo(top)) || !finite_f(bf16_hi(top)));
+    if (odd) {
+        amax = 0.f;
+        for (int i = tid; i < (b - a) * (HD / 2); i += kStoreThreads)
+            amax = kv8_finite_max(amax, *reinterpret_cast<const uint32_t *>(sm + place(a + i / (HD / 2), 2 * (i % (HD / 2)))));
     }
     amax = warp_max(amax);
     if ((tid & 31) == 0) red[tid >> 5] = amax;
@@ -249,16 +271,16 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_
     float *scales = isv ? c.v_scale : c.k_scale;
     uint8_t *pool = static_cast<uint8_t *>(isv ? c.v : c.k);
     const long long blk = kv8_block(c, layer, to, head), old = from >= 0 ? kv8_block(c, layer, from, head) : 0;
+    const long long bytes = static_cast<long long>(c.page) * HD;
     const int e_old = from >= 0 ? kv8_scale_exponent(scales[old]) : kKv8MinExp;
     const int e = max(e_old, kv8_exponent(amax));
-    const long long bytes = static_cast<long long>(c.page) * HD;
     uint8_t *out = pool + blk * bytes;
     __syncthreads();                                               // every thread has read the old scale
     if (tid == 0) scales[blk] = kv8_power(e);
     // Stored tokens: in a new place, or at a grown scale.
     if (from >= 0 && (e > e_old || from != to)) {
         const uint8_t *was = pool + old * bytes;
-        const float f = kv8_power(e_old - e < -126 ? -126 : e_old - e);
+        const float f = kv8_power(e_old - e);
         for (int i = tid; i < a * HD; i += kStoreThreads) {
             const int at = isv ? (i / a) * c.page + i % a : i;
             out[at] = static_cast<uint8_t>(kv8_shrink(was[at], f));
@@ -269,58 +291,60 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_
     if (!isv) {
         for (int i = tid; i < (b - a) * (HD / 16); i += kStoreThreads) {
             const int t = a + i / (HD / 16), d = (i % (HD / 16)) * 16;
+            const uint4 lo = *reinterpret_cast<const uint4 *>(sm + place(t, d)), hi = *reinterpret_cast<const uint4 *>(sm + place(t, d + 8));
+            const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                w[k] = 0;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) w[k] |= kv8_byte(__bfloat162float(sm[place(t, d + 4 * k + q)]) * f) << (8 * q);
+                const uint32_t p = u[2 * k], q = u[2 * k + 1];
+                w[k] = odd ? kv8_byte(bf16_lo(p) * f) | kv8_byte(bf16_hi(p) * f) << 8 | kv8_byte(bf16_lo(q) * f) << 16 | kv8_byte(bf16_hi(q) * f) << 24
+                           : kv8_pair(bf16_lo(p) * f, bf16_hi(p) * f) | kv8_pair(bf16_lo(q) * f, bf16_hi(q) * f) << 16;
             }
             *reinterpret_cast<uint4 *>(out + static_cast<long long>(t) * HD + d) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     } else {
-        // A warp writes 16-token pieces of neighbouring dims; the padding
-        // keeps its reads of one dim's tokens in different banks.
+        // 16 tokens of two neighbouring dims per thread; a warp covers whole
+        // runs of a dim's tokens, and the padding spreads their reads over the banks.
         const int pieces = c.page / 16;
-        for (int i = tid; i < HD * pieces; i += kStoreThreads) {
-            const int d = i / pieces, t0 = (i % pieces) * 16;
+        for (int i = tid; i < HD / 2 * pieces; i += kStoreThreads) {
+            const int d = 2 * (i / pieces), t0 = (i % pieces) * 16;
             uint8_t *dst = out + static_cast<long long>(d) * c.page + t0;
-            if (t0 >= a && t0 + 16 <= b) {
-                uint32_t w[4];
+            if (t0 >= a && t0 + 16 <= b && !odd) {
+                uint32_t w[2][4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    w[k] = 0;
+                    uint32_t u[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) w[k] |= kv8_byte(__bfloat162float(sm[place(t0 + 4 * k + q, d)]) * f) << (8 * q);
+                    for (int q = 0; q < 4; ++q) u[q] = *reinterpret_cast<const uint32_t *>(sm + place(t0 + 4 * k + q, d));
+                    w[0][k] = kv8_pair(bf16_lo(u[0]) * f, bf16_lo(u[1]) * f) | kv8_pair(bf16_lo(u[2]) * f, bf16_lo(u[3]) * f) << 16;
+                    w[1][k] = kv8_pair(bf16_hi(u[0]) * f, bf16_hi(u[1]) * f) | kv8_pair(bf16_hi(u[2]) * f, bf16_hi(u[3]) * f) << 16;
                 }
-                *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) *reinterpret_cast<uint4 *>(dst + h * c.page) = make_uint4(w[h][0], w[h][1], w[h][2], w[h][3]);
             } else {
                 for (int t = max(t0, a); t < min(t0 + 16, b); ++t)
-                    dst[t - t0] = static_cast<uint8_t>(kv8_byte(__bfloat162float(sm[place(t, d)]) * f));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        dst[h * c.page + t - t0] = static_cast<uint8_t>(kv8_byte(__bfloat162float(sm[place(t, d + h)]) * f));
             }
         }
     }
 }
 
 // A decoding step appends a row or a few to each sequence: one warp per
-// (sequence, touched page, KV head, layer) writes both K and V.  A CTA per
-// item, as above, spends its time on launching and barriers for 512 bytes of
-// input (64 sequences x 32 layers x 8 heads: 129 us against this kernel's).
-constexpr int kFewRows = 8, kFewWarps = 4;
+// (sequence, touched page, KV head, layer, K or V), a CTA for the heads of one
+// (sequence, page, layer).  A CTA per block, as above, spends its time on
+// launching and barriers for 256 bytes of input: 64 sequences x 32 layers x 8
+// heads took 129 us.
+constexpr int kFewRows = 8, kFewWarps = 8;
 
 template <int HD>
-__global__ void __launch_bounds__(32 * kFewWarps) k_kv8_store_few(la_kv8_cache c, la_kv8_rows r, const int4 *record, int touched,
-                                                                  long long items) {
+__global__ void __launch_bounds__(32 * kFewWarps, 4) k_kv8_store_few(la_kv8_cache c, la_kv8_rows r, const int4 *record, int touched) {
     constexpr int E = HD / 32;                                     // a lane's elements of a row
     pdl_trigger();
     pdl_wait();
-    const long long item = static_cast<long long>(blockIdx.x) * kFewWarps + (threadIdx.x >> 5);
-    if (item >= items) return;
     const int lane = threadIdx.x & 31;
-    const int head = static_cast<int>(item % c.n_kv_heads);
-    const long long up = item / c.n_kv_heads;
-    const int isv = static_cast<int>(up & 1), layer = static_cast<int>((up >> 1) % c.n_layers);
-    const int sj = static_cast<int>((up >> 1) / c.n_layers), s = sj / touched, j = sj % touched;
+    const int s = blockIdx.x / touched, j = blockIdx.x % touched, layer = blockIdx.y;
     const int4 rec = record[s];
     const int first = r.row_start ? r.row_start[s] : s;
     const int n = rec.x, len = rec.y;
@@ -333,99 +357,98 @@ __global__ void __launch_bounds__(32 * kFewWarps) k_kv8_store_few(la_kv8_cache c
     const int to = j == 0 ? rec.w : kv8_page(c, s, pj), from = a > 0 ? rec.z : -1;
     if (to < 0) return;
     const int row0 = first + pj * c.page + a - len;
-    const long long blk = kv8_block(c, layer, to, head), old = from >= 0 ? kv8_block(c, layer, from, head) : 0;
-    const long long bytes = static_cast<long long>(c.page) * HD;
-    float *scales = isv ? c.v_scale : c.k_scale;
-    uint8_t *pool = static_cast<uint8_t *>(isv ? c.v : c.k), *out = pool + blk * bytes;
-    const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(isv ? r.v : r.k) + layer * (isv ? r.v_layer_stride : r.k_layer_stride) +
-                             static_cast<long long>(head) * HD + lane * E;
-    const long long stride = isv ? r.v_stride : r.k_stride;
-    const float was = from >= 0 ? scales[old] : 0.f;
-    // This lane's elements of row i, as bf16 pairs.
-    uint32_t w[E / 2];
-    auto load = [&](int i) {
-        const int row = r.row_idx ? r.row_idx[row0 + i] : row0 + i;
-        const bool in = static_cast<unsigned>(row) < static_cast<unsigned>(r.n_src);
-        if (!in && lane == 0) atomicOr(c.status, LA_KV8_BAD);      // stored as zeros
-        if constexpr (E == 4) {
-            const uint2 u = in ? *reinterpret_cast<const uint2 *>(x + row * stride) : make_uint2(0, 0);
-            w[0] = u.x;
-            w[1] = u.y;
-        } else {
-            w[0] = in ? *reinterpret_cast<const uint32_t *>(x + row * stride) : 0u;
-        }
-    };
-    float amax = 0.f;
-    for (int i = 0; i < b - a; ++i) {
-        load(i);
-#pragma unroll
-        for (int k = 0; k < E / 2; ++k) {
-            const float lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xffff0000u);
-            if (finite_f(lo)) amax = fmaxf(amax, fabsf(lo));
-            if (finite_f(hi)) amax = fmaxf(amax, fabsf(hi));
-        }
-    }
-    const int e_old = from >= 0 ? kv8_scale_exponent(was) : kKv8MinExp;
-    const int e = max(e_old, kv8_exponent(warp_max(amax)));
-    __syncwarp();                                                  // every lane has the old scale
-    if (lane == 0) scales[blk] = kv8_power(e);
-    if (from >= 0 && (e > e_old || from != to)) {                  // stored tokens: a grown scale, or a copy
-        const uint8_t *in = pool + old * bytes;
-        const float f = kv8_power(e_old - e);
-        // 16 bytes at a time: of K from token t0's dims, of V's dim d from
-        // token t0.  A piece that ends behind the stored tokens keeps the
-        // bytes there (this warp alone writes the block).
-        const int pieces = isv ? (a + 15) / 16 : a * (HD / 16), total = isv ? HD * pieces : pieces;
-        constexpr int B = 4;
-        for (int i0 = lane; i0 < total; i0 += 32 * B) {
-            uint4 o[B], v[B];
-            long long at[B];
-            int keep[B];                                           // bytes of the piece that belong to stored tokens
-#pragma unroll
-            for (int k = 0; k < B; ++k) {
-                const int i = i0 + 32 * k;
-                if (i >= total) {
-                    keep[k] = 0;
-                    continue;
-                }
-                const int d = isv ? i / pieces : 0, t0 = isv ? (i % pieces) * 16 : 16 * i;
-                at[k] = isv ? static_cast<long long>(d) * c.page + t0 : static_cast<long long>(t0);
-                keep[k] = isv ? min(a - t0, 16) : 16;
-                v[k] = *reinterpret_cast<const uint4 *>(in + at[k]);
-                if (keep[k] < 16) o[k] = *reinterpret_cast<const uint4 *>(out + at[k]);
+    const int bytes = c.page * HD;
+    const long long blk0 = kv8_block(c, layer, to, 0), old0 = from >= 0 ? kv8_block(c, layer, from, 0) : 0;
+    for (int hv = threadIdx.x >> 5; hv < 2 * c.n_kv_heads; hv += blockDim.x >> 5) {
+        const int isv = hv >= c.n_kv_heads, head = isv ? hv - c.n_kv_heads : hv;
+        const long long blk = blk0 + head, old = old0 + head;
+        float *scales = isv ? c.v_scale : c.k_scale;
+        uint8_t *pool = static_cast<uint8_t *>(isv ? c.v : c.k), *out = pool + blk * bytes;
+        const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(isv ? r.v : r.k) + layer * (isv ? r.v_layer_stride : r.k_layer_stride) +
+                                 head * HD + lane * E;
+        const long long stride = isv ? r.v_stride : r.k_stride;
+        const float was = from >= 0 ? scales[old] : 0.f;
+        // This lane's elements of row i, as bf16 pairs.
+        uint32_t w[E / 2];
+        auto load = [&](int i) {
+            const int row = r.row_idx ? r.row_idx[row0 + i] : row0 + i;
+            const bool in = static_cast<unsigned>(row) < static_cast<unsigned>(r.n_src);
+            if (!in && lane == 0) atomicOr(c.status, LA_KV8_BAD);  // stored as zeros
+            if constexpr (E == 4) {
+                const uint2 u = in ? *reinterpret_cast<const uint2 *>(x + row * stride) : make_uint2(0, 0);
+                w[0] = u.x;
+                w[1] = u.y;
+            } else {
+                w[0] = in ? *reinterpret_cast<const uint32_t *>(x + row * stride) : 0u;
             }
+        };
+        float amax = 0.f;
+        for (int i = 0; i < b - a; ++i) {
+            load(i);
 #pragma unroll
-            for (int k = 0; k < B; ++k) {
-                if (keep[k] == 0) continue;
-                uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-                const uint32_t q[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    if (e > e_old)
-                        u[y] = kv8_shrink(u[y] & 255u, f) | kv8_shrink(u[y] >> 8 & 255u, f) << 8 | kv8_shrink(u[y] >> 16 & 255u, f) << 16 |
-                               kv8_shrink(u[y] >> 24, f) << 24;
-                    const int m = keep[k] - 4 * y;
-                    const uint32_t mask = m >= 4 ? 0xffffffffu : m <= 0 ? 0u : (1u << (8 * m)) - 1u;
-                    u[y] = keep[k] < 16 ? (u[y] & mask) | (q[y] & ~mask) : u[y];
-                }
-                *reinterpret_cast<uint4 *>(out + at[k]) = make_uint4(u[0], u[1], u[2], u[3]);
-            }
+            for (int k = 0; k < E / 2; ++k) amax = kv8_finite_max(amax, w[k]);
         }
-        __syncwarp();                                              // a kept piece may hold bytes that new tokens replace
-    }
-    const float f = kv8_power(-e);
-    for (int i = 0; i < b - a; ++i) {
-        if (b - a > 1) load(i);                                    // a single row is still in registers
-        uint32_t q[E];
+        const int e_old = from >= 0 ? kv8_scale_exponent(was) : kKv8MinExp;
+        const int e = max(e_old, kv8_exponent(warp_max(amax)));
+        __syncwarp();                                              // every lane has the old scale
+        if (lane == 0) scales[blk] = kv8_power(e);
+        if (from >= 0 && (e > e_old || from != to)) {              // stored tokens: a grown scale, or a copy
+            const uint8_t *in = pool + old * bytes;
+            const float f = kv8_power(e_old - e);
+            // 16 bytes at a time: of K from token t0's dims, of V's dim d from
+            // token t0.  A piece that ends behind the stored tokens keeps the
+            // bytes there (this warp alone writes the block).
+            const int pieces = (a + 15) / 16, total = isv ? HD * pieces : a * (HD / 16);
+            constexpr int B = 2;
+            for (int i0 = lane; i0 < total; i0 += 32 * B) {
+                uint4 o[B], v[B];
+                int at[B], keep[B];                                // place; bytes of the piece that belong to stored tokens
 #pragma unroll
-        for (int k = 0; k < E; ++k) q[k] = kv8_byte(__uint_as_float(k & 1 ? w[k >> 1] & 0xffff0000u : w[k >> 1] << 16) * f);
-        if (!isv) {
-            uint8_t *dst = out + static_cast<long long>(a + i) * HD + lane * E;
-            if constexpr (E == 4) *reinterpret_cast<uint32_t *>(dst) = q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24;
-            else *reinterpret_cast<uint16_t *>(dst) = static_cast<uint16_t>(q[0] | q[1] << 8);
-        } else {
+                for (int k = 0; k < B; ++k) {
+                    const int i = i0 + 32 * k, d = i / pieces, t0 = (i - d * pieces) * 16;
+                    at[k] = isv ? d * c.page + t0 : 16 * i;
+                    keep[k] = i >= total ? 0 : isv ? min(a - t0, 16) : 16;
+                    if (keep[k] > 0) v[k] = *reinterpret_cast<const uint4 *>(in + at[k]);
+                    if (keep[k] > 0 && keep[k] < 16) o[k] = *reinterpret_cast<const uint4 *>(out + at[k]);
+                }
 #pragma unroll
-            for (int k = 0; k < E; ++k) out[static_cast<long long>(lane * E + k) * c.page + a + i] = static_cast<uint8_t>(q[k]);
+                for (int k = 0; k < B; ++k) {
+                    if (keep[k] == 0) continue;
+                    uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                    if (e > e_old) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            u[y] = kv8_shrink(u[y] & 255u, f) | kv8_shrink(u[y] >> 8 & 255u, f) << 8 | kv8_shrink(u[y] >> 16 & 255u, f) << 16 |
+                                   kv8_shrink(u[y] >> 24, f) << 24;
+                    }
+                    if (keep[k] < 16) {
+                        const uint32_t q[4] = {o[k].x, o[k].y, o[k].z, o[k].w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const int m = keep[k] - 4 * y;
+                            const uint32_t mask = m >= 4 ? 0xffffffffu : m <= 0 ? 0u : (1u << (8 * m)) - 1u;
+                            u[y] = (u[y] & mask) | (q[y] & ~mask);
+                        }
+                    }
+                    *reinterpret_cast<uint4 *>(out + at[k]) = make_uint4(u[0], u[1], u[2], u[3]);
+                }
+            }
+            __syncwarp();                                          // a kept piece may hold bytes that new tokens replace
+        }
+        const float f = kv8_power(-e);
+        for (int i = 0; i < b - a; ++i) {
+            if (b - a > 1) load(i);                                // a single row is still in registers
+            uint32_t q[E];
+#pragma unroll
+            for (int k = 0; k < E; ++k) q[k] = kv8_byte((k & 1 ? bf16_hi(w[k >> 1]) : bf16_lo(w[k >> 1])) * f);
+            if (!isv) {
+                uint8_t *dst = out + (a + i) * HD + lane * E;
+                if constexpr (E == 4) *reinterpret_cast<uint32_t *>(dst) = q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24;
+                else *reinterpret_cast<uint16_t *>(dst) = static_cast<uint16_t>(q[0] | q[1] << 8);
+            } else {
+#pragma unroll
+                for (int k = 0; k < E; ++k) out[(lane * E + k) * c.page + a + i] = static_cast<uint8_t>(q[k]);
+            }
         }
     }
 }
@@ -435,14 +458,14 @@ cudaError_t kv8_append_launch(const la_kv8_cache &c, const la_kv8_rows &r, int *
     if (e != cudaSuccess) return e;
     const int touched = kv8_touched(r.max_rows, c.page);
     const int4 *record = reinterpret_cast<const int4 *>(ws);
-    const long long items = 2ll * c.n_seqs * touched * c.n_kv_heads * c.n_layers;
-    if (r.max_rows <= kFewRows && items / kFewWarps < 0x7fffffffll) {
-        const dim3 g(static_cast<unsigned>((items + kFewWarps - 1) / kFewWarps));
-        if (c.head_dim == 128) return launch_k(k_kv8_store_few<128>, g, dim3(32 * kFewWarps), 0, s, c, r, record, touched, items);
-        return launch_k(k_kv8_store_few<64>, g, dim3(32 * kFewWarps), 0, s, c, r, record, touched, items);
+    const unsigned blocks = static_cast<unsigned>(c.n_seqs) * touched;
+    if (r.max_rows <= kFewRows) {
+        const dim3 grid(blocks, c.n_layers), block(32 * std::min(kFewWarps, 2 * c.n_kv_heads));
+        if (c.head_dim == 128) return launch_k(k_kv8_store_few<128>, grid, block, 0, s, c, r, record, touched);
+        return launch_k(k_kv8_store_few<64>, grid, block, 0, s, c, r, record, touched);
     }
-    const dim3 grid(static_cast<unsigned>(c.n_seqs) * touched, c.n_kv_heads, 2 * c.n_layers);
-    const size_t smem = (static_cast<size_t>(c.page) * c.head_dim + c.page / 16 * 8) * 2;
+    const dim3 grid(blocks, c.n_kv_heads, 2 * c.n_layers);
+    const size_t smem = static_cast<size_t>(c.page) * (c.head_dim + 1) * 2;   // 16 elements for every 16 rows
     if (c.head_dim == 128) return launch_k(k_kv8_store<128>, grid, dim3(kStoreThreads), smem, s, c, r, record, touched);
     return launch_k(k_kv8_store<64>, grid, dim3(kStoreThreads), smem, s, c, r, record, touched);
 }
