@@ -601,6 +601,648 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
     }
 }
 
+// ------------------------------------------------------------------ many query vectors per KV head
+// k_kv8_tiles: 128 query vectors per unit and 128 keys per tile on the
+// tcgen05 tensor cores.  With more than a few query vectors per KV head the
+// products, not the bytes, bound the attention.
+//   warps 4..7   turn a tile's e4m3 bytes (or the new rows' bf16) into fp16
+//                operands in shared memory (128-byte swizzle): K [128 keys x
+//                HD], V^T [HD x 128 keys], two buffers each; the next tile's
+//                bytes are in registers meanwhile
+//   warp 8       issues S = Q K^T (Q from tensor memory) of tile i + 1 and
+//                then O += P V (P from tensor memory) of tile i
+//   warps 0..3   softmax: thread = query vector; P replaces S in tensor memory
+// O stays in tensor memory.  Its scale follows the running maximum only when
+// that has grown by 2^8 since (fp16 weights up to 2^8 lose nothing), so O is
+// rarely read back.  Units are split and joined like those of k_kv8_rows.
+constexpr int kTileQ = 128, kTileK = 128;
+constexpr int kOperandWarps = 4, kMmaWarp = 4 + kOperandWarps;
+constexpr int kTileThreads = 32 * (kMmaWarp + 1);   // 9 warps: at most 3 to a quarter of an SM, 168 registers each
+constexpr float kLazy = 8.f;
+
+template <int HD>
+struct Tiles {
+    static constexpr uint32_t k_block = kTileK * 128;              // [128 keys x 64 dims]
+    static constexpr uint32_t v_block = HD * 128;                  // [HD dims x 64 keys]
+    static constexpr uint32_t k_bytes = HD / 64 * k_block, v_bytes = 2 * v_block;
+    static constexpr uint32_t k_off = 0, v_off = 2 * k_bytes;      // two buffers each
+    static constexpr uint32_t meta_off = v_off + 2 * v_bytes;      // [4] tiles: kf[4], vx[4], live[4], odd
+    static constexpr uint32_t red_off = meta_off + 4 * 64;         // [2][2][8] maxima of the new rows' tile
+    static constexpr uint32_t bar_off = red_off + 128;
+    static constexpr uint32_t tiles_off = bar_off + 24 * 8 + (kMmaWarp + 1) * 8;
+    static size_t bytes(int n_seqs) { return tiles_off + (static_cast<size_t>(n_seqs) + 1) * 8 + 1024; }
+};
+// TMEM columns: S of even and odd tiles (P over their first halves), O, Q.
+constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kColAll = 512;
+
+struct Kv8Meta {
+    float kf[4];   // per 32 keys: factor of K, exponent of V, keys that count
+    int vx[4];
+    int live[4];
+    int odd;       // new rows: V holds a NaN or infinity
+    int pad[3];
+};
+static_assert(sizeof(Kv8Meta) == 64, "layout");
+
+// kind::f16 with fp16 operands, fp32 accumulation.
+__device__ constexpr uint32_t idesc_f16(int m, int n) {
+    return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_one(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The pieces of work of one worker, in order; every role of the CTA walks them.
+struct Kv8Walk {
+    long long at, end, skip;
+};
+struct Kv8Piece {
+    int s, head, qv0, nqv;
+    int k0, k1;          // key tiles
+    bool all, begins;    // the whole unit; its first piece
+    Kv8Seq sq;
+};
+__device__ __forceinline__ bool kv8_next(const Kv8Args &p, const long long *tiles, Kv8Walk &w, Kv8Piece &u) {
+    while (w.at < w.end) {
+        u.s = kv8_find(tiles, p.c.n_seqs, w.at);
+        u.sq = kv8_seq(p, u.s);
+        const int kt = u.sq.ktiles();
+        if (p.whole) {
+            const long long units = (tiles[u.s + 1] - w.at) / kt;   // of this slot from `at` on
+            if (w.skip >= units) {
+                w.skip -= units;
+                w.at = tiles[u.s + 1];
+                continue;
+            }
+            w.at += w.skip * kt;
+            w.skip = p.workers - 1;
+        }
+        const int unit = static_cast<int>((w.at - tiles[u.s]) / kt), v0 = static_cast<int>((w.at - tiles[u.s]) % kt);
+        const int v1 = static_cast<int>(min(static_cast<long long>(kt), v0 + (w.end - w.at)));
+        u.k0 = max(v0 - kUnitCost, 0);
+        u.k1 = max(v1 - kUnitCost, 0);
+        u.all = v0 == 0 && v1 == kt;
+        u.begins = v0 == 0;
+        u.head = unit / u.sq.qtiles;
+        u.qv0 = (unit % u.sq.qtiles) * p.q_tile;
+        u.nqv = min(p.q_tile, u.sq.rows * p.gq - u.qv0);
+        w.at += v1 - v0;
+        return true;
+    }
+    return false;
+}
+
+// 16 e4m3 bytes as 32 bytes of fp16.
+__device__ __forceinline__ void e4m3x16_f16(const uint4 &w, uint4 &a, uint4 &b) {
+    e4m3x4_f16(w.x, a.x, a.y);
+    e4m3x4_f16(w.y, a.z, a.w);
+    e4m3x4_f16(w.z, b.x, b.y);
+    e4m3x4_f16(w.w, b.z, b.w);
+}
+__device__ __forceinline__ void st_shared(uint32_t at, const uint4 &v) { st_shared_u32x4(at, v.x, v.y, v.z, v.w); }
+
+template <int HD>
+__global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_constant__ Kv8Args p) {
+    using Lay = Tiles<HD>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    const uint32_t sm = smem_u32(smem);
+    Kv8Meta *meta = reinterpret_cast<Kv8Meta *>(smem + Lay::meta_off);
+    float *red = reinterpret_cast<float *>(smem + Lay::red_off);
+    long long *tiles = reinterpret_cast<long long *>(smem + Lay::tiles_off);
+    const uint32_t bars = sm + Lay::bar_off;
+    auto k_full = [&](int b) { return bars + 8 * b; };             // operand warps
+    auto k_empty = [&](int b) { return bars + 8 * (2 + b); };      // commit of S
+    auto v_full = [&](int b) { return bars + 8 * (4 + b); };
+    auto v_empty = [&](int b) { return bars + 8 * (6 + b); };      // commit of O
+    auto s_full = [&](int b) { return bars + 8 * (8 + b); };
+    auto p_full = [&](int b) { return bars + 8 * (10 + b); };      // 4 softmax warps
+    auto m_full = [&](int t) { return bars + 8 * (12 + t); };      // meta of tile % 4
+    auto o_full = [&](int b) { return bars + 8 * (16 + b); };      // commit of O
+    const uint32_t q_full = bars + 8 * 18, r_full = bars + 8 * 19, drain = bars + 8 * 20;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::bar_off + 8 * 21);
+    long long *warp_sum = reinterpret_cast<long long *>(smem + Lay::bar_off + 24 * 8);
+
+    const la_kv8_cache &c = p.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(k_full(b), kOperandWarps);
+            mbar_init(k_empty(b), 1);
+            mbar_init(v_full(b), kOperandWarps);
+            mbar_init(v_empty(b), 1);
+            mbar_init(s_full(b), 1);
+            mbar_init(p_full(b), 4);
+            mbar_init(o_full(b), 1);
+        }
+        for (int t = 0; t < 4; ++t) mbar_init(m_full(t), 1);
+        mbar_init(q_full, 4);
+        mbar_init(r_full, kOperandWarps);
+        mbar_init(drain, 1);
+        fence_barrier_init();
+    }
+    // Tensor memory is taken once the kernel before has finished, and the one
+    // behind may start only when it is taken: neither can wait for the other's.
+    pdl_wait();
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(tmem_slot), kColAll);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    kv8_plan(p, tiles, warp_sum);   // barriers inside
+    tc_fence_after();
+    pdl_trigger();
+    const uint32_t tmem = *tmem_slot;
+    const long long total = tiles[c.n_seqs];
+    const int workers = kv8_workers(p, total);
+    Kv8Walk walk{0, total, static_cast<long long>(blockIdx.x)};
+    if (!p.whole) {
+        const bool none = static_cast<int>(blockIdx.x) >= workers;
+        walk.at = none ? 0 : kv8_share(total, blockIdx.x, workers);
+        walk.end = none ? 0 : kv8_share(total, blockIdx.x + 1, workers);
+    }
+    Kv8Piece u;
+    int it = 0;          // key tiles so far, the same count in every role: buffer it & 1, its use it >> 1
+    bool ok = true;
+    unsigned *err = c.status;
+
+    if (warp >= 4 && warp < kMmaWarp) {
+        // ================================================ operands
+        const int w = warp - 4, r8 = lane & 7, cq = lane >> 3;
+        int new_tiles = 0;
+        constexpr int NR = HD / (4 * kOperandWarps);   // 16-byte pieces of K, and of V, per thread and tile
+        const uint8_t *kp = static_cast<const uint8_t *>(c.k), *vp = static_cast<const uint8_t *>(c.v);
+        while (ok && kv8_next(p, tiles, walk, u)) {
+            const Kv8Seq sq = u.sq;
+            // piece i of this thread: K row and 16-dim chunk, V dim and 16-key chunk
+            auto k_row = [&](int i) { return w * (kTileK / kOperandWarps) + r8 + 8 * (HD == 128 ? i >> 1 : i); };
+            auto k_chunk = [&](int i) { return HD == 128 ? cq + 4 * (i & 1) : cq; };
+            auto v_dim = [&](int i) { return w * (HD / kOperandWarps) + r8 + 8 * (i >> 1); };
+            auto v_chunk = [&](int i) { return cq + 4 * (i & 1); };
+            const int c_first = max(u.k0, sq.ntiles);   // first cached tile of this piece
+            // Pages of cached tile kt: lane l < 4 holds that of keys 32 l .. of the tile.
+            auto pages = [&](int kt) {
+                const int key = (kt - sq.ntiles) * kTileK + 32 * (lane & 3);
+                return kt < u.k1 && key < sq.len ? kv8_page(c, u.s, key / c.page) : -1;
+            };
+            uint4 kraw[NR], vraw[NR];
+            auto load_k = [&](int kt, int pg) {
+                const int pid = __shfl_sync(0xffffffffu, pg, w * (kTileK / kOperandWarps) / 32);
+                const uint8_t *src = kp + kv8_block(c, p.a.layer, max(pid, 0), u.head) * c.page * HD;
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    const int in_page = ((kt - sq.ntiles) * kTileK + k_row(i)) % c.page;
+                    kraw[i] = pid < 0 ? make_uint4(0, 0, 0, 0) : __ldcg(reinterpret_cast<const uint4 *>(src + in_page * HD + 16 * k_chunk(i)));
+                }
+            };
+            auto load_v = [&](int kt, int pg) {
+#pragma unroll
+                for (int i = 0; i < NR; ++i) {
+                    const int ch = v_chunk(i), key = (kt - sq.ntiles) * kTileK + 16 * ch;
+                    const int pid = __shfl_sync(0xffffffffu, pg, ch >> 1), live = pid < 0 ? 0 : min(max(sq.len - key, 0), 16);
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (live > 0) {
+                        x = __ldcg(reinterpret_cast<const uint4 *>(vp + (kv8_block(c, p.a.layer, pid, u.head) * HD + v_dim(i)) * c.page + key % c.page));
+                        if (live < 16) {   // bytes behind the last token may be anything
+                            const int n0 = live, n1 = live - 4, n2 = live - 8, n3 = live - 12;
+                            auto cut = [](uint32_t a, int n) { return n >= 4 ? a : n <= 0 ? 0u : a & ((1u << (8 * n)) - 1u); };
+                            x = make_uint4(cut(x.x, n0), cut(x.y, n1), cut(x.z, n2), cut(x.w, n3));
+                        }
+                    }
+                    vraw[i] = x;
+                }
+            };
+            int pg_now = pages(c_first), pg_next = pages(c_first + 1);
+            if (c_first < u.k1) {
+                load_k(c_first, pg_now);
+                load_v(c_first, pg_now);
+            }
+            for (int kt = u.k0; ok && kt < u.k1; ++kt, ++it) {
+                const int b = it & 1, use = it >> 1;
+                const uint32_t sk = sm + Lay::k_off + b * Lay::k_bytes, sv = sm + Lay::v_off + b * Lay::v_bytes;
+                if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(k_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
+                if (!ok) break;
+                if (kt >= sq.ntiles) {
+                    if (w == 0 && lane < 4) {
+                        Kv8Meta &mt = meta[it & 3];
+                        const int key = (kt - sq.ntiles) * kTileK + 32 * lane;
+                        const bool have = pg_now >= 0;
+                        const long long blk = kv8_block(c, p.a.layer, max(pg_now, 0), u.head);
+                        mt.kf[lane] = have ? c.k_scale[blk] : 0.f;
+                        mt.vx[lane] = have ? exponent_of(c.v_scale[blk]) : 0;
+                        mt.live[lane] = have ? min(max(sq.len - key, 0), 32) : 0;
+                        if (lane == 0) mt.odd = 0;
+                    }
+                    if (w == 0) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_one(m_full(it & 3));
+                    }
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) {
+                        uint4 x, y;
+                        e4m3x16_f16(kraw[i], x, y);
+                        const int r = k_row(i), ch = 2 * (k_chunk(i) & 3);
+                        const uint32_t at = sk + (k_chunk(i) >> 2) * Lay::k_block + r * 128;
+                        st_shared(at + ((ch ^ r8) << 4), x);
+                        st_shared(at + (((ch + 1) ^ r8) << 4), y);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_one(k_full(b));
+                    if (kt + 1 < u.k1) load_k(kt + 1, pg_next);
+                    if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(v_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
+                    if (!ok) break;
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) {
+                        uint4 x, y;
+                        e4m3x16_f16(vraw[i], x, y);
+                        const int ch = 2 * (v_chunk(i) & 3);
+                        const uint32_t at = sv + (v_chunk(i) >> 2) * Lay::v_block + v_dim(i) * 128;
+                        st_shared(at + ((ch ^ r8) << 4), x);
+                        st_shared(at + (((ch + 1) ^ r8) << 4), y);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_one(v_full(b));
+                    if (kt + 1 < u.k1) load_v(kt + 1, pg_next);
+                    pg_now = pg_next;
+                    pg_next = pages(kt + 2);
+                } else {
+                    // New rows: bf16, scaled by a power of two for the whole tile.
+                    const int key0 = kt * kTileK, nkeys = min(kTileK, sq.rows - key0);
+                    const __nv_bfloat16 *kn = static_cast<const __nv_bfloat16 *>(p.a.k) + (sq.first + key0) * p.a.k_stride + u.head * HD;
+                    const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + u.head * HD;
+                    constexpr int NT = 32 * kOperandWarps;
+                    const int ot = w * 32 + lane;
+                    constexpr int C8 = HD / 8;      // 16-byte pieces of a row
+                    float ak = 0.f, av = 0.f;
+                    bool odd = false;
+                    for (int i = ot; i < nkeys * C8; i += NT) {
+                        const int r = i / C8, d = 8 * (i % C8);
+                        const uint4 a = *reinterpret_cast<const uint4 *>(kn + r * p.a.k_stride + d), v = *reinterpret_cast<const uint4 *>(vn + r * p.a.v_stride + d);
+                        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const float e = bf16_bits(h ? x[k] >> 16 : x[k] & 0xffffu), f = bf16_bits(h ? y[k] >> 16 : y[k] & 0xffffu);
+                                if (is_finite(e)) ak = fmaxf(ak, fabsf(e));
+                                if (is_finite(f)) av = fmaxf(av, fabsf(f));
+                                else odd = true;
+                            }
+                    }
+                    ak = warp_max(ak);
+                    av = warp_max(av);
+                    odd = __any_sync(0xffffffffu, odd);
+                    // The warps' maxima: two halves, one for each buffer, so that no
+                    // warp writes what another still reads.
+                    float *mine = red + 16 * b;
+                    if (lane == 0) {
+                        mine[w] = ak;
+                        mine[8 + w] = odd ? -av - 1.f : av;   // the sign says that it is odd
+                        mbar_arrive_one(r_full);
+                    }
+                    __syncwarp();
+                    ok = __all_sync(0xffffffffu, mbar_wait(r_full, new_tiles & 1, err, LA_KV8_TIMEOUT));
+                    if (!ok) break;
+                    ++new_tiles;
+                    ak = av = 0.f;
+                    odd = false;
+#pragma unroll
+                    for (int k = 0; k < kOperandWarps; ++k) {
+                        ak = fmaxf(ak, mine[k]);
+                        const float x = mine[8 + k];
+                        odd |= x < 0.f;
+                        av = fmaxf(av, x < 0.f ? -x - 1.f : x);
+                    }
+                    const int kx = fit_f16(ak), vx = fit_f16(av);
+                    if (w == 0) {
+                        if (lane < 4) {
+                            Kv8Meta &mt = meta[it & 3];
+                            mt.kf[lane] = power_of(kx);
+                            mt.vx[lane] = vx;
+                            mt.live[lane] = min(max(nkeys - 32 * lane, 0), 32);
+                            if (lane == 0) mt.odd = odd;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_one(m_full(it & 3));
+                    }
+                    const float fk = power_of(-kx), fv = power_of(-vx);
+                    for (int i = ot; i < kTileK * C8; i += NT) {
+                        const int r = i / C8, d8 = i % C8;
+                        const uint4 a = r < nkeys ? *reinterpret_cast<const uint4 *>(kn + r * p.a.k_stride + 8 * d8) : make_uint4(0, 0, 0, 0);
+                        const uint32_t x[4] = {a.x, a.y, a.z, a.w};
+                        uint32_t y[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) y[k] = pack_f16(bf16_bits(x[k] & 0xffffu) * fk, bf16_bits(x[k] >> 16) * fk);
+                        st_shared_u32x4(sk + (d8 >> 3) * Lay::k_block + r * 128 + (((d8 & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_one(k_full(b));
+                    if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(v_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
+                    if (!ok) break;
+                    // Two keys of eight dims at a time, transposed.  A NaN or
+                    // infinity counts 0 here and is added at the end for the
+                    // rows that see it.
+                    for (int i = ot; i < kTileK / 2 * C8; i += NT) {
+                        const int r = 2 * (i / C8), d = 8 * (i % C8);
+                        const uint4 a = r < nkeys ? *reinterpret_cast<const uint4 *>(vn + r * p.a.v_stride + d) : make_uint4(0, 0, 0, 0);
+                        const uint4 e = r + 1 < nkeys ? *reinterpret_cast<const uint4 *>(vn + (r + 1) * p.a.v_stride + d) : make_uint4(0, 0, 0, 0);
+                        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {e.x, e.y, e.z, e.w};
+                        const uint32_t at = sv + (r >> 6) * Lay::v_block + (r & 7) * 2;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            float f0 = bf16_bits(k & 1 ? x[k >> 1] >> 16 : x[k >> 1] & 0xffffu), f1 = bf16_bits(k & 1 ? y[k >> 1] >> 16 : y[k >> 1] & 0xffffu);
+                            f0 = is_finite(f0) ? f0 * fv : 0.f;
+                            f1 = is_finite(f1) ? f1 * fv : 0.f;
+                            const int dim = d + k;
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + dim * 128 + ((((r >> 3) & 7) ^ (dim & 7)) << 4)), "r"(pack_f16(f0, f1)) : "memory");
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_one(v_full(b));
+                }
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        // ================================================ products
+        if (lane == 0) {
+            constexpr uint32_t is = idesc_f16(kTileQ, kTileK), io = idesc_f16(kTileQ, HD);
+            int units = 0;
+            auto product_o = [&](int j, bool begins) {
+                const int b = j & 1;
+                ok = mbar_wait(p_full(b), j >> 1 & 1, err, LA_KV8_TIMEOUT) && mbar_wait(v_full(b), j >> 1 & 1, err, LA_KV8_TIMEOUT);
+                if (!ok) return;
+                tc_fence_after();
+                const uint32_t sv = sm + Lay::v_off + b * Lay::v_bytes, pt = tmem + kColS + 128 * b;
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    const uint64_t d = umma_desc_sw128(sv + kb * Lay::v_block);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) umma_ts(tmem + kColO, pt + kb * 32 + k * 8, d + 2 * k, io, begins && !(kb | k) ? 0u : 1u);
+                }
+                umma_commit(v_empty(b));
+                umma_commit(o_full(b));
+            };
+            while (ok && kv8_next(p, tiles, walk, u)) {
+                if (u.k0 >= u.k1) continue;
+                ok = mbar_wait(q_full, units & 1, err, LA_KV8_TIMEOUT);
+                ++units;
+                const int first = it;
+                for (int kt = u.k0; ok && kt < u.k1; ++kt, ++it) {
+                    const int b = it & 1;
+                    ok = mbar_wait(k_full(b), it >> 1 & 1, err, LA_KV8_TIMEOUT);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sk = sm + Lay::k_off + b * Lay::k_bytes;
+#pragma unroll
+                    for (int db = 0; db < HD / 64; ++db) {
+                        const uint64_t d = umma_desc_sw128(sk + db * Lay::k_block);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            umma_ts(tmem + kColS + 128 * b, tmem + kColQ + db * 32 + k * 8, d + 2 * k, is, (db | k) ? 1u : 0u);
+                    }
+                    umma_commit(s_full(b));
+                    umma_commit(k_empty(b));
+                    if (it > first) product_o(it - 1, it - 1 == first);
+                }
+                if (ok) product_o(it - 1, it - 1 == first);
+            }
+            if (!ok) {   // void: wait (bounded) for the products in flight
+                umma_commit(drain);
+                mbar_wait(drain, 0, err, LA_KV8_TIMEOUT);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ================================================ softmax
+        const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+        const int row = 32 * warp + lane;
+        while (ok && kv8_next(p, tiles, walk, u)) {
+            const Kv8Seq sq = u.sq;
+            const bool in = row < u.nqv, idle = 32 * warp >= u.nqv;   // idle: none of this warp's rows is in use
+            const int qv = u.qv0 + row, myrow = in ? qv / p.gq : 0, myhead = u.head * p.gq + (in ? qv % p.gq : 0);
+            float qf = 0.f;
+            if (u.k0 < u.k1) {
+                if (!idle) {
+                    // q as fp16, scaled by a power of two to fit, into tensor memory
+                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.q) + (sq.first + myrow) * p.a.q_stride + myhead * HD);
+                    float amax = 0.f;
+                    uint4 x[HD / 8];
+#pragma unroll
+                    for (int i = 0; i < HD / 8; ++i) {
+                        x[i] = in ? src[i] : make_uint4(0, 0, 0, 0);
+                        const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float lo = bf16_bits(y[k] & 0xffffu), hi = bf16_bits(y[k] >> 16);
+                            if (is_finite(lo)) amax = fmaxf(amax, fabsf(lo));
+                            if (is_finite(hi)) amax = fmaxf(amax, fabsf(hi));
+                        }
+                    }
+                    const int qx = fit_f16(amax);
+                    const float f = power_of(-qx);
+                    qf = power_of(qx) * p.scale_log2;
+#pragma unroll
+                    for (int i = 0; i < HD / 32; ++i) {   // 32 dims, 16 columns at a time
+                        uint32_t z[16];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint4 v = x[4 * i + k];
+                            z[4 * k] = pack_f16(bf16_bits(v.x & 0xffffu) * f, bf16_bits(v.x >> 16) * f);
+                            z[4 * k + 1] = pack_f16(bf16_bits(v.y & 0xffffu) * f, bf16_bits(v.y >> 16) * f);
+                            z[4 * k + 2] = pack_f16(bf16_bits(v.z & 0xffffu) * f, bf16_bits(v.z >> 16) * f);
+                            z[4 * k + 3] = pack_f16(bf16_bits(v.w & 0xffffu) * f, bf16_bits(v.w >> 16) * f);
+                        }
+                        tmem_st_32x32b_x16(tmem + lanes + kColQ + 16 * i, z);
+                    }
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_one(q_full);
+            }
+            float m = -INFINITY, l = 0.f;
+            bool odd = false;
+            const int first = it;
+            for (int kt = u.k0; ok && kt < u.k1; ++kt, ++it) {
+                const int b = it & 1;
+                ok = mbar_wait(s_full(b), it >> 1 & 1, err, LA_KV8_TIMEOUT) && mbar_wait(m_full(it & 3), it >> 2 & 1, err, LA_KV8_TIMEOUT);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const Kv8Meta &mt = meta[it & 3];
+                odd |= mt.odd != 0;
+                if (!idle) {
+                    const uint32_t ts = tmem + lanes + kColS + 128 * b;
+                    uint32_t see[4];   // keys 32 c .. 32 c + 31 of the tile that this row sees
+                    bool dense = true;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int live = mt.live[k];
+                        see[k] = live >= 32 ? 0xffffffffu : (1u << live) - 1u;
+                        if (kt < sq.ntiles) {
+                            const int key = kt * kTileK + 32 * k;
+                            if (!in) see[k] = 0;
+                            else if (p.a.vis)
+                                see[k] &= key < 256 ? p.a.vis[(static_cast<long long>(sq.first) + myrow) * 8 + key / 32] : 0u;
+                            else
+                                see[k] &= myrow >= key + 31 ? 0xffffffffu : myrow < key ? 0u : (2u << (myrow - key)) - 1u;
+                        }
+                        dense &= see[k] == 0xffffffffu;
+                    }
+                    dense = __all_sync(0xffffffffu, dense);
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t v0[32], v1[32];
+                        tmem_ld_32x32b_x32(ts + 64 * h, v0);
+                        tmem_ld_32x32b_x32(ts + 64 * h + 32, v1);
+                        tmem_ld_wait();
+                        float a = -INFINITY, e = -INFINITY;
+                        if (dense) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                a = fmaxf(a, __uint_as_float(v0[k]));
+                                e = fmaxf(e, __uint_as_float(v1[k]));
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                if (see[2 * h] >> k & 1u) a = fmaxf(a, __uint_as_float(v0[k]));
+                                if (see[2 * h + 1] >> k & 1u) e = fmaxf(e, __uint_as_float(v1[k]));
+                            }
+                        }
+                        // factors are positive: the maximum commutes with them
+                        mx = fmaxf(mx, fmaxf(fmaf(a, mt.kf[2 * h] * qf, static_cast<float>(mt.vx[2 * h])),
+                                             fmaf(e, mt.kf[2 * h + 1] * qf, static_cast<float>(mt.vx[2 * h + 1]))));
+                    }
+                    const bool grow = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float alpha = grow ? ex2(m - mx) : 1.f;
+                        if (grow) m = mx;
+                        l *= alpha;
+                        if (it > first) {
+                            ok = mbar_wait(o_full((it - 1) & 1), (it - 1) >> 1 & 1, err, LA_KV8_TIMEOUT);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int k = 0; k < HD / 32; ++k) {
+                                uint32_t o[32];
+                                tmem_ld_32x32b_x32(tmem + lanes + kColO + 32 * k, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st_32x32b_x32(tmem + lanes + kColO + 32 * k, o);
+                            }
+                            tmem_st_wait();
+                        }
+                    }
+                    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t v[32], w[16];
+                        tmem_ld_32x32b_x32(ts + 32 * k, v);
+                        tmem_ld_wait();
+                        const float f = mt.kf[k] * qf, add = static_cast<float>(mt.vx[k]) - base;
+                        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            float x = ex2(fmaf(__uint_as_float(v[2 * e]), f, add)), y = ex2(fmaf(__uint_as_float(v[2 * e + 1]), f, add));
+                            if (!dense) {
+                                x = see[k] >> (2 * e) & 1u ? x : 0.f;
+                                y = see[k] >> (2 * e + 1) & 1u ? y : 0.f;
+                            }
+                            s0 += x;
+                            s1 += y;
+                            w[e] = pack_f16(x, y);
+                        }
+                        l += (s0 + s1) * power_of(-mt.vx[k]);
+                        tmem_st_32x32b_x16(ts + 16 * k, w);   // over columns of S that are read already
+                    }
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_one(p_full(b));
+            }
+            if (!ok) break;
+            if (it > first) {
+                ok = __all_sync(0xffffffffu, mbar_wait(o_full((it - 1) & 1), (it - 1) >> 1 & 1, err, LA_KV8_TIMEOUT));
+                if (!ok) break;
+                tc_fence_after();
+            }
+            if (idle) continue;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const int slot = 2 * blockIdx.x + (u.begins ? 1 : 0);
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + (sq.first + myrow) * p.a.out_stride + myhead * HD;
+            float *part = p.part + (static_cast<long long>(slot) * kTileQ + row) * HD;
+#pragma unroll
+            for (int k = 0; k < HD / 32; ++k) {
+                uint32_t o[32];
+                __syncwarp();
+                if (it > first) {
+                    tmem_ld_32x32b_x32(tmem + lanes + kColO + 32 * k, o);
+                    tmem_ld_wait();
+                }
+                if (it == first || l == 0.f) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0;
+                }
+                if (odd && in) {   // NaN and infinities of the new rows that this row sees
+                    for (int r = u.k0 * kTileK; r < min(sq.rows, min(u.k1, sq.ntiles) * kTileK); ++r) {
+                        const bool seen = p.a.vis ? r < 256 && (p.a.vis[(static_cast<long long>(sq.first) + myrow) * 8 + r / 32] >> (r % 32) & 1u) : r <= myrow;
+                        if (!seen) continue;
+                        const __nv_bfloat16 *vr = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + r) * p.a.v_stride + u.head * HD + 32 * k;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const float x = __bfloat162float(vr[e]);
+                            if (!is_finite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+                        }
+                    }
+                }
+                if (!in) continue;
+                if (u.all) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * q]) * inv, __uint_as_float(o[8 * e + 2 * q + 1]) * inv);
+                            y[q] = *reinterpret_cast<const uint32_t *>(&h);
+                        }
+                        *reinterpret_cast<uint4 *>(out + 32 * k + 8 * e) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4 *>(part + 32 * k + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                }
+            }
+            if (!u.all && in) *reinterpret_cast<float2 *>(p.part_ml + (static_cast<long long>(slot) * kTileQ + row) * 2) = make_float2(m, l);
+            tc_fence_before();
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kColAll);
+    }
+}
+
 // ------------------------------------------------------------------ join
 // A unit that several workers share: worker ranges are contiguous, so the
 // unit's pieces are those of consecutive workers, the first in its slot 1
@@ -669,7 +1311,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv8_join(const __grid_constant
 constexpr int kRowsPerSm = 4;   // most CTAs of k_kv8_rows per SM
 
 int64_t kv8_workspace_bytes(const la_kv8_cache &c, int nsm) {
-    const int64_t part = static_cast<int64_t>(nsm) * kRowsPerSm * 2 * kRowsQ * (c.head_dim + 2) * 4;
+    const int64_t part = static_cast<int64_t>(nsm) * std::max(kRowsPerSm * kRowsQ, kTileQ) * 2 * (c.head_dim + 2) * 4;
     const int64_t plans = (std::max<int64_t>(6ll * c.n_seqs + c.n_pages, 4ll * c.n_pages) + 16) * 4;
     return (std::max(part, plans) + 255) / 256 * 256;
 }
@@ -715,7 +1357,35 @@ static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
 }
 
 template <int HD>
+static cudaError_t tiles_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
+    using Lay = Tiles<HD>;
+    p.q_tile = kTileQ;
+    p.k_tile = p.n_tile = kTileK;
+    const long long units = ((static_cast<long long>(p.a.n_rows) * p.gq) / kTileQ + p.c.n_seqs) * p.c.n_kv_heads;   // at most
+    const long long tiles = (p.a.max_len + kTileK - 1) / kTileK + (p.a.k ? (p.a.max_rows + kTileK - 1) / kTileK : 0);
+    p.whole = tiles <= 2;   // as for k_kv8_rows
+    p.workers = p.whole ? static_cast<int>(std::min<long long>(units, 1 << 20)) : nsm;
+    p.part = static_cast<float *>(ws);
+    p.part_ml = p.part + static_cast<long long>(nsm) * 2 * kTileQ * HD;
+    static std::atomic<unsigned long long> configured{0};
+    unsigned long long bit = 0;
+    if (attrs_needed(configured, &bit)) {
+        cudaError_t e = cudaFuncSetAttribute(k_kv8_tiles<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(Lay::bytes(LA_KV8_MAX_SEQS)));
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit);
+    }
+    cudaError_t e = launch_k(k_kv8_tiles<HD>, dim3(p.workers), dim3(kTileThreads), Lay::bytes(p.c.n_seqs), s, p);
+    if (e != cudaSuccess || p.whole || p.workers < 2) return e;
+    return launch_k(k_kv8_join<HD>, dim3(p.workers - 1), dim3(kJoinThreads), (static_cast<size_t>(p.c.n_seqs) + 1) * 8, s, p);
+}
+
+// Query vectors per sequence and KV head up to which k_kv8_rows is used.
+constexpr int kFewVectors = 16;
+
+template <int HD>
 static cudaError_t attention_launch_hd(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
+    if (static_cast<long long>(p.a.max_rows) * p.gq > kFewVectors) return tiles_launch<HD>(p, nsm, ws, s);
     if (p.c.page == 32) return rows_launch<HD, 32>(p, nsm, ws, s);
     if (p.c.page == 64) return rows_launch<HD, 64>(p, nsm, ws, s);
     return rows_launch<HD, 128>(p, nsm, ws, s);
