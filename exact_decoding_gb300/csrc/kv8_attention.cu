@@ -29,6 +29,7 @@ struct Kv8Args {
     la_kv8_cache c;
     la_kv8_attn a;
     int gq;            // query heads per KV head
+    int page_log2;
     int q_tile;        // query vectors per unit
     int k_tile, n_tile;   // cached tokens, new rows per key tile
     int whole;         // 1: worker w runs units w, w + workers, ... whole, and nothing is joined
@@ -604,20 +605,24 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
 // ------------------------------------------------------------------ many query vectors per KV head
 // k_kv8_tiles: 128 query vectors per unit and 128 keys per tile on the
 // tcgen05 tensor cores.  With more than a few query vectors per KV head the
-// products, not the bytes, bound the attention.
-//   warps 4..7   turn a tile's e4m3 bytes (or the new rows' bf16) into fp16
+// products and the softmax, not the bytes, bound the attention.
+//   warps 8..11  turn a tile's e4m3 bytes (or the new rows' bf16) into fp16
 //                operands in shared memory (128-byte swizzle): K [128 keys x
-//                HD], V^T [HD x 128 keys], two buffers each; the next tile's
-//                bytes are in registers meanwhile
-//   warp 8       issues S = Q K^T (Q from tensor memory) of tile i + 1 and
-//                then O += P V (P from tensor memory) of tile i
-//   warps 0..3   softmax: thread = query vector; P replaces S in tensor memory
-// O stays in tensor memory.  Its scale follows the running maximum only when
-// that has grown by 2^8 since (fp16 weights up to 2^8 lose nothing), so O is
-// rarely read back.  Units are split and joined like those of k_kv8_rows.
+//                HD], V^T [HD x 128 keys], two buffers each, K one tile ahead
+//                of V; the next tile's bytes are in registers meanwhile
+//   warp 12      issues S = Q K^T of tile i + 1, then O += P V (P from tensor
+//                memory) of tile i
+//   warps 0..3   softmax of the even tiles, warps 4..7 of the odd ones, each
+//                thread a query vector; P replaces S in tensor memory.  Two
+//                groups, since one alone waits for tensor memory half of the
+//                time: 2.4 us per tile.
+// The groups have an O each in tensor memory, added at the end.  An O's scale
+// follows the running maximum only when that has grown by 2^8 since (fp16
+// weights up to 2^8 lose nothing), so it is rarely read back.  Units are split
+// and joined like those of k_kv8_rows.
 constexpr int kTileQ = 128, kTileK = 128;
-constexpr int kOperandWarps = 4, kMmaWarp = 4 + kOperandWarps;
-constexpr int kTileThreads = 32 * (kMmaWarp + 1);   // 9 warps: at most 3 to a quarter of an SM, 168 registers each
+constexpr int kOperandWarps = 4, kMmaWarp = 8 + kOperandWarps;
+constexpr int kTileThreads = 32 * (kMmaWarp + 1);   // 13 warps: 4 to a quarter of an SM, 128 registers a thread
 constexpr float kLazy = 8.f;
 
 template <int HD>
@@ -626,14 +631,17 @@ struct Tiles {
     static constexpr uint32_t v_block = HD * 128;                  // [HD dims x 64 keys]
     static constexpr uint32_t k_bytes = HD / 64 * k_block, v_bytes = 2 * v_block;
     static constexpr uint32_t k_off = 0, v_off = 2 * k_bytes;      // two buffers each
-    static constexpr uint32_t meta_off = v_off + 2 * v_bytes;      // [4] tiles: kf[4], vx[4], live[4], odd
+    static constexpr uint32_t q_off = v_off + 2 * v_bytes;         // Q [128 x HD]
+    static constexpr uint32_t meta_off = q_off + k_bytes;          // [4] Kv8Meta of the last tiles
     static constexpr uint32_t red_off = meta_off + 4 * 64;         // [2][2][8] maxima of the new rows' tile
-    static constexpr uint32_t bar_off = red_off + 128;
+    static constexpr uint32_t ml_off = red_off + 128;              // [2 groups][128] running maximum and sum
+    static constexpr uint32_t odd_off = ml_off + 2 * kTileQ * 8;   // [2 groups]
+    static constexpr uint32_t bar_off = odd_off + 16;
     static constexpr uint32_t tiles_off = bar_off + 24 * 8 + (kMmaWarp + 1) * 8;
     static size_t bytes(int n_seqs) { return tiles_off + (static_cast<size_t>(n_seqs) + 1) * 8 + 1024; }
 };
-// TMEM columns: S of even and odd tiles (P over their first halves), O, Q.
-constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kColAll = 512;
+// TMEM columns: S of even and odd tiles (P over their first halves), then their O.
+constexpr uint32_t kColS = 0, kColO = 256, kColAll = 512;
 
 struct Kv8Meta {
     float kf[4];   // per 32 keys: factor of K, exponent of V, keys that count
@@ -717,7 +725,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     const uint32_t sm = smem_u32(smem);
     Kv8Meta *meta = reinterpret_cast<Kv8Meta *>(smem + Lay::meta_off);
-    float *red = reinterpret_cast<float *>(smem + Lay::red_off);
+    uint32_t *red = reinterpret_cast<uint32_t *>(smem + Lay::red_off);
     long long *tiles = reinterpret_cast<long long *>(smem + Lay::tiles_off);
     const uint32_t bars = sm + Lay::bar_off;
     auto k_full = [&](int b) { return bars + 8 * b; };             // operand warps
@@ -728,8 +736,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     auto p_full = [&](int b) { return bars + 8 * (10 + b); };      // 4 softmax warps
     auto m_full = [&](int t) { return bars + 8 * (12 + t); };      // meta of tile % 4
     auto o_full = [&](int b) { return bars + 8 * (16 + b); };      // commit of O
-    const uint32_t q_full = bars + 8 * 18, r_full = bars + 8 * 19, drain = bars + 8 * 20;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::bar_off + 8 * 21);
+    const uint32_t q_full = bars + 8 * 18, r_full = bars + 8 * 19, drain = bars + 8 * 20, e_full = bars + 8 * 21;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::bar_off + 8 * 22);
     long long *warp_sum = reinterpret_cast<long long *>(smem + Lay::bar_off + 24 * 8);
 
     const la_kv8_cache &c = p.c;
@@ -745,7 +753,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             mbar_init(o_full(b), 1);
         }
         for (int t = 0; t < 4; ++t) mbar_init(m_full(t), 1);
-        mbar_init(q_full, 4);
+        mbar_init(q_full, 8);
+        mbar_init(e_full, 8);
         mbar_init(r_full, kOperandWarps);
         mbar_init(drain, 1);
         fence_barrier_init();
@@ -775,9 +784,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     bool ok = true;
     unsigned *err = c.status;
 
-    if (warp >= 4 && warp < kMmaWarp) {
+    if (warp >= 8 && warp < kMmaWarp) {
         // ================================================ operands
-        const int w = warp - 4, r8 = lane & 7, cq = lane >> 3;
+        const int w = warp - 8, r8 = lane & 7, cq = lane >> 3;
         int new_tiles = 0;
         constexpr int NR = HD / (4 * kOperandWarps);   // 16-byte pieces of K, and of V, per thread and tile
         const uint8_t *kp = static_cast<const uint8_t *>(c.k), *vp = static_cast<const uint8_t *>(c.v);
@@ -789,55 +798,109 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             auto v_dim = [&](int i) { return w * (HD / kOperandWarps) + r8 + 8 * (i >> 1); };
             auto v_chunk = [&](int i) { return cq + 4 * (i & 1); };
             const int c_first = max(u.k0, sq.ntiles);   // first cached tile of this piece
-            // Pages of cached tile kt: lane l < 4 holds that of keys 32 l .. of the tile.
-            auto pages = [&](int kt) {
+            // Table entries of cached tile kt: lane l < 4 holds that of keys 32 l ..
+            // of the tile (-2: none).  They are checked a tile later, so that
+            // nothing waits for the load.
+            auto entry = [&](int kt) {
                 const int key = (kt - sq.ntiles) * kTileK + 32 * (lane & 3);
-                return kt < u.k1 && key < sq.len ? kv8_page(c, u.s, key / c.page) : -1;
+                return kt < u.k1 && key < sq.len ? c.table[static_cast<long long>(u.s) * c.max_pages + (key >> p.page_log2)] : -2;
+            };
+            auto checked = [&](int e) {
+                if (static_cast<unsigned>(e) < static_cast<unsigned>(c.n_pages)) return e;
+                if (e != -2) atomicOr(err, LA_KV8_BAD);
+                return -1;
             };
             uint4 kraw[NR], vraw[NR];
             auto load_k = [&](int kt, int pg) {
-                const int pid = __shfl_sync(0xffffffffu, pg, w * (kTileK / kOperandWarps) / 32);
-                const uint8_t *src = kp + kv8_block(c, p.a.layer, max(pid, 0), u.head) * c.page * HD;
+                const int pid = max(__shfl_sync(0xffffffffu, pg, w * (kTileK / kOperandWarps) / 32), 0);
+                const int row0 = ((kt - sq.ntiles) * kTileK + w * (kTileK / kOperandWarps)) & (c.page - 1);   // this warp's rows lie in one page
+                const uint8_t *src = kp + (kv8_block(c, p.a.layer, pid, u.head) * c.page + row0) * HD;
 #pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    const int in_page = ((kt - sq.ntiles) * kTileK + k_row(i)) % c.page;
-                    kraw[i] = pid < 0 ? make_uint4(0, 0, 0, 0) : __ldcg(reinterpret_cast<const uint4 *>(src + in_page * HD + 16 * k_chunk(i)));
-                }
+                for (int i = 0; i < NR; ++i)
+                    kraw[i] = __ldcg(reinterpret_cast<const uint4 *>(src + (k_row(i) - w * (kTileK / kOperandWarps)) * HD + 16 * k_chunk(i)));
             };
+            // (A piece of a missing page may be anything: its bytes are cut below.)
             auto load_v = [&](int kt, int pg) {
+                const int pid0 = max(__shfl_sync(0xffffffffu, pg, cq >> 1), 0), pid1 = max(__shfl_sync(0xffffffffu, pg, (cq >> 1) + 2), 0);
+                const int key = (kt - sq.ntiles) * kTileK + 16 * cq;
+                const uint8_t *src0 = vp + kv8_block(c, p.a.layer, pid0, u.head) * c.page * HD + (key & (c.page - 1));
+                const uint8_t *src1 = vp + kv8_block(c, p.a.layer, pid1, u.head) * c.page * HD + ((key + 64) & (c.page - 1));
 #pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    const int ch = v_chunk(i), key = (kt - sq.ntiles) * kTileK + 16 * ch;
-                    const int pid = __shfl_sync(0xffffffffu, pg, ch >> 1), live = pid < 0 ? 0 : min(max(sq.len - key, 0), 16);
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (live > 0) {
-                        x = __ldcg(reinterpret_cast<const uint4 *>(vp + (kv8_block(c, p.a.layer, pid, u.head) * HD + v_dim(i)) * c.page + key % c.page));
-                        if (live < 16) {   // bytes behind the last token may be anything
-                            const int n0 = live, n1 = live - 4, n2 = live - 8, n3 = live - 12;
+                for (int i = 0; i < NR; ++i) vraw[i] = __ldcg(reinterpret_cast<const uint4 *>((i & 1 ? src1 : src0) + v_dim(i) * c.page));
+            };
+            // Pages of tiles kt - 1, kt, kt + 1 and the entries of kt + 2, kt being the tile whose K is put next.
+            int pg_v = -1, pg_k = checked(entry(c_first)), pg_next = checked(entry(c_first + 1)), after = entry(c_first + 2);
+            if (c_first < u.k1) {
+                load_k(c_first, pg_k);
+                load_v(c_first, pg_k);
+            }
+            float fv = 0.f;   // new rows: factor on V of tile kt - 1
+            // V of tile kt (number i) to its buffer.
+            auto put_v = [&](int kt, int i) {
+                const int b = i & 1, use = i >> 1;
+                const uint32_t sv = sm + Lay::v_off + b * Lay::v_bytes;
+                if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(v_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
+                if (!ok) return;
+                if (kt >= sq.ntiles) {
+                    // Bytes behind the last token, and of missing pages, may be anything.
+                    const int key0 = (kt - sq.ntiles) * kTileK, held = __ballot_sync(0xffffffffu, pg_v >= 0 && lane < 4);
+                    if (sq.len - key0 < kTileK || held != 15) {
+#pragma unroll
+                        for (int i = 0; i < NR; ++i) {
+                            const int ch = v_chunk(i), live = held >> (ch >> 1) & 1 ? sq.len - key0 - 16 * ch : 0;
                             auto cut = [](uint32_t a, int n) { return n >= 4 ? a : n <= 0 ? 0u : a & ((1u << (8 * n)) - 1u); };
-                            x = make_uint4(cut(x.x, n0), cut(x.y, n1), cut(x.z, n2), cut(x.w, n3));
+                            vraw[i] = make_uint4(cut(vraw[i].x, live), cut(vraw[i].y, live - 4), cut(vraw[i].z, live - 8), cut(vraw[i].w, live - 12));
                         }
                     }
-                    vraw[i] = x;
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) {
+                        uint4 x, y;
+                        e4m3x16_f16(vraw[i], x, y);
+                        const int ch = 2 * (v_chunk(i) & 3);
+                        const uint32_t at = sv + (v_chunk(i) >> 2) * Lay::v_block + v_dim(i) * 128;
+                        st_shared(at + ((ch ^ r8) << 4), x);
+                        st_shared(at + (((ch + 1) ^ r8) << 4), y);
+                    }
+                } else {
+                    // Two new rows of eight dims at a time, transposed.  A NaN or
+                    // infinity counts 0 here and is added at the end for the
+                    // rows that see it.
+                    const int key0 = kt * kTileK, nkeys = min(kTileK, sq.rows - key0);
+                    const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + u.head * HD;
+                    for (int i = w * 32 + lane; i < kTileK / 2 * (HD / 8); i += 32 * kOperandWarps) {
+                        const int r = 2 * (i / (HD / 8)), d = 8 * (i % (HD / 8));
+                        const uint4 a = r < nkeys ? *reinterpret_cast<const uint4 *>(vn + r * p.a.v_stride + d) : make_uint4(0, 0, 0, 0);
+                        const uint4 e = r + 1 < nkeys ? *reinterpret_cast<const uint4 *>(vn + (r + 1) * p.a.v_stride + d) : make_uint4(0, 0, 0, 0);
+                        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {e.x, e.y, e.z, e.w};
+                        const uint32_t at = sv + (r >> 6) * Lay::v_block + (r & 7) * 2;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            float f0 = bf16_bits(k & 1 ? x[k >> 1] >> 16 : x[k >> 1] & 0xffffu), f1 = bf16_bits(k & 1 ? y[k >> 1] >> 16 : y[k >> 1] & 0xffffu);
+                            f0 = is_finite(f0) ? f0 * fv : 0.f;
+                            f1 = is_finite(f1) ? f1 * fv : 0.f;
+                            const int dim = d + k;
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + dim * 128 + ((((r >> 3) & 7) ^ (dim & 7)) << 4)), "r"(pack_f16(f0, f1)) : "memory");
+                        }
+                    }
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_one(v_full(b));
             };
-            int pg_now = pages(c_first), pg_next = pages(c_first + 1);
-            if (c_first < u.k1) {
-                load_k(c_first, pg_now);
-                load_v(c_first, pg_now);
-            }
+            const int begin = it;
             for (int kt = u.k0; ok && kt < u.k1; ++kt, ++it) {
                 const int b = it & 1, use = it >> 1;
-                const uint32_t sk = sm + Lay::k_off + b * Lay::k_bytes, sv = sm + Lay::v_off + b * Lay::v_bytes;
+                const uint32_t sk = sm + Lay::k_off + b * Lay::k_bytes;
+                float fv_next = 0.f;
                 if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(k_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
                 if (!ok) break;
                 if (kt >= sq.ntiles) {
                     if (w == 0 && lane < 4) {
                         Kv8Meta &mt = meta[it & 3];
                         const int key = (kt - sq.ntiles) * kTileK + 32 * lane;
-                        const bool have = pg_now >= 0;
-                        const long long blk = kv8_block(c, p.a.layer, max(pg_now, 0), u.head);
-                        mt.kf[lane] = have ? c.k_scale[blk] : 0.f;
+                        const bool have = pg_k >= 0;
+                        const long long blk = kv8_block(c, p.a.layer, max(pg_k, 0), u.head);
+                        mt.kf[lane] = have ? c.k_scale[blk] : 1.f;
                         mt.vx[lane] = have ? exponent_of(c.v_scale[blk]) : 0;
                         mt.live[lane] = have ? min(max(sq.len - key, 0), 32) : 0;
                         if (lane == 0) mt.odd = 0;
@@ -855,36 +918,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                         st_shared(at + ((ch ^ r8) << 4), x);
                         st_shared(at + (((ch + 1) ^ r8) << 4), y);
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_one(k_full(b));
-                    if (kt + 1 < u.k1) load_k(kt + 1, pg_next);
-                    if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(v_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
-                    if (!ok) break;
-#pragma unroll
-                    for (int i = 0; i < NR; ++i) {
-                        uint4 x, y;
-                        e4m3x16_f16(vraw[i], x, y);
-                        const int ch = 2 * (v_chunk(i) & 3);
-                        const uint32_t at = sv + (v_chunk(i) >> 2) * Lay::v_block + v_dim(i) * 128;
-                        st_shared(at + ((ch ^ r8) << 4), x);
-                        st_shared(at + (((ch + 1) ^ r8) << 4), y);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_one(v_full(b));
-                    if (kt + 1 < u.k1) load_v(kt + 1, pg_next);
-                    pg_now = pg_next;
-                    pg_next = pages(kt + 2);
                 } else {
                     // New rows: bf16, scaled by a power of two for the whole tile.
                     const int key0 = kt * kTileK, nkeys = min(kTileK, sq.rows - key0);
                     const __nv_bfloat16 *kn = static_cast<const __nv_bfloat16 *>(p.a.k) + (sq.first + key0) * p.a.k_stride + u.head * HD;
                     const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + u.head * HD;
-                    constexpr int NT = 32 * kOperandWarps;
+                    constexpr int C8 = HD / 8, NT = 32 * kOperandWarps;   // 16-byte pieces of a row
                     const int ot = w * 32 + lane;
-                    constexpr int C8 = HD / 8;      // 16-byte pieces of a row
-                    float ak = 0.f, av = 0.f;
+                    uint32_t ak = 0, av = 0;   // magnitudes order like their bits
                     bool odd = false;
                     for (int i = ot; i < nkeys * C8; i += NT) {
                         const int r = i / C8, d = 8 * (i % C8);
@@ -894,37 +935,37 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                         for (int k = 0; k < 4; ++k)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                const float e = bf16_bits(h ? x[k] >> 16 : x[k] & 0xffffu), f = bf16_bits(h ? y[k] >> 16 : y[k] & 0xffffu);
-                                if (is_finite(e)) ak = fmaxf(ak, fabsf(e));
-                                if (is_finite(f)) av = fmaxf(av, fabsf(f));
+                                const uint32_t e = (x[k] >> (16 * h)) & 0x7fffu, f = (y[k] >> (16 * h)) & 0x7fffu;
+                                if (e < 0x7f80u) ak = max(ak, e);
+                                if (f < 0x7f80u) av = max(av, f);
                                 else odd = true;
                             }
                     }
-                    ak = warp_max(ak);
-                    av = warp_max(av);
+                    ak = __reduce_max_sync(0xffffffffu, ak);
+                    av = __reduce_max_sync(0xffffffffu, av);
                     odd = __any_sync(0xffffffffu, odd);
                     // The warps' maxima: two halves, one for each buffer, so that no
                     // warp writes what another still reads.
-                    float *mine = red + 16 * b;
+                    uint32_t *mine = red + 16 * b;
                     if (lane == 0) {
                         mine[w] = ak;
-                        mine[8 + w] = odd ? -av - 1.f : av;   // the sign says that it is odd
+                        mine[8 + w] = av | (odd ? 0x10000u : 0u);
                         mbar_arrive_one(r_full);
                     }
                     __syncwarp();
                     ok = __all_sync(0xffffffffu, mbar_wait(r_full, new_tiles & 1, err, LA_KV8_TIMEOUT));
                     if (!ok) break;
                     ++new_tiles;
-                    ak = av = 0.f;
+                    ak = av = 0;
                     odd = false;
 #pragma unroll
                     for (int k = 0; k < kOperandWarps; ++k) {
-                        ak = fmaxf(ak, mine[k]);
-                        const float x = mine[8 + k];
-                        odd |= x < 0.f;
-                        av = fmaxf(av, x < 0.f ? -x - 1.f : x);
+                        ak = max(ak, mine[k]);
+                        av = max(av, mine[8 + k] & 0xffffu);
+                        odd |= mine[8 + k] >> 16 != 0;
                     }
-                    const int kx = fit_f16(ak), vx = fit_f16(av);
+                    const int kx = fit_f16(bf16_bits(ak)), vx = fit_f16(bf16_bits(av));
+                    fv_next = power_of(-vx);
                     if (w == 0) {
                         if (lane < 4) {
                             Kv8Meta &mt = meta[it & 3];
@@ -936,7 +977,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                         __syncwarp();
                         if (lane == 0) mbar_arrive_one(m_full(it & 3));
                     }
-                    const float fk = power_of(-kx), fv = power_of(-vx);
+                    const float fk = power_of(-kx);
                     for (int i = ot; i < kTileK * C8; i += NT) {
                         const int r = i / C8, d8 = i % C8;
                         const uint4 a = r < nkeys ? *reinterpret_cast<const uint4 *>(kn + r * p.a.k_stride + 8 * d8) : make_uint4(0, 0, 0, 0);
@@ -946,34 +987,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                         for (int k = 0; k < 4; ++k) y[k] = pack_f16(bf16_bits(x[k] & 0xffffu) * fk, bf16_bits(x[k] >> 16) * fk);
                         st_shared_u32x4(sk + (d8 >> 3) * Lay::k_block + r * 128 + (((d8 & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_one(k_full(b));
-                    if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(v_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
-                    if (!ok) break;
-                    // Two keys of eight dims at a time, transposed.  A NaN or
-                    // infinity counts 0 here and is added at the end for the
-                    // rows that see it.
-                    for (int i = ot; i < kTileK / 2 * C8; i += NT) {
-                        const int r = 2 * (i / C8), d = 8 * (i % C8);
-                        const uint4 a = r < nkeys ? *reinterpret_cast<const uint4 *>(vn + r * p.a.v_stride + d) : make_uint4(0, 0, 0, 0);
-                        const uint4 e = r + 1 < nkeys ? *reinterpret_cast<const uint4 *>(vn + (r + 1) * p.a.v_stride + d) : make_uint4(0, 0, 0, 0);
-                        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {e.x, e.y, e.z, e.w};
-                        const uint32_t at = sv + (r >> 6) * Lay::v_block + (r & 7) * 2;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            float f0 = bf16_bits(k & 1 ? x[k >> 1] >> 16 : x[k >> 1] & 0xffffu), f1 = bf16_bits(k & 1 ? y[k >> 1] >> 16 : y[k >> 1] & 0xffffu);
-                            f0 = is_finite(f0) ? f0 * fv : 0.f;
-                            f1 = is_finite(f1) ? f1 * fv : 0.f;
-                            const int dim = d + k;
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + dim * 128 + ((((r >> 3) & 7) ^ (dim & 7)) << 4)), "r"(pack_f16(f0, f1)) : "memory");
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_one(v_full(b));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_one(k_full(b));
+                if (kt >= sq.ntiles && kt + 1 < u.k1) load_k(kt + 1, pg_next);
+                if (it > begin) put_v(kt - 1, it - 1);
+                fv = fv_next;
+                if (kt >= sq.ntiles) {
+                    if (kt > c_first) load_v(kt, pg_k);
+                    pg_v = pg_k;
+                    pg_k = pg_next;
+                    pg_next = checked(after);
+                    after = entry(kt + 3);
                 }
             }
+            if (ok && it > begin) put_v(u.k1 - 1, it - 1);
         }
     } else if (warp == kMmaWarp) {
         // ================================================ products
@@ -985,12 +1014,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 ok = mbar_wait(p_full(b), j >> 1 & 1, err, LA_KV8_TIMEOUT) && mbar_wait(v_full(b), j >> 1 & 1, err, LA_KV8_TIMEOUT);
                 if (!ok) return;
                 tc_fence_after();
-                const uint32_t sv = sm + Lay::v_off + b * Lay::v_bytes, pt = tmem + kColS + 128 * b;
+                const uint32_t sv = sm + Lay::v_off + b * Lay::v_bytes, pt = tmem + kColS + 128 * b, ot = tmem + kColO + 128 * b;
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
                     const uint64_t d = umma_desc_sw128(sv + kb * Lay::v_block);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) umma_ts(tmem + kColO, pt + kb * 32 + k * 8, d + 2 * k, io, begins && !(kb | k) ? 0u : 1u);
+                    for (int k = 0; k < 4; ++k) umma_ts(ot, pt + kb * 32 + k * 8, d + 2 * k, io, begins && !(kb | k) ? 0u : 1u);
                 }
                 umma_commit(v_empty(b));
                 umma_commit(o_full(b));
@@ -1008,16 +1037,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                     const uint32_t sk = sm + Lay::k_off + b * Lay::k_bytes;
 #pragma unroll
                     for (int db = 0; db < HD / 64; ++db) {
-                        const uint64_t d = umma_desc_sw128(sk + db * Lay::k_block);
+                        const uint64_t d = umma_desc_sw128(sk + db * Lay::k_block), q = umma_desc_sw128(sm + Lay::q_off + db * Lay::k_block);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            umma_ts(tmem + kColS + 128 * b, tmem + kColQ + db * 32 + k * 8, d + 2 * k, is, (db | k) ? 1u : 0u);
+                        for (int k = 0; k < 4; ++k) umma_bf16(tmem + kColS + 128 * b, q + 2 * k, d + 2 * k, is, (db | k) ? 1u : 0u);
                     }
                     umma_commit(s_full(b));
                     umma_commit(k_empty(b));
-                    if (it > first) product_o(it - 1, it - 1 == first);
+                    if (it > first) product_o(it - 1, it - 1 < first + 2);
                 }
-                if (ok) product_o(it - 1, it - 1 == first);
+                if (ok) product_o(it - 1, it - 1 < first + 2);
             }
             if (!ok) {   // void: wait (bounded) for the products in flight
                 umma_commit(drain);
@@ -1027,213 +1055,226 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         __syncwarp();
     } else {
         // ================================================ softmax
-        const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
-        const int row = 32 * warp + lane;
+        const int grp = warp >> 2, row = 32 * (warp & 3) + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lanes + kColS + 128 * grp, to = tmem + lanes + kColO + 128 * grp;
+        float2 *ml = reinterpret_cast<float2 *>(smem + Lay::ml_off);
+        int *odds = reinterpret_cast<int *>(smem + Lay::odd_off);
+        int units = 0;
         while (ok && kv8_next(p, tiles, walk, u)) {
             const Kv8Seq sq = u.sq;
-            const bool in = row < u.nqv, idle = 32 * warp >= u.nqv;   // idle: none of this warp's rows is in use
+            const bool in = row < u.nqv, idle = row - lane >= u.nqv;   // idle: none of this warp's rows is in use
             const int qv = u.qv0 + row, myrow = in ? qv / p.gq : 0, myhead = u.head * p.gq + (in ? qv % p.gq : 0);
+            const int first = it, end = it + max(u.k1 - u.k0, 0);
             float qf = 0.f;
-            if (u.k0 < u.k1) {
+            if (first < end) {
                 if (!idle) {
-                    // q as fp16, scaled by a power of two to fit, into tensor memory
+                    // q as fp16, scaled by a power of two to fit; the first group stores it
                     const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.q) + (sq.first + myrow) * p.a.q_stride + myhead * HD);
-                    float amax = 0.f;
-                    uint4 x[HD / 8];
+                    uint32_t top = 0;
 #pragma unroll
                     for (int i = 0; i < HD / 8; ++i) {
-                        x[i] = in ? src[i] : make_uint4(0, 0, 0, 0);
-                        const uint32_t y[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                        const uint4 x = in ? src[i] : make_uint4(0, 0, 0, 0);
+                        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const float lo = bf16_bits(y[k] & 0xffffu), hi = bf16_bits(y[k] >> 16);
-                            if (is_finite(lo)) amax = fmaxf(amax, fabsf(lo));
-                            if (is_finite(hi)) amax = fmaxf(amax, fabsf(hi));
+                            const uint32_t lo = y[k] & 0x7fffu, hi = y[k] >> 16 & 0x7fffu;   // magnitudes order like their bits
+                            if (lo < 0x7f80u) top = max(top, lo);
+                            if (hi < 0x7f80u) top = max(top, hi);
                         }
                     }
-                    const int qx = fit_f16(amax);
-                    const float f = power_of(-qx);
+                    const int qx = fit_f16(bf16_bits(top));
                     qf = power_of(qx) * p.scale_log2;
+                    if (grp == 0) {
+                        const float f = power_of(-qx);
 #pragma unroll
-                    for (int i = 0; i < HD / 32; ++i) {   // 32 dims, 16 columns at a time
-                        uint32_t z[16];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint4 v = x[4 * i + k];
-                            z[4 * k] = pack_f16(bf16_bits(v.x & 0xffffu) * f, bf16_bits(v.x >> 16) * f);
-                            z[4 * k + 1] = pack_f16(bf16_bits(v.y & 0xffffu) * f, bf16_bits(v.y >> 16) * f);
-                            z[4 * k + 2] = pack_f16(bf16_bits(v.z & 0xffffu) * f, bf16_bits(v.z >> 16) * f);
-                            z[4 * k + 3] = pack_f16(bf16_bits(v.w & 0xffffu) * f, bf16_bits(v.w >> 16) * f);
+                        for (int i = 0; i < HD / 8; ++i) {
+                            const uint4 x = in ? src[i] : make_uint4(0, 0, 0, 0);
+                            st_shared_u32x4(sm + Lay::q_off + (i >> 3) * Lay::k_block + row * 128 + (((i & 7) ^ (row & 7)) << 4),
+                                            pack_f16(bf16_bits(x.x & 0xffffu) * f, bf16_bits(x.x >> 16) * f), pack_f16(bf16_bits(x.y & 0xffffu) * f, bf16_bits(x.y >> 16) * f),
+                                            pack_f16(bf16_bits(x.z & 0xffffu) * f, bf16_bits(x.z >> 16) * f), pack_f16(bf16_bits(x.w & 0xffffu) * f, bf16_bits(x.w >> 16) * f));
                         }
-                        tmem_st_32x32b_x16(tmem + lanes + kColQ + 16 * i, z);
+                        fence_proxy_async_smem();
                     }
-                    tmem_st_wait();
                 }
-                tc_fence_before();
+                tc_fence_before();   // the last unit's O is read
                 __syncwarp();
                 if (lane == 0) mbar_arrive_one(q_full);
             }
             float m = -INFINITY, l = 0.f;
             bool odd = false;
-            const int first = it;
-            for (int kt = u.k0; ok && kt < u.k1; ++kt, ++it) {
-                const int b = it & 1;
-                ok = mbar_wait(s_full(b), it >> 1 & 1, err, LA_KV8_TIMEOUT) && mbar_wait(m_full(it & 3), it >> 2 & 1, err, LA_KV8_TIMEOUT);
+            for (int kt = u.k0 + ((first ^ grp) & 1); kt < u.k1; kt += 2) {
+                const int i = first + kt - u.k0, b = grp;   // tile number, of this group's parity
+                ok = mbar_wait(s_full(b), i >> 1 & 1, err, LA_KV8_TIMEOUT) && mbar_wait(m_full(i & 3), i >> 2 & 1, err, LA_KV8_TIMEOUT);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const Kv8Meta &mt = meta[it & 3];
+                const Kv8Meta &mt = meta[i & 3];
                 odd |= mt.odd != 0;
                 if (!idle) {
-                    const uint32_t ts = tmem + lanes + kColS + 128 * b;
-                    uint32_t see[4];   // keys 32 c .. 32 c + 31 of the tile that this row sees
-                    bool dense = true;
-#pragma unroll
+                    // 32 keys at a time: t relative to the maximum as it stands, then
+                    // the weights, over columns of S that are read already.  One
+                    // copy of this code: unrolled, the roles' code does not fit
+                    // the instruction cache (5 us per pair of tiles).
+                    const bool cached = kt >= sq.ntiles;
+#pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
-                        const int live = mt.live[k];
-                        see[k] = live >= 32 ? 0xffffffffu : (1u << live) - 1u;
-                        if (kt < sq.ntiles) {
-                            const int key = kt * kTileK + 32 * k;
-                            if (!in) see[k] = 0;
-                            else if (p.a.vis)
-                                see[k] &= key < 256 ? p.a.vis[(static_cast<long long>(sq.first) + myrow) * 8 + key / 32] : 0u;
-                            else
-                                see[k] &= myrow >= key + 31 ? 0xffffffffu : myrow < key ? 0u : (2u << (myrow - key)) - 1u;
-                        }
-                        dense &= see[k] == 0xffffffffu;
-                    }
-                    dense = __all_sync(0xffffffffu, dense);
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t v0[32], v1[32];
-                        tmem_ld_32x32b_x32(ts + 64 * h, v0);
-                        tmem_ld_32x32b_x32(ts + 64 * h + 32, v1);
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(ts + 32 * k, v);
+                        const int live = mt.live[k], vx = mt.vx[k];
+                        const float f = mt.kf[k] * qf, add = static_cast<float>(vx) - (m == -INFINITY ? 0.f : m);
                         tmem_ld_wait();
-                        float a = -INFINITY, e = -INFINITY;
-                        if (dense) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                a = fmaxf(a, __uint_as_float(v0[k]));
-                                e = fmaxf(e, __uint_as_float(v1[k]));
+                        if (live < 32 || !cached) {
+                            uint32_t see = live >= 32 ? 0xffffffffu : (1u << live) - 1u;   // keys that this row sees
+                            if (!cached) {
+                                const int key = kt * kTileK + 32 * k;
+                                if (!in) see = 0;
+                                else if (p.a.vis)
+                                    see &= key < 256 ? p.a.vis[(static_cast<long long>(sq.first) + myrow) * 8 + key / 32] : 0u;
+                                else
+                                    see &= myrow >= key + 31 ? 0xffffffffu : myrow < key ? 0u : (2u << (myrow - key)) - 1u;
                             }
-                        } else {
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                if (see[2 * h] >> k & 1u) a = fmaxf(a, __uint_as_float(v0[k]));
-                                if (see[2 * h + 1] >> k & 1u) e = fmaxf(e, __uint_as_float(v1[k]));
-                            }
+                            for (int e = 0; e < 32; ++e) v[e] = see >> e & 1u ? v[e] : 0xff800000u;   // -infinity
                         }
-                        // factors are positive: the maximum commutes with them
-                        mx = fmaxf(mx, fmaxf(fmaf(a, mt.kf[2 * h] * qf, static_cast<float>(mt.vx[2 * h])),
-                                             fmaf(e, mt.kf[2 * h + 1] * qf, static_cast<float>(mt.vx[2 * h + 1]))));
-                    }
-                    const bool grow = mx > m + kLazy || (m == -INFINITY && mx > -INFINITY);
-                    if (__any_sync(0xffffffffu, grow)) {
-                        const float alpha = grow ? ex2(m - mx) : 1.f;
-                        if (grow) m = mx;
-                        l *= alpha;
-                        if (it > first) {
-                            ok = mbar_wait(o_full((it - 1) & 1), (it - 1) >> 1 & 1, err, LA_KV8_TIMEOUT);
-                            ok = __all_sync(0xffffffffu, ok);
-                            if (!ok) break;
-                            tc_fence_after();
+                        float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
-                            for (int k = 0; k < HD / 32; ++k) {
-                                uint32_t o[32];
-                                tmem_ld_32x32b_x32(tmem + lanes + kColO + 32 * k, o);
+                        for (int e = 0; e < 32; e += 2) {
+                            const float x = fmaf(__uint_as_float(v[e]), f, add), y = fmaf(__uint_as_float(v[e + 1]), f, add);
+                            x0 = fmaxf(x0, x);
+                            x1 = fmaxf(x1, y);
+                            v[e] = __float_as_uint(x);
+                            v[e + 1] = __float_as_uint(y);
+                        }
+                        x0 = fmaxf(x0, x1);   // past the maximum by this much
+                        const bool grow = m == -INFINITY ? x0 > -INFINITY : x0 > kLazy;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            // a whole number past the first, so that scaling by 2^-by rounds nothing
+                            const float by = !grow ? 0.f : m == -INFINITY ? x0 : ceilf(x0), alpha = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(-by);
+                            if (grow) m = m == -INFINITY ? x0 : m + by;
+                            l *= alpha;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) - by);
+                            for (int q = 0; q < k; ++q) {   // this tile's weights so far
+                                uint32_t w[16];
+                                tmem_ld_32x32b_x16(ts + 16 * q, w);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                                tmem_st_32x32b_x32(tmem + lanes + kColO + 32 * k, o);
+                                for (int e = 0; e < 16; ++e) {
+                                    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+                                    w[e] = pack_f16(x.x * alpha, x.y * alpha);
+                                }
+                                tmem_st_32x32b_x16(ts + 16 * q, w);
+                            }
+                            if (i >= first + 2) {   // this group's O holds its tile i - 2
+                                ok = __all_sync(0xffffffffu, mbar_wait(o_full(b), (i - 2) >> 1 & 1, err, LA_KV8_TIMEOUT));
+                                if (!ok) break;
+                                tc_fence_after();
+                                for (int q = 0; q < HD / 16; ++q) {
+                                    uint32_t o[16];
+                                    tmem_ld_32x32b_x16(to + 16 * q, o);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                    tmem_st_32x32b_x16(to + 16 * q, o);
+                                }
                             }
                             tmem_st_wait();
                         }
-                    }
-                    const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t v[32], w[16];
-                        tmem_ld_32x32b_x32(ts + 32 * k, v);
-                        tmem_ld_wait();
-                        const float f = mt.kf[k] * qf, add = static_cast<float>(mt.vx[k]) - base;
+                        uint32_t w[16];
                         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            float x = ex2(fmaf(__uint_as_float(v[2 * e]), f, add)), y = ex2(fmaf(__uint_as_float(v[2 * e + 1]), f, add));
-                            if (!dense) {
-                                x = see[k] >> (2 * e) & 1u ? x : 0.f;
-                                y = see[k] >> (2 * e + 1) & 1u ? y : 0.f;
-                            }
+                            const float x = ex2(__uint_as_float(v[2 * e])), y = ex2(__uint_as_float(v[2 * e + 1]));
                             s0 += x;
                             s1 += y;
                             w[e] = pack_f16(x, y);
                         }
-                        l += (s0 + s1) * power_of(-mt.vx[k]);
-                        tmem_st_32x32b_x16(ts + 16 * k, w);   // over columns of S that are read already
+                        l += (s0 + s1) * power_of(-vx);
+                        tmem_st_32x32b_x16(ts + 16 * k, w);
                     }
+                    if (!ok) break;
                     tmem_st_wait();
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_one(p_full(b));
             }
+            it = end;
             if (!ok) break;
-            if (it > first) {
-                ok = __all_sync(0xffffffffu, mbar_wait(o_full((it - 1) & 1), (it - 1) >> 1 & 1, err, LA_KV8_TIMEOUT));
+            float fa = 0.f, fb = 0.f, M = m, L = l;
+            if (first < end) {
+                // Both groups' maxima and sums, once all products are done; then
+                // each group writes half of the dims.
+                ml[grp * kTileQ + row] = make_float2(m, l);
+                if (lane == 0 && (warp & 3) == 0) odds[grp] = odd;
+                __syncwarp();
+                if (lane == 0) mbar_arrive_one(e_full);
+                ok = mbar_wait(e_full, units & 1, err, LA_KV8_TIMEOUT) &&
+                     mbar_wait(o_full((end - 1) & 1), (end - 1) >> 1 & 1, err, LA_KV8_TIMEOUT) &&
+                     (end - first < 2 || mbar_wait(o_full(end & 1), (end - 2) >> 1 & 1, err, LA_KV8_TIMEOUT));
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
+                ++units;
+                const float2 x = ml[row], y = ml[kTileQ + row];
+                odd = (odds[0] | odds[1]) != 0;
+                M = fmaxf(x.x, y.x);
+                fa = x.y == 0.f ? 0.f : ex2(x.x - M);
+                fb = y.y == 0.f ? 0.f : ex2(y.x - M);
+                L = (x.y == 0.f ? 0.f : fa * x.y) + (y.y == 0.f ? 0.f : fb * y.y);
+                // a group that saw no key may have an O that was never written
+                if (x.y == 0.f) fa = -1.f;
+                if (y.y == 0.f) fb = -1.f;
+            } else {
+                fa = fb = -1.f;
             }
             if (idle) continue;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-            const int slot = 2 * blockIdx.x + (u.begins ? 1 : 0);
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + (sq.first + myrow) * p.a.out_stride + myhead * HD;
-            float *part = p.part + (static_cast<long long>(slot) * kTileQ + row) * HD;
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            const int slot = 2 * blockIdx.x + (u.begins ? 1 : 0), d0 = grp * (HD / 2);
+            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + (sq.first + myrow) * p.a.out_stride + myhead * HD + d0;
+            float *part = p.part + (static_cast<long long>(slot) * kTileQ + row) * HD + d0;
 #pragma unroll
-            for (int k = 0; k < HD / 32; ++k) {
-                uint32_t o[32];
+            for (int k = 0; k < HD / 32; ++k) {   // 16 dims at a time
+                uint32_t oa[16], ob[16];
+                float o[16];
                 __syncwarp();
-                if (it > first) {
-                    tmem_ld_32x32b_x32(tmem + lanes + kColO + 32 * k, o);
+                if (first < end) {
+                    tmem_ld_32x32b_x16(tmem + lanes + kColO + d0 + 16 * k, oa);
+                    tmem_ld_32x32b_x16(tmem + lanes + kColO + 128 + d0 + 16 * k, ob);
                     tmem_ld_wait();
                 }
-                if (it == first || l == 0.f) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0;
-                }
+                for (int e = 0; e < 16; ++e) o[e] = (fa == -1.f ? 0.f : fa * __uint_as_float(oa[e])) + (fb == -1.f ? 0.f : fb * __uint_as_float(ob[e]));
                 if (odd && in) {   // NaN and infinities of the new rows that this row sees
                     for (int r = u.k0 * kTileK; r < min(sq.rows, min(u.k1, sq.ntiles) * kTileK); ++r) {
                         const bool seen = p.a.vis ? r < 256 && (p.a.vis[(static_cast<long long>(sq.first) + myrow) * 8 + r / 32] >> (r % 32) & 1u) : r <= myrow;
                         if (!seen) continue;
-                        const __nv_bfloat16 *vr = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + r) * p.a.v_stride + u.head * HD + 32 * k;
+                        const __nv_bfloat16 *vr = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + r) * p.a.v_stride + u.head * HD + d0 + 16 * k;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
+                        for (int e = 0; e < 16; ++e) {
                             const float x = __bfloat162float(vr[e]);
-                            if (!is_finite(x)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+                            if (!is_finite(x)) o[e] += x;
                         }
                     }
                 }
-                if (!in) continue;
-                if (u.all) {
+                if (in && u.all) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 2; ++e) {
                         uint32_t y[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * q]) * inv, __uint_as_float(o[8 * e + 2 * q + 1]) * inv);
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(o[8 * e + 2 * q] * inv, o[8 * e + 2 * q + 1] * inv);
                             y[q] = *reinterpret_cast<const uint32_t *>(&h);
                         }
-                        *reinterpret_cast<uint4 *>(out + 32 * k + 8 * e) = make_uint4(y[0], y[1], y[2], y[3]);
+                        *reinterpret_cast<uint4 *>(out + 16 * k + 8 * e) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
-                } else {
+                } else if (in) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4 *>(part + 32 * k + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4 *>(part + 16 * k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
             }
-            if (!u.all && in) *reinterpret_cast<float2 *>(p.part_ml + (static_cast<long long>(slot) * kTileQ + row) * 2) = make_float2(m, l);
-            tc_fence_before();
-            __syncwarp();
+            if (!u.all && in && grp == 0) *reinterpret_cast<float2 *>(p.part_ml + (static_cast<long long>(slot) * kTileQ + row) * 2) = make_float2(M, L);
         }
     }
     __syncthreads();
@@ -1397,6 +1438,7 @@ cudaError_t kv8_attention_launch(const la_kv8_cache &c, const la_kv8_attn &a, vo
     p.c = c;
     p.a = a;
     p.gq = a.n_heads / c.n_kv_heads;
+    p.page_log2 = c.page == 32 ? 5 : c.page == 64 ? 6 : 7;
     p.scale_log2 = a.scale * kKv8Log2e;
     return c.head_dim == 128 ? attention_launch_hd<128>(p, nsm, ws, s) : attention_launch_hd<64>(p, nsm, ws, s);
 }
