@@ -25,7 +25,7 @@ int check_cache(const la_kv8_cache *c, const char *where) {
     if (c->n_layers < 1 || c->n_layers > 32767 || c->n_pages < 1 || c->n_pages > (1 << 24) || c->n_kv_heads < 1 ||
         c->n_kv_heads > 1024 || c->n_seqs < 1 || c->n_seqs > LA_KV8_MAX_SEQS || c->max_pages < 1 ||
         static_cast<int64_t>(c->max_pages) * c->page > (1 << 30))
-        return bad(where, "cache sizes out of range (n_layers 1..32767, n_pages 1..2^24, n_kv_heads 1..1024, n_seqs 1..4096, "
+        return bad(where, "cache sizes out of range (n_layers 1..32767, n_pages 1..2^24, n_kv_heads 1..1024, n_seqs 1..2048, "
                           "max_pages * page <= 2^30)");
     if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->table || !c->lens || !c->refs || !c->status)
         return bad(where, "null cache array");

@@ -16,6 +16,11 @@
 // units, read off the device-side lengths, so ragged batches and single long
 // sequences fill the GPU alike.  A unit that one worker does not cover leaves
 // partial (O, m, L) in the workspace, and k_kv8_join adds them in key order.
+//
+// Short calls are bound by instruction fetches: code that runs once per call
+// comes from L2 a line at a time, about 50 instructions per microsecond.  So
+// what runs once is written as small loops, and only the loops over keys are
+// unrolled.
 #include <algorithm>
 #include <atomic>
 
@@ -31,12 +36,20 @@ struct Kv8Args {
     int gq;            // query heads per KV head
     int page_log2;
     int q_tile;        // query vectors per unit
-    int k_tile, n_tile;   // cached tokens, new rows per key tile
+    int k_tile, n_tile;   // cached tokens, new rows per key tile (0: the new rows are not counted in tiles)
     int whole;         // 1: worker w runs units w, w + workers, ... whole, and nothing is joined
     int workers;
     float scale_log2;  // scale * log2(e)
     float *part;       // [workers][2][q_tile][head_dim] unnormalised sums
     float *part_ml;    // [workers][2][q_tile][2] running maximum and L
+    struct Kv8Split *split;   // [workers]
+};
+// What a worker's range begins with: a unit that earlier workers began, or not.
+struct Kv8Split {
+    long long t0, t1, total;   // the unit's place in the flattened list, and the list's length
+    int inside;                // 1: the range begins inside a unit
+    int first, head, qv0, nqv; // the unit: first row of its slot, KV head, query vectors
+    int pad;
 };
 
 // ------------------------------------------------------------------ work list
@@ -59,7 +72,7 @@ __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Args &p, int s) {
     q.len = kv8_len(p.c, s);
     q.qtiles = static_cast<int>((static_cast<long long>(q.rows) * p.gq + p.q_tile - 1) / p.q_tile);
     q.ctiles = (q.len + p.k_tile - 1) / p.k_tile;
-    q.ntiles = p.a.k ? (q.rows + p.n_tile - 1) / p.n_tile : 0;
+    q.ntiles = p.a.k && p.n_tile ? (q.rows + p.n_tile - 1) / p.n_tile : 0;
     return q;
 }
 
@@ -109,7 +122,74 @@ __device__ __forceinline__ int kv8_workers(const Kv8Args &p, long long total) {
     return static_cast<int>(min(static_cast<long long>(p.workers), total));
 }
 // First tile of worker w.
-__device__ __forceinline__ long long kv8_share(long long total, int w, int workers) { return total * w / workers; }
+__device__ __forceinline__ long long kv8_div(long long a, int b) {   // a >= 0; 32 bits where they do: 64-bit division is long code
+    return a >> 32 ? a / b : static_cast<long long>(static_cast<unsigned>(a) / static_cast<unsigned>(b));
+}
+__device__ __forceinline__ long long kv8_share(long long total, int w, int workers) { return kv8_div(total * w, workers); }
+
+// The pieces of work of one worker, in order.
+struct Kv8Walk {
+    long long at, end, skip;
+};
+__device__ __forceinline__ Kv8Walk kv8_walk(const Kv8Args &p, long long total) {
+    const int workers = kv8_workers(p, total), b = static_cast<int>(blockIdx.x);
+    if (p.whole) return {0, total, b};
+    if (b >= workers) return {0, 0, 0};
+    return {kv8_share(total, b, workers), kv8_share(total, b + 1, workers), 0};
+}
+struct Kv8Piece {
+    int s, head, qv0, nqv;
+    int k0, k1;          // key tiles
+    bool all, begins;    // the whole unit; its first piece
+    Kv8Seq sq;
+};
+__device__ __forceinline__ bool kv8_next(const Kv8Args &p, const long long *tiles, Kv8Walk &w, Kv8Piece &u) {
+    while (w.at < w.end) {
+        u.s = kv8_find(tiles, p.c.n_seqs, w.at);
+        u.sq = kv8_seq(p, u.s);
+        const int kt = u.sq.ktiles();
+        if (p.whole) {
+            const long long units = kv8_div(tiles[u.s + 1] - w.at, kt);   // of this slot from `at` on
+            if (w.skip >= units) {
+                w.skip -= units;
+                w.at = tiles[u.s + 1];
+                continue;
+            }
+            w.at += w.skip * kt;
+            w.skip = p.workers - 1;
+        }
+        const int unit = static_cast<int>(kv8_div(w.at - tiles[u.s], kt)), v0 = static_cast<int>(w.at - tiles[u.s] - static_cast<long long>(unit) * kt);
+        const int v1 = static_cast<int>(min(static_cast<long long>(kt), v0 + (w.end - w.at)));
+        u.k0 = max(v0 - kUnitCost, 0);
+        u.k1 = max(v1 - kUnitCost, 0);
+        u.all = v0 == 0 && v1 == kt;
+        u.begins = v0 == 0;
+        u.head = unit / u.sq.qtiles;
+        u.qv0 = (unit % u.sq.qtiles) * p.q_tile;
+        u.nqv = min(p.q_tile, u.sq.rows * p.gq - u.qv0);
+        w.at += v1 - v0;
+        return true;
+    }
+    return false;
+}
+
+// Worker b's entry for k_kv8_join, by one thread: `inside` if its first piece u does not begin its unit.
+__device__ __forceinline__ void kv8_note(const Kv8Args &p, const long long *tiles, bool any, const Kv8Piece &u) {
+    Kv8Split x{};
+    x.total = tiles[p.c.n_seqs];
+    x.inside = any && !u.begins;
+    if (x.inside) {
+        const int kt = u.sq.ktiles();
+        const int unit = u.head * u.sq.qtiles + u.qv0 / p.q_tile;
+        x.t0 = tiles[u.s] + static_cast<long long>(unit) * kt;
+        x.t1 = x.t0 + kt;
+        x.first = u.sq.first;
+        x.head = u.head;
+        x.qv0 = u.qv0;
+        x.nqv = u.nqv;
+    }
+    p.split[blockIdx.x] = x;
+}
 
 // ------------------------------------------------------------------ mma
 // D (16 x 8, fp32) += A (16 x 16, fp16) * B (16 x 8, fp16).
@@ -153,9 +233,9 @@ __device__ __forceinline__ int fit_f16(float amax) { return max(exponent_of(amax
 //   V: lane (n, t) reads its KT / 4 consecutive keys of dim 8 i + n.
 // Then the weights of product j's columns 2 t, 2 t + 1 are this lane's keys
 // KT/4 t + 2 j, + 1: already the A operand of the second product.
+// The new rows, at most a few here, are added key by key in fp32.
 constexpr int kRowsWarps = 4;
 constexpr int kRowsQ = 16;
-constexpr int kRowsNew = 64;     // new rows per tile
 
 template <int HD, int PAGE>
 struct Rows {
@@ -163,12 +243,17 @@ struct Rows {
     static constexpr int slots = block >= 8192 ? 3 : 6;                         // of a warp's ring; K and V alternate
     static constexpr int ring = block * slots * kRowsWarps;
     static constexpr int join = kRowsWarps * kRowsQ * (HD + 4) * 4;             // over the ring, at the end of a unit
-    static constexpr int ml_off = ring > join ? ring : join;
+    // q in fp16: lane t's HD / 4 dims and 16 bytes more, so that the lanes
+    // (g, t) of a quarter warp read different banks
+    static constexpr int q_piece = HD / 2 + 16, q_row = 4 * q_piece;
+    static constexpr int q_off = ring > join ? ring : join;
+    static constexpr int qf_off = q_off + kRowsQ * q_row;                       // [16] factor on a row's scores
+    static constexpr int ml_off = qf_off + kRowsQ * 4;
     static constexpr int bar_off = ml_off + kRowsWarps * kRowsQ * 2 * 4;
     static constexpr int meta_off = bar_off + kRowsWarps * slots * 8;           // [warp][slot] factor of K, exponent of V
     static constexpr int sum_off = meta_off + kRowsWarps * slots * 8;
     static constexpr int tiles_off = sum_off + kRowsWarps * 8;                  // (n_seqs + 1) prefix sums follow
-    static constexpr int per_sm = block > 8192 ? 1 : block < 4096 ? 3 : 2;         // CTAs per SM that registers and the ring allow
+    static constexpr int per_sm = block > 8192 ? 1 : block < 4096 ? 3 : 2;      // CTAs per SM that registers and the ring allow
     static size_t bytes(int n_seqs) { return tiles_off + (static_cast<size_t>(n_seqs) + 1) * 8; }
 };
 
@@ -183,37 +268,53 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  "r"(bytes), "r"(bar)
                  : "memory");
 }
+// Larger magnitudes of bf16 pairs: they order like their bits.
+__device__ __forceinline__ uint32_t most2(uint32_t m, uint32_t x) {
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(x & 0x7fff7fffu));
+    return r;
+}
+// Exponent that fits the larger half of `top` into fp16 (1 stays for what is not finite: it reaches no finite result).
+__device__ __forceinline__ int fit_pair(uint32_t top) {
+    const uint32_t x = max(top & 0xffffu, top >> 16);
+    return x < 0x7f80u ? fit_f16(bf16_bits(x)) : 0;
+}
+// A bf16 pair times f, as an fp16 pair.
+__device__ __forceinline__ uint32_t scaled_f16(uint32_t w, float f) { return pack_f16(bf16_bits(w & 0xffffu) * f, __uint_as_float(w & 0xffff0000u) * f); }
 
-// Online softmax of one piece: scores sc (columns: this lane's keys) to the
-// fp16 weights w16, with the running maximum m, the sum l and O's factor.
+// Online softmax of one piece: scores sc (columns: this lane's keys, `live`
+// of them) to the fp16 weights w16, with the running maximum m, the sum l and
+// O's factor.
 template <int NJ, int NI>
-__device__ __forceinline__ void rows_softmax(float (&sc)[NJ][4], const uint32_t (&see)[2], float kf, const float (&qf)[2], int vx,
-                                             float (&m)[2], float (&l)[2], float (&o)[NI][4], uint32_t (&w16)[NJ][2]) {
+__device__ __forceinline__ void rows_softmax(float (&sc)[NJ][4], int live, float kf, const float (&qf)[2], int vx, float (&m)[2],
+                                             float (&l)[2], float (&o)[NI][4], uint32_t (&w16)[NJ][2]) {
+    if (live < 2 * NJ) {
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (2 * j + (e & 1) >= live) sc[j][e] = -INFINITY;   // factors are positive
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {   // rows g (elements 0, 1 of a product) and g + 8 (2, 3)
         const float f = kf * qf[h], add = static_cast<float>(vx);
         float mx = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float &x = sc[j][2 * h + e];
-                x = (see[h] >> (2 * j + e)) & 1u ? fmaf(x, f, add) : -INFINITY;
-                mx = fmaxf(mx, x);
-            }
+        for (int j = 0; j < NJ; ++j) mx = fmaxf(mx, fmaxf(sc[j][2 * h], sc[j][2 * h + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[h], mx), base = mn == -INFINITY ? 0.f : mn;
-        const float alpha = ex2(m[h] - base);
+        const float mn = fmaxf(m[h], fmaf(mx, f, add)), base = mn == -INFINITY ? 0.f : mn;
+        const float alpha = ex2(m[h] - base), off = add - base;
         m[h] = mn;
-        float sum = 0.f;
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            const float a = ex2(sc[j][2 * h] - base), b = ex2(sc[j][2 * h + 1] - base);
-            sum += a + b;
+            const float a = ex2(fmaf(sc[j][2 * h], f, off)), b = ex2(fmaf(sc[j][2 * h + 1], f, off));
+            s0 += a;
+            s1 += b;
             w16[j][h] = pack_f16(a, b);
         }
-        l[h] = l[h] * alpha + sum * power_of(-vx);
+        l[h] = l[h] * alpha + (s0 + s1) * power_of(-vx);
         if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
@@ -228,13 +329,13 @@ template <int HD, int PAGE>
 __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8_rows(const __grid_constant__ Kv8Args p) {
     using Lay = Rows<HD, PAGE>;
     constexpr int NI = HD / 8;                    // 8-dim groups of the output
-    constexpr int KS = HD / 16;                   // steps of the first product
     constexpr int KT = PAGE < 64 ? PAGE : 64;     // keys per piece
-    constexpr int CH = KT / 4;                    // of them, one lane's
+    constexpr int CH = KT / 4, NJ = KT / 8;       // of them, one lane's; products
     constexpr int NS = Lay::slots;
     extern __shared__ __align__(128) uint8_t smem[];
-    float *sh_ml = reinterpret_cast<float *>(smem + Lay::ml_off);   // [warp][16][m, l]
-    float *sh_o = reinterpret_cast<float *>(smem);                  // [warp][16][HD + 4], over the ring
+    float2 *sh_ml = reinterpret_cast<float2 *>(smem + Lay::ml_off);  // [warp][16] m, l
+    float *sh_o = reinterpret_cast<float *>(smem);                   // [warp][16][HD + 4], over the ring
+    float *sh_qf = reinterpret_cast<float *>(smem + Lay::qf_off);
     long long *tiles = reinterpret_cast<long long *>(smem + Lay::tiles_off);
     pdl_trigger();
     const la_kv8_cache &c = p.c;
@@ -246,42 +347,24 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
     fence_barrier_init();
     pdl_wait();
     kv8_plan(p, tiles, reinterpret_cast<long long *>(smem + Lay::sum_off));
-    const long long total = tiles[c.n_seqs];
-    const int workers = kv8_workers(p, total);
-    if (!p.whole && static_cast<int>(blockIdx.x) >= workers) return;
-    long long at = p.whole ? 0 : kv8_share(total, blockIdx.x, workers);
-    const long long end = p.whole ? total : kv8_share(total, blockIdx.x + 1, workers);
-    long long skip = blockIdx.x;   // whole: units to pass over
+    Kv8Walk walk = kv8_walk(p, tiles[c.n_seqs]);
+    Kv8Piece u;
     int in_slot = 0, out_slot = 0;   // ring positions: the next block to load, the next to read
     uint32_t out_phase = 0;
     bool ok = true;                  // false once a wait gave up: this warp loads nothing more
+    bool noted = p.whole;
 
-    while (at < end) {
-        const int s = kv8_find(tiles, c.n_seqs, at);
-        const Kv8Seq sq = kv8_seq(p, s);
-        const int kt = sq.ktiles();
-        if (p.whole) {
-            const long long units = (tiles[s + 1] - at) / kt;   // of this slot from `at` on
-            if (skip >= units) {
-                skip -= units;
-                at = tiles[s + 1];
-                continue;
-            }
-            at += skip * kt;
-            skip = p.workers - 1;
+    for (;;) {
+        const bool any = kv8_next(p, tiles, walk, u);
+        if (!noted) {
+            if (tid == 0) kv8_note(p, tiles, any, u);
+            noted = true;
         }
-        const int unit = static_cast<int>((at - tiles[s]) / kt), v0 = static_cast<int>((at - tiles[s]) % kt);
-        const int v1 = static_cast<int>(min(static_cast<long long>(kt), v0 + (end - at)));
-        const int k0 = max(v0 - kUnitCost, 0), k_end = max(v1 - kUnitCost, 0);   // key tiles of this piece
-        const int head = unit / sq.qtiles, qv0 = (unit % sq.qtiles) * kRowsQ;
-        const int nqv = min(kRowsQ, sq.rows * p.gq - qv0);
-
-        // This warp's tiles: k0 + warp, + 4, ...; the new rows' come first in
-        // the unit.  Cached ones are numbered i = 0 .. nc - 1, page first + 4 i.
-        int kt0 = k0 + warp, first = kt0;
-        while (first < sq.ntiles) first += kRowsWarps;
-        const int nc = ok && first < k_end ? (k_end - first + kRowsWarps - 1) / kRowsWarps : 0;
-        const int page0 = first - sq.ntiles;
+        if (!any) break;
+        const Kv8Seq sq = u.sq;
+        // This warp's tiles: pages page0 + 4 i, i = 0 .. nc - 1.
+        const int page0 = u.k0 + warp, s = u.s, head = u.head;
+        const int nc = ok && page0 < u.k1 ? (u.k1 - page0 + kRowsWarps - 1) / kRowsWarps : 0;
         // Block 2 i is K of tile i, block 2 i + 1 its V.  Page numbers and
         // scales are looked up 32 tiles at a time, lane i for tile 32 n + i.
         int my_page = -1, my_vx = 0, issued = 0;
@@ -312,133 +395,97 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
             in_slot = in_slot + 1 == NS ? 0 : in_slot + 1;
             ++issued;
         };
+#pragma unroll 1
         while (issued < min(NS, 2 * nc)) issue();
 
-        // q as fp16 A operands, each vector scaled by a power of two to fit.
-        uint32_t q[KS][4];
-        float qf[2];
-        int myrow[2];
+        // q as fp16, each vector scaled by a power of two to fit: 8 threads a row.
+        {
+            constexpr int NW = HD / 64;   // 16-byte pieces of a thread's HD / 8 dims
+            const int r = tid >> 3, part = tid & 7, qv = u.qv0 + r;
+            const bool in = r < u.nqv;
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.q) + (sq.first + (in ? qv / p.gq : 0)) * p.a.q_stride +
+                                                               (head * p.gq + (in ? qv % p.gq : 0)) * HD + part * (HD / 8));
+            uint4 w[NW];
+            uint32_t top = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int qv = qv0 + g + 8 * h;
-            const bool in = g + 8 * h < nqv;
-            myrow[h] = in ? qv / p.gq : -1;
-            uint4 w[KS / 2];
-            float amax = 0.f;
-            const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.a.q) + (sq.first + max(myrow[h], 0)) * p.a.q_stride +
-                                       (head * p.gq + (in ? qv % p.gq : 0)) * HD + t * (HD / 4);
+            for (int i = 0; i < NW; ++i) w[i] = in ? src[i] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < KS / 2; ++i) {
-                w[i] = in ? reinterpret_cast<const uint4 *>(src)[i] : make_uint4(0, 0, 0, 0);
-                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            for (int i = 0; i < NW; ++i) top = most2(most2(most2(most2(top, w[i].x), w[i].y), w[i].z), w[i].w);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float lo = bf16_bits(u[k] & 0xffffu), hi = bf16_bits(u[k] >> 16);
-                    if (is_finite(lo)) amax = fmaxf(amax, fabsf(lo));
-                    if (is_finite(hi)) amax = fmaxf(amax, fabsf(hi));
-                }
-            }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const int qx = fit_f16(amax);
+            for (int k = 1; k < 8; k <<= 1) top = most2(top, __shfl_xor_sync(0xffffffffu, top, k));
+            const int qx = fit_pair(top);
             const float f = power_of(-qx);
-            qf[h] = power_of(qx) * p.scale_log2;
+            uint4 *dst = reinterpret_cast<uint4 *>(smem + Lay::q_off + r * Lay::q_row + (part >> 1) * Lay::q_piece + (part & 1) * (HD / 4));
 #pragma unroll
-            for (int i = 0; i < KS / 2; ++i) {
-                const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)   // word k: dims 2k, 2k + 1 of 8; step 2 i + k / 2, half k & 1
-                    q[2 * i + (k >> 1)][h + 2 * (k & 1)] = pack_f16(bf16_bits(u[k] & 0xffffu) * f, bf16_bits(u[k] >> 16) * f);
-            }
+            for (int i = 0; i < NW; ++i) dst[i] = make_uint4(scaled_f16(w[i].x, f), scaled_f16(w[i].y, f), scaled_f16(w[i].z, f), scaled_f16(w[i].w, f));
+            if (part == 0) sh_qf[r] = power_of(qx) * p.scale_log2;
         }
+        __syncthreads();
+        const uint8_t *my_q = smem + Lay::q_off + g * Lay::q_row + t * Lay::q_piece;   // row g; row g + 8 lies 8 rows behind
+        const float qf[2] = {sh_qf[g], sh_qf[g + 8]};
 
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
         float o[NI][4];
 #pragma unroll
         for (int i = 0; i < NI; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-        // ---- new rows: bf16, scaled by a power of two for the whole tile
-        for (; kt0 < min(k_end, sq.ntiles); kt0 += kRowsWarps) {
-            constexpr int NJ = kRowsNew / 8;
-            const int key0 = kt0 * kRowsNew, nkeys = min(kRowsNew, sq.rows - key0);
-            const __nv_bfloat16 *kn = static_cast<const __nv_bfloat16 *>(p.a.k) + (sq.first + key0) * p.a.k_stride + head * HD;
-            const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + head * HD;
-            float ak = 0.f, av = 0.f;
-            for (int i = lane; i < nkeys * (HD / 2); i += 32) {
-                const int r = i / (HD / 2), d = 2 * (i % (HD / 2));
-                const uint32_t a = *reinterpret_cast<const uint32_t *>(kn + r * p.a.k_stride + d);
-                const uint32_t b = *reinterpret_cast<const uint32_t *>(vn + r * p.a.v_stride + d);
-                const float x[4] = {bf16_bits(a & 0xffffu), bf16_bits(a >> 16), bf16_bits(b & 0xffffu), bf16_bits(b >> 16)};
+        // ---- new rows, in the piece that begins the unit: one key at a time
+        if (u.begins && p.a.k) {
+            const int r0 = g < u.nqv ? (u.qv0 + g) / p.gq : -1, r1 = g + 8 < u.nqv ? (u.qv0 + g + 8) / p.gq : -1;
+#pragma unroll 1
+            for (int j = warp; j < sq.rows; j += kRowsWarps) {
+                const uint4 *kj = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.k) + (sq.first + j) * p.a.k_stride + head * HD + t * (HD / 4));
+                const uint32_t *vj = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + j) * p.a.v_stride + head * HD) + t;
+                uint4 kw[HD / 32];
+                uint32_t vw[NI];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if (is_finite(x[k])) ak = fmaxf(ak, fabsf(x[k]));
-                    if (is_finite(x[2 + k])) av = fmaxf(av, fabsf(x[2 + k]));
+                for (int i = 0; i < HD / 32; ++i) kw[i] = kj[i];
+#pragma unroll
+                for (int i = 0; i < NI; ++i) vw[i] = vj[4 * i];
+                bool see[2];
+                if (p.a.vis) {
+                    see[0] = r0 >= 0 && j < 256 && (p.a.vis[(static_cast<long long>(sq.first) + r0) * 8 + j / 32] >> (j % 32) & 1u);
+                    see[1] = r1 >= 0 && j < 256 && (p.a.vis[(static_cast<long long>(sq.first) + r1) * 8 + j / 32] >> (j % 32) & 1u);
+                } else {
+                    see[0] = j <= r0;
+                    see[1] = j <= r1;
                 }
-            }
-            const int kx = fit_f16(warp_max(ak)), vx = fit_f16(warp_max(av));
-            const int live = min(max(nkeys - 16 * t, 0), 16);
-            uint32_t see[2];   // bit 2 j + e: this lane's key 16 t + 2 j + e is seen by row h
+                float z[2] = {0.f, 0.f};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = key0 + 16 * t;
-                if (myrow[h] < 0) see[h] = 0;
-                else if (p.a.vis)
-                    see[h] = k < 256 ? p.a.vis[(static_cast<long long>(sq.first) + myrow[h]) * 8 + k / 32] >> (k % 32) & 0xffffu : 0;
-                else see[h] = myrow[h] >= k + 15 ? 0xffffu : myrow[h] < k ? 0u : (2u << (myrow[h] - k)) - 1u;
-                if (live < 16) see[h] &= (1u << live) - 1u;
-            }
-            float sc[NJ][4];
-            const float f = power_of(-kx);
+                for (int i = 0; i < HD / 32; ++i) {
+                    const uint4 a = *reinterpret_cast<const uint4 *>(my_q + 16 * i), b = *reinterpret_cast<const uint4 *>(my_q + 8 * Lay::q_row + 16 * i);
+                    const uint32_t x[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w}, y[4] = {a.x, a.y, a.z, a.w}, w[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) {
-                sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
-                if (2 * j >= nkeys) continue;
-                const int r = 16 * (g >> 1) + 2 * j + (g & 1);
-                const __nv_bfloat16 *row = kn + r * p.a.k_stride + t * (HD / 4);
-#pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    const uint2 w = r < nkeys ? *reinterpret_cast<const uint2 *>(row + 4 * i) : make_uint2(0, 0);
-                    mma_f16(sc[j], q[i], pack_f16(bf16_bits(w.x & 0xffffu) * f, bf16_bits(w.x >> 16) * f),
-                            pack_f16(bf16_bits(w.y & 0xffffu) * f, bf16_bits(w.y >> 16) * f));
-                }
-            }
-            uint32_t w16[NJ][2];
-            rows_softmax<NJ, NI>(sc, see, power_of(kx), qf, vx, m, l, o, w16);
-            // A NaN or infinity of V counts 0 in the product (0 * inf would
-            // reach rows that do not see it) and is added for the rows that do.
-            const float fv = power_of(-vx);
-            bool odd = false;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-#pragma unroll
-                for (int k = 0; k < NJ / 2; ++k) {
-                    if (4 * k >= nkeys) continue;
-                    float x[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = 16 * t + 4 * k + e;
-                        x[e] = r < nkeys ? __bfloat162float(vn[r * p.a.v_stride + 8 * i + g]) : 0.f;
-                        odd |= !is_finite(x[e]);
-                        x[e] = is_finite(x[e]) ? x[e] * fv : 0.f;
+                    for (int k = 0; k < 4; ++k) {
+                        const float lo = bf16_bits(x[k] & 0xffffu), hi = __uint_as_float(x[k] & 0xffff0000u);
+                        const float2 qa = __half22float2(*reinterpret_cast<const __half2 *>(&y[k])), qb = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+                        z[0] = fmaf(qa.x, lo, fmaf(qa.y, hi, z[0]));
+                        z[1] = fmaf(qb.x, lo, fmaf(qb.y, hi, z[1]));
                     }
-                    const uint32_t a[4] = {w16[2 * k][0], w16[2 * k][1], w16[2 * k + 1][0], w16[2 * k + 1][1]};
-                    mma_f16(o[i], a, pack_f16(x[0], x[1]), pack_f16(x[2], x[3]));
+                }
+                float w[2], alpha[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    z[h] += __shfl_xor_sync(0xffffffffu, z[h], 1);
+                    z[h] += __shfl_xor_sync(0xffffffffu, z[h], 2);
+                    const float x = see[h] ? z[h] * qf[h] : -INFINITY, mn = fmaxf(m[h], x), base = mn == -INFINITY ? 0.f : mn;
+                    alpha[h] = ex2(m[h] - base);
+                    w[h] = ex2(x - base);
+                    m[h] = mn;
+                    l[h] = l[h] * alpha[h] + w[h];
+                }
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const float lo = bf16_bits(vw[i] & 0xffffu), hi = __uint_as_float(vw[i] & 0xffff0000u);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {   // what a row does not see never meets it, not even times 0
+                        o[i][2 * h] = fmaf(w[h], see[h] ? lo : 0.f, o[i][2 * h] * alpha[h]);
+                        o[i][2 * h + 1] = fmaf(w[h], see[h] ? hi : 0.f, o[i][2 * h + 1] * alpha[h]);
+                    }
                 }
             }
-            if (__any_sync(0xffffffffu, odd)) {
-#pragma unroll
-                for (int i = 0; i < NI; ++i)
-                    for (int r = 0; r < nkeys; ++r) {
-                        const uint32_t b0 = __shfl_sync(0xffffffffu, see[0], 4 * g + (r >> 4)), b1 = __shfl_sync(0xffffffffu, see[1], 4 * g + (r >> 4));
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float x = __bfloat162float(vn[r * p.a.v_stride + 8 * i + 2 * t + e]);
-                            if (is_finite(x)) continue;
-                            if ((b0 >> (r & 15)) & 1u) o[i][e] += x;
-                            if ((b1 >> (r & 15)) & 1u) o[i][2 + e] += x;
-                        }
-                    }
-            }
+            // Every lane of a quad has added the key: l is summed over the quad below.
+            if (t != 0) l[0] = l[1] = 0.f;
         }
 
         // ---- cached tokens
@@ -455,22 +502,25 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
             if (issued < 2 * nc) issue();
         };
         int read = 0;           // blocks read
+#pragma unroll 1
         for (int i = 0; i < nc; ++i) {
             if (!landed()) break;
             const int2 mt = meta[out_slot];
-            const float kf = __int_as_float(mt.x);
+            const float kf = mt.x == -1 ? 1.f : __int_as_float(mt.x);
             const int vx = mt.y;
             const int left = mt.x == -1 ? 0 : sq.len - (page0 + kRowsWarps * i) * PAGE;   // keys of this page that count
-            constexpr int NJ = KT / 8;
-            float sc[PAGE / KT][NJ][4];
-            const uint8_t *kblk = my_ring + out_slot * Lay::block;
-#pragma unroll
+            const uint8_t *kblk = my_ring + out_slot * Lay::block, *vblk = nullptr;
+#pragma unroll 1
             for (int piece = 0; piece < PAGE / KT; ++piece) {
+                float sc[NJ][4];
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
                 const uint8_t *row = kblk + (piece * KT + CH * (g >> 1) + (g & 1)) * HD + t * (HD / 4);
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) sc[piece][j][0] = sc[piece][j][1] = sc[piece][j][2] = sc[piece][j][3] = 0.f;
-#pragma unroll
+#pragma unroll 1
                 for (int x = 0; x < HD / 64; ++x) {   // steps outside, products inside: their sums do not wait on one another
+                    const uint4 qa0 = *reinterpret_cast<const uint4 *>(my_q + 32 * x), qa1 = *reinterpret_cast<const uint4 *>(my_q + 32 * x + 16);
+                    const uint4 qb0 = *reinterpret_cast<const uint4 *>(my_q + 8 * Lay::q_row + 32 * x), qb1 = *reinterpret_cast<const uint4 *>(my_q + 8 * Lay::q_row + 32 * x + 16);
+                    const uint32_t q[4][4] = {{qa0.x, qb0.x, qa0.y, qb0.y}, {qa0.z, qb0.z, qa0.w, qb0.w}, {qa1.x, qb1.x, qa1.y, qb1.y}, {qa1.z, qb1.z, qa1.w, qb1.w}};
                     uint4 w[NJ];
 #pragma unroll
                     for (int j = 0; j < NJ; ++j) w[j] = *reinterpret_cast<const uint4 *>(row + 2 * j * HD + 16 * x);
@@ -480,35 +530,37 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
                         for (int j = 0; j < NJ; ++j) {
                             uint32_t b0, b1;
                             e4m3x4_f16(k == 0 ? w[j].x : k == 1 ? w[j].y : k == 2 ? w[j].z : w[j].w, b0, b1);
-                            mma_f16(sc[piece][j], q[4 * x + k], b0, b1);
+                            mma_f16(sc[j], q[k], b0, b1);
                         }
                 }
-            }
-            next();
-            ++read;
-            if (!landed()) break;
-            const uint8_t *vblk = my_ring + out_slot * Lay::block;
-#pragma unroll
-            for (int piece = 0; piece < PAGE / KT; ++piece) {
+                if (piece == PAGE / KT - 1) {
+                    next();
+                    ++read;
+                }
                 const int live = min(max(left - piece * KT - CH * t, 0), CH);
-                const uint32_t see1 = (1u << live) - 1u;
-                const uint32_t see[2] = {see1, see1};
                 uint32_t w16[NJ][2];
-                rows_softmax<NJ, NI>(sc[piece], see, kf, qf, vx, m, l, o, w16);
+                rows_softmax<NJ, NI>(sc, live, kf, qf, vx, m, l, o, w16);
+                if (piece == 0) {   // V is the block behind K
+                    const int vs = PAGE / KT == 1 ? out_slot : out_slot + 1 == NS ? 0 : out_slot + 1;
+                    const uint32_t ph = PAGE / KT == 1 || out_slot + 1 < NS ? out_phase : out_phase ^ 1;
+                    ok = __all_sync(0xffffffffu, mbar_wait(bars + vs * 8, ph, c.status, LA_KV8_TIMEOUT));
+                    if (!ok) break;
+                    vblk = my_ring + vs * Lay::block;
+                }
                 const uint8_t *col = vblk + g * PAGE + piece * KT + CH * t;
                 const bool whole = left >= PAGE;
                 constexpr int NG = 4;   // output groups in flight together
 #pragma unroll
                 for (int n0 = 0; n0 < NI; n0 += NG) {
-                    uint32_t u[NG][CH / 4];
+                    uint32_t w[NG][CH / 4];
 #pragma unroll
                     for (int n = 0; n < NG; ++n) {
                         if constexpr (CH == 16) {
-                            const uint4 w = *reinterpret_cast<const uint4 *>(col + 8 * (n0 + n) * PAGE);
-                            u[n][0] = w.x, u[n][1] = w.y, u[n][2] = w.z, u[n][3] = w.w;
+                            const uint4 x = *reinterpret_cast<const uint4 *>(col + 8 * (n0 + n) * PAGE);
+                            w[n][0] = x.x, w[n][1] = x.y, w[n][2] = x.z, w[n][3] = x.w;
                         } else {
-                            const uint2 w = *reinterpret_cast<const uint2 *>(col + 8 * (n0 + n) * PAGE);
-                            u[n][0] = w.x, u[n][1] = w.y;
+                            const uint2 x = *reinterpret_cast<const uint2 *>(col + 8 * (n0 + n) * PAGE);
+                            w[n][0] = x.x, w[n][1] = x.y;
                         }
                     }
                     if (!whole) {   // bytes behind the last token may be anything
@@ -517,7 +569,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
                             const int b = live - 4 * k;
                             const uint32_t mask = b >= 4 ? 0xffffffffu : b <= 0 ? 0u : (1u << (8 * b)) - 1u;
 #pragma unroll
-                            for (int n = 0; n < NG; ++n) u[n][k] &= mask;
+                            for (int n = 0; n < NG; ++n) w[n][k] &= mask;
                         }
                     }
 #pragma unroll
@@ -526,12 +578,13 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
 #pragma unroll
                         for (int n = 0; n < NG; ++n) {
                             uint32_t b0, b1;
-                            e4m3x4_f16(u[n][k], b0, b1);
+                            e4m3x4_f16(w[n][k], b0, b1);
                             mma_f16(o[n0 + n], a, b0, b1);
                         }
                     }
                 }
             }
+            if (!ok) break;
             next();
             ++read;
         }
@@ -552,41 +605,38 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
             const int r = warp * kRowsQ + g + 8 * h;
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            if (t == 0) *reinterpret_cast<float2 *>(sh_ml + 2 * r) = make_float2(m[h], l[h]);
-            if (g + 8 * h < nqv) {
+            if (t == 0) sh_ml[r] = make_float2(m[h], l[h]);
+            if (g + 8 * h < u.nqv) {
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
                     *reinterpret_cast<float2 *>(sh_o + r * (HD + 4) + 8 * i + 2 * t) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
             }
         }
         __syncthreads();
-        const bool all = v0 == 0 && v1 == kt;
-        const int slot = 2 * blockIdx.x + (v0 == 0 ? 1 : 0);
-        for (int i = tid; i < nqv * (HD / 4); i += 32 * kRowsWarps) {
+        const int slot = 2 * blockIdx.x + (u.begins ? 1 : 0);
+#pragma unroll 1
+        for (int i = tid; i < u.nqv * (HD / 4); i += 32 * kRowsWarps) {
             const int r = i / (HD / 4), d = 4 * (i % (HD / 4));
-            float2 ml[kRowsWarps];
             float mx = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kRowsWarps; ++w) {
-                ml[w] = *reinterpret_cast<const float2 *>(sh_ml + 2 * (w * kRowsQ + r));
-                mx = fmaxf(mx, ml[w].x);
-            }
+            for (int w = 0; w < kRowsWarps; ++w) mx = fmaxf(mx, sh_ml[w * kRowsQ + r].x);
             float L = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
+#pragma unroll 1
             for (int w = 0; w < kRowsWarps; ++w) {
-                if (ml[w].y == 0.f) continue;   // saw no key
-                const float f = ex2(ml[w].x - mx);
+                const float2 ml = sh_ml[w * kRowsQ + r];
+                if (ml.y == 0.f) continue;   // saw no key
+                const float f = ex2(ml.x - mx);
                 const float4 x = *reinterpret_cast<const float4 *>(sh_o + (w * kRowsQ + r) * (HD + 4) + d);
-                L += f * ml[w].y;
+                L += f * ml.y;
                 acc.x += f * x.x;
                 acc.y += f * x.y;
                 acc.z += f * x.z;
                 acc.w += f * x.w;
             }
-            if (all) {
+            if (u.all) {
                 const float inv = L == 0.f ? 0.f : 1.f / L;
-                const int qv = qv0 + r;
+                const int qv = u.qv0 + r;
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + (sq.first + qv / p.gq) * p.a.out_stride +
                                      (head * p.gq + qv % p.gq) * HD + d;
                 const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
@@ -598,7 +648,6 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
         }
         fence_proxy_async_smem();   // these accesses before the next unit's bulk copies into the same bytes
         __syncthreads();
-        at += v1 - v0;
     }
 }
 
@@ -668,46 +717,6 @@ __device__ __forceinline__ void mbar_arrive_one(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// The pieces of work of one worker, in order; every role of the CTA walks them.
-struct Kv8Walk {
-    long long at, end, skip;
-};
-struct Kv8Piece {
-    int s, head, qv0, nqv;
-    int k0, k1;          // key tiles
-    bool all, begins;    // the whole unit; its first piece
-    Kv8Seq sq;
-};
-__device__ __forceinline__ bool kv8_next(const Kv8Args &p, const long long *tiles, Kv8Walk &w, Kv8Piece &u) {
-    while (w.at < w.end) {
-        u.s = kv8_find(tiles, p.c.n_seqs, w.at);
-        u.sq = kv8_seq(p, u.s);
-        const int kt = u.sq.ktiles();
-        if (p.whole) {
-            const long long units = (tiles[u.s + 1] - w.at) / kt;   // of this slot from `at` on
-            if (w.skip >= units) {
-                w.skip -= units;
-                w.at = tiles[u.s + 1];
-                continue;
-            }
-            w.at += w.skip * kt;
-            w.skip = p.workers - 1;
-        }
-        const int unit = static_cast<int>((w.at - tiles[u.s]) / kt), v0 = static_cast<int>((w.at - tiles[u.s]) % kt);
-        const int v1 = static_cast<int>(min(static_cast<long long>(kt), v0 + (w.end - w.at)));
-        u.k0 = max(v0 - kUnitCost, 0);
-        u.k1 = max(v1 - kUnitCost, 0);
-        u.all = v0 == 0 && v1 == kt;
-        u.begins = v0 == 0;
-        u.head = unit / u.sq.qtiles;
-        u.qv0 = (unit % u.sq.qtiles) * p.q_tile;
-        u.nqv = min(p.q_tile, u.sq.rows * p.gq - u.qv0);
-        w.at += v1 - v0;
-        return true;
-    }
-    return false;
-}
-
 // 16 e4m3 bytes as 32 bytes of fp16.
 __device__ __forceinline__ void e4m3x16_f16(const uint4 &w, uint4 &a, uint4 &b) {
     e4m3x4_f16(w.x, a.x, a.y);
@@ -771,14 +780,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     tc_fence_after();
     pdl_trigger();
     const uint32_t tmem = *tmem_slot;
-    const long long total = tiles[c.n_seqs];
-    const int workers = kv8_workers(p, total);
-    Kv8Walk walk{0, total, static_cast<long long>(blockIdx.x)};
-    if (!p.whole) {
-        const bool none = static_cast<int>(blockIdx.x) >= workers;
-        walk.at = none ? 0 : kv8_share(total, blockIdx.x, workers);
-        walk.end = none ? 0 : kv8_share(total, blockIdx.x + 1, workers);
-    }
+    Kv8Walk walk = kv8_walk(p, tiles[c.n_seqs]);
     Kv8Piece u;
     int it = 0;          // key tiles so far, the same count in every role: buffer it & 1, its use it >> 1
     bool ok = true;
@@ -830,7 +832,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             };
             // Pages of tiles kt - 1, kt, kt + 1 and the entries of kt + 2, kt being the tile whose K is put next.
             int pg_v = -1, pg_k = checked(entry(c_first)), pg_next = checked(entry(c_first + 1)), after = entry(c_first + 2);
-            if (c_first < u.k1) {
+            if (c_first < u.k1 && c_first == u.k0) {   // else behind the new rows' tiles
                 load_k(c_first, pg_k);
                 load_v(c_first, pg_k);
             }
@@ -867,19 +869,29 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                     // rows that see it.
                     const int key0 = kt * kTileK, nkeys = min(kTileK, sq.rows - key0);
                     const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + u.head * HD;
-                    for (int i = w * 32 + lane; i < kTileK / 2 * (HD / 8); i += 32 * kOperandWarps) {
-                        const int r = 2 * (i / (HD / 8)), d = 8 * (i % (HD / 8));
-                        const uint4 a = r < nkeys ? *reinterpret_cast<const uint4 *>(vn + r * p.a.v_stride + d) : make_uint4(0, 0, 0, 0);
-                        const uint4 e = r + 1 < nkeys ? *reinterpret_cast<const uint4 *>(vn + (r + 1) * p.a.v_stride + d) : make_uint4(0, 0, 0, 0);
-                        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {e.x, e.y, e.z, e.w};
-                        const uint32_t at = sv + (r >> 6) * Lay::v_block + (r & 7) * 2;
+                    constexpr int NT = 32 * kOperandWarps, NB = kTileK / 2 * (HD / 8) / NT, B = 4;   // pairs of rows per thread, in flight
+#pragma unroll 1
+                    for (int i0 = 0; i0 < NB; i0 += B) {
+                        uint4 va[B], vb[B];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            float f0 = bf16_bits(k & 1 ? x[k >> 1] >> 16 : x[k >> 1] & 0xffffu), f1 = bf16_bits(k & 1 ? y[k >> 1] >> 16 : y[k >> 1] & 0xffffu);
-                            f0 = is_finite(f0) ? f0 * fv : 0.f;
-                            f1 = is_finite(f1) ? f1 * fv : 0.f;
-                            const int dim = d + k;
-                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + dim * 128 + ((((r >> 3) & 7) ^ (dim & 7)) << 4)), "r"(pack_f16(f0, f1)) : "memory");
+                        for (int q = 0; q < B; ++q) {
+                            const int j = w * 32 + lane + (i0 + q) * NT, r = 2 * (j % (kTileK / 2)), d = 8 * (j / (kTileK / 2));   // lanes: rows, other banks
+                            va[q] = r < nkeys ? *reinterpret_cast<const uint4 *>(vn + r * p.a.v_stride + d) : make_uint4(0, 0, 0, 0);
+                            vb[q] = r + 1 < nkeys ? *reinterpret_cast<const uint4 *>(vn + (r + 1) * p.a.v_stride + d) : make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int q = 0; q < B; ++q) {
+                            const int j = w * 32 + lane + (i0 + q) * NT, r = 2 * (j % (kTileK / 2)), d = 8 * (j / (kTileK / 2));   // lanes: rows, other banks
+                            const uint32_t x[4] = {va[q].x, va[q].y, va[q].z, va[q].w}, y[4] = {vb[q].x, vb[q].y, vb[q].z, vb[q].w};
+                            const uint32_t at = sv + (r >> 6) * Lay::v_block + (r & 7) * 2;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                float f0 = bf16_bits(k & 1 ? x[k >> 1] >> 16 : x[k >> 1] & 0xffffu), f1 = bf16_bits(k & 1 ? y[k >> 1] >> 16 : y[k >> 1] & 0xffffu);
+                                f0 = is_finite(f0) ? f0 * fv : 0.f;
+                                f1 = is_finite(f1) ? f1 * fv : 0.f;
+                                const int dim = d + k;
+                                asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + dim * 128 + ((((r >> 3) & 7) ^ (dim & 7)) << 4)), "r"(pack_f16(f0, f1)) : "memory");
+                            }
                         }
                     }
                 }
@@ -925,21 +937,41 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                     const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + u.head * HD;
                     constexpr int C8 = HD / 8, NT = 32 * kOperandWarps;   // 16-byte pieces of a row
                     const int ot = w * 32 + lane;
+                    // Loads go out 8 at a time (one by one they took 12 us); K stays in
+                    // the registers that hold cached bytes otherwise.
+                    constexpr int NB = kTileK * C8 / NT / 2;   // half of a thread's pieces of K, or of V
+                    static_assert(NB == NR, "kraw and vraw hold a tile of new rows");
                     uint32_t ak = 0, av = 0;   // magnitudes order like their bits
                     bool odd = false;
-                    for (int i = ot; i < nkeys * C8; i += NT) {
+                    auto most = [&](const uint4 &x, uint32_t &top) {
+                        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t e = y[k] & 0x7fffu, f = y[k] >> 16 & 0x7fffu;
+                            if (e < 0x7f80u) top = max(top, e);
+                            else odd = true;
+                            if (f < 0x7f80u) top = max(top, f);
+                            else odd = true;
+                        }
+                    };
+                    auto fetch = [&](const __nv_bfloat16 *from, int64_t stride, int i) {
                         const int r = i / C8, d = 8 * (i % C8);
-                        const uint4 a = *reinterpret_cast<const uint4 *>(kn + r * p.a.k_stride + d), v = *reinterpret_cast<const uint4 *>(vn + r * p.a.v_stride + d);
-                        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {v.x, v.y, v.z, v.w};
+                        return r < nkeys ? *reinterpret_cast<const uint4 *>(from + r * stride + d) : make_uint4(0, 0, 0, 0);
+                    };
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
+                    for (int i = 0; i < NB; ++i) kraw[i] = fetch(kn, p.a.k_stride, ot + i * NT);
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const uint32_t e = (x[k] >> (16 * h)) & 0x7fffu, f = (y[k] >> (16 * h)) & 0x7fffu;
-                                if (e < 0x7f80u) ak = max(ak, e);
-                                if (f < 0x7f80u) av = max(av, f);
-                                else odd = true;
-                            }
+                    for (int i = 0; i < NB; ++i) vraw[i] = fetch(kn, p.a.k_stride, ot + (NB + i) * NT);
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) most(kraw[i], ak), most(vraw[i], ak);
+                    odd = false;   // only V's matter
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        uint4 x[NB];
+#pragma unroll
+                        for (int i = 0; i < NB; ++i) x[i] = fetch(vn, p.a.v_stride, ot + (h * NB + i) * NT);
+#pragma unroll
+                        for (int i = 0; i < NB; ++i) most(x[i], av);
                     }
                     ak = __reduce_max_sync(0xffffffffu, ak);
                     av = __reduce_max_sync(0xffffffffu, av);
@@ -978,19 +1010,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                         if (lane == 0) mbar_arrive_one(m_full(it & 3));
                     }
                     const float fk = power_of(-kx);
-                    for (int i = ot; i < kTileK * C8; i += NT) {
+                    auto put = [&](const uint4 &a, int i) {
                         const int r = i / C8, d8 = i % C8;
-                        const uint4 a = r < nkeys ? *reinterpret_cast<const uint4 *>(kn + r * p.a.k_stride + 8 * d8) : make_uint4(0, 0, 0, 0);
                         const uint32_t x[4] = {a.x, a.y, a.z, a.w};
                         uint32_t y[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) y[k] = pack_f16(bf16_bits(x[k] & 0xffffu) * fk, bf16_bits(x[k] >> 16) * fk);
                         st_shared_u32x4(sk + (d8 >> 3) * Lay::k_block + r * 128 + (((d8 & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
-                    }
+                    };
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) put(kraw[i], ot + i * NT), put(vraw[i], ot + (NB + i) * NT);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_one(k_full(b));
+                // (The entry is checked before the loads below are issued: a wait for
+                // it would wait for them too.)
+                const int pg_after = checked(after);
                 if (kt >= sq.ntiles && kt + 1 < u.k1) load_k(kt + 1, pg_next);
                 if (it > begin) put_v(kt - 1, it - 1);
                 fv = fv_next;
@@ -998,8 +1034,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                     if (kt > c_first) load_v(kt, pg_k);
                     pg_v = pg_k;
                     pg_k = pg_next;
-                    pg_next = checked(after);
+                    pg_next = pg_after;
                     after = entry(kt + 3);
+                } else if (kt + 1 == c_first && c_first < u.k1) {
+                    load_k(c_first, pg_k);
+                    load_v(c_first, pg_k);
                 }
             }
             if (ok && it > begin) put_v(u.k1 - 1, it - 1);
@@ -1007,6 +1046,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     } else if (warp == kMmaWarp) {
         // ================================================ products
         if (lane == 0) {
+            if (!p.whole) {
+                Kv8Walk w = walk;
+                const bool any = kv8_next(p, tiles, w, u);
+                kv8_note(p, tiles, any, u);
+            }
             constexpr uint32_t is = idesc_f16(kTileQ, kTileK), io = idesc_f16(kTileQ, HD);
             int units = 0;
             auto product_o = [&](int j, bool begins) {
@@ -1288,61 +1332,56 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
 // A unit that several workers share: worker ranges are contiguous, so the
 // unit's pieces are those of consecutive workers, the first in its slot 1
 // (the piece begins the unit), the others in their slot 0.  One CTA per border
-// between workers; the first border inside a unit adds its pieces, in order.
-constexpr int kJoinThreads = 512, kJoinBatch = 8;
+// between workers; the borders inside a unit share its query vectors and add
+// its pieces in order.
+constexpr int kJoinThreads = 256, kJoinBatch = 4;
 
 template <int HD>
 __global__ void __launch_bounds__(kJoinThreads) k_kv8_join(const __grid_constant__ Kv8Args p) {
-    extern __shared__ long long join_tiles[];   // [n_seqs + 1]
-    __shared__ long long warp_sum[kJoinThreads / 32];
     pdl_trigger();
     pdl_wait();
-    long long *tiles = join_tiles;
-    kv8_plan(p, tiles, warp_sum);
-    const long long total = tiles[p.c.n_seqs];
-    const int workers = kv8_workers(p, total), border = blockIdx.x + 1;
-    if (border >= workers) return;
-    const long long cut = kv8_share(total, border, workers);
-    const int s = kv8_find(tiles, p.c.n_seqs, cut);
-    const Kv8Seq sq = kv8_seq(p, s);
-    const int kt = sq.ktiles();
-    const long long u = (cut - tiles[s]) / kt, t0 = tiles[s] + u * kt, t1 = t0 + kt;
-    if (cut == t0 || kv8_share(total, border - 1, workers) > t0) return;
-    const int w0 = border - 1;
-    int w1 = border;   // the last worker with a piece
-    while (w1 + 1 < workers && kv8_share(total, w1 + 1, workers) < t1) ++w1;
-    const int head = static_cast<int>(u) / sq.qtiles, qv0 = (static_cast<int>(u) % sq.qtiles) * p.q_tile;
-    const int nqv = min(p.q_tile, sq.rows * p.gq - qv0);
-    for (int i = threadIdx.x; i < nqv * (HD / 4); i += kJoinThreads) {
+    const int border = blockIdx.x + 1;
+    const Kv8Split x = p.split[border];
+    if (!x.inside) return;
+    const int workers = kv8_workers(p, x.total);
+    int w0 = border - 1, w1 = border;   // first and last worker with a piece
+#pragma unroll 1
+    while (kv8_share(x.total, w0, workers) > x.t0) --w0;
+#pragma unroll 1
+    while (w1 + 1 < workers && kv8_share(x.total, w1 + 1, workers) < x.t1) ++w1;
+    const int items = x.nqv * (HD / 4), share = border - w0 - 1, shares = w1 - w0;
+#pragma unroll 1
+    for (int i = items * share / shares + threadIdx.x; i < items * (share + 1) / shares; i += kJoinThreads) {
         const int r = i / (HD / 4), d = 4 * (i % (HD / 4));
         // pieces kJoinBatch at a time, so that their loads are in flight together
         float mx = -INFINITY, L = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
         for (int w = w0; w <= w1; w += kJoinBatch) {
             float2 ml[kJoinBatch];
-            float4 x[kJoinBatch];
+            float4 v[kJoinBatch];
 #pragma unroll
             for (int b = 0; b < kJoinBatch; ++b) {
                 const int ww = min(w + b, w1);
                 const long long rec = static_cast<long long>(2 * ww + (ww == w0 ? 1 : 0)) * p.q_tile + r;
                 ml[b] = *reinterpret_cast<const float2 *>(p.part_ml + rec * 2);
-                x[b] = *reinterpret_cast<const float4 *>(p.part + rec * HD + d);
+                v[b] = *reinterpret_cast<const float4 *>(p.part + rec * HD + d);
             }
 #pragma unroll
             for (int b = 0; b < kJoinBatch; ++b) {
                 if (w + b > w1 || ml[b].y == 0.f) continue;   // a piece that saw no key
-                const float mn = fmaxf(mx, ml[b].x), f0 = exp2f(mx - mn), f1 = exp2f(ml[b].x - mn);
+                const float mn = fmaxf(mx, ml[b].x), f0 = ex2(mx - mn), f1 = ex2(ml[b].x - mn);
                 L = L * f0 + ml[b].y * f1;
-                acc.x = acc.x * f0 + x[b].x * f1;
-                acc.y = acc.y * f0 + x[b].y * f1;
-                acc.z = acc.z * f0 + x[b].z * f1;
-                acc.w = acc.w * f0 + x[b].w * f1;
+                acc.x = acc.x * f0 + v[b].x * f1;
+                acc.y = acc.y * f0 + v[b].y * f1;
+                acc.z = acc.z * f0 + v[b].z * f1;
+                acc.w = acc.w * f0 + v[b].w * f1;
                 mx = mn;
             }
         }
         const float inv = L == 0.f ? 0.f : 1.f / L;
-        const int qv = qv0 + r;
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + (sq.first + qv / p.gq) * p.a.out_stride + (head * p.gq + qv % p.gq) * HD + d;
+        const int qv = x.qv0 + r;
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + (x.first + qv / p.gq) * p.a.out_stride + (x.head * p.gq + qv % p.gq) * HD + d;
         const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
         *reinterpret_cast<uint2 *>(out) = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
     }
@@ -1353,8 +1392,9 @@ constexpr int kRowsPerSm = 4;   // most CTAs of k_kv8_rows per SM
 
 int64_t kv8_workspace_bytes(const la_kv8_cache &c, int nsm) {
     const int64_t part = static_cast<int64_t>(nsm) * std::max(kRowsPerSm * kRowsQ, kTileQ) * 2 * (c.head_dim + 2) * 4;
+    const int64_t splits = static_cast<int64_t>(nsm) * kRowsPerSm * sizeof(Kv8Split);
     const int64_t plans = (std::max<int64_t>(6ll * c.n_seqs + c.n_pages, 4ll * c.n_pages) + 16) * 4;
-    return (std::max(part, plans) + 255) / 256 * 256;
+    return (std::max(part + splits, plans) + 255) / 256 * 256;
 }
 
 // Kernel attributes are per device: bit d of `mask` says they are set on device d.
@@ -1374,15 +1414,16 @@ static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     static_assert(Lay::per_sm <= kRowsPerSm, "workspace");
     p.q_tile = kRowsQ;
     p.k_tile = PAGE;
-    p.n_tile = kRowsNew;
+    p.n_tile = 0;
     const long long units = ((static_cast<long long>(p.a.n_rows) * p.gq) / kRowsQ + p.c.n_seqs) * p.c.n_kv_heads;   // at most
-    const long long tiles = (p.a.max_len + PAGE - 1) / PAGE + (p.a.k ? (p.a.max_rows + kRowsNew - 1) / kRowsNew : 0);
+    const long long tiles = (p.a.max_len + PAGE - 1) / PAGE;
     // A unit of at most two tiles per warp is not worth splitting: its pieces
     // would cost a second kernel.
     p.whole = tiles <= 2 * kRowsWarps;
     p.workers = p.whole ? static_cast<int>(std::min<long long>(units, 1 << 20)) : nsm * Lay::per_sm;
     p.part = static_cast<float *>(ws);
     p.part_ml = p.part + static_cast<long long>(nsm) * kRowsPerSm * 2 * kRowsQ * HD;
+    p.split = reinterpret_cast<Kv8Split *>(p.part_ml + static_cast<long long>(nsm) * kRowsPerSm * 2 * kRowsQ * 2);
     static std::atomic<unsigned long long> configured{0};
     unsigned long long bit = 0;
     if (attrs_needed(configured, &bit)) {
@@ -1394,7 +1435,7 @@ static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     cudaError_t e = launch_k(k_kv8_rows<HD, PAGE>, dim3(p.workers), dim3(32 * kRowsWarps), Lay::bytes(p.c.n_seqs), s, p);
     if (e != cudaSuccess || p.whole) return e;
     if (p.workers < 2) return cudaSuccess;
-    return launch_k(k_kv8_join<HD>, dim3(p.workers - 1), dim3(kJoinThreads), (static_cast<size_t>(p.c.n_seqs) + 1) * 8, s, p);
+    return launch_k(k_kv8_join<HD>, dim3(p.workers - 1), dim3(kJoinThreads), 0, s, p);
 }
 
 template <int HD>
@@ -1408,6 +1449,7 @@ static cudaError_t tiles_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     p.workers = p.whole ? static_cast<int>(std::min<long long>(units, 1 << 20)) : nsm;
     p.part = static_cast<float *>(ws);
     p.part_ml = p.part + static_cast<long long>(nsm) * 2 * kTileQ * HD;
+    p.split = reinterpret_cast<Kv8Split *>(p.part_ml + static_cast<long long>(nsm) * 2 * kTileQ * 2);
     static std::atomic<unsigned long long> configured{0};
     unsigned long long bit = 0;
     if (attrs_needed(configured, &bit)) {
@@ -1418,7 +1460,7 @@ static cudaError_t tiles_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     }
     cudaError_t e = launch_k(k_kv8_tiles<HD>, dim3(p.workers), dim3(kTileThreads), Lay::bytes(p.c.n_seqs), s, p);
     if (e != cudaSuccess || p.whole || p.workers < 2) return e;
-    return launch_k(k_kv8_join<HD>, dim3(p.workers - 1), dim3(kJoinThreads), (static_cast<size_t>(p.c.n_seqs) + 1) * 8, s, p);
+    return launch_k(k_kv8_join<HD>, dim3(p.workers - 1), dim3(kJoinThreads), 0, s, p);
 }
 
 // Query vectors per sequence and KV head up to which k_kv8_rows is used.

@@ -363,7 +363,7 @@ int la_gemm_schedule(int32_t tiles, int32_t n_kb, int32_t ctas, int32_t whole_fi
  * other call on it; la_kv8_attention calls may overlap with one another when
  * each has a workspace of its own (that holds for captured graphs too).
  * The pages name 8-bit caches nowhere: a library extension with no passage. */
-#define LA_KV8_MAX_SEQS 4096
+#define LA_KV8_MAX_SEQS 2048
 
 /* Bits of la_kv8_cache.status. */
 #define LA_KV8_FULL     1u   /* append: no free page or table entry left; that sequence's rows were not stored */

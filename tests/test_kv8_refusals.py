@@ -51,7 +51,7 @@ def refused(call, code, word):
 @pytest.mark.parametrize("kw,code,word", [
     (dict(head_dim=96), UNSUPPORTED, "head_dim"), (dict(page=16), UNSUPPORTED, "page"), (dict(page=0), UNSUPPORTED, "page"),
     (dict(n_layers=0), INVALID, "n_layers"), (dict(n_pages=0), INVALID, "n_pages"), (dict(n_pages=2 ** 24 + 1), INVALID, "n_pages"),
-    (dict(n_seqs=0), INVALID, "n_seqs"), (dict(n_seqs=4097), INVALID, "n_seqs"), (dict(max_pages=2 ** 25), INVALID, "max_pages"),
+    (dict(n_seqs=0), INVALID, "n_seqs"), (dict(n_seqs=2049), INVALID, "n_seqs"), (dict(max_pages=2 ** 25), INVALID, "max_pages"),
     (dict(n_kv_heads=0), INVALID, "n_kv_heads"), (dict(k=None), INVALID, "null"), (dict(status=None), INVALID, "null"),
     (dict(v=264), INVALID, "aligned")])
 def test_cache_is_checked_by_every_call(L, kw, code, word):
@@ -87,7 +87,7 @@ def test_bookkeeping_refuses(L):
     c = cache(L)
     refused(lambda: L.la_kv8_fork(c, None, 256, 1), INVALID, "null")
     refused(lambda: L.la_kv8_fork(c, 256, 256, -1), INVALID, "n out of range")
-    refused(lambda: L.la_kv8_fork(c, 256, 256, 4097), INVALID, "n out of range")
+    refused(lambda: L.la_kv8_fork(c, 256, 256, 2049), INVALID, "n out of range")
     refused(lambda: L.la_kv8_free(c, None, None, 1), INVALID, "null")
     refused(lambda: L.la_kv8_free(c, 256, None, -1), INVALID, "n out of range")
     refused(lambda: L.la_kv8_compact(c, None, 256, None, 256, 1 << 30), INVALID, "null")
