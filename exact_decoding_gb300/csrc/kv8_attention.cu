@@ -684,7 +684,8 @@ struct Tiles {
     static constexpr uint32_t meta_off = q_off + k_bytes;          // [4] Kv8Meta of the last tiles
     static constexpr uint32_t red_off = meta_off + 4 * 64;         // [2][2][8] maxima of the new rows' tile
     static constexpr uint32_t ml_off = red_off + 128;              // [2 groups][128] running maximum and sum
-    static constexpr uint32_t odd_off = ml_off + 2 * kTileQ * 8;   // [2 groups]
+    static constexpr uint32_t qf_off = ml_off + 2 * kTileQ * 8;    // [128] factors on the rows' scores
+    static constexpr uint32_t odd_off = qf_off + kTileQ * 4;       // [2 groups]
     static constexpr uint32_t bar_off = odd_off + 16;
     static constexpr uint32_t tiles_off = bar_off + 24 * 8 + (kMmaWarp + 1) * 8;
     static size_t bytes(int n_seqs) { return tiles_off + (static_cast<size_t>(n_seqs) + 1) * 8 + 1024; }
@@ -723,6 +724,11 @@ __device__ __forceinline__ void e4m3x16_f16(const uint4 &w, uint4 &a, uint4 &b) 
     e4m3x4_f16(w.y, a.z, a.w);
     e4m3x4_f16(w.z, b.x, b.y);
     e4m3x4_f16(w.w, b.z, b.w);
+}
+__device__ __forceinline__ uint4 ld_shared(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
 }
 __device__ __forceinline__ void st_shared(uint32_t at, const uint4 &v) { st_shared_u32x4(at, v.x, v.y, v.z, v.w); }
 
@@ -937,42 +943,44 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                     const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + u.head * HD;
                     constexpr int C8 = HD / 8, NT = 32 * kOperandWarps;   // 16-byte pieces of a row
                     const int ot = w * 32 + lane;
-                    // Loads go out 8 at a time (one by one they took 12 us); K stays in
-                    // the registers that hold cached bytes otherwise.
-                    constexpr int NB = kTileK * C8 / NT / 2;   // half of a thread's pieces of K, or of V
-                    static_assert(NB == NR, "kraw and vraw hold a tile of new rows");
-                    uint32_t ak = 0, av = 0;   // magnitudes order like their bits
-                    bool odd = false;
-                    auto most = [&](const uint4 &x, uint32_t &top) {
-                        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t e = y[k] & 0x7fffu, f = y[k] >> 16 & 0x7fffu;
-                            if (e < 0x7f80u) top = max(top, e);
-                            else odd = true;
-                            if (f < 0x7f80u) top = max(top, f);
-                            else odd = true;
-                        }
-                    };
-                    auto fetch = [&](const __nv_bfloat16 *from, int64_t stride, int i) {
-                        const int r = i / C8, d = 8 * (i % C8);
-                        return r < nkeys ? *reinterpret_cast<const uint4 *>(from + r * stride + d) : make_uint4(0, 0, 0, 0);
-                    };
-#pragma unroll
-                    for (int i = 0; i < NB; ++i) kraw[i] = fetch(kn, p.a.k_stride, ot + i * NT);
-#pragma unroll
-                    for (int i = 0; i < NB; ++i) vraw[i] = fetch(kn, p.a.k_stride, ot + (NB + i) * NT);
-#pragma unroll
-                    for (int i = 0; i < NB; ++i) most(kraw[i], ak), most(vraw[i], ak);
-                    odd = false;   // only V's matter
+                    // K's rows come into its operand buffer as they are (asynchronous
+                    // copies, all in flight: one load after another took 12 us) and
+                    // are turned into fp16 in place; V's largest magnitude meanwhile.
+                    auto kat = [&](int i) { return sk + ((i % C8) >> 3) * Lay::k_block + (i / C8) * 128 + (((i % 8) ^ (i / C8 & 7)) << 4); };
+                    uint32_t ak = 0, av = 0;
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        uint4 x[NB];
-#pragma unroll
-                        for (int i = 0; i < NB; ++i) x[i] = fetch(vn, p.a.v_stride, ot + (h * NB + i) * NT);
-#pragma unroll
-                        for (int i = 0; i < NB; ++i) most(x[i], av);
+                    for (int i = ot; i < kTileK * C8; i += NT) {
+                        const int r = i / C8;
+                        const uint32_t n = r < nkeys ? 16 : 0;   // rows past the last: zeros
+                        const __nv_bfloat16 *from = kn + (n ? r : 0) * p.a.k_stride + 8 * (i % C8);
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(kat(i)), "l"(from), "r"(n) : "memory");
                     }
+                    asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll 4
+                    for (int i = ot; i < nkeys * C8; i += NT) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(vn + (i / C8) * p.a.v_stride + 8 * (i % C8));
+                        av = most2(most2(most2(most2(av, x.x), x.y), x.z), x.w);
+                    }
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll 2
+                    for (int i = ot; i < kTileK * C8; i += NT) {   // the pieces that this thread copied
+                        const uint4 x = ld_shared(kat(i));
+                        ak = most2(most2(most2(most2(ak, x.x), x.y), x.z), x.w);
+                    }
+                    // A NaN or infinity among them: the maxima again, without those.
+                    bool odd = max(av & 0xffffu, av >> 16) >= 0x7f80u;
+                    if (__any_sync(0xffffffffu, odd || max(ak & 0xffffu, ak >> 16) >= 0x7f80u)) {
+                        auto tame = [](uint32_t w) { return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0x7fffu) | ((w >> 16 & 0x7f80u) == 0x7f80u ? 0u : w & 0x7fff0000u); };
+                        ak = av = 0;
+#pragma unroll 1
+                        for (int i = ot; i < nkeys * C8; i += NT) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(vn + (i / C8) * p.a.v_stride + 8 * (i % C8)), y = ld_shared(kat(i));
+                            av = most2(most2(most2(most2(av, tame(x.x)), tame(x.y)), tame(x.z)), tame(x.w));
+                            ak = most2(most2(most2(most2(ak, tame(y.x)), tame(y.y)), tame(y.z)), tame(y.w));
+                        }
+                    }
+                    ak = max(ak & 0xffffu, ak >> 16);
+                    av = max(av & 0xffffu, av >> 16);
                     ak = __reduce_max_sync(0xffffffffu, ak);
                     av = __reduce_max_sync(0xffffffffu, av);
                     odd = __any_sync(0xffffffffu, odd);
@@ -1010,16 +1018,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                         if (lane == 0) mbar_arrive_one(m_full(it & 3));
                     }
                     const float fk = power_of(-kx);
-                    auto put = [&](const uint4 &a, int i) {
-                        const int r = i / C8, d8 = i % C8;
-                        const uint32_t x[4] = {a.x, a.y, a.z, a.w};
-                        uint32_t y[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) y[k] = pack_f16(bf16_bits(x[k] & 0xffffu) * fk, bf16_bits(x[k] >> 16) * fk);
-                        st_shared_u32x4(sk + (d8 >> 3) * Lay::k_block + r * 128 + (((d8 & 7) ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
-                    };
-#pragma unroll
-                    for (int i = 0; i < NB; ++i) put(kraw[i], ot + i * NT), put(vraw[i], ot + (NB + i) * NT);
+#pragma unroll 2
+                    for (int i = ot; i < kTileK * C8; i += NT) {
+                        const uint4 x = ld_shared(kat(i));
+                        st_shared_u32x4(kat(i), scaled_f16(x.x, fk), scaled_f16(x.y, fk), scaled_f16(x.z, fk), scaled_f16(x.w, fk));
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -1103,6 +1106,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + kColS + 128 * grp, to = tmem + lanes + kColO + 128 * grp;
         float2 *ml = reinterpret_cast<float2 *>(smem + Lay::ml_off);
+        float *qfs = reinterpret_cast<float *>(smem + Lay::qf_off);
         int *odds = reinterpret_cast<int *>(smem + Lay::odd_off);
         int units = 0;
         while (ok && kv8_next(p, tiles, walk, u)) {
@@ -1112,38 +1116,50 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             const int first = it, end = it + max(u.k1 - u.k0, 0);
             float qf = 0.f;
             if (first < end) {
-                if (!idle) {
-                    // q as fp16, scaled by a power of two to fit; the first group stores it
-                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.q) + (sq.first + myrow) * p.a.q_stride + myhead * HD);
+                // q as fp16, each vector scaled by a power of two to fit: 8 lanes a
+                // row, 32 rows at a time.  The rows come in by asynchronous copies,
+                // all in flight, and are turned in place.
+                constexpr int NW = HD / 64;   // 16-byte pieces of a lane's HD / 8 dims
+                tc_fence_before();            // the last unit's O is read
+                const int part = tid & 7, rows = (u.nqv + 31) / 32 * 32;
+                auto qat = [&](int r, int k) {
+                    const int ch = part * NW + k;   // 8 dims
+                    return sm + Lay::q_off + (ch >> 3) * Lay::k_block + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+                };
+#pragma unroll 1
+                for (int r = tid >> 3; r < rows; r += 32) {
+                    const int v = u.qv0 + r, n = r < u.nqv ? 16 : 0;
+                    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.a.q) + (sq.first + (n ? v / p.gq : 0)) * p.a.q_stride +
+                                               (u.head * p.gq + (n ? v % p.gq : 0)) * HD + part * (HD / 8);
+#pragma unroll
+                    for (int k = 0; k < NW; ++k)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(qat(r, k)), "l"(src + 8 * k), "r"(n) : "memory");
+                }
+                asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+#pragma unroll 1
+                for (int r = tid >> 3; r < rows; r += 32) {
+                    uint4 x[NW];
                     uint32_t top = 0;
 #pragma unroll
-                    for (int i = 0; i < HD / 8; ++i) {
-                        const uint4 x = in ? src[i] : make_uint4(0, 0, 0, 0);
-                        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t lo = y[k] & 0x7fffu, hi = y[k] >> 16 & 0x7fffu;   // magnitudes order like their bits
-                            if (lo < 0x7f80u) top = max(top, lo);
-                            if (hi < 0x7f80u) top = max(top, hi);
-                        }
+                    for (int k = 0; k < NW; ++k) {
+                        x[k] = ld_shared(qat(r, k));
+                        top = most2(most2(most2(most2(top, x[k].x), x[k].y), x[k].z), x[k].w);
                     }
-                    const int qx = fit_f16(bf16_bits(top));
-                    qf = power_of(qx) * p.scale_log2;
-                    if (grp == 0) {
-                        const float f = power_of(-qx);
 #pragma unroll
-                        for (int i = 0; i < HD / 8; ++i) {
-                            const uint4 x = in ? src[i] : make_uint4(0, 0, 0, 0);
-                            st_shared_u32x4(sm + Lay::q_off + (i >> 3) * Lay::k_block + row * 128 + (((i & 7) ^ (row & 7)) << 4),
-                                            pack_f16(bf16_bits(x.x & 0xffffu) * f, bf16_bits(x.x >> 16) * f), pack_f16(bf16_bits(x.y & 0xffffu) * f, bf16_bits(x.y >> 16) * f),
-                                            pack_f16(bf16_bits(x.z & 0xffffu) * f, bf16_bits(x.z >> 16) * f), pack_f16(bf16_bits(x.w & 0xffffu) * f, bf16_bits(x.w >> 16) * f));
-                        }
-                        fence_proxy_async_smem();
-                    }
+                    for (int k = 1; k < 8; k <<= 1) top = most2(top, __shfl_xor_sync(0xffffffffu, top, k));
+                    const int qx = fit_pair(top);
+                    const float f = power_of(-qx);
+#pragma unroll
+                    for (int k = 0; k < NW; ++k)
+                        st_shared_u32x4(qat(r, k), scaled_f16(x[k].x, f), scaled_f16(x[k].y, f), scaled_f16(x[k].z, f), scaled_f16(x[k].w, f));
+                    if (part == 0) qfs[r] = power_of(qx) * p.scale_log2;
                 }
-                tc_fence_before();   // the last unit's O is read
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_one(q_full);
+                ok = __all_sync(0xffffffffu, mbar_wait(q_full, units & 1, err, LA_KV8_TIMEOUT));
+                if (!ok) break;
+                qf = idle ? 0.f : qfs[row];
             }
             float m = -INFINITY, l = 0.f;
             bool odd = false;
@@ -1278,7 +1294,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             const int slot = 2 * blockIdx.x + (u.begins ? 1 : 0), d0 = grp * (HD / 2);
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + (sq.first + myrow) * p.a.out_stride + myhead * HD + d0;
             float *part = p.part + (static_cast<long long>(slot) * kTileQ + row) * HD + d0;
-#pragma unroll
+#pragma unroll 1
             for (int k = 0; k < HD / 32; ++k) {   // 16 dims at a time
                 uint32_t oa[16], ob[16];
                 float o[16];
@@ -1291,6 +1307,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[e] = (fa == -1.f ? 0.f : fa * __uint_as_float(oa[e])) + (fb == -1.f ? 0.f : fb * __uint_as_float(ob[e]));
                 if (odd && in) {   // NaN and infinities of the new rows that this row sees
+#pragma unroll 1
                     for (int r = u.k0 * kTileK; r < min(sq.rows, min(u.k1, sq.ntiles) * kTileK); ++r) {
                         const bool seen = p.a.vis ? r < 256 && (p.a.vis[(static_cast<long long>(sq.first) + myrow) * 8 + r / 32] >> (r % 32) & 1u) : r <= myrow;
                         if (!seen) continue;
@@ -1334,7 +1351,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
 // (the piece begins the unit), the others in their slot 0.  One CTA per border
 // between workers; the borders inside a unit share its query vectors and add
 // its pieces in order.
-constexpr int kJoinThreads = 256, kJoinBatch = 4;
+constexpr int kJoinThreads = 512, kJoinBatch = 8;
 
 template <int HD>
 __global__ void __launch_bounds__(kJoinThreads) k_kv8_join(const __grid_constant__ Kv8Args p) {

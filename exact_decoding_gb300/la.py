@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import List, Optional, Tuple
 
 import numpy as np
@@ -92,6 +93,11 @@ class la_kv8_rows(ctypes.Structure):
                 ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("k_layer_stride", ctypes.c_int64),
                 ("v_layer_stride", ctypes.c_int64), ("row_start", ctypes.c_void_p), ("row_idx", ctypes.c_void_p),
                 ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("stored", ctypes.c_void_p)]
+
+
+_KV8_ATTN = struct.Struct("@5i4q6Pf4x")    # la_kv8_attn
+_KV8_ROWS = struct.Struct("@3i4q5P")       # la_kv8_rows
+assert _KV8_ATTN.size == ctypes.sizeof(la_kv8_attn) and _KV8_ROWS.size == ctypes.sizeof(la_kv8_rows)
 
 
 def load_library():
@@ -415,6 +421,7 @@ class Kv8Cache:
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
         self.device = dev
+        self._index = dev.index if dev.type == "cuda" else -1
         pool = (n_layers, n_pages, n_kv_heads)
         shapes = {"k": (*pool, page, head_dim), "v": (*pool, head_dim, page), "k_scale": pool, "v_scale": pool,
                   "table": (n_seqs, max_pages), "lens": (n_seqs,), "refs": (n_pages,), "status": (1,)}
@@ -436,8 +443,18 @@ class Kv8Cache:
         self.struct = la_kv8_cache(n_layers, n_pages, page, n_kv_heads, head_dim, n_seqs, max_pages,
                                    *[getattr(self, "status_word" if n == "status" else n).data_ptr()
                                      for n in shapes])
-        with torch.cuda.device(dev):
-            self._ws = self.workspace()
+        self._ref = ctypes.addressof(self.struct)
+        lib, P, I = load_library(), ctypes.c_void_p, ctypes.c_int32
+        # The arguments as packed bytes: a ctypes structure costs more to fill than a call to launch.
+        self._fn = {}
+        for name, kinds in (("la_kv8_attention", (P, ctypes.c_int64)), ("la_kv8_append", (P, ctypes.c_int64)),
+                            ("la_kv8_fork", (P, I)), ("la_kv8_free", (P, I)),
+                            ("la_kv8_compact", (P, P, P, ctypes.c_int64)), ("la_kv8_status", ())):
+            f = lib[name]
+            f.argtypes, f.restype = [P, P, *kinds, P], ctypes.c_int
+            self._fn[name] = f
+        self._ws = self.workspace()
+        self._ws_ptr, self._ws_bytes = self._ws.data_ptr(), self._ws.numel()
         self._stored = torch.zeros(n_seqs, dtype=torch.int32, device=dev)
         self._live = torch.zeros(1, dtype=torch.int32, device=dev)
 
@@ -448,34 +465,51 @@ class Kv8Cache:
 
     # -------------------------------------------------------------- checks
     def _checked(self, t, name, dtype, shape):
-        if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != self.device:
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != self._index:
             raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {self.device}, not "
                              f"{t.dtype} {tuple(t.shape)} on {t.device}")
         return t.data_ptr()
 
     def _ints(self, t, name, n):
-        """int32 device vector of n values, or None."""
-        return None if t is None else self._checked(t, name, self._torch.int32, (n,))
+        """Address of an int32 device vector of n values; 0 for None."""
+        return 0 if t is None else self._checked(t, name, self._torch.int32, (n,))
 
-    def _heads(self, t, name, heads, lead):
-        """bf16 [*lead, rows, heads, dim] with dense (heads, dim); returns rows, row stride."""
-        if t.dtype != self._torch.bfloat16 or t.device != self.device or t.dim() != lead + 3 or t.shape[-1] != self.head_dim \
-                or (heads and t.shape[-2] != heads) or t.stride(-1) != 1 or (t.shape[-2] > 1 and t.stride(-2) != self.head_dim):
-            raise ValueError(f"{name} must be a bfloat16 tensor [{'layers, ' if lead else ''}rows, {heads or 'heads'}, "
-                             f"{self.head_dim}] on {self.device} with dense heads, not {t.dtype} {tuple(t.shape)} strides "
-                             f"{t.stride()} on {t.device}")
-        rows = t.shape[-3]
-        return rows, t.stride(-3) if rows > 1 else t.shape[-2] * self.head_dim
+    def _rows(self, t, name, heads):
+        """bf16 [rows, heads, dim] with dense (heads, dim): rows, row stride."""
+        sh, st = t.shape, t.stride()
+        if t.dtype is not self._torch.bfloat16 or t.get_device() != self._index or len(sh) != 3 or sh[2] != self.head_dim \
+                or (heads and sh[1] != heads) or st[2] != 1 or (st[1] != sh[2] and sh[1] > 1):
+            raise ValueError(f"{name} must be a bfloat16 tensor [rows, {heads or 'heads'}, {self.head_dim}] on {self.device} "
+                             f"with dense heads, not {t.dtype} {tuple(sh)} strides {st} on {t.device}")
+        return sh[0], st[0] if sh[0] > 1 else sh[1] * sh[2]
 
-    def _call(self, fn, *args, stream=None):
-        """fn(self.struct, *args, stream) with the cache's device current."""
-        cuda = self._torch.cuda
-        idx = self.device.index
-        if cuda.current_device() == idx:
-            fn(self.struct, *args, stream.cuda_stream if stream is not None else cuda.current_stream(idx).cuda_stream)
+    def _layers(self, t, name, rows):
+        """bf16 [layers, rows, kv heads, dim] with dense (heads, dim): row and layer strides."""
+        sh, st, h, d = t.shape, t.stride(), self.n_kv_heads, self.head_dim
+        if t.dtype is not self._torch.bfloat16 or t.get_device() != self._index or sh != (self.n_layers, rows, h, d) or st[3] != 1 \
+                or (st[2] != d and h > 1):
+            raise ValueError(f"{name} must be a bfloat16 tensor [{self.n_layers} layers, {rows or 'rows'}, {h}, {d}] on {self.device} "
+                             f"with dense heads, not {t.dtype} {tuple(sh)} strides {st} on {t.device}")
+        return st[1] if rows > 1 else h * d, st[0]
+
+    def _workspace(self, ws):
+        if ws is None:
+            return self._ws_ptr, self._ws_bytes
+        if ws.get_device() != self._index or not ws.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
+        return ws.data_ptr(), ws.numel() * ws.element_size()
+
+    def _call(self, fn, where, *args, stream=None):
+        """fn(cache, *args, stream) with the cache's device current."""
+        c = self._torch._C
+        st = c._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream
+        if c._cuda_getDevice() == self._index:
+            rc = fn(self._ref, *args, st)
         else:
-            with cuda.device(idx):
-                fn(self.struct, *args, stream.cuda_stream if stream is not None else cuda.current_stream(idx).cuda_stream)
+            with self._torch.cuda.device(self._index):
+                rc = fn(self._ref, *args, st)
+        if rc:
+            _check(rc, where)
 
     # -------------------------------------------------------------- calls
     def attention(self, q, k=None, v=None, row_start=None, layer: int = 0, vis=None, out=None, scale: float = 0.0,
@@ -484,28 +518,27 @@ class Kv8Cache:
         cached tokens and the visible new rows k, v [rows, kv heads, dim];
         see la_kv8_attention.  max_rows and max_len are bounds that the host
         knows (0: none); they steer the split of the work only.  Returns out."""
-        rows, qs = self._heads(q, "q", 0, 0)
+        rows, qs = self._rows(q, "q", 0)
+        heads = q.shape[1]
         if out is None:
-            out = self._torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        n, os_ = self._heads(out, "out", q.shape[1], 0)
-        ks = vs = 0
-        kp = vp = None
-        if k is not None or v is not None:
-            if k is None or v is None:
-                raise ValueError("k and v come together")
-            nk, ks = self._heads(k, "k", self.n_kv_heads, 0)
-            nv, vs = self._heads(v, "v", self.n_kv_heads, 0)
+            out = self._torch.empty((rows, heads, self.head_dim), dtype=q.dtype, device=self.device)
+        n, os_ = self._rows(out, "out", heads)
+        kp = vp = ks = vs = 0
+        if k is not None and v is not None:
+            nk, ks = self._rows(k, "k", self.n_kv_heads)
+            nv, vs = self._rows(v, "v", self.n_kv_heads)
             if nk != rows or nv != rows:
                 raise ValueError(f"k and v must have q's {rows} rows, not {nk} and {nv}")
             kp, vp = k.data_ptr(), v.data_ptr()
+        elif k is not None or v is not None:
+            raise ValueError("k and v come together")
         if n != rows:
             raise ValueError(f"out must have q's {rows} rows, not {n}")
-        a = la_kv8_attn(layer, q.shape[1], rows, max_rows, max_len, qs, ks, vs, os_,
-                        self._ints(row_start, "row_start", self.n_seqs + 1), q.data_ptr(), kp, vp,
-                        None if vis is None else self._checked(vis, "vis", self._torch.int32, (rows, 8)), out.data_ptr(),
-                        scale)
-        ws = self._ws if workspace is None else workspace
-        self._call(la_kv8_attention, a, ws.data_ptr(), ws.numel() * ws.element_size(), stream=stream)
+        ws, wb = self._workspace(workspace)
+        args = _KV8_ATTN.pack(layer, heads, rows, max_rows, max_len, qs, ks, vs, os_,
+                              self._ints(row_start, "row_start", self.n_seqs + 1), q.data_ptr(), kp, vp,
+                              0 if vis is None else self._checked(vis, "vis", self._torch.int32, (rows, 8)), out.data_ptr(), scale)
+        self._call(self._fn["la_kv8_attention"], "la_kv8_attention", args, ws, wb, stream=stream)
         return out
 
     def append(self, k, v, row_start=None, row_idx=None, stored=None, max_rows: int = 0, workspace=None, stream=None):
@@ -513,30 +546,26 @@ class Kv8Cache:
         row_idx of them) behind the sequences; see la_kv8_append.  Returns
         stored [seqs], the rows stored for each sequence (without `stored`, a
         tensor that the next append overwrites)."""
-        n, ks = self._heads(k, "k", self.n_kv_heads, 1)
-        nv, vs = self._heads(v, "v", self.n_kv_heads, 1)
-        if k.shape[0] != self.n_layers or v.shape[0] != self.n_layers or nv != n:
-            raise ValueError(f"k and v must be [{self.n_layers} layers, rows, ...], not {tuple(k.shape)} and {tuple(v.shape)}")
-        if row_idx is not None:
-            self._ints(row_idx, "row_idx", row_idx.numel())
+        n = k.shape[1] if k.dim() == 4 else 0
+        ks, vs = self._layers(k, "k", n), self._layers(v, "v", n)
         stored = self._stored if stored is None else stored
-        r = la_kv8_rows(n if row_idx is None else row_idx.numel(), n, max_rows, ks, vs, k.stride(0), v.stride(0),
-                        self._ints(row_start, "row_start", self.n_seqs + 1),
-                        None if row_idx is None else row_idx.data_ptr(), k.data_ptr(), v.data_ptr(),
-                        self._ints(stored, "stored", self.n_seqs))
-        ws = self._ws if workspace is None else workspace
-        self._call(la_kv8_append, r, ws.data_ptr(), ws.numel() * ws.element_size(), stream=stream)
+        ws, wb = self._workspace(workspace)
+        args = _KV8_ROWS.pack(n if row_idx is None else row_idx.numel(), n, max_rows, ks[0], vs[0], ks[1], vs[1],
+                              self._ints(row_start, "row_start", self.n_seqs + 1),
+                              0 if row_idx is None else self._ints(row_idx, "row_idx", row_idx.numel()), k.data_ptr(), v.data_ptr(),
+                              self._ints(stored, "stored", self.n_seqs))
+        self._call(self._fn["la_kv8_append"], "la_kv8_append", args, ws, wb, stream=stream)
         return stored
 
     def fork(self, src, dst, stream=None) -> None:
         """The empty slots dst continue the sequences src (int32 device vectors); see la_kv8_fork."""
-        self._call(la_kv8_fork, self._ints(src, "src", src.numel()), self._ints(dst, "dst", src.numel()), src.numel(),
-                   stream=stream)
+        n = src.numel()
+        self._call(self._fn["la_kv8_fork"], "la_kv8_fork", self._ints(src, "src", n), self._ints(dst, "dst", n), n, stream=stream)
 
     def free(self, slots, keep=None, stream=None) -> None:
         """Shorten the sequences in slots to keep tokens (None: 0); see la_kv8_free."""
-        self._call(la_kv8_free, self._ints(slots, "slots", slots.numel()), self._ints(keep, "keep", slots.numel()),
-                   slots.numel(), stream=stream)
+        n = slots.numel()
+        self._call(self._fn["la_kv8_free"], "la_kv8_free", self._ints(slots, "slots", n), self._ints(keep, "keep", n), n, stream=stream)
 
     def compact(self, table_out=None, refs_out=None, n_live=None, workspace=None, stream=None):
         """Move the used pages to the pool's front; see la_kv8_compact.  The new
@@ -545,15 +574,15 @@ class Kv8Cache:
         table_out = self.table if table_out is None else table_out
         refs_out = self.refs if refs_out is None else refs_out
         n_live = self._live if n_live is None else n_live
-        ws = self._ws if workspace is None else workspace
-        self._call(la_kv8_compact, self._checked(table_out, "table_out", self._torch.int32, self.table.shape),
-                   self._ints(refs_out, "refs_out", self.n_pages), self._ints(n_live, "n_live", 1), ws.data_ptr(),
-                   ws.numel() * ws.element_size(), stream=stream)
+        ws, wb = self._workspace(workspace)
+        self._call(self._fn["la_kv8_compact"], "la_kv8_compact",
+                   self._checked(table_out, "table_out", self._torch.int32, (self.n_seqs, self.max_pages)),
+                   self._ints(refs_out, "refs_out", self.n_pages), self._ints(n_live, "n_live", 1), ws, wb, stream=stream)
         return n_live
 
     def status(self, stream=None) -> None:
         """Wait for the stream and raise LaError for what earlier calls met; see la_kv8_status."""
-        self._call(la_kv8_status, stream=stream)
+        self._call(self._fn["la_kv8_status"], "la_kv8_status", None, stream=stream)
 
 
 class Decoder:
