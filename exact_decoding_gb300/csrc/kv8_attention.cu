@@ -655,23 +655,26 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
 // k_kv8_tiles: 128 query vectors per unit and 128 keys per tile on the
 // tcgen05 tensor cores.  With more than a few query vectors per KV head the
 // products and the softmax, not the bytes, bound the attention.
-//   warps 8..11  turn a tile's e4m3 bytes (or the new rows' bf16) into fp16
-//                operands in shared memory (128-byte swizzle): K [128 keys x
-//                HD], V^T [HD x 128 keys], two buffers each, K one tile ahead
-//                of V; the next tile's bytes are in registers meanwhile
-//   warp 12      issues S = Q K^T of tile i + 1, then O += P V (P from tensor
+//   warps 8..11  turn a tile's e4m3 bytes of K (or the new rows' bf16) into an
+//                fp16 operand in shared memory (128-byte swizzle), [128 keys x
+//                HD], two buffers; the next two tiles' bytes are in registers
+//   warps 12..14 the same for V^T [HD x 128 keys], one tile in registers
+//   warp 15      issues S = Q K^T of tile i + 1, then O += P V (P from tensor
 //                memory) of tile i
 //   warps 0..3   softmax of the even tiles, warps 4..7 of the odd ones, each
 //                thread a query vector; P replaces S in tensor memory.  Two
 //                groups, since one alone waits for tensor memory half of the
 //                time: 2.4 us per tile.
+// Bytes through a ring in shared memory instead of registers measured slower
+// (256 rows over 16k tokens, 8 KV heads: 176 us against 155): operands, bytes
+// and products share its bandwidth.
 // The groups have an O each in tensor memory, added at the end.  An O's scale
 // follows the running maximum only when that has grown by 2^8 since (fp16
 // weights up to 2^8 lose nothing), so it is rarely read back.  Units are split
 // and joined like those of k_kv8_rows.
 constexpr int kTileQ = 128, kTileK = 128;
-constexpr int kOperandWarps = 4, kMmaWarp = 8 + kOperandWarps;
-constexpr int kTileThreads = 32 * (kMmaWarp + 1);   // 13 warps: 4 to a quarter of an SM, 128 registers a thread
+constexpr int kKWarps = 4, kVWarps = 3, kVWarp0 = 8 + kKWarps, kMmaWarp = kVWarp0 + kVWarps;
+constexpr int kTileThreads = 32 * (kMmaWarp + 1);   // 16 warps: 4 to a quarter of an SM, 128 registers a thread
 constexpr float kLazy = 8.f;
 
 template <int HD>
@@ -714,6 +717,32 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2_f32(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ void mbar_arrive_one(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -743,9 +772,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     uint32_t *red = reinterpret_cast<uint32_t *>(smem + Lay::red_off);
     long long *tiles = reinterpret_cast<long long *>(smem + Lay::tiles_off);
     const uint32_t bars = sm + Lay::bar_off;
-    auto k_full = [&](int b) { return bars + 8 * b; };             // operand warps
+    auto k_full = [&](int b) { return bars + 8 * b; };             // K's warps
     auto k_empty = [&](int b) { return bars + 8 * (2 + b); };      // commit of S
-    auto v_full = [&](int b) { return bars + 8 * (4 + b); };
+    auto v_full = [&](int b) { return bars + 8 * (4 + b); };       // V's warps
     auto v_empty = [&](int b) { return bars + 8 * (6 + b); };      // commit of O
     auto s_full = [&](int b) { return bars + 8 * (8 + b); };
     auto p_full = [&](int b) { return bars + 8 * (10 + b); };      // 4 softmax warps
@@ -759,9 +788,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int b = 0; b < 2; ++b) {
-            mbar_init(k_full(b), kOperandWarps);
+            mbar_init(k_full(b), kKWarps);
             mbar_init(k_empty(b), 1);
-            mbar_init(v_full(b), kOperandWarps);
+            mbar_init(v_full(b), kVWarps);
             mbar_init(v_empty(b), 1);
             mbar_init(s_full(b), 1);
             mbar_init(p_full(b), 4);
@@ -770,7 +799,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         for (int t = 0; t < 4; ++t) mbar_init(m_full(t), 1);
         mbar_init(q_full, 8);
         mbar_init(e_full, 8);
-        mbar_init(r_full, kOperandWarps);
+        mbar_init(r_full, kKWarps);
         mbar_init(drain, 1);
         fence_barrier_init();
     }
@@ -787,161 +816,101 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     pdl_trigger();
     const uint32_t tmem = *tmem_slot;
     Kv8Walk walk = kv8_walk(p, tiles[c.n_seqs]);
-    Kv8Piece u;
+    Kv8Piece u{};
     int it = 0;          // key tiles so far, the same count in every role: buffer it & 1, its use it >> 1
     bool ok = true;
     unsigned *err = c.status;
 
-    if (warp >= 8 && warp < kMmaWarp) {
-        // ================================================ operands
-        const int w = warp - 8, r8 = lane & 7, cq = lane >> 3;
+    // Table entries of cached tile kt of piece u: lane l < 4 holds that of keys
+    // 32 l .. of the tile (-2: none).  They are checked a tile later, so that
+    // nothing waits for the load.
+    auto entry = [&](int kt) {
+        const int key = (kt - u.sq.ntiles) * kTileK + 32 * (lane & 3);
+        return kt < u.k1 && key < u.sq.len ? c.table[static_cast<long long>(u.s) * c.max_pages + (key >> p.page_log2)] : -2;
+    };
+    auto checked = [&](int e) {
+        if (static_cast<unsigned>(e) < static_cast<unsigned>(c.n_pages)) return e;
+        if (e != -2) atomicOr(err, LA_KV8_BAD);
+        return -1;
+    };
+    const int r8 = lane & 7, cq = lane >> 3;
+
+    if (warp >= 8 && warp < kVWarp0) {
+        // ================================================ K
+        const int w = warp - 8;
+        constexpr int NR = HD / (4 * kKWarps);   // 16-byte pieces per thread and tile
+        static_assert(NR * 32 * kKWarps * 16 == kTileK * HD, "every piece once");
         int new_tiles = 0;
-        constexpr int NR = HD / (4 * kOperandWarps);   // 16-byte pieces of K, and of V, per thread and tile
-        const uint8_t *kp = static_cast<const uint8_t *>(c.k), *vp = static_cast<const uint8_t *>(c.v);
         while (ok && kv8_next(p, tiles, walk, u)) {
             const Kv8Seq sq = u.sq;
-            // piece i of this thread: K row and 16-dim chunk, V dim and 16-key chunk
-            auto k_row = [&](int i) { return w * (kTileK / kOperandWarps) + r8 + 8 * (HD == 128 ? i >> 1 : i); };
+            auto k_row = [&](int i) { return r8 + 8 * (HD == 128 ? i >> 1 : i); };   // of this warp's 32 rows, which lie in one page
             auto k_chunk = [&](int i) { return HD == 128 ? cq + 4 * (i & 1) : cq; };
-            auto v_dim = [&](int i) { return w * (HD / kOperandWarps) + r8 + 8 * (i >> 1); };
-            auto v_chunk = [&](int i) { return cq + 4 * (i & 1); };
+            auto load = [&](uint4 (&raw)[NR], int kt, int pg) {
+                const int pid = max(__shfl_sync(0xffffffffu, pg, w), 0);
+                const int row0 = ((kt - sq.ntiles) * kTileK + 32 * w) & (c.page - 1);
+                const uint8_t *src = static_cast<const uint8_t *>(c.k) + (kv8_block(c, p.a.layer, pid, u.head) * c.page + row0) * HD;
+#pragma unroll
+                for (int i = 0; i < NR; ++i) raw[i] = __ldcg(reinterpret_cast<const uint4 *>(src + k_row(i) * HD + 16 * k_chunk(i)));
+            };
+            // K of tile kt (number it) to its buffer; its registers take tile kt + 2.
+            // pg0, pg2: the pages of both; pg1, after: those between, entries of kt + 3.
+            uint4 raw0[NR], raw1[NR];
             const int c_first = max(u.k0, sq.ntiles);   // first cached tile of this piece
-            // Table entries of cached tile kt: lane l < 4 holds that of keys 32 l ..
-            // of the tile (-2: none).  They are checked a tile later, so that
-            // nothing waits for the load.
-            auto entry = [&](int kt) {
-                const int key = (kt - sq.ntiles) * kTileK + 32 * (lane & 3);
-                return kt < u.k1 && key < sq.len ? c.table[static_cast<long long>(u.s) * c.max_pages + (key >> p.page_log2)] : -2;
-            };
-            auto checked = [&](int e) {
-                if (static_cast<unsigned>(e) < static_cast<unsigned>(c.n_pages)) return e;
-                if (e != -2) atomicOr(err, LA_KV8_BAD);
-                return -1;
-            };
-            uint4 kraw[NR], vraw[NR];
-            auto load_k = [&](int kt, int pg) {
-                const int pid = max(__shfl_sync(0xffffffffu, pg, w * (kTileK / kOperandWarps) / 32), 0);
-                const int row0 = ((kt - sq.ntiles) * kTileK + w * (kTileK / kOperandWarps)) & (c.page - 1);   // this warp's rows lie in one page
-                const uint8_t *src = kp + (kv8_block(c, p.a.layer, pid, u.head) * c.page + row0) * HD;
-#pragma unroll
-                for (int i = 0; i < NR; ++i)
-                    kraw[i] = __ldcg(reinterpret_cast<const uint4 *>(src + (k_row(i) - w * (kTileK / kOperandWarps)) * HD + 16 * k_chunk(i)));
-            };
-            // (A piece of a missing page may be anything: its bytes are cut below.)
-            auto load_v = [&](int kt, int pg) {
-                const int pid0 = max(__shfl_sync(0xffffffffu, pg, cq >> 1), 0), pid1 = max(__shfl_sync(0xffffffffu, pg, (cq >> 1) + 2), 0);
-                const int key = (kt - sq.ntiles) * kTileK + 16 * cq;
-                const uint8_t *src0 = vp + kv8_block(c, p.a.layer, pid0, u.head) * c.page * HD + (key & (c.page - 1));
-                const uint8_t *src1 = vp + kv8_block(c, p.a.layer, pid1, u.head) * c.page * HD + ((key + 64) & (c.page - 1));
-#pragma unroll
-                for (int i = 0; i < NR; ++i) vraw[i] = __ldcg(reinterpret_cast<const uint4 *>((i & 1 ? src1 : src0) + v_dim(i) * c.page));
-            };
-            // Pages of tiles kt - 1, kt, kt + 1 and the entries of kt + 2, kt being the tile whose K is put next.
-            int pg_v = -1, pg_k = checked(entry(c_first)), pg_next = checked(entry(c_first + 1)), after = entry(c_first + 2);
-            if (c_first < u.k1 && c_first == u.k0) {   // else behind the new rows' tiles
-                load_k(c_first, pg_k);
-                load_v(c_first, pg_k);
-            }
-            float fv = 0.f;   // new rows: factor on V of tile kt - 1
-            // V of tile kt (number i) to its buffer.
-            auto put_v = [&](int kt, int i) {
-                const int b = i & 1, use = i >> 1;
-                const uint32_t sv = sm + Lay::v_off + b * Lay::v_bytes;
-                if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(v_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
-                if (!ok) return;
-                if (kt >= sq.ntiles) {
-                    // Bytes behind the last token, and of missing pages, may be anything.
-                    const int key0 = (kt - sq.ntiles) * kTileK, held = __ballot_sync(0xffffffffu, pg_v >= 0 && lane < 4);
-                    if (sq.len - key0 < kTileK || held != 15) {
-#pragma unroll
-                        for (int i = 0; i < NR; ++i) {
-                            const int ch = v_chunk(i), live = held >> (ch >> 1) & 1 ? sq.len - key0 - 16 * ch : 0;
-                            auto cut = [](uint32_t a, int n) { return n >= 4 ? a : n <= 0 ? 0u : a & ((1u << (8 * n)) - 1u); };
-                            vraw[i] = make_uint4(cut(vraw[i].x, live), cut(vraw[i].y, live - 4), cut(vraw[i].z, live - 8), cut(vraw[i].w, live - 12));
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < NR; ++i) {
-                        uint4 x, y;
-                        e4m3x16_f16(vraw[i], x, y);
-                        const int ch = 2 * (v_chunk(i) & 3);
-                        const uint32_t at = sv + (v_chunk(i) >> 2) * Lay::v_block + v_dim(i) * 128;
-                        st_shared(at + ((ch ^ r8) << 4), x);
-                        st_shared(at + (((ch + 1) ^ r8) << 4), y);
-                    }
-                } else {
-                    // Two new rows of eight dims at a time, transposed.  A NaN or
-                    // infinity counts 0 here and is added at the end for the
-                    // rows that see it.
-                    const int key0 = kt * kTileK, nkeys = min(kTileK, sq.rows - key0);
-                    const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + u.head * HD;
-                    constexpr int NT = 32 * kOperandWarps, NB = kTileK / 2 * (HD / 8) / NT, B = 4;   // pairs of rows per thread, in flight
-#pragma unroll 1
-                    for (int i0 = 0; i0 < NB; i0 += B) {
-                        uint4 va[B], vb[B];
-#pragma unroll
-                        for (int q = 0; q < B; ++q) {
-                            const int j = w * 32 + lane + (i0 + q) * NT, r = 2 * (j % (kTileK / 2)), d = 8 * (j / (kTileK / 2));   // lanes: rows, other banks
-                            va[q] = r < nkeys ? *reinterpret_cast<const uint4 *>(vn + r * p.a.v_stride + d) : make_uint4(0, 0, 0, 0);
-                            vb[q] = r + 1 < nkeys ? *reinterpret_cast<const uint4 *>(vn + (r + 1) * p.a.v_stride + d) : make_uint4(0, 0, 0, 0);
-                        }
-#pragma unroll
-                        for (int q = 0; q < B; ++q) {
-                            const int j = w * 32 + lane + (i0 + q) * NT, r = 2 * (j % (kTileK / 2)), d = 8 * (j / (kTileK / 2));   // lanes: rows, other banks
-                            const uint32_t x[4] = {va[q].x, va[q].y, va[q].z, va[q].w}, y[4] = {vb[q].x, vb[q].y, vb[q].z, vb[q].w};
-                            const uint32_t at = sv + (r >> 6) * Lay::v_block + (r & 7) * 2;
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                float f0 = bf16_bits(k & 1 ? x[k >> 1] >> 16 : x[k >> 1] & 0xffffu), f1 = bf16_bits(k & 1 ? y[k >> 1] >> 16 : y[k >> 1] & 0xffffu);
-                                f0 = is_finite(f0) ? f0 * fv : 0.f;
-                                f1 = is_finite(f1) ? f1 * fv : 0.f;
-                                const int dim = d + k;
-                                asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + dim * 128 + ((((r >> 3) & 7) ^ (dim & 7)) << 4)), "r"(pack_f16(f0, f1)) : "memory");
-                            }
-                        }
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_one(v_full(b));
-            };
-            const int begin = it;
-            for (int kt = u.k0; ok && kt < u.k1; ++kt, ++it) {
+            int pg0 = checked(entry(c_first)), pg1 = checked(entry(c_first + 1)), pg2 = checked(entry(c_first + 2)), after = entry(c_first + 3);
+            auto put = [&](uint4 (&raw)[NR], int kt) {
                 const int b = it & 1, use = it >> 1;
                 const uint32_t sk = sm + Lay::k_off + b * Lay::k_bytes;
-                float fv_next = 0.f;
                 if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(k_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
-                if (!ok) break;
-                if (kt >= sq.ntiles) {
-                    if (w == 0 && lane < 4) {
+                if (!ok) return;
+                if (w == 0) {
+                    if (lane < 4) {
                         Kv8Meta &mt = meta[it & 3];
                         const int key = (kt - sq.ntiles) * kTileK + 32 * lane;
-                        const bool have = pg_k >= 0;
-                        const long long blk = kv8_block(c, p.a.layer, max(pg_k, 0), u.head);
+                        const bool have = pg0 >= 0;
+                        const long long blk = kv8_block(c, p.a.layer, max(pg0, 0), u.head);
                         mt.kf[lane] = have ? c.k_scale[blk] : 1.f;
                         mt.vx[lane] = have ? exponent_of(c.v_scale[blk]) : 0;
                         mt.live[lane] = have ? min(max(sq.len - key, 0), 32) : 0;
                         if (lane == 0) mt.odd = 0;
                     }
-                    if (w == 0) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_one(m_full(it & 3));
-                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_one(m_full(it & 3));
+                }
 #pragma unroll
-                    for (int i = 0; i < NR; ++i) {
-                        uint4 x, y;
-                        e4m3x16_f16(kraw[i], x, y);
-                        const int r = k_row(i), ch = 2 * (k_chunk(i) & 3);
-                        const uint32_t at = sk + (k_chunk(i) >> 2) * Lay::k_block + r * 128;
-                        st_shared(at + ((ch ^ r8) << 4), x);
-                        st_shared(at + (((ch + 1) ^ r8) << 4), y);
-                    }
-                } else {
+                for (int i = 0; i < NR; ++i) {
+                    uint4 x, y;
+                    e4m3x16_f16(raw[i], x, y);
+                    const int ch = 2 * (k_chunk(i) & 3);
+                    const uint32_t at = sk + (k_chunk(i) >> 2) * Lay::k_block + (32 * w + k_row(i)) * 128;
+                    st_shared(at + ((ch ^ r8) << 4), x);
+                    st_shared(at + (((ch + 1) ^ r8) << 4), y);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_one(k_full(b));
+                // (The entry is checked before the loads below are issued: a wait for
+                // it would wait for them too.)
+                const int pg3 = checked(after);
+                if (kt + 2 < u.k1) load(raw, kt + 2, pg2);
+                after = entry(kt + 4);
+                pg0 = pg1;
+                pg1 = pg2;
+                pg2 = pg3;
+                ++it;
+            };
+            if (c_first < u.k1) load(raw0, c_first, pg0);
+            if (c_first + 1 < u.k1) load(raw1, c_first + 1, pg1);
+            for (int kt = u.k0; ok && kt < min(u.k1, sq.ntiles); ++kt, ++it) {
+                const int b = it & 1, use = it >> 1;
+                const uint32_t sk = sm + Lay::k_off + b * Lay::k_bytes;
+                if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(k_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
+                if (!ok) break;
+                {
                     // New rows: bf16, scaled by a power of two for the whole tile.
                     const int key0 = kt * kTileK, nkeys = min(kTileK, sq.rows - key0);
                     const __nv_bfloat16 *kn = static_cast<const __nv_bfloat16 *>(p.a.k) + (sq.first + key0) * p.a.k_stride + u.head * HD;
                     const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + u.head * HD;
-                    constexpr int C8 = HD / 8, NT = 32 * kOperandWarps;   // 16-byte pieces of a row
+                    constexpr int C8 = HD / 8, NT = 32 * kKWarps;   // 16-byte pieces of a row
                     const int ot = w * 32 + lane;
                     // K's rows come into its operand buffer as they are (asynchronous
                     // copies, all in flight: one load after another took 12 us) and
@@ -999,13 +968,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                     ak = av = 0;
                     odd = false;
 #pragma unroll
-                    for (int k = 0; k < kOperandWarps; ++k) {
+                    for (int k = 0; k < kKWarps; ++k) {
                         ak = max(ak, mine[k]);
                         av = max(av, mine[8 + k] & 0xffffu);
                         odd |= mine[8 + k] >> 16 != 0;
                     }
                     const int kx = fit_f16(bf16_bits(ak)), vx = fit_f16(bf16_bits(av));
-                    fv_next = power_of(-vx);
                     if (w == 0) {
                         if (lane < 4) {
                             Kv8Meta &mt = meta[it & 3];
@@ -1027,24 +995,110 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_one(k_full(b));
-                // (The entry is checked before the loads below are issued: a wait for
-                // it would wait for them too.)
-                const int pg_after = checked(after);
-                if (kt >= sq.ntiles && kt + 1 < u.k1) load_k(kt + 1, pg_next);
-                if (it > begin) put_v(kt - 1, it - 1);
-                fv = fv_next;
+            }
+#pragma unroll 1
+            for (int kt = c_first; ok && kt < u.k1; kt += 2) {
+                put(raw0, kt);
+                if (ok && kt + 1 < u.k1) put(raw1, kt + 1);
+            }
+        }
+    } else if (warp >= kVWarp0 && warp < kMmaWarp) {
+        // ================================================ V
+        const int w = warp - kVWarp0;
+        // Groups of 32 pieces (8 dims x 4 pieces of 16 keys), dealt to the warps in turn.
+        constexpr int NG = HD / 4, NR = (NG + kVWarps - 1) / kVWarps;
+        while (ok && kv8_next(p, tiles, walk, u)) {
+            const Kv8Seq sq = u.sq;
+            auto v_dim = [&](int n) { return (w + n * kVWarps) / 2 * 8 + r8; };
+            auto v_chunk = [&](int n) { return cq + 4 * ((w + n * kVWarps) & 1); };
+            uint4 raw[NR];
+            auto load = [&](int kt, int pg) {
+                const int pid0 = max(__shfl_sync(0xffffffffu, pg, cq >> 1), 0), pid1 = max(__shfl_sync(0xffffffffu, pg, (cq >> 1) + 2), 0);
+                const int key = (kt - sq.ntiles) * kTileK + 16 * cq;
+                const uint8_t *vp = static_cast<const uint8_t *>(c.v);
+                const uint8_t *src0 = vp + kv8_block(c, p.a.layer, pid0, u.head) * c.page * HD + (key & (c.page - 1));
+                const uint8_t *src1 = vp + kv8_block(c, p.a.layer, pid1, u.head) * c.page * HD + ((key + 64) & (c.page - 1));
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+                    if (w + n * kVWarps < NG) raw[n] = __ldcg(reinterpret_cast<const uint4 *>(((w + n * kVWarps) & 1 ? src1 : src0) + v_dim(n) * c.page));
+            };
+            const int c_first = max(u.k0, sq.ntiles);
+            int pg0 = checked(entry(c_first)), pg1 = checked(entry(c_first + 1)), after = entry(c_first + 2);
+            if (c_first < u.k1) load(c_first, pg0);
+#pragma unroll 1
+            for (int kt = u.k0; ok && kt < u.k1; ++kt, ++it) {
+                const int b = it & 1, use = it >> 1;
+                const uint32_t sv = sm + Lay::v_off + b * Lay::v_bytes;
+                if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(v_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
+                if (!ok) break;
                 if (kt >= sq.ntiles) {
-                    if (kt > c_first) load_v(kt, pg_k);
-                    pg_v = pg_k;
-                    pg_k = pg_next;
-                    pg_next = pg_after;
+                    // Bytes behind the last token, and of missing pages, may be anything.
+                    const int key0 = (kt - sq.ntiles) * kTileK, held = __ballot_sync(0xffffffffu, pg0 >= 0 && lane < 4);
+                    if (sq.len - key0 < kTileK || held != 15) {
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) {
+                            const int ch = v_chunk(n), live = held >> (ch >> 1) & 1 ? sq.len - key0 - 16 * ch : 0;
+                            auto cut = [](uint32_t a, int m) { return m >= 4 ? a : m <= 0 ? 0u : a & ((1u << (8 * m)) - 1u); };
+                            raw[n] = make_uint4(cut(raw[n].x, live), cut(raw[n].y, live - 4), cut(raw[n].z, live - 8), cut(raw[n].w, live - 12));
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        if (w + n * kVWarps >= NG) break;
+                        uint4 x, y;
+                        e4m3x16_f16(raw[n], x, y);
+                        const int ch = 2 * (v_chunk(n) & 3);
+                        const uint32_t at = sv + (v_chunk(n) >> 2) * Lay::v_block + v_dim(n) * 128;
+                        st_shared(at + ((ch ^ r8) << 4), x);
+                        st_shared(at + (((ch + 1) ^ r8) << 4), y);
+                    }
+                } else {
+                    // Two new rows of eight dims at a time, transposed.  A NaN or
+                    // infinity counts 0 here and is added at the end for the
+                    // rows that see it.
+                    ok = __all_sync(0xffffffffu, mbar_wait(m_full(it & 3), it >> 2 & 1, err, LA_KV8_TIMEOUT));
+                    if (!ok) break;
+                    const float fv = power_of(-meta[it & 3].vx[0]);
+                    const int key0 = kt * kTileK, nkeys = min(kTileK, sq.rows - key0);
+                    const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + u.head * HD;
+                    constexpr int NT = 32 * kVWarps, NP = kTileK / 2 * (HD / 8), B = 4;   // pairs of rows, in flight
+#pragma unroll 1
+                    for (int j0 = w * 32 + lane; j0 < NP; j0 += B * NT) {
+                        uint4 va[B], vb[B];
+#pragma unroll
+                        for (int q = 0; q < B; ++q) {
+                            const int j = j0 + q * NT, r = 2 * (j % (kTileK / 2)), d = 8 * (j / (kTileK / 2));   // lanes: rows, other banks
+                            va[q] = j < NP && r < nkeys ? *reinterpret_cast<const uint4 *>(vn + r * p.a.v_stride + d) : make_uint4(0, 0, 0, 0);
+                            vb[q] = j < NP && r + 1 < nkeys ? *reinterpret_cast<const uint4 *>(vn + (r + 1) * p.a.v_stride + d) : make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int q = 0; q < B; ++q) {
+                            const int j = j0 + q * NT, r = 2 * (j % (kTileK / 2)), d = 8 * (j / (kTileK / 2));
+                            if (j >= NP) break;
+                            const uint32_t x[4] = {va[q].x, va[q].y, va[q].z, va[q].w}, y[4] = {vb[q].x, vb[q].y, vb[q].z, vb[q].w};
+                            const uint32_t at = sv + (r >> 6) * Lay::v_block + (r & 7) * 2;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                float f0 = bf16_bits(k & 1 ? x[k >> 1] >> 16 : x[k >> 1] & 0xffffu), f1 = bf16_bits(k & 1 ? y[k >> 1] >> 16 : y[k >> 1] & 0xffffu);
+                                f0 = is_finite(f0) ? f0 * fv : 0.f;
+                                f1 = is_finite(f1) ? f1 * fv : 0.f;
+                                const int dim = d + k;
+                                asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + dim * 128 + ((((r >> 3) & 7) ^ (dim & 7)) << 4)), "r"(pack_f16(f0, f1)) : "memory");
+                            }
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_one(v_full(b));
+                if (kt >= sq.ntiles) {
+                    const int pg2 = checked(after);
+                    if (kt + 1 < u.k1) load(kt + 1, pg1);
                     after = entry(kt + 3);
-                } else if (kt + 1 == c_first && c_first < u.k1) {
-                    load_k(c_first, pg_k);
-                    load_v(c_first, pg_k);
+                    pg0 = pg1;
+                    pg1 = pg2;
                 }
             }
-            if (ok && it > begin) put_v(u.k1 - 1, it - 1);
         }
     } else if (warp == kMmaWarp) {
         // ================================================ products
@@ -1198,13 +1252,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                             for (int e = 0; e < 32; ++e) v[e] = see >> e & 1u ? v[e] : 0xff800000u;   // -infinity
                         }
                         float x0 = -INFINITY, x1 = -INFINITY;
+                        const uint64_t f2 = pair(f, f), add2 = pair(add, add);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float x = fmaf(__uint_as_float(v[e]), f, add), y = fmaf(__uint_as_float(v[e + 1]), f, add);
-                            x0 = fmaxf(x0, x);
-                            x1 = fmaxf(x1, y);
-                            v[e] = __float_as_uint(x);
-                            v[e + 1] = __float_as_uint(y);
+                        for (int e = 0; e < 32; e += 4) {
+                            const float2 x = halves(fma2(pair(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), f2, add2));
+                            const float2 y = halves(fma2(pair(__uint_as_float(v[e + 2]), __uint_as_float(v[e + 3])), f2, add2));
+                            x0 = max3(x0, x.x, x.y);
+                            x1 = max3(x1, y.x, y.y);
+                            v[e] = __float_as_uint(x.x);
+                            v[e + 1] = __float_as_uint(x.y);
+                            v[e + 2] = __float_as_uint(y.x);
+                            v[e + 3] = __float_as_uint(y.y);
                         }
                         x0 = fmaxf(x0, x1);   // past the maximum by this much
                         const bool grow = m == -INFINITY ? x0 > -INFINITY : x0 > kLazy;
@@ -1242,15 +1300,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                             tmem_st_wait();
                         }
                         uint32_t w[16];
-                        float s0 = 0.f, s1 = 0.f;
+                        uint64_t s0 = 0, s1 = 0;   // pairs of sums
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const float x = ex2(__uint_as_float(v[2 * e])), y = ex2(__uint_as_float(v[2 * e + 1]));
-                            s0 += x;
-                            s1 += y;
+                            uint64_t &sum = e & 1 ? s1 : s0;
+                            sum = add2_f32(sum, pair(x, y));
                             w[e] = pack_f16(x, y);
                         }
-                        l += (s0 + s1) * power_of(-vx);
+                        const float2 sum = halves(add2_f32(s0, s1));
+                        l += (sum.x + sum.y) * power_of(-vx);
                         tmem_st_32x32b_x16(ts + 16 * k, w);
                     }
                     if (!ok) break;
