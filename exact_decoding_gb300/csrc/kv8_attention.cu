@@ -743,6 +743,31 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+// Bounded wait like mbar_wait, without the suspension of try_wait: that wakes
+// up late, and the products and the softmax wait on one another each tile.
+__device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity, unsigned *err, unsigned bit) {
+    uint64_t t0 = 0;
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i) {
+            uint32_t done;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(done)
+                : "r"(bar), "r"(parity)
+                : "memory");
+            if (done) return true;
+        }
+        const uint64_t now = globaltimer();
+        if (t0 == 0) t0 = now;
+        else if (now - t0 > kWaitNs) {
+            atomicOr(err, bit);
+            return false;
+        }
+    }
+}
 __device__ __forceinline__ void mbar_arrive_one(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -1112,7 +1137,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             int units = 0;
             auto product_o = [&](int j, bool begins) {
                 const int b = j & 1;
-                ok = mbar_wait(p_full(b), j >> 1 & 1, err, LA_KV8_TIMEOUT) && mbar_wait(v_full(b), j >> 1 & 1, err, LA_KV8_TIMEOUT);
+                ok = mbar_spin(p_full(b), j >> 1 & 1, err, LA_KV8_TIMEOUT) && mbar_spin(v_full(b), j >> 1 & 1, err, LA_KV8_TIMEOUT);
                 if (!ok) return;
                 tc_fence_after();
                 const uint32_t sv = sm + Lay::v_off + b * Lay::v_bytes, pt = tmem + kColS + 128 * b, ot = tmem + kColO + 128 * b;
@@ -1127,12 +1152,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             };
             while (ok && kv8_next(p, tiles, walk, u)) {
                 if (u.k0 >= u.k1) continue;
-                ok = mbar_wait(q_full, units & 1, err, LA_KV8_TIMEOUT);
+                ok = mbar_spin(q_full, units & 1, err, LA_KV8_TIMEOUT);
                 ++units;
                 const int first = it;
                 for (int kt = u.k0; ok && kt < u.k1; ++kt, ++it) {
                     const int b = it & 1;
-                    ok = mbar_wait(k_full(b), it >> 1 & 1, err, LA_KV8_TIMEOUT);
+                    ok = mbar_spin(k_full(b), it >> 1 & 1, err, LA_KV8_TIMEOUT);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t sk = sm + Lay::k_off + b * Lay::k_bytes;
@@ -1150,7 +1175,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             }
             if (!ok) {   // void: wait (bounded) for the products in flight
                 umma_commit(drain);
-                mbar_wait(drain, 0, err, LA_KV8_TIMEOUT);
+                mbar_spin(drain, 0, err, LA_KV8_TIMEOUT);
             }
         }
         __syncwarp();
@@ -1219,7 +1244,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             bool odd = false;
             for (int kt = u.k0 + ((first ^ grp) & 1); kt < u.k1; kt += 2) {
                 const int i = first + kt - u.k0, b = grp;   // tile number, of this group's parity
-                ok = mbar_wait(s_full(b), i >> 1 & 1, err, LA_KV8_TIMEOUT) && mbar_wait(m_full(i & 3), i >> 2 & 1, err, LA_KV8_TIMEOUT);
+                ok = mbar_spin(s_full(b), i >> 1 & 1, err, LA_KV8_TIMEOUT) && mbar_spin(m_full(i & 3), i >> 2 & 1, err, LA_KV8_TIMEOUT);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
