@@ -234,26 +234,27 @@ __device__ __forceinline__ int fit_f16(float amax) { return max(exponent_of(amax
 // Then the weights of product j's columns 2 t, 2 t + 1 are this lane's keys
 // KT/4 t + 2 j, + 1: already the A operand of the second product.
 // The new rows, at most a few here, are added key by key in fp32.
-constexpr int kRowsWarps = 4;
 constexpr int kRowsQ = 16;
 
 template <int HD, int PAGE>
 struct Rows {
     static constexpr int block = HD * PAGE;                                     // bytes of one page's K (or V) of a head
+    // 8 warps an SM at up to 255 registers.  (12 at 168, two blocks each,
+    // spill: 133 us against 118 for 64 sequences of up to 8192 tokens, 8 KV heads.)
+    static constexpr int warps = 4;
     static constexpr int slots = block >= 8192 ? 3 : 6;                         // of a warp's ring; K and V alternate
-    static constexpr int ring = block * slots * kRowsWarps;
-    static constexpr int join = kRowsWarps * kRowsQ * (HD + 4) * 4;             // over the ring, at the end of a unit
+    static constexpr int per_sm = block > 8192 ? 1 : block < 4096 ? 3 : 2;      // CTAs per SM that registers and the ring allow
+    static constexpr int ring = block * slots * warps;
+    static constexpr int join = warps * kRowsQ * (HD + 4) * 4;                  // over the ring, at the end of a unit
     // q in fp16: lane t's HD / 4 dims and 16 bytes more, so that the lanes
     // (g, t) of a quarter warp read different banks
     static constexpr int q_piece = HD / 2 + 16, q_row = 4 * q_piece;
     static constexpr int q_off = ring > join ? ring : join;
     static constexpr int qf_off = q_off + kRowsQ * q_row;                       // [16] factor on a row's scores
     static constexpr int ml_off = qf_off + kRowsQ * 4;
-    static constexpr int bar_off = ml_off + kRowsWarps * kRowsQ * 2 * 4;
-    static constexpr int meta_off = bar_off + kRowsWarps * slots * 8;           // [warp][slot] factor of K, exponent of V
-    static constexpr int sum_off = meta_off + kRowsWarps * slots * 8;
-    static constexpr int tiles_off = sum_off + kRowsWarps * 8;                  // (n_seqs + 1) prefix sums follow
-    static constexpr int per_sm = block > 8192 ? 1 : block < 4096 ? 3 : 2;      // CTAs per SM that registers and the ring allow
+    static constexpr int bar_off = ml_off + warps * kRowsQ * 2 * 4;
+    static constexpr int sum_off = bar_off + warps * slots * 8;
+    static constexpr int tiles_off = sum_off + warps * 8;                  // (n_seqs + 1) prefix sums follow
     static size_t bytes(int n_seqs) { return tiles_off + (static_cast<size_t>(n_seqs) + 1) * 8; }
 };
 
@@ -326,12 +327,12 @@ __device__ __forceinline__ void rows_softmax(float (&sc)[NJ][4], int live, float
 }
 
 template <int HD, int PAGE>
-__global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8_rows(const __grid_constant__ Kv8Args p) {
+__global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::per_sm) k_kv8_rows(const __grid_constant__ Kv8Args p) {
     using Lay = Rows<HD, PAGE>;
     constexpr int NI = HD / 8;                    // 8-dim groups of the output
     constexpr int KT = PAGE < 64 ? PAGE : 64;     // keys per piece
     constexpr int CH = KT / 4, NJ = KT / 8;       // of them, one lane's; products
-    constexpr int NS = Lay::slots;
+    constexpr int NS = Lay::slots, NW = Lay::warps;
     extern __shared__ __align__(128) uint8_t smem[];
     float2 *sh_ml = reinterpret_cast<float2 *>(smem + Lay::ml_off);  // [warp][16] m, l
     float *sh_o = reinterpret_cast<float *>(smem);                   // [warp][16][HD + 4], over the ring
@@ -342,7 +343,6 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * NS * Lay::block, bars = smem_u32(smem + Lay::bar_off) + warp * NS * 8;
     const uint8_t *my_ring = smem + warp * NS * Lay::block;
-    int2 *meta = reinterpret_cast<int2 *>(smem + Lay::meta_off) + warp * NS;
     if (lane < NS) mbar_init(bars + lane * 8, 1);
     fence_barrier_init();
     pdl_wait();
@@ -362,25 +362,26 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
         }
         if (!any) break;
         const Kv8Seq sq = u.sq;
-        // This warp's tiles: pages page0 + 4 i, i = 0 .. nc - 1.
+        // This warp's tiles: pages page0 + NW i, i = 0 .. nc - 1.
         const int page0 = u.k0 + warp, s = u.s, head = u.head;
-        const int nc = ok && page0 < u.k1 ? (u.k1 - page0 + kRowsWarps - 1) / kRowsWarps : 0;
+        const int nc = ok && page0 < u.k1 ? (u.k1 - page0 + NW - 1) / NW : 0;
         // Block 2 i is K of tile i, block 2 i + 1 its V.  Page numbers and
-        // scales are looked up 32 tiles at a time, lane i for tile 32 n + i.
-        int my_page = -1, my_vx = 0, issued = 0;
-        float my_kf = 0.f;
+        // scales are looked up 32 tiles at a time, lane i for tile 32 n + i
+        // (last_*: the 32 tiles before, some of which may still be read).
+        int my_page = -1, my_vx = 0, last_page = -1, last_vx = 0, issued = 0;
+        float my_kf = 0.f, last_kf = 0.f;
         auto issue = [&]() {
             const int i = issued >> 1;
             if ((issued & 63) == 0) {
-                my_page = i + lane < nc ? kv8_page(c, s, page0 + kRowsWarps * (i + lane)) : -1;
-                if (my_page >= 0) {
-                    const long long blk = kv8_block(c, p.a.layer, my_page, head);
-                    my_kf = c.k_scale[blk];
-                    my_vx = exponent_of(c.v_scale[blk]);
-                }
+                last_page = my_page;
+                last_vx = my_vx;
+                last_kf = my_kf;
+                my_page = i + lane < nc ? kv8_page(c, s, page0 + NW * (i + lane)) : -1;
+                const long long blk = kv8_block(c, p.a.layer, max(my_page, 0), head);
+                my_kf = c.k_scale[blk];
+                my_vx = exponent_of(c.v_scale[blk]);
             }
             const int pg = __shfl_sync(0xffffffffu, my_page, i & 31);
-            if (lane == (i & 31)) meta[in_slot] = make_int2(pg < 0 ? -1 : __float_as_int(my_kf), my_vx);
             if (lane == 0) {
                 const uint32_t bar = bars + in_slot * 8;
                 if (pg >= 0) {
@@ -399,25 +400,25 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
         while (issued < min(NS, 2 * nc)) issue();
 
         // q as fp16, each vector scaled by a power of two to fit: 8 threads a row.
-        {
-            constexpr int NW = HD / 64;   // 16-byte pieces of a thread's HD / 8 dims
+        if (tid < 8 * kRowsQ) {
+            constexpr int NP = HD / 64;   // 16-byte pieces of a thread's HD / 8 dims
             const int r = tid >> 3, part = tid & 7, qv = u.qv0 + r;
             const bool in = r < u.nqv;
             const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.q) + (sq.first + (in ? qv / p.gq : 0)) * p.a.q_stride +
                                                                (head * p.gq + (in ? qv % p.gq : 0)) * HD + part * (HD / 8));
-            uint4 w[NW];
+            uint4 w[NP];
             uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < NW; ++i) w[i] = in ? src[i] : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < NP; ++i) w[i] = in ? src[i] : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < NW; ++i) top = most2(most2(most2(most2(top, w[i].x), w[i].y), w[i].z), w[i].w);
+            for (int i = 0; i < NP; ++i) top = most2(most2(most2(most2(top, w[i].x), w[i].y), w[i].z), w[i].w);
 #pragma unroll
             for (int k = 1; k < 8; k <<= 1) top = most2(top, __shfl_xor_sync(0xffffffffu, top, k));
             const int qx = fit_pair(top);
             const float f = power_of(-qx);
             uint4 *dst = reinterpret_cast<uint4 *>(smem + Lay::q_off + r * Lay::q_row + (part >> 1) * Lay::q_piece + (part & 1) * (HD / 4));
 #pragma unroll
-            for (int i = 0; i < NW; ++i) dst[i] = make_uint4(scaled_f16(w[i].x, f), scaled_f16(w[i].y, f), scaled_f16(w[i].z, f), scaled_f16(w[i].w, f));
+            for (int i = 0; i < NP; ++i) dst[i] = make_uint4(scaled_f16(w[i].x, f), scaled_f16(w[i].y, f), scaled_f16(w[i].z, f), scaled_f16(w[i].w, f));
             if (part == 0) sh_qf[r] = power_of(qx) * p.scale_log2;
         }
         __syncthreads();
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
         if (u.begins && p.a.k) {
             const int r0 = g < u.nqv ? (u.qv0 + g) / p.gq : -1, r1 = g + 8 < u.nqv ? (u.qv0 + g + 8) / p.gq : -1;
 #pragma unroll 1
-            for (int j = warp; j < sq.rows; j += kRowsWarps) {
+            for (int j = warp; j < sq.rows; j += NW) {
                 const uint4 *kj = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.k) + (sq.first + j) * p.a.k_stride + head * HD + t * (HD / 4));
                 const uint32_t *vj = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + j) * p.a.v_stride + head * HD) + t;
                 uint4 kw[HD / 32];
@@ -505,10 +506,11 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
 #pragma unroll 1
         for (int i = 0; i < nc; ++i) {
             if (!landed()) break;
-            const int2 mt = meta[out_slot];
-            const float kf = mt.x == -1 ? 1.f : __int_as_float(mt.x);
-            const int vx = mt.y;
-            const int left = mt.x == -1 ? 0 : sq.len - (page0 + kRowsWarps * i) * PAGE;   // keys of this page that count
+            const bool old = i >> 5 != (issued - 1) >> 6;   // issue() is in the next 32 tiles already
+            const int pg = __shfl_sync(0xffffffffu, old ? last_page : my_page, i & 31);
+            const float kf_ = __shfl_sync(0xffffffffu, old ? last_kf : my_kf, i & 31), kf = pg < 0 ? 1.f : kf_;
+            const int vx = __shfl_sync(0xffffffffu, old ? last_vx : my_vx, i & 31);
+            const int left = pg < 0 ? 0 : sq.len - (page0 + NW * i) * PAGE;   // keys of this page that count
             const uint8_t *kblk = my_ring + out_slot * Lay::block, *vblk = nullptr;
 #pragma unroll 1
             for (int piece = 0; piece < PAGE / KT; ++piece) {
@@ -615,15 +617,15 @@ __global__ void __launch_bounds__(32 * kRowsWarps, Rows<HD, PAGE>::per_sm) k_kv8
         __syncthreads();
         const int slot = 2 * blockIdx.x + (u.begins ? 1 : 0);
 #pragma unroll 1
-        for (int i = tid; i < u.nqv * (HD / 4); i += 32 * kRowsWarps) {
+        for (int i = tid; i < u.nqv * (HD / 4); i += 32 * NW) {
             const int r = i / (HD / 4), d = 4 * (i % (HD / 4));
             float mx = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kRowsWarps; ++w) mx = fmaxf(mx, sh_ml[w * kRowsQ + r].x);
+            for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sh_ml[w * kRowsQ + r].x);
             float L = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-            for (int w = 0; w < kRowsWarps; ++w) {
+            for (int w = 0; w < NW; ++w) {
                 const float2 ml = sh_ml[w * kRowsQ + r];
                 if (ml.y == 0.f) continue;   // saw no key
                 const float f = ex2(ml.x - mx);
@@ -1520,7 +1522,7 @@ static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     const long long tiles = (p.a.max_len + PAGE - 1) / PAGE;
     // A unit of at most two tiles per warp is not worth splitting: its pieces
     // would cost a second kernel.
-    p.whole = tiles <= 2 * kRowsWarps;
+    p.whole = tiles <= 2 * Lay::warps;
     p.workers = p.whole ? static_cast<int>(std::min<long long>(units, 1 << 20)) : nsm * Lay::per_sm;
     p.part = static_cast<float *>(ws);
     p.part_ml = p.part + static_cast<long long>(nsm) * kRowsPerSm * 2 * kRowsQ * HD;
@@ -1533,7 +1535,7 @@ static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
-    cudaError_t e = launch_k(k_kv8_rows<HD, PAGE>, dim3(p.workers), dim3(32 * kRowsWarps), Lay::bytes(p.c.n_seqs), s, p);
+    cudaError_t e = launch_k(k_kv8_rows<HD, PAGE>, dim3(p.workers), dim3(32 * Lay::warps), Lay::bytes(p.c.n_seqs), s, p);
     if (e != cudaSuccess || p.whole) return e;
     if (p.workers < 2) return cudaSuccess;
     return launch_k(k_kv8_join<HD>, dim3(p.workers - 1), dim3(kJoinThreads), 0, s, p);
@@ -1565,7 +1567,7 @@ static cudaError_t tiles_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
 }
 
 // Query vectors per sequence and KV head up to which k_kv8_rows is used.
-constexpr int kFewVectors = 16;
+constexpr int kFewVectors = 64;
 
 template <int HD>
 static cudaError_t attention_launch_hd(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
