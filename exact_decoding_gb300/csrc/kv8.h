@@ -50,11 +50,30 @@ __host__ __device__ inline int kv8_touched(int m, int page) { return m == 1 ? 1 
 // Workspace of one cache: the attention's partial results, or the plans of
 // append and compact (calls that overlap need a workspace each).
 int64_t kv8_workspace_bytes(const la_kv8_cache &c, int nsm);
-cudaError_t kv8_attention_launch(const la_kv8_cache &c, const la_kv8_attn &a, void *ws, int nsm, cudaStream_t s);
+// *launched (or nullptr) grows by the kernels launched.
+cudaError_t kv8_attention_launch(const la_kv8_cache &c, const la_kv8_attn &a, void *ws, int nsm, cudaStream_t s,
+                                 int64_t *launched = nullptr);
 cudaError_t kv8_append_launch(const la_kv8_cache &c, const la_kv8_rows &r, int *ws, cudaStream_t s);
 cudaError_t kv8_fork_launch(const la_kv8_cache &c, const int *src, const int *dst, int n, cudaStream_t s);
 cudaError_t kv8_free_launch(const la_kv8_cache &c, const int *slots, const int *keep, int n, cudaStream_t s);
 cudaError_t kv8_compact_launch(const la_kv8_cache &c, int *table_out, int *refs_out, int *n_live, int *ws, int nsm,
                                cudaStream_t s);
+
+// Checks of a cache's sizes and pointers (an error code, with the message set).
+int kv8_check_cache(const la_kv8_cache *c, const char *where);
+
+// ------------------------------------------------------------------ decoders over the cache
+struct SpecState;
+// Step-state error bits: the cache had no room for a pass's rows; the slot
+// does not hold the decoder's tokens, or the cache's status word has
+// LA_KV8_BAD or LA_KV8_TIMEOUT.
+constexpr unsigned kErrKv8Full = 128u, kErrKv8Bad = 256u;
+cudaError_t kv8_qkv_launch(const float *part, const int *planes, long long sstride, int ldp, int nrows, int nh, int nkv, int hd, int k_off,
+                           int v_off, const float2 *rope, const int *P_dev, int P, const int *depth, __nv_bfloat16 *q, __nv_bfloat16 *k,
+                           __nv_bfloat16 *v, cudaStream_t s);
+cudaError_t kv8_rows_of_launch(int *row_start, int n_seqs, int slot, int n, const SpecState *st, int W, int N, int *row_idx, cudaStream_t s);
+// tokens: the slot's length afterwards, or -1: the step state's P.
+cudaError_t kv8_check_launch(const la_kv8_cache &c, const int *row_start, const int *stored, int slot, int tokens, SpecState *st,
+                             cudaStream_t s);
 
 }  // namespace la

@@ -18,7 +18,9 @@ int cuda_failed(const char *where, cudaError_t e) { return bad(where, cudaGetErr
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-int check_cache(const la_kv8_cache *c, const char *where) {
+}  // namespace
+
+int la::kv8_check_cache(const la_kv8_cache *c, const char *where) {
     if (!c) return bad(where, "null cache");
     if (c->head_dim != 64 && c->head_dim != 128) return bad(where, "head_dim must be 64 or 128", LA_ERR_UNSUPPORTED);
     if (c->page != 32 && c->page != 64 && c->page != 128) return bad(where, "page must be 32, 64 or 128", LA_ERR_UNSUPPORTED);
@@ -32,6 +34,8 @@ int check_cache(const la_kv8_cache *c, const char *where) {
     if (!aligned16(c->k) || !aligned16(c->v)) return bad(where, "k and v must be 16-byte aligned");
     return LA_OK;
 }
+
+namespace {
 
 int sm_count(int *n) {
     static int cached[64] = {};   // 0: not asked yet; any thread writes the same value
@@ -57,7 +61,7 @@ int check_workspace(const la_kv8_cache *c, const void *ws, int64_t bytes, int *n
 }
 
 int workspace_body(const la_kv8_cache *c, int64_t *bytes) {
-    int rc = check_cache(c, "la_kv8_workspace"), nsm = 0;
+    int rc = kv8_check_cache(c, "la_kv8_workspace"), nsm = 0;
     if (rc != LA_OK) return rc;
     if (!bytes) return bad("la_kv8_workspace", "null argument");
     if ((rc = sm_count(&nsm)) != LA_OK) return rc;
@@ -67,7 +71,7 @@ int workspace_body(const la_kv8_cache *c, int64_t *bytes) {
 
 int attention_body(const la_kv8_cache *c, const la_kv8_attn *args, void *ws, int64_t ws_bytes, void *stream) {
     const char *where = "la_kv8_attention";
-    int rc = check_cache(c, where);
+    int rc = kv8_check_cache(c, where);
     if (rc != LA_OK) return rc;
     if (!args) return bad(where, "null arguments");
     la_kv8_attn a = *args;
@@ -101,7 +105,7 @@ int attention_body(const la_kv8_cache *c, const la_kv8_attn *args, void *ws, int
 
 int append_body(const la_kv8_cache *c, const la_kv8_rows *rows, void *ws, int64_t ws_bytes, void *stream) {
     const char *where = "la_kv8_append";
-    int rc = check_cache(c, where);
+    int rc = kv8_check_cache(c, where);
     if (rc != LA_OK) return rc;
     if (!rows) return bad(where, "null arguments");
     la_kv8_rows r = *rows;
@@ -131,7 +135,7 @@ int append_body(const la_kv8_cache *c, const la_kv8_rows *rows, void *ws, int64_
 
 int fork_body(const la_kv8_cache *c, const int32_t *src, const int32_t *dst, int32_t n, void *stream) {
     const char *where = "la_kv8_fork";
-    const int rc = check_cache(c, where);
+    const int rc = kv8_check_cache(c, where);
     if (rc != LA_OK) return rc;
     if (n < 0 || n > LA_KV8_MAX_SEQS) return bad(where, "n out of range (0 .. LA_KV8_MAX_SEQS)");
     if (n > 0 && (!src || !dst)) return bad(where, "null src or dst");
@@ -141,7 +145,7 @@ int fork_body(const la_kv8_cache *c, const int32_t *src, const int32_t *dst, int
 
 int free_body(const la_kv8_cache *c, const int32_t *slots, const int32_t *keep, int32_t n, void *stream) {
     const char *where = "la_kv8_free";
-    const int rc = check_cache(c, where);
+    const int rc = kv8_check_cache(c, where);
     if (rc != LA_OK) return rc;
     if (n < 0 || n > (1 << 20)) return bad(where, "n out of range (0 .. 2^20)");
     if (n > 0 && !slots) return bad(where, "null slots");
@@ -152,7 +156,7 @@ int free_body(const la_kv8_cache *c, const int32_t *slots, const int32_t *keep, 
 int compact_body(const la_kv8_cache *c, int32_t *table_out, int32_t *refs_out, int32_t *n_live, void *ws, int64_t ws_bytes,
                  void *stream) {
     const char *where = "la_kv8_compact";
-    int rc = check_cache(c, where), nsm = 0;
+    int rc = kv8_check_cache(c, where), nsm = 0;
     if (rc != LA_OK) return rc;
     if (!table_out || !refs_out) return bad(where, "null table_out or refs_out");
     if ((rc = check_workspace(c, ws, ws_bytes, &nsm, where)) != LA_OK) return rc;
@@ -163,7 +167,7 @@ int compact_body(const la_kv8_cache *c, int32_t *table_out, int32_t *refs_out, i
 
 int status_body(const la_kv8_cache *c, uint32_t *out, void *stream) {
     const char *where = "la_kv8_status";
-    const int rc = check_cache(c, where);
+    const int rc = kv8_check_cache(c, where);
     if (rc != LA_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint32_t bits = 0;

@@ -1577,7 +1577,7 @@ static cudaError_t attention_launch_hd(Kv8Args &p, int nsm, void *ws, cudaStream
     return rows_launch<HD, 128>(p, nsm, ws, s);
 }
 
-cudaError_t kv8_attention_launch(const la_kv8_cache &c, const la_kv8_attn &a, void *ws, int nsm, cudaStream_t s) {
+cudaError_t kv8_attention_launch(const la_kv8_cache &c, const la_kv8_attn &a, void *ws, int nsm, cudaStream_t s, int64_t *launched) {
     if (a.n_rows < 1) return cudaSuccess;
     Kv8Args p{};
     p.c = c;
@@ -1585,7 +1585,9 @@ cudaError_t kv8_attention_launch(const la_kv8_cache &c, const la_kv8_attn &a, vo
     p.gq = a.n_heads / c.n_kv_heads;
     p.page_log2 = c.page == 32 ? 5 : c.page == 64 ? 6 : 7;
     p.scale_log2 = a.scale * kKv8Log2e;
-    return c.head_dim == 128 ? attention_launch_hd<128>(p, nsm, ws, s) : attention_launch_hd<64>(p, nsm, ws, s);
+    const cudaError_t e = c.head_dim == 128 ? attention_launch_hd<128>(p, nsm, ws, s) : attention_launch_hd<64>(p, nsm, ws, s);
+    if (launched) *launched += p.whole ? 1 : 2;
+    return e;
 }
 
 }  // namespace la

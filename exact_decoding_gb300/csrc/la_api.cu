@@ -20,6 +20,7 @@
 
 #include "../../include/la.h"
 #include "abi_guard.h"
+#include "kv8.h"
 #include "la_kernels.h"
 
 using namespace la;
@@ -91,6 +92,15 @@ struct la_handle {
     __nv_bfloat16 *qs = nullptr, *kcs = nullptr, *vcs = nullptr;
     int qv_pad = 0, seq = 0, nsm = 0;
     AttnUmmaParams attn_proto{};
+    // Decoders over the paged 8-bit cache (la_create_kv8): the cache, this
+    // decoder's slot, and a pass's rows: q8 [R][nh * hd], k8 and v8
+    // [L][R][nkv * hd] bf16, whose accepted rows are appended at the end.
+    bool kv8 = false;
+    la_kv8_cache kv8c{};
+    int kv8_slot = 0;
+    int *slot_dev = nullptr, *rs_step = nullptr, *rs_pass = nullptr, *row_idx = nullptr, *stored = nullptr;
+    __nv_bfloat16 *q8 = nullptr, *k8 = nullptr, *v8 = nullptr;
+    void *kv8_ws = nullptr;
     float2 *rope = nullptr;
     int *amax = nullptr, *tok = nullptr, *depth = nullptr, *anc = nullptr, *anc_cnt = nullptr, *used = nullptr;
     unsigned *thr_key = nullptr;   // [U] sampling keep rule of each used row (top-k / top-p)
@@ -431,8 +441,33 @@ int forward(la_handle *h, Mode mode, const int *tok, int nrows, int P, bool want
         const long long ss_qkv = static_cast<long long>(h->Rp[mode]) * h->ldo[QKV];
         // Algorithmic bytes of one attention launch: the prefix and step K/V
         // once at the weights' element size (the hi/lo planes double that).
-        const double attn_bytes = (2.0 * P * h->kvd + 2.0 * nrows * h->kvd) * h->act;
-        if (h->bf16) {
+        const double attn_bytes = 2.0 * P * h->kvd * (h->kv8 ? 1 : h->act) + 2.0 * nrows * h->kvd * h->act;
+        if (h->kv8) {
+            const long long kv_rows = static_cast<long long>(h->R) * h->kvd;
+            __nv_bfloat16 *k = h->k8 + l * kv_rows, *v = h->v8 + l * kv_rows;
+            pe = mode == STEP ? h->prof_begin() : -1;
+            CK(kv8_qkv_launch(h->part, h->planes[mode][QKV], ss_qkv, h->ldo[QKV], nrows, h->nh, h->nkv, h->hd, h->k_off, h->v_off, h->rope,
+                              mode == STEP ? &h->st->P : nullptr, P, mode == STEP ? h->depth : nullptr, h->q8, k, v, s));
+            h->prof_end(pe, 2, 0.0);
+            la_kv8_attn a{};
+            a.layer = l;
+            a.n_heads = h->nh;
+            a.n_rows = a.max_rows = nrows;
+            a.max_len = mode == STEP ? h->max_seq : std::max(P, 1);   // a step may replay from a captured graph
+            a.q_stride = a.out_stride = h->qd;
+            a.k_stride = a.v_stride = h->kvd;
+            a.row_start = mode == STEP ? h->rs_step : h->rs_pass;
+            a.q = h->q8;
+            a.k = k;
+            a.v = v;
+            a.vis = mode == STEP ? h->vis_bits : nullptr;
+            a.out = h->ao;   // the hi rows; the lo rows stay 0
+            a.scale = 1.f / std::sqrt(static_cast<float>(h->hd));
+            pe = mode == STEP ? h->prof_begin() : -1;
+            CK(kv8_attention_launch(h->kv8c, a, h->kv8_ws, h->nsm, s, &h->launches));
+            h->prof_end(pe, 1, attn_bytes);
+            h->launches += 1;   // kv8_qkv
+        } else if (h->bf16) {
             AttnUmmaParams ap = h->attn_proto;
             ap.part = h->part;
             ap.planes = h->planes[mode][QKV];
@@ -520,7 +555,37 @@ int forward_any(la_handle *h, Mode mode, const int *tok, int nrows, int P, bool 
                    : forward<float>(h, mode, tok, nrows, P, want_logits);
 }
 
+// Appends rows of the last pass (row_start, row_idx or nullptr: rows 0 ..; at
+// most `rows`) of every layer to the decoder's slot, which holds `tokens`
+// then (-1: the step state's P).
+int kv8_append_rows(la_handle *h, const int *row_start, const int *row_idx, int rows, int tokens) {
+    la_kv8_rows r{};
+    r.n_rows = r.max_rows = rows;
+    r.n_src = h->R;
+    r.k_stride = r.v_stride = h->kvd;
+    r.k_layer_stride = r.v_layer_stride = static_cast<int64_t>(h->R) * h->kvd;
+    r.row_start = row_start;
+    r.row_idx = row_idx;
+    r.k = h->k8;
+    r.v = h->v8;
+    r.stored = h->stored;
+    CK(kv8_append_launch(h->kv8c, r, static_cast<int *>(h->kv8_ws), h->stream));
+    CK(kv8_check_launch(h->kv8c, row_start, h->stored, h->kv8_slot, tokens, h->st, h->stream));
+    h->launches += 3;
+    return LA_OK;
+}
+
+// The slot's tokens and pages go (before a prefill).
+int kv8_reset(la_handle *h) {
+    if (h->kv8) CK(kv8_free_launch(h->kv8c, h->slot_dev, nullptr, 1, h->stream));
+    return LA_OK;
+}
+
 int kv_commit(la_handle *h) {
+    if (h->kv8) {
+        CK(kv8_rows_of_launch(h->rs_pass, h->kv8c.n_seqs, h->kv8_slot, 0, h->st, h->W, h->N, h->row_idx, h->stream));
+        return kv8_append_rows(h, h->rs_pass, h->row_idx, h->N, -1);
+    }
     if (h->bf16)
         CK(kv_commit_split_launch(h->spec(), h->kcs, h->vcs, h->L, h->nkv, h->hd, h->seq, h->stream));
     else
@@ -535,6 +600,10 @@ int check_device_error(la_handle *h) {
         // A gate/up launch whose waits gave up may have left arrival counts
         // (the next step's row build also clears them).
         if (h->fuse_cnt) cudaMemsetAsync(h->fuse_cnt, 0, sizeof(int) * h->fuse_tiles, h->stream);
+        if (!(e & ~(kErrKv8Full | kErrKv8Bad)))
+            return e & kErrKv8Full ? fail(LA_ERR_CAPACITY, "no free page or table entry in the cache for this decoder's tokens")
+                                   : fail(LA_ERR_STATE, "slot %d of the cache does not hold this decoder's tokens, or the cache's "
+                                                        "status word is set", h->kv8_slot);
         return fail(LA_ERR_DEVICE_TIMEOUT, "device error bits 0x%x (bounded wait gave up or pool full)", e);
     }
     return LA_OK;
@@ -545,9 +614,14 @@ int run_prefix(la_handle *h, int n, bool want_logits) {
     for (int c0 = 0; c0 < n; c0 += kPrefillRows) {
         const int rows = std::min(kPrefillRows, n - c0);
         const bool last = c0 + rows >= n;
+        if (h->kv8) CK(kv8_rows_of_launch(h->rs_pass, h->kv8c.n_seqs, h->kv8_slot, rows, nullptr, h->W, h->N, nullptr, h->stream));
         int rc = forward_any(h, PREFILL, h->tokens_log + c0, rows, c0, want_logits && last);
-        if (rc != LA_OK) return rc;
+        if (rc != LA_OK || (h->kv8 && (rc = kv8_append_rows(h, h->rs_pass, nullptr, rows, c0 + rows)) != LA_OK)) return rc;
     }
+    // A pass's hi rows lie over a step's lo rows, which nothing else writes.
+    if (h->kv8)
+        CK(cudaMemsetAsync(static_cast<__nv_bfloat16 *>(h->ao) + static_cast<size_t>(h->bh_step) * h->qd, 0,
+                           static_cast<size_t>(h->bh_step) * h->qd * 2, h->stream));
     if (want_logits) {
         int rc = run_lm_head(h, 1, false);
         if (rc != LA_OK) return rc;
@@ -787,7 +861,8 @@ const char *la_last_error(void) { return g_last_error.c_str(); }
 
 static int la_prefill_impl(la_handle *h, const int32_t *prompt, int32_t n, int32_t *first_token);
 
-static int la_create_body(const la_model_dims *dims, const la_weights *w, const la_opts *opts, la_handle **out) {
+static int la_create_body(const la_model_dims *dims, const la_weights *w, const la_opts *opts, const la_kv8_cache *kv8,
+                          int32_t slot, la_handle **out) {
     if (!dims || !w || !opts || !out) return fail(LA_ERR_INVALID_ARG, "null argument");
     *out = nullptr;
     const la_model_dims &D = *dims;
@@ -812,8 +887,19 @@ static int la_create_body(const la_model_dims *dims, const la_weights *w, const 
         !w->ffn_norm || !w->w_gate || !w->w_up || !w->w_down)
         return fail(LA_ERR_INVALID_ARG, "null weight pointer");
 
+    if (kv8) {
+        if (D.dtype != LA_BF16) return fail(LA_ERR_UNSUPPORTED, "a decoder over the 8-bit cache needs a bf16 model");
+        if (kv8->n_layers != D.n_layers || kv8->n_kv_heads != D.n_kv_heads || kv8->head_dim != D.head_dim)
+            return fail(LA_ERR_INVALID_ARG, "the cache's n_layers, n_kv_heads and head_dim must be the model's");
+        if (slot < 0 || slot >= kv8->n_seqs) return fail(LA_ERR_INVALID_ARG, "slot outside the cache");
+        if (O.max_seq > static_cast<int64_t>(kv8->max_pages) * kv8->page)
+            return fail(LA_ERR_INVALID_ARG, "max_seq is more than the cache's max_pages * page");
+    }
     std::unique_ptr<la_handle> owner(new la_handle());   // freed on every early return
     la_handle *h = owner.get();
+    h->kv8 = kv8 != nullptr;
+    if (kv8) h->kv8c = *kv8;
+    h->kv8_slot = slot;
     h->dims = D;
     h->opts = O;
     h->stream = static_cast<cudaStream_t>(O.cuda_stream);
@@ -907,14 +993,26 @@ static int la_create_body(const la_model_dims *dims, const la_weights *w, const 
     A(h->alloc(&h->thr_key, std::max(h->U, 1)));
     A(h->alloc(&h->thr_cut, std::max(h->U, 1)));
     const size_t cache_bytes = static_cast<size_t>(h->L) * 2 * h->nkv * h->seq * h->hd * sizeof(float);
-    if (h->bf16) {
+    if (h->kv8) {
+        int64_t ws = 0;
+        A(la_kv8_workspace(&h->kv8c, &ws));
+        A(h->alloc_bytes(&h->kv8_ws, static_cast<size_t>(ws)));
+        A(h->alloc(&h->q8, static_cast<size_t>(R) * h->qd));
+        A(h->alloc(&h->k8, static_cast<size_t>(h->L) * R * h->kvd));
+        A(h->alloc(&h->v8, static_cast<size_t>(h->L) * R * h->kvd));
+        A(h->alloc(&h->slot_dev, 1));
+        A(h->alloc(&h->rs_step, h->kv8c.n_seqs + 1));
+        A(h->alloc(&h->rs_pass, h->kv8c.n_seqs + 1));
+        A(h->alloc(&h->row_idx, h->N));
+        A(h->alloc(&h->stored, h->kv8c.n_seqs));
+    } else if (h->bf16) {
         A(h->alloc(&h->attn_ws, 1));
         A(h->alloc(&h->qs, static_cast<size_t>(2) * h->nkv * h->qv_pad * h->hd));
     } else {
         const int nch_max = (h->max_seq + kAttnChunk - 1) / kAttnChunk;
         A(h->alloc(&h->attn_ws, static_cast<size_t>(nch_max) * R * h->nh * (h->hd + 4)));
     }
-    A(h->alloc_bytes(&h->cache, cache_bytes));
+    if (!h->kv8) A(h->alloc_bytes(&h->cache, cache_bytes));
     A(h->alloc(&h->rope, static_cast<size_t>(h->max_seq) * (h->hd / 2)));
     A(h->alloc(&h->tok, M));
     A(h->alloc(&h->depth, M));
@@ -983,7 +1081,15 @@ static int la_create_body(const la_model_dims *dims, const la_weights *w, const 
         cudaMemsetAsync(h->st, 0, sizeof(SpecState), s) != cudaSuccess) {
         return fail(LA_ERR_CUDA, "memset failed");
     }
-    if (h->bf16) {
+    if (h->kv8) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&h->nsm, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaMemcpy(h->slot_dev, &h->kv8_slot, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess ||
+            kv8_rows_of_launch(h->rs_step, h->kv8c.n_seqs, h->kv8_slot, M, nullptr, h->W, h->N, nullptr, s) != cudaSuccess) {
+            return fail(LA_ERR_CUDA, "setting up the rows of the 8-bit cache failed");
+        }
+    } else if (h->bf16) {
         // The tensor-core attention reads whole 128-key chunks and 128-row
         // query tiles: slots and rows past the live ones must hold finite
         // values (they are masked, and 0 * finite = 0 in P V).
@@ -1065,7 +1171,7 @@ static int la_prefill_impl(la_handle *h, const int32_t *prompt, int32_t n, int32
     h->prefilled = false;
     CK(cudaMemsetAsync(h->st, 0, sizeof(SpecState), s));
     int rc = reset_pool(h);
-    if (rc != LA_OK) return rc;
+    if (rc != LA_OK || (rc = kv8_reset(h)) != LA_OK) return rc;
     CK(cudaMemcpyAsync(h->tokens_log, prompt, static_cast<size_t>(n) * sizeof(int32_t), cudaMemcpyHostToDevice, s));
     if ((rc = run_prefix(h, n, true)) != LA_OK) return rc;
     CK(first_token_launch(h->spec(), n, s));
@@ -1230,8 +1336,9 @@ static int la_ar_step_body(la_handle *h, int32_t *token) {
     if (h->P + 2 > h->max_seq) return fail(LA_ERR_CAPACITY, "max_seq reached");
     cudaStream_t s = h->stream;
     const int P = h->P;   // tokens_log[P] is the last committed token, at position P
+    if (h->kv8) CK(kv8_rows_of_launch(h->rs_pass, h->kv8c.n_seqs, h->kv8_slot, 1, nullptr, h->W, h->N, nullptr, s));
     int rc = forward_any(h, PREFILL, h->tokens_log + P, 1, P, true);
-    if (rc != LA_OK) return rc;
+    if (rc != LA_OK || (h->kv8 && (rc = kv8_append_rows(h, h->rs_pass, nullptr, 1, P + 1)) != LA_OK)) return rc;
     if ((rc = run_lm_head(h, 1, false)) != LA_OK) return rc;
     CK(argmax_launch(h->lm_part, h->planes_lm, h->lm_stride, h->ldo_lm, h->logits, 1, h->V,
                      h->opts.temperature > 0.f ? 1.f / h->opts.temperature : 0.f, h->amax, h->lmax, h->lsum,
@@ -1352,9 +1459,14 @@ static int la_import_state_body(la_handle *h, const la_state_t *stt) {
     h->prefilled = false;
     CK(cudaMemsetAsync(h->st, 0, sizeof(SpecState), s));
     int rc = reset_pool(h);
-    if (rc != LA_OK) return rc;
+    if (rc != LA_OK || (rc = kv8_reset(h)) != LA_OK) return rc;
     CK(cudaMemcpyAsync(h->tokens_log, stt->tokens, static_cast<size_t>(n) * sizeof(int), cudaMemcpyHostToDevice, s));
     if ((rc = run_prefix(h, n - 1, false)) != LA_OK) return rc;
+    if (h->kv8) {   // the appends' errors, before the state is written over
+        CK(cudaMemcpyAsync(h->st_host, h->st, sizeof(SpecState), cudaMemcpyDeviceToHost, s));
+        CK(cudaStreamSynchronize(s));
+        if ((rc = check_device_error(h)) != LA_OK) return rc;
+    }
     SpecState init{};
     init.P = n - 1;
     init.o = stt->tokens[n - 1];
@@ -1394,6 +1506,51 @@ static int la_import_state_body(la_handle *h, const la_state_t *stt) {
     h->P = n - 1;
     h->prefilled = true;
     h->logits_rows = 0;
+    return LA_OK;
+}
+
+static int la_fork_body(la_handle *a, la_handle *b) {
+    if (!a || !b || a == b) return fail(LA_ERR_INVALID_ARG, "la_fork needs two decoders");
+    if (!a->kv8 || !b->kv8 || a->kv8c.table != b->kv8c.table || a->kv8c.k != b->kv8c.k || a->kv8_slot == b->kv8_slot)
+        return fail(LA_ERR_INVALID_ARG, "la_fork needs two slots of one 8-bit cache");
+    if (a->N != b->N || a->W != b->W || a->cap != b->cap || a->V != b->V || a->opts.pool_policy != b->opts.pool_policy ||
+        a->d != b->d || a->nh != b->nh || a->F != b->F)
+        return fail(LA_ERR_INVALID_ARG, "la_fork needs the same model, N, W, pool capacity and policy");
+    if (!a->prefilled) return fail(LA_ERR_STATE, "la_fork before la_prefill");
+    if (a->P + b->M + b->N + 2 > b->max_seq) return fail(LA_ERR_CAPACITY, "state too long for max_seq");
+    cudaStream_t s = b->stream;
+    CK(cudaStreamSynchronize(a->stream));
+    b->prefilled = false;
+    int rc = kv8_reset(b);
+    if (rc != LA_OK) return rc;
+    CK(kv8_fork_launch(b->kv8c, a->slot_dev, b->slot_dev, 1, s));
+    const size_t nslots = static_cast<size_t>(1) << a->nslots_log2;
+    const struct {
+        int *to;
+        const int *from;
+        size_t n;
+    } parts[] = {{b->tokens_log, a->tokens_log, static_cast<size_t>(a->P) + 1},
+                 {b->window, a->window, static_cast<size_t>(a->N - 1) * a->W},
+                 {b->pkeys, a->pkeys, nslots},
+                 {b->pcnt, a->pcnt, nslots},
+                 {b->phead, a->phead, nslots},
+                 {b->pent, a->pent, nslots * a->cap * (a->N - 1)},
+                 {b->puse, a->puse, nslots * a->cap}};
+    for (const auto &p : parts) CK(cudaMemcpyAsync(p.to, p.from, p.n * sizeof(int), cudaMemcpyDeviceToDevice, s));
+    CK(cudaMemcpyAsync(b->st, a->st, sizeof(SpecState), cudaMemcpyDeviceToDevice, s));
+    int32_t lens[2] = {-1, -1};
+    CK(cudaMemcpyAsync(&lens[0], a->kv8c.lens + a->kv8_slot, sizeof(int32_t), cudaMemcpyDeviceToHost, s));
+    CK(cudaMemcpyAsync(&lens[1], b->kv8c.lens + b->kv8_slot, sizeof(int32_t), cudaMemcpyDeviceToHost, s));
+    CK(cudaStreamSynchronize(s));
+    if (lens[0] != a->P || lens[1] != a->P)
+        return fail(LA_ERR_STATE, "the slots hold %d and %d tokens, not the decoder's %d", lens[0], lens[1], a->P);
+    b->P = a->P;
+    b->prefilled = true;
+    b->steps = 0;
+    b->generated = 0;
+    b->last_A = b->last_g = 0;
+    b->logits_rows = 0;
+    b->launches = 0;
     return LA_OK;
 }
 
@@ -1515,7 +1672,19 @@ static int la_gemm_schedule_body(int32_t tiles, int32_t n_kb, int32_t ctas, int3
 // Exported entry points: each runs its body under abi_guard, so no C++
 // exception crosses the C ABI.
 int la_create(const la_model_dims *dims, const la_weights *w, const la_opts *opts, la_handle **out) {
-    return abi_guard("la_create", [&] { return la_create_body(dims, w, opts, out); });
+    return abi_guard("la_create", [&] { return la_create_body(dims, w, opts, nullptr, 0, out); });
+}
+
+int la_create_kv8(const la_model_dims *dims, const la_weights *w, const la_opts *opts, const la_kv8_cache *cache, int32_t slot,
+                  la_handle **out) {
+    return abi_guard("la_create_kv8", [&] {
+        const int rc = kv8_check_cache(cache, "la_create_kv8");
+        return rc == LA_OK ? la_create_body(dims, w, opts, cache, slot, out) : rc;
+    });
+}
+
+int la_fork(la_handle *src, la_handle *dst) {
+    return abi_guard("la_fork", [&] { return la_fork_body(src, dst); });
 }
 
 int la_prefill(la_handle *h, const int32_t *prompt, int32_t n, int32_t *first_token) {

@@ -111,6 +111,9 @@ def load_library():
     H = ctypes.c_void_p
     lib.la_create.argtypes = [ctypes.POINTER(la_model_dims), ctypes.POINTER(la_weights), ctypes.POINTER(la_opts),
                               ctypes.POINTER(H)]
+    lib.la_create_kv8.argtypes = [ctypes.POINTER(la_model_dims), ctypes.POINTER(la_weights), ctypes.POINTER(la_opts),
+                                  ctypes.POINTER(la_kv8_cache), ctypes.c_int32, ctypes.POINTER(H)]
+    lib.la_fork.argtypes = [H, H]
     lib.la_prefill.argtypes = [H, _I32P, ctypes.c_int32, _I32P]
     lib.la_step.argtypes = [H, _I32P, _I32P]
     lib.la_ar_step.argtypes = [H, _I32P]
@@ -147,7 +150,8 @@ def load_library():
     for name in ("la_create", "la_prefill", "la_step", "la_ar_step", "la_generate", "la_stats", "la_export_state",
                  "la_import_state", "la_debug_logits", "la_gemm_bf16", "la_gemm_bf16_noalloc", "la_gemm_status",
                  "la_selftest_timeout", "la_gemm_schedule", "la_step_tables", "la_kv8_workspace", "la_kv8_attention",
-                 "la_kv8_append", "la_kv8_fork", "la_kv8_free", "la_kv8_compact", "la_kv8_status"):
+                 "la_kv8_append", "la_kv8_fork", "la_kv8_free", "la_kv8_compact", "la_kv8_status", "la_create_kv8",
+                 "la_fork"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -173,6 +177,17 @@ def la_create(dims: la_model_dims, weights: la_weights, opts: la_opts) -> ctypes
     _check(load_library().la_create(ctypes.byref(dims), ctypes.byref(weights), ctypes.byref(opts),
                                     ctypes.byref(h)), "la_create")
     return h
+
+
+def la_create_kv8(dims: la_model_dims, weights: la_weights, opts: la_opts, cache: la_kv8_cache, slot: int) -> ctypes.c_void_p:
+    h = ctypes.c_void_p()
+    _check(load_library().la_create_kv8(ctypes.byref(dims), ctypes.byref(weights), ctypes.byref(opts), ctypes.byref(cache),
+                                        slot, ctypes.byref(h)), "la_create_kv8")
+    return h
+
+
+def la_fork(src, dst) -> None:
+    _check(load_library().la_fork(src, dst), "la_fork")
 
 
 def la_prefill(h, prompt) -> int:
@@ -586,11 +601,13 @@ class Kv8Cache:
 
 
 class Decoder:
-    """A la_handle over DeviceWeights (or a host weight dict, uploaded here)."""
+    """A la_handle over DeviceWeights (or a host weight dict, uploaded here).
+    With `kv_cache` (a Kv8Cache) its KV cache is slot `slot` of that cache."""
 
     def __init__(self, weights, N: int, W: int, G: int, max_seq: int, temperature: float = 0.0,
                  seed: int = 0, prompt_as_reference: bool = False, pool_cap: int = 0, stream=None, device="cuda",
-                 profile: bool = False, top_k: int = 0, top_p: float = 1.0, pool_policy: str = "fifo"):
+                 profile: bool = False, top_k: int = 0, top_p: float = 1.0, pool_policy: str = "fifo",
+                 kv_cache: Optional["Kv8Cache"] = None, slot: int = 0):
         self.weights = weights if isinstance(weights, DeviceWeights) else DeviceWeights(weights, device)
         self.dims, self.N, self.W, self.G = self.weights.dims, N, W, G
         self.stream = stream
@@ -600,7 +617,11 @@ class Decoder:
             raise ValueError(f"pool_policy must be 'fifo', 'lru' or 'lfu', not {pool_policy!r}")
         o = la_opts(N, W, G, max_seq, int(prompt_as_reference), pool_cap, temperature, seed, sp, int(profile),
                     top_k, top_p, policies[pool_policy])
-        self.h = la_create(self.weights.dims_struct, self.weights.struct, o)
+        self.kv_cache, self.slot = kv_cache, slot
+        if kv_cache is None:
+            self.h = la_create(self.weights.dims_struct, self.weights.struct, o)
+        else:
+            self.h = la_create_kv8(self.weights.dims_struct, self.weights.struct, o, kv_cache.struct, slot)
 
     def prefill(self, prompt) -> int:
         return la_prefill(self.h, prompt)
@@ -625,6 +646,10 @@ class Decoder:
 
     def debug_logits(self) -> np.ndarray:
         return la_debug_logits(self.h)
+
+    def fork_from(self, src: "Decoder") -> None:
+        """Continue from src's state in this decoder's slot of the same cache."""
+        la_fork(src.h, self.h)
 
     def close(self):
         if getattr(self, "h", None):

@@ -487,6 +487,35 @@ int la_kv8_compact(const la_kv8_cache *c, int32_t *table_out, int32_t *refs_out,
  * NULL) receives the word.  Errors: those and INVALID_ARG, CUDA. */
 int la_kv8_status(const la_kv8_cache *c, uint32_t *bits, void *stream);
 
+/* A decoder whose KV cache is slot `slot` of a paged 8-bit cache instead of
+ * memory of its own: a quarter of the bytes, and several decoders (slots) may
+ * share one pool and, after la_fork, one prompt's pages.  Everything else is
+ * as with la_create; the model is LA_BF16, its n_layers, n_kv_heads and
+ * head_dim are the cache's, and max_seq <= max_pages * page.  The decoder
+ * copies the struct, not the arrays: they outlive it, and table, lens and refs
+ * stay where they are (la_kv8_compact in place is fine between calls).  A
+ * step's own rows meet the attention at 16 bits; the cached ones are e4m3, so
+ * tokens may differ from those of la_create's cache.  la_prefill and
+ * la_import_state empty the slot first; la_destroy leaves it as it is (free it
+ * with la_kv8_free).  Calls on decoders that share a cache must not overlap,
+ * nor overlap other la_kv8 calls on it.
+ * When the pool runs out, the call returns LA_ERR_CAPACITY; when the slot does
+ * not hold the decoder's tokens any more, or the cache's status word has
+ * LA_KV8_BAD or LA_KV8_TIMEOUT (la_kv8_status clears it), LA_ERR_STATE.  The
+ * decoder needs la_prefill then.
+ * Errors: INVALID_ARG (also a cache that does not fit the model),
+ * UNSUPPORTED, OOM, CUDA. */
+int la_create_kv8(const la_model_dims *dims, const la_weights *weights, const la_opts *opts, const la_kv8_cache *cache,
+                  int32_t slot, la_handle **out);
+
+/* dst continues from src's state: its tokens, window and n-gram pool, and by
+ * la_kv8_fork its cached tokens, without running the model.  Both are
+ * la_create_kv8 decoders of the same model on the same cache, with the same N,
+ * W, pool capacity and policy and dst's max_seq large enough; dst's slot is
+ * emptied first.  The two then decode independently.
+ * Errors: INVALID_ARG, STATE (src has no state), CAPACITY, CUDA. */
+int la_fork(la_handle *src, la_handle *dst);
+
 void la_destroy(la_handle *h);
 const char *la_strerror(int code);
 const char *la_last_error(void);

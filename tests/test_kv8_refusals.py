@@ -103,3 +103,20 @@ def test_plain_form_is_e4m3():
     b = torch.arange(256, dtype=torch.uint8)
     assert np.array_equal(M.E4M3, b.view(torch.float8_e4m3fn).double().numpy(), equal_nan=True)
     assert M.scale_for(448.0) == 1.0 and M.scale_for(448.5) == 2.0 and M.scale_for(0.0) == 2.0 ** -60
+
+
+@pytest.mark.parametrize("kw,slot,dtype,max_seq,code,word", [
+    (dict(n_layers=3), 0, 1, 256, INVALID, "n_layers"), (dict(n_kv_heads=4), 0, 1, 256, INVALID, "n_kv_heads"),
+    (dict(head_dim=64), 0, 1, 256, INVALID, "head_dim"), ({}, 2, 1, 256, INVALID, "slot"), ({}, -1, 1, 256, INVALID, "slot"),
+    ({}, 0, 1, 257, INVALID, "max_seq"), ({}, 0, 0, 256, UNSUPPORTED, "bf16"), (dict(page=48), 0, 1, 256, UNSUPPORTED, "page"),
+    (dict(refs=None), 0, 1, 256, INVALID, "null")])
+def test_decoder_over_a_cache_refuses(L, kw, slot, dtype, max_seq, code, word):
+    dims = L.la_model_dims(1, 512, 4, 2, 128, 1024, 2048, 1e-5, 10000.0, dtype)
+    ptrs = (ctypes.c_void_p * 1)(256)
+    w = L.la_weights(*[ctypes.cast(ptrs, t) if t is not ctypes.c_void_p else 256 for _, t in L.la_weights._fields_])
+    o = L.la_opts(4, 5, 3, max_seq, 0, 0, 0.0, 0, None, 0, 0, 1.0, 0)
+    refused(lambda: L.la_create_kv8(dims, w, o, cache(L, **kw), slot), code, word)
+
+
+def test_fork_of_decoders_refuses_null(L):
+    refused(lambda: L.la_fork(None, None), INVALID, "two decoders")
