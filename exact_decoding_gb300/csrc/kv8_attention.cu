@@ -770,8 +770,22 @@ __device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity, unsigne
         }
     }
 }
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ void mbar_arrive_one(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Waits for this thread's loads from tensor memory; v is what they wrote, which nothing may read before.
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[N]) {
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
 }
 
 // 16 e4m3 bytes as 32 bytes of fp16.
@@ -1129,20 +1143,23 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         }
     } else if (warp == kMmaWarp) {
         // ================================================ products
-        if (lane == 0) {
-            if (!p.whole) {
-                Kv8Walk w = walk;
-                const bool any = kv8_next(p, tiles, w, u);
-                kv8_note(p, tiles, any, u);
-            }
-            constexpr uint32_t is = idesc_f16(kTileQ, kTileK), io = idesc_f16(kTileQ, HD);
-            int units = 0;
-            auto product_o = [&](int j, bool begins) {
-                const int b = j & 1;
-                ok = mbar_spin(p_full(b), j >> 1 & 1, err, LA_KV8_TIMEOUT) && mbar_spin(v_full(b), j >> 1 & 1, err, LA_KV8_TIMEOUT);
-                if (!ok) return;
-                tc_fence_after();
-                const uint32_t sv = sm + Lay::v_off + b * Lay::v_bytes, pt = tmem + kColS + 128 * b, ot = tmem + kColO + 128 * b;
+        // The whole warp runs this loop; one elected lane issues.  (Inside a
+        // branch on the lane's number each product took 90 cycles to issue.)
+        if (!p.whole) {
+            Kv8Walk w = walk;
+            const bool any = kv8_next(p, tiles, w, u);
+            if (lane == 0) kv8_note(p, tiles, any, u);
+        }
+        constexpr uint32_t is = idesc_f16(kTileQ, kTileK), io = idesc_f16(kTileQ, HD);
+        auto wait = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, mbar_spin(bar, parity & 1, err, LA_KV8_TIMEOUT)); };
+        int units = 0;
+        auto product_o = [&](int j, bool begins) {
+            const int b = j & 1;
+            ok = wait(p_full(b), j >> 1) && wait(v_full(b), j >> 1);
+            if (!ok) return;
+            tc_fence_after();
+            const uint32_t sv = sm + Lay::v_off + b * Lay::v_bytes, pt = tmem + kColS + 128 * b, ot = tmem + kColO + 128 * b;
+            if (elect_one()) {
 #pragma unroll
                 for (int kb = 0; kb < 2; ++kb) {
                     const uint64_t d = umma_desc_sw128(sv + kb * Lay::v_block);
@@ -1151,18 +1168,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 }
                 umma_commit(v_empty(b));
                 umma_commit(o_full(b));
-            };
-            while (ok && kv8_next(p, tiles, walk, u)) {
-                if (u.k0 >= u.k1) continue;
-                ok = mbar_spin(q_full, units & 1, err, LA_KV8_TIMEOUT);
-                ++units;
-                const int first = it;
-                for (int kt = u.k0; ok && kt < u.k1; ++kt, ++it) {
-                    const int b = it & 1;
-                    ok = mbar_spin(k_full(b), it >> 1 & 1, err, LA_KV8_TIMEOUT);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t sk = sm + Lay::k_off + b * Lay::k_bytes;
+            }
+            __syncwarp();
+        };
+        while (ok && kv8_next(p, tiles, walk, u)) {
+            if (u.k0 >= u.k1) continue;
+            ok = wait(q_full, units);
+            ++units;
+            const int first = it;
+            for (int kt = u.k0; ok && kt < u.k1; ++kt, ++it) {
+                const int b = it & 1;
+                ok = wait(k_full(b), it >> 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sk = sm + Lay::k_off + b * Lay::k_bytes;
+                if (elect_one()) {
 #pragma unroll
                     for (int db = 0; db < HD / 64; ++db) {
                         const uint64_t d = umma_desc_sw128(sk + db * Lay::k_block), q = umma_desc_sw128(sm + Lay::q_off + db * Lay::k_block);
@@ -1171,14 +1191,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                     }
                     umma_commit(s_full(b));
                     umma_commit(k_empty(b));
-                    if (it > first) product_o(it - 1, it - 1 < first + 2);
                 }
-                if (ok) product_o(it - 1, it - 1 < first + 2);
+                __syncwarp();
+                if (it > first) product_o(it - 1, it - 1 < first + 2);
             }
-            if (!ok) {   // void: wait (bounded) for the products in flight
-                umma_commit(drain);
-                mbar_spin(drain, 0, err, LA_KV8_TIMEOUT);
-            }
+            if (ok) product_o(it - 1, it - 1 < first + 2);
+        }
+        if (!ok) {   // void: wait (bounded) for the products in flight
+            if (elect_one()) umma_commit(drain);
+            __syncwarp();
+            mbar_spin(drain, 0, err, LA_KV8_TIMEOUT);
         }
         __syncwarp();
     } else {
@@ -1264,7 +1286,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                         tmem_ld_32x32b_x32(ts + 32 * k, v);
                         const int live = mt.live[k], vx = mt.vx[k];
                         const float f = mt.kf[k] * qf, add = static_cast<float>(vx) - (m == -INFINITY ? 0.f : m);
-                        tmem_ld_wait();
+                        tmem_ld_wait_for(v);
                         if (live < 32 || !cached) {
                             uint32_t see = live >= 32 ? 0xffffffffu : (1u << live) - 1u;   // keys that this row sees
                             if (!cached) {
@@ -1300,10 +1322,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                             l *= alpha;
 #pragma unroll
                             for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) - by);
+                            tmem_st_wait();
                             for (int q = 0; q < k; ++q) {   // this tile's weights so far
                                 uint32_t w[16];
                                 tmem_ld_32x32b_x16(ts + 16 * q, w);
-                                tmem_ld_wait();
+                                tmem_ld_wait_for(w);
 #pragma unroll
                                 for (int e = 0; e < 16; ++e) {
                                     const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
@@ -1318,7 +1341,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                                 for (int q = 0; q < HD / 16; ++q) {
                                     uint32_t o[16];
                                     tmem_ld_32x32b_x16(to + 16 * q, o);
-                                    tmem_ld_wait();
+                                    tmem_ld_wait_for(o);
 #pragma unroll
                                     for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
                                     tmem_st_32x32b_x16(to + 16 * q, o);
@@ -1388,7 +1411,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 if (first < end) {
                     tmem_ld_32x32b_x16(tmem + lanes + kColO + d0 + 16 * k, oa);
                     tmem_ld_32x32b_x16(tmem + lanes + kColO + 128 + d0 + 16 * k, ob);
-                    tmem_ld_wait();
+                    tmem_ld_wait_for(oa);
+                    tmem_ld_wait_for(ob);
                 }
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[e] = (fa == -1.f ? 0.f : fa * __uint_as_float(oa[e])) + (fb == -1.f ? 0.f : fb * __uint_as_float(ob[e]));
