@@ -657,10 +657,12 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
 // k_kv8_tiles: 128 query vectors per unit and 128 keys per tile on the
 // tcgen05 tensor cores.  With more than a few query vectors per KV head the
 // products and the softmax, not the bytes, bound the attention.
-//   warps 8..11  turn a tile's e4m3 bytes of K (or the new rows' bf16) into an
+//   warps 8..14  turn a tile's e4m3 bytes of K (or the new rows' bf16) into an
 //                fp16 operand in shared memory (128-byte swizzle), [128 keys x
-//                HD], two buffers; the next two tiles' bytes are in registers
-//   warps 12..14 the same for V^T [HD x 128 keys], one tile in registers
+//                HD], then the same for V^T [HD x 128 keys] of the tile before;
+//                two buffers each, the next tiles' bytes in registers.  (Four
+//                warps for K and three for V: 140 us against 136 for 256 rows
+//                over 16k tokens, 8 KV heads, 121 rows over 2k 35.1 against 32.4.)
 //   warp 15      issues S = Q K^T of tile i + 1, then O += P V (P from tensor
 //                memory) of tile i
 //   warps 0..3   softmax of the even tiles, warps 4..7 of the odd ones, each
@@ -675,7 +677,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
 // weights up to 2^8 lose nothing), so it is rarely read back.  Units are split
 // and joined like those of k_kv8_rows.
 constexpr int kTileQ = 128, kTileK = 128;
-constexpr int kKWarps = 4, kVWarps = 3, kVWarp0 = 8 + kKWarps, kMmaWarp = kVWarp0 + kVWarps;
+constexpr int kOpWarps = 7, kMmaWarp = 8 + kOpWarps;
 constexpr int kTileThreads = 32 * (kMmaWarp + 1);   // 16 warps: 4 to a quarter of an SM, 128 registers a thread
 constexpr float kLazy = 8.f;
 
@@ -829,9 +831,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int b = 0; b < 2; ++b) {
-            mbar_init(k_full(b), kKWarps);
+            mbar_init(k_full(b), kOpWarps);
             mbar_init(k_empty(b), 1);
-            mbar_init(v_full(b), kVWarps);
+            mbar_init(v_full(b), kOpWarps);
             mbar_init(v_empty(b), 1);
             mbar_init(s_full(b), 1);
             mbar_init(p_full(b), 4);
@@ -840,7 +842,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         for (int t = 0; t < 4; ++t) mbar_init(m_full(t), 1);
         mbar_init(q_full, 8);
         mbar_init(e_full, 8);
-        mbar_init(r_full, kKWarps);
+        mbar_init(r_full, kOpWarps);
         mbar_init(drain, 1);
         fence_barrier_init();
     }
@@ -876,82 +878,68 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     };
     const int r8 = lane & 7, cq = lane >> 3;
 
-    if (warp >= 8 && warp < kVWarp0) {
-        // ================================================ K
+    if (warp >= 8 && warp < kMmaWarp) {
+        // ================================================ operands
         const int w = warp - 8;
-        constexpr int NR = HD / (4 * kKWarps);   // 16-byte pieces per thread and tile
-        static_assert(NR * 32 * kKWarps * 16 == kTileK * HD, "every piece once");
+        // A tile of K, or of V, is NG groups of 32 16-byte pieces: 8 keys x 64
+        // bytes of K (lane: key r8, piece cq), 8 dims x 64 keys of V.  They are
+        // dealt to the warps in turn, K's from the first and V's from the last on.
+        constexpr int NG = HD / 4, NR = (NG + kOpWarps - 1) / kOpWarps;
+        auto k_group = [&](int n) { return w + n * kOpWarps; };
+        auto v_group = [&](int n) { return kOpWarps - 1 - w + n * kOpWarps; };
+        const uint32_t at0 = r8 * 128 + (((2 * cq) ^ r8) << 4), at1 = r8 * 128 + (((2 * cq + 1) ^ r8) << 4);   // both fp16 halves of a piece
         int new_tiles = 0;
         while (ok && kv8_next(p, tiles, walk, u)) {
             const Kv8Seq sq = u.sq;
-            auto k_row = [&](int i) { return r8 + 8 * (HD == 128 ? i >> 1 : i); };   // of this warp's 32 rows, which lie in one page
-            auto k_chunk = [&](int i) { return HD == 128 ? cq + 4 * (i & 1) : cq; };
-            auto load = [&](uint4 (&raw)[NR], int kt, int pg) {
-                const int pid = max(__shfl_sync(0xffffffffu, pg, w), 0);
-                const int row0 = ((kt - sq.ntiles) * kTileK + 32 * w) & (c.page - 1);
-                const uint8_t *src = static_cast<const uint8_t *>(c.k) + (kv8_block(c, p.a.layer, pid, u.head) * c.page + row0) * HD;
-#pragma unroll
-                for (int i = 0; i < NR; ++i) raw[i] = __ldcg(reinterpret_cast<const uint4 *>(src + k_row(i) * HD + 16 * k_chunk(i)));
-            };
-            // K of tile kt (number it) to its buffer; its registers take tile kt + 2.
-            // pg0, pg2: the pages of both; pg1, after: those between, entries of kt + 3.
-            uint4 raw0[NR], raw1[NR];
             const int c_first = max(u.k0, sq.ntiles);   // first cached tile of this piece
-            int pg0 = checked(entry(c_first)), pg1 = checked(entry(c_first + 1)), pg2 = checked(entry(c_first + 2)), after = entry(c_first + 3);
-            auto put = [&](uint4 (&raw)[NR], int kt) {
+            // Lane l < 4: block number of keys 32 l .. of a tile (a block is 2 KB
+            // at least, so 32 bits reach all memory), and which lanes have one.
+            auto block_of = [&](int page, uint32_t &held) {
+                held = __ballot_sync(0xffffffffu, page >= 0) & 15u;
+                return static_cast<uint32_t>(kv8_block(c, p.a.layer, max(page, 0), u.head));
+            };
+            uint4 kraw[NR], vraw[NR];                   // the next tiles' bytes
+            uint32_t k_held, k_blk = block_of(checked(entry(c_first)), k_held);   // the tile in kraw
+            uint32_t next_held = 0, next_blk = 0;       // the tile that vraw takes next
+            uint32_t v_held = k_held;                   // the tile in vraw
+            int after = entry(c_first + 1);             // the tile that kraw takes next
+            float k_sc = 1.f, v_sc = 1.f;               // scales of the tile in kraw (warp 8, lanes 0..3)
+            auto load_k = [&]() {
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    const int g = k_group(n), row = 8 * (HD == 128 ? g >> 1 : g);
+                    if (g >= NG) break;
+                    const uint32_t blk = __shfl_sync(0xffffffffu, k_blk, row >> 5);
+                    const uint8_t *src = static_cast<const uint8_t *>(c.k) + static_cast<uint64_t>(blk) * static_cast<uint32_t>(c.page * HD);
+                    kraw[n] = __ldcg(reinterpret_cast<const uint4 *>(src + ((row & (c.page - 1)) + r8) * HD + (HD == 128 ? 64 * (g & 1) : 0) + 16 * cq));
+                }
+                if (w == 0 && lane < 4) {
+                    k_sc = c.k_scale[k_blk];
+                    v_sc = c.v_scale[k_blk];
+                }
+            };
+            auto load_v = [&](uint32_t mine) {
+                const uint32_t b0 = __shfl_sync(0xffffffffu, mine, cq >> 1), b1 = __shfl_sync(0xffffffffu, mine, (cq >> 1) + 2);
+                const uint8_t *v0 = static_cast<const uint8_t *>(c.v) + static_cast<uint64_t>(b0) * static_cast<uint32_t>(c.page * HD) + (16 * cq & (c.page - 1));
+                const uint8_t *v1 = static_cast<const uint8_t *>(c.v) + static_cast<uint64_t>(b1) * static_cast<uint32_t>(c.page * HD) + ((16 * cq + 64) & (c.page - 1));
+#pragma unroll
+                for (int n = 0; n < NR; ++n) {
+                    const int g = v_group(n);
+                    if (g >= NG) break;
+                    vraw[n] = __ldcg(reinterpret_cast<const uint4 *>((g & 1 ? v1 : v0) + (8 * (g >> 1) + r8) * c.page));
+                }
+            };
+            auto k_tile = [&](int kt, int it) {
                 const int b = it & 1, use = it >> 1;
                 const uint32_t sk = sm + Lay::k_off + b * Lay::k_bytes;
                 if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(k_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
                 if (!ok) return;
-                if (w == 0) {
-                    if (lane < 4) {
-                        Kv8Meta &mt = meta[it & 3];
-                        const int key = (kt - sq.ntiles) * kTileK + 32 * lane;
-                        const bool have = pg0 >= 0;
-                        const long long blk = kv8_block(c, p.a.layer, max(pg0, 0), u.head);
-                        mt.kf[lane] = have ? c.k_scale[blk] : 1.f;
-                        mt.vx[lane] = have ? exponent_of(c.v_scale[blk]) : 0;
-                        mt.live[lane] = have ? min(max(sq.len - key, 0), 32) : 0;
-                        if (lane == 0) mt.odd = 0;
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_one(m_full(it & 3));
-                }
-#pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    uint4 x, y;
-                    e4m3x16_f16(raw[i], x, y);
-                    const int ch = 2 * (k_chunk(i) & 3);
-                    const uint32_t at = sk + (k_chunk(i) >> 2) * Lay::k_block + (32 * w + k_row(i)) * 128;
-                    st_shared(at + ((ch ^ r8) << 4), x);
-                    st_shared(at + (((ch + 1) ^ r8) << 4), y);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_one(k_full(b));
-                // (The entry is checked before the loads below are issued: a wait for
-                // it would wait for them too.)
-                const int pg3 = checked(after);
-                if (kt + 2 < u.k1) load(raw, kt + 2, pg2);
-                after = entry(kt + 4);
-                pg0 = pg1;
-                pg1 = pg2;
-                pg2 = pg3;
-                ++it;
-            };
-            if (c_first < u.k1) load(raw0, c_first, pg0);
-            if (c_first + 1 < u.k1) load(raw1, c_first + 1, pg1);
-            for (int kt = u.k0; ok && kt < min(u.k1, sq.ntiles); ++kt, ++it) {
-                const int b = it & 1, use = it >> 1;
-                const uint32_t sk = sm + Lay::k_off + b * Lay::k_bytes;
-                if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(k_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
-                if (!ok) break;
-                {
+                if (kt < sq.ntiles) {
                     // New rows: bf16, scaled by a power of two for the whole tile.
                     const int key0 = kt * kTileK, nkeys = min(kTileK, sq.rows - key0);
                     const __nv_bfloat16 *kn = static_cast<const __nv_bfloat16 *>(p.a.k) + (sq.first + key0) * p.a.k_stride + u.head * HD;
                     const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + u.head * HD;
-                    constexpr int C8 = HD / 8, NT = 32 * kKWarps;   // 16-byte pieces of a row
+                    constexpr int C8 = HD / 8, NT = 32 * kOpWarps;   // 16-byte pieces of a row
                     const int ot = w * 32 + lane;
                     // K's rows come into its operand buffer as they are (asynchronous
                     // copies, all in flight: one load after another took 12 us) and
@@ -1004,12 +992,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                     }
                     __syncwarp();
                     ok = __all_sync(0xffffffffu, mbar_wait(r_full, new_tiles & 1, err, LA_KV8_TIMEOUT));
-                    if (!ok) break;
+                    if (!ok) return;
                     ++new_tiles;
                     ak = av = 0;
                     odd = false;
 #pragma unroll
-                    for (int k = 0; k < kKWarps; ++k) {
+                    for (int k = 0; k < kOpWarps; ++k) {
                         ak = max(ak, mine[k]);
                         av = max(av, mine[8 + k] & 0xffffu);
                         odd |= mine[8 + k] >> 16 != 0;
@@ -1032,77 +1020,58 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                         const uint4 x = ld_shared(kat(i));
                         st_shared_u32x4(kat(i), scaled_f16(x.x, fk), scaled_f16(x.y, fk), scaled_f16(x.z, fk), scaled_f16(x.w, fk));
                     }
+                } else {
+                    if (w == 0) {
+                        if (lane < 4) {
+                            Kv8Meta &mt = meta[it & 3];
+                            const bool have = k_held >> lane & 1u;
+                            mt.kf[lane] = have ? k_sc : 1.f;
+                            mt.vx[lane] = have ? exponent_of(v_sc) : 0;
+                            mt.live[lane] = have ? min(max(sq.len - (kt - sq.ntiles) * kTileK - 32 * lane, 0), 32) : 0;
+                            if (lane == 0) mt.odd = 0;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_one(m_full(it & 3));
+                    }
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        const int g = k_group(n);
+                        if (g >= NG) break;
+                        uint4 x, y;
+                        e4m3x16_f16(kraw[n], x, y);
+                        const uint32_t at = sk + (HD == 128 ? (g & 1) * Lay::k_block + (g >> 1) * 1024 : g * 1024);
+                        st_shared(at + at0, x);
+                        st_shared(at + at1, y);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_one(k_full(b));
-            }
-#pragma unroll 1
-            for (int kt = c_first; ok && kt < u.k1; kt += 2) {
-                put(raw0, kt);
-                if (ok && kt + 1 < u.k1) put(raw1, kt + 1);
-            }
-        }
-    } else if (warp >= kVWarp0 && warp < kMmaWarp) {
-        // ================================================ V
-        const int w = warp - kVWarp0;
-        // Groups of 32 pieces (8 dims x 4 pieces of 16 keys), dealt to the warps in turn.
-        constexpr int NG = HD / 4, NR = (NG + kVWarps - 1) / kVWarps;
-        while (ok && kv8_next(p, tiles, walk, u)) {
-            const Kv8Seq sq = u.sq;
-            auto v_dim = [&](int n) { return (w + n * kVWarps) / 2 * 8 + r8; };
-            auto v_chunk = [&](int n) { return cq + 4 * ((w + n * kVWarps) & 1); };
-            uint4 raw[NR];
-            auto load = [&](int kt, int pg) {
-                const int pid0 = max(__shfl_sync(0xffffffffu, pg, cq >> 1), 0), pid1 = max(__shfl_sync(0xffffffffu, pg, (cq >> 1) + 2), 0);
-                const int key = (kt - sq.ntiles) * kTileK + 16 * cq;
-                const uint8_t *vp = static_cast<const uint8_t *>(c.v);
-                const uint8_t *src0 = vp + kv8_block(c, p.a.layer, pid0, u.head) * c.page * HD + (key & (c.page - 1));
-                const uint8_t *src1 = vp + kv8_block(c, p.a.layer, pid1, u.head) * c.page * HD + ((key + 64) & (c.page - 1));
-#pragma unroll
-                for (int n = 0; n < NR; ++n)
-                    if (w + n * kVWarps < NG) raw[n] = __ldcg(reinterpret_cast<const uint4 *>(((w + n * kVWarps) & 1 ? src1 : src0) + v_dim(n) * c.page));
+                if (kt >= sq.ntiles) {
+                    // (The entry is checked before the loads below are issued: a wait
+                    // for it would wait for them too.)
+                    next_blk = k_blk;
+                    next_held = k_held;
+                    k_blk = block_of(checked(after), k_held);
+                    if (kt + 1 < u.k1) load_k();
+                    after = entry(kt + 2);
+                }
             };
-            const int c_first = max(u.k0, sq.ntiles);
-            int pg0 = checked(entry(c_first)), pg1 = checked(entry(c_first + 1)), after = entry(c_first + 2);
-            if (c_first < u.k1) load(c_first, pg0);
-#pragma unroll 1
-            for (int kt = u.k0; ok && kt < u.k1; ++kt, ++it) {
+            auto v_tile = [&](int kt, int it) {
                 const int b = it & 1, use = it >> 1;
                 const uint32_t sv = sm + Lay::v_off + b * Lay::v_bytes;
                 if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(v_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
-                if (!ok) break;
-                if (kt >= sq.ntiles) {
-                    // Bytes behind the last token, and of missing pages, may be anything.
-                    const int key0 = (kt - sq.ntiles) * kTileK, held = __ballot_sync(0xffffffffu, pg0 >= 0 && lane < 4);
-                    if (sq.len - key0 < kTileK || held != 15) {
-#pragma unroll
-                        for (int n = 0; n < NR; ++n) {
-                            const int ch = v_chunk(n), live = held >> (ch >> 1) & 1 ? sq.len - key0 - 16 * ch : 0;
-                            auto cut = [](uint32_t a, int m) { return m >= 4 ? a : m <= 0 ? 0u : a & ((1u << (8 * m)) - 1u); };
-                            raw[n] = make_uint4(cut(raw[n].x, live), cut(raw[n].y, live - 4), cut(raw[n].z, live - 8), cut(raw[n].w, live - 12));
-                        }
-                    }
-#pragma unroll
-                    for (int n = 0; n < NR; ++n) {
-                        if (w + n * kVWarps >= NG) break;
-                        uint4 x, y;
-                        e4m3x16_f16(raw[n], x, y);
-                        const int ch = 2 * (v_chunk(n) & 3);
-                        const uint32_t at = sv + (v_chunk(n) >> 2) * Lay::v_block + v_dim(n) * 128;
-                        st_shared(at + ((ch ^ r8) << 4), x);
-                        st_shared(at + (((ch + 1) ^ r8) << 4), y);
-                    }
-                } else {
+                if (!ok) return;
+                if (kt < sq.ntiles) {
                     // Two new rows of eight dims at a time, transposed.  A NaN or
                     // infinity counts 0 here and is added at the end for the
                     // rows that see it.
                     ok = __all_sync(0xffffffffu, mbar_wait(m_full(it & 3), it >> 2 & 1, err, LA_KV8_TIMEOUT));
-                    if (!ok) break;
+                    if (!ok) return;
                     const float fv = power_of(-meta[it & 3].vx[0]);
                     const int key0 = kt * kTileK, nkeys = min(kTileK, sq.rows - key0);
                     const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + u.head * HD;
-                    constexpr int NT = 32 * kVWarps, NP = kTileK / 2 * (HD / 8), B = 4;   // pairs of rows, in flight
+                    constexpr int NT = 32 * kOpWarps, NP = kTileK / 2 * (HD / 8), B = 4;   // pairs of rows, in flight
 #pragma unroll 1
                     for (int j0 = w * 32 + lane; j0 < NP; j0 += B * NT) {
                         uint4 va[B], vb[B];
@@ -1128,18 +1097,48 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                             }
                         }
                     }
+                } else {
+                    // Bytes behind the last token, and of missing pages, may be anything.
+                    const int key0 = (kt - sq.ntiles) * kTileK;
+                    if (sq.len - key0 < kTileK || v_held != 15u) {
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) {
+                            const int ch = cq + 4 * (v_group(n) & 1), live = v_held >> (ch >> 1) & 1u ? sq.len - key0 - 16 * ch : 0;
+                            auto cut = [](uint32_t a, int m) { return m >= 4 ? a : m <= 0 ? 0u : a & ((1u << (8 * m)) - 1u); };
+                            vraw[n] = make_uint4(cut(vraw[n].x, live), cut(vraw[n].y, live - 4), cut(vraw[n].z, live - 8), cut(vraw[n].w, live - 12));
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        const int g = v_group(n);
+                        if (g >= NG) break;
+                        uint4 x, y;
+                        e4m3x16_f16(vraw[n], x, y);
+                        const uint32_t at = sv + (g & 1) * Lay::v_block + (g >> 1) * 1024;
+                        st_shared(at + at0, x);
+                        st_shared(at + at1, y);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_one(v_full(b));
-                if (kt >= sq.ntiles) {
-                    const int pg2 = checked(after);
-                    if (kt + 1 < u.k1) load(kt + 1, pg1);
-                    after = entry(kt + 3);
-                    pg0 = pg1;
-                    pg1 = pg2;
+                if (kt >= sq.ntiles && kt + 1 < u.k1) {
+                    load_v(next_blk);
+                    v_held = next_held;
                 }
+            };
+            if (c_first < u.k1) {
+                load_k();
+                load_v(k_blk);
             }
+            // K a tile ahead of V: S of the next tile is issued before O of this one.
+            const int first = it;
+#pragma unroll 1
+            for (int kt = u.k0 - 1; ok && kt < u.k1; ++kt) {
+                if (kt + 1 < u.k1) k_tile(kt + 1, first + kt + 1 - u.k0);
+                if (ok && kt >= u.k0) v_tile(kt, first + kt - u.k0);
+            }
+            it = first + max(u.k1 - u.k0, 0);
         }
     } else if (warp == kMmaWarp) {
         // ================================================ products
