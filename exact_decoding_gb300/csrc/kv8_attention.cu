@@ -28,6 +28,14 @@
 
 namespace la {
 
+// Bounded wait.  Its loop exists once, not at every wait: the code of a kernel's
+// roles has to stay in the instruction cache (k_kv8_tiles, 256 rows over 16k
+// tokens, 8 KV heads: 131.6 us with the loops inline, 125.7 without).
+__device__ __noinline__ bool bar_wait_on(uint32_t bar, uint32_t parity, unsigned *err, unsigned bit) { return mbar_wait(bar, parity, err, bit); }
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, unsigned *err, unsigned bit) {
+    return mbar_try_wait(bar, parity) || bar_wait_on(bar, parity, err, bit);
+}
+
 constexpr float kKv8Log2e = 1.4426950408889634f;
 
 struct Kv8Args {
@@ -491,7 +499,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
 
         // ---- cached tokens
         auto landed = [&]() {   // the next block to read is there
-            ok = __all_sync(0xffffffffu, mbar_wait(bars + out_slot * 8, out_phase, c.status, LA_KV8_TIMEOUT));
+            ok = __all_sync(0xffffffffu, bar_wait(bars + out_slot * 8, out_phase, c.status, LA_KV8_TIMEOUT));
             return ok;
         };
         auto next = [&]() {     // it has been read: its slot takes the next block to load
@@ -545,7 +553,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
                 if (piece == 0) {   // V is the block behind K
                     const int vs = PAGE / KT == 1 ? out_slot : out_slot + 1 == NS ? 0 : out_slot + 1;
                     const uint32_t ph = PAGE / KT == 1 || out_slot + 1 < NS ? out_phase : out_phase ^ 1;
-                    ok = __all_sync(0xffffffffu, mbar_wait(bars + vs * 8, ph, c.status, LA_KV8_TIMEOUT));
+                    ok = __all_sync(0xffffffffu, bar_wait(bars + vs * 8, ph, c.status, LA_KV8_TIMEOUT));
                     if (!ok) break;
                     vblk = my_ring + vs * Lay::block;
                 }
@@ -592,7 +600,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
         }
         if (!ok) {   // void: wait (bounded) for what is still in flight
             for (; read < issued; ++read) {
-                mbar_wait(bars + out_slot * 8, out_phase, c.status, LA_KV8_TIMEOUT);
+                bar_wait(bars + out_slot * 8, out_phase, c.status, LA_KV8_TIMEOUT);
                 if (++out_slot == NS) {
                     out_slot = 0;
                     out_phase ^= 1;
@@ -657,27 +665,30 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
 // k_kv8_tiles: 128 query vectors per unit and 128 keys per tile on the
 // tcgen05 tensor cores.  With more than a few query vectors per KV head the
 // products and the softmax, not the bytes, bound the attention.
-//   warps 8..14  turn a tile's e4m3 bytes of K (or the new rows' bf16) into an
+//   warps 8..13  turn a tile's e4m3 bytes of K (or the new rows' bf16) into an
 //                fp16 operand in shared memory (128-byte swizzle), [128 keys x
 //                HD], then the same for V^T [HD x 128 keys] of the tile before;
-//                two buffers each, the next tiles' bytes in registers.  (Four
-//                warps for K and three for V: 140 us against 136 for 256 rows
-//                over 16k tokens, 8 KV heads, 121 rows over 2k 35.1 against 32.4.)
+//                two buffers each
+//   warp 14      brings the bytes into a ring in shared memory, a page's block of
+//                K or V by one bulk copy
 //   warp 15      issues S = Q K^T of tile i + 1, then O += P V (P from tensor
 //                memory) of tile i
 //   warps 0..3   softmax of the even tiles, warps 4..7 of the odd ones, each
 //                thread a query vector; P replaces S in tensor memory.  Two
 //                groups, since one alone waits for tensor memory half of the
 //                time: 2.4 us per tile.
-// Bytes through a ring in shared memory instead of registers measured slower
-// (256 rows over 16k tokens, 8 KV heads: 176 us against 155): operands, bytes
-// and products share its bandwidth.
+// What bounds a tile (1.8 us; its products take 0.55 us) are the instructions of
+// these warps, which share four schedulers: anything that waits must not poll
+// (the softmax and the products polling: 123.4 us against 118.0 for 256 rows over
+// 16k tokens, 8 KV heads), the bytes come by bulk copies (loads to registers by
+// seven operand warps: 131.3), and S is read 32 columns at a time (16: 136.0,
+// 64: 134.3, both polling).
 // The groups have an O each in tensor memory, added at the end.  An O's scale
 // follows the running maximum only when that has grown by 2^8 since (fp16
 // weights up to 2^8 lose nothing), so it is rarely read back.  Units are split
 // and joined like those of k_kv8_rows.
 constexpr int kTileQ = 128, kTileK = 128;
-constexpr int kOpWarps = 7, kMmaWarp = 8 + kOpWarps;
+constexpr int kOpWarps = 6, kLoadWarp = 8 + kOpWarps, kMmaWarp = kLoadWarp + 1;
 constexpr int kTileThreads = 32 * (kMmaWarp + 1);   // 16 warps: 4 to a quarter of an SM, 128 registers a thread
 constexpr float kLazy = 8.f;
 
@@ -688,16 +699,21 @@ struct Tiles {
     static constexpr uint32_t k_bytes = HD / 64 * k_block, v_bytes = 2 * v_block;
     static constexpr uint32_t k_off = 0, v_off = 2 * k_bytes;      // two buffers each
     static constexpr uint32_t q_off = v_off + 2 * v_bytes;         // Q [128 x HD]
-    static constexpr uint32_t meta_off = q_off + k_bytes;          // [4] Kv8Meta of the last tiles
+    // The cache's bytes as they come: stages of K or V of a tile, in a ring
+    static constexpr int raw_slots = HD == 128 ? 3 : 6;
+    static constexpr uint32_t raw_off = q_off + k_bytes, raw_bytes = kTileK * HD;
+    static constexpr uint32_t head_off = raw_off + raw_slots * raw_bytes;   // [raw_slots] Kv8Meta of the bytes in the ring
+    static constexpr uint32_t meta_off = head_off + raw_slots * 64;         // [4] Kv8Meta of the last tiles
     static constexpr uint32_t red_off = meta_off + 4 * 64;         // [2][2][8] maxima of the new rows' tile
-    static constexpr uint32_t ml_off = red_off + 128;              // [2 groups][128] running maximum and sum
-    static constexpr uint32_t qf_off = ml_off + 2 * kTileQ * 8;    // [128] factors on the rows' scores
+    static constexpr uint32_t qf_off = red_off + 128;              // [128] factors on the rows' scores
     static constexpr uint32_t odd_off = qf_off + kTileQ * 4;       // [2 groups]
     static constexpr uint32_t bar_off = odd_off + 16;
-    static constexpr uint32_t tiles_off = bar_off + 24 * 8 + (kMmaWarp + 1) * 8;
-    static size_t bytes(int n_seqs) { return tiles_off + (static_cast<size_t>(n_seqs) + 1) * 8 + 1024; }
+    static constexpr uint32_t tiles_off = bar_off + 40 * 8 + (kMmaWarp + 1) * 8;
+    static constexpr size_t bytes(int n_seqs) { return tiles_off + (static_cast<size_t>(n_seqs) + 1) * 8; }
+    static_assert(tiles_off + (LA_KV8_MAX_SEQS + 1) * 8 <= 227 * 1024, "shared memory of a block");
 };
-// TMEM columns: S of even and odd tiles (P over their first halves), then their O.
+// TMEM columns: S of even and odd tiles (P over their first halves; behind it,
+// once a group is through with a unit, its rows' maximum and sum), then their O.
 constexpr uint32_t kColS = 0, kColO = 256, kColAll = 512;
 
 struct Kv8Meta {
@@ -747,31 +763,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-// Bounded wait like mbar_wait, without the suspension of try_wait: that wakes
-// up late, and the products and the softmax wait on one another each tile.
-__device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity, unsigned *err, unsigned bit) {
-    uint64_t t0 = 0;
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 64; ++i) {
-            uint32_t done;
-            asm volatile(
-                "{\n\t.reg .pred p;\n\t"
-                "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                "selp.u32 %0, 1, 0, p;\n\t}"
-                : "=r"(done)
-                : "r"(bar), "r"(parity)
-                : "memory");
-            if (done) return true;
-        }
-        const uint64_t now = globaltimer();
-        if (t0 == 0) t0 = now;
-        else if (now - t0 > kWaitNs) {
-            atomicOr(err, bit);
-            return false;
-        }
-    }
-}
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -790,6 +781,17 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[N]) {
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
 }
 
+// Two columns of this thread's row of tensor memory.
+__device__ __forceinline__ void tmem_st_pair(uint32_t at, float a, float b) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(at), "f"(a), "f"(b) : "memory");
+}
+__device__ __forceinline__ float2 tmem_ld_pair(uint32_t at) {
+    uint32_t v[2];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at));
+    tmem_ld_wait_for(v);
+    return make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+}
+
 // 16 e4m3 bytes as 32 bytes of fp16.
 __device__ __forceinline__ void e4m3x16_f16(const uint4 &w, uint4 &a, uint4 &b) {
     e4m3x4_f16(w.x, a.x, a.y);
@@ -804,14 +806,17 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t at) {
 }
 __device__ __forceinline__ void st_shared(uint32_t at, const uint4 &v) { st_shared_u32x4(at, v.x, v.y, v.z, v.w); }
 
+// One copy for the roles of k_kv8_tiles (123.5 us against 126.0).  k_kv8_rows has it inline: a call costs its short runs 2 us.
+__device__ __noinline__ bool kv8_next_call(const Kv8Args &p, const long long *tiles, Kv8Walk &w, Kv8Piece &u) { return kv8_next(p, tiles, w, u); }
+
 template <int HD>
 __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_constant__ Kv8Args p) {
     using Lay = Tiles<HD>;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = smem_u32(smem_raw);
-    uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t tiles_smem[];   // the operands' swizzle repeats every 1024 bytes
+    uint8_t *smem = tiles_smem;
     const uint32_t sm = smem_u32(smem);
     Kv8Meta *meta = reinterpret_cast<Kv8Meta *>(smem + Lay::meta_off);
+    Kv8Meta *head = reinterpret_cast<Kv8Meta *>(smem + Lay::head_off);
     uint32_t *red = reinterpret_cast<uint32_t *>(smem + Lay::red_off);
     long long *tiles = reinterpret_cast<long long *>(smem + Lay::tiles_off);
     const uint32_t bars = sm + Lay::bar_off;
@@ -823,9 +828,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     auto p_full = [&](int b) { return bars + 8 * (10 + b); };      // 4 softmax warps
     auto m_full = [&](int t) { return bars + 8 * (12 + t); };      // meta of tile % 4
     auto o_full = [&](int b) { return bars + 8 * (16 + b); };      // commit of O
-    const uint32_t q_full = bars + 8 * 18, r_full = bars + 8 * 19, drain = bars + 8 * 20, e_full = bars + 8 * 21;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::bar_off + 8 * 22);
-    long long *warp_sum = reinterpret_cast<long long *>(smem + Lay::bar_off + 24 * 8);
+    auto raw_full = [&](int s) { return bars + 8 * (22 + s); };    // bulk copies
+    auto raw_empty = [&](int s) { return bars + 8 * (28 + s); };   // the operand warps
+    const uint32_t q_full = bars + 8 * 34, r_full = bars + 8 * 35, drain = bars + 8 * 36, e_full = bars + 8 * 37;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::bar_off + 8 * 38);
+    long long *warp_sum = reinterpret_cast<long long *>(smem + Lay::bar_off + 40 * 8);
 
     const la_kv8_cache &c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -840,6 +847,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             mbar_init(o_full(b), 1);
         }
         for (int t = 0; t < 4; ++t) mbar_init(m_full(t), 1);
+        for (int t = 0; t < Lay::raw_slots; ++t) {
+            mbar_init(raw_full(t), 1);
+            mbar_init(raw_empty(t), kOpWarps);
+        }
         mbar_init(q_full, 8);
         mbar_init(e_full, 8);
         mbar_init(r_full, kOpWarps);
@@ -876,63 +887,49 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         if (e != -2) atomicOr(err, LA_KV8_BAD);
         return -1;
     };
-    const int r8 = lane & 7, cq = lane >> 3;
 
-    if (warp >= 8 && warp < kMmaWarp) {
+    if (warp >= 8 && warp < kLoadWarp) {
         // ================================================ operands
-        const int w = warp - 8;
-        // A tile of K, or of V, is NG groups of 32 16-byte pieces: 8 keys x 64
-        // bytes of K (lane: key r8, piece cq), 8 dims x 64 keys of V.  They are
-        // dealt to the warps in turn, K's from the first and V's from the last on.
+        const int w = __shfl_sync(0xffffffffu, warp - 8, 0);   // the same in all lanes, for the compiler too
+        // A tile of K, or of V, is NG groups of 32 16-byte pieces, dealt to the
+        // warps in turn, K's from the first and V's from the last on: 8 keys x 64
+        // bytes of K, 8 dims x 64 keys of V.  Lane: key (dim) r8, piece cq; where a
+        // row has 128 bytes, the odd rows take the other 64, so that the lanes read
+        // (and write) different banks.
         constexpr int NG = HD / 4, NR = (NG + kOpWarps - 1) / kOpWarps;
-        auto k_group = [&](int n) { return w + n * kOpWarps; };
-        auto v_group = [&](int n) { return kOpWarps - 1 - w + n * kOpWarps; };
-        const uint32_t at0 = r8 * 128 + (((2 * cq) ^ r8) << 4), at1 = r8 * 128 + (((2 * cq + 1) ^ r8) << 4);   // both fp16 halves of a piece
-        int new_tiles = 0;
-        while (ok && kv8_next(p, tiles, walk, u)) {
+        const int r8 = lane >> 2, cq = lane & 3;
+        const uint32_t half = HD == 128 ? r8 & 1 : 0, vhalf = r8 & 1;
+        const uint32_t put0 = r8 * 128 + (((2 * cq) ^ r8) << 4), put1 = r8 * 128 + (((2 * cq + 1) ^ r8) << 4);
+        auto put_f16 = [&](uint32_t at, const uint4 &bytes) {   // a piece's values, as fp16, to their rows
+            uint4 x, y;
+            e4m3x16_f16(bytes, x, y);
+            st_shared(at + put0, x);
+            st_shared(at + put1, y);
+        };
+        auto v_at = [&](uint32_t h) {   // byte of keys 64 h + 16 cq of dim r8 in V's stage: pages of [HD][page]
+            const uint32_t key = 64 * h + 16 * cq;
+            return (key >> p.page_log2) * static_cast<uint32_t>(HD << p.page_log2) + (r8 << p.page_log2) + (key & (c.page - 1));
+        };
+        const uint32_t v_at0 = v_at(vhalf), v_at1 = v_at(vhalf ^ 1);
+        int new_tiles = 0, slot = 0;
+        uint32_t phase = 0;
+        auto landed = [&]() {   // the next stage of bytes is there
+            ok = __all_sync(0xffffffffu, bar_wait(raw_full(slot), phase, err, LA_KV8_TIMEOUT));
+            return sm + Lay::raw_off + slot * Lay::raw_bytes;
+        };
+        auto read = [&]() {     // and has been read
+            if (lane == 0) mbar_arrive_one(raw_empty(slot));
+            if (++slot == Lay::raw_slots) {
+                slot = 0;
+                phase ^= 1;
+            }
+        };
+        while (ok && kv8_next_call(p, tiles, walk, u)) {
             const Kv8Seq sq = u.sq;
-            const int c_first = max(u.k0, sq.ntiles);   // first cached tile of this piece
-            // Lane l < 4: block number of keys 32 l .. of a tile (a block is 2 KB
-            // at least, so 32 bits reach all memory), and which lanes have one.
-            auto block_of = [&](int page, uint32_t &held) {
-                held = __ballot_sync(0xffffffffu, page >= 0) & 15u;
-                return static_cast<uint32_t>(kv8_block(c, p.a.layer, max(page, 0), u.head));
-            };
-            uint4 kraw[NR], vraw[NR];                   // the next tiles' bytes
-            uint32_t k_held, k_blk = block_of(checked(entry(c_first)), k_held);   // the tile in kraw
-            uint32_t next_held = 0, next_blk = 0;       // the tile that vraw takes next
-            uint32_t v_held = k_held;                   // the tile in vraw
-            int after = entry(c_first + 1);             // the tile that kraw takes next
-            float k_sc = 1.f, v_sc = 1.f;               // scales of the tile in kraw (warp 8, lanes 0..3)
-            auto load_k = [&]() {
-#pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    const int g = k_group(n), row = 8 * (HD == 128 ? g >> 1 : g);
-                    if (g >= NG) break;
-                    const uint32_t blk = __shfl_sync(0xffffffffu, k_blk, row >> 5);
-                    const uint8_t *src = static_cast<const uint8_t *>(c.k) + static_cast<uint64_t>(blk) * static_cast<uint32_t>(c.page * HD);
-                    kraw[n] = __ldcg(reinterpret_cast<const uint4 *>(src + ((row & (c.page - 1)) + r8) * HD + (HD == 128 ? 64 * (g & 1) : 0) + 16 * cq));
-                }
-                if (w == 0 && lane < 4) {
-                    k_sc = c.k_scale[k_blk];
-                    v_sc = c.v_scale[k_blk];
-                }
-            };
-            auto load_v = [&](uint32_t mine) {
-                const uint32_t b0 = __shfl_sync(0xffffffffu, mine, cq >> 1), b1 = __shfl_sync(0xffffffffu, mine, (cq >> 1) + 2);
-                const uint8_t *v0 = static_cast<const uint8_t *>(c.v) + static_cast<uint64_t>(b0) * static_cast<uint32_t>(c.page * HD) + (16 * cq & (c.page - 1));
-                const uint8_t *v1 = static_cast<const uint8_t *>(c.v) + static_cast<uint64_t>(b1) * static_cast<uint32_t>(c.page * HD) + ((16 * cq + 64) & (c.page - 1));
-#pragma unroll
-                for (int n = 0; n < NR; ++n) {
-                    const int g = v_group(n);
-                    if (g >= NG) break;
-                    vraw[n] = __ldcg(reinterpret_cast<const uint4 *>((g & 1 ? v1 : v0) + (8 * (g >> 1) + r8) * c.page));
-                }
-            };
             auto k_tile = [&](int kt, int it) {
                 const int b = it & 1, use = it >> 1;
                 const uint32_t sk = sm + Lay::k_off + b * Lay::k_bytes;
-                if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(k_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
+                if (use > 0) ok = __all_sync(0xffffffffu, bar_wait(k_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
                 if (!ok) return;
                 if (kt < sq.ntiles) {
                     // New rows: bf16, scaled by a power of two for the whole tile.
@@ -991,7 +988,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                         mbar_arrive_one(r_full);
                     }
                     __syncwarp();
-                    ok = __all_sync(0xffffffffu, mbar_wait(r_full, new_tiles & 1, err, LA_KV8_TIMEOUT));
+                    ok = __all_sync(0xffffffffu, bar_wait(r_full, new_tiles & 1, err, LA_KV8_TIMEOUT));
                     if (!ok) return;
                     ++new_tiles;
                     ak = av = 0;
@@ -1021,52 +1018,40 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                         st_shared_u32x4(kat(i), scaled_f16(x.x, fk), scaled_f16(x.y, fk), scaled_f16(x.z, fk), scaled_f16(x.w, fk));
                     }
                 } else {
+                    const uint32_t raw = landed();
+                    if (!ok) return;
                     if (w == 0) {
-                        if (lane < 4) {
-                            Kv8Meta &mt = meta[it & 3];
-                            const bool have = k_held >> lane & 1u;
-                            mt.kf[lane] = have ? k_sc : 1.f;
-                            mt.vx[lane] = have ? exponent_of(v_sc) : 0;
-                            mt.live[lane] = have ? min(max(sq.len - (kt - sq.ntiles) * kTileK - 32 * lane, 0), 32) : 0;
-                            if (lane == 0) mt.odd = 0;
-                        }
+                        if (lane < 16) reinterpret_cast<uint32_t *>(meta + (it & 3))[lane] = reinterpret_cast<const uint32_t *>(head + slot)[lane];
                         __syncwarp();
                         if (lane == 0) mbar_arrive_one(m_full(it & 3));
                     }
+                    uint4 x[NR];
 #pragma unroll
                     for (int n = 0; n < NR; ++n) {
-                        const int g = k_group(n);
-                        if (g >= NG) break;
-                        uint4 x, y;
-                        e4m3x16_f16(kraw[n], x, y);
-                        const uint32_t at = sk + (HD == 128 ? (g & 1) * Lay::k_block + (g >> 1) * 1024 : g * 1024);
-                        st_shared(at + at0, x);
-                        st_shared(at + at1, y);
+                        const int g = w + n * kOpWarps;
+                        if (g < NG) x[n] = ld_shared(raw + (HD == 128 ? (g >> 1) * 1024 + r8 * 128 + (((g & 1) ^ half) << 6) : g * 512 + r8 * 64) + 16 * cq);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        const int g = w + n * kOpWarps;
+                        if (g < NG) put_f16(sk + (HD == 128 ? ((g & 1) ^ half) * Lay::k_block + (g >> 1) * 1024 : g * 1024), x[n]);
                     }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_one(k_full(b));
-                if (kt >= sq.ntiles) {
-                    // (The entry is checked before the loads below are issued: a wait
-                    // for it would wait for them too.)
-                    next_blk = k_blk;
-                    next_held = k_held;
-                    k_blk = block_of(checked(after), k_held);
-                    if (kt + 1 < u.k1) load_k();
-                    after = entry(kt + 2);
-                }
+                if (kt >= sq.ntiles) read();
             };
             auto v_tile = [&](int kt, int it) {
                 const int b = it & 1, use = it >> 1;
                 const uint32_t sv = sm + Lay::v_off + b * Lay::v_bytes;
-                if (use > 0) ok = __all_sync(0xffffffffu, mbar_wait(v_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
+                if (use > 0) ok = __all_sync(0xffffffffu, bar_wait(v_empty(b), (use - 1) & 1, err, LA_KV8_TIMEOUT));
                 if (!ok) return;
                 if (kt < sq.ntiles) {
                     // Two new rows of eight dims at a time, transposed.  A NaN or
                     // infinity counts 0 here and is added at the end for the
                     // rows that see it.
-                    ok = __all_sync(0xffffffffu, mbar_wait(m_full(it & 3), it >> 2 & 1, err, LA_KV8_TIMEOUT));
+                    ok = __all_sync(0xffffffffu, bar_wait(m_full(it & 3), it >> 2 & 1, err, LA_KV8_TIMEOUT));
                     if (!ok) return;
                     const float fv = power_of(-meta[it & 3].vx[0]);
                     const int key0 = kt * kTileK, nkeys = min(kTileK, sq.rows - key0);
@@ -1098,39 +1083,35 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                         }
                     }
                 } else {
+                    const uint32_t raw = landed();
+                    if (!ok) return;
+                    uint4 x[NR];
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) {
+                        const int g = kOpWarps - 1 - w + n * kOpWarps;
+                        if (g < NG) x[n] = ld_shared(raw + (g & 1 ? v_at1 : v_at0) + (g >> 1) * (8 << p.page_log2));
+                    }
                     // Bytes behind the last token, and of missing pages, may be anything.
-                    const int key0 = (kt - sq.ntiles) * kTileK;
-                    if (sq.len - key0 < kTileK || v_held != 15u) {
+                    const int4 live = *reinterpret_cast<const int4 *>(head[slot].live);
+                    if ((live.x & live.y & live.z & live.w) != 32) {
 #pragma unroll
                         for (int n = 0; n < NR; ++n) {
-                            const int ch = cq + 4 * (v_group(n) & 1), live = v_held >> (ch >> 1) & 1u ? sq.len - key0 - 16 * ch : 0;
+                            const int ch = cq + 4 * (((kOpWarps - 1 - w + n * kOpWarps) & 1) ^ vhalf), keys = head[slot].live[ch >> 1] - 16 * (ch & 1);
                             auto cut = [](uint32_t a, int m) { return m >= 4 ? a : m <= 0 ? 0u : a & ((1u << (8 * m)) - 1u); };
-                            vraw[n] = make_uint4(cut(vraw[n].x, live), cut(vraw[n].y, live - 4), cut(vraw[n].z, live - 8), cut(vraw[n].w, live - 12));
+                            x[n] = make_uint4(cut(x[n].x, keys), cut(x[n].y, keys - 4), cut(x[n].z, keys - 8), cut(x[n].w, keys - 12));
                         }
                     }
 #pragma unroll
                     for (int n = 0; n < NR; ++n) {
-                        const int g = v_group(n);
-                        if (g >= NG) break;
-                        uint4 x, y;
-                        e4m3x16_f16(vraw[n], x, y);
-                        const uint32_t at = sv + (g & 1) * Lay::v_block + (g >> 1) * 1024;
-                        st_shared(at + at0, x);
-                        st_shared(at + at1, y);
+                        const int g = kOpWarps - 1 - w + n * kOpWarps;
+                        if (g < NG) put_f16(sv + ((g & 1) ^ vhalf) * Lay::v_block + (g >> 1) * 1024, x[n]);
                     }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_one(v_full(b));
-                if (kt >= sq.ntiles && kt + 1 < u.k1) {
-                    load_v(next_blk);
-                    v_held = next_held;
-                }
+                if (kt >= sq.ntiles) read();
             };
-            if (c_first < u.k1) {
-                load_k();
-                load_v(k_blk);
-            }
             // K a tile ahead of V: S of the next tile is issued before O of this one.
             const int first = it;
 #pragma unroll 1
@@ -1140,66 +1121,130 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             }
             it = first + max(u.k1 - u.k0, 0);
         }
+    } else if (warp == kLoadWarp) {
+        // ================================================ bytes
+        // Stages in the order in which they are read: K of a tile, V of the tile before.
+        const uint32_t bytes = static_cast<uint32_t>(c.page) * HD;                        // a page's block, of K or V
+        const uint32_t starts = c.page == 32 ? 15u : c.page == 64 ? 5u : 1u;              // lanes whose keys begin a page
+        int slot = 0;
+        uint32_t phase = 0, staged = 0;
+        // Lane l < 4: block number of keys 32 l .. of a tile (a block is 2 KB at
+        // least, so 32 bits reach all memory), and which lanes have one.
+        auto block_of = [&](int page, uint32_t &held) {
+            held = __ballot_sync(0xffffffffu, page >= 0) & 15u;
+            return static_cast<uint32_t>(kv8_block(c, p.a.layer, max(page, 0), u.head));
+        };
+        // Tile kt's K or V, with what its readers need to know of its pages.
+        auto stage = [&](const void *pool, int kt, uint32_t blk, uint32_t held, float ks, float vs) {
+            if (staged >= Lay::raw_slots) ok = __all_sync(0xffffffffu, bar_wait(raw_empty(slot), phase ^ 1, err, LA_KV8_TIMEOUT));
+            if (!ok) return;
+            if (lane < 4) {
+                const bool have = held >> lane & 1u;
+                head[slot].kf[lane] = have ? ks : 1.f;
+                head[slot].vx[lane] = have ? exponent_of(vs) : 0;
+                head[slot].live[lane] = have ? min(max(u.sq.len - (kt - u.sq.ntiles) * kTileK - 32 * lane, 0), 32) : 0;
+                if (lane == 0) head[slot].odd = 0;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(raw_full(slot), __popc(held & starts) * bytes);
+            __syncwarp();
+            if (held & starts & 1u << lane)
+                bulk_load(sm + Lay::raw_off + slot * Lay::raw_bytes + (lane >> (p.page_log2 - 5)) * bytes,
+                          static_cast<const uint8_t *>(pool) + static_cast<uint64_t>(blk) * bytes, bytes, raw_full(slot));
+            __syncwarp();
+            ++staged;
+            if (++slot == Lay::raw_slots) {
+                slot = 0;
+                phase ^= 1;
+            }
+        };
+        while (ok && kv8_next_call(p, tiles, walk, u)) {
+            const int c_first = max(u.k0, u.sq.ntiles);   // first cached tile of this piece
+            if (c_first >= u.k1) continue;
+            uint32_t held = 0, v_held = 0, v_blk = 0, blk = block_of(checked(entry(c_first)), held);
+            int after = entry(c_first + 1);
+            float ks = c.k_scale[blk], vs = c.v_scale[blk];
+#pragma unroll 1
+            for (int kt = c_first; ok && kt <= u.k1; ++kt) {
+                if (kt < u.k1) stage(c.k, kt, blk, held, ks, vs);
+                if (ok && kt > c_first) stage(c.v, kt - 1, v_blk, v_held, 1.f, 1.f);
+                v_blk = blk;
+                v_held = held;
+                blk = block_of(checked(after), held);   // entries and scales are read a tile ahead
+                ks = c.k_scale[blk];
+                vs = c.v_scale[blk];
+                after = entry(kt + 2);
+            }
+        }
+        // The last copies have landed (where a wait gave up, nobody else has seen that).
+        for (uint32_t n = min(staged, static_cast<uint32_t>(Lay::raw_slots)); n > 0; --n) {
+            slot = slot == 0 ? Lay::raw_slots - 1 : slot - 1;
+            if (slot == Lay::raw_slots - 1) phase ^= 1;
+            bar_wait(raw_full(slot), phase, err, LA_KV8_TIMEOUT);
+        }
+        __syncwarp();
     } else if (warp == kMmaWarp) {
         // ================================================ products
         // The whole warp runs this loop; one elected lane issues.  (Inside a
         // branch on the lane's number each product took 90 cycles to issue.)
         if (!p.whole) {
             Kv8Walk w = walk;
-            const bool any = kv8_next(p, tiles, w, u);
+            const bool any = kv8_next_call(p, tiles, w, u);
             if (lane == 0) kv8_note(p, tiles, any, u);
         }
         constexpr uint32_t is = idesc_f16(kTileQ, kTileK), io = idesc_f16(kTileQ, HD);
-        auto wait = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, mbar_spin(bar, parity & 1, err, LA_KV8_TIMEOUT)); };
+        auto wait = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity & 1, err, LA_KV8_TIMEOUT)); };
         int units = 0;
-        auto product_o = [&](int j, bool begins) {
-            const int b = j & 1;
-            ok = wait(p_full(b), j >> 1) && wait(v_full(b), j >> 1);
-            if (!ok) return;
-            tc_fence_after();
-            const uint32_t sv = sm + Lay::v_off + b * Lay::v_bytes, pt = tmem + kColS + 128 * b, ot = tmem + kColO + 128 * b;
-            if (elect_one()) {
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb) {
-                    const uint64_t d = umma_desc_sw128(sv + kb * Lay::v_block);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) umma_ts(ot, pt + kb * 32 + k * 8, d + 2 * k, io, begins && !(kb | k) ? 0u : 1u);
-                }
-                umma_commit(v_empty(b));
-                umma_commit(o_full(b));
-            }
-            __syncwarp();
-        };
-        while (ok && kv8_next(p, tiles, walk, u)) {
+        while (ok && kv8_next_call(p, tiles, walk, u)) {
             if (u.k0 >= u.k1) continue;
             ok = wait(q_full, units);
             ++units;
-            const int first = it;
-            for (int kt = u.k0; ok && kt < u.k1; ++kt, ++it) {
-                const int b = it & 1;
-                ok = wait(k_full(b), it >> 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t sk = sm + Lay::k_off + b * Lay::k_bytes;
-                if (elect_one()) {
+            const int first = it, end = it + u.k1 - u.k0;
+#pragma unroll 1
+            for (; ok && it <= end; ++it) {   // S of tile `it`, then O of the one before
+                if (it < end) {
+                    const int b = it & 1;
+                    ok = wait(k_full(b), it >> 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sk = sm + Lay::k_off + b * Lay::k_bytes;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int db = 0; db < HD / 64; ++db) {
-                        const uint64_t d = umma_desc_sw128(sk + db * Lay::k_block), q = umma_desc_sw128(sm + Lay::q_off + db * Lay::k_block);
+                        for (int db = 0; db < HD / 64; ++db) {
+                            const uint64_t d = umma_desc_sw128(sk + db * Lay::k_block), q = umma_desc_sw128(sm + Lay::q_off + db * Lay::k_block);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) umma_bf16(tmem + kColS + 128 * b, q + 2 * k, d + 2 * k, is, (db | k) ? 1u : 0u);
+                            for (int k = 0; k < 4; ++k) umma_bf16(tmem + kColS + 128 * b, q + 2 * k, d + 2 * k, is, (db | k) ? 1u : 0u);
+                        }
+                        umma_commit(s_full(b));
+                        umma_commit(k_empty(b));
                     }
-                    umma_commit(s_full(b));
-                    umma_commit(k_empty(b));
+                    __syncwarp();
                 }
-                __syncwarp();
-                if (it > first) product_o(it - 1, it - 1 < first + 2);
+                if (it > first) {
+                    const int j = it - 1, b = j & 1;
+                    ok = wait(p_full(b), j >> 1) && wait(v_full(b), j >> 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t sv = sm + Lay::v_off + b * Lay::v_bytes, pt = tmem + kColS + 128 * b, ot = tmem + kColO + 128 * b;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kb = 0; kb < 2; ++kb) {
+                            const uint64_t d = umma_desc_sw128(sv + kb * Lay::v_block);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) umma_ts(ot, pt + kb * 32 + k * 8, d + 2 * k, io, j < first + 2 && !(kb | k) ? 0u : 1u);
+                        }
+                        umma_commit(v_empty(b));
+                        umma_commit(o_full(b));
+                    }
+                    __syncwarp();
+                }
             }
-            if (ok) product_o(it - 1, it - 1 < first + 2);
+            it = end;
         }
         if (!ok) {   // void: wait (bounded) for the products in flight
             if (elect_one()) umma_commit(drain);
             __syncwarp();
-            mbar_spin(drain, 0, err, LA_KV8_TIMEOUT);
+            bar_wait(drain, 0, err, LA_KV8_TIMEOUT);
         }
         __syncwarp();
     } else {
@@ -1207,11 +1252,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         const int grp = warp >> 2, row = 32 * (warp & 3) + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + kColS + 128 * grp, to = tmem + lanes + kColO + 128 * grp;
-        float2 *ml = reinterpret_cast<float2 *>(smem + Lay::ml_off);
         float *qfs = reinterpret_cast<float *>(smem + Lay::qf_off);
         int *odds = reinterpret_cast<int *>(smem + Lay::odd_off);
         int units = 0;
-        while (ok && kv8_next(p, tiles, walk, u)) {
+        while (ok && kv8_next_call(p, tiles, walk, u)) {
             const Kv8Seq sq = u.sq;
             const bool in = row < u.nqv, idle = row - lane >= u.nqv;   // idle: none of this warp's rows is in use
             const int qv = u.qv0 + row, myrow = in ? qv / p.gq : 0, myhead = u.head * p.gq + (in ? qv % p.gq : 0);
@@ -1259,7 +1303,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_one(q_full);
-                ok = __all_sync(0xffffffffu, mbar_wait(q_full, units & 1, err, LA_KV8_TIMEOUT));
+                ok = __all_sync(0xffffffffu, bar_wait(q_full, units & 1, err, LA_KV8_TIMEOUT));
                 if (!ok) break;
                 qf = idle ? 0.f : qfs[row];
             }
@@ -1267,7 +1311,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             bool odd = false;
             for (int kt = u.k0 + ((first ^ grp) & 1); kt < u.k1; kt += 2) {
                 const int i = first + kt - u.k0, b = grp;   // tile number, of this group's parity
-                ok = mbar_spin(s_full(b), i >> 1 & 1, err, LA_KV8_TIMEOUT) && mbar_spin(m_full(i & 3), i >> 2 & 1, err, LA_KV8_TIMEOUT);
+                ok = bar_wait(s_full(b), i >> 1 & 1, err, LA_KV8_TIMEOUT) && bar_wait(m_full(i & 3), i >> 2 & 1, err, LA_KV8_TIMEOUT);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
@@ -1334,7 +1378,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                                 tmem_st_32x32b_x16(ts + 16 * q, w);
                             }
                             if (i >= first + 2) {   // this group's O holds its tile i - 2
-                                ok = __all_sync(0xffffffffu, mbar_wait(o_full(b), (i - 2) >> 1 & 1, err, LA_KV8_TIMEOUT));
+                                ok = __all_sync(0xffffffffu, bar_wait(o_full(b), (i - 2) >> 1 & 1, err, LA_KV8_TIMEOUT));
                                 if (!ok) break;
                                 tc_fence_after();
                                 for (int q = 0; q < HD / 16; ++q) {
@@ -1374,18 +1418,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             if (first < end) {
                 // Both groups' maxima and sums, once all products are done; then
                 // each group writes half of the dims.
-                ml[grp * kTileQ + row] = make_float2(m, l);
+                tmem_st_pair(ts + kTileK / 2, m, l);
+                tmem_st_wait();
+                tc_fence_before();
                 if (lane == 0 && (warp & 3) == 0) odds[grp] = odd;
                 __syncwarp();
                 if (lane == 0) mbar_arrive_one(e_full);
-                ok = mbar_wait(e_full, units & 1, err, LA_KV8_TIMEOUT) &&
-                     mbar_wait(o_full((end - 1) & 1), (end - 1) >> 1 & 1, err, LA_KV8_TIMEOUT) &&
-                     (end - first < 2 || mbar_wait(o_full(end & 1), (end - 2) >> 1 & 1, err, LA_KV8_TIMEOUT));
+                ok = bar_wait(e_full, units & 1, err, LA_KV8_TIMEOUT) &&
+                     bar_wait(o_full((end - 1) & 1), (end - 1) >> 1 & 1, err, LA_KV8_TIMEOUT) &&
+                     (end - first < 2 || bar_wait(o_full(end & 1), (end - 2) >> 1 & 1, err, LA_KV8_TIMEOUT));
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
                 ++units;
-                const float2 x = ml[row], y = ml[kTileQ + row];
+                const float2 x = tmem_ld_pair(tmem + lanes + kColS + kTileK / 2), y = tmem_ld_pair(tmem + lanes + kColS + 128 + kTileK / 2);
                 odd = (odds[0] | odds[1]) != 0;
                 M = fmaxf(x.x, y.x);
                 fa = x.y == 0.f ? 0.f : ex2(x.x - M);
