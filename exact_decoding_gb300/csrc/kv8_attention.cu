@@ -45,6 +45,8 @@ struct Kv8Args {
     int page_log2;
     int q_tile;        // query vectors per unit
     int k_tile, n_tile;   // cached tokens, new rows per key tile (0: the new rows are not counted in tiles)
+    int unit_cost;     // what a unit costs beside its key tiles, in tiles
+    int snap;          // a share that begins within this many tiles of a unit's begin begins with the unit
     int whole;         // 1: worker w runs units w, w + workers, ... whole, and nothing is joined
     int workers;
     float scale_log2;  // scale * log2(e)
@@ -61,17 +63,15 @@ struct Kv8Split {
 };
 
 // ------------------------------------------------------------------ work list
-constexpr int kUnitCost = 4;
-
 struct Kv8Seq {
     int first, rows;         // rows of the slot
     int len;                 // cached tokens
     int qtiles;              // tiles of query vectors
     int ctiles, ntiles;      // key tiles of the cache and of the new rows
-    // A unit's length in the flattened list: its key tiles behind kUnitCost
+    // A unit's length in the flattened list: its key tiles behind unit_cost
     // empty ones, which stand for what a unit costs beside its tiles (its
     // queries, the first copies' latency, the join of the warps).
-    __device__ int ktiles() const { return kUnitCost + ctiles + ntiles; }
+    int ktiles;
 };
 
 __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Args &p, int s) {
@@ -81,6 +81,7 @@ __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Args &p, int s) {
     q.qtiles = static_cast<int>((static_cast<long long>(q.rows) * p.gq + p.q_tile - 1) / p.q_tile);
     q.ctiles = (q.len + p.k_tile - 1) / p.k_tile;
     q.ntiles = p.a.k && p.n_tile ? (q.rows + p.n_tile - 1) / p.n_tile : 0;
+    q.ktiles = p.unit_cost + q.ctiles + q.ntiles;
     return q;
 }
 
@@ -92,7 +93,7 @@ __device__ __forceinline__ void kv8_plan(const Kv8Args &p, long long *tiles, lon
     long long mine = 0;
     for (int s = s0; s < s1; ++s) {
         const Kv8Seq q = kv8_seq(p, s);
-        const long long t = static_cast<long long>(q.qtiles) * p.c.n_kv_heads * q.ktiles();
+        const long long t = static_cast<long long>(q.qtiles) * p.c.n_kv_heads * q.ktiles;
         tiles[s + 1] = t;
         mine += t;
     }
@@ -139,11 +140,21 @@ __device__ __forceinline__ long long kv8_share(long long total, int w, int worke
 struct Kv8Walk {
     long long at, end, skip;
 };
-__device__ __forceinline__ Kv8Walk kv8_walk(const Kv8Args &p, long long total) {
-    const int workers = kv8_workers(p, total), b = static_cast<int>(blockIdx.x);
+// With snap = unit_cost - 1 a share that begins in a unit's empty tiles begins
+// with the unit: a piece without key tiles would cost as much as one with some.
+__device__ __forceinline__ Kv8Walk kv8_walk(const Kv8Args &p, const long long *tiles) {
+    const long long total = tiles[p.c.n_seqs];
+    const int workers = kv8_workers(p, total), b = static_cast<int>(blockIdx.x), w = b + (threadIdx.x & 1);
     if (p.whole) return {0, total, b};
     if (b >= workers) return {0, 0, 0};
-    return {kv8_share(total, b, workers), kv8_share(total, b + 1, workers), 0};
+    long long at = kv8_share(total, w, workers);   // even lanes: where the share begins, odd ones: where it ends
+    if (p.snap > 0 && w < workers) {
+        const int s = kv8_find(tiles, p.c.n_seqs, at), kt = kv8_seq(p, s).ktiles;
+        const long long in_slot = at - tiles[s];
+        const int in_unit = static_cast<int>(in_slot - kv8_div(in_slot, kt) * kt);
+        if (in_unit <= p.snap) at -= in_unit;
+    }
+    return {__shfl_sync(0xffffffffu, at, 0), __shfl_sync(0xffffffffu, at, 1), 0};
 }
 struct Kv8Piece {
     int s, head, qv0, nqv;
@@ -155,7 +166,7 @@ __device__ __forceinline__ bool kv8_next(const Kv8Args &p, const long long *tile
     while (w.at < w.end) {
         u.s = kv8_find(tiles, p.c.n_seqs, w.at);
         u.sq = kv8_seq(p, u.s);
-        const int kt = u.sq.ktiles();
+        const int kt = u.sq.ktiles;
         if (p.whole) {
             const long long units = kv8_div(tiles[u.s + 1] - w.at, kt);   // of this slot from `at` on
             if (w.skip >= units) {
@@ -168,8 +179,8 @@ __device__ __forceinline__ bool kv8_next(const Kv8Args &p, const long long *tile
         }
         const int unit = static_cast<int>(kv8_div(w.at - tiles[u.s], kt)), v0 = static_cast<int>(w.at - tiles[u.s] - static_cast<long long>(unit) * kt);
         const int v1 = static_cast<int>(min(static_cast<long long>(kt), v0 + (w.end - w.at)));
-        u.k0 = max(v0 - kUnitCost, 0);
-        u.k1 = max(v1 - kUnitCost, 0);
+        u.k0 = max(v0 - p.unit_cost, 0);
+        u.k1 = max(v1 - p.unit_cost, 0);
         u.all = v0 == 0 && v1 == kt;
         u.begins = v0 == 0;
         u.head = unit / u.sq.qtiles;
@@ -187,7 +198,7 @@ __device__ __forceinline__ void kv8_note(const Kv8Args &p, const long long *tile
     x.total = tiles[p.c.n_seqs];
     x.inside = any && !u.begins;
     if (x.inside) {
-        const int kt = u.sq.ktiles();
+        const int kt = u.sq.ktiles;
         const int unit = u.head * u.sq.qtiles + u.qv0 / p.q_tile;
         x.t0 = tiles[u.s] + static_cast<long long>(unit) * kt;
         x.t1 = x.t0 + kt;
@@ -355,7 +366,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
     fence_barrier_init();
     pdl_wait();
     kv8_plan(p, tiles, reinterpret_cast<long long *>(smem + Lay::sum_off));
-    Kv8Walk walk = kv8_walk(p, tiles[c.n_seqs]);
+    Kv8Walk walk = kv8_walk(p, tiles);
     Kv8Piece u;
     int in_slot = 0, out_slot = 0;   // ring positions: the next block to load, the next to read
     uint32_t out_phase = 0;
@@ -869,7 +880,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     tc_fence_after();
     pdl_trigger();
     const uint32_t tmem = *tmem_slot;
-    Kv8Walk walk = kv8_walk(p, tiles[c.n_seqs]);
+    Kv8Walk walk = kv8_walk(p, tiles);
     Kv8Piece u{};
     int it = 0;          // key tiles so far, the same count in every role: buffer it & 1, its use it >> 1
     bool ok = true;
@@ -1518,7 +1529,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv8_join(const __grid_constant
     const int workers = kv8_workers(p, x.total);
     int w0 = border - 1, w1 = border;   // first and last worker with a piece
 #pragma unroll 1
-    while (kv8_share(x.total, w0, workers) > x.t0) --w0;
+    while (kv8_share(x.total, w0, workers) > x.t0 + p.snap) --w0;
 #pragma unroll 1
     while (w1 + 1 < workers && kv8_share(x.total, w1 + 1, workers) < x.t1) ++w1;
     const int items = x.nqv * (HD / 4), share = border - w0 - 1, shares = w1 - w0;
@@ -1560,6 +1571,12 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv8_join(const __grid_constant
 }
 
 // ------------------------------------------------------------------ launch
+// What a unit costs beside its key tiles, in tiles.  k_kv8_rows: 64 sequences of up
+// to 8192 tokens, 8 KV heads: 119.0 us with 4, 99.4 with 10, 95.4 with 13, 95.3
+// with 16, 98.8 with 26; 48 of up to 1500, head_dim 64, 4 KV heads: 20.5 with 4,
+// 16.4 with 13, 17.4 with 26.  k_kv8_tiles (256 rows over 16k tokens): 121.3 with
+// 2, 118.6 with 4, 118.2 with 6.
+constexpr int kRowsUnitCost = 14, kTilesUnitCost = 4;
 constexpr int kRowsPerSm = 4;   // most CTAs of k_kv8_rows per SM
 
 int64_t kv8_workspace_bytes(const la_kv8_cache &c, int nsm) {
@@ -1587,6 +1604,8 @@ static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     p.q_tile = kRowsQ;
     p.k_tile = PAGE;
     p.n_tile = 0;
+    p.unit_cost = kRowsUnitCost;
+    p.snap = p.unit_cost - 1;
     const long long units = ((static_cast<long long>(p.a.n_rows) * p.gq) / kRowsQ + p.c.n_seqs) * p.c.n_kv_heads;   // at most
     const long long tiles = (p.a.max_len + PAGE - 1) / PAGE;
     // A unit of at most two tiles per warp is not worth splitting: its pieces
@@ -1615,6 +1634,8 @@ static cudaError_t tiles_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     using Lay = Tiles<HD>;
     p.q_tile = kTileQ;
     p.k_tile = p.n_tile = kTileK;
+    p.unit_cost = kTilesUnitCost;
+    p.snap = 0;   // finding the unit costs more than an empty piece (121 rows over 2k tokens, 32 heads: 34.4 us against 33.1)
     const long long units = ((static_cast<long long>(p.a.n_rows) * p.gq) / kTileQ + p.c.n_seqs) * p.c.n_kv_heads;   // at most
     const long long tiles = (p.a.max_len + kTileK - 1) / kTileK + (p.a.k ? (p.a.max_rows + kTileK - 1) / kTileK : 0);
     p.whole = tiles <= 2;   // as for k_kv8_rows
