@@ -621,6 +621,8 @@ class Decoder:
         if kv_cache is None:
             self.h = la_create(self.weights.dims_struct, self.weights.struct, o)
         else:
+            if kv_cache.device.type == "cuda" and stream is not None:   # the cache's tensors are written on the current one
+                stream.wait_stream(kv_cache._torch.cuda.current_stream(kv_cache.device))
             self.h = la_create_kv8(self.weights.dims_struct, self.weights.struct, o, kv_cache.struct, slot)
 
     def prefill(self, prompt) -> int:

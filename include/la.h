@@ -495,7 +495,8 @@ int la_kv8_status(const la_kv8_cache *c, uint32_t *bits, void *stream);
  * copies the struct, not the arrays: they outlive it, and table, lens and refs
  * stay where they are (la_kv8_compact in place is fine between calls).  A
  * step's own rows meet the attention at 16 bits; the cached ones are e4m3, so
- * tokens may differ from those of la_create's cache.  la_prefill and
+ * tokens may differ from those of la_create's cache.  A slot serves one
+ * decoder; what it holds before la_prefill does not matter: la_prefill and
  * la_import_state empty the slot first; la_destroy leaves it as it is (free it
  * with la_kv8_free).  Calls on decoders that share a cache must not overlap,
  * nor overlap other la_kv8 calls on it.

@@ -411,3 +411,51 @@ def test_refused_forks(lib):
     with pytest.raises(lib.LaError):
         cache.status()
     model.same_as(cache)
+
+
+@pytest.mark.parametrize("hd,page,heads,kv,lens,rows", [
+    (128, 32, 4, 2, [2600], [150]),                 # many query vectors: a long cache over many workers
+    (64, 128, 8, 2, [3000, 40], [70, 3]),
+    (128, 64, 4, 2, [500, 0, 77], [300, 5, 129]),   # several key tiles of new rows before the cached ones
+    (64, 32, 2, 1, [129, 700, 64, 0], [257, 1, 128, 384]),
+    (128, 128, 2, 1, [1000], [1100])])
+def test_attention_of_many_rows(lib, hd, page, heads, kv, lens, rows):
+    cache = build(lib, lens, hd, page, kv, seed=len(lens) + hd)
+    n = sum(rows)
+    q, k, v = normal((n, heads, hd), 4, 1.5), normal((n, kv, hd), 5), normal((n, kv, hd), 6)
+    out = cache.attention(q, k, v, row_start=starts(rows))
+    close(out, *M.attention(cache, q, k, v, rows))
+    cache.status()
+
+
+@pytest.mark.parametrize("hd,page,kv", [(64, 32, 2), (128, 64, 1)])
+def test_many_short_sequences_and_few_long_ones(lib, hd, page, kv):
+    """More units than a worker's share is long: shares begin with units, some workers get none."""
+    g = np.random.default_rng(5)
+    lens = [int(x) for x in g.integers(0, 70, 200)]
+    lens[3], lens[120], lens[121] = 2500, 1700, 0
+    cache = build(lib, lens, hd, page, kv, seed=3)
+    q, k, v = normal((200, 2 * kv, hd), 7, 1.5), normal((200, kv, hd), 8), normal((200, kv, hd), 9)
+    out = cache.attention(q, k, v)
+    close(out, *M.attention(cache, q, k, v, [1] * 200))
+    cache.status()
+
+
+@pytest.mark.parametrize("rows", [1, 60])
+@pytest.mark.parametrize("page", [32, 64, 128])
+def test_keys_of_missing_pages_do_not_count(lib, rows, page):
+    """Few and many query vectors: the keys of a page number outside the pool are left out, its neighbours' are right."""
+    lens = [5 * page + 7, 3 * page]
+    cache, whole = (build(lib, lens, 128, page, 2, seed=11) for _ in range(2))
+    cache.table[0, 1] = cache.n_pages + 5
+    cache.table[0, 4] = -7
+    q, k, v = normal((2 * rows, 4, 128), 1), normal((2 * rows, 2, 128), 2), normal((2 * rows, 2, 128), 3)
+    out = cache.attention(q, k, v, row_start=starts([rows, rows]))
+    # the same keys without those pages: the later ones move up (their order does not matter)
+    for j, p in enumerate([0, 2, 3, 5]):
+        whole.table[0, j] = cache.table[0, p]
+    whole.lens[0] = 3 * page + 7
+    close(out, *M.attention(whole, q, k, v, [rows, rows]))
+    with pytest.raises(lib.LaError) as e:
+        cache.status()
+    assert e.value.code == STATE

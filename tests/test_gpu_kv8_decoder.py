@@ -383,3 +383,26 @@ def test_fork_refuses(lib):
     a.step()
     for d in (a, twin, far, n5, small, plain):
         d.close()
+
+
+def test_a_stream_of_its_own(lib):
+    """On another stream than the cache was made on; two decoders, two streams, calls in turn."""
+    dims = SMALL["gqa-hd128"]
+    dev = lib.DeviceWeights(weights("gqa-hd128", 5))
+    p = synth.uniform_tokens(60, dims.vocab, seed=6)
+    alone = lib.Decoder(dev, 4, 5, 4, 256, kv_cache=new_cache(lib, dims, 64, max_seq=256))
+    alone.prefill(p)
+    want = run(alone, 5)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    cache = new_cache(lib, dims, 64, max_seq=256)
+    decs = [lib.Decoder(dev, 4, 5, 4, 256, kv_cache=cache, slot=i, stream=s) for i, s in enumerate(streams)]
+    for d in decs:
+        d.prefill(p)
+    got = [[], []]
+    for _ in range(5):
+        for i, d in enumerate(decs):
+            got[i] += run(d, 1)
+    same(got[0], want)
+    same(got[1], want)
+    for d in (alone, *decs):
+        d.close()
