@@ -70,7 +70,8 @@ struct Kv8Seq {
     int ctiles, ntiles;      // key tiles of the cache and of the new rows
     // A unit's length in the flattened list: its key tiles behind unit_cost
     // empty ones, which stand for what a unit costs beside its tiles (its
-    // queries, the first copies' latency, the join of the warps).
+    // queries, the first copies' latency, the join of the warps).  Where units
+    // stay whole the list is one of units.
     int ktiles;
 };
 
@@ -81,7 +82,7 @@ __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Args &p, int s) {
     q.qtiles = static_cast<int>((static_cast<long long>(q.rows) * p.gq + p.q_tile - 1) / p.q_tile);
     q.ctiles = (q.len + p.k_tile - 1) / p.k_tile;
     q.ntiles = p.a.k && p.n_tile ? (q.rows + p.n_tile - 1) / p.n_tile : 0;
-    q.ktiles = p.unit_cost + q.ctiles + q.ntiles;
+    q.ktiles = p.whole ? 1 : p.unit_cost + q.ctiles + q.ntiles;
     return q;
 }
 
@@ -138,15 +139,15 @@ __device__ __forceinline__ long long kv8_share(long long total, int w, int worke
 
 // The pieces of work of one worker, in order.
 struct Kv8Walk {
-    long long at, end, skip;
+    long long at, end;
 };
 // With snap = unit_cost - 1 a share that begins in a unit's empty tiles begins
 // with the unit: a piece without key tiles would cost as much as one with some.
 __device__ __forceinline__ Kv8Walk kv8_walk(const Kv8Args &p, const long long *tiles) {
     const long long total = tiles[p.c.n_seqs];
     const int workers = kv8_workers(p, total), b = static_cast<int>(blockIdx.x), w = b + (threadIdx.x & 1);
-    if (p.whole) return {0, total, b};
-    if (b >= workers) return {0, 0, 0};
+    if (p.whole) return {b, total};
+    if (b >= workers) return {0, 0};
     long long at = kv8_share(total, w, workers);   // even lanes: where the share begins, odd ones: where it ends
     if (p.snap > 0 && w < workers) {
         const int s = kv8_find(tiles, p.c.n_seqs, at), kt = kv8_seq(p, s).ktiles;
@@ -154,7 +155,7 @@ __device__ __forceinline__ Kv8Walk kv8_walk(const Kv8Args &p, const long long *t
         const int in_unit = static_cast<int>(in_slot - kv8_div(in_slot, kt) * kt);
         if (in_unit <= p.snap) at -= in_unit;
     }
-    return {__shfl_sync(0xffffffffu, at, 0), __shfl_sync(0xffffffffu, at, 1), 0};
+    return {__shfl_sync(0xffffffffu, at, 0), __shfl_sync(0xffffffffu, at, 1)};
 }
 struct Kv8Piece {
     int s, head, qv0, nqv;
@@ -163,33 +164,30 @@ struct Kv8Piece {
     Kv8Seq sq;
 };
 __device__ __forceinline__ bool kv8_next(const Kv8Args &p, const long long *tiles, Kv8Walk &w, Kv8Piece &u) {
-    while (w.at < w.end) {
-        u.s = kv8_find(tiles, p.c.n_seqs, w.at);
-        u.sq = kv8_seq(p, u.s);
-        const int kt = u.sq.ktiles;
-        if (p.whole) {
-            const long long units = kv8_div(tiles[u.s + 1] - w.at, kt);   // of this slot from `at` on
-            if (w.skip >= units) {
-                w.skip -= units;
-                w.at = tiles[u.s + 1];
-                continue;
-            }
-            w.at += w.skip * kt;
-            w.skip = p.workers - 1;
-        }
-        const int unit = static_cast<int>(kv8_div(w.at - tiles[u.s], kt)), v0 = static_cast<int>(w.at - tiles[u.s] - static_cast<long long>(unit) * kt);
+    if (w.at >= w.end) return false;
+    u.s = kv8_find(tiles, p.c.n_seqs, w.at);
+    u.sq = kv8_seq(p, u.s);
+    const int kt = u.sq.ktiles;
+    const long long in_slot = w.at - tiles[u.s];
+    const int unit = static_cast<int>(kv8_div(in_slot, kt));
+    if (p.whole) {
+        u.k0 = 0;
+        u.k1 = u.sq.ctiles + u.sq.ntiles;
+        u.all = u.begins = true;
+        w.at += p.workers;
+    } else {
+        const int v0 = static_cast<int>(in_slot - static_cast<long long>(unit) * kt);
         const int v1 = static_cast<int>(min(static_cast<long long>(kt), v0 + (w.end - w.at)));
         u.k0 = max(v0 - p.unit_cost, 0);
         u.k1 = max(v1 - p.unit_cost, 0);
         u.all = v0 == 0 && v1 == kt;
         u.begins = v0 == 0;
-        u.head = unit / u.sq.qtiles;
-        u.qv0 = (unit % u.sq.qtiles) * p.q_tile;
-        u.nqv = min(p.q_tile, u.sq.rows * p.gq - u.qv0);
         w.at += v1 - v0;
-        return true;
     }
-    return false;
+    u.head = unit / u.sq.qtiles;
+    u.qv0 = (unit % u.sq.qtiles) * p.q_tile;
+    u.nqv = min(p.q_tile, u.sq.rows * p.gq - u.qv0);
+    return true;
 }
 
 // Worker b's entry for k_kv8_join, by one thread: `inside` if its first piece u does not begin its unit.
@@ -1597,6 +1595,11 @@ static bool attrs_needed(const std::atomic<unsigned long long> &mask, unsigned l
     return !(mask.load() & *bit);
 }
 
+// Units of the call, at most.
+static long long unit_bound(const Kv8Args &p) {
+    return (static_cast<long long>(p.a.n_rows) * p.gq + static_cast<long long>(p.q_tile - 1) * p.c.n_seqs) / p.q_tile * p.c.n_kv_heads;
+}
+
 template <int HD, int PAGE>
 static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     using Lay = Rows<HD, PAGE>;
@@ -1606,11 +1609,14 @@ static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     p.n_tile = 0;
     p.unit_cost = kRowsUnitCost;
     p.snap = p.unit_cost - 1;
-    const long long units = ((static_cast<long long>(p.a.n_rows) * p.gq) / kRowsQ + p.c.n_seqs) * p.c.n_kv_heads;   // at most
-    const long long tiles = (p.a.max_len + PAGE - 1) / PAGE;
-    // A unit of at most two tiles per warp is not worth splitting: its pieces
-    // would cost a second kernel.
-    p.whole = tiles <= 2 * Lay::warps;
+    const long long units = unit_bound(p), tiles = (p.a.max_len + PAGE - 1) / PAGE;
+    // Splitting a unit costs a second kernel and the pieces' way through memory.
+    // One row of 64 heads over 8 KV heads, pages of 64, whole against split: 13
+    // tiles 13.1 us against 14.5, 32 tiles 19.9 against 19.3; 16 such sequences
+    // 15.1 against 17.5 and 24.6 against 22.7; 32 KV heads 12.9 against 12.3 and
+    // 19.6 against 14.1; 48 sequences, head_dim 64, 4 KV heads, pages of 32: 16
+    // tiles 10.5 against 13.5, 47 tiles 19.2 against 16.7.
+    p.whole = tiles <= std::min(32, (256 << 10) / (2 * Lay::block));
     p.workers = p.whole ? static_cast<int>(std::min<long long>(units, 1 << 20)) : nsm * Lay::per_sm;
     p.part = static_cast<float *>(ws);
     p.part_ml = p.part + static_cast<long long>(nsm) * kRowsPerSm * 2 * kRowsQ * HD;
@@ -1636,9 +1642,12 @@ static cudaError_t tiles_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     p.k_tile = p.n_tile = kTileK;
     p.unit_cost = kTilesUnitCost;
     p.snap = 0;   // finding the unit costs more than an empty piece (121 rows over 2k tokens, 32 heads: 34.4 us against 33.1)
-    const long long units = ((static_cast<long long>(p.a.n_rows) * p.gq) / kTileQ + p.c.n_seqs) * p.c.n_kv_heads;   // at most
+    const long long units = unit_bound(p);
     const long long tiles = (p.a.max_len + kTileK - 1) / kTileK + (p.a.k ? (p.a.max_rows + kTileK - 1) / kTileK : 0);
-    p.whole = tiles <= 2;   // as for k_kv8_rows
+    // Splitting costs about five tiles' time (121 rows of 32 heads, whole against
+    // split: 6 tiles 26.4 us against 29.2, 9 tiles 32.1 against 29.5; four such
+    // sequences, which fill the SMs whole: 12 tiles 38.3 against 60.0).
+    p.whole = (units + nsm - 1) / nsm * tiles - units * (tiles + kTilesUnitCost) / nsm <= 5;
     p.workers = p.whole ? static_cast<int>(std::min<long long>(units, 1 << 20)) : nsm;
     p.part = static_cast<float *>(ws);
     p.part_ml = p.part + static_cast<long long>(nsm) * 2 * kTileQ * HD;

@@ -101,6 +101,7 @@ struct la_handle {
     int *slot_dev = nullptr, *rs_step = nullptr, *rs_pass = nullptr, *row_idx = nullptr, *stored = nullptr;
     __nv_bfloat16 *q8 = nullptr, *k8 = nullptr, *v8 = nullptr;
     void *kv8_ws = nullptr;
+    int kv8_len = 0;   // the steps' kernels are chosen for at most this many cached tokens
     float2 *rope = nullptr;
     int *amax = nullptr, *tok = nullptr, *depth = nullptr, *anc = nullptr, *anc_cnt = nullptr, *used = nullptr;
     unsigned *thr_key = nullptr;   // [U] sampling keep rule of each used row (top-k / top-p)
@@ -453,7 +454,7 @@ int forward(la_handle *h, Mode mode, const int *tok, int nrows, int P, bool want
             a.layer = l;
             a.n_heads = h->nh;
             a.n_rows = a.max_rows = nrows;
-            a.max_len = mode == STEP ? h->max_seq : std::max(P, 1);   // a step may replay from a captured graph
+            a.max_len = mode == STEP ? h->kv8_len : std::max(P, 1);   // a hint
             a.q_stride = a.out_stride = h->qd;
             a.k_stride = a.v_stride = h->kvd;
             a.row_start = mode == STEP ? h->rs_step : h->rs_pass;
@@ -1300,6 +1301,13 @@ static int la_step_body(la_handle *h, int32_t *out_tokens, int32_t *out_n) {
     if (h->P + h->M + h->N + 2 > h->max_seq) return fail(LA_ERR_CAPACITY, "max_seq reached");
     cudaStream_t s = h->stream;
     int rc;
+    // A step's graph holds kernels chosen for up to kv8_len cached tokens:
+    // behind that it is captured again, for twice as many.
+    if (h->kv8 && (h->P > h->kv8_len || 4 * h->P < h->kv8_len)) {
+        h->kv8_len = std::min(std::max(2 * h->P, 512), h->max_seq);
+        if (h->step_graph) cudaGraphExecDestroy(h->step_graph);
+        h->step_graph = nullptr;
+    }
     // The first step of a handle runs directly (one-time kernel attributes are
     // set outside any capture); later non-profiled steps replay a graph.
     if (h->bf16 && !h->prof_on && !h->graph_off && h->steps > 0 && !h->step_graph) capture_step(h);

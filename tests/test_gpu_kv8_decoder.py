@@ -211,6 +211,30 @@ def test_graph_replay_matches_direct_launches(lib):
     same(*outs)
 
 
+def test_graphs_follow_a_growing_and_a_new_prompt(lib):
+    """Steps past the length that the first graph was captured for, then a short
+    prompt again: the same tokens as without graphs, and logits bit for bit."""
+    dims = SMALL["mha-hd64"]
+    dev = lib.DeviceWeights(synth.model_weights(dims, 11))
+    p = synth.uniform_tokens(490, dims.vocab, 11, 5)
+    decs = [lib.Decoder(dev, 4, 5, 4, 1024, profile=prof, kv_cache=new_cache(lib, dims, 64)) for prof in (False, True)]
+    for d in decs:
+        d.prefill(p[:250])      # graphs for up to 512 tokens
+    n = 250
+    while n < 530:
+        a, b = (d.step() for d in decs)
+        assert a == b
+        n += len(a)
+        if n > 505:
+            assert np.array_equal(decs[0].debug_logits(), decs[1].debug_logits())
+    for m in (490, 30):
+        for d in decs:
+            d.prefill(p[:m])
+        same(run(decs[0], 3), run(decs[1], 3))
+    for d in decs:
+        d.close()
+
+
 @pytest.mark.parametrize("n", [64, 77])
 def test_fork_continues_like_its_source(lib, n):
     """A fork from a full page and from a partly filled one: both decoders, in
