@@ -207,7 +207,9 @@ constexpr int kStoreThreads = 256;
 
 // One CTA per (sequence, touched page, KV head, layer, K or V): the page's
 // new rows go through shared memory once, for the largest magnitude and then
-// for the bytes (V is transposed on the way).
+// for the bytes (V is transposed on the way).  Bound by memory: 2048 rows x 40
+// layers x 8 heads, 336 MB in and 168 MB out, take 113 us (4.5 TB/s); what is
+// missing is the time in which a CTA waits for its page and then writes it.
 template <int HD>
 __global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_kv8_rows r, const int4 *record, int touched) {
     pdl_trigger();
@@ -334,9 +336,16 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_
 // A decoding step appends a row or a few to each sequence: one warp per
 // (sequence, touched page, KV head, layer, K or V), a CTA for the heads of one
 // (sequence, page, layer).  A CTA per block, as above, spends its time on
-// launching and barriers for 256 bytes of input: 64 sequences x 32 layers x 8
-// heads took 129 us.
-constexpr int kFewRows = 8, kFewWarps = 8;
+// launching and barriers for 256 bytes of input.  What bounds it are V's bytes:
+// a token has one byte in each dim's row, so a sector of 32 bytes is read and
+// written for each (64 sequences x 32 layers x 8 heads, one row each: 33.9 us
+// and 205 MB for 16 MB of new bytes).
+// Against k_kv8_store, with la_kv8_free behind: 64 sequences, 1, 4 and 8 rows
+// 33.9 us, 85 and 150 against 91.5, 152 and 203; 32 sequences x 8 layers x 4 heads
+// 7.7, 11.2 and 14.9 against 11.1, 13.2 and 14.1; but 4 sequences x 32 layers x 8
+// heads 9.3, 21.5 and 36.7 against 11.3, 16.1 and 20.6: there each SM has a CTA at
+// most, and stored tokens that are rounded again occupy one warp instead of eight.
+constexpr int kFewRows = 8, kFewWarps = 8, kFewCtas = 256;
 
 template <int HD>
 __global__ void __launch_bounds__(32 * kFewWarps, 4) k_kv8_store_few(la_kv8_cache c, la_kv8_rows r, const int4 *record, int touched) {
@@ -359,7 +368,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 4) k_kv8_store_few(la_kv8_cach
     const int row0 = first + pj * c.page + a - len;
     const int bytes = c.page * HD;
     const long long blk0 = kv8_block(c, layer, to, 0), old0 = from >= 0 ? kv8_block(c, layer, from, 0) : 0;
-    for (int hv = threadIdx.x >> 5; hv < 2 * c.n_kv_heads; hv += blockDim.x >> 5) {
+    for (int hv = blockIdx.z * (blockDim.x >> 5) + (threadIdx.x >> 5); hv < 2 * c.n_kv_heads; hv += gridDim.z * (blockDim.x >> 5)) {
         const int isv = hv >= c.n_kv_heads, head = isv ? hv - c.n_kv_heads : hv;
         const long long blk = blk0 + head, old = old0 + head;
         float *scales = isv ? c.v_scale : c.k_scale;
@@ -459,8 +468,13 @@ cudaError_t kv8_append_launch(const la_kv8_cache &c, const la_kv8_rows &r, int *
     const int touched = kv8_touched(r.max_rows, c.page);
     const int4 *record = reinterpret_cast<const int4 *>(ws);
     const unsigned blocks = static_cast<unsigned>(c.n_seqs) * touched;
-    if (r.max_rows <= kFewRows) {
-        const dim3 grid(blocks, c.n_layers), block(32 * std::min(kFewWarps, 2 * c.n_kv_heads));
+    // At most this many (sequence, layer) have rows; below kFewCtas the SMs are not full.
+    const bool small = static_cast<int64_t>(std::min(c.n_seqs, r.n_rows)) * c.n_layers < kFewCtas;
+    if (r.max_rows == 1 || (r.max_rows <= kFewRows && !small)) {
+        // Not full: a warp for each head (1 sequence x 32 layers x 32 heads 9.3 us
+        // against 16.6); else the warps take several (64 sequences 33.9 against 39.2).
+        const int split = small ? (2 * c.n_kv_heads + kFewWarps - 1) / kFewWarps : 1;
+        const dim3 grid(blocks, c.n_layers, split), block(32 * std::min(kFewWarps, 2 * c.n_kv_heads));
         if (c.head_dim == 128) return launch_k(k_kv8_store_few<128>, grid, block, 0, s, c, r, record, touched);
         return launch_k(k_kv8_store_few<64>, grid, block, 0, s, c, r, record, touched);
     }
@@ -577,6 +591,7 @@ constexpr int kMoveThreads = 256;
 
 // Copies the pairs' pages, layer by layer, and rewrites the table and refs.
 // A (layer, page)'s K (or V) is one run of n_kv_heads * page * head_dim bytes.
+// Bound by memory: half of 500 pages x 32 layers x 8 heads in 383 us (5.6 TB/s).
 __global__ void __launch_bounds__(kMoveThreads) k_kv8_move(la_kv8_cache c, int *table_out, int *refs_out, const int *ws) {
     pdl_trigger();
     pdl_wait();

@@ -459,3 +459,25 @@ def test_keys_of_missing_pages_do_not_count(lib, rows, page):
     with pytest.raises(lib.LaError) as e:
         cache.status()
     assert e.value.code == STATE
+
+
+@pytest.mark.parametrize("hd,page,kv,most", [(64, 32, 1, 8), (128, 32, 3, 4), (128, 64, 5, 1), (64, 64, 6, 8)])
+def test_append_few_rows_to_many_sequences(lib, hd, page, kv, most):
+    """0 .. most rows for each of 130 sequences in two layers, three times over growing magnitudes: pages that fill
+    up, rows over two pages, stored tokens rounded again, shared last pages copied."""
+    g = np.random.default_rng(hd + most)
+    lens = [int(x) for x in g.integers(0, 2 * page, 130)]
+    cache = lib.Kv8Cache(2, 130 * 4, page, kv, hd, 133, 4)
+    M.fill(cache, lens + [0, 0, 0], 3)
+    model = M.Model(cache)
+    cache.fork(ints([4, 5, 6]), ints([130, 131, 132]))
+    model.fork([4, 5, 6], [130, 131, 132])
+    for turn in range(3):
+        rows = [int(x) for x in g.integers(0, most + 1, 133)]
+        rows[4] = rows[130] = most
+        n = sum(rows)
+        k, v = normal((2, n, kv, hd), 20 + turn, 3.0 ** turn), normal((2, n, kv, hd), 30 + turn, 5.0 ** turn)
+        want = model.append(k.cpu().double().numpy(), v.cpu().double().numpy(), rows)
+        assert cache.append(k, v, row_start=starts(rows), max_rows=most).tolist() == want
+        model.same_as(cache)
+    cache.status()
