@@ -203,13 +203,14 @@ __device__ __forceinline__ float kv8_finite_max(float m, uint32_t w) {
     return m;
 }
 
-constexpr int kStoreThreads = 256;
+constexpr int kStoreThreads = 128;
 
 // One CTA per (sequence, touched page, KV head, layer, K or V): the page's
 // new rows go through shared memory once, for the largest magnitude and then
 // for the bytes (V is transposed on the way).  Bound by memory: 2048 rows x 40
-// layers x 8 heads, 336 MB in and 168 MB out, take 113 us (4.5 TB/s); what is
-// missing is the time in which a CTA waits for its page and then writes it.
+// layers x 8 heads, 336 MB in and 168 MB out, take 91.5 us (5.5 TB/s) with 128
+// threads and 8 loads of each in flight; 256 threads, 4 loads: 109; 64 threads, 8
+// loads: 104.5; 256 threads, 8 loads: 131 (too few CTAs on an SM).
 template <int HD>
 __global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_kv8_rows r, const int4 *record, int touched) {
     pdl_trigger();
@@ -237,22 +238,23 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_
     auto place = [](int t, int d) { return t * HD + (t >> 4) * 16 + d; };
 
     uint32_t top = 0;
-    constexpr int C = HD / 8, B = 4;                               // 16-byte pieces of a row; loads in flight
-    for (int i0 = tid; i0 < (b - a) * C; i0 += B * kStoreThreads) {
+    constexpr int C = HD / 8, RT = kStoreThreads / C, B = 8;       // 16-byte pieces of a row; rows of a sweep; loads in flight
+    const int d0 = (tid % C) * 8;
+    for (int t0 = tid / C; t0 < b - a; t0 += B * RT) {
         uint4 w[B];
 #pragma unroll
         for (int k = 0; k < B; ++k) {
-            const int i = i0 + k * kStoreThreads, t = i / C, d = (i % C) * 8;
+            const int t = t0 + k * RT;
             w[k] = make_uint4(0, 0, 0, 0);
             if (t >= b - a) continue;
             const int row = r.row_idx ? r.row_idx[row0 + t] : row0 + t;
-            if (static_cast<unsigned>(row) < static_cast<unsigned>(n_src)) w[k] = *reinterpret_cast<const uint4 *>(x + row * stride + d);
+            if (static_cast<unsigned>(row) < static_cast<unsigned>(n_src)) w[k] = *reinterpret_cast<const uint4 *>(x + row * stride + d0);
             else atomicOr(c.status, LA_KV8_BAD);                   // stored as zeros
         }
 #pragma unroll
         for (int k = 0; k < B; ++k) {
-            const int i = i0 + k * kStoreThreads, t = i / C, d = (i % C) * 8;
-            if (t < b - a) *reinterpret_cast<uint4 *>(sm + place(a + t, d)) = w[k];
+            const int t = t0 + k * RT;
+            if (t < b - a) *reinterpret_cast<uint4 *>(sm + place(a + t, d0)) = w[k];
             top = kv8_max2(kv8_max2(kv8_max2(kv8_max2(top, w[k].x), w[k].y), w[k].z), w[k].w);
         }
     }
@@ -291,25 +293,22 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_
     // New tokens.
     const float f = kv8_power(-e);
     if (!isv) {
-        for (int i = tid; i < (b - a) * (HD / 16); i += kStoreThreads) {
-            const int t = a + i / (HD / 16), d = (i % (HD / 16)) * 16;
-            const uint4 lo = *reinterpret_cast<const uint4 *>(sm + place(t, d)), hi = *reinterpret_cast<const uint4 *>(sm + place(t, d + 8));
-            const uint32_t u[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t p = u[2 * k], q = u[2 * k + 1];
-                w[k] = odd ? kv8_byte(bf16_lo(p) * f) | kv8_byte(bf16_hi(p) * f) << 8 | kv8_byte(bf16_lo(q) * f) << 16 | kv8_byte(bf16_hi(q) * f) << 24
-                           : kv8_pair(bf16_lo(p) * f, bf16_hi(p) * f) | kv8_pair(bf16_lo(q) * f, bf16_hi(q) * f) << 16;
+        auto put = [&](auto pair) {
+            for (int i = tid; i < (b - a) * (HD / 16); i += kStoreThreads) {
+                const int t = a + i / (HD / 16), d = (i % (HD / 16)) * 16;
+                const uint4 lo = *reinterpret_cast<const uint4 *>(sm + place(t, d)), hi = *reinterpret_cast<const uint4 *>(sm + place(t, d + 8));
+                *reinterpret_cast<uint4 *>(out + t * HD + d) = make_uint4(pair(lo.x) | pair(lo.y) << 16, pair(lo.z) | pair(lo.w) << 16,
+                                                                          pair(hi.x) | pair(hi.y) << 16, pair(hi.z) | pair(hi.w) << 16);
             }
-            *reinterpret_cast<uint4 *>(out + static_cast<long long>(t) * HD + d) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+        };
+        if (odd) put([f](uint32_t w) { return kv8_byte(bf16_lo(w) * f) | kv8_byte(bf16_hi(w) * f) << 8; });
+        else put([f](uint32_t w) { return kv8_pair(bf16_lo(w) * f, bf16_hi(w) * f); });
     } else {
         // 16 tokens of two neighbouring dims per thread; a warp covers whole
         // runs of a dim's tokens, and the padding spreads their reads over the banks.
-        const int pieces = c.page / 16;
-        for (int i = tid; i < HD / 2 * pieces; i += kStoreThreads) {
-            const int d = 2 * (i / pieces), t0 = (i % pieces) * 16;
+        const int log2 = c.page == 32 ? 1 : c.page == 64 ? 2 : 3;  // 16-token pieces of a page
+        for (int i = tid; i < HD / 2 << log2; i += kStoreThreads) {
+            const int d = 2 * (i >> log2), t0 = (i & ((1 << log2) - 1)) * 16;
             uint8_t *dst = out + static_cast<long long>(d) * c.page + t0;
             if (t0 >= a && t0 + 16 <= b && !odd) {
                 uint32_t w[2][4];
@@ -591,7 +590,8 @@ constexpr int kMoveThreads = 256;
 
 // Copies the pairs' pages, layer by layer, and rewrites the table and refs.
 // A (layer, page)'s K (or V) is one run of n_kv_heads * page * head_dim bytes.
-// Bound by memory: half of 500 pages x 32 layers x 8 heads in 383 us (5.6 TB/s).
+// Bound by memory: half of 500 pages x 32 layers x 8 heads in 333 us (6.4 TB/s)
+// with 8 loads of each thread in flight, 387 with one.
 __global__ void __launch_bounds__(kMoveThreads) k_kv8_move(la_kv8_cache c, int *table_out, int *refs_out, const int *ws) {
     pdl_trigger();
     pdl_wait();
@@ -622,7 +622,16 @@ __global__ void __launch_bounds__(kMoveThreads) k_kv8_move(la_kv8_cache c, int *
         const long long bytes = static_cast<long long>(c.page) * c.head_dim;
         const uint4 *x = reinterpret_cast<const uint4 *>(pool + a * bytes);
         uint4 *y = reinterpret_cast<uint4 *>(pool + b * bytes);
-        for (int k = threadIdx.x; k < run / 16; k += kMoveThreads) y[k] = x[k];
+        constexpr int B = 8;                                           // loads in flight
+        for (int k0 = threadIdx.x; k0 < run / 16; k0 += B * kMoveThreads) {
+            uint4 w[B];
+#pragma unroll
+            for (int q = 0; q < B; ++q)
+                if (k0 + q * kMoveThreads < run / 16) w[q] = x[k0 + q * kMoveThreads];
+#pragma unroll
+            for (int q = 0; q < B; ++q)
+                if (k0 + q * kMoveThreads < run / 16) y[k0 + q * kMoveThreads] = w[q];
+        }
         for (int k = threadIdx.x; k < c.n_kv_heads; k += kMoveThreads) scales[b + k] = scales[a + k];
     }
 }
