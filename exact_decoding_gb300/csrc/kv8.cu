@@ -339,12 +339,13 @@ __global__ void __launch_bounds__(kStoreThreads) k_kv8_store(la_kv8_cache c, la_
 // a token has one byte in each dim's row, so a sector of 32 bytes is read and
 // written for each (64 sequences x 32 layers x 8 heads, one row each: 33.9 us
 // and 205 MB for 16 MB of new bytes).
-// Against k_kv8_store, with la_kv8_free behind: 64 sequences, 1, 4 and 8 rows
-// 33.9 us, 85 and 150 against 91.5, 152 and 203; 32 sequences x 8 layers x 4 heads
-// 7.7, 11.2 and 14.9 against 11.1, 13.2 and 14.1; but 4 sequences x 32 layers x 8
-// heads 9.3, 21.5 and 36.7 against 11.3, 16.1 and 20.6: there each SM has a CTA at
-// most, and stored tokens that are rounded again occupy one warp instead of eight.
-constexpr int kFewRows = 8, kFewWarps = 8, kFewCtas = 256;
+// Against k_kv8_store, with la_kv8_free behind: 64 sequences, 2, 4 and 8 rows
+// 55 us, 85 and 150 against 84, 110 and 161; 32 sequences x 8 layers x 4 heads, 4
+// and 8 rows 10.6 and 14.3 against 11.2 and 12.6; but 4 sequences x 32 layers x 8
+// heads, 2 and 4 rows 14.0 and 21.5 against 11.3 and 14.0: there each SM has a CTA
+// at most, and stored tokens that are rounded again occupy one warp instead of
+// four.  (One row: 9.3.)
+constexpr int kFewRows = 4, kFewWarps = 8, kFewCtas = 256;
 
 template <int HD>
 __global__ void __launch_bounds__(32 * kFewWarps, 4) k_kv8_store_few(la_kv8_cache c, la_kv8_rows r, const int4 *record, int touched) {

@@ -1301,10 +1301,11 @@ static int la_step_body(la_handle *h, int32_t *out_tokens, int32_t *out_n) {
     if (h->P + h->M + h->N + 2 > h->max_seq) return fail(LA_ERR_CAPACITY, "max_seq reached");
     cudaStream_t s = h->stream;
     int rc;
-    // A step's graph holds kernels chosen for up to kv8_len cached tokens:
-    // behind that it is captured again, for twice as many.
-    if (h->kv8 && (h->P > h->kv8_len || 4 * h->P < h->kv8_len)) {
-        h->kv8_len = std::min(std::max(2 * h->P, 512), h->max_seq);
+    // A step's graph holds kernels chosen for up to kv8_len cached tokens.  Past
+    // that, or far below it after a new prompt, it is captured again.
+    const int kv8_len = std::min(std::max(2 * h->P, 512), h->max_seq);
+    if (h->kv8 && (h->P > h->kv8_len || h->kv8_len > 2 * kv8_len)) {
+        h->kv8_len = kv8_len;
         if (h->step_graph) cudaGraphExecDestroy(h->step_graph);
         h->step_graph = nullptr;
     }
