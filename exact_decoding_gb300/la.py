@@ -407,6 +407,7 @@ class DeviceWeights:
         self.dims_struct = la_model_dims(dims.n_layers, dims.d_model, dims.n_heads, dims.n_kv_heads, dims.head_dim,
                                          dims.ffn, dims.vocab, dims.rms_eps, dims.rope_base,
                                          LA_BF16 if dims.dtype == "bf16" else LA_F32)
+        self.device = self._keep[0].device
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in self._keep if hasattr(t, "numel"))
@@ -535,8 +536,11 @@ class Kv8Cache:
         knows (0: none); they steer the split of the work only.  Returns out."""
         rows, qs = self._rows(q, "q", 0)
         heads = q.shape[1]
-        if out is None:
+        if out is None and stream is None:
             out = self._torch.empty((rows, heads, self.head_dim), dtype=q.dtype, device=self.device)
+        elif out is None:
+            with self._torch.cuda.stream(stream):   # its memory belongs to the stream that writes it
+                out = self._torch.empty((rows, heads, self.head_dim), dtype=q.dtype, device=self.device)
         n, os_ = self._rows(out, "out", heads)
         kp = vp = ks = vs = 0
         if k is not None and v is not None:
@@ -621,7 +625,9 @@ class Decoder:
         if kv_cache is None:
             self.h = la_create(self.weights.dims_struct, self.weights.struct, o)
         else:
-            if kv_cache.device.type == "cuda" and stream is not None:   # the cache's tensors are written on the current one
+            if kv_cache.device != self.weights.device:
+                raise ValueError(f"kv_cache must be on the weights' device {self.weights.device}, not {kv_cache.device}")
+            if stream is not None:   # the cache's tensors are written on the current one
                 stream.wait_stream(kv_cache._torch.cuda.current_stream(kv_cache.device))
             self.h = la_create_kv8(self.weights.dims_struct, self.weights.struct, o, kv_cache.struct, slot)
 

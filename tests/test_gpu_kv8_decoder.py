@@ -430,3 +430,12 @@ def test_a_stream_of_its_own(lib):
     same(got[1], want)
     for d in (alone, *decs):
         d.close()
+
+
+def test_a_cache_on_another_device_is_refused(lib):
+    dims = SMALL["mha-hd64"]
+    dev = lib.DeviceWeights(weights("mha-hd64", 7))
+    cache = new_cache(lib, dims, 32, max_seq=256)
+    cache.device = torch.device("cuda", 5)
+    with pytest.raises(ValueError, match="device"):
+        lib.Decoder(dev, 4, 5, 4, 256, kv_cache=cache)
