@@ -132,8 +132,8 @@ __device__ __forceinline__ int kv8_workers(const Kv8Args &p, long long total) {
     return static_cast<int>(min(static_cast<long long>(p.workers), total));
 }
 // First tile of worker w.
-__device__ __forceinline__ long long kv8_div(long long a, int b) {   // a >= 0; 32 bits where they do: 64-bit division is long code
-    return a >> 32 ? a / b : static_cast<long long>(static_cast<unsigned>(a) / static_cast<unsigned>(b));
+__device__ __forceinline__ long long kv8_div(long long a, long long b) {   // a >= 0, b > 0; 32 bits where they do: 64-bit division is long code
+    return (a | b) >> 32 ? a / b : static_cast<long long>(static_cast<unsigned>(a) / static_cast<unsigned>(b));
 }
 __device__ __forceinline__ long long kv8_share(long long total, int w, int workers) { return kv8_div(total * w, workers); }
 
@@ -374,11 +374,14 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
 
     for (;;) {
         const bool any = kv8_next(p, tiles, walk, u);
-        if (!noted) {
-            if (tid == 0) kv8_note(p, tiles, any, u);
+        auto note = [&]() {
+            if (!noted && tid == 0) kv8_note(p, tiles, any, u);
             noted = true;
+        };
+        if (!any) {
+            note();
+            break;
         }
-        if (!any) break;
         const Kv8Seq sq = u.sq;
         // This warp's tiles: pages page0 + NW i, i = 0 .. nc - 1.
         const int page0 = u.k0 + warp, s = u.s, head = u.head;
@@ -386,18 +389,18 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
         // Block 2 i is K of tile i, block 2 i + 1 its V.  Page numbers and
         // scales are looked up 32 tiles at a time, lane i for tile 32 n + i
         // (last_*: the 32 tiles before, some of which may still be read).
-        int my_page = -1, my_vx = 0, last_page = -1, last_vx = 0, issued = 0;
-        float my_kf = 0.f, last_kf = 0.f;
+        int my_page = -1, last_page = -1, issued = 0;
+        float my_kf = 0.f, last_kf = 0.f, my_vs = 0.f, last_vs = 0.f;
         auto issue = [&]() {
             const int i = issued >> 1;
             if ((issued & 63) == 0) {
                 last_page = my_page;
-                last_vx = my_vx;
+                last_vs = my_vs;
                 last_kf = my_kf;
                 my_page = i + lane < nc ? kv8_page(c, s, page0 + NW * (i + lane)) : -1;
                 const long long blk = kv8_block(c, p.a.layer, max(my_page, 0), head);
                 my_kf = c.k_scale[blk];
-                my_vx = exponent_of(c.v_scale[blk]);
+                my_vs = c.v_scale[blk];
             }
             const int pg = __shfl_sync(0xffffffffu, my_page, i & 31);
             if (lane == 0) {
@@ -416,6 +419,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
         };
 #pragma unroll 1
         while (issued < min(NS, 2 * nc)) issue();
+        note();   // while the first copies are on their way
 
         // q as fp16, each vector scaled by a power of two to fit: 8 threads a row.
         if (tid < 8 * kRowsQ) {
@@ -527,7 +531,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
             const bool old = i >> 5 != (issued - 1) >> 6;   // issue() is in the next 32 tiles already
             const int pg = __shfl_sync(0xffffffffu, old ? last_page : my_page, i & 31);
             const float kf_ = __shfl_sync(0xffffffffu, old ? last_kf : my_kf, i & 31), kf = pg < 0 ? 1.f : kf_;
-            const int vx = __shfl_sync(0xffffffffu, old ? last_vx : my_vx, i & 31);
+            const int vx = exponent_of(__shfl_sync(0xffffffffu, old ? last_vs : my_vs, i & 31));
             const int left = pg < 0 ? 0 : sq.len - (page0 + NW * i) * PAGE;   // keys of this page that count
             const uint8_t *kblk = my_ring + out_slot * Lay::block, *vblk = nullptr;
 #pragma unroll 1
@@ -1514,53 +1518,69 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
 // A unit that several workers share: worker ranges are contiguous, so the
 // unit's pieces are those of consecutive workers, the first in its slot 1
 // (the piece begins the unit), the others in their slot 0.  One CTA per border
-// between workers; the borders inside a unit share its query vectors and add
-// its pieces in order.
-constexpr int kJoinThreads = 512, kJoinBatch = 8;
+// between workers; the borders inside a unit share its query vectors.  An item
+// (4 dims of a row) is added up in a fixed order, by as many lanes as the pieces
+// ask for and the items leave.  BATCH loads are in flight: 4 behind k_kv8_rows (64
+// sequences, 8 KV heads: 95.0 us against 97.7 with 8), 8 behind k_kv8_tiles, whose
+// units have many rows (121 rows of 32 heads: 31.5 us against 35.0 with 4).
+constexpr int kJoinThreads = 512;
 
-template <int HD>
+template <int HD, int BATCH>
 __global__ void __launch_bounds__(kJoinThreads) k_kv8_join(const __grid_constant__ Kv8Args p) {
     pdl_trigger();
     pdl_wait();
     const int border = blockIdx.x + 1;
     const Kv8Split x = p.split[border];
     if (!x.inside) return;
-    const int workers = kv8_workers(p, x.total);
-    int w0 = border - 1, w1 = border;   // first and last worker with a piece
-#pragma unroll 1
-    while (kv8_share(x.total, w0, workers) > x.t0 + p.snap) --w0;
-#pragma unroll 1
-    while (w1 + 1 < workers && kv8_share(x.total, w1 + 1, workers) < x.t1) ++w1;
+    // First and last worker with a piece: the largest with a share that begins
+    // at t0 + snap at most, and before t1.
+    const long long total = x.total, workers = kv8_workers(p, total);
+    const int w0 = static_cast<int>(kv8_div((x.t0 + p.snap + 1) * workers + total - 1, total)) - 1;
+    const int w1 = static_cast<int>(min(kv8_div(x.t1 * workers + total - 1, total), workers)) - 1;
+    // The border's share of the unit's items (4 dims of a row), `group` lanes for
+    // each: the pieces in turn, BATCH loads in flight, then among the lanes.
     const int items = x.nqv * (HD / 4), share = border - w0 - 1, shares = w1 - w0;
+    const int i0 = items * share / shares, n = items * (share + 1) / shares - i0;
+    int group = 1;
+    while (group < 8 && group * BATCH < shares + 1 && 2 * group * n <= kJoinThreads) group <<= 1;
 #pragma unroll 1
-    for (int i = items * share / shares + threadIdx.x; i < items * (share + 1) / shares; i += kJoinThreads) {
-        const int r = i / (HD / 4), d = 4 * (i % (HD / 4));
-        // pieces kJoinBatch at a time, so that their loads are in flight together
+    for (int j = threadIdx.x; (j & ~31) < n * group; j += kJoinThreads) {
+        const bool on = j < n * group;
+        const int i = i0 + (on ? j / group : 0), first = w0 + j % group, r = i / (HD / 4), d = 4 * (i % (HD / 4));
         float mx = -INFINITY, L = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto add = [&](float m, float l, float4 v) {
+            const float mn = fmaxf(mx, m), base = mn == -INFINITY ? 0.f : mn, f0 = ex2(mx - base), f1 = ex2(m - base);
+            L = L * f0 + l * f1;
+            acc.x = acc.x * f0 + v.x * f1;
+            acc.y = acc.y * f0 + v.y * f1;
+            acc.z = acc.z * f0 + v.z * f1;
+            acc.w = acc.w * f0 + v.w * f1;
+            mx = mn;
+        };
 #pragma unroll 1
-        for (int w = w0; w <= w1; w += kJoinBatch) {
-            float2 ml[kJoinBatch];
-            float4 v[kJoinBatch];
+        for (int w = first; on && w <= w1; w += BATCH * group) {
+            float2 ml[BATCH];
+            float4 v[BATCH];
 #pragma unroll
-            for (int b = 0; b < kJoinBatch; ++b) {
-                const int ww = min(w + b, w1);
+            for (int b = 0; b < BATCH; ++b) {
+                const int ww = min(w + b * group, w1);
                 const long long rec = static_cast<long long>(2 * ww + (ww == w0 ? 1 : 0)) * p.q_tile + r;
                 ml[b] = *reinterpret_cast<const float2 *>(p.part_ml + rec * 2);
                 v[b] = *reinterpret_cast<const float4 *>(p.part + rec * HD + d);
             }
 #pragma unroll
-            for (int b = 0; b < kJoinBatch; ++b) {
-                if (w + b > w1 || ml[b].y == 0.f) continue;   // a piece that saw no key
-                const float mn = fmaxf(mx, ml[b].x), f0 = ex2(mx - mn), f1 = ex2(ml[b].x - mn);
-                L = L * f0 + ml[b].y * f1;
-                acc.x = acc.x * f0 + v[b].x * f1;
-                acc.y = acc.y * f0 + v[b].y * f1;
-                acc.z = acc.z * f0 + v[b].z * f1;
-                acc.w = acc.w * f0 + v[b].w * f1;
-                mx = mn;
-            }
+            for (int b = 0; b < BATCH; ++b)
+                if (w + b * group <= w1 && ml[b].y != 0.f) add(ml[b].x, ml[b].y, v[b]);   // 0: a piece that saw no key
         }
+#pragma unroll 1
+        for (int o = 1; o < group; o <<= 1) {
+            const float m = __shfl_xor_sync(0xffffffffu, mx, o), l = __shfl_xor_sync(0xffffffffu, L, o);
+            const float4 v = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o),
+                                         __shfl_xor_sync(0xffffffffu, acc.z, o), __shfl_xor_sync(0xffffffffu, acc.w, o));
+            if (l != 0.f) add(m, l, v);
+        }
+        if (!on || j % group != 0) continue;
         const float inv = L == 0.f ? 0.f : 1.f / L;
         const int qv = x.qv0 + r;
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + (x.first + qv / p.gq) * p.a.out_stride + (x.head * p.gq + qv % p.gq) * HD + d;
@@ -1633,7 +1653,7 @@ static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     cudaError_t e = launch_k(k_kv8_rows<HD, PAGE>, dim3(p.workers), dim3(32 * Lay::warps), Lay::bytes(p.c.n_seqs), s, p);
     if (e != cudaSuccess || p.whole) return e;
     if (p.workers < 2) return cudaSuccess;
-    return launch_k(k_kv8_join<HD>, dim3(p.workers - 1), dim3(kJoinThreads), 0, s, p);
+    return launch_k(k_kv8_join<HD, 4>, dim3(p.workers - 1), dim3(kJoinThreads), 0, s, p);
 }
 
 template <int HD>
@@ -1663,7 +1683,7 @@ static cudaError_t tiles_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     }
     cudaError_t e = launch_k(k_kv8_tiles<HD>, dim3(p.workers), dim3(kTileThreads), Lay::bytes(p.c.n_seqs), s, p);
     if (e != cudaSuccess || p.whole || p.workers < 2) return e;
-    return launch_k(k_kv8_join<HD>, dim3(p.workers - 1), dim3(kJoinThreads), 0, s, p);
+    return launch_k(k_kv8_join<HD, 8>, dim3(p.workers - 1), dim3(kJoinThreads), 0, s, p);
 }
 
 // Query vectors per sequence and KV head up to which k_kv8_rows is used (8
