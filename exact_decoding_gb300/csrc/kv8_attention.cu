@@ -237,7 +237,7 @@ __device__ __forceinline__ int fit_f16(float amax) { return max(exponent_of(amax
 // k_kv8_rows: 16 query vectors per unit (all heads of a KV head's group for
 // one row, or some rows).  Bound by the cache's bytes: every byte is read
 // once and meets 16 query vectors (64 sequences of up to 8192 tokens, 8 KV
-// heads: 548 MB in 95.3 us).  The warps of a CTA take the unit's tiles
+// heads: 548 MB in 94.0 us).  The warps of a CTA take the unit's tiles
 // (one page each) in turn, each with its own running softmax and its own ring
 // of page blocks in shared memory, so no barrier is met inside a unit; they
 // are joined through shared memory at the unit's end.  A block of K or V of
@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
 //                thread a query vector; P replaces S in tensor memory.  Two
 //                groups, since one alone waits for tensor memory half of the
 //                time: 2.4 us per tile.
-// What bounds a tile (1.8 us; its products take 0.55 us) are the instructions of
+// What bounds a tile (1.45 us; its products take 0.55 us) are the instructions of
 // these warps, which share four schedulers: anything that waits must not poll
 // (the softmax and the products polling: 123.4 us against 118.0 for 256 rows over
 // 16k tokens, 8 KV heads), the bytes come by bulk copies (loads to registers by
@@ -820,7 +820,9 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t at) {
 }
 __device__ __forceinline__ void st_shared(uint32_t at, const uint4 &v) { st_shared_u32x4(at, v.x, v.y, v.z, v.w); }
 
-// One copy for the roles of k_kv8_tiles (123.5 us against 126.0).  k_kv8_rows has it inline: a call costs its short runs 2 us.
+// The pieces behind the first: one copy of the code for the roles of k_kv8_tiles
+// (123.5 us against 126.0 for 256 rows over 16k tokens).  The first piece is found
+// before the roles part, which a call like this would delay by 2.3 us.
 __device__ __noinline__ bool kv8_next_call(const Kv8Args &p, const long long *tiles, Kv8Walk &w, Kv8Piece &u) { return kv8_next(p, tiles, w, u); }
 
 template <int HD>
@@ -885,6 +887,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     const uint32_t tmem = *tmem_slot;
     Kv8Walk walk = kv8_walk(p, tiles);
     Kv8Piece u{};
+    const bool begun = kv8_next(p, tiles, walk, u);   // the first piece
     int it = 0;          // key tiles so far, the same count in every role: buffer it & 1, its use it >> 1
     bool ok = true;
     unsigned *err = c.status;
@@ -938,7 +941,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 phase ^= 1;
             }
         };
-        while (ok && kv8_next_call(p, tiles, walk, u)) {
+        for (bool any = begun; ok && any; any = kv8_next_call(p, tiles, walk, u)) {
             const Kv8Seq sq = u.sq;
             auto k_tile = [&](int kt, int it) {
                 const int b = it & 1, use = it >> 1;
@@ -1172,7 +1175,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 phase ^= 1;
             }
         };
-        while (ok && kv8_next_call(p, tiles, walk, u)) {
+        for (bool any = begun; ok && any; any = kv8_next_call(p, tiles, walk, u)) {
             const int c_first = max(u.k0, u.sq.ntiles);   // first cached tile of this piece
             if (c_first >= u.k1) continue;
             uint32_t held = 0, v_held = 0, v_blk = 0, blk = block_of(checked(entry(c_first)), held);
@@ -1201,15 +1204,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         // ================================================ products
         // The whole warp runs this loop; one elected lane issues.  (Inside a
         // branch on the lane's number each product took 90 cycles to issue.)
-        if (!p.whole) {
-            Kv8Walk w = walk;
-            const bool any = kv8_next_call(p, tiles, w, u);
-            if (lane == 0) kv8_note(p, tiles, any, u);
-        }
+        if (!p.whole && lane == 0) kv8_note(p, tiles, begun, u);
         constexpr uint32_t is = idesc_f16(kTileQ, kTileK), io = idesc_f16(kTileQ, HD);
         auto wait = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity & 1, err, LA_KV8_TIMEOUT)); };
         int units = 0;
-        while (ok && kv8_next_call(p, tiles, walk, u)) {
+        for (bool any = begun; ok && any; any = kv8_next_call(p, tiles, walk, u)) {
             if (u.k0 >= u.k1) continue;
             ok = wait(q_full, units);
             ++units;
@@ -1269,7 +1268,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         float *qfs = reinterpret_cast<float *>(smem + Lay::qf_off);
         int *odds = reinterpret_cast<int *>(smem + Lay::odd_off);
         int units = 0;
-        while (ok && kv8_next_call(p, tiles, walk, u)) {
+        for (bool any = begun; ok && any; any = kv8_next_call(p, tiles, walk, u)) {
             const Kv8Seq sq = u.sq;
             const bool in = row < u.nqv, idle = row - lane >= u.nqv;   // idle: none of this warp's rows is in use
             const int qv = u.qv0 + row, myrow = in ? qv / p.gq : 0, myhead = u.head * p.gq + (in ? qv % p.gq : 0);
@@ -1593,8 +1592,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv8_join(const __grid_constant
 // What a unit costs beside its key tiles, in tiles.  k_kv8_rows: 64 sequences of up
 // to 8192 tokens, 8 KV heads: 119.0 us with 4, 99.4 with 10, 95.4 with 13, 95.3
 // with 16, 98.8 with 26; 48 of up to 1500, head_dim 64, 4 KV heads: 20.5 with 4,
-// 16.4 with 13, 17.4 with 26.  k_kv8_tiles (256 rows over 16k tokens): 121.3 with
-// 2, 118.6 with 4, 118.2 with 6.
+// 16.4 with 13, 17.4 with 26.  k_kv8_tiles, with 4, 8 and 12: 256 rows over 16k
+// tokens 114.5, 113.1 and 110.2; 121 rows of 32 heads over 4000 tokens 33.5, 36.4
+// and 36.5.
 constexpr int kRowsUnitCost = 14, kTilesUnitCost = 4;
 constexpr int kRowsPerSm = 4;   // most CTAs of k_kv8_rows per SM
 
@@ -1616,9 +1616,18 @@ static bool attrs_needed(const std::atomic<unsigned long long> &mask, unsigned l
     return !(mask.load() & *bit);
 }
 
-// Units of the call, at most.
+// Units of the call, at most, if max_rows holds.
 static long long unit_bound(const Kv8Args &p) {
-    return (static_cast<long long>(p.a.n_rows) * p.gq + static_cast<long long>(p.q_tile - 1) * p.c.n_seqs) / p.q_tile * p.c.n_kv_heads;
+    const long long qt = p.q_tile, all = (static_cast<long long>(p.a.n_rows) * p.gq + (qt - 1) * p.c.n_seqs) / qt;
+    return std::min(all, (static_cast<long long>(p.a.max_rows) * p.gq + qt - 1) / qt * p.c.n_seqs) * p.c.n_kv_heads;
+}
+
+// Units are split where that saves more than `cost` tiles' time: a split costs the
+// join's kernel and the pieces' way through memory.  Units of more than `most` tiles
+// always: where the lengths differ, whole ones leave SMs idle at the end.
+static bool keep_whole(const Kv8Args &p, long long units, long long tiles, int cost, int most) {
+    const long long rounds = (units + p.workers - 1) / p.workers;
+    return tiles <= most && rounds * tiles - units * (tiles + p.unit_cost) / p.workers <= cost;
 }
 
 template <int HD, int PAGE>
@@ -1630,15 +1639,14 @@ static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     p.n_tile = 0;
     p.unit_cost = kRowsUnitCost;
     p.snap = p.unit_cost - 1;
-    const long long units = unit_bound(p), tiles = (p.a.max_len + PAGE - 1) / PAGE;
-    // Splitting a unit costs a second kernel and the pieces' way through memory.
-    // One row of 64 heads over 8 KV heads, pages of 64, whole against split: 13
-    // tiles 13.1 us against 14.5, 32 tiles 19.9 against 19.3; 16 such sequences
-    // 15.1 against 17.5 and 24.6 against 22.7; 32 KV heads 12.9 against 12.3 and
-    // 19.6 against 14.1; 48 sequences, head_dim 64, 4 KV heads, pages of 32: 16
-    // tiles 10.5 against 13.5, 47 tiles 19.2 against 16.7.
-    p.whole = tiles <= std::min(32, (256 << 10) / (2 * Lay::block));
-    p.workers = p.whole ? static_cast<int>(std::min<long long>(units, 1 << 20)) : nsm * Lay::per_sm;
+    // Whole against split: one row of 64 heads over 8 KV heads, pages of 64, 13
+    // tiles 13.1 us against 11.3, 19 tiles 14.8 against 11.5; 16 such sequences 19
+    // tiles 17.7 against 19.7, 32 tiles 24.4 against 22.5; 48 sequences, head_dim
+    // 64, 4 KV heads, pages of 32, 16 tiles 10.7 against 13.5, 47 tiles 19.6
+    // against 16.4.
+    const long long tiles = (p.a.max_len + PAGE - 1) / PAGE;
+    p.workers = nsm * Lay::per_sm;
+    if (keep_whole(p, unit_bound(p), tiles, 8, 32)) p.whole = 1, p.workers = static_cast<int>(std::min<long long>(unit_bound(p), 1 << 20));
     p.part = static_cast<float *>(ws);
     p.part_ml = p.part + static_cast<long long>(nsm) * kRowsPerSm * 2 * kRowsQ * HD;
     p.split = reinterpret_cast<Kv8Split *>(p.part_ml + static_cast<long long>(nsm) * kRowsPerSm * 2 * kRowsQ * 2);
@@ -1663,13 +1671,13 @@ static cudaError_t tiles_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     p.k_tile = p.n_tile = kTileK;
     p.unit_cost = kTilesUnitCost;
     p.snap = 0;   // finding the unit costs more than an empty piece (121 rows over 2k tokens, 32 heads: 34.4 us against 33.1)
-    const long long units = unit_bound(p);
+    // Whole against split: 121 rows of 32 heads, 6 tiles 24.2 us against 25.4, 9
+    // tiles 29.9 against 25.4; four such sequences, which fill the SMs whole, 12
+    // tiles 35.7 against 57, 25 tiles 58.5 against 73, and 33 tiles of 8 sequences
+    // with 160 query vectors for each of 8 KV heads 62.8 against 73.8.
     const long long tiles = (p.a.max_len + kTileK - 1) / kTileK + (p.a.k ? (p.a.max_rows + kTileK - 1) / kTileK : 0);
-    // Splitting costs about five tiles' time (121 rows of 32 heads, whole against
-    // split: 6 tiles 26.4 us against 29.2, 9 tiles 32.1 against 29.5; four such
-    // sequences, which fill the SMs whole: 12 tiles 38.3 against 60.0).
-    p.whole = (units + nsm - 1) / nsm * tiles - units * (tiles + kTilesUnitCost) / nsm <= 5;
-    p.workers = p.whole ? static_cast<int>(std::min<long long>(units, 1 << 20)) : nsm;
+    p.workers = nsm;
+    if (keep_whole(p, unit_bound(p), tiles, 5, 64)) p.whole = 1, p.workers = static_cast<int>(std::min<long long>(unit_bound(p), 1 << 20));
     p.part = static_cast<float *>(ws);
     p.part_ml = p.part + static_cast<long long>(nsm) * 2 * kTileQ * HD;
     p.split = reinterpret_cast<Kv8Split *>(p.part_ml + static_cast<long long>(nsm) * 2 * kTileQ * 2);
@@ -1686,11 +1694,12 @@ static cudaError_t tiles_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     return launch_k(k_kv8_join<HD, 8>, dim3(p.workers - 1), dim3(kJoinThreads), 0, s, p);
 }
 
-// Query vectors per sequence and KV head up to which k_kv8_rows is used (8
-// sequences of 4000 tokens, 8 KV heads, k_kv8_rows against k_kv8_tiles: 16
-// vectors 23.4 us against 39.6, 48 vectors 41.9 against 44.0, 64 vectors 51.2
-// against 45.3, 96 vectors 70.7 against 49.1).
-constexpr int kFewVectors = 48;
+// Query vectors per sequence and KV head up to which k_kv8_rows is used (k_kv8_rows
+// against k_kv8_tiles: 8 sequences of 4000 tokens, 8 KV heads, 16 vectors 22.7 us
+// against 36.9, 32 vectors 31.8 against 38.3, 48 vectors 41.1 against 40.9, 64
+// vectors 50.6 against 42.1; one of 2000 tokens, 32 KV heads, 64 vectors 32.7
+// against 24.0).
+constexpr int kFewVectors = 32;
 
 template <int HD>
 static cudaError_t attention_launch_hd(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
