@@ -1592,9 +1592,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv8_join(const __grid_constant
 // What a unit costs beside its key tiles, in tiles.  k_kv8_rows: 64 sequences of up
 // to 8192 tokens, 8 KV heads: 119.0 us with 4, 99.4 with 10, 95.4 with 13, 95.3
 // with 16, 98.8 with 26; 48 of up to 1500, head_dim 64, 4 KV heads: 20.5 with 4,
-// 16.4 with 13, 17.4 with 26.  k_kv8_tiles, with 4, 8 and 12: 256 rows over 16k
-// tokens 114.5, 113.1 and 110.2; 121 rows of 32 heads over 4000 tokens 33.5, 36.4
-// and 36.5.
+// 16.4 with 13, 17.4 with 26.  k_kv8_tiles counts 4, and of long units a tenth up to
+// 12: with 4, 8 and 12 256 rows, 8 KV heads, take over 16k tokens 114.4, 113.1 and
+// 110.2 us, over 8k 76.9, 74.2 and 79.5; 121 rows of 32 heads over 4k 33.5, 36.4 and
+// 36.5 (with so few tiles for each CTA a wide count only moves the borders).
 constexpr int kRowsUnitCost = 14, kTilesUnitCost = 4;
 constexpr int kRowsPerSm = 4;   // most CTAs of k_kv8_rows per SM
 
@@ -1669,13 +1670,13 @@ static cudaError_t tiles_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     using Lay = Tiles<HD>;
     p.q_tile = kTileQ;
     p.k_tile = p.n_tile = kTileK;
-    p.unit_cost = kTilesUnitCost;
     p.snap = 0;   // finding the unit costs more than an empty piece (121 rows over 2k tokens, 32 heads: 34.4 us against 33.1)
     // Whole against split: 121 rows of 32 heads, 6 tiles 24.2 us against 25.4, 9
     // tiles 29.9 against 25.4; four such sequences, which fill the SMs whole, 12
     // tiles 35.7 against 57, 25 tiles 58.5 against 73, and 33 tiles of 8 sequences
     // with 160 query vectors for each of 8 KV heads 62.8 against 73.8.
     const long long tiles = (p.a.max_len + kTileK - 1) / kTileK + (p.a.k ? (p.a.max_rows + kTileK - 1) / kTileK : 0);
+    p.unit_cost = static_cast<int>(std::min<long long>(std::max<long long>(tiles / 10, kTilesUnitCost), 3 * kTilesUnitCost));
     p.workers = nsm;
     if (keep_whole(p, unit_bound(p), tiles, 5, 64)) p.whole = 1, p.workers = static_cast<int>(std::min<long long>(unit_bound(p), 1 << 20));
     p.part = static_cast<float *>(ws);
