@@ -481,3 +481,29 @@ def test_append_few_rows_to_many_sequences(lib, hd, page, kv, most):
         assert cache.append(k, v, row_start=starts(rows), max_rows=most).tolist() == want
         model.same_as(cache)
     cache.status()
+
+
+@pytest.mark.parametrize("hd,page", [(128, 128), (128, 32), (64, 64)])
+@pytest.mark.parametrize("rows", [1, 70])
+def test_as_many_slots_as_there_may_be(lib, hd, page, rows):
+    """2048 slots of which a few hold tokens or get rows, the first and the last among them."""
+    lens = [0] * 2048
+    lens[0], lens[1], lens[900], lens[2047] = 300, 5, 130, 77
+    cache = build(lib, lens, hd, page, 2, seed=2)
+    counts = [0] * 2048
+    for s in (0, 900, 1500, 2047):
+        counts[s] = rows
+    n = 4 * rows
+    q, k, v = normal((n, 4, hd), 1), normal((n, 2, hd), 2), normal((n, 2, hd), 3)
+    out = cache.attention(q, k, v, row_start=starts(counts))
+    close(out, *M.attention(cache, q, k, v, counts))
+    cache.status()
+    model = M.Model(cache)
+    want = model.append(k[None].cpu().double().numpy(), v[None].cpu().double().numpy(), counts)
+    assert cache.append(k[None], v[None], row_start=starts(counts)).tolist() == want
+    model.same_as(cache)
+    if want != counts:                      # three free pages do not take 70 rows of four sequences
+        with pytest.raises(lib.LaError) as e:
+            cache.status()
+        assert e.value.code == CAPACITY
+    cache.status()
