@@ -718,7 +718,8 @@ struct Tiles {
     static constexpr uint32_t raw_off = q_off + k_bytes, raw_bytes = kTileK * HD;
     static constexpr uint32_t head_off = raw_off + raw_slots * raw_bytes;   // [raw_slots] Kv8Meta of the bytes in the ring
     static constexpr uint32_t meta_off = head_off + raw_slots * 64;         // [4] Kv8Meta of the last tiles
-    static constexpr uint32_t red_off = meta_off + 4 * 64;         // [2][2][8] maxima of the new rows' tile
+    static constexpr uint32_t exp_off = meta_off + 4 * 64;         // [4] Kv8Exps of the last tiles, where those are kMixed
+    static constexpr uint32_t red_off = exp_off + 4 * 256;         // [2][2][8] largest and least of the new rows' tile, by warp
     static constexpr uint32_t qf_off = red_off + 128;              // [128] factors on the rows' scores
     static constexpr uint32_t odd_off = qf_off + kTileQ * 4;       // [2 groups]
     static constexpr uint32_t bar_off = odd_off + 16;
@@ -734,10 +735,23 @@ struct Kv8Meta {
     float kf[4];   // per 32 keys: factor of K, exponent of V, keys that count
     int vx[4];
     int live[4];
-    int odd;       // new rows: V holds a NaN or infinity
+    int odd;       // new rows: kOddV, kMixed
     int pad[3];
 };
 static_assert(sizeof(Kv8Meta) == 64, "layout");
+constexpr int kOddV = 1;    // V holds a NaN or infinity
+constexpr int kMixed = 2;   // each row has exponents of its own
+// A tile's new rows share one factor of K and one of V (the largest value's)
+// where all of their 8-dim pieces that are not zero reach within 2^kSpread of
+// it: values keep at least 15 + 24 - kSpread = 23 bits below their piece's
+// largest.  Else each row has its own, or a huge row would leave nothing of the
+// others, for query vectors too that do not see it.  The code for that is apart:
+// in line it cost every call 7 us (121 rows of 32 heads over 2k tokens, 31.6 us; so 32.9).
+constexpr int kSpread = 16;
+struct Kv8Exps {
+    signed char k[kTileK], v[kTileK];   // of fit_f16, -60 .. 113
+};
+static_assert(sizeof(Kv8Exps) == 256, "layout");
 
 // kind::f16 with fp16 operands, fp32 accumulation.
 __device__ constexpr uint32_t idesc_f16(int m, int n) {
@@ -820,6 +834,105 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t at) {
 }
 __device__ __forceinline__ void st_shared(uint32_t at, const uint4 &v) { st_shared_u32x4(at, v.x, v.y, v.z, v.w); }
 
+// ---- new rows that are many binades apart (kMixed): code apart from the roles'
+// Largest finite magnitude of 8 bf16 values, as pairs.
+__device__ __noinline__ uint32_t finite_top(uint4 x) {
+    auto tame = [](uint32_t w) { return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0x7fffu) | ((w >> 16 & 0x7f80u) == 0x7f80u ? 0u : w & 0x7fff0000u); };
+    return most2(most2(most2(most2(0u, tame(x.x)), tame(x.y)), tame(x.z)), tame(x.w));
+}
+
+// Exponents of a tile's rows, and K's rows turned into fp16 in place.  Thread t
+// of the operand warps has the 16-byte pieces t, t + 32 kOpWarps, ..., as when K
+// was copied: a row's pieces belong to neighbouring lanes of one warp.
+template <int HD>
+__device__ __noinline__ void mixed_rows(uint32_t sk, uint32_t k_block, const __nv_bfloat16 *vn, int64_t v_stride, int nkeys, int t, Kv8Exps *ex) {
+    constexpr int C8 = HD / 8;
+    auto fit_row = [](uint4 x) {
+        uint32_t top = finite_top(x);
+#pragma unroll
+        for (int o = 1; o < C8; o <<= 1) top = most2(top, __shfl_xor_sync(0xffffffffu, top, o));
+        return fit_pair(top);
+    };
+#pragma unroll 1
+    for (int i = t; i < kTileK * C8; i += 32 * kOpWarps) {   // whole warps
+        const int r = i / C8, c = i % C8;
+        const uint32_t at = sk + (c >> 3) * k_block + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+        const uint4 x = ld_shared(at), y = r < nkeys ? *reinterpret_cast<const uint4 *>(vn + r * v_stride + 8 * c) : make_uint4(0, 0, 0, 0);
+        const int kx = fit_row(x), vx = fit_row(y);
+        const float f = power_of(-kx);
+        st_shared_u32x4(at, scaled_f16(x.x, f), scaled_f16(x.y, f), scaled_f16(x.z, f), scaled_f16(x.w, f));
+        if (c == 0) {
+            ex->k[r] = static_cast<signed char>(kx);
+            ex->v[r] = static_cast<signed char>(vx);
+        }
+    }
+}
+
+// Such rows' V^T operand: 8 dims of a row at a time.  NaN and infinities count 0, as in the roles' code.
+template <int HD>
+__device__ __noinline__ void mixed_v(uint32_t sv, uint32_t v_block, const __nv_bfloat16 *vn, int64_t v_stride, int nkeys, int t, const signed char *vx) {
+#pragma unroll 1
+    for (int j = t; j < kTileK * (HD / 8); j += 32 * kOpWarps) {
+        const int r = j % kTileK, d = 8 * (j / kTileK);
+        const uint4 x = r < nkeys ? *reinterpret_cast<const uint4 *>(vn + r * v_stride + d) : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        const float f = power_of(-vx[r]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float y = bf16_bits(k & 1 ? w[k >> 1] >> 16 : w[k >> 1] & 0xffffu);
+            const __half h = __float2half_rn(is_finite(y) ? y * f : 0.f);
+            const uint32_t at = sv + (r >> 6) * v_block + (d + k) * 128 + ((((r >> 3) & 7) ^ k) << 4) + (r & 7) * 2;
+            asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(*reinterpret_cast<const uint16_t *>(&h)) : "memory");
+        }
+    }
+}
+
+// Which of new rows key .. key + 31 row `row` of a sequence (-1: none) sees.
+__device__ __forceinline__ uint32_t new_rows_seen(const Kv8Args &p, int first, int row, int key) {
+    if (row < 0) return 0u;
+    if (p.a.vis) return key < 256 ? p.a.vis[(static_cast<long long>(first) + row) * 8 + key / 32] : 0u;
+    return row >= key + 31 ? 0xffffffffu : row < key ? 0u : (2u << (row - key)) - 1u;
+}
+
+// Such a tile's scores: turns this thread's row of S, at ts, into t_j = z_j + vx_j
+// (-infinity for keys that it does not see).  Returns max z_j and
+// sum_j 2^(z_j - max), and m and l as they stand, for mixed_sum.
+__device__ __noinline__ float4 mixed_scores(const Kv8Args &p, uint32_t ts, const Kv8Exps *ex, int first, int row, int key0, int nkeys, float qf,
+                                            float m, float l) {
+    float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {   // 16 keys at a time
+        uint32_t v[16];
+        tmem_ld_32x32b_x16(ts + 16 * k, v);
+        const int live = nkeys - 16 * k;
+        const uint32_t see = (live <= 0 ? 0u : live >= 16 ? 0xffffu : (1u << live) - 1u) & new_rows_seen(p, first, row, key0 + 32 * (k >> 1)) >> 16 * (k & 1);
+        tmem_ld_wait_for(v);
+        float most = top;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float z = see >> e & 1u ? __uint_as_float(v[e]) * (power_of(ex->k[16 * k + e]) * qf) : -INFINITY;
+            most = fmaxf(most, z);
+            v[e] = __float_as_uint(z);
+        }
+        const float base = most == -INFINITY ? 0.f : most;
+        sum *= ex2(top - base);
+        top = most;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            sum += ex2(__uint_as_float(v[e]) - base);
+            v[e] = __float_as_uint(__uint_as_float(v[e]) + static_cast<float>(ex->v[16 * k + e]));
+        }
+        tmem_st_32x32b_x16(ts + 16 * k, v);
+    }
+    tmem_st_wait();
+    return make_float4(top, sum, m, l);
+}
+// l behind such a tile, whose weights' sum is not that of the 2^z_j: the sum
+// before it, at the maximum as it is now, and the tile's.
+__device__ __noinline__ float mixed_sum(float4 keep, float m) {
+    return (keep.w == 0.f ? 0.f : keep.w * ex2(keep.z - m)) + (keep.y == 0.f ? 0.f : keep.y * ex2(keep.x - m));
+}
+
 // The pieces behind the first: one copy of the code for the roles of k_kv8_tiles
 // (123.5 us against 126.0 for 256 rows over 16k tokens).  The first piece is found
 // before the roles part, which a call like this would delay by 2.3 us.
@@ -833,6 +946,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     const uint32_t sm = smem_u32(smem);
     Kv8Meta *meta = reinterpret_cast<Kv8Meta *>(smem + Lay::meta_off);
     Kv8Meta *head = reinterpret_cast<Kv8Meta *>(smem + Lay::head_off);
+    Kv8Exps *exps = reinterpret_cast<Kv8Exps *>(smem + Lay::exp_off);
     uint32_t *red = reinterpret_cast<uint32_t *>(smem + Lay::red_off);
     long long *tiles = reinterpret_cast<long long *>(smem + Lay::tiles_off);
     const uint32_t bars = sm + Lay::bar_off;
@@ -959,7 +1073,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                     // copies, all in flight: one load after another took 12 us) and
                     // are turned into fp16 in place; V's largest magnitude meanwhile.
                     auto kat = [&](int i) { return sk + ((i % C8) >> 3) * Lay::k_block + (i / C8) * 128 + (((i % 8) ^ (i / C8 & 7)) << 4); };
-                    uint32_t ak = 0, av = 0;
+                    uint32_t ak = 0, av = 0, lk = ~0u, lv = ~0u;   // largest; least but zeros, less 1
+                    auto least = [](uint32_t l, uint32_t top) { return min(l, max(top & 0xffffu, top >> 16) - 1u); };
 #pragma unroll 1
                     for (int i = ot; i < kTileK * C8; i += NT) {
                         const int r = i / C8;
@@ -971,37 +1086,45 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
 #pragma unroll 4
                     for (int i = ot; i < nkeys * C8; i += NT) {
                         const uint4 x = *reinterpret_cast<const uint4 *>(vn + (i / C8) * p.a.v_stride + 8 * (i % C8));
-                        av = most2(most2(most2(most2(av, x.x), x.y), x.z), x.w);
+                        const uint32_t top = most2(most2(most2(most2(0u, x.x), x.y), x.z), x.w);
+                        av = most2(av, top);
+                        lv = least(lv, top);
                     }
                     asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll 2
                     for (int i = ot; i < kTileK * C8; i += NT) {   // the pieces that this thread copied
                         const uint4 x = ld_shared(kat(i));
-                        ak = most2(most2(most2(most2(ak, x.x), x.y), x.z), x.w);
+                        const uint32_t top = most2(most2(most2(most2(0u, x.x), x.y), x.z), x.w);
+                        ak = most2(ak, top);
+                        lk = least(lk, top);
                     }
                     // A NaN or infinity among them: the maxima again, without those.
                     bool odd = max(av & 0xffffu, av >> 16) >= 0x7f80u;
                     if (__any_sync(0xffffffffu, odd || max(ak & 0xffffu, ak >> 16) >= 0x7f80u)) {
-                        auto tame = [](uint32_t w) { return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0x7fffu) | ((w >> 16 & 0x7f80u) == 0x7f80u ? 0u : w & 0x7fff0000u); };
                         ak = av = 0;
+                        lk = lv = ~0u;
 #pragma unroll 1
                         for (int i = ot; i < nkeys * C8; i += NT) {
-                            const uint4 x = *reinterpret_cast<const uint4 *>(vn + (i / C8) * p.a.v_stride + 8 * (i % C8)), y = ld_shared(kat(i));
-                            av = most2(most2(most2(most2(av, tame(x.x)), tame(x.y)), tame(x.z)), tame(x.w));
-                            ak = most2(most2(most2(most2(ak, tame(y.x)), tame(y.y)), tame(y.z)), tame(y.w));
+                            const uint32_t x = finite_top(*reinterpret_cast<const uint4 *>(vn + (i / C8) * p.a.v_stride + 8 * (i % C8))), y = finite_top(ld_shared(kat(i)));
+                            av = most2(av, x);
+                            lv = least(lv, x);
+                            ak = most2(ak, y);
+                            lk = least(lk, y);
                         }
                     }
                     ak = max(ak & 0xffffu, ak >> 16);
                     av = max(av & 0xffffu, av >> 16);
                     ak = __reduce_max_sync(0xffffffffu, ak);
                     av = __reduce_max_sync(0xffffffffu, av);
+                    lk = min(__reduce_min_sync(0xffffffffu, lk), 0x7fffu);
+                    lv = min(__reduce_min_sync(0xffffffffu, lv), 0x7fffu);
                     odd = __any_sync(0xffffffffu, odd);
                     // The warps' maxima: two halves, one for each buffer, so that no
                     // warp writes what another still reads.
                     uint32_t *mine = red + 16 * b;
                     if (lane == 0) {
-                        mine[w] = ak;
-                        mine[8 + w] = av | (odd ? 0x10000u : 0u);
+                        mine[w] = ak | lk << 16;
+                        mine[8 + w] = av | lv << 16 | (odd ? 0x80000000u : 0u);
                         mbar_arrive_one(r_full);
                     }
                     __syncwarp();
@@ -1009,28 +1132,45 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                     if (!ok) return;
                     ++new_tiles;
                     ak = av = 0;
+                    lk = lv = 0x7fffu;
                     odd = false;
 #pragma unroll
                     for (int k = 0; k < kOpWarps; ++k) {
-                        ak = max(ak, mine[k]);
-                        av = max(av, mine[8 + k] & 0xffffu);
-                        odd |= mine[8 + k] >> 16 != 0;
+                        const uint32_t x = mine[k], y = mine[8 + k];
+                        ak = max(ak, x & 0xffffu);
+                        av = max(av, y & 0xffffu);
+                        lk = min(lk, x >> 16);
+                        lv = min(lv, y >> 16 & 0x7fffu);
+                        odd |= y >> 31 != 0;
                     }
-                    const int kx = fit_f16(bf16_bits(ak)), vx = fit_f16(bf16_bits(av));
+                    int kx = fit_f16(bf16_bits(ak)), vx = fit_f16(bf16_bits(av));
+                    // Exponents of bf16 bits; a least of 0x7fff: only zeros
+                    const bool mixed = static_cast<int>(ak >> 7) - static_cast<int>((lk + 1) >> 7) > kSpread ||
+                                       static_cast<int>(av >> 7) - static_cast<int>((lv + 1) >> 7) > kSpread;
+                    if (mixed) {
+                        mixed_rows<HD>(sk, Lay::k_block, vn, p.a.v_stride, nkeys, ot, &exps[it & 3]);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_one(r_full);
+                        __syncwarp();
+                        ok = __all_sync(0xffffffffu, bar_wait(r_full, new_tiles & 1, err, LA_KV8_TIMEOUT));
+                        if (!ok) return;
+                        ++new_tiles;
+                        kx = vx = 0;   // the scores come with all factors (mixed_scores)
+                    }
                     if (w == 0) {
                         if (lane < 4) {
                             Kv8Meta &mt = meta[it & 3];
                             mt.kf[lane] = power_of(kx);
                             mt.vx[lane] = vx;
                             mt.live[lane] = min(max(nkeys - 32 * lane, 0), 32);
-                            if (lane == 0) mt.odd = odd;
+                            if (lane == 0) mt.odd = (odd ? kOddV : 0) | (mixed ? kMixed : 0);
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive_one(m_full(it & 3));
                     }
                     const float fk = power_of(-kx);
 #pragma unroll 2
-                    for (int i = ot; i < kTileK * C8; i += NT) {
+                    for (int i = mixed ? kTileK * C8 : ot; i < kTileK * C8; i += NT) {
                         const uint4 x = ld_shared(kat(i));
                         st_shared_u32x4(kat(i), scaled_f16(x.x, fk), scaled_f16(x.y, fk), scaled_f16(x.z, fk), scaled_f16(x.w, fk));
                     }
@@ -1071,11 +1211,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                     ok = __all_sync(0xffffffffu, bar_wait(m_full(it & 3), it >> 2 & 1, err, LA_KV8_TIMEOUT));
                     if (!ok) return;
                     const float fv = power_of(-meta[it & 3].vx[0]);
+                    const bool mixed = meta[it & 3].odd & kMixed;
                     const int key0 = kt * kTileK, nkeys = min(kTileK, sq.rows - key0);
                     const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + u.head * HD;
                     constexpr int NT = 32 * kOpWarps, NP = kTileK / 2 * (HD / 8), B = 4;   // pairs of rows, in flight
+                    if (mixed) mixed_v<HD>(sv, Lay::v_block, vn, p.a.v_stride, nkeys, w * 32 + lane, exps[it & 3].v);
 #pragma unroll 1
-                    for (int j0 = w * 32 + lane; j0 < NP; j0 += B * NT) {
+                    for (int j0 = mixed ? NP : w * 32 + lane; j0 < NP; j0 += B * NT) {
                         uint4 va[B], vb[B];
 #pragma unroll
                         for (int q = 0; q < B; ++q) {
@@ -1321,6 +1463,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 qf = idle ? 0.f : qfs[row];
             }
             float m = -INFINITY, l = 0.f;
+            float4 keep;
             bool odd = false;
             for (int kt = u.k0 + ((first ^ grp) & 1); kt < u.k1; kt += 2) {
                 const int i = first + kt - u.k0, b = grp;   // tile number, of this group's parity
@@ -1329,13 +1472,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 if (!ok) break;
                 tc_fence_after();
                 const Kv8Meta &mt = meta[i & 3];
-                odd |= mt.odd != 0;
+                odd |= (mt.odd & kOddV) != 0;
                 if (!idle) {
                     // 32 keys at a time: t relative to the maximum as it stands, then
                     // the weights, over columns of S that are read already.  One
                     // copy of this code: unrolled, the roles' code does not fit
                     // the instruction cache (5 us per pair of tiles).
                     const bool cached = kt >= sq.ntiles;
+                    if (!cached && (mt.odd & kMixed)) {
+                        keep = mixed_scores(p, ts, &exps[i & 3], sq.first, in ? myrow : -1, kt * kTileK, min(sq.rows - kt * kTileK, kTileK), qf, m, l);
+                        qf = 1.f;
+                    }
 #pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
                         uint32_t v[32];
@@ -1419,6 +1566,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                         tmem_st_32x32b_x16(ts + 16 * k, w);
                     }
                     if (!ok) break;
+                    if (!cached && (mt.odd & kMixed)) {
+                        l = mixed_sum(keep, m);
+                        qf = qfs[row];
+                    }
                     tmem_st_wait();
                 }
                 tc_fence_before();
