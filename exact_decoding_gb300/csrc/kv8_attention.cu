@@ -3,19 +3,23 @@
 // For a query vector q (one row, one head) and the keys j it sees,
 //   z_j = scale * q . K_j,   o = sum_j e^(z_j) V_j / sum_j e^(z_j),
 // computed in one pass over the keys with the running maximum of the softmax.
-// With a power-of-two scale 2^kx on a page's K and 2^vx on its V (kx, vx its
-// scales' exponents), the kernels keep, in base 2,
-//   t_j = z_j log2(e) + vx,  m = max t_j,  w_j = 2^(t_j - m)  (fp16, <= 1),
-//   O = sum_j w_j V8_j,      L = sum_j w_j 2^-vx,   o = O / L,
-// so the weights that meet the 8-bit values carry V's scale and stay in
-// fp16's range, whatever the pages' scales are.
+// With a power-of-two scale 2^vx on a page's V (new rows: on a row's or a tile's), the
+// kernels keep for each row, z in base 2, two whole numbers r and d and
+//   L = sum_j 2^(z_j - r),   w_j = 2^(z_j - r + u), u = vx - d   (fp16),
+//   O = sum_j w_j V8_j,      o = O 2^d / L.
+// r follows the maximum of z lazily (z_j - r <= kLazy), d follows vx so that u
+// stays within kUnitLow .. kUnitHigh: weights are at most 2^15, and those
+// below 2^-14 are off by 2^-25 at most, 2^(-25 - kUnitLow) of the largest key's
+// weight, whatever scales other pages have.  Were one number (a maximum of
+// z + vx) to follow both, a page of large scale would leave no bits of the
+// others, even where it has no weight.
 //
 // The work is the list of (sequence, KV head, tile of query vectors) units,
 // each a run of key tiles: the sequence's new rows, then its cached tokens.
 // Every worker (CTA) takes an equal share of the flattened key tiles of all
 // units, read off the device-side lengths, so ragged batches and single long
 // sequences fill the GPU alike.  A unit that one worker does not cover leaves
-// partial (O, m, L) in the workspace, and k_kv8_join adds them in key order.
+// partial (O, r, d, L) in the workspace, and k_kv8_join adds them in key order.
 //
 // Short calls are bound by instruction fetches: code that runs once per call
 // comes from L2 a line at a time, about 50 instructions per microsecond.  So
@@ -37,6 +41,12 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, unsigned
 }
 
 constexpr float kKv8Log2e = 1.4426950408889634f;
+constexpr float kLazy = 8.f;
+constexpr float kUnitLow = -5.f, kUnitHigh = 7.f, kUnit = 2.f;   // u, and what it becomes when d changes
+// O's reach: |w_j V_j| 2^-d for the keys so far is below 2^(reach - d).  What the
+// pages in the window add is kReach above d at most; d stays within kSpan of the
+// reach, so that O (2^30 keys) never passes fp32's range.
+constexpr float kReach = 25.f, kSpan = 90.f;
 
 struct Kv8Args {
     la_kv8_cache c;
@@ -51,7 +61,7 @@ struct Kv8Args {
     int workers;
     float scale_log2;  // scale * log2(e)
     float *part;       // [workers][2][q_tile][head_dim] unnormalised sums
-    float *part_ml;    // [workers][2][q_tile][2] running maximum and L
+    float *part_ml;    // [workers][2][q_tile][4] r, d and L
     struct Kv8Split *split;   // [workers]
 };
 // What a worker's range begins with: a unit that earlier workers began, or not.
@@ -253,6 +263,7 @@ __device__ __forceinline__ int fit_f16(float amax) { return max(exponent_of(amax
 // KT/4 t + 2 j, + 1: already the A operand of the second product.
 // The new rows, at most a few here, are added key by key in fp32.
 constexpr int kRowsQ = 16;
+constexpr float kRowsUnit = -9.f;   // d at first: a page of values of order one has a scale of 2^-7, which this fits
 
 template <int HD, int PAGE>
 struct Rows {
@@ -270,7 +281,8 @@ struct Rows {
     static constexpr int q_off = ring > join ? ring : join;
     static constexpr int qf_off = q_off + kRowsQ * q_row;                       // [16] factor on a row's scores
     static constexpr int ml_off = qf_off + kRowsQ * 4;
-    static constexpr int bar_off = ml_off + warps * kRowsQ * 2 * 4;
+    static constexpr int reach_off = ml_off + warps * kRowsQ * 16;              // [warp][16] reach of O, relative to r
+    static constexpr int bar_off = reach_off + warps * kRowsQ * 4;
     static constexpr int sum_off = bar_off + warps * slots * 8;
     static constexpr int tiles_off = sum_off + warps * 8;                  // (n_seqs + 1) prefix sums follow
     static size_t bytes(int n_seqs) { return tiles_off + (static_cast<size_t>(n_seqs) + 1) * 8; }
@@ -302,11 +314,11 @@ __device__ __forceinline__ int fit_pair(uint32_t top) {
 __device__ __forceinline__ uint32_t scaled_f16(uint32_t w, float f) { return pack_f16(bf16_bits(w & 0xffffu) * f, __uint_as_float(w & 0xffff0000u) * f); }
 
 // Online softmax of one piece: scores sc (columns: this lane's keys, `live`
-// of them) to the fp16 weights w16, with the running maximum m, the sum l and
-// O's factor.
+// of them) to the fp16 weights w16, with r, d, the sum l and O's factor.
+// reach: of O, for rows g and g + 8 (in shared memory: it is seldom asked for).
 template <int NJ, int NI>
-__device__ __forceinline__ void rows_softmax(float (&sc)[NJ][4], int live, float kf, const float (&qf)[2], int vx, float (&m)[2],
-                                             float (&l)[2], float (&o)[NI][4], uint32_t (&w16)[NJ][2]) {
+__device__ __forceinline__ void rows_softmax(float (&sc)[NJ][4], int live, float kf, const float (&qf)[2], int vx, float (&r)[2], float (&d)[2],
+                                             float (&l)[2], float *reach, float (&o)[NI][4], uint32_t (&w16)[NJ][2]) {
     if (live < 2 * NJ) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
@@ -316,15 +328,32 @@ __device__ __forceinline__ void rows_softmax(float (&sc)[NJ][4], int live, float
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {   // rows g (elements 0, 1 of a product) and g + 8 (2, 3)
-        const float f = kf * qf[h], add = static_cast<float>(vx);
+        const float f = kf * qf[h];
         float mx = -INFINITY;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) mx = fmaxf(mx, fmaxf(sc[j][2 * h], sc[j][2 * h + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[h], fmaf(mx, f, add)), base = mn == -INFINITY ? 0.f : mn;
-        const float alpha = ex2(m[h] - base), off = add - base;
-        m[h] = mn;
+        const float z = mx * f, v = static_cast<float>(vx);
+        const bool grow = r[h] == -INFINITY ? z > -INFINITY : z - r[h] > kLazy;
+        const bool shift = z > -INFINITY && (v - d[h] > kUnitHigh || v - d[h] < kUnitLow);
+        if (__any_sync(0xffffffffu, grow || shift)) {
+            const float nr = grow ? ceilf(z) : r[h], far = fmaxf(reach[8 * h], d[h] + kReach) - (grow ? nr - r[h] : 0.f);
+            const float nd = shift ? fmaxf(v - kUnit, far - kSpan) : d[h];
+            const float fl = grow ? ex2(r[h] - nr) : 1.f, fo = fl * ex2(d[h] - nd);
+            __syncwarp();
+            reach[8 * h] = far;   // the quad's lanes write the same
+            __syncwarp();
+            r[h] = nr;
+            d[h] = nd;
+            l[h] *= fl;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                o[i][2 * h] *= fo;
+                o[i][2 * h + 1] *= fo;
+            }
+        }
+        const float u = v - d[h], off = u - (r[h] == -INFINITY ? 0.f : r[h]);
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
@@ -333,14 +362,7 @@ __device__ __forceinline__ void rows_softmax(float (&sc)[NJ][4], int live, float
             s1 += b;
             w16[j][h] = pack_f16(a, b);
         }
-        l[h] = l[h] * alpha + (s0 + s1) * power_of(-vx);
-        if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                o[i][2 * h] *= alpha;
-                o[i][2 * h + 1] *= alpha;
-            }
-        }
+        l[h] += (s0 + s1) * ex2(-u);
     }
 }
 
@@ -352,7 +374,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
     constexpr int CH = KT / 4, NJ = KT / 8;       // of them, one lane's; products
     constexpr int NS = Lay::slots, NW = Lay::warps;
     extern __shared__ __align__(128) uint8_t smem[];
-    float2 *sh_ml = reinterpret_cast<float2 *>(smem + Lay::ml_off);  // [warp][16] m, l
+    float4 *sh_ml = reinterpret_cast<float4 *>(smem + Lay::ml_off);  // [warp][16] r, d, l
     float *sh_o = reinterpret_cast<float *>(smem);                   // [warp][16][HD + 4], over the ring
     float *sh_qf = reinterpret_cast<float *>(smem + Lay::qf_off);
     long long *tiles = reinterpret_cast<long long *>(smem + Lay::tiles_off);
@@ -361,6 +383,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const uint32_t ring = smem_u32(smem) + warp * NS * Lay::block, bars = smem_u32(smem + Lay::bar_off) + warp * NS * 8;
     const uint8_t *my_ring = smem + warp * NS * Lay::block;
+    float *reach = reinterpret_cast<float *>(smem + Lay::reach_off) + warp * kRowsQ + g;
     if (lane < NS) mbar_init(bars + lane * 8, 1);
     fence_barrier_init();
     pdl_wait();
@@ -447,7 +470,8 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
         const uint8_t *my_q = smem + Lay::q_off + g * Lay::q_row + t * Lay::q_piece;   // row g; row g + 8 lies 8 rows behind
         const float qf[2] = {sh_qf[g], sh_qf[g + 8]};
 
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float r[2] = {-INFINITY, -INFINITY}, d[2] = {kRowsUnit, kRowsUnit}, l[2] = {0.f, 0.f};
+        float far[2] = {-INFINITY, -INFINITY};   // reach of O, of the new rows
         float o[NI][4];
 #pragma unroll
         for (int i = 0; i < NI; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -486,16 +510,27 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
                         z[1] = fmaf(qb.x, lo, fmaf(qb.y, hi, z[1]));
                     }
                 }
+                // V's largest magnitude: what it reaches in O may raise d.
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) top = most2(top, vw[i]);
+                top = most2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = most2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int ve = exponent_of(bf16_bits(max(top & 0xffffu, top >> 16)));   // 128: a NaN or infinity, which hides its neighbours' size
                 float w[2], alpha[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     z[h] += __shfl_xor_sync(0xffffffffu, z[h], 1);
                     z[h] += __shfl_xor_sync(0xffffffffu, z[h], 2);
-                    const float x = see[h] ? z[h] * qf[h] : -INFINITY, mn = fmaxf(m[h], x), base = mn == -INFINITY ? 0.f : mn;
-                    alpha[h] = ex2(m[h] - base);
-                    w[h] = ex2(x - base);
-                    m[h] = mn;
-                    l[h] = l[h] * alpha[h] + w[h];
+                    const float x = see[h] ? z[h] * qf[h] : -INFINITY, nr = x > r[h] ? ceilf(x) : r[h], base = nr == -INFINITY ? 0.f : nr;
+                    const float fl = ex2(r[h] - base);
+                    far[h] = fmaxf(far[h] - (base - r[h]), (x - base) + static_cast<float>(ve == 128 ? 0 : ve + 1));
+                    const float nd = fmaxf(d[h], far[h] - kSpan);
+                    alpha[h] = fl * ex2(d[h] - nd);
+                    r[h] = nr;
+                    d[h] = nd;
+                    l[h] = l[h] * fl + ex2(x - base);
+                    w[h] = ex2((x - base) - nd);
                 }
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
@@ -510,6 +545,8 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
             // Every lane of a quad has added the key: l is summed over the quad below.
             if (t != 0) l[0] = l[1] = 0.f;
         }
+        reach[0] = far[0];
+        reach[8] = far[1];
 
         // ---- cached tokens
         auto landed = [&]() {   // the next block to read is there
@@ -531,7 +568,8 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
             const bool old = i >> 5 != (issued - 1) >> 6;   // issue() is in the next 32 tiles already
             const int pg = __shfl_sync(0xffffffffu, old ? last_page : my_page, i & 31);
             const float kf_ = __shfl_sync(0xffffffffu, old ? last_kf : my_kf, i & 31), kf = pg < 0 ? 1.f : kf_;
-            const int vx = exponent_of(__shfl_sync(0xffffffffu, old ? last_vs : my_vs, i & 31));
+            const float vs_ = __shfl_sync(0xffffffffu, old ? last_vs : my_vs, i & 31);
+            const int vx = pg < 0 ? 0 : exponent_of(vs_);
             const int left = pg < 0 ? 0 : sq.len - (page0 + NW * i) * PAGE;   // keys of this page that count
             const uint8_t *kblk = my_ring + out_slot * Lay::block, *vblk = nullptr;
 #pragma unroll 1
@@ -563,7 +601,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
                 }
                 const int live = min(max(left - piece * KT - CH * t, 0), CH);
                 uint32_t w16[NJ][2];
-                rows_softmax<NJ, NI>(sc, live, kf, qf, vx, m, l, o, w16);
+                rows_softmax<NJ, NI>(sc, live, kf, qf, vx, r, d, l, reach, o, w16);
                 if (piece == 0) {   // V is the block behind K
                     const int vs = PAGE / KT == 1 ? out_slot : out_slot + 1 == NS ? 0 : out_slot + 1;
                     const uint32_t ph = PAGE / KT == 1 || out_slot + 1 < NS ? out_phase : out_phase ^ 1;
@@ -622,18 +660,18 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
             }
         }
 
-        // ---- join the warps: weights 2^(m_w - M), then the sum in warp order
+        // ---- join the warps at the largest r and d of those that saw a key, in warp order
         __syncthreads();   // the rings are free
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int r = warp * kRowsQ + g + 8 * h;
+            const int at = warp * kRowsQ + g + 8 * h;
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-            if (t == 0) sh_ml[r] = make_float2(m[h], l[h]);
+            if (t == 0) sh_ml[at] = make_float4(r[h], l[h] == 0.f ? -INFINITY : d[h], l[h], 0.f);
             if (g + 8 * h < u.nqv) {
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
-                    *reinterpret_cast<float2 *>(sh_o + r * (HD + 4) + 8 * i + 2 * t) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
+                    *reinterpret_cast<float2 *>(sh_o + at * (HD + 4) + 8 * i + 2 * t) = make_float2(o[i][2 * h], o[i][2 * h + 1]);
             }
         }
         __syncthreads();
@@ -641,25 +679,28 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
 #pragma unroll 1
         for (int i = tid; i < u.nqv * (HD / 4); i += 32 * NW) {
             const int r = i / (HD / 4), d = 4 * (i % (HD / 4));
-            float mx = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) mx = fmaxf(mx, sh_ml[w * kRowsQ + r].x);
-            float L = 0.f;
+            float R = -INFINITY, D = -INFINITY, L = 0.f;
+#pragma unroll 1
+            for (int w = 0; w < NW; ++w) {
+                const float4 x = sh_ml[w * kRowsQ + r];
+                R = fmaxf(R, x.x);
+                D = fmaxf(D, x.y);
+            }
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
             for (int w = 0; w < NW; ++w) {
-                const float2 ml = sh_ml[w * kRowsQ + r];
-                if (ml.y == 0.f) continue;   // saw no key
-                const float f = ex2(ml.x - mx);
+                const float4 ml = sh_ml[w * kRowsQ + r];
+                if (ml.z == 0.f) continue;   // saw no key
+                const float fl = ex2(ml.x - R), f = ex2((ml.x - R) + (ml.y - D));
                 const float4 x = *reinterpret_cast<const float4 *>(sh_o + (w * kRowsQ + r) * (HD + 4) + d);
-                L += f * ml.y;
+                L += fl * ml.z;
                 acc.x += f * x.x;
                 acc.y += f * x.y;
                 acc.z += f * x.z;
                 acc.w += f * x.w;
             }
             if (u.all) {
-                const float inv = L == 0.f ? 0.f : 1.f / L;
+                const float inv = L == 0.f ? 0.f : ex2(D) / L;
                 const int qv = u.qv0 + r;
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + (sq.first + qv / p.gq) * p.a.out_stride +
                                      (head * p.gq + qv % p.gq) * HD + d;
@@ -667,7 +708,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
                 *reinterpret_cast<uint2 *>(out) = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
             } else {
                 *reinterpret_cast<float4 *>(p.part + (static_cast<long long>(slot) * kRowsQ + r) * HD + d) = acc;
-                if (d == 0) *reinterpret_cast<float2 *>(p.part_ml + (static_cast<long long>(slot) * kRowsQ + r) * 2) = make_float2(mx, L);
+                if (d == 0) *reinterpret_cast<float4 *>(p.part_ml + (static_cast<long long>(slot) * kRowsQ + r) * 4) = make_float4(R, D, L, 0.f);
             }
         }
         fence_proxy_async_smem();   // these accesses before the next unit's bulk copies into the same bytes
@@ -697,14 +738,17 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
 // 16k tokens, 8 KV heads), the bytes come by bulk copies (loads to registers by
 // seven operand warps: 131.3), and S is read 32 columns at a time (16: 136.0,
 // 64: 134.3, both polling).
-// The groups have an O each in tensor memory, added at the end.  An O's scale
-// follows the running maximum only when that has grown by 2^8 since (fp16
-// weights up to 2^8 lose nothing), so it is rarely read back.  Units are split
-// and joined like those of k_kv8_rows.
+// The groups have an O each in tensor memory, added at the end, with r and d of
+// its own; both follow lazily, so O is rarely read back.  A tile has one d:
+// what its page of the largest scale asks for.  Groups of 32 keys of pages that
+// are more than 2^kNear below it are left out of the product and added to O in
+// fp32 (far_group).  Units are split and joined like those of k_kv8_rows.
 constexpr int kTileQ = 128, kTileK = 128;
 constexpr int kOpWarps = 6, kLoadWarp = 8 + kOpWarps, kMmaWarp = kLoadWarp + 1;
 constexpr int kTileThreads = 32 * (kMmaWarp + 1);   // 16 warps: 4 to a quarter of an SM, 128 registers a thread
-constexpr float kLazy = 8.f;
+// u of the tile's largest scale: with kNear, u of every group in the product is kUnitLow or more.
+constexpr int kNear = 6;
+constexpr float kTopLow = kUnitLow + kNear, kTop = 4.f;
 
 template <int HD>
 struct Tiles {
@@ -735,12 +779,14 @@ struct Kv8Meta {
     float kf[4];   // per 32 keys: factor of K, exponent of V, keys that count
     int vx[4];
     int live[4];
-    int odd;       // new rows: kOddV, kMixed
-    int pad[3];
+    int flags;     // kOddV, kMixed, kFar << k
+    int top;       // largest vx of the groups that have keys (new rows: 5 more, as their fp16 values are 2^6 times a page's)
+    int pad[2];
 };
 static_assert(sizeof(Kv8Meta) == 64, "layout");
-constexpr int kOddV = 1;    // V holds a NaN or infinity
-constexpr int kMixed = 2;   // each row has exponents of its own
+constexpr int kOddV = 1;    // new rows: V holds a NaN or infinity
+constexpr int kMixed = 2;   // new rows: each has exponents of its own
+constexpr int kFar = 4;     // << k: group k's page has a V scale more than 2^kNear below `top`
 // A tile's new rows share one factor of K and one of V (the largest value's)
 // where all of their 8-dim pieces that are not zero reach within 2^kSpread of
 // it: values keep at least 15 + 24 - kSpread = 23 bits below their piece's
@@ -809,15 +855,15 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[N]) {
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
 }
 
-// Two columns of this thread's row of tensor memory.
-__device__ __forceinline__ void tmem_st_pair(uint32_t at, float a, float b) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1, %2};" ::"r"(at), "f"(a), "f"(b) : "memory");
+// Four columns of this thread's row of tensor memory.
+__device__ __forceinline__ void tmem_st_four(uint32_t at, float a, float b, float c) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %3};" ::"r"(at), "f"(a), "f"(b), "f"(c) : "memory");
 }
-__device__ __forceinline__ float2 tmem_ld_pair(uint32_t at) {
-    uint32_t v[2];
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(at));
+__device__ __forceinline__ float4 tmem_ld_four(uint32_t at) {
+    uint32_t v[4];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(at));
     tmem_ld_wait_for(v);
-    return make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+    return make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]), __uint_as_float(v[3]));
 }
 
 // 16 e4m3 bytes as 32 bytes of fp16.
@@ -894,43 +940,196 @@ __device__ __forceinline__ uint32_t new_rows_seen(const Kv8Args &p, int first, i
     return row >= key + 31 ? 0xffffffffu : row < key ? 0u : (2u << (row - key)) - 1u;
 }
 
-// Such a tile's scores: turns this thread's row of S, at ts, into t_j = z_j + vx_j
-// (-infinity for keys that it does not see).  Returns max z_j and
-// sum_j 2^(z_j - max), and m and l as they stand, for mixed_sum.
-__device__ __noinline__ float4 mixed_scores(const Kv8Args &p, uint32_t ts, const Kv8Exps *ex, int first, int row, int key0, int nkeys, float qf,
-                                            float m, float l) {
-    float top = -INFINITY, sum = 0.f;
+// A row's state, and what the softmax seldom asks for.
+struct Kv8Row {
+    float r, d, l, qf;
+    float reach, at;             // of O, relative to r when that was `at`
+    float own_r, own_d, own_l;   // behind a tile of own_scores
+    // The softmax's other values while begin_tile runs.  Kept in registers over the
+    // call they would be spilled in every tile (256 rows over 16k tokens 123 us, so 115).
+    int grp, row, units, it, first, end, i, kt, myrow, myhead;
+    uint32_t lanes, ts, to;
+    bool in, odd;
+};
+// O's reach relative to r, where r has grown from s.r.
+__device__ __forceinline__ float reach_now(const Kv8Row &s, float r) { return fmaxf(s.reach - (r - s.at), s.d + kReach - (r - s.r)); }
+
+// O *= f, for this thread's row.
+template <int HD>
+__device__ __forceinline__ void scale_o(uint32_t to, float f) {
 #pragma unroll 1
-    for (int k = 0; k < 8; ++k) {   // 16 keys at a time
-        uint32_t v[16];
-        tmem_ld_32x32b_x16(ts + 16 * k, v);
-        const int live = nkeys - 16 * k;
-        const uint32_t see = (live <= 0 ? 0u : live >= 16 ? 0xffffu : (1u << live) - 1u) & new_rows_seen(p, first, row, key0 + 32 * (k >> 1)) >> 16 * (k & 1);
-        tmem_ld_wait_for(v);
-        float most = top;
+    for (int q = 0; q < HD / 16; ++q) {
+        uint32_t o[16];
+        tmem_ld_32x32b_x16(to + 16 * q, o);
+        tmem_ld_wait_for(o);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const float z = see >> e & 1u ? __uint_as_float(v[e]) * (power_of(ex->k[16 * k + e]) * qf) : -INFINITY;
-            most = fmaxf(most, z);
-            v[e] = __float_as_uint(z);
-        }
-        const float base = most == -INFINITY ? 0.f : most;
-        sum *= ex2(top - base);
-        top = most;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            sum += ex2(__uint_as_float(v[e]) - base);
-            v[e] = __float_as_uint(__uint_as_float(v[e]) + static_cast<float>(ex->v[16 * k + e]));
-        }
-        tmem_st_32x32b_x16(ts + 16 * k, v);
+        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        tmem_st_32x32b_x16(to + 16 * q, o);
     }
     tmem_st_wait();
-    return make_float4(top, sum, m, l);
 }
-// l behind such a tile, whose weights' sum is not that of the 2^z_j: the sum
-// before it, at the maximum as it is now, and the tile's.
-__device__ __noinline__ float mixed_sum(float4 keep, float m) {
-    return (keep.w == 0.f ? 0.f : keep.w * ex2(keep.z - m)) + (keep.y == 0.f ? 0.f : keep.y * ex2(keep.x - m));
+
+// A tile of new rows with exponents of their own (kMixed), or which O's reach keeps
+// from having the d that it asks for: turns this thread's row of S, at ts, into
+// the exponents of its weights, z_j - r + vx_j - d (-infinity for keys that it
+// does not see), with r and d as this tile's largest ones have them.  s.own_*
+// has r, d and l behind this tile; for the loop over its groups the scores are
+// final (r 0, u 0, a factor of 1), and l < 0 says so.
+template <int HD>
+__device__ __forceinline__ void own_scores(const Kv8Args &p, const Kv8Piece &u, uint32_t ts, uint32_t to, const Kv8Meta &mt, const Kv8Exps &ex, int key0,
+                                           int row, bool has_o, Kv8Row &s) {
+    const int nkeys = min(u.sq.rows - key0, kTileK);
+    const bool mixed = mt.flags & kMixed;
+    const float was = s.r;
+    float zmax = -INFINITY, xmax = -INFINITY, sum = 0.f, nr = was, nd = s.d;
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {   // 16 keys at a time
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(ts + 16 * k, v);
+            tmem_ld_wait_for(v);
+            if (pass == 0) {
+                const int live = nkeys - 16 * k;
+                const uint32_t see = (live <= 0 ? 0u : live >= 16 ? 0xffffu : (1u << live) - 1u) & new_rows_seen(p, u.sq.first, row, key0 + 32 * (k >> 1)) >> 16 * (k & 1);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float z = see >> e & 1u ? __uint_as_float(v[e]) * ((mixed ? power_of(ex.k[16 * k + e]) : mt.kf[0]) * s.qf) : -INFINITY;
+                    zmax = fmaxf(zmax, z);
+                    v[e] = __float_as_uint(z);
+                }
+            } else if (pass == 1) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float y = __uint_as_float(v[e]) - (nr == -INFINITY ? 0.f : nr), x = y + static_cast<float>(mixed ? ex.v[16 * k + e] : mt.vx[0]);
+                    sum += ex2(y);
+                    xmax = fmaxf(xmax, x);
+                    v[e] = __float_as_uint(x);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) - nd);
+            }
+            tmem_st_32x32b_x16(ts + 16 * k, v);
+        }
+        tmem_st_wait();
+        if (pass == 0 && zmax > was) nr = ceilf(zmax);
+        if (pass == 1 && xmax > -INFINITY) {
+            const float reach = was == -INFINITY ? -INFINITY : reach_now(s, nr);
+            if (was == -INFINITY || xmax - nd > kUnitHigh || xmax - nd < 0.f) nd = fmaxf(ceilf(xmax) - kTop, reach - kSpan);
+            s.reach = fmaxf(reach, xmax + 16.f);   // new rows' fp16 values are below 2^15
+            s.at = nr;
+        }
+    }
+    const float fl = nr > was ? ex2(was - nr) : 1.f;
+    if (has_o) scale_o<HD>(to, was == -INFINITY ? 0.f : fl * ex2(s.d - nd));
+    s.own_r = nr, s.own_d = nd, s.own_l = s.l * fl + sum;
+    s.r = 0.f, s.d = static_cast<float>(mt.vx[0]), s.l = -1e30f, s.qf = 1.f / mt.kf[0];
+}
+
+// Group k of a cached tile that is left out of the product: its weights' product with
+// V in fp32, onto O; S = -infinity.
+template <int HD>
+__device__ __forceinline__ void far_group(const Kv8Args &p, const Kv8Piece &u, uint32_t ts, uint32_t to, const Kv8Meta &mt, int kt, int k, Kv8Row &s) {
+    const int live = mt.live[k], key = (kt - u.sq.ntiles) * kTileK + 32 * k;   // its page is in the pool: it has keys
+    const int page = p.c.table[static_cast<long long>(u.s) * p.c.max_pages + (key >> p.page_log2)];
+    const uint8_t *v8 = static_cast<const uint8_t *>(p.c.v) + kv8_block(p.c, p.a.layer, page, u.head) * (p.c.page * HD) + (key & (p.c.page - 1));
+    const float f = mt.kf[k] * s.qf, ux = static_cast<float>(mt.vx[k]) - s.d;
+    float w[32], top = -INFINITY;
+    {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(ts + 32 * k, v);
+        tmem_ld_wait_for(v);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            w[e] = e < live ? __uint_as_float(v[e]) * f : -INFINITY;
+            top = fmaxf(top, w[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = 0xff800000u;
+        tmem_st_32x32b_x16(ts + 32 * k, reinterpret_cast<const uint32_t(&)[16]>(v));
+        tmem_st_32x32b_x16(ts + 32 * k + 16, reinterpret_cast<const uint32_t(&)[16]>(v));
+    }
+    const bool grow = s.r == -INFINITY ? top > -INFINITY : top - s.r > kLazy;
+    if (__any_sync(0xffffffffu, grow)) {
+        const float nr = grow ? ceilf(top) : s.r, fl = !grow ? 1.f : s.r == -INFINITY ? 0.f : ex2(s.r - nr);
+        scale_o<HD>(to, fl);
+        s.l *= fl;
+        s.reach = reach_now(s, nr);
+        s.at = s.r = nr;
+    }
+    const float at = s.r == -INFINITY ? 0.f : s.r;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+        s.l += ex2(w[e] - at);
+        w[e] = ex2((w[e] - at) + ux);
+    }
+#pragma unroll 1
+    for (int q = 0; q < HD / 4; ++q) {
+        uint32_t o[4];
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]) : "r"(to + 4 * q));
+        tmem_ld_wait_for(o);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint4 *src = reinterpret_cast<const uint4 *>(v8 + static_cast<long long>(4 * q + e) * p.c.page);
+            const uint4 x = src[0], y = src[1];
+            const uint32_t b[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+            float acc = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int n = live - 4 * i;   // bytes behind the last token may be anything
+                uint32_t lo, hi;
+                e4m3x4_f16(n >= 4 ? b[i] : n <= 0 ? 0u : b[i] & ((1u << (8 * n)) - 1u), lo, hi);
+                const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo)), c = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                acc = fmaf(w[4 * i], a.x, fmaf(w[4 * i + 1], a.y, fmaf(w[4 * i + 2], c.x, fmaf(w[4 * i + 3], c.y, acc))));
+            }
+            o[e] = __float_as_uint(__uint_as_float(o[e]) + acc);
+        }
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + 4 * q), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+    }
+    tmem_st_wait();
+}
+
+// What a tile needs before its weights: d of a tile whose largest scale is
+// 2^mt.top, with O following, and the groups and rows that the loop over them cannot take as
+// they are.  `row`: this thread's new row, or -1.
+template <int HD>
+__device__ __noinline__ void begin_tile(const Kv8Args &p, const Kv8Piece &u, uint32_t ts, uint32_t to, const Kv8Meta &mt, const Kv8Exps &ex, int kt, int row,
+                                        bool has_o, Kv8Row &s) {
+    const bool cached = kt >= u.sq.ntiles;
+    const float top = static_cast<float>(mt.top);
+    int far = mt.flags / kFar;
+    if (!(mt.flags & kMixed)) {
+        float nd = s.d, f = 1.f;
+        if (top - nd < kTopLow || top - nd > kUnitHigh) {   // not where nothing has been seen: d is the tile's there
+            s.reach = reach_now(s, s.r);
+            s.at = s.r;
+            nd = fmaxf(top - kTop, s.reach - kSpan);
+            f = ex2(s.d - nd);
+        }
+        if (__any_sync(0xffffffffu, f != 1.f)) scale_o<HD>(to, f);   // such a row has an O
+        s.d = nd;
+        if (__any_sync(0xffffffffu, top - nd < kTopLow)) {   // O's reach keeps d above: no bits would be left of fp16 weights
+            if (!cached) {
+                own_scores<HD>(p, u, ts, to, mt, ex, kt * kTileK, row, has_o, s);
+                return;
+            }
+            far = 0;
+            for (int k = 0; k < 4; ++k) far |= mt.live[k] > 0 ? 1 << k : 0;
+        }
+    } else {
+        own_scores<HD>(p, u, ts, to, mt, ex, kt * kTileK, row, has_o, s);
+        return;
+    }
+    if (far && !has_o) {   // O, to add to
+        const uint32_t zero[16] = {};
+#pragma unroll 1
+        for (int q = 0; q < HD / 16; ++q) tmem_st_32x32b_x16(to + 16 * q, zero);
+        tmem_st_wait();
+    }
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k)
+        if (far >> k & 1) far_group<HD>(p, u, ts, to, mt, kt, k, s);
 }
 
 // The pieces behind the first: one copy of the code for the roles of k_kv8_tiles
@@ -1163,7 +1362,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                             mt.kf[lane] = power_of(kx);
                             mt.vx[lane] = vx;
                             mt.live[lane] = min(max(nkeys - 32 * lane, 0), 32);
-                            if (lane == 0) mt.odd = (odd ? kOddV : 0) | (mixed ? kMixed : 0);
+                            if (lane == 0) {
+                                mt.flags = (odd ? kOddV : 0) | (mixed ? kMixed : 0);
+                                mt.top = vx + 5;
+                            }
                         }
                         __syncwarp();
                         if (lane == 0) mbar_arrive_one(m_full(it & 3));
@@ -1211,7 +1413,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                     ok = __all_sync(0xffffffffu, bar_wait(m_full(it & 3), it >> 2 & 1, err, LA_KV8_TIMEOUT));
                     if (!ok) return;
                     const float fv = power_of(-meta[it & 3].vx[0]);
-                    const bool mixed = meta[it & 3].odd & kMixed;
+                    const bool mixed = meta[it & 3].flags & kMixed;
                     const int key0 = kt * kTileK, nkeys = min(kTileK, sq.rows - key0);
                     const __nv_bfloat16 *vn = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + key0) * p.a.v_stride + u.head * HD;
                     constexpr int NT = 32 * kOpWarps, NP = kTileK / 2 * (HD / 8), B = 4;   // pairs of rows, in flight
@@ -1297,12 +1499,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         auto stage = [&](const void *pool, int kt, uint32_t blk, uint32_t held, float ks, float vs) {
             if (staged >= Lay::raw_slots) ok = __all_sync(0xffffffffu, bar_wait(raw_empty(slot), phase ^ 1, err, LA_KV8_TIMEOUT));
             if (!ok) return;
+            const bool have = held >> lane & 1u;
+            const int live = have ? min(max(u.sq.len - (kt - u.sq.ntiles) * kTileK - 32 * lane, 0), 32) : 0, vx = exponent_of(vs);
+            const int top = __reduce_max_sync(0xffffffffu, live > 0 ? vx : -127);
+            const uint32_t far = __ballot_sync(0xffffffffu, live > 0 && vx < top - kNear);
             if (lane < 4) {
-                const bool have = held >> lane & 1u;
                 head[slot].kf[lane] = have ? ks : 1.f;
-                head[slot].vx[lane] = have ? exponent_of(vs) : 0;
-                head[slot].live[lane] = have ? min(max(u.sq.len - (kt - u.sq.ntiles) * kTileK - 32 * lane, 0), 32) : 0;
-                if (lane == 0) head[slot].odd = 0;
+                head[slot].vx[lane] = have ? vx : 0;
+                head[slot].live[lane] = live;
+                if (lane == 0) {
+                    head[slot].flags = far * kFar;
+                    head[slot].top = top;
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(raw_full(slot), __popc(held & starts) * bytes);
@@ -1381,12 +1589,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t sv = sm + Lay::v_off + b * Lay::v_bytes, pt = tmem + kColS + 128 * b, ot = tmem + kColO + 128 * b;
+                    const bool fresh = j < first + 2 && meta[j & 3].flags < kFar;   // O holds nothing yet
                     if (elect_one()) {
 #pragma unroll
                         for (int kb = 0; kb < 2; ++kb) {
                             const uint64_t d = umma_desc_sw128(sv + kb * Lay::v_block);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) umma_ts(ot, pt + kb * 32 + k * 8, d + 2 * k, io, j < first + 2 && !(kb | k) ? 0u : 1u);
+                            for (int k = 0; k < 4; ++k) umma_ts(ot, pt + kb * 32 + k * 8, d + 2 * k, io, fresh && !(kb | k) ? 0u : 1u);
                         }
                         umma_commit(v_empty(b));
                         umma_commit(o_full(b));
@@ -1404,17 +1613,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         __syncwarp();
     } else {
         // ================================================ softmax
-        const int grp = warp >> 2, row = 32 * (warp & 3) + lane;
-        const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-        const uint32_t ts = tmem + lanes + kColS + 128 * grp, to = tmem + lanes + kColO + 128 * grp;
+        int grp = warp >> 2, row = 32 * (warp & 3) + lane;
+        uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+        uint32_t ts = tmem + lanes + kColS + 128 * grp, to = tmem + lanes + kColO + 128 * grp;
         float *qfs = reinterpret_cast<float *>(smem + Lay::qf_off);
         int *odds = reinterpret_cast<int *>(smem + Lay::odd_off);
         int units = 0;
         for (bool any = begun; ok && any; any = kv8_next_call(p, tiles, walk, u)) {
-            const Kv8Seq sq = u.sq;
-            const bool in = row < u.nqv, idle = row - lane >= u.nqv;   // idle: none of this warp's rows is in use
-            const int qv = u.qv0 + row, myrow = in ? qv / p.gq : 0, myhead = u.head * p.gq + (in ? qv % p.gq : 0);
-            const int first = it, end = it + max(u.k1 - u.k0, 0);
+            Kv8Seq sq = u.sq;
+            bool in = row < u.nqv;
+            const bool idle = row - lane >= u.nqv;   // none of this warp's rows is in use
+            const int qv = u.qv0 + row;
+            int myrow = in ? qv / p.gq : 0, myhead = u.head * p.gq + (in ? qv % p.gq : 0), first = it, end = it + max(u.k1 - u.k0, 0);
             float qf = 0.f;
             if (first < end) {
                 // q as fp16, each vector scaled by a power of two to fit: 8 lanes a
@@ -1462,44 +1672,52 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 if (!ok) break;
                 qf = idle ? 0.f : qfs[row];
             }
-            float m = -INFINITY, l = 0.f;
-            float4 keep;
+            float r = -INFINITY, d = 0.f, l = 0.f;
+            Kv8Row keep;   // in memory: what only the rare paths ask for
+            keep.reach = keep.at = -INFINITY;
             bool odd = false;
             for (int kt = u.k0 + ((first ^ grp) & 1); kt < u.k1; kt += 2) {
-                const int i = first + kt - u.k0, b = grp;   // tile number, of this group's parity
+                int i = first + kt - u.k0, b = grp;   // tile number, of this group's parity
                 ok = bar_wait(s_full(b), i >> 1 & 1, err, LA_KV8_TIMEOUT) && bar_wait(m_full(i & 3), i >> 2 & 1, err, LA_KV8_TIMEOUT);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const Kv8Meta &mt = meta[i & 3];
-                odd |= (mt.odd & kOddV) != 0;
+                const Kv8Meta *mt = &meta[i & 3];
+                odd |= (mt->flags & kOddV) != 0;
                 if (!idle) {
                     // 32 keys at a time: t relative to the maximum as it stands, then
                     // the weights, over columns of S that are read already.  One
                     // copy of this code: unrolled, the roles' code does not fit
                     // the instruction cache (5 us per pair of tiles).
-                    const bool cached = kt >= sq.ntiles;
-                    if (!cached && (mt.odd & kMixed)) {
-                        keep = mixed_scores(p, ts, &exps[i & 3], sq.first, in ? myrow : -1, kt * kTileK, min(sq.rows - kt * kTileK, kTileK), qf, m, l);
-                        qf = 1.f;
+                    bool cached = kt >= sq.ntiles;
+                    const float top = static_cast<float>(mt->top);
+                    if (r == -INFINITY) d = top - kTop;
+                    if (__any_sync(0xffffffffu, top - d < kTopLow || top - d > kUnitHigh) || (mt->flags & ~kOddV)) {
+                        if (i >= first + 2) {   // this group's O holds its tile i - 2
+                            ok = __all_sync(0xffffffffu, bar_wait(o_full(b), (i - 2) >> 1 & 1, err, LA_KV8_TIMEOUT));
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        keep.r = r, keep.d = d, keep.l = l, keep.qf = qf;
+                        keep.grp = grp, keep.row = row, keep.units = units, keep.it = it, keep.first = first, keep.end = end, keep.i = i, keep.kt = kt;
+                        keep.myrow = myrow, keep.myhead = myhead, keep.lanes = lanes, keep.ts = ts, keep.to = to, keep.in = in, keep.odd = odd;
+                        begin_tile<HD>(p, u, ts, to, *mt, exps[i & 3], kt, in ? myrow : -1, i >= first + 2, keep);
+                        r = keep.r, d = keep.d, l = keep.l, qf = keep.qf;
+                        grp = b = keep.grp, row = keep.row, units = keep.units, it = keep.it, first = keep.first, end = keep.end, i = keep.i, kt = keep.kt;
+                        myrow = keep.myrow, myhead = keep.myhead, lanes = keep.lanes, ts = keep.ts, to = keep.to, in = keep.in, odd = keep.odd;
+                        sq = u.sq, mt = &meta[i & 3], cached = kt >= sq.ntiles;
                     }
 #pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
                         uint32_t v[32];
                         tmem_ld_32x32b_x32(ts + 32 * k, v);
-                        const int live = mt.live[k], vx = mt.vx[k];
-                        const float f = mt.kf[k] * qf, add = static_cast<float>(vx) - (m == -INFINITY ? 0.f : m);
+                        const int live = mt->live[k];
+                        const float ux = static_cast<float>(mt->vx[k]) - d;   // u of this group
+                        const float f = mt->kf[k] * qf, add = ux - (r == -INFINITY ? 0.f : r);
                         tmem_ld_wait_for(v);
                         if (live < 32 || !cached) {
                             uint32_t see = live >= 32 ? 0xffffffffu : (1u << live) - 1u;   // keys that this row sees
-                            if (!cached) {
-                                const int key = kt * kTileK + 32 * k;
-                                if (!in) see = 0;
-                                else if (p.a.vis)
-                                    see &= key < 256 ? p.a.vis[(static_cast<long long>(sq.first) + myrow) * 8 + key / 32] : 0u;
-                                else
-                                    see &= myrow >= key + 31 ? 0xffffffffu : myrow < key ? 0u : (2u << (myrow - key)) - 1u;
-                            }
+                            if (!cached) see &= new_rows_seen(p, sq.first, in ? myrow : -1, kt * kTileK + 32 * k);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) v[e] = see >> e & 1u ? v[e] : 0xff800000u;   // -infinity
                         }
@@ -1516,12 +1734,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                             v[e + 2] = __float_as_uint(y.x);
                             v[e + 3] = __float_as_uint(y.y);
                         }
-                        x0 = fmaxf(x0, x1);   // past the maximum by this much
-                        const bool grow = m == -INFINITY ? x0 > -INFINITY : x0 > kLazy;
+                        x0 = fmaxf(x0, x1) - ux;   // past r by this much
+                        const bool grow = r == -INFINITY ? x0 > -INFINITY : x0 > kLazy;
                         if (__any_sync(0xffffffffu, grow)) {
-                            // a whole number past the first, so that scaling by 2^-by rounds nothing
-                            const float by = !grow ? 0.f : m == -INFINITY ? x0 : ceilf(x0), alpha = !grow ? 1.f : m == -INFINITY ? 0.f : ex2(-by);
-                            if (grow) m = m == -INFINITY ? x0 : m + by;
+                            const float by = !grow ? 0.f : ceilf(x0), alpha = !grow ? 1.f : r == -INFINITY ? 0.f : ex2(-by);
+                            if (grow) r = r == -INFINITY ? by : r + by;
                             l *= alpha;
 #pragma unroll
                             for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) - by);
@@ -1537,8 +1754,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                                 }
                                 tmem_st_32x32b_x16(ts + 16 * q, w);
                             }
-                            if (i >= first + 2) {   // this group's O holds its tile i - 2
-                                ok = __all_sync(0xffffffffu, bar_wait(o_full(b), (i - 2) >> 1 & 1, err, LA_KV8_TIMEOUT));
+                            if (i >= first + 2 || mt->flags >= kFar) {   // this group's O holds its tile i - 2, or far groups of this one
+                                if (i >= first + 2) ok = __all_sync(0xffffffffu, bar_wait(o_full(b), (i - 2) >> 1 & 1, err, LA_KV8_TIMEOUT));
                                 if (!ok) break;
                                 tc_fence_after();
                                 for (int q = 0; q < HD / 16; ++q) {
@@ -1562,14 +1779,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                             w[e] = pack_f16(x, y);
                         }
                         const float2 sum = halves(add2_f32(s0, s1));
-                        l += (sum.x + sum.y) * power_of(-vx);
+                        l += (sum.x + sum.y) * ex2(fminf(-ux, 126.f));   // a far group: 0
                         tmem_st_32x32b_x16(ts + 16 * k, w);
                     }
                     if (!ok) break;
-                    if (!cached && (mt.odd & kMixed)) {
-                        l = mixed_sum(keep, m);
-                        qf = qfs[row];
-                    }
+                    if (l < 0.f) r = keep.own_r, d = keep.own_d, l = keep.own_l, qf = qfs[row];   // behind own_scores
                     tmem_st_wait();
                 }
                 tc_fence_before();
@@ -1578,11 +1792,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             }
             it = end;
             if (!ok) break;
-            float fa = 0.f, fb = 0.f, M = m, L = l;
+            float fa = 0.f, fb = 0.f, R = r, D = d, L = l;
             if (first < end) {
                 // Both groups' maxima and sums, once all products are done; then
                 // each group writes half of the dims.
-                tmem_st_pair(ts + kTileK / 2, m, l);
+                tmem_st_four(ts + kTileK / 2, r, d, l);
                 tmem_st_wait();
                 tc_fence_before();
                 if (lane == 0 && (warp & 3) == 0) odds[grp] = odd;
@@ -1595,20 +1809,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 if (!ok) break;
                 tc_fence_after();
                 ++units;
-                const float2 x = tmem_ld_pair(tmem + lanes + kColS + kTileK / 2), y = tmem_ld_pair(tmem + lanes + kColS + 128 + kTileK / 2);
+                const float4 x = tmem_ld_four(tmem + lanes + kColS + kTileK / 2), y = tmem_ld_four(tmem + lanes + kColS + 128 + kTileK / 2);
                 odd = (odds[0] | odds[1]) != 0;
-                M = fmaxf(x.x, y.x);
-                fa = x.y == 0.f ? 0.f : ex2(x.x - M);
-                fb = y.y == 0.f ? 0.f : ex2(y.x - M);
-                L = (x.y == 0.f ? 0.f : fa * x.y) + (y.y == 0.f ? 0.f : fb * y.y);
-                // a group that saw no key may have an O that was never written
-                if (x.y == 0.f) fa = -1.f;
-                if (y.y == 0.f) fb = -1.f;
+                // a group that saw no key (a sum of 0) may have an O that was never written
+                const bool xs = x.z != 0.f, ys = y.z != 0.f;
+                R = fmaxf(x.x, y.x);
+                D = !xs ? y.y : !ys ? x.y : fmaxf(x.y, y.y);
+                L = (xs ? x.z * ex2(x.x - R) : 0.f) + (ys ? y.z * ex2(y.x - R) : 0.f);
+                fa = xs ? ex2((x.x - R) + (x.y - D)) : -1.f;
+                fb = ys ? ex2((y.x - R) + (y.y - D)) : -1.f;
             } else {
                 fa = fb = -1.f;
             }
             if (idle) continue;
-            const float inv = L == 0.f ? 0.f : 1.f / L;
+            const float inv = L == 0.f ? 0.f : ex2(D) / L;
             const int slot = 2 * blockIdx.x + (u.begins ? 1 : 0), d0 = grp * (HD / 2);
             __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + (sq.first + myrow) * p.a.out_stride + myhead * HD + d0;
             float *part = p.part + (static_cast<long long>(slot) * kTileQ + row) * HD + d0;
@@ -1654,7 +1868,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                     for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4 *>(part + 16 * k + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
             }
-            if (!u.all && in && grp == 0) *reinterpret_cast<float2 *>(p.part_ml + (static_cast<long long>(slot) * kTileQ + row) * 2) = make_float2(M, L);
+            if (!u.all && in && grp == 0) *reinterpret_cast<float4 *>(p.part_ml + (static_cast<long long>(slot) * kTileQ + row) * 4) = make_float4(R, D, L, 0.f);
         }
     }
     __syncthreads();
@@ -1697,41 +1911,41 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv8_join(const __grid_constant
     for (int j = threadIdx.x; (j & ~31) < n * group; j += kJoinThreads) {
         const bool on = j < n * group;
         const int i = i0 + (on ? j / group : 0), first = w0 + j % group, r = i / (HD / 4), d = 4 * (i % (HD / 4));
-        float mx = -INFINITY, L = 0.f;
+        float4 rdl = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);   // r, d, L so far
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        auto add = [&](float m, float l, float4 v) {
-            const float mn = fmaxf(mx, m), base = mn == -INFINITY ? 0.f : mn, f0 = ex2(mx - base), f1 = ex2(m - base);
-            L = L * f0 + l * f1;
+        auto add = [&](const float4 &y, const float4 &v) {   // y.z != 0: a piece that saw a key
+            const float R = fmaxf(rdl.x, y.x), D = fmaxf(rdl.y, y.y), e0 = rdl.x - R, e1 = y.x - R;
+            const float f0 = ex2(e0 + (rdl.y - D)), f1 = ex2(e1 + (y.y - D));
             acc.x = acc.x * f0 + v.x * f1;
             acc.y = acc.y * f0 + v.y * f1;
             acc.z = acc.z * f0 + v.z * f1;
             acc.w = acc.w * f0 + v.w * f1;
-            mx = mn;
+            rdl = make_float4(R, D, rdl.z * ex2(e0) + y.z * ex2(e1), 0.f);
         };
 #pragma unroll 1
         for (int w = first; on && w <= w1; w += BATCH * group) {
-            float2 ml[BATCH];
+            float4 ml[BATCH];
             float4 v[BATCH];
 #pragma unroll
             for (int b = 0; b < BATCH; ++b) {
                 const int ww = min(w + b * group, w1);
                 const long long rec = static_cast<long long>(2 * ww + (ww == w0 ? 1 : 0)) * p.q_tile + r;
-                ml[b] = *reinterpret_cast<const float2 *>(p.part_ml + rec * 2);
+                ml[b] = *reinterpret_cast<const float4 *>(p.part_ml + rec * 4);
                 v[b] = *reinterpret_cast<const float4 *>(p.part + rec * HD + d);
             }
 #pragma unroll
             for (int b = 0; b < BATCH; ++b)
-                if (w + b * group <= w1 && ml[b].y != 0.f) add(ml[b].x, ml[b].y, v[b]);   // 0: a piece that saw no key
+                if (w + b * group <= w1 && ml[b].z != 0.f) add(ml[b], v[b]);
         }
 #pragma unroll 1
         for (int o = 1; o < group; o <<= 1) {
-            const float m = __shfl_xor_sync(0xffffffffu, mx, o), l = __shfl_xor_sync(0xffffffffu, L, o);
+            const float4 y = make_float4(__shfl_xor_sync(0xffffffffu, rdl.x, o), __shfl_xor_sync(0xffffffffu, rdl.y, o), __shfl_xor_sync(0xffffffffu, rdl.z, o), 0.f);
             const float4 v = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o),
                                          __shfl_xor_sync(0xffffffffu, acc.z, o), __shfl_xor_sync(0xffffffffu, acc.w, o));
-            if (l != 0.f) add(m, l, v);
+            if (y.z != 0.f) add(y, v);
         }
         if (!on || j % group != 0) continue;
-        const float inv = L == 0.f ? 0.f : 1.f / L;
+        const float inv = rdl.z == 0.f ? 0.f : ex2(rdl.y) / rdl.z;
         const int qv = x.qv0 + r;
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + (x.first + qv / p.gq) * p.a.out_stride + (x.head * p.gq + qv % p.gq) * HD + d;
         const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
@@ -1751,7 +1965,7 @@ constexpr int kRowsUnitCost = 14, kTilesUnitCost = 4;
 constexpr int kRowsPerSm = 4;   // most CTAs of k_kv8_rows per SM
 
 int64_t kv8_workspace_bytes(const la_kv8_cache &c, int nsm) {
-    const int64_t part = static_cast<int64_t>(nsm) * std::max(kRowsPerSm * kRowsQ, kTileQ) * 2 * (c.head_dim + 2) * 4;
+    const int64_t part = static_cast<int64_t>(nsm) * std::max(kRowsPerSm * kRowsQ, kTileQ) * 2 * (c.head_dim + 4) * 4;
     const int64_t splits = static_cast<int64_t>(nsm) * kRowsPerSm * sizeof(Kv8Split);
     const int64_t plans = (std::max<int64_t>(6ll * c.n_seqs + c.n_pages, 4ll * c.n_pages) + 16) * 4;
     return (std::max(part + splits, plans) + 255) / 256 * 256;
@@ -1801,7 +2015,7 @@ static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     if (keep_whole(p, unit_bound(p), tiles, 8, 32)) p.whole = 1, p.workers = static_cast<int>(std::min<long long>(unit_bound(p), 1 << 20));
     p.part = static_cast<float *>(ws);
     p.part_ml = p.part + static_cast<long long>(nsm) * kRowsPerSm * 2 * kRowsQ * HD;
-    p.split = reinterpret_cast<Kv8Split *>(p.part_ml + static_cast<long long>(nsm) * kRowsPerSm * 2 * kRowsQ * 2);
+    p.split = reinterpret_cast<Kv8Split *>(p.part_ml + static_cast<long long>(nsm) * kRowsPerSm * 2 * kRowsQ * 4);
     static std::atomic<unsigned long long> configured{0};
     unsigned long long bit = 0;
     if (attrs_needed(configured, &bit)) {
@@ -1832,7 +2046,7 @@ static cudaError_t tiles_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     if (keep_whole(p, unit_bound(p), tiles, 5, 64)) p.whole = 1, p.workers = static_cast<int>(std::min<long long>(unit_bound(p), 1 << 20));
     p.part = static_cast<float *>(ws);
     p.part_ml = p.part + static_cast<long long>(nsm) * 2 * kTileQ * HD;
-    p.split = reinterpret_cast<Kv8Split *>(p.part_ml + static_cast<long long>(nsm) * 2 * kTileQ * 2);
+    p.split = reinterpret_cast<Kv8Split *>(p.part_ml + static_cast<long long>(nsm) * 2 * kTileQ * 4);
     static std::atomic<unsigned long long> configured{0};
     unsigned long long bit = 0;
     if (attrs_needed(configured, &bit)) {

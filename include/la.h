@@ -420,8 +420,12 @@ int la_kv8_workspace(const la_kv8_cache *c, int64_t *bytes);
 /* out[r] = sum over the keys j that row r sees of softmax_j(scale * q[r] . K_j) V_j,
  * where the keys are the lens[s] cached tokens of its sequence and its visible
  * new rows.  Sums and the softmax are fp32; the products' operands are fp16
- * with power-of-two factors (e4m3 and bf16 values are exact in them, the
- * softmax weights rounded to 11 bits); out is rounded once to bf16.  A row
+ * with power-of-two factors: e4m3 values are exact in them, q and new rows to
+ * 2^-23 of their largest value, the softmax weights are rounded to 11 bits or
+ * to 2^-19 of the row's largest weight, whatever the sizes of the values that
+ * they meet.  (Where values that a row sees differ by more than 2^70, the small
+ * ones may be lost beside the large ones' sum.)  Sums past fp32's range become
+ * infinite; out is rounded once to bf16.  A row
  * that sees nothing gives 0.  Values of keys that a row does not see, and
  * bytes behind a sequence's last token, never reach it, NaN and infinities
  * included.  Results do not depend on other sequences' contents but may
