@@ -240,6 +240,9 @@ __device__ __forceinline__ float bf16_bits(uint32_t h) { return __uint_as_float(
 __device__ __forceinline__ int exponent_of(float scale) { return static_cast<int>((__float_as_uint(scale) >> 23) & 255u) - 127; }
 __device__ __forceinline__ float power_of(int e) { return __uint_as_float(static_cast<unsigned>(min(max(e + 127, 1), 254)) << 23); }
 __device__ __forceinline__ bool is_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
+// a * b for factors on scores, within fp32's normal numbers: 0 times a masked
+// key's -infinity, and infinity times a score of 0, would be NaN.
+__device__ __forceinline__ float factor(float a, float b) { return fminf(fmaxf(a * b, 1.17549435e-38f), 3.40282347e38f); }
 // Exponent x such that |v| < 2^(x + 15) for the largest finite |v| = amax: v * 2^-x fits fp16.
 __device__ __forceinline__ int fit_f16(float amax) { return max(exponent_of(amax) - 14, kKv8MinExp); }
 
@@ -328,7 +331,7 @@ __device__ __forceinline__ void rows_softmax(float (&sc)[NJ][4], int live, float
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {   // rows g (elements 0, 1 of a product) and g + 8 (2, 3)
-        const float f = kf * qf[h];
+        const float f = factor(kf, qf[h]);
         float mx = -INFINITY;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) mx = fmaxf(mx, fmaxf(sc[j][2 * h], sc[j][2 * h + 1]));
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
             uint4 *dst = reinterpret_cast<uint4 *>(smem + Lay::q_off + r * Lay::q_row + (part >> 1) * Lay::q_piece + (part & 1) * (HD / 4));
 #pragma unroll
             for (int i = 0; i < NP; ++i) dst[i] = make_uint4(scaled_f16(w[i].x, f), scaled_f16(w[i].y, f), scaled_f16(w[i].z, f), scaled_f16(w[i].w, f));
-            if (part == 0) sh_qf[r] = power_of(qx) * p.scale_log2;
+            if (part == 0) sh_qf[r] = factor(power_of(qx), p.scale_log2);
         }
         __syncthreads();
         const uint8_t *my_q = smem + Lay::q_off + g * Lay::q_row + t * Lay::q_piece;   // row g; row g + 8 lies 8 rows behind
@@ -994,7 +997,7 @@ __device__ __forceinline__ void own_scores(const Kv8Args &p, const Kv8Piece &u, 
                 const uint32_t see = (live <= 0 ? 0u : live >= 16 ? 0xffffu : (1u << live) - 1u) & new_rows_seen(p, u.sq.first, row, key0 + 32 * (k >> 1)) >> 16 * (k & 1);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    const float z = see >> e & 1u ? __uint_as_float(v[e]) * ((mixed ? power_of(ex.k[16 * k + e]) : mt.kf[0]) * s.qf) : -INFINITY;
+                    const float z = see >> e & 1u ? __uint_as_float(v[e]) * factor(mixed ? power_of(ex.k[16 * k + e]) : mt.kf[0], s.qf) : -INFINITY;
                     zmax = fmaxf(zmax, z);
                     v[e] = __float_as_uint(z);
                 }
@@ -1034,7 +1037,7 @@ __device__ __forceinline__ void far_group(const Kv8Args &p, const Kv8Piece &u, u
     const int live = mt.live[k], key = (kt - u.sq.ntiles) * kTileK + 32 * k;   // its page is in the pool: it has keys
     const int page = p.c.table[static_cast<long long>(u.s) * p.c.max_pages + (key >> p.page_log2)];
     const uint8_t *v8 = static_cast<const uint8_t *>(p.c.v) + kv8_block(p.c, p.a.layer, page, u.head) * (p.c.page * HD) + (key & (p.c.page - 1));
-    const float f = mt.kf[k] * s.qf, ux = static_cast<float>(mt.vx[k]) - s.d;
+    const float f = factor(mt.kf[k], s.qf), ux = static_cast<float>(mt.vx[k]) - s.d;
     float w[32], top = -INFINITY;
     {
         uint32_t v[32];
@@ -1663,7 +1666,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
 #pragma unroll
                     for (int k = 0; k < NW; ++k)
                         st_shared_u32x4(qat(r, k), scaled_f16(x[k].x, f), scaled_f16(x[k].y, f), scaled_f16(x[k].z, f), scaled_f16(x[k].w, f));
-                    if (part == 0) qfs[r] = power_of(qx) * p.scale_log2;
+                    if (part == 0) qfs[r] = factor(power_of(qx), p.scale_log2);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -1713,7 +1716,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                         tmem_ld_32x32b_x32(ts + 32 * k, v);
                         const int live = mt->live[k];
                         const float ux = static_cast<float>(mt->vx[k]) - d;   // u of this group
-                        const float f = mt->kf[k] * qf, add = ux - (r == -INFINITY ? 0.f : r);
+                        const float f = factor(mt->kf[k], qf), add = ux - (r == -INFINITY ? 0.f : r);
                         tmem_ld_wait_for(v);
                         if (live < 32 || !cached) {
                             uint32_t see = live >= 32 ? 0xffffffffu : (1u << live) - 1u;   // keys that this row sees

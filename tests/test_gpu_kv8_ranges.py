@@ -180,3 +180,30 @@ def test_a_huge_row_that_all_see(lib, rows, hd, score, size):
     out = cache.attention(q, k, v, row_start=starts([rows]), max_rows=rows)
     cache.status()
     within(out, *exact(cache, q, k, v, [list(range(r + 1)) for r in range(rows)]))
+
+
+@pytest.mark.parametrize("rows,hd,page", [(1, 128, 64), (4, 64, 32), (40, 128, 32), (140, 64, 128)])
+@pytest.mark.parametrize("scale,k_scale,zero", [(1e-38, 2.0 ** -60, False), (1e-45, 1.0, False), (3e38, 2.0 ** 60, True), (2.9e38, 2.0 ** -60, True)])
+def test_factors_past_fp32(lib, rows, hd, page, scale, k_scale, zero):
+    """scale * K's scale below or above what fp32 holds: scores of 0, for the keys that a row sees alone.  Tolerance: bf16's
+    2^-8 of the mean, fp32 sums of n equal weights n 2^-24 of the mean magnitude."""
+    import torch
+    n = 77
+    cache = build(lib, [n], hd, page, 1, seed=2)
+    cache.k_scale[:] = k_scale
+    q, k, v = normal((rows, 2, hd), 1), normal((rows, 1, hd), 2), normal((rows, 1, hd), 3)
+    if zero:
+        cache.k[:] = 0
+        k[:] = 0
+        q[0] *= 2.0 ** 100
+    out = cache.attention(q, k, v, row_start=starts([rows]), scale=scale, max_rows=rows)
+    cache.status()
+    ids = cache.table[0, :-(-n // page)].long()
+    V = torch.from_numpy(M.E4M3[cache.v[0, ids, 0].cpu().numpy()]) * cache.v_scale[0, ids, 0].cpu().double()[:, None, None]
+    V = V.transpose(1, 2).reshape(-1, hd)[:n]
+    got = out.cpu().double()
+    for r in range(rows):
+        Vr = torch.cat([V, v[:r + 1, 0].cpu().double()])
+        want = Vr.mean(0)
+        tol = 2.0 ** -8 * want.abs() + len(Vr) * 2.0 ** -24 * Vr.abs().mean(0)
+        assert torch.all((got[r] - want).abs() <= tol), (r, got[r], want)
