@@ -93,10 +93,6 @@ int attention_body(const la_kv8_cache *c, const la_kv8_attn *args, void *ws, int
             return bad(where, "k_stride and v_stride must be multiples of 8 and at least n_kv_heads * head_dim");
     }
     if (a.scale == 0.f) a.scale = c->head_dim == 128 ? 0.08838834764831845f : 0.125f;
-    const int64_t room = static_cast<int64_t>(c->max_pages) * c->page;
-    if (!a.row_start) a.max_rows = 1;
-    if (a.max_rows <= 0 || a.max_rows > a.n_rows) a.max_rows = a.n_rows;
-    if (a.max_len <= 0 || a.max_len > room) a.max_len = static_cast<int32_t>(room);
     int nsm = 0;
     if ((rc = check_workspace(c, ws, ws_bytes, &nsm, where)) != LA_OK) return rc;
     const cudaError_t e = kv8_attention_launch(*c, a, ws, nsm, static_cast<cudaStream_t>(stream));

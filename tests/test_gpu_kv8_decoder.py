@@ -439,3 +439,26 @@ def test_a_cache_on_another_device_is_refused(lib):
     cache.device = torch.device("cuda", 5)
     with pytest.raises(ValueError, match="device"):
         lib.Decoder(dev, 4, 5, 4, 256, kv_cache=cache)
+
+
+def test_idle_slots_do_not_change_the_work(lib):
+    """A decoder in the last of 1, 64 or 2048 slots, the others empty: the same kernels per step, the same tokens and the
+    same logits, bit for bit."""
+    dims = SMALL["gqa-hd128"]
+    dev = lib.DeviceWeights(weights("gqa-hd128", 5))
+    p = synth.uniform_tokens(300, dims.vocab, seed=6)
+    outs, counts = [], []
+    for n_seqs in (1, 64, 2048):
+        cache = new_cache(lib, dims, 64, n_seqs=n_seqs, max_seq=1024, n_pages=20)
+        dec = lib.Decoder(dev, 5, 7, 7, 1024, kv_cache=cache, slot=n_seqs - 1)
+        dec.prefill(p)
+        got = run(dec, 3)
+        for _ in range(2):
+            got.append(([dec.ar_step()], dec.debug_logits().copy()))
+        outs.append(got)
+        counts.append(dec.stats()["kernel_launches"])
+        cache.status()
+        dec.close()
+    assert counts[1:] == counts[:-1], counts
+    same(outs[0], outs[1])
+    same(outs[0], outs[2])
