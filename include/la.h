@@ -497,9 +497,15 @@ int la_kv8_status(const la_kv8_cache *c, uint32_t *bits, void *stream);
  * as with la_create; the model is LA_BF16, its n_layers, n_kv_heads and
  * head_dim are the cache's, and max_seq <= max_pages * page.  The decoder
  * copies the struct, not the arrays: they outlive it, and table, lens and refs
- * stay where they are (la_kv8_compact in place is fine between calls).  A
- * step's own rows meet the attention at 16 bits; the cached ones are e4m3, so
- * tokens may differ from those of la_create's cache.  A slot serves one
+ * stay where they are (la_kv8_compact in place is fine between calls).
+ * Rounding: q, a pass's own k and v and the attention's output are bf16 (one
+ * rounding each, without the low halves that la_create's cache and GEMM inputs
+ * have); cached tokens are e4m3.  So tokens may differ from those of la_create's
+ * cache, and la_step is not exact here: a candidate meets the candidates before
+ * it at bf16, where la_ar_step meets them as stored bytes, whose scale depends
+ * on how the rows were grouped.  Logits of a step's row 0 are those of
+ * la_ar_step up to the kernels' own error; a candidate's differ by some 1e-2 for logits
+ * of order one, which can turn a close choice.  A slot serves one
  * decoder; what it holds before la_prefill does not matter: la_prefill and
  * la_import_state empty the slot first; la_destroy leaves it as it is (free it
  * with la_kv8_free).  Calls on decoders that share a cache must not overlap,

@@ -462,3 +462,38 @@ def test_idle_slots_do_not_change_the_work(lib):
     assert counts[1:] == counts[:-1], counts
     same(outs[0], outs[1])
     same(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("name,page,n", [("gqa-hd128", 64, 60), ("mha-hd64", 32, 31)])
+def test_a_step_is_close_to_single_steps(lib, name, page, n):
+    """la_step against la_ar_step from the same state, the step's candidate being what the single steps give: the last token's
+    logits agree within both sides' contract, the candidates' within what e4m3 adds (PIN of test_kv8_step_exactness), and
+    so do the tokens where that leaves no choice."""
+    from test_kv8_step_exactness import PIN
+    dims = SMALL[name]
+    dev = lib.DeviceWeights(weights(name, 3))
+    N, W, G = 5, 4, 3
+    where = la.used_rows(N, W, G)
+    for seed in range(3):
+        p = [int(t) for t in synth.uniform_tokens(n, dims.vocab, seed=20 + seed)]
+        cache = new_cache(lib, dims, page, max_seq=256)
+        a, b = (lib.Decoder(dev, N, W, G, 256, kv_cache=cache, slot=s) for s in (0, 2))
+        o = b.prefill(p)
+        s0 = b.export_state()
+        tokens, single = [], []
+        for _ in range(N):
+            tokens.append(b.ar_step())
+            single.append(b.debug_logits()[0].copy())
+        a.import_state(p + [o], s0["window"], [(o, tuple(tokens[:N - 1]))])
+        acc = a.step()
+        step = a.debug_logits()
+        assert np.abs(step[0] - single[0]).max() <= 2 * TOL
+        for m in range(1, N):
+            row = step[where.index(la.cand_row(N, W, 0, m))]
+            assert np.abs(row - single[m]).max() <= PIN + 2 * TOL
+        sure = [top2_margin(x) > 2 * (PIN + 2 * TOL) for x in single]
+        upto = sure.index(False) if False in sure else N
+        assert acc[:upto] == tokens[:upto][:len(acc)] and len(acc) >= upto
+        cache.status()
+        a.close()
+        b.close()
