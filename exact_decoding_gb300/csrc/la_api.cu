@@ -1523,7 +1523,7 @@ static int la_fork_body(la_handle *a, la_handle *b) {
     if (!a->kv8 || !b->kv8 || a->kv8c.table != b->kv8c.table || a->kv8c.k != b->kv8c.k || a->kv8_slot == b->kv8_slot)
         return fail(LA_ERR_INVALID_ARG, "la_fork needs two slots of one 8-bit cache");
     if (a->N != b->N || a->W != b->W || a->cap != b->cap || a->V != b->V || a->opts.pool_policy != b->opts.pool_policy ||
-        a->d != b->d || a->nh != b->nh || a->F != b->F)
+        a->d != b->d || a->nh != b->nh || a->F != b->F || a->dims.rms_eps != b->dims.rms_eps || a->dims.rope_base != b->dims.rope_base)
         return fail(LA_ERR_INVALID_ARG, "la_fork needs the same model, N, W, pool capacity and policy");
     if (!a->prefilled) return fail(LA_ERR_STATE, "la_fork before la_prefill");
     if (a->P + b->M + b->N + 2 > b->max_seq) return fail(LA_ERR_CAPACITY, "state too long for max_seq");

@@ -523,7 +523,9 @@ int la_create_kv8(const la_model_dims *dims, const la_weights *weights, const la
  * la_kv8_fork its cached tokens, without running the model.  Both are
  * la_create_kv8 decoders of the same model on the same cache, with the same N,
  * W, pool capacity and policy and dst's max_seq large enough; dst's slot is
- * emptied first.  The two then decode independently.
+ * emptied first.  The two then decode independently.  (Of the model the sizes,
+ * rms_eps and rope_base are compared, not the weights: two uploads of one model
+ * are one model.)
  * Errors: INVALID_ARG, STATE (src has no state), CAPACITY, CUDA. */
 int la_fork(la_handle *src, la_handle *dst);
 

@@ -497,3 +497,22 @@ def test_a_step_is_close_to_single_steps(lib, name, page, n):
         cache.status()
         a.close()
         b.close()
+
+
+@pytest.mark.parametrize("kw", [dict(rope_base=5000.0), dict(rms_eps=1e-3)])
+def test_fork_refuses_another_model_of_the_same_sizes(lib, kw):
+    import dataclasses
+    dims = SMALL["mha-hd64"]
+    w = weights("mha-hd64", 7)
+    cache = new_cache(lib, dims, 32, max_seq=256)
+    a = lib.Decoder(w, 4, 5, 4, 256, kv_cache=cache, slot=0)
+    a.prefill(synth.uniform_tokens(50, dims.vocab, seed=8))
+    other = dict(w, dims=dataclasses.replace(w["dims"], **kw))
+    b, same_model = lib.Decoder(other, 4, 5, 4, 256, kv_cache=cache, slot=1), lib.Decoder(w, 4, 5, 4, 256, kv_cache=cache, slot=2)
+    with pytest.raises(lib.LaError) as e:
+        b.fork_from(a)
+    assert e.value.code == INVALID and cache.lens.tolist() == [50, 0, 0]
+    same_model.fork_from(a)                 # its own upload of the same weights
+    same([(a.step(), a.debug_logits())], [(same_model.step(), same_model.debug_logits())])
+    for d in (a, b, same_model):
+        d.close()
