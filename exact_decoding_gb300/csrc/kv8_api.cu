@@ -1,5 +1,6 @@
 // Entry points of the paged 8-bit KV cache (la_kv8_*, include/la.h): argument
 // checks on the host, then launches on the caller's stream.
+#include <atomic>
 #include <cstdio>
 
 #include "abi_guard.h"
@@ -38,7 +39,7 @@ int la::kv8_check_cache(const la_kv8_cache *c, const char *where) {
 namespace {
 
 int sm_count(int *n) {
-    static int cached[64] = {};   // 0: not asked yet; any thread writes the same value
+    static std::atomic<int> cached[64] = {};   // 0: not asked yet; any thread writes the same value
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_failed("cudaGetDevice", e);

@@ -507,3 +507,21 @@ def test_as_many_slots_as_there_may_be(lib, hd, page, rows):
             cache.status()
         assert e.value.code == CAPACITY
     cache.status()
+
+
+def test_workspace_is_the_same_for_all_threads(lib):
+    """The first calls of several threads at once ask for the device's size together."""
+    import threading
+    cache = build(lib, [5], 64, 32, 1)
+    got, go = [0] * 16, threading.Barrier(16)
+
+    def ask(i):
+        go.wait()
+        got[i] = lib.la_kv8_workspace(cache.struct)
+
+    threads = [threading.Thread(target=ask, args=(i,)) for i in range(16)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert got == [cache.workspace().numel()] * 16
