@@ -251,7 +251,7 @@ __device__ __forceinline__ int fit_f16(float amax) { return max(exponent_of(amax
 // k_kv8_rows: 16 query vectors per unit (all heads of a KV head's group for
 // one row, or some rows).  Bound by the cache's bytes: every byte is read
 // once and meets 16 query vectors (64 sequences of up to 8192 tokens, 8 KV
-// heads: 548 MB in 94.0 us).  The warps of a CTA take the unit's tiles
+// heads: 548 MB in 97 us).  The warps of a CTA take the unit's tiles
 // (one page each) in turn, each with its own running softmax and its own ring
 // of page blocks in shared memory, so no barrier is met inside a unit; they
 // are joined through shared memory at the unit's end.  A block of K or V of
@@ -776,7 +776,7 @@ struct Tiles {
     static_assert(tiles_off + (LA_KV8_MAX_SEQS + 1) * 8 <= 227 * 1024, "shared memory of a block");
 };
 // TMEM columns: S of even and odd tiles (P over their first halves; behind it,
-// once a group is through with a unit, its rows' maximum and sum), then their O.
+// once a group is through with a unit, its rows' r, d and sum), then their O.
 constexpr uint32_t kColS = 0, kColO = 256, kColAll = 512;
 
 struct Kv8Meta {
@@ -796,7 +796,7 @@ constexpr int kFar = 4;     // << k: group k's page has a V scale more than 2^kN
 // it: values keep at least 15 + 24 - kSpread = 23 bits below their piece's
 // largest.  Else each row has its own, or a huge row would leave nothing of the
 // others, for query vectors too that do not see it.  The code for that is apart:
-// in line it cost every call 7 us (121 rows of 32 heads over 2k tokens, 31.6 us; so 32.9).
+// in line it cost every call 7 us (121 rows of 32 heads over 2k tokens, 31.6 us; so 32.7).
 constexpr int kSpread = 16;
 struct Kv8Exps {
     signed char k[kTileK], v[kTileK];   // of fit_f16, -60 .. 113

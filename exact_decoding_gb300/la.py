@@ -425,7 +425,9 @@ class Kv8Cache:
     `tensors` adopts existing tensors by those names.  Calls run on `stream`
     (default: torch's current stream of the cache's device) and do not
     synchronise; status() does, and raises what they met.  Calls that overlap
-    (streams, captured graphs) need a `workspace` of their own (workspace())."""
+    (streams, captured graphs) need a `workspace` of their own (workspace()).
+    On another stream than their own, the cache's tensors and the arguments
+    have to live until that stream is through with them."""
 
     def __init__(self, n_layers: int, n_pages: int, page: int, n_kv_heads: int, head_dim: int, n_seqs: int,
                  max_pages: int, device="cuda", tensors: Optional[dict] = None):
@@ -533,7 +535,8 @@ class Kv8Cache:
         """Attention of the rows q [rows, heads, dim] over their sequences'
         cached tokens and the visible new rows k, v [rows, kv heads, dim];
         see la_kv8_attention.  max_rows and max_len are bounds that the host
-        knows (0: none); they steer the split of the work only.  Returns out."""
+        knows (0: none); they steer the split of the work only, and a batch
+        without max_rows is slow.  Returns out."""
         rows, qs = self._rows(q, "q", 0)
         heads = q.shape[1]
         if out is None and stream is None:
@@ -562,8 +565,9 @@ class Kv8Cache:
 
     def append(self, k, v, row_start=None, row_idx=None, stored=None, max_rows: int = 0, workspace=None, stream=None):
         """Append the rows of k, v [layers, rows, kv heads, dim] (or the rows
-        row_idx of them) behind the sequences; see la_kv8_append.  Returns
-        stored [seqs], the rows stored for each sequence (without `stored`, a
+        row_idx of them) behind the sequences; see la_kv8_append.  max_rows:
+        the most rows of one sequence; with many slots the call is slow without.
+        Returns stored [seqs], the rows stored for each sequence (without `stored`, a
         tensor that the next append overwrites)."""
         n = k.shape[1] if k.dim() == 4 else 0
         ks, vs = self._layers(k, "k", n), self._layers(v, "v", n)
