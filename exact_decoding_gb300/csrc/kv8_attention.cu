@@ -1689,8 +1689,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 const Kv8Meta *mt = &meta[i & 3];
                 odd |= (mt->flags & kOddV) != 0;
                 if (!idle) {
-                    // 32 keys at a time: t relative to the maximum as it stands, then
-                    // the weights, over columns of S that are read already.  One
+                    // What is rare first (begin_tile).  Then 32 keys at a time: the weights'
+                    // exponents at r and d as they stand, then the weights, over
+                    // columns of S that are read already.  One
                     // copy of this code: unrolled, the roles' code does not fit
                     // the instruction cache (5 us per pair of tiles).
                     bool cached = kt >= sq.ntiles;
