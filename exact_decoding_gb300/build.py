@@ -17,7 +17,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libla.so")
 BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["gemm.cu", "elementwise.cu", "attention.cu", "spec.cu", "la_api.cu", "noalloc.cu", "kv8.cu", "kv8_attention.cu",
-           "kv8_api.cu", "kv8_decoder.cu"]
+           "kv8_api.cu", "kv8_decoder.cu", "kv8_rope.cu", "gemv_w4.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
 

@@ -15,6 +15,8 @@
 namespace la {
 
 int set_last_error(int code, const char *msg);
+// SMs of the current device (an error code, with the message set).
+int sm_count(int *n);
 
 template <typename Body>
 int abi_guard(const char *where, Body &&body) noexcept {

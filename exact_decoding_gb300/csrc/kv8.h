@@ -53,6 +53,7 @@ int64_t kv8_workspace_bytes(const la_kv8_cache &c, int nsm);
 // *launched (or nullptr) grows by the kernels launched.
 cudaError_t kv8_attention_launch(const la_kv8_cache &c, const la_kv8_attn &a, void *ws, int nsm, cudaStream_t s,
                                  int64_t *launched = nullptr);
+cudaError_t kv8_norm_rope_launch(const la_kv8_cache &c, const la_kv8_qkv &a, int nsm, cudaStream_t s);
 cudaError_t kv8_append_launch(const la_kv8_cache &c, const la_kv8_rows &r, int *ws, cudaStream_t s);
 cudaError_t kv8_fork_launch(const la_kv8_cache &c, const int *src, const int *dst, int n, cudaStream_t s);
 cudaError_t kv8_free_launch(const la_kv8_cache &c, const int *slots, const int *keep, int n, cudaStream_t s);

@@ -36,9 +36,7 @@ int la::kv8_check_cache(const la_kv8_cache *c, const char *where) {
     return LA_OK;
 }
 
-namespace {
-
-int sm_count(int *n) {
+int la::sm_count(int *n) {
     static std::atomic<int> cached[64] = {};   // 0: not asked yet; any thread writes the same value
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -52,6 +50,8 @@ int sm_count(int *n) {
     if (dev >= 0 && dev < 64) cached[dev] = *n;
     return LA_OK;
 }
+
+namespace {
 
 int check_workspace(const la_kv8_cache *c, const void *ws, int64_t bytes, int *nsm, const char *where) {
     const int rc = sm_count(nsm);
@@ -97,6 +97,37 @@ int attention_body(const la_kv8_cache *c, const la_kv8_attn *args, void *ws, int
     int nsm = 0;
     if ((rc = check_workspace(c, ws, ws_bytes, &nsm, where)) != LA_OK) return rc;
     const cudaError_t e = kv8_attention_launch(*c, a, ws, nsm, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? LA_OK : cuda_failed(where, e);
+}
+
+int norm_rope_body(const la_kv8_cache *c, const la_kv8_qkv *args, void *stream) {
+    const char *where = "la_kv8_norm_rope";
+    int rc = kv8_check_cache(c, where);
+    if (rc != LA_OK) return rc;
+    if (!args) return bad(where, "null arguments");
+    const la_kv8_qkv &a = *args;
+    if (a.type != LA_F32 && a.type != LA_BF16) return bad(where, "type must be LA_F32 or LA_BF16", LA_ERR_UNSUPPORTED);
+    if ((a.q_weight || a.k_weight) && a.weight_type != LA_F32 && a.weight_type != LA_BF16)
+        return bad(where, "weight_type must be LA_F32 or LA_BF16", LA_ERR_UNSUPPORTED);
+    if (a.n_heads < 1 || a.n_heads > (1 << 18) || a.n_heads % c->n_kv_heads) return bad(where, "n_heads must be a multiple of n_kv_heads, at most 2^18");
+    if (a.n_rows < 0 || a.n_rows > (1 << 22)) return bad(where, "n_rows out of range (0 .. 2^22)");
+    if (!a.pos && !a.row_start && a.n_rows != c->n_seqs)
+        return bad(where, "without pos and row_start every slot has one row: n_rows must be n_seqs");
+    if (!(a.eps >= 0.f) || a.eps > 3e38f) return bad(where, "eps must be a finite number, not negative");
+    if (!a.inv_freq && (!(a.rope_base > 0.f) || a.rope_base > 3e38f)) return bad(where, "rope_base must be a finite number above 0");
+    if (!a.v != !a.v_out) return bad(where, "v and v_out come together or not at all");
+    if (a.n_rows == 0) return LA_OK;
+    if (!a.q || !a.k || !a.q_out || !a.k_out) return bad(where, "null q, k, q_out or k_out");
+    for (const void *x : {a.q, a.k, a.v, static_cast<const void *>(a.q_out), static_cast<const void *>(a.k_out), static_cast<const void *>(a.v_out)})
+        if (!aligned16(x)) return bad(where, "q, k, v and the outputs must be 16-byte aligned");
+    const int64_t qd = static_cast<int64_t>(a.n_heads) * c->head_dim, kd = static_cast<int64_t>(c->n_kv_heads) * c->head_dim;
+    auto strided = [](int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0; };
+    if (!strided(a.q_stride, qd) || !strided(a.q_out_stride, qd) || !strided(a.k_stride, kd) || !strided(a.k_out_stride, kd) ||
+        (a.v && (!strided(a.v_stride, kd) || !strided(a.v_out_stride, kd))))
+        return bad(where, "strides must be multiples of 8 and at least the row's width");
+    int nsm = 0;
+    if ((rc = sm_count(&nsm)) != LA_OK) return rc;
+    const cudaError_t e = kv8_norm_rope_launch(*c, a, nsm, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LA_OK : cuda_failed(where, e);
 }
 
@@ -188,6 +219,9 @@ int la_kv8_workspace(const la_kv8_cache *c, int64_t *bytes) {
 }
 int la_kv8_attention(const la_kv8_cache *c, const la_kv8_attn *a, void *workspace, int64_t workspace_bytes, void *stream) {
     return abi_guard("la_kv8_attention", [&] { return attention_body(c, a, workspace, workspace_bytes, stream); });
+}
+int la_kv8_norm_rope(const la_kv8_cache *c, const la_kv8_qkv *a, void *stream) {
+    return abi_guard("la_kv8_norm_rope", [&] { return norm_rope_body(c, a, stream); });
 }
 int la_kv8_append(const la_kv8_cache *c, const la_kv8_rows *r, void *workspace, int64_t workspace_bytes, void *stream) {
     return abi_guard("la_kv8_append", [&] { return append_body(c, r, workspace, workspace_bytes, stream); });

@@ -95,6 +95,27 @@ class la_kv8_rows(ctypes.Structure):
                 ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("stored", ctypes.c_void_p)]
 
 
+class la_kv8_qkv(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("weight_type", ctypes.c_int32), ("eps", ctypes.c_float), ("rope_base", ctypes.c_float),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64), ("v_out_stride", ctypes.c_int64),
+                ("row_start", ctypes.c_void_p), ("pos", ctypes.c_void_p), ("depth", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+                ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p)]
+
+
+class la_logprobs_args(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("vocab", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("n_tokens", ctypes.c_int32), ("n_top", ctypes.c_int32), ("stride", ctypes.c_int64),
+                ("logits", ctypes.c_void_p), ("tokens", ctypes.c_void_p), ("logprob", ctypes.c_void_p),
+                ("entropy", ctypes.c_void_p), ("top_ids", ctypes.c_void_p), ("top_logprob", ctypes.c_void_p)]
+
+
+_KV8_QKV = struct.Struct("@4i2f6q12P")     # la_kv8_qkv
+_LOGPROBS = struct.Struct("@5i4xq6P")      # la_logprobs_args
+assert _KV8_QKV.size == ctypes.sizeof(la_kv8_qkv) and _LOGPROBS.size == ctypes.sizeof(la_logprobs_args)
 _KV8_ATTN = struct.Struct("@5i4q6Pf4x")    # la_kv8_attn
 _KV8_ROWS = struct.Struct("@3i4q5P")       # la_kv8_rows
 assert _KV8_ATTN.size == ctypes.sizeof(la_kv8_attn) and _KV8_ROWS.size == ctypes.sizeof(la_kv8_rows)
@@ -141,6 +162,10 @@ def load_library():
     lib.la_kv8_compact.argtypes = [KV8, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                    ctypes.c_int64, ctypes.c_void_p]
     lib.la_kv8_status.argtypes = [KV8, ctypes.POINTER(ctypes.c_uint32), ctypes.c_void_p]
+    lib.la_kv8_norm_rope.argtypes = [KV8, ctypes.POINTER(la_kv8_qkv), ctypes.c_void_p]
+    lib.la_logprobs.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    lib.la_gemv_w4.argtypes = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                               ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]
     lib.la_destroy.argtypes = [H]
     lib.la_destroy.restype = None
     lib.la_strerror.argtypes = [ctypes.c_int]
@@ -151,7 +176,7 @@ def load_library():
                  "la_import_state", "la_debug_logits", "la_gemm_bf16", "la_gemm_bf16_noalloc", "la_gemm_status",
                  "la_selftest_timeout", "la_gemm_schedule", "la_step_tables", "la_kv8_workspace", "la_kv8_attention",
                  "la_kv8_append", "la_kv8_fork", "la_kv8_free", "la_kv8_compact", "la_kv8_status", "la_create_kv8",
-                 "la_fork"):
+                 "la_fork", "la_kv8_norm_rope", "la_logprobs", "la_gemv_w4"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -342,6 +367,19 @@ def la_kv8_attention(cache: la_kv8_cache, args: la_kv8_attn, workspace_ptr: int,
     _check(load_library().la_kv8_attention(cache, args, workspace_ptr, workspace_bytes, stream), "la_kv8_attention")
 
 
+def la_kv8_norm_rope(cache: la_kv8_cache, args: la_kv8_qkv, stream: Optional[int] = None) -> None:
+    _check(load_library().la_kv8_norm_rope(cache, args, stream), "la_kv8_norm_rope")
+
+
+def la_logprobs(args: la_logprobs_args, stream: Optional[int] = None) -> None:
+    _check(load_library().la_logprobs(ctypes.byref(args), stream), "la_logprobs")
+
+
+def la_gemv_w4(x_ptr: int, x_stride: int, w_ptr: int, scales_ptr: int, y_ptr: int, y_stride: int, rows: int, out: int, k: int,
+               group: int, stream: Optional[int] = None) -> None:
+    _check(load_library().la_gemv_w4(x_ptr, x_stride, w_ptr, scales_ptr, y_ptr, y_stride, rows, out, k, group, stream), "la_gemv_w4")
+
+
 def la_kv8_append(cache: la_kv8_cache, rows: la_kv8_rows, workspace_ptr: int, workspace_bytes: int,
                   stream: Optional[int] = None) -> None:
     _check(load_library().la_kv8_append(cache, rows, workspace_ptr, workspace_bytes, stream), "la_kv8_append")
@@ -371,6 +409,113 @@ def la_kv8_status(cache: la_kv8_cache, stream: Optional[int] = None) -> None:
 def la_destroy(h) -> None:
     if h:
         load_library().la_destroy(h)
+
+
+# ---------------------------------------------------------------------------- operators on tensors
+def _on(index: int, stream, fn, where: str, *args) -> None:
+    """fn(*args, stream) with CUDA device `index` current; stream None: torch's current one there."""
+    import torch
+    c = torch._C
+    st = c._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if c._cuda_getDevice() == index:
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, st)
+    if rc:
+        _check(rc, where)
+
+
+def _empty(stream, *shape, dtype, device):
+    """A new tensor whose memory belongs to the stream that writes it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _cuda_index(t, name: str) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device, not on {t.device}")
+    return t.get_device()
+
+
+def logprobs(logits, tokens=None, top: int = 0, out=None, stream=None):
+    """Log probabilities of given tokens, the entropy, and the most probable
+    tokens of every row of logits [rows, vocab] (float32 or bfloat16, rows at
+    any stride); see la_logprobs.  tokens: int32 [rows] or [rows, n], or None;
+    top: alternatives of a row, 0 .. 32.  Returns (logprob like tokens or
+    None, entropy [rows], ids [rows, top] int32, their log probabilities
+    [rows, top]); `out` has tensors of these shapes to write to.  Runs on
+    `stream` (default: torch's current one of the logits' device) and does not
+    synchronise."""
+    import torch
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16) or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError(f"logits must be float32 or bfloat16 [rows, vocab] with dense rows, not {logits.dtype} {tuple(logits.shape)} "
+                         f"strides {logits.stride()}")
+    index = _cuda_index(logits, "logits")
+    rows, vocab = logits.shape
+    n = 0
+    if tokens is not None:
+        if tokens.dtype is not torch.int32 or tokens.dim() not in (1, 2) or tokens.shape[0] != rows or not tokens.is_contiguous() or tokens.get_device() != index:
+            raise ValueError(f"tokens must be a contiguous int32 tensor [{rows}] or [{rows}, n] on {logits.device}, not {tokens.dtype} "
+                             f"{tuple(tokens.shape)} on {tokens.device}")
+        n = tokens.shape[1] if tokens.dim() == 2 else 1
+    if out is None:
+        f = {"dtype": torch.float32, "device": logits.device}
+        out = (None if tokens is None else _empty(stream, *tokens.shape, **f), _empty(stream, rows, **f),
+               _empty(stream, rows, max(top, 0), dtype=torch.int32, device=logits.device), _empty(stream, rows, max(top, 0), **f))
+    else:
+        want = ((None if tokens is None else tokens.shape, torch.float32), ((rows,), torch.float32), ((rows, top), torch.int32), ((rows, top), torch.float32))
+        for name, t, (shape, dtype) in zip(("logprob", "entropy", "ids", "top logprob"), out, want):
+            if (t is None) != (shape is None) or t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != index):
+                raise ValueError(f"out's {name} must be {'None' if shape is None else f'a contiguous {dtype} tensor {tuple(shape)} on {logits.device}'}")
+    lp, entropy, ids, best = out
+    args = _LOGPROBS.pack(rows, vocab, LA_F32 if logits.dtype is torch.float32 else LA_BF16, n, top, logits.stride(0) if rows > 1 else vocab,
+                          logits.data_ptr(), tokens.data_ptr() if n else 0, lp.data_ptr() if n else 0, entropy.data_ptr(),
+                          ids.data_ptr() if top > 0 else 0, best.data_ptr() if top > 0 else 0)
+    _on(index, stream, load_library().la_logprobs, "la_logprobs", args)
+    return out
+
+
+class W4Matrix:
+    """A matrix [out, k] of 4-bit weights: w uint8 [out, k / 2] (the even k in a
+    byte's low half), scales bfloat16 [out, k / group], group 32, 64 or 128.
+    Element (o, k) is (q - 8) * scales[o, k / group]; see la_gemv_w4."""
+
+    def __init__(self, w, scales):
+        import torch
+        self._torch = torch
+        if w.dtype is not torch.uint8 or w.dim() != 2 or not w.is_contiguous() or scales.dtype is not torch.bfloat16 or scales.dim() != 2 \
+                or not scales.is_contiguous() or scales.device != w.device or scales.shape[0] != w.shape[0] or scales.shape[1] < 1 \
+                or 2 * w.shape[1] % scales.shape[1]:
+            raise ValueError(f"W4Matrix needs contiguous uint8 [out, k / 2] and bfloat16 [out, k / group] on one device, not {w.dtype} "
+                             f"{tuple(w.shape)} on {w.device} and {scales.dtype} {tuple(scales.shape)} on {scales.device}")
+        self._index = _cuda_index(w, "w")
+        self.w, self.scales = w, scales
+        self.out, self.k, self.group = w.shape[0], 2 * w.shape[1], 2 * w.shape[1] // scales.shape[1]
+        self._fn = load_library().la_gemv_w4
+
+    def matvec(self, x, out=None, stream=None):
+        """x W^T for the bfloat16 rows x [rows, k] (or [k]), as float32 [rows, out]
+        (or [out]).  For a batch of single tokens: the matrix is read once for
+        every 16 rows.  Runs on `stream` (default: torch's current one of the
+        matrix's device) and does not synchronise."""
+        torch = self._torch
+        rows = x.shape[0] if x.dim() == 2 else 1
+        if x.dtype is not torch.bfloat16 or x.dim() not in (1, 2) or x.shape[-1] != self.k or x.stride(-1) != 1 or x.get_device() != self._index:
+            raise ValueError(f"x must be bfloat16 [rows, {self.k}] with dense rows on {self.w.device}, not {x.dtype} {tuple(x.shape)} strides "
+                             f"{x.stride()} on {x.device}")
+        shape = (*x.shape[:-1], self.out)
+        if out is None:
+            out = _empty(stream, *shape, dtype=torch.float32, device=self.w.device)
+        elif out.dtype is not torch.float32 or out.shape != shape or (out.stride(-1) != 1 and self.out > 1) or out.get_device() != self._index:
+            raise ValueError(f"out must be float32 {shape} with dense rows on {self.w.device}, not {out.dtype} {tuple(out.shape)} strides "
+                             f"{out.stride()} on {out.device}")
+        _on(self._index, stream, self._fn, "la_gemv_w4", x.data_ptr(), x.stride(0) if rows > 1 else self.k, self.w.data_ptr(), self.scales.data_ptr(),
+            out.data_ptr(), out.stride(0) if rows > 1 else self.out, rows, self.out, self.k, self.group)
+        return out
 
 
 # ---------------------------------------------------------------------------- owners
@@ -467,7 +612,7 @@ class Kv8Cache:
         self._fn = {}
         for name, kinds in (("la_kv8_attention", (P, ctypes.c_int64)), ("la_kv8_append", (P, ctypes.c_int64)),
                             ("la_kv8_fork", (P, I)), ("la_kv8_free", (P, I)),
-                            ("la_kv8_compact", (P, P, P, ctypes.c_int64)), ("la_kv8_status", ())):
+                            ("la_kv8_compact", (P, P, P, ctypes.c_int64)), ("la_kv8_status", ()), ("la_kv8_norm_rope", ())):
             f = lib[name]
             f.argtypes, f.restype = [P, P, *kinds, P], ctypes.c_int
             self._fn[name] = f
@@ -492,12 +637,13 @@ class Kv8Cache:
         """Address of an int32 device vector of n values; 0 for None."""
         return 0 if t is None else self._checked(t, name, self._torch.int32, (n,))
 
-    def _rows(self, t, name, heads):
-        """bf16 [rows, heads, dim] with dense (heads, dim): rows, row stride."""
+    def _rows(self, t, name, heads, dtype=None):
+        """bf16 (or `dtype`) [rows, heads, dim] with dense (heads, dim): rows, row stride."""
         sh, st = t.shape, t.stride()
-        if t.dtype is not self._torch.bfloat16 or t.get_device() != self._index or len(sh) != 3 or sh[2] != self.head_dim \
+        dtype = dtype or self._torch.bfloat16
+        if t.dtype is not dtype or t.get_device() != self._index or len(sh) != 3 or sh[2] != self.head_dim \
                 or (heads and sh[1] != heads) or st[2] != 1 or (st[1] != sh[2] and sh[1] > 1):
-            raise ValueError(f"{name} must be a bfloat16 tensor [rows, {heads or 'heads'}, {self.head_dim}] on {self.device} "
+            raise ValueError(f"{name} must be a {str(dtype)[6:]} tensor [rows, {heads or 'heads'}, {self.head_dim}] on {self.device} "
                              f"with dense heads, not {t.dtype} {tuple(sh)} strides {st} on {t.device}")
         return sh[0], st[0] if sh[0] > 1 else sh[1] * sh[2]
 
@@ -539,11 +685,8 @@ class Kv8Cache:
         without max_rows is slow.  Returns out."""
         rows, qs = self._rows(q, "q", 0)
         heads = q.shape[1]
-        if out is None and stream is None:
-            out = self._torch.empty((rows, heads, self.head_dim), dtype=q.dtype, device=self.device)
-        elif out is None:
-            with self._torch.cuda.stream(stream):   # its memory belongs to the stream that writes it
-                out = self._torch.empty((rows, heads, self.head_dim), dtype=q.dtype, device=self.device)
+        if out is None:
+            out = _empty(stream, rows, heads, self.head_dim, dtype=q.dtype, device=self.device)
         n, os_ = self._rows(out, "out", heads)
         kp = vp = ks = vs = 0
         if k is not None and v is not None:
@@ -562,6 +705,51 @@ class Kv8Cache:
                               0 if vis is None else self._checked(vis, "vis", self._torch.int32, (rows, 8)), out.data_ptr(), scale)
         self._call(self._fn["la_kv8_attention"], "la_kv8_attention", args, ws, wb, stream=stream)
         return out
+
+    def norm_rope(self, q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-5, rope_base: float = 10000.0, inv_freq=None,
+                  row_start=None, pos=None, depth=None, out=None, stream=None):
+        """Rows of a projection for attention() and append(): the heads of q
+        [rows, heads, dim] and k [rows, kv heads, dim] (float32 or bfloat16) are
+        normed (with q_weight, k_weight [dim]; None: not), rotated by their
+        positions behind the sequences' cached tokens, and rounded to bfloat16,
+        with v rounded along; see la_kv8_norm_rope.  pos [rows]: positions that
+        have nothing to do with the cache; depth [rows]: places of a tree's
+        rows.  Returns (q, k) or (q, k, v), or writes to `out`, which may be
+        the bfloat16 inputs themselves."""
+        torch = self._torch
+        dtype = q.dtype
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"q must be float32 or bfloat16, not {dtype}")
+        rows, qs = self._rows(q, "q", 0, dtype)
+        heads, ins = q.shape[1], (q, k) if v is None else (q, k, v)
+        strides = [qs]
+        for t, name in zip(ins[1:], "kv"):
+            n, st = self._rows(t, name, self.n_kv_heads, dtype)
+            if n != rows:
+                raise ValueError(f"{name} must have q's {rows} rows, not {n}")
+            strides.append(st)
+        if out is None:
+            out = tuple(_empty(stream, *t.shape, dtype=torch.bfloat16, device=self.device) for t in ins)
+        elif len(out) != len(ins):
+            raise ValueError(f"out must be {len(ins)} tensors, as q, k{'' if v is None else ' and v'}")
+        out_strides = []
+        for t, name, h in zip(out, ("out's q", "out's k", "out's v"), (heads, self.n_kv_heads, self.n_kv_heads)):
+            n, st = self._rows(t, name, h)
+            if n != rows:
+                raise ValueError(f"{name} must have q's {rows} rows, not {n}")
+            out_strides.append(st)
+        kind = torch.bfloat16 if (q_weight is None and k_weight is None) else (k_weight if q_weight is None else q_weight).dtype
+        if kind not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"q_weight and k_weight must be float32 or bfloat16, not {kind}")
+        vec = lambda t, name, dt, n: 0 if t is None else self._checked(t, name, dt, (n,))  # noqa: E731
+        none = [0] if v is None else []
+        args = _KV8_QKV.pack(heads, rows, LA_F32 if dtype is torch.float32 else LA_BF16, LA_F32 if kind is torch.float32 else LA_BF16, eps, rope_base,
+                             *strides, *none, *out_strides, *none, self._ints(row_start, "row_start", self.n_seqs + 1), self._ints(pos, "pos", rows),
+                             self._ints(depth, "depth", rows), *[t.data_ptr() for t in ins], *none, vec(q_weight, "q_weight", kind, self.head_dim),
+                             vec(k_weight, "k_weight", kind, self.head_dim), vec(inv_freq, "inv_freq", torch.float32, self.head_dim // 2),
+                             *[t.data_ptr() for t in out], *none)
+        self._call(self._fn["la_kv8_norm_rope"], "la_kv8_norm_rope", args, stream=stream)
+        return tuple(out)
 
     def append(self, k, v, row_start=None, row_idx=None, stored=None, max_rows: int = 0, workspace=None, stream=None):
         """Append the rows of k, v [layers, rows, kv heads, dim] (or the rows

@@ -242,6 +242,35 @@ int la_export_state(la_handle *h, la_state_t *st);
  * tokens, loads window and pool.  Errors: INVALID_ARG, CAPACITY, CUDA. */
 int la_import_state(la_handle *h, const la_state_t *st);
 
+/* Log probabilities out of logits that another model computed. */
+typedef struct la_logprobs_args {
+    int32_t rows;             /* 0 .. 2^24 */
+    int32_t vocab;            /* 1 .. 2^28 */
+    int32_t type;             /* of the logits: LA_F32 or LA_BF16 */
+    int32_t n_tokens;         /* given tokens of a row, or 0 */
+    int32_t n_top;            /* alternatives of a row, 0 .. 32 and at most vocab */
+    int64_t stride;           /* elements between rows, >= vocab (any: rows need no more than their type's alignment) */
+    const void *logits;       /* device [rows][vocab] */
+    const int32_t *tokens;    /* device [rows][n_tokens], or NULL with n_tokens 0 */
+    float *logprob;           /* device [rows][n_tokens], or NULL with n_tokens 0 */
+    float *entropy;           /* device [rows] or NULL */
+    int32_t *top_ids;         /* device [rows][n_top], or NULL with n_top 0 */
+    float *top_logprob;       /* device [rows][n_top], or NULL with n_top 0 */
+} la_logprobs_args;
+
+/* Of softmax(z) for each row z of logits: the natural logarithms of the
+ * probabilities of its given tokens, the entropy (in nats), and its n_top most
+ * probable tokens in falling order, the lower number first among equals.  In
+ * one pass, in fp32; a probability near 1 keeps its logarithm's bits.  A logit
+ * of -infinity is a token that cannot occur: its logarithm is -infinity, and it
+ * is no alternative (-1 and -infinity fill the list up).  So is a given token
+ * outside 0 .. vocab - 1.  A row of nothing but -infinity has an entropy of 0.
+ * A NaN or +infinity makes all of a row's logarithms and its entropy NaN;
+ * top_ids is then the order of the values, NaN left out.  Asynchronous, no
+ * workspace; results do not depend on the order of threads.  No passage: a
+ * library extension.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int la_logprobs(const la_logprobs_args *a, void *stream);
+
 /* Debug utility (no passage): the rows are those the verification and the
  * lookahead branch read (paper-graph-ui page, section 3.4).
  * Logits of the last step's used rows, fp32, to host[rows * vocab]: row 0,
@@ -286,6 +315,20 @@ int la_gemm_bf16(const void *x, const void *w, float *y, int32_t rows, int32_t o
 #define LA_NOALLOC_SCRATCH_FLOATS (4 * 1024 * 1024)
 int la_gemm_bf16_noalloc(const void *x, const void *w, float *y, int32_t rows, int32_t out, int32_t k,
                          int32_t splits, void *stream);
+
+/* Products of a few vectors with a matrix of 4-bit weights:
+ *   y[r][o] = sum_k x[r][k] * (q[o][k] - 8) * scales[o][k / group]
+ * x device bf16 [rows][k], 16-byte aligned, rows x_stride elements apart (a
+ * multiple of 8, at least k); w device [out][k / 2] bytes, 16-byte aligned: q of
+ * an even k in the low half of byte k / 2, of the odd k behind it in the high
+ * half; scales device bf16 [out][k / group], group 32, 64 or 128, a divisor of
+ * k; y device fp32, rows y_stride elements apart.  0 <= rows <= 256; the
+ * matrix is read once for every 16 rows, so it is for a batch of single tokens.
+ * Sums are fp32 of exact products, a group's sum meets its scale once; results
+ * are deterministic.  Asynchronous, no workspace, no bounded waits.
+ * No passage: a library extension.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int la_gemv_w4(const void *x, int64_t x_stride, const void *w, const void *scales, float *y, int64_t y_stride,
+               int32_t rows, int32_t out, int32_t k, int32_t group, void *stream);
 
 /* Error status of the standalone GEMMs (la_gemm_bf16, la_gemm_bf16_noalloc)
  * on the current device.  Their kernels wait on TMA loads and tensor-core
@@ -434,6 +477,44 @@ int la_kv8_workspace(const la_kv8_cache *c, int64_t *bytes);
  * Errors: INVALID_ARG, UNSUPPORTED, CAPACITY (workspace too small), CUDA. */
 int la_kv8_attention(const la_kv8_cache *c, const la_kv8_attn *a, void *workspace, int64_t workspace_bytes,
                      void *stream);
+
+/* Rows of a projection, on their way to la_kv8_attention and la_kv8_append:
+ * q, k and v of the new rows (columns of one fused projection are fine), as
+ * fp32 or bf16; the outputs are bf16.  Strides are in elements between rows,
+ * multiples of 8 and at least the row's width; q, k, v and the outputs are
+ * 16-byte aligned.  An output may be its input (bf16, same address and
+ * stride); outputs overlap nothing else. */
+typedef struct la_kv8_qkv {
+    int32_t n_heads;          /* query heads, a multiple of the cache's n_kv_heads */
+    int32_t n_rows;           /* rows of all sequences together */
+    int32_t type;             /* of q, k and v: LA_F32 or LA_BF16 */
+    int32_t weight_type;      /* of q_weight and k_weight: LA_F32 or LA_BF16 */
+    float   eps;              /* of the norms, >= 0 */
+    float   rope_base;        /* > 0; not read with inv_freq */
+    int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride, v_out_stride;
+    const int32_t *row_start; /* device [n_seqs + 1] as in la_kv8_attn, or NULL: one row for every slot.  Rows of no slot
+                                 are left as they are */
+    const int32_t *pos;       /* device [n_rows] or NULL: the rows' positions, whatever the cache holds (row_start and
+                                 depth are not read) */
+    const int32_t *depth;     /* device [n_rows] or NULL: row r of slot s is at position lens[s] + depth[r]; NULL: at
+                                 lens[s] + its place among the slot's rows */
+    const void *q;            /* device [n_rows][n_heads * head_dim] */
+    const void *k;            /* device [n_rows][n_kv_heads * head_dim] */
+    const void *v;            /* likewise, or NULL with v_out */
+    const void *q_weight;     /* device [head_dim] or NULL: queries are not normed */
+    const void *k_weight;     /* device [head_dim] or NULL: keys are not normed */
+    const float *inv_freq;    /* device [head_dim / 2] or NULL: rope_base^(-2 i / head_dim) */
+    void *q_out, *k_out, *v_out;
+} la_kv8_qkv;
+
+/* For each head x of q and of k: n = x / sqrt(mean(x^2) + eps) * weight (n = x
+ * without a weight), then the rotation of the pairs (i, i + head_dim / 2) by
+ * position * inv_freq[i]; v is only rounded.  All in fp32, rounded once to
+ * bf16; the rotation's angles are exact to 2^-30 of a turn up to position
+ * 2^20, and to 2^-24 for every position.  Of the cache it reads the sizes,
+ * lens and status alone, before the rows are appended.  Asynchronous, without
+ * a workspace.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int la_kv8_norm_rope(const la_kv8_cache *c, const la_kv8_qkv *a, void *stream);
 
 /* Rows to append, all layers at once. */
 typedef struct la_kv8_rows {

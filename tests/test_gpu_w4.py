@@ -1,0 +1,101 @@
+"""Products with 4-bit weights (W4Matrix, la_gemv_w4) against their formula in 64 bits."""
+import numpy as np
+import pytest
+
+from helpers import ensure_built
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    ensure_built()
+    import exact_decoding_gb300 as e
+    return e
+
+
+def case(rows, out, k, group, seed=0, device="cuda"):
+    """x, packed weights and scales on the GPU, with y and its tolerance in 64 bits.
+
+    Tolerance: products of a bf16 number and a whole number up to 8 are exact in
+    fp32.  One matrix product adds 16 of them to a sum and may cut each term at
+    2^-23 of the largest, so it is off by 17 * 2^-23 of the terms' magnitudes at
+    most; a group takes group / 16 of them.  Its scale, the sum over the groups and
+    over at most 64 parts of k round by 2^-24 each."""
+    import torch
+    g = np.random.default_rng(seed)
+    x = torch.from_numpy(g.standard_normal((rows, k)) * np.exp(g.standard_normal((1, k)))).to(torch.bfloat16)
+    q = g.integers(0, 16, (out, k), dtype=np.uint8)
+    s = torch.from_numpy(np.exp(g.standard_normal((out, k // group))) * 0.01).to(torch.bfloat16)
+    w = torch.from_numpy(q[:, ::2] | (q[:, 1::2] << 4))
+    m = (q.astype(np.float64) - 8) * np.repeat(s.double().numpy(), group, 1)
+    xd = x.double().numpy()
+    y, a = xd @ m.T, np.abs(xd) @ np.abs(m).T
+    return x.to(device), w.to(device), s.to(device), y, a * (group / 16 * 17 * 2.0 ** -23 + (k // group + 66) * 2.0 ** -24)
+
+
+def close(got, want, tol):
+    d = np.abs(got.cpu().double().numpy() - want)
+    assert np.all(d <= tol), f"{(~(d <= tol)).sum()} of {d.size} off, worst {np.nanmax(d / tol):.3g} of the tolerance at {np.argwhere(~(d <= tol))[:3].tolist()}"
+
+
+@pytest.mark.parametrize("rows,out,k,group", [
+    (1, 1, 32, 32), (1, 16, 128, 128), (1, 17, 96, 32), (2, 33, 192, 64), (1, 300, 4096, 128), (8, 129, 640, 128), (9, 100, 1600, 64),
+    (16, 257, 1056, 32), (3, 4096, 512, 128), (5, 1000, 5120, 64), (17, 64, 256, 128), (33, 48, 384, 64), (256, 20, 128, 32),
+    (1, 5000, 128, 128), (16, 3, 28672, 128), (7, 2500, 2080, 32)])
+def test_products(lib, rows, out, k, group):
+    x, w, s, y, tol = case(rows, out, k, group, seed=rows + out)
+    m = lib.W4Matrix(w, s)
+    close(m.matvec(x), y, tol)
+    if rows == 1:
+        close(m.matvec(x[0]).view(1, -1), y, tol)
+
+
+def test_strides_and_order(lib):
+    """Rows of a wider buffer, and outputs into one, whose other columns stay as they were."""
+    import torch
+    x, w, s, y, tol = case(6, 70, 256, 64)
+    wide = torch.full((6, 300), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, 8:264] = x
+    out = torch.full((6, 99), -7.0, device="cuda")
+    got = lib.W4Matrix(w, s).matvec(wide[:, 8:264], out=out[:, 5:75]) if (wide.data_ptr() + 16) % 16 == 0 and 300 % 8 == 0 else None
+    if got is None:                                          # 300 is no multiple of 8: refused
+        with pytest.raises(lib.LaError):
+            lib.W4Matrix(w, s).matvec(wide[:, 8:264], out=out[:, 5:75])
+        wide = torch.full((6, 304), float("nan"), dtype=torch.bfloat16, device="cuda")
+        wide[:, 8:264] = x
+        got = lib.W4Matrix(w, s).matvec(wide[:, 8:264], out=out[:, 5:75])
+    close(got, y, tol)
+    assert torch.all(out[:, :5] == -7) and torch.all(out[:, 75:] == -7)
+
+
+def test_values_that_are_not_finite(lib):
+    """They reach their own row alone, everywhere in it (0 times infinity is NaN as well)."""
+    import torch
+    x, w, s, y, tol = case(4, 40, 256, 128)
+    x[2, 77] = float("inf")
+    got = lib.W4Matrix(w, s).matvec(x)
+    keep = [0, 1, 3]
+    close(got[keep], y[keep], tol[keep])
+    assert not torch.isfinite(got[2]).any()
+
+
+def test_repeats_and_graphs(lib):
+    """The same bits every time: alone, on another stream, and replayed from a graph with new vectors."""
+    import torch
+    x, w, s, y, tol = case(3, 900, 1024, 128)
+    m = lib.W4Matrix(w, s)
+    first = m.matvec(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = m.matvec(x, stream=side)
+    side.synchronize()
+    assert torch.equal(first, other)
+    out, xin = torch.empty_like(first), torch.zeros_like(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m.matvec(xin, out=out)
+    xin.copy_(x)
+    graph.replay()
+    assert torch.equal(first, out)
+    assert lib.W4Matrix(w, s).matvec(x[:0]).shape == (0, 900)
