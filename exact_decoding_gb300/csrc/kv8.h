@@ -50,8 +50,8 @@ __host__ __device__ inline int kv8_touched(int m, int page) { return m == 1 ? 1 
 // Workspace of one cache: the attention's partial results, or the plans of
 // append and compact (calls that overlap need a workspace each).
 int64_t kv8_workspace_bytes(const la_kv8_cache &c, int nsm);
-// *launched (or nullptr) grows by the kernels launched.
-cudaError_t kv8_attention_launch(const la_kv8_cache &c, const la_kv8_attn &a, void *ws, int nsm, cudaStream_t s,
+// window 0: none.  *launched (or nullptr) grows by the kernels launched.
+cudaError_t kv8_attention_launch(const la_kv8_cache &c, const la_kv8_attn &a, int window, int sinks, void *ws, int nsm, cudaStream_t s,
                                  int64_t *launched = nullptr);
 cudaError_t kv8_norm_rope_launch(const la_kv8_cache &c, const la_kv8_qkv &a, int nsm, cudaStream_t s);
 cudaError_t kv8_append_launch(const la_kv8_cache &c, const la_kv8_rows &r, int *ws, cudaStream_t s);

@@ -70,8 +70,8 @@ int workspace_body(const la_kv8_cache *c, int64_t *bytes) {
     return LA_OK;
 }
 
-int attention_body(const la_kv8_cache *c, const la_kv8_attn *args, void *ws, int64_t ws_bytes, void *stream) {
-    const char *where = "la_kv8_attention";
+// window 0: none
+int attention_body(const char *where, const la_kv8_cache *c, const la_kv8_attn *args, int32_t window, int32_t sinks, void *ws, int64_t ws_bytes, void *stream) {
     int rc = kv8_check_cache(c, where);
     if (rc != LA_OK) return rc;
     if (!args) return bad(where, "null arguments");
@@ -96,7 +96,7 @@ int attention_body(const la_kv8_cache *c, const la_kv8_attn *args, void *ws, int
     if (a.scale == 0.f) a.scale = c->head_dim == 128 ? 0.08838834764831845f : 0.125f;
     int nsm = 0;
     if ((rc = check_workspace(c, ws, ws_bytes, &nsm, where)) != LA_OK) return rc;
-    const cudaError_t e = kv8_attention_launch(*c, a, ws, nsm, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = kv8_attention_launch(*c, a, window, sinks, ws, nsm, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? LA_OK : cuda_failed(where, e);
 }
 
@@ -218,7 +218,15 @@ int la_kv8_workspace(const la_kv8_cache *c, int64_t *bytes) {
     return abi_guard("la_kv8_workspace", [&] { return workspace_body(c, bytes); });
 }
 int la_kv8_attention(const la_kv8_cache *c, const la_kv8_attn *a, void *workspace, int64_t workspace_bytes, void *stream) {
-    return abi_guard("la_kv8_attention", [&] { return attention_body(c, a, workspace, workspace_bytes, stream); });
+    return abi_guard("la_kv8_attention", [&] { return attention_body("la_kv8_attention", c, a, 0, 0, workspace, workspace_bytes, stream); });
+}
+int la_kv8_attention_window(const la_kv8_cache *c, const la_kv8_attn *a, int32_t window, int32_t sinks, void *workspace, int64_t workspace_bytes,
+                            void *stream) {
+    const char *where = "la_kv8_attention_window";
+    return abi_guard(where, [&] {
+        if (window < 1 || window > (1 << 30) || sinks < 0 || sinks > (1 << 30)) return bad(where, "window must be 1 .. 2^30 and sinks 0 .. 2^30");
+        return attention_body(where, c, a, window, sinks, workspace, workspace_bytes, stream);
+    });
 }
 int la_kv8_norm_rope(const la_kv8_cache *c, const la_kv8_qkv *a, void *stream) {
     return abi_guard("la_kv8_norm_rope", [&] { return norm_rope_body(c, a, stream); });

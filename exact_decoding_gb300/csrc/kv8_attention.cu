@@ -61,6 +61,7 @@ struct Kv8Args {
     int workers;
     int hinted;        // max_rows is the caller's
     float scale_log2;  // scale * log2(e)
+    int window, sinks; // of la_kv8_attention_window
     float *part;       // [workers][2][q_tile][head_dim] unnormalised sums
     float *part_ml;    // [workers][2][q_tile][4] r, d and L
     struct Kv8Split *split;   // [workers]
@@ -79,6 +80,7 @@ struct Kv8Seq {
     int len;                 // cached tokens
     int qtiles;              // tiles of query vectors
     int ctiles, ntiles;      // key tiles of the cache and of the new rows
+    int keep, skip;          // with a window: the cache's first `keep` tiles, then those `skip` behind
     // A unit's length in the flattened list: its key tiles behind unit_cost
     // empty ones, which stand for what a unit costs beside its tiles (its
     // queries, the first copies' latency, the join of the warps).  Where units
@@ -86,25 +88,44 @@ struct Kv8Seq {
     int ktiles;
 };
 
+// With a window (WIN) a row sees the first `sinks` and the last `window` of its
+// list of keys: the cached tokens in order, then the new rows that it sees, in
+// order.  Its window begins at place len + n - window of that list, n the new
+// rows that it sees: cached tokens before it are seen if they are among the
+// first, and tiles between the two that no row of the slot sees are left out of
+// the slot's tiles.  So a unit's work is what its rows see, but for tiles at the
+// two edges, in which keys are masked.
+template <bool WIN>
 __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Args &p, int s) {
     Kv8Seq q;
     q.rows = kv8_rows(p.c, p.a.row_start, p.a.n_rows, s, &q.first);
     q.len = kv8_len(p.c, s);
     q.qtiles = static_cast<int>((static_cast<long long>(q.rows) * p.gq + p.q_tile - 1) / p.q_tile);
     q.ctiles = (q.len + p.k_tile - 1) / p.k_tile;
+    if constexpr (WIN) {
+        const int first = min(max(q.len + (p.a.k && !p.a.vis ? 1 : 0) - p.window, 0), q.len);   // of the slot's earliest window
+        q.keep = (min(p.sinks, q.len) + p.k_tile - 1) / p.k_tile;
+        q.skip = max((first == q.len ? q.ctiles : first / p.k_tile) - q.keep, 0);
+        q.ctiles -= q.skip;
+    }
     q.ntiles = p.a.k && p.n_tile ? (q.rows + p.n_tile - 1) / p.n_tile : 0;
     q.ktiles = p.whole ? 1 : p.unit_cost + q.ctiles + q.ntiles;
     return q;
 }
 
+// The cached tile that is number ct of the slot's.
+template <bool WIN>
+__device__ __forceinline__ int kv8_tile(const Kv8Seq &q, int ct) { return WIN && ct >= q.keep ? ct + q.skip : ct; }
+
 // tiles[s] for s = 0 .. n_seqs; every thread of the CTA calls it.
+template <bool WIN>
 __device__ __forceinline__ void kv8_plan(const Kv8Args &p, long long *tiles, long long *warp_sum) {
     const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int per = (p.c.n_seqs + nt - 1) / nt;
     const int s0 = min(tid * per, p.c.n_seqs), s1 = min(s0 + per, p.c.n_seqs);
     long long mine = 0;
     for (int s = s0; s < s1; ++s) {
-        const Kv8Seq q = kv8_seq(p, s);
+        const Kv8Seq q = kv8_seq<WIN>(p, s);
         const long long t = static_cast<long long>(q.qtiles) * p.c.n_kv_heads * q.ktiles;
         tiles[s + 1] = t;
         mine += t;
@@ -154,6 +175,7 @@ struct Kv8Walk {
 };
 // With snap = unit_cost - 1 a share that begins in a unit's empty tiles begins
 // with the unit: a piece without key tiles would cost as much as one with some.
+template <bool WIN>
 __device__ __forceinline__ Kv8Walk kv8_walk(const Kv8Args &p, const long long *tiles) {
     const long long total = tiles[p.c.n_seqs];
     const int workers = kv8_workers(p, total), b = static_cast<int>(blockIdx.x), w = b + (threadIdx.x & 1);
@@ -161,7 +183,7 @@ __device__ __forceinline__ Kv8Walk kv8_walk(const Kv8Args &p, const long long *t
     if (b >= workers) return {0, 0};
     long long at = kv8_share(total, w, workers);   // even lanes: where the share begins, odd ones: where it ends
     if (p.snap > 0 && w < workers) {
-        const int s = kv8_find(tiles, p.c.n_seqs, at), kt = kv8_seq(p, s).ktiles;
+        const int s = kv8_find(tiles, p.c.n_seqs, at), kt = kv8_seq<WIN>(p, s).ktiles;
         const long long in_slot = at - tiles[s];
         const int in_unit = static_cast<int>(in_slot - kv8_div(in_slot, kt) * kt);
         if (in_unit <= p.snap) at -= in_unit;
@@ -174,10 +196,11 @@ struct Kv8Piece {
     bool all, begins;    // the whole unit; its first piece
     Kv8Seq sq;
 };
+template <bool WIN>
 __device__ __forceinline__ bool kv8_next(const Kv8Args &p, const long long *tiles, Kv8Walk &w, Kv8Piece &u) {
     if (w.at >= w.end) return false;
     u.s = kv8_find(tiles, p.c.n_seqs, w.at);
-    u.sq = kv8_seq(p, u.s);
+    u.sq = kv8_seq<WIN>(p, u.s);
     const int kt = u.sq.ktiles;
     const long long in_slot = w.at - tiles[u.s];
     const int unit = static_cast<int>(kv8_div(in_slot, kt));
@@ -217,6 +240,46 @@ __device__ __forceinline__ void kv8_note(const Kv8Args &p, const long long *tile
         x.nqv = u.nqv;
     }
     p.split[blockIdx.x] = x;
+}
+
+// ------------------------------------------------------------------ window
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+// The n lowest of x's bits that are set.
+__device__ __forceinline__ uint32_t low_set(uint32_t x, int n) {
+    uint32_t rest = x;
+    for (int i = 0; i < n && rest; ++i) rest &= rest - 1;
+    return x & ~rest;
+}
+// New rows that `row` of a slot with `rows` rows, the first at `first`, sees without a window.
+__device__ __noinline__ int kv8_seen(const Kv8Args &p, int first, int rows, int row) {
+    if (!p.a.k) return 0;
+    if (!p.a.vis) return row + 1;
+    int n = 0;
+    for (int w = 0; w < 8; ++w) n += __popc(p.a.vis[(static_cast<long long>(first) + row) * 8 + w] & low_bits(rows - 32 * w));
+    return n;
+}
+// Of new rows key .. key + 31 (key a multiple of 32) those that `row` sees with the window.
+__device__ __noinline__ uint32_t kv8_window_new(const Kv8Args &p, int first, int rows, int len, int row, int key) {
+    if (!p.a.vis) return low_bits(row + 1 - key) & (low_bits(p.sinks - len - key) | ~low_bits(row + 1 - p.window - key));
+    if (key >= 256) return 0u;
+    uint32_t word = 0;
+    int before = 0, all = 0;   // of the rows that it sees: those before the word
+    for (int w = 0; w < 8; ++w) {
+        const uint32_t x = p.a.vis[(static_cast<long long>(first) + row) * 8 + w] & low_bits(rows - 32 * w);
+        if (w == key / 32) {
+            word = x;
+            before = all;
+        }
+        all += __popc(x);
+    }
+    return word & (low_set(word, p.sinks - len - before) | ~low_set(word, all - p.window - before));
+}
+// Of cached tokens key .. key + 31 those that a row sees whose window begins at place `from`.
+__device__ __forceinline__ uint32_t kv8_window_old(const Kv8Args &p, int from, int key) { return low_bits(p.sinks - key) | ~low_bits(from - key); }
+// Whether some row of a piece may not see some of cached tokens key .. key + n - 1 of its tiles.
+__device__ __forceinline__ bool kv8_edge(const Kv8Args &p, const Kv8Seq &q, int last_row, int key, int n) {
+    const int seen = !p.a.k ? 0 : p.a.vis ? min(q.rows, 256) : last_row + 1;   // at most
+    return key + n > p.sinks && key < q.len + seen - p.window;
 }
 
 // ------------------------------------------------------------------ mma
@@ -370,7 +433,7 @@ __device__ __forceinline__ void rows_softmax(float (&sc)[NJ][4], int live, float
     }
 }
 
-template <int HD, int PAGE>
+template <int HD, int PAGE, bool WIN>
 __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::per_sm) k_kv8_rows(const __grid_constant__ Kv8Args p) {
     using Lay = Rows<HD, PAGE>;
     constexpr int NI = HD / 8;                    // 8-dim groups of the output
@@ -391,8 +454,8 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
     if (lane < NS) mbar_init(bars + lane * 8, 1);
     fence_barrier_init();
     pdl_wait();
-    kv8_plan(p, tiles, reinterpret_cast<long long *>(smem + Lay::sum_off));
-    Kv8Walk walk = kv8_walk(p, tiles);
+    kv8_plan<WIN>(p, tiles, reinterpret_cast<long long *>(smem + Lay::sum_off));
+    Kv8Walk walk = kv8_walk<WIN>(p, tiles);
     Kv8Piece u;
     int in_slot = 0, out_slot = 0;   // ring positions: the next block to load, the next to read
     uint32_t out_phase = 0;
@@ -400,7 +463,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
     bool noted = p.whole;
 
     for (;;) {
-        const bool any = kv8_next(p, tiles, walk, u);
+        const bool any = kv8_next<WIN>(p, tiles, walk, u);
         auto note = [&]() {
             if (!noted && tid == 0) kv8_note(p, tiles, any, u);
             noted = true;
@@ -424,7 +487,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
                 last_page = my_page;
                 last_vs = my_vs;
                 last_kf = my_kf;
-                my_page = i + lane < nc ? kv8_page(c, s, page0 + NW * (i + lane)) : -1;
+                my_page = i + lane < nc ? kv8_page(c, s, kv8_tile<WIN>(sq, page0 + NW * (i + lane))) : -1;
                 const long long blk = kv8_block(c, p.a.layer, max(my_page, 0), head);
                 my_kf = c.k_scale[blk];
                 my_vs = c.v_scale[blk];
@@ -480,6 +543,13 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
 #pragma unroll
         for (int i = 0; i < NI; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
+        int from[2] = {0, 0};   // where the rows' windows begin
+        if constexpr (WIN) {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h)
+                from[h] = sq.len + kv8_seen(p, sq.first, sq.rows, min(u.qv0 + g + 8 * h, u.qv0 + u.nqv - 1) / p.gq) - p.window;
+        }
+
         // ---- new rows, in the piece that begins the unit: one key at a time
         if (u.begins && p.a.k) {
             const int r0 = g < u.nqv ? (u.qv0 + g) / p.gq : -1, r1 = g + 8 < u.nqv ? (u.qv0 + g + 8) / p.gq : -1;
@@ -494,7 +564,10 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
 #pragma unroll
                 for (int i = 0; i < NI; ++i) vw[i] = vj[4 * i];
                 bool see[2];
-                if (p.a.vis) {
+                if constexpr (WIN) {
+                    see[0] = r0 >= 0 && (kv8_window_new(p, sq.first, sq.rows, sq.len, r0, j & ~31) >> (j & 31) & 1u);
+                    see[1] = r1 >= 0 && (kv8_window_new(p, sq.first, sq.rows, sq.len, r1, j & ~31) >> (j & 31) & 1u);
+                } else if (p.a.vis) {
                     see[0] = r0 >= 0 && j < 256 && (p.a.vis[(static_cast<long long>(sq.first) + r0) * 8 + j / 32] >> (j % 32) & 1u);
                     see[1] = r1 >= 0 && j < 256 && (p.a.vis[(static_cast<long long>(sq.first) + r1) * 8 + j / 32] >> (j % 32) & 1u);
                 } else {
@@ -574,7 +647,8 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
             const float kf_ = __shfl_sync(0xffffffffu, old ? last_kf : my_kf, i & 31), kf = pg < 0 ? 1.f : kf_;
             const float vs_ = __shfl_sync(0xffffffffu, old ? last_vs : my_vs, i & 31);
             const int vx = pg < 0 ? 0 : exponent_of(vs_);
-            const int left = pg < 0 ? 0 : sq.len - (page0 + NW * i) * PAGE;   // keys of this page that count
+            const int key0 = kv8_tile<WIN>(sq, page0 + NW * i) * PAGE, left = pg < 0 ? 0 : sq.len - key0;   // keys of this page that count
+            const bool edge = WIN && kv8_edge(p, sq, (u.qv0 + u.nqv - 1) / p.gq, key0, PAGE);
             const uint8_t *kblk = my_ring + out_slot * Lay::block, *vblk = nullptr;
 #pragma unroll 1
             for (int piece = 0; piece < PAGE / KT; ++piece) {
@@ -604,6 +678,17 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
                     ++read;
                 }
                 const int live = min(max(left - piece * KT - CH * t, 0), CH);
+                if constexpr (WIN) {
+                    if (edge) {
+                        const int key = key0 + piece * KT + CH * t;   // this lane's first
+                        const uint32_t see[2] = {kv8_window_old(p, from[0], key), kv8_window_old(p, from[1], key)};
+#pragma unroll
+                        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (!(see[e >> 1] >> (2 * j + (e & 1)) & 1u)) sc[j][e] = -INFINITY;
+                    }
+                }
                 uint32_t w16[NJ][2];
                 rows_softmax<NJ, NI>(sc, live, kf, qf, vx, r, d, l, reach, o, w16);
                 if (piece == 0) {   // V is the block behind K
@@ -616,6 +701,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
                 const uint8_t *col = vblk + g * PAGE + piece * KT + CH * t;
                 const bool whole = left >= PAGE;
                 constexpr int NG = 4;   // output groups in flight together
+                [[maybe_unused]] uint32_t odd = 0;   // an edge's bytes that are NaN
 #pragma unroll
                 for (int n0 = 0; n0 < NI; n0 += NG) {
                     uint32_t w[NG][CH / 4];
@@ -638,6 +724,18 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
                             for (int n = 0; n < NG; ++n) w[n][k] &= mask;
                         }
                     }
+                    if constexpr (WIN) {
+                        if (edge) {   // a NaN counts 0 here: a row that does not see it has a weight of 0
+#pragma unroll
+                            for (int k = 0; k < CH / 4; ++k)
+#pragma unroll
+                                for (int n = 0; n < NG; ++n) {
+                                    const uint32_t nan = __vcmpeq4(w[n][k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                    odd |= nan;
+                                    w[n][k] &= ~nan;
+                                }
+                        }
+                    }
 #pragma unroll
                     for (int k = 0; k < CH / 4; ++k) {
                         const uint32_t a[4] = {w16[2 * k][0], w16[2 * k][1], w16[2 * k + 1][0], w16[2 * k + 1][1]};
@@ -646,6 +744,20 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
                             uint32_t b0, b1;
                             e4m3x4_f16(w[n][k], b0, b1);
                             mma_f16(o[n0 + n], a, b0, b1);
+                        }
+                    }
+                }
+                if constexpr (WIN) {
+                    if (edge && __any_sync(0xffffffffu, odd != 0)) {   // and is added for the rows that do
+#pragma unroll 1
+                        for (int j = 0; j < min(left - piece * KT, KT); ++j) {
+                            const int key = key0 + piece * KT + j;
+                            const uint8_t *at = vblk + 2 * t * PAGE + piece * KT + j;
+#pragma unroll
+                            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if ((at[(8 * i + (e & 1)) * PAGE] & 0x7f) == 0x7f && (key < p.sinks || key >= from[e >> 1])) o[i][e] = NAN;
                         }
                     }
                 }
@@ -772,8 +884,11 @@ struct Tiles {
     static constexpr uint32_t odd_off = qf_off + kTileQ * 4;       // [2 groups]
     static constexpr uint32_t bar_off = odd_off + 16;
     static constexpr uint32_t tiles_off = bar_off + 40 * 8 + (kMmaWarp + 1) * 8;
-    static constexpr size_t bytes(int n_seqs) { return tiles_off + (static_cast<size_t>(n_seqs) + 1) * 8; }
-    static_assert(tiles_off + (LA_KV8_MAX_SEQS + 1) * 8 <= 227 * 1024, "shared memory of a block");
+    static constexpr size_t tiles_end(int n_seqs) { return tiles_off + (static_cast<size_t>(n_seqs) + 1) * 8; }
+    // With a window: barriers [4] and flags [4][kOpWarps] of NaN in cached V, by unit.
+    static constexpr size_t win_bytes = 4 * 8 + 4 * kOpWarps * 4;
+    static constexpr size_t bytes(int n_seqs, bool win) { return tiles_end(n_seqs) + (win ? win_bytes : 0); }
+    static_assert(tiles_off + (LA_KV8_MAX_SEQS + 1) * 8 + win_bytes <= 227 * 1024, "shared memory of a block");
 };
 // TMEM columns: S of even and odd tiles (P over their first halves; behind it,
 // once a group is through with a unit, its rows' r, d and sum), then their O.
@@ -938,8 +1053,11 @@ __device__ __noinline__ void mixed_v(uint32_t sv, uint32_t v_block, const __nv_b
 }
 
 // Which of new rows key .. key + 31 row `row` of a sequence (-1: none) sees.
-__device__ __forceinline__ uint32_t new_rows_seen(const Kv8Args &p, int first, int row, int key) {
+template <bool WIN>
+__device__ __forceinline__ uint32_t new_rows_seen(const Kv8Args &p, const Kv8Seq &q, int row, int key) {
+    const int first = q.first;
     if (row < 0) return 0u;
+    if constexpr (WIN) return kv8_window_new(p, first, q.rows, q.len, row, key);
     if (p.a.vis) return key < 256 ? p.a.vis[(static_cast<long long>(first) + row) * 8 + key / 32] : 0u;
     return row >= key + 31 ? 0xffffffffu : row < key ? 0u : (2u << (row - key)) - 1u;
 }
@@ -954,6 +1072,7 @@ struct Kv8Row {
     int grp, row, units, it, first, end, i, kt, myrow, myhead;
     uint32_t lanes, ts, to;
     bool in, odd;
+    int from;   // where the row's window begins
 };
 // O's reach relative to r, where r has grown from s.r.
 __device__ __forceinline__ float reach_now(const Kv8Row &s, float r) { return fmaxf(s.reach - (r - s.at), s.d + kReach - (r - s.r)); }
@@ -979,7 +1098,7 @@ __device__ __forceinline__ void scale_o(uint32_t to, float f) {
 // does not see), with r and d as this tile's largest ones have them.  s.own_*
 // has r, d and l behind this tile; for the loop over its groups the scores are
 // final (r 0, u 0, a factor of 1), and l < 0 says so.
-template <int HD>
+template <int HD, bool WIN>
 __device__ __forceinline__ void own_scores(const Kv8Args &p, const Kv8Piece &u, uint32_t ts, uint32_t to, const Kv8Meta &mt, const Kv8Exps &ex, int key0,
                                            int row, bool has_o, Kv8Row &s) {
     const int nkeys = min(u.sq.rows - key0, kTileK);
@@ -995,7 +1114,7 @@ __device__ __forceinline__ void own_scores(const Kv8Args &p, const Kv8Piece &u, 
             tmem_ld_wait_for(v);
             if (pass == 0) {
                 const int live = nkeys - 16 * k;
-                const uint32_t see = (live <= 0 ? 0u : live >= 16 ? 0xffffu : (1u << live) - 1u) & new_rows_seen(p, u.sq.first, row, key0 + 32 * (k >> 1)) >> 16 * (k & 1);
+                const uint32_t see = (live <= 0 ? 0u : live >= 16 ? 0xffffu : (1u << live) - 1u) & new_rows_seen<WIN>(p, u.sq, row, key0 + 32 * (k >> 1)) >> 16 * (k & 1);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const float z = see >> e & 1u ? __uint_as_float(v[e]) * factor(mixed ? power_of(ex.k[16 * k + e]) : mt.kf[0], s.qf) : -INFINITY;
@@ -1033,12 +1152,13 @@ __device__ __forceinline__ void own_scores(const Kv8Args &p, const Kv8Piece &u, 
 
 // Group k of a cached tile that is left out of the product: its weights' product with
 // V in fp32, onto O; S = -infinity.
-template <int HD>
+template <int HD, bool WIN>
 __device__ __forceinline__ void far_group(const Kv8Args &p, const Kv8Piece &u, uint32_t ts, uint32_t to, const Kv8Meta &mt, int kt, int k, Kv8Row &s) {
-    const int live = mt.live[k], key = (kt - u.sq.ntiles) * kTileK + 32 * k;   // its page is in the pool: it has keys
+    const int live = mt.live[k], key = kv8_tile<WIN>(u.sq, kt - u.sq.ntiles) * kTileK + 32 * k;   // its page is in the pool: it has keys
     const int page = p.c.table[static_cast<long long>(u.s) * p.c.max_pages + (key >> p.page_log2)];
     const uint8_t *v8 = static_cast<const uint8_t *>(p.c.v) + kv8_block(p.c, p.a.layer, page, u.head) * (p.c.page * HD) + (key & (p.c.page - 1));
     const float f = factor(mt.kf[k], s.qf), ux = static_cast<float>(mt.vx[k]) - s.d;
+    [[maybe_unused]] const uint32_t see = WIN ? kv8_window_old(p, s.from, key) : 0u;
     float w[32], top = -INFINITY;
     {
         uint32_t v[32];
@@ -1046,7 +1166,7 @@ __device__ __forceinline__ void far_group(const Kv8Args &p, const Kv8Piece &u, u
         tmem_ld_wait_for(v);
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
-            w[e] = e < live ? __uint_as_float(v[e]) * f : -INFINITY;
+            w[e] = e < live && (!WIN || (see >> e & 1u)) ? __uint_as_float(v[e]) * f : -INFINITY;
             top = fmaxf(top, w[e]);
         }
 #pragma unroll
@@ -1083,7 +1203,9 @@ __device__ __forceinline__ void far_group(const Kv8Args &p, const Kv8Piece &u, u
             for (int i = 0; i < 8; ++i) {
                 const int n = live - 4 * i;   // bytes behind the last token may be anything
                 uint32_t lo, hi;
-                e4m3x4_f16(n >= 4 ? b[i] : n <= 0 ? 0u : b[i] & ((1u << (8 * n)) - 1u), lo, hi);
+                uint32_t bytes = n >= 4 ? b[i] : n <= 0 ? 0u : b[i] & ((1u << (8 * n)) - 1u);
+                if constexpr (WIN) bytes &= ((see >> 4 * i & 15u) * 0x00204081u & 0x01010101u) * 255u;   // a byte for each of 4 bits
+                e4m3x4_f16(bytes, lo, hi);
                 const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo)), c = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
                 acc = fmaf(w[4 * i], a.x, fmaf(w[4 * i + 1], a.y, fmaf(w[4 * i + 2], c.x, fmaf(w[4 * i + 3], c.y, acc))));
             }
@@ -1097,7 +1219,7 @@ __device__ __forceinline__ void far_group(const Kv8Args &p, const Kv8Piece &u, u
 // What a tile needs before its weights: d of a tile whose largest scale is
 // 2^mt.top, with O following, and the groups and rows that the loop over them cannot take as
 // they are.  `row`: this thread's new row, or -1.
-template <int HD>
+template <int HD, bool WIN>
 __device__ __noinline__ void begin_tile(const Kv8Args &p, const Kv8Piece &u, uint32_t ts, uint32_t to, const Kv8Meta &mt, const Kv8Exps &ex, int kt, int row,
                                         bool has_o, Kv8Row &s) {
     const bool cached = kt >= u.sq.ntiles;
@@ -1115,14 +1237,14 @@ __device__ __noinline__ void begin_tile(const Kv8Args &p, const Kv8Piece &u, uin
         s.d = nd;
         if (__any_sync(0xffffffffu, top - nd < kTopLow)) {   // O's reach keeps d above: no bits would be left of fp16 weights
             if (!cached) {
-                own_scores<HD>(p, u, ts, to, mt, ex, kt * kTileK, row, has_o, s);
+                own_scores<HD, WIN>(p, u, ts, to, mt, ex, kt * kTileK, row, has_o, s);
                 return;
             }
             far = 0;
             for (int k = 0; k < 4; ++k) far |= mt.live[k] > 0 ? 1 << k : 0;
         }
     } else {
-        own_scores<HD>(p, u, ts, to, mt, ex, kt * kTileK, row, has_o, s);
+        own_scores<HD, WIN>(p, u, ts, to, mt, ex, kt * kTileK, row, has_o, s);
         return;
     }
     if (far && !has_o) {   // O, to add to
@@ -1133,15 +1255,16 @@ __device__ __noinline__ void begin_tile(const Kv8Args &p, const Kv8Piece &u, uin
     }
 #pragma unroll 1
     for (int k = 0; k < 4; ++k)
-        if (far >> k & 1) far_group<HD>(p, u, ts, to, mt, kt, k, s);
+        if (far >> k & 1) far_group<HD, WIN>(p, u, ts, to, mt, kt, k, s);
 }
 
 // The pieces behind the first: one copy of the code for the roles of k_kv8_tiles
 // (123.5 us against 126.0 for 256 rows over 16k tokens).  The first piece is found
 // before the roles part, which a call like this would delay by 2.3 us.
-__device__ __noinline__ bool kv8_next_call(const Kv8Args &p, const long long *tiles, Kv8Walk &w, Kv8Piece &u) { return kv8_next(p, tiles, w, u); }
+template <bool WIN>
+__device__ __noinline__ bool kv8_next_call(const Kv8Args &p, const long long *tiles, Kv8Walk &w, Kv8Piece &u) { return kv8_next<WIN>(p, tiles, w, u); }
 
-template <int HD>
+template <int HD, bool WIN>
 __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_constant__ Kv8Args p) {
     using Lay = Tiles<HD>;
     extern __shared__ __align__(1024) uint8_t tiles_smem[];   // the operands' swizzle repeats every 1024 bytes
@@ -1165,6 +1288,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     auto raw_empty = [&](int s) { return bars + 8 * (28 + s); };   // the operand warps
     const uint32_t q_full = bars + 8 * 34, r_full = bars + 8 * 35, drain = bars + 8 * 36, e_full = bars + 8 * 37;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + Lay::bar_off + 8 * 38);
+    // With a window, by unit % 4: the operand warps are through with the unit's V, and each of them met a NaN at its edges or not.
+    const uint32_t win_off = static_cast<uint32_t>(Lay::tiles_end(p.c.n_seqs));
+    [[maybe_unused]] auto n_full = [&](int t) { return sm + win_off + 8 * t; };
+    [[maybe_unused]] int *nans = reinterpret_cast<int *>(smem + win_off + 32);
     long long *warp_sum = reinterpret_cast<long long *>(smem + Lay::bar_off + 40 * 8);
 
     const la_kv8_cache &c = p.c;
@@ -1188,6 +1315,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         mbar_init(e_full, 8);
         mbar_init(r_full, kOpWarps);
         mbar_init(drain, 1);
+        if constexpr (WIN)
+            for (int t = 0; t < 4; ++t) mbar_init(n_full(t), kOpWarps);
         fence_barrier_init();
     }
     // Tensor memory is taken once the kernel before has finished, and the one
@@ -1198,13 +1327,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         tmem_relinquish();
     }
     tc_fence_before();
-    kv8_plan(p, tiles, warp_sum);   // barriers inside
+    kv8_plan<WIN>(p, tiles, warp_sum);   // barriers inside
     tc_fence_after();
     pdl_trigger();
     const uint32_t tmem = *tmem_slot;
-    Kv8Walk walk = kv8_walk(p, tiles);
+    Kv8Walk walk = kv8_walk<WIN>(p, tiles);
     Kv8Piece u{};
-    const bool begun = kv8_next(p, tiles, walk, u);   // the first piece
+    const bool begun = kv8_next<WIN>(p, tiles, walk, u);   // the first piece
     int it = 0;          // key tiles so far, the same count in every role: buffer it & 1, its use it >> 1
     bool ok = true;
     unsigned *err = c.status;
@@ -1213,7 +1342,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
     // 32 l .. of the tile (-2: none).  They are checked a tile later, so that
     // nothing waits for the load.
     auto entry = [&](int kt) {
-        const int key = (kt - u.sq.ntiles) * kTileK + 32 * (lane & 3);
+        const int key = kv8_tile<WIN>(u.sq, kt - u.sq.ntiles) * kTileK + 32 * (lane & 3);
         return kt < u.k1 && key < u.sq.len ? c.table[static_cast<long long>(u.s) * c.max_pages + (key >> p.page_log2)] : -2;
     };
     auto checked = [&](int e) {
@@ -1247,6 +1376,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         const uint32_t v_at0 = v_at(vhalf), v_at1 = v_at(vhalf ^ 1);
         int new_tiles = 0, slot = 0;
         uint32_t phase = 0;
+        [[maybe_unused]] int units = 0;
+        [[maybe_unused]] uint32_t nan_met = 0;
         auto landed = [&]() {   // the next stage of bytes is there
             ok = __all_sync(0xffffffffu, bar_wait(raw_full(slot), phase, err, LA_KV8_TIMEOUT));
             return sm + Lay::raw_off + slot * Lay::raw_bytes;
@@ -1258,7 +1389,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 phase ^= 1;
             }
         };
-        for (bool any = begun; ok && any; any = kv8_next_call(p, tiles, walk, u)) {
+        for (bool any = begun; ok && any; any = kv8_next_call<WIN>(p, tiles, walk, u)) {
             const Kv8Seq sq = u.sq;
             auto k_tile = [&](int kt, int it) {
                 const int b = it & 1, use = it >> 1;
@@ -1466,6 +1597,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                             x[n] = make_uint4(cut(x[n].x, keys), cut(x[n].y, keys - 4), cut(x[n].z, keys - 8), cut(x[n].w, keys - 12));
                         }
                     }
+                    if constexpr (WIN) {
+                        // In a tile that has keys which some rows do not see a NaN counts 0, and
+                        // is added at the end for the rows that see it.
+                        if (kv8_edge(p, sq, (u.qv0 + u.nqv - 1) / p.gq, kv8_tile<WIN>(sq, kt - sq.ntiles) * kTileK, kTileK)) {
+#pragma unroll
+                            for (int n = 0; n < NR; ++n) {
+                                if (kOpWarps - 1 - w + n * kOpWarps >= NG) continue;
+                                auto tame = [&](uint32_t &v) {
+                                    const uint32_t nan = __vcmpeq4(v & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                    nan_met |= nan;
+                                    v &= ~nan;
+                                };
+                                tame(x[n].x), tame(x[n].y), tame(x[n].z), tame(x[n].w);
+                            }
+                        }
+                    }
 #pragma unroll
                     for (int n = 0; n < NR; ++n) {
                         const int g = kOpWarps - 1 - w + n * kOpWarps;
@@ -1485,6 +1632,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 if (ok && kt >= u.k0) v_tile(kt, first + kt - u.k0);
             }
             it = first + max(u.k1 - u.k0, 0);
+            if constexpr (WIN) {
+                if (ok && u.k1 > u.k0) {
+                    const bool met = __any_sync(0xffffffffu, nan_met != 0);
+                    if (lane == 0) {
+                        nans[(units & 3) * kOpWarps + w] = met;
+                        mbar_arrive_one(n_full(units & 3));
+                    }
+                    __syncwarp();
+                    nan_met = 0;
+                    ++units;
+                }
+            }
         }
     } else if (warp == kLoadWarp) {
         // ================================================ bytes
@@ -1504,7 +1663,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             if (staged >= Lay::raw_slots) ok = __all_sync(0xffffffffu, bar_wait(raw_empty(slot), phase ^ 1, err, LA_KV8_TIMEOUT));
             if (!ok) return;
             const bool have = held >> lane & 1u;
-            const int live = have ? min(max(u.sq.len - (kt - u.sq.ntiles) * kTileK - 32 * lane, 0), 32) : 0, vx = exponent_of(vs);
+            const int live = have ? min(max(u.sq.len - kv8_tile<WIN>(u.sq, kt - u.sq.ntiles) * kTileK - 32 * lane, 0), 32) : 0, vx = exponent_of(vs);
             const int top = __reduce_max_sync(0xffffffffu, live > 0 ? vx : -127);
             const uint32_t far = __ballot_sync(0xffffffffu, live > 0 && vx < top - kNear);
             if (lane < 4) {
@@ -1529,7 +1688,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 phase ^= 1;
             }
         };
-        for (bool any = begun; ok && any; any = kv8_next_call(p, tiles, walk, u)) {
+        for (bool any = begun; ok && any; any = kv8_next_call<WIN>(p, tiles, walk, u)) {
             const int c_first = max(u.k0, u.sq.ntiles);   // first cached tile of this piece
             if (c_first >= u.k1) continue;
             uint32_t held = 0, v_held = 0, v_blk = 0, blk = block_of(checked(entry(c_first)), held);
@@ -1562,7 +1721,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         constexpr uint32_t is = idesc_f16(kTileQ, kTileK), io = idesc_f16(kTileQ, HD);
         auto wait = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, bar_wait(bar, parity & 1, err, LA_KV8_TIMEOUT)); };
         int units = 0;
-        for (bool any = begun; ok && any; any = kv8_next_call(p, tiles, walk, u)) {
+        for (bool any = begun; ok && any; any = kv8_next_call<WIN>(p, tiles, walk, u)) {
             if (u.k0 >= u.k1) continue;
             ok = wait(q_full, units);
             ++units;
@@ -1623,7 +1782,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
         float *qfs = reinterpret_cast<float *>(smem + Lay::qf_off);
         int *odds = reinterpret_cast<int *>(smem + Lay::odd_off);
         int units = 0;
-        for (bool any = begun; ok && any; any = kv8_next_call(p, tiles, walk, u)) {
+        for (bool any = begun; ok && any; any = kv8_next_call<WIN>(p, tiles, walk, u)) {
             Kv8Seq sq = u.sq;
             bool in = row < u.nqv;
             const bool idle = row - lane >= u.nqv;   // none of this warp's rows is in use
@@ -1677,6 +1836,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 qf = idle ? 0.f : qfs[row];
             }
             float r = -INFINITY, d = 0.f, l = 0.f;
+            [[maybe_unused]] int from = 0;
+            if constexpr (WIN) from = sq.len + kv8_seen(p, sq.first, sq.rows, myrow) - p.window;
             Kv8Row keep;   // in memory: what only the rare paths ask for
             keep.reach = keep.at = -INFINITY;
             bool odd = false;
@@ -1696,6 +1857,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                     // the instruction cache (5 us per pair of tiles).
                     bool cached = kt >= sq.ntiles;
                     const float top = static_cast<float>(mt->top);
+                    [[maybe_unused]] const int key0 = kv8_tile<WIN>(sq, kt - sq.ntiles) * kTileK;
                     if (r == -INFINITY) d = top - kTop;
                     if (__any_sync(0xffffffffu, top - d < kTopLow || top - d > kUnitHigh) || (mt->flags & ~kOddV)) {
                         if (i >= first + 2) {   // this group's O holds its tile i - 2
@@ -1706,11 +1868,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                         keep.r = r, keep.d = d, keep.l = l, keep.qf = qf;
                         keep.grp = grp, keep.row = row, keep.units = units, keep.it = it, keep.first = first, keep.end = end, keep.i = i, keep.kt = kt;
                         keep.myrow = myrow, keep.myhead = myhead, keep.lanes = lanes, keep.ts = ts, keep.to = to, keep.in = in, keep.odd = odd;
-                        begin_tile<HD>(p, u, ts, to, *mt, exps[i & 3], kt, in ? myrow : -1, i >= first + 2, keep);
+                        if constexpr (WIN) keep.from = from;
+                        begin_tile<HD, WIN>(p, u, ts, to, *mt, exps[i & 3], kt, in ? myrow : -1, i >= first + 2, keep);
                         r = keep.r, d = keep.d, l = keep.l, qf = keep.qf;
                         grp = b = keep.grp, row = keep.row, units = keep.units, it = keep.it, first = keep.first, end = keep.end, i = keep.i, kt = keep.kt;
                         myrow = keep.myrow, myhead = keep.myhead, lanes = keep.lanes, ts = keep.ts, to = keep.to, in = keep.in, odd = keep.odd;
                         sq = u.sq, mt = &meta[i & 3], cached = kt >= sq.ntiles;
+                        if constexpr (WIN) from = keep.from;
                     }
 #pragma unroll 1
                     for (int k = 0; k < 4; ++k) {
@@ -1720,9 +1884,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                         const float ux = static_cast<float>(mt->vx[k]) - d;   // u of this group
                         const float f = factor(mt->kf[k], qf), add = ux - (r == -INFINITY ? 0.f : r);
                         tmem_ld_wait_for(v);
-                        if (live < 32 || !cached) {
+                        if (live < 32 || !cached || (WIN && key0 + 32 * k + 32 > p.sinks && key0 + 32 * k < from)) {
                             uint32_t see = live >= 32 ? 0xffffffffu : (1u << live) - 1u;   // keys that this row sees
-                            if (!cached) see &= new_rows_seen(p, sq.first, in ? myrow : -1, kt * kTileK + 32 * k);
+                            if (!cached) see &= new_rows_seen<WIN>(p, sq, in ? myrow : -1, kt * kTileK + 32 * k);
+                            else if constexpr (WIN) see &= kv8_window_old(p, from, key0 + 32 * k);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) v[e] = see >> e & 1u ? v[e] : 0xff800000u;   // -infinity
                         }
@@ -1798,6 +1963,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
             it = end;
             if (!ok) break;
             float fa = 0.f, fb = 0.f, R = r, D = d, L = l;
+            [[maybe_unused]] bool nan_old = false;
             if (first < end) {
                 // Both groups' maxima and sums, once all products are done; then
                 // each group writes half of the dims.
@@ -1816,6 +1982,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 ++units;
                 const float4 x = tmem_ld_four(tmem + lanes + kColS + kTileK / 2), y = tmem_ld_four(tmem + lanes + kColS + 128 + kTileK / 2);
                 odd = (odds[0] | odds[1]) != 0;
+                if constexpr (WIN) {
+                    ok = __all_sync(0xffffffffu, bar_wait(n_full((units - 1) & 3), (units - 1) >> 2 & 1, err, LA_KV8_TIMEOUT));
+                    if (!ok) break;
+                    for (int k = 0; k < kOpWarps; ++k) nan_old |= nans[((units - 1) & 3) * kOpWarps + k] != 0;
+                }
                 // a group that saw no key (a sum of 0) may have an O that was never written
                 const bool xs = x.z != 0.f, ys = y.z != 0.f;
                 R = fmaxf(x.x, y.x);
@@ -1847,13 +2018,33 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_kv8_tiles(const __grid_cons
                 if (odd && in) {   // NaN and infinities of the new rows that this row sees
 #pragma unroll 1
                     for (int r = u.k0 * kTileK; r < min(sq.rows, min(u.k1, sq.ntiles) * kTileK); ++r) {
-                        const bool seen = p.a.vis ? r < 256 && (p.a.vis[(static_cast<long long>(sq.first) + myrow) * 8 + r / 32] >> (r % 32) & 1u) : r <= myrow;
+                        const bool seen = WIN ? kv8_window_new(p, sq.first, sq.rows, sq.len, myrow, r & ~31) >> (r & 31) & 1u : p.a.vis ? r < 256 && (p.a.vis[(static_cast<long long>(sq.first) + myrow) * 8 + r / 32] >> (r % 32) & 1u) : r <= myrow;
                         if (!seen) continue;
                         const __nv_bfloat16 *vr = static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + r) * p.a.v_stride + u.head * HD + d0 + 16 * k;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const float x = __bfloat162float(vr[e]);
                             if (!is_finite(x)) o[e] += x;
+                        }
+                    }
+                }
+                if constexpr (WIN) {
+                    if (nan_old && in) {   // and those of cached tokens at the window's edges
+#pragma unroll 1
+                        for (int kt = max(u.k0, sq.ntiles); kt < u.k1; ++kt) {
+                            const int key0 = kv8_tile<WIN>(sq, kt - sq.ntiles) * kTileK;
+                            if (!kv8_edge(p, sq, (u.qv0 + u.nqv - 1) / p.gq, key0, kTileK)) continue;
+#pragma unroll 1
+                            for (int key = key0; key < min(sq.len, key0 + kTileK); ++key) {
+                                if (key >= p.sinks && key < from) continue;
+                                const int page = c.table[static_cast<long long>(u.s) * c.max_pages + (key >> p.page_log2)];
+                                if (static_cast<unsigned>(page) >= static_cast<unsigned>(c.n_pages)) continue;
+                                const uint8_t *vb = static_cast<const uint8_t *>(c.v) + kv8_block(c, p.a.layer, page, u.head) * (c.page * HD) +
+                                                    static_cast<long long>(d0 + 16 * k) * c.page + (key & (c.page - 1));
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    if ((vb[e * c.page] & 0x7f) == 0x7f) o[e] = NAN;
+                            }
                         }
                     }
                 }
@@ -2005,7 +2196,7 @@ static bool keep_whole(const Kv8Args &p, long long units, long long tiles, int c
     return tiles <= most && rounds * tiles - units * (tiles + p.unit_cost) / p.workers <= cost;
 }
 
-template <int HD, int PAGE>
+template <int HD, int PAGE, bool WIN>
 static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     using Lay = Rows<HD, PAGE>;
     static_assert(Lay::per_sm <= kRowsPerSm, "workspace");
@@ -2028,18 +2219,18 @@ static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     static std::atomic<unsigned long long> configured{0};
     unsigned long long bit = 0;
     if (attrs_needed(configured, &bit)) {
-        cudaError_t e = cudaFuncSetAttribute(k_kv8_rows<HD, PAGE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(k_kv8_rows<HD, PAGE, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(Lay::bytes(LA_KV8_MAX_SEQS)));
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
-    cudaError_t e = launch_k(k_kv8_rows<HD, PAGE>, dim3(p.workers), dim3(32 * Lay::warps), Lay::bytes(p.c.n_seqs), s, p);
+    cudaError_t e = launch_k(k_kv8_rows<HD, PAGE, WIN>, dim3(p.workers), dim3(32 * Lay::warps), Lay::bytes(p.c.n_seqs), s, p);
     if (e != cudaSuccess || p.whole) return e;
     if (p.workers < 2) return cudaSuccess;
     return launch_k(k_kv8_join<HD, 4>, dim3(p.workers - 1), dim3(kJoinThreads), 0, s, p);
 }
 
-template <int HD>
+template <int HD, bool WIN>
 static cudaError_t tiles_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     using Lay = Tiles<HD>;
     p.q_tile = kTileQ;
@@ -2059,12 +2250,12 @@ static cudaError_t tiles_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     static std::atomic<unsigned long long> configured{0};
     unsigned long long bit = 0;
     if (attrs_needed(configured, &bit)) {
-        cudaError_t e = cudaFuncSetAttribute(k_kv8_tiles<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(Lay::bytes(LA_KV8_MAX_SEQS)));
+        cudaError_t e = cudaFuncSetAttribute(k_kv8_tiles<HD, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(Lay::bytes(LA_KV8_MAX_SEQS, WIN)));
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
-    cudaError_t e = launch_k(k_kv8_tiles<HD>, dim3(p.workers), dim3(kTileThreads), Lay::bytes(p.c.n_seqs), s, p);
+    cudaError_t e = launch_k(k_kv8_tiles<HD, WIN>, dim3(p.workers), dim3(kTileThreads), Lay::bytes(p.c.n_seqs, WIN), s, p);
     if (e != cudaSuccess || p.whole || p.workers < 2) return e;
     return launch_k(k_kv8_join<HD, 8>, dim3(p.workers - 1), dim3(kJoinThreads), 0, s, p);
 }
@@ -2076,15 +2267,16 @@ static cudaError_t tiles_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
 // against 24.0).
 constexpr int kFewVectors = 32;
 
-template <int HD>
+template <int HD, bool WIN>
 static cudaError_t attention_launch_hd(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
-    if (static_cast<long long>(p.a.max_rows) * p.gq > kFewVectors) return tiles_launch<HD>(p, nsm, ws, s);
-    if (p.c.page == 32) return rows_launch<HD, 32>(p, nsm, ws, s);
-    if (p.c.page == 64) return rows_launch<HD, 64>(p, nsm, ws, s);
-    return rows_launch<HD, 128>(p, nsm, ws, s);
+    if (static_cast<long long>(p.a.max_rows) * p.gq > kFewVectors) return tiles_launch<HD, WIN>(p, nsm, ws, s);
+    if (p.c.page == 32) return rows_launch<HD, 32, WIN>(p, nsm, ws, s);
+    if (p.c.page == 64) return rows_launch<HD, 64, WIN>(p, nsm, ws, s);
+    return rows_launch<HD, 128, WIN>(p, nsm, ws, s);
 }
 
-cudaError_t kv8_attention_launch(const la_kv8_cache &c, const la_kv8_attn &a, void *ws, int nsm, cudaStream_t s, int64_t *launched) {
+cudaError_t kv8_attention_launch(const la_kv8_cache &c, const la_kv8_attn &a, int window, int sinks, void *ws, int nsm, cudaStream_t s,
+                                 int64_t *launched) {
     if (a.n_rows < 1) return cudaSuccess;
     Kv8Args p{};
     p.c = c;
@@ -2097,7 +2289,15 @@ cudaError_t kv8_attention_launch(const la_kv8_cache &c, const la_kv8_attn &a, vo
     p.gq = a.n_heads / c.n_kv_heads;
     p.page_log2 = c.page == 32 ? 5 : c.page == 64 ? 6 : 7;
     p.scale_log2 = a.scale * kKv8Log2e;
-    const cudaError_t e = c.head_dim == 128 ? attention_launch_hd<128>(p, nsm, ws, s) : attention_launch_hd<64>(p, nsm, ws, s);
+    // What a slot's rows see together, at most; a window as long as every list is none.
+    const bool win = window > 0 && window < static_cast<int64_t>(room) + a.n_rows;
+    if (win) {
+        p.window = window;
+        p.sinks = sinks;
+        p.a.max_len = static_cast<int>(std::min<int64_t>(p.a.max_len, static_cast<int64_t>(window) + sinks + p.a.max_rows + 128));
+    }
+    const cudaError_t e = c.head_dim == 128 ? (win ? attention_launch_hd<128, true>(p, nsm, ws, s) : attention_launch_hd<128, false>(p, nsm, ws, s))
+                                            : (win ? attention_launch_hd<64, true>(p, nsm, ws, s) : attention_launch_hd<64, false>(p, nsm, ws, s));
     if (launched) *launched += p.whole ? 1 : 2;
     return e;
 }

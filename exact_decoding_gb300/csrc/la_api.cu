@@ -465,7 +465,7 @@ int forward(la_handle *h, Mode mode, const int *tok, int nrows, int P, bool want
             a.out = h->ao;   // the hi rows; the lo rows stay 0
             a.scale = 1.f / std::sqrt(static_cast<float>(h->hd));
             pe = mode == STEP ? h->prof_begin() : -1;
-            CK(kv8_attention_launch(h->kv8c, a, h->kv8_ws, h->nsm, s, &h->launches));
+            CK(kv8_attention_launch(h->kv8c, a, 0, 0, h->kv8_ws, h->nsm, s, &h->launches));
             h->prof_end(pe, 1, attn_bytes);
             h->launches += 1;   // kv8_qkv
         } else if (h->bf16) {

@@ -156,6 +156,8 @@ def load_library():
     KV8 = ctypes.POINTER(la_kv8_cache)
     lib.la_kv8_workspace.argtypes = [KV8, ctypes.POINTER(ctypes.c_int64)]
     lib.la_kv8_attention.argtypes = [KV8, ctypes.POINTER(la_kv8_attn), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]
+    lib.la_kv8_attention_window.argtypes = [KV8, ctypes.POINTER(la_kv8_attn), ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                            ctypes.c_int64, ctypes.c_void_p]
     lib.la_kv8_append.argtypes = [KV8, ctypes.POINTER(la_kv8_rows), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]
     lib.la_kv8_fork.argtypes = [KV8, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]
     lib.la_kv8_free.argtypes = [KV8, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]
@@ -176,7 +178,7 @@ def load_library():
                  "la_import_state", "la_debug_logits", "la_gemm_bf16", "la_gemm_bf16_noalloc", "la_gemm_status",
                  "la_selftest_timeout", "la_gemm_schedule", "la_step_tables", "la_kv8_workspace", "la_kv8_attention",
                  "la_kv8_append", "la_kv8_fork", "la_kv8_free", "la_kv8_compact", "la_kv8_status", "la_create_kv8",
-                 "la_fork", "la_kv8_norm_rope", "la_logprobs", "la_gemv_w4"):
+                 "la_fork", "la_kv8_attention_window", "la_kv8_norm_rope", "la_logprobs", "la_gemv_w4"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -365,6 +367,12 @@ def la_kv8_workspace(cache: la_kv8_cache) -> int:
 def la_kv8_attention(cache: la_kv8_cache, args: la_kv8_attn, workspace_ptr: int, workspace_bytes: int,
                      stream: Optional[int] = None) -> None:
     _check(load_library().la_kv8_attention(cache, args, workspace_ptr, workspace_bytes, stream), "la_kv8_attention")
+
+
+def la_kv8_attention_window(cache: la_kv8_cache, args: la_kv8_attn, window: int, sinks: int, workspace_ptr: int, workspace_bytes: int,
+                            stream: Optional[int] = None) -> None:
+    _check(load_library().la_kv8_attention_window(cache, args, window, sinks, workspace_ptr, workspace_bytes, stream),
+           "la_kv8_attention_window")
 
 
 def la_kv8_norm_rope(cache: la_kv8_cache, args: la_kv8_qkv, stream: Optional[int] = None) -> None:
@@ -612,7 +620,8 @@ class Kv8Cache:
         self._fn = {}
         for name, kinds in (("la_kv8_attention", (P, ctypes.c_int64)), ("la_kv8_append", (P, ctypes.c_int64)),
                             ("la_kv8_fork", (P, I)), ("la_kv8_free", (P, I)),
-                            ("la_kv8_compact", (P, P, P, ctypes.c_int64)), ("la_kv8_status", ()), ("la_kv8_norm_rope", ())):
+                            ("la_kv8_compact", (P, P, P, ctypes.c_int64)), ("la_kv8_status", ()), ("la_kv8_norm_rope", ()),
+                            ("la_kv8_attention_window", (I, I, P, ctypes.c_int64))):
             f = lib[name]
             f.argtypes, f.restype = [P, P, *kinds, P], ctypes.c_int
             self._fn[name] = f
@@ -677,12 +686,14 @@ class Kv8Cache:
 
     # -------------------------------------------------------------- calls
     def attention(self, q, k=None, v=None, row_start=None, layer: int = 0, vis=None, out=None, scale: float = 0.0,
-                  max_rows: int = 0, max_len: int = 0, workspace=None, stream=None):
+                  max_rows: int = 0, max_len: int = 0, workspace=None, stream=None, window: int = 0, sinks: int = 0):
         """Attention of the rows q [rows, heads, dim] over their sequences'
         cached tokens and the visible new rows k, v [rows, kv heads, dim];
         see la_kv8_attention.  max_rows and max_len are bounds that the host
         knows (0: none); they steer the split of the work only, and a batch
-        without max_rows is slow.  Returns out."""
+        without max_rows is slow.  window (0: none) and sinks: a row sees the
+        last `window` and the first `sinks` of its keys alone; see
+        la_kv8_attention_window.  Returns out."""
         rows, qs = self._rows(q, "q", 0)
         heads = q.shape[1]
         if out is None:
@@ -703,7 +714,10 @@ class Kv8Cache:
         args = _KV8_ATTN.pack(layer, heads, rows, max_rows, max_len, qs, ks, vs, os_,
                               self._ints(row_start, "row_start", self.n_seqs + 1), q.data_ptr(), kp, vp,
                               0 if vis is None else self._checked(vis, "vis", self._torch.int32, (rows, 8)), out.data_ptr(), scale)
-        self._call(self._fn["la_kv8_attention"], "la_kv8_attention", args, ws, wb, stream=stream)
+        if window == 0 and sinks == 0:
+            self._call(self._fn["la_kv8_attention"], "la_kv8_attention", args, ws, wb, stream=stream)
+        else:
+            self._call(self._fn["la_kv8_attention_window"], "la_kv8_attention_window", args, window, sinks, ws, wb, stream=stream)
         return out
 
     def norm_rope(self, q, k, v=None, q_weight=None, k_weight=None, eps: float = 1e-5, rope_base: float = 10000.0, inv_freq=None,

@@ -478,6 +478,19 @@ int la_kv8_workspace(const la_kv8_cache *c, int64_t *bytes);
 int la_kv8_attention(const la_kv8_cache *c, const la_kv8_attn *a, void *workspace, int64_t workspace_bytes,
                      void *stream);
 
+/* la_kv8_attention with a sliding window and a few first tokens that stay
+ * visible.  The list of keys that a row would see there, its sequence's cached
+ * tokens in order and then its visible new rows in order, is cut to its first
+ * `sinks` and its last `window` (of a causal row itself and the window - 1
+ * tokens before it; with vis the row's ancestors count, so every branch of a
+ * tree has a window of its own).  1 <= window <= 2^30, 0 <= sinks <= 2^30; what
+ * both cover counts once.  Cached tokens that no row of a sequence sees are not
+ * read, but for those that share a page, or 128 keys, with seen ones.
+ * Everything else is as above: what a row does not see never reaches it.
+ * Errors: as la_kv8_attention. */
+int la_kv8_attention_window(const la_kv8_cache *c, const la_kv8_attn *a, int32_t window, int32_t sinks,
+                            void *workspace, int64_t workspace_bytes, void *stream);
+
 /* Rows of a projection, on their way to la_kv8_attention and la_kv8_append:
  * q, k and v of the new rows (columns of one fused projection are fine), as
  * fp32 or bf16; the outputs are bf16.  Strides are in elements between rows,

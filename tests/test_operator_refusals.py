@@ -75,3 +75,15 @@ def test_tensors_are_checked(L):
         L.W4Matrix(w, s)
     with pytest.raises(ValueError, match="W4Matrix needs"):
         L.W4Matrix(w, s[:3])
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (0, 4), (-1, 0), (2 ** 30 + 1, 0), (4, -1), (4, 2 ** 30 + 1)])
+def test_attention_window_refuses(L, window, sinks):
+    from test_kv8_refusals import attn
+    refused(lambda: L.la_kv8_attention_window(cache(L), attn(L), window, sinks, 256, 1 << 30), INVALID, "window")
+
+
+def test_attention_window_checks_as_attention_does(L):
+    from test_kv8_refusals import attn
+    refused(lambda: L.la_kv8_attention_window(cache(L), attn(L, layer=1), 4, 0, 256, 1 << 30), INVALID, "layer")
+    refused(lambda: L.la_kv8_attention_window(cache(L, page=16), attn(L), 4, 0, 256, 1 << 30), UNSUPPORTED, "page")
