@@ -920,6 +920,20 @@ int make_tmap_bf16(CUtensorMap *m, const void *base, uint64_t inner, uint64_t ou
     return r == CUDA_SUCCESS ? 0 : -3;
 }
 
+int make_tmap_rows64(CUtensorMap *m, const void *base, uint64_t row_bytes, uint64_t rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return -1;
+    if ((reinterpret_cast<uintptr_t>(base) & 15) || (row_bytes & 15)) return -2;
+    cuuint64_t dims[2] = {row_bytes, rows};
+    cuuint64_t strides[1] = {row_bytes};
+    cuuint32_t box[2] = {64, 128};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? 0 : -3;
+}
+
 // ------------------------------------------------------------------ fp32 SIMT path
 __global__ void k_gemm_simt(const SimtGemmParams p, int total_f) {
     pdl_trigger();

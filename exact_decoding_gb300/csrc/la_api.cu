@@ -1613,18 +1613,19 @@ static int la_gemm_bf16_body(const void *x, const void *w, float *y, int32_t row
 
 static int la_gemm_status_body(void *stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    unsigned *w = nullptr, bits = 0, bits_na = 0;
+    unsigned *w = nullptr, bits = 0, bits_na = 0, bits_w4 = 0;
     CK(gemm_err_word(&w, false));
     if (w) {
         CK(cudaMemcpyAsync(&bits, w, sizeof(unsigned), cudaMemcpyDeviceToHost, s));
         CK(cudaMemsetAsync(w, 0, sizeof(unsigned), s));
     }
     CK(noalloc_err_take(s, &bits_na));
+    CK(w4_err_take(s, &bits_w4));
     CK(cudaStreamSynchronize(s));
-    if (bits | bits_na)
+    if (bits | bits_na | bits_w4)
         return fail(LA_ERR_DEVICE_TIMEOUT,
                     "a bounded wait of an earlier GEMM call gave up (error bits 0x%x la_gemm_bf16, 0x%x "
-                    "la_gemm_bf16_noalloc); that call's output is void", bits, bits_na);
+                    "la_gemm_bf16_noalloc, 0x%x la_gemv_w4); that call's output is void", bits, bits_na, bits_w4);
     return LA_OK;
 }
 

@@ -86,6 +86,10 @@ int set_last_error(int code, const char *msg);
 // Tensor-map construction (driver entry point fetched through the runtime).
 int make_tmap_bf16(CUtensorMap *m, const void *base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                    uint32_t box_inner, uint32_t box_outer);
+// Tensor map over rows of bytes: boxes of 128 rows x 64 bytes, 64-byte swizzle.
+int make_tmap_rows64(CUtensorMap *m, const void *base, uint64_t row_bytes, uint64_t rows);
+// Waits of la_gemv_w4 that gave up on the current device, cleared.
+cudaError_t w4_err_take(cudaStream_t s, unsigned *bits);
 
 // Number of CTAs of the tcgen05 GEMM that fit on one SM with `stages` at `bn`.
 size_t tc_gemm_smem_bytes(int bn, int stages);

@@ -166,8 +166,10 @@ def load_library():
     lib.la_kv8_status.argtypes = [KV8, ctypes.POINTER(ctypes.c_uint32), ctypes.c_void_p]
     lib.la_kv8_norm_rope.argtypes = [KV8, ctypes.POINTER(la_kv8_qkv), ctypes.c_void_p]
     lib.la_logprobs.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+    lib.la_gemv_w4_workspace.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(ctypes.c_int64)]
     lib.la_gemv_w4.argtypes = [ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
-                               ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p]
+                               ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int64,
+                               ctypes.c_void_p]
     lib.la_destroy.argtypes = [H]
     lib.la_destroy.restype = None
     lib.la_strerror.argtypes = [ctypes.c_int]
@@ -178,7 +180,7 @@ def load_library():
                  "la_import_state", "la_debug_logits", "la_gemm_bf16", "la_gemm_bf16_noalloc", "la_gemm_status",
                  "la_selftest_timeout", "la_gemm_schedule", "la_step_tables", "la_kv8_workspace", "la_kv8_attention",
                  "la_kv8_append", "la_kv8_fork", "la_kv8_free", "la_kv8_compact", "la_kv8_status", "la_create_kv8",
-                 "la_fork", "la_kv8_attention_window", "la_kv8_norm_rope", "la_logprobs", "la_gemv_w4"):
+                 "la_fork", "la_kv8_attention_window", "la_kv8_norm_rope", "la_logprobs", "la_gemv_w4", "la_gemv_w4_workspace"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -383,9 +385,16 @@ def la_logprobs(args: la_logprobs_args, stream: Optional[int] = None) -> None:
     _check(load_library().la_logprobs(ctypes.byref(args), stream), "la_logprobs")
 
 
+def la_gemv_w4_workspace(rows: int, out: int, k: int, group: int) -> int:
+    n = ctypes.c_int64()
+    _check(load_library().la_gemv_w4_workspace(rows, out, k, group, ctypes.byref(n)), "la_gemv_w4_workspace")
+    return n.value
+
+
 def la_gemv_w4(x_ptr: int, x_stride: int, w_ptr: int, scales_ptr: int, y_ptr: int, y_stride: int, rows: int, out: int, k: int,
-               group: int, stream: Optional[int] = None) -> None:
-    _check(load_library().la_gemv_w4(x_ptr, x_stride, w_ptr, scales_ptr, y_ptr, y_stride, rows, out, k, group, stream), "la_gemv_w4")
+               group: int, workspace_ptr: Optional[int] = None, workspace_bytes: int = 0, stream: Optional[int] = None) -> None:
+    _check(load_library().la_gemv_w4(x_ptr, x_stride, w_ptr, scales_ptr, y_ptr, y_stride, rows, out, k, group, workspace_ptr, workspace_bytes,
+                                     stream), "la_gemv_w4")
 
 
 def la_kv8_append(cache: la_kv8_cache, rows: la_kv8_rows, workspace_ptr: int, workspace_bytes: int,
@@ -420,15 +429,26 @@ def la_destroy(h) -> None:
 
 
 # ---------------------------------------------------------------------------- operators on tensors
+_torch_module = None
+
+
+def _torch():
+    """torch, which this module needs for its tensors alone."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
 def _on(index: int, stream, fn, where: str, *args) -> None:
     """fn(*args, stream) with CUDA device `index` current; stream None: torch's current one there."""
-    import torch
-    c = torch._C
+    c = _torch()._C
     st = c._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if c._cuda_getDevice() == index:
         rc = fn(*args, st)
     else:
-        with torch.cuda.device(index):
+        with _torch().cuda.device(index):
             rc = fn(*args, st)
     if rc:
         _check(rc, where)
@@ -436,7 +456,7 @@ def _on(index: int, stream, fn, where: str, *args) -> None:
 
 def _empty(stream, *shape, dtype, device):
     """A new tensor whose memory belongs to the stream that writes it."""
-    import torch
+    torch = _torch()
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
@@ -458,7 +478,7 @@ def logprobs(logits, tokens=None, top: int = 0, out=None, stream=None):
     [rows, top]); `out` has tensors of these shapes to write to.  Runs on
     `stream` (default: torch's current one of the logits' device) and does not
     synchronise."""
-    import torch
+    torch = _torch()
     if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16) or (logits.stride(1) != 1 and logits.shape[1] > 1):
         raise ValueError(f"logits must be float32 or bfloat16 [rows, vocab] with dense rows, not {logits.dtype} {tuple(logits.shape)} "
                          f"strides {logits.stride()}")
@@ -503,26 +523,30 @@ class W4Matrix:
         self._index = _cuda_index(w, "w")
         self.w, self.scales = w, scales
         self.out, self.k, self.group = w.shape[0], 2 * w.shape[1], 2 * w.shape[1] // scales.shape[1]
-        self._fn = load_library().la_gemv_w4
+        self._w_ptr, self._s_ptr, self._fn, self._need = w.data_ptr(), scales.data_ptr(), load_library().la_gemv_w4, {}
 
     def matvec(self, x, out=None, stream=None):
         """x W^T for the bfloat16 rows x [rows, k] (or [k]), as float32 [rows, out]
         (or [out]).  For a batch of single tokens: the matrix is read once for
         every 16 rows.  Runs on `stream` (default: torch's current one of the
         matrix's device) and does not synchronise."""
-        torch = self._torch
-        rows = x.shape[0] if x.dim() == 2 else 1
-        if x.dtype is not torch.bfloat16 or x.dim() not in (1, 2) or x.shape[-1] != self.k or x.stride(-1) != 1 or x.get_device() != self._index:
-            raise ValueError(f"x must be bfloat16 [rows, {self.k}] with dense rows on {self.w.device}, not {x.dtype} {tuple(x.shape)} strides "
-                             f"{x.stride()} on {x.device}")
-        shape = (*x.shape[:-1], self.out)
+        torch, sh, st = self._torch, x.shape, x.stride()
+        if x.dtype is not torch.bfloat16 or not 1 <= len(sh) <= 2 or sh[-1] != self.k or st[-1] != 1 or x.get_device() != self._index:
+            raise ValueError(f"x must be bfloat16 [rows, {self.k}] with dense rows on {self.w.device}, not {x.dtype} {tuple(sh)} strides {st} on {x.device}")
+        rows, shape = (1, (self.out,)) if len(sh) == 1 else (sh[0], (sh[0], self.out))
         if out is None:
             out = _empty(stream, *shape, dtype=torch.float32, device=self.w.device)
         elif out.dtype is not torch.float32 or out.shape != shape or (out.stride(-1) != 1 and self.out > 1) or out.get_device() != self._index:
             raise ValueError(f"out must be float32 {shape} with dense rows on {self.w.device}, not {out.dtype} {tuple(out.shape)} strides "
                              f"{out.stride()} on {out.device}")
-        _on(self._index, stream, self._fn, "la_gemv_w4", x.data_ptr(), x.stride(0) if rows > 1 else self.k, self.w.data_ptr(), self.scales.data_ptr(),
-            out.data_ptr(), out.stride(0) if rows > 1 else self.out, rows, self.out, self.k, self.group)
+        need = self._need.get(rows)
+        if need is None:
+            with torch.cuda.device(self._index):
+                need = self._need[rows] = la_gemv_w4_workspace(rows, self.out, self.k, self.group)
+        # the allocator keeps it for the stream that uses it
+        ws = _empty(stream, need, dtype=torch.uint8, device=self.w.device) if need else None
+        _on(self._index, stream, self._fn, "la_gemv_w4", x.data_ptr(), st[0] if rows > 1 else self.k, self._w_ptr, self._s_ptr, out.data_ptr(),
+            out.stride(0) if rows > 1 else self.out, rows, self.out, self.k, self.group, 0 if ws is None else ws.data_ptr(), need)
         return out
 
 

@@ -324,17 +324,24 @@ int la_gemm_bf16_noalloc(const void *x, const void *w, float *y, int32_t rows, i
  * half; scales device bf16 [out][k / group], group 32, 64 or 128, a divisor of
  * k; y device fp32, rows y_stride elements apart.  0 <= rows <= 256; the
  * matrix is read once for every 16 rows, so it is for a batch of single tokens.
- * Sums are fp32 of exact products, a group's sum meets its scale once; results
- * are deterministic.  Asynchronous, no workspace, no bounded waits.
- * No passage: a library extension.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+ * x is exact to 2^-35 of the largest value of its group (of one row), the
+ * products' sums are fp32, and a group's sum meets its scale once; results are
+ * deterministic.  A row with a value that is not finite is not finite at all.
+ * Calls of many rows need a workspace: la_gemv_w4_workspace says how many bytes
+ * on the current device (0: none), 16-byte aligned device memory with any
+ * contents; calls that overlap need one each.  Asynchronous: a bounded wait that
+ * gives up is reported by la_gemm_status.  No passage: a library extension.
+ * Errors: INVALID_ARG, UNSUPPORTED, CAPACITY (workspace too small), CUDA. */
+int la_gemv_w4_workspace(int32_t rows, int32_t out, int32_t k, int32_t group, int64_t *bytes);
 int la_gemv_w4(const void *x, int64_t x_stride, const void *w, const void *scales, float *y, int64_t y_stride,
-               int32_t rows, int32_t out, int32_t k, int32_t group, void *stream);
+               int32_t rows, int32_t out, int32_t k, int32_t group, void *workspace, int64_t workspace_bytes,
+               void *stream);
 
-/* Error status of the standalone GEMMs (la_gemm_bf16, la_gemm_bf16_noalloc)
- * on the current device.  Their kernels wait on TMA loads and tensor-core
+/* Error status of the standalone GEMMs (la_gemm_bf16, la_gemm_bf16_noalloc and
+ * la_gemv_w4) on the current device.  Their kernels wait on TMA loads and tensor-core
  * commits with a bounded wait; one that gives up sets a bit in a per-device
  * error word and leaves that call's output incomplete.  This call
- * synchronises `stream` (cudaStream_t or NULL), reads and clears both words,
+ * synchronises `stream` (cudaStream_t or NULL), reads and clears their words,
  * and returns LA_ERR_DEVICE_TIMEOUT if any bit was set since the last status
  * call, else LA_OK.  It allocates nothing.  No passage: library plumbing.
  * Errors: DEVICE_TIMEOUT, CUDA. */

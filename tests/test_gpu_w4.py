@@ -17,11 +17,15 @@ def lib():
 def case(rows, out, k, group, seed=0, device="cuda"):
     """x, packed weights and scales on the GPU, with y and its tolerance in 64 bits.
 
-    Tolerance: products of a bf16 number and a whole number up to 8 are exact in
-    fp32.  One matrix product adds 16 of them to a sum and may cut each term at
-    2^-23 of the largest, so it is off by 17 * 2^-23 of the terms' magnitudes at
-    most; a group takes group / 16 of them.  Its scale, the sum over the groups and
-    over at most 64 parts of k round by 2^-24 each."""
+    Tolerance: products of a bf16 number and a whole number up to 15 are exact in
+    fp32 (x is, to 2^-35 of its group's largest value).  One matrix product adds 16
+    of them to a sum and may cut each term at 2^-23 of the largest, so it is off
+    by 17 * 2^-23 of the terms' magnitudes at most; a group takes group / 16 of
+    them, and 8 times the sum of its x, which rounds by (group + 8) * 2^-24 of
+    their magnitudes.  q - 8 is 1 in 16 times 0: terms with q and 8 x are bounded by
+    15 |x| and 8 |x|, so 23 times the group's |x| stands for the magnitudes.  Its
+    power is exact, its scale, the sum over the groups and over at most 64 parts
+    of k round by 2^-24 each."""
     import torch
     g = np.random.default_rng(seed)
     x = torch.from_numpy(g.standard_normal((rows, k)) * np.exp(g.standard_normal((1, k)))).to(torch.bfloat16)
@@ -31,7 +35,8 @@ def case(rows, out, k, group, seed=0, device="cuda"):
     m = (q.astype(np.float64) - 8) * np.repeat(s.double().numpy(), group, 1)
     xd = x.double().numpy()
     y, a = xd @ m.T, np.abs(xd) @ np.abs(m).T
-    return x.to(device), w.to(device), s.to(device), y, a * (group / 16 * 17 * 2.0 ** -23 + (k // group + 66) * 2.0 ** -24)
+    size = np.abs(xd) @ np.repeat(s.double().numpy(), group, 1).T
+    return x.to(device), w.to(device), s.to(device), y, 23 * size * (group / 16 * 17 * 2.0 ** -23 + (group + 8) * 2.0 ** -24) + a * (k // group + 68) * 2.0 ** -24
 
 
 def close(got, want, tol):
@@ -42,7 +47,8 @@ def close(got, want, tol):
 @pytest.mark.parametrize("rows,out,k,group", [
     (1, 1, 32, 32), (1, 16, 128, 128), (1, 17, 96, 32), (2, 33, 192, 64), (1, 300, 4096, 128), (8, 129, 640, 128), (9, 100, 1600, 64),
     (16, 257, 1056, 32), (3, 4096, 512, 128), (5, 1000, 5120, 64), (17, 64, 256, 128), (33, 48, 384, 64), (256, 20, 128, 32),
-    (1, 5000, 128, 128), (16, 3, 28672, 128), (7, 2500, 2080, 32)])
+    (1, 5000, 128, 128), (16, 3, 28672, 128), (7, 2500, 2080, 32), (6, 129, 8192, 128), (1, 9, 28672, 32), (6, 200, 28672, 64), (40, 130, 4160, 64),
+    (7, 128, 96, 32), (12, 5000, 416, 32), (2, 12000, 288, 32)])
 def test_products(lib, rows, out, k, group):
     x, w, s, y, tol = case(rows, out, k, group, seed=rows + out)
     m = lib.W4Matrix(w, s)
@@ -99,3 +105,51 @@ def test_repeats_and_graphs(lib):
     graph.replay()
     assert torch.equal(first, out)
     assert lib.W4Matrix(w, s).matvec(x[:0]).shape == (0, 900)
+
+
+@pytest.mark.parametrize("rows", [3, 16])
+def test_values_of_all_sizes(lib, rows):
+    """Groups of x many binades apart, the smallest and largest bf16 values, scales likewise: each group to its own bits."""
+    import torch
+    g = np.random.default_rng(5)
+    k, out, group = 1024, 50, 64
+    x = g.standard_normal((rows, k)) * 2.0 ** np.repeat(g.integers(-60, 60, (rows, k // group)), group, 1)
+    x[:, 3] = 0
+    x[0, 64:128] = 2.0 ** -133
+    x = torch.from_numpy(x).to(torch.bfloat16)
+    q = g.integers(0, 16, (out, k), dtype=np.uint8)
+    s = torch.from_numpy(2.0 ** g.integers(-40, 40, (out, k // group)).astype(np.float64)).to(torch.bfloat16)
+    w = torch.from_numpy(q[:, ::2] | (q[:, 1::2] << 4))
+    m = (q.astype(np.float64) - 8) * np.repeat(s.double().numpy(), group, 1)
+    xd = x.double().numpy()
+    size = np.abs(xd) @ np.repeat(s.double().numpy(), group, 1).T
+    got = lib.W4Matrix(w.cuda(), s.cuda()).matvec(x.cuda())
+    close(got, xd @ m.T, 23 * size * (4 * 17 * 2.0 ** -23 + 72 * 2.0 ** -24) + 23 * size * 84 * 2.0 ** -24 + 2.0 ** -100)
+
+
+def test_workspace(lib):
+    """Too small a workspace is refused; calls of few rows need none."""
+    x, w, s, y, tol = case(16, 300, 512, 128)
+    need = lib.la_gemv_w4_workspace(16, 300, 512, 128)
+    assert need > 0 and lib.la_gemv_w4_workspace(1, 300, 512, 128) == 0 and lib.la_gemv_w4_workspace(0, 300, 512, 128) == 0
+    with pytest.raises(lib.LaError) as err:
+        lib.la_gemv_w4(x.data_ptr(), 512, w.data_ptr(), s.data_ptr(), x.data_ptr(), 300, 16, 300, 512, 128, w.data_ptr(), need - 1)
+    assert err.value.code == -3
+    lib.la_gemm_status()
+
+
+def test_calls_at_once(lib):
+    """Two streams use one matrix, each with workspaces of its own."""
+    import torch
+    x, w, s, y, tol = case(16, 3000, 4096, 128)
+    m = lib.W4Matrix(w, s)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    outs = [[m.matvec(x if i % 2 else x[:5], stream=st) for i in range(10)] for st in streams]
+    torch.cuda.synchronize()
+    for o in outs:
+        for i, got in enumerate(o):
+            n = 16 if i % 2 else 5
+            close(got, y[:n], tol[:n])
+    lib.la_gemm_status()

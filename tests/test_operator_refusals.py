@@ -60,6 +60,8 @@ def test_gemv_w4_refuses(L, kw, code, word):
     f = dict(x=256, x_stride=256, w=256, scales=256, y=256, y_stride=10, rows=2, out=10, k=256, group=128)
     f.update(kw)
     refused(lambda: L.la_gemv_w4(*f.values()), code, word)
+    if word in ("group", "rows", "out", "k out of range", "multiple"):
+        refused(lambda: L.la_gemv_w4_workspace(*[f[n] for n in ("rows", "out", "k", "group")]), code, word)
 
 
 def test_tensors_are_checked(L):
