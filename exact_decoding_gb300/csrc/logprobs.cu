@@ -8,20 +8,25 @@
 // nearly all of the probability, log p = -log1p(r) and H keep all their bits, which
 // log of a sum of 1 and little more would lose.  Both terms of H are >= 0.
 //
-// Each thread holds 16 logits at a time and a running (m, r, s).
-// The row's best tokens are kept as keys (value, then lowest index) that are
-// all different, 32 in the lanes of one warp.  A value enters only if it is above the
-// last of them; a thread that holds one pushes it to shared memory, and
-// the warp merges what was pushed.  The first threshold comes from the threads'
-// own maxima: if k of a warp's 32 lanes hold a key above T, the row's k-th best
-// does not lie below T.
+// Each thread copies 16 logits after 16 to a place of its own in shared memory, a
+// pass ahead, so that only it waits for them, and keeps its part of its warp's running
+// (m, r, s), with the terms equal to the maximum counted apart.
+// Each warp keeps its best tokens as keys (value, then lowest index), which are all
+// different, 32 in its lanes.  A value enters only if it is above a threshold that
+// the block's warps share, the largest k-th key that any of them has: old ones are too low,
+// never too high, so nobody waits for it.  The first comes from the threads' own
+// maxima: if k of them are T or more, the row's k-th best is not below T, and a
+// short search finds such a T that few more reach.  Lanes push such keys to shared memory; when 32 have
+// gathered the warp sorts them and merges.  The warps' lists are merged at the end.
 //
 // A row is one block's, or a cluster's: each block takes a run of it, and the
 // first joins their sums and keys through distributed shared memory.  So there
 // is one launch, no workspace, and results that do not depend on any order.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
+#include <type_traits>
 
 #include "abi_guard.h"
 #include "la_common.cuh"
@@ -58,7 +63,7 @@ __device__ __forceinline__ LpSum lp_join(const LpSum &x, const LpSum &y) {
     const bool xb = x.m >= y.m;
     const LpSum a = xb ? x : y, b = xb ? y : x;
     if (b.m == -INFINITY) return {a.m, a.r + b.r, a.s};   // r is 0, or NaN where a value was
-    const float d = b.m - a.m, f = expf(d), n = 1.f + b.r;
+    const float d = b.m - a.m, f = lp_ex2(d * 1.4426950408889634f), n = 1.f + b.r;
     // f = 0 and d = -infinity: a product that is 0
     return {a.m, fmaf(n, f, a.r), f > 0.f ? fmaf(f, fmaf(d, n, b.s), a.s) : a.s};
 }
@@ -98,24 +103,72 @@ struct LpArgs {
     int blocks;   // of a row
 };
 
+// The larger, NaN if either is.
+__device__ __forceinline__ float lp_max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+__device__ __forceinline__ float lp_max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t lp_two(float a, float b) {
+    uint64_t y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float2 lp_halves(uint64_t v) {
+    float2 y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(v));
+    return y;
+}
+__device__ __forceinline__ uint64_t lp_add2(uint64_t a, uint64_t b) {
+    uint64_t y;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+__device__ __forceinline__ uint64_t lp_mul2(uint64_t a, uint64_t b) {
+    uint64_t y;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+__device__ __forceinline__ uint64_t lp_fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+    return y;
+}
+
+// Keys that a warp gathers before it merges them, and room for half a pass's.
+constexpr int kLpGather = 32, kLpRoom = kLpGather + 16 * kLpPass + 32;
+constexpr int kLpStages = 2;   // passes of a thread in shared memory
+
+__device__ __forceinline__ void lp_copy(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) k_logprobs(const __grid_constant__ LpArgs p) {
+__global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constant__ LpArgs p) {
     constexpr int VEC = LpType<T>::vec, E = kLpPass, NV = E / VEC;   // 16-byte loads of a pass
     constexpr float kLog2e = 1.4426950408889634f;
-    __shared__ LpKey sh_push[kLpThreads * E];    // a pass can push all that it holds
-    __shared__ LpKey sh_list[kLpTop];
-    __shared__ LpKey sh_first[kLpWarps];
+    constexpr uint32_t kNone = VEC == 4 ? 0xff800000u : 0xff80ff80u;  // -infinity
+    extern __shared__ __align__(16) uint8_t lp_smem[];
+    uint4(*sh_ring)[NV][kLpThreads] = reinterpret_cast<uint4(*)[NV][kLpThreads]>(lp_smem);
+    LpKey(*sh_push)[kLpRoom] = reinterpret_cast<LpKey(*)[kLpRoom]>(lp_smem + kLpStages * NV * kLpThreads * 16);
+    __shared__ LpKey sh_list[kLpWarps][kLpTop];
+    __shared__ uint2 sh_first[kLpWarps];
     __shared__ LpSum sh_sum[kLpWarps];
     __shared__ LpSum sh_block;
-    __shared__ LpKey sh_t;                       // last key of the list, once it is full
-    __shared__ int sh_n;
+    __shared__ LpKey sh_t;                       // the largest last key of a full list
+    __shared__ int sh_n[kLpWarps];               // keys that a warp has gathered
     const la_logprobs_args &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, C = p.blocks, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int row = blockIdx.x / C, top = a.n_top;
-    if (tid == 0) {
-        sh_n = 0;
-        sh_t = 0;
-    }
+    if (lane == 0) sh_n[warp] = 0;
+    if (tid == 0) sh_t = 0;
     pdl_trigger();
     pdl_wait();
     const T *z = static_cast<const T *>(a.logits) + row * a.stride;
@@ -124,171 +177,228 @@ __global__ void __launch_bounds__(kLpThreads) k_logprobs(const __grid_constant__
     const int vecs = (a.vocab - head) / VEC, tail = head + vecs * VEC, odd = head + a.vocab - tail;
     const int per = (vecs + C - 1) / C, v0 = min(rank * per, vecs), v1 = min(v0 + per, vecs);
     const uint4 *zv = reinterpret_cast<const uint4 *>(z + head);
-
+    // A pass's copies; past the run's end the last vector again, which does not count then
+    auto copy = [&](int base, int stage) {
+        if (base < v1) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) lp_copy(smem_u32(&sh_ring[stage][k][tid]), zv + min(base + k * kLpThreads + tid, v1 - 1));
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    copy(v0, 0);
     float given = -INFINITY;   // the logit of this thread's given token, read while the row is
     if (rank == 0 && tid < a.n_tokens) {
         const int t = a.tokens[static_cast<long long>(row) * a.n_tokens + tid];
         if (t >= 0 && t < a.vocab) given = to_f32<T>(z[t]);
     }
-    LpSum sum = {-INFINITY, 0.f, 0.f};
-    LpKey list = 0;   // warp 0: the lane's best so far
-    // Adds N values (-infinity: none) to the thread's sums.
-    auto add = [&](auto &v, float most) {
+    // Terms of this thread: r those below its warp's maximum m, ones those equal to it; pairs of sums
+    float m = -INFINITY;
+    uint64_t r = 0, s = 0;
+    int ones = 0;
+    auto add = [&](auto &v, float most) {   // all lanes of a warp call it
         constexpr int N = sizeof(v) / sizeof(float);
-        if (most > sum.m) {
-            const float f = expf(sum.m - most), n = 1.f + sum.r;   // sum.m = -infinity: f = 0
-            sum.s = f > 0.f ? f * fmaf(sum.m - most, n, sum.s) : 0.f;
-            sum.r = f > 0.f ? n * f : 0.f;
-            sum.m = most;
-            bool out = false;   // one maximal value stands apart
+        const uint32_t key = __reduce_max_sync(0xffffffffu, order_key(most + 0.f));
+        most = lp_value(static_cast<LpKey>(key) << 32);
+        if (most > m) {
+            const float d = m - most, f = lp_ex2(d * kLog2e);   // m = -infinity: f = 0
+            const float2 y = lp_halves(r), z = lp_halves(s);
+            const float n = y.x + y.y + static_cast<float>(ones), old = z.x + z.y;
+            s = lp_two(f > 0.f ? f * fmaf(d, n, old) : 0.f, 0.f);
+            r = lp_two(n * f, 0.f);
+            ones = 0;
+            m = most;
+        }
+        const float base = m == -INFINITY ? 0.f : -m;
+        const bool hit = most == m;         // some of these are equal to m
+        const uint64_t base2 = lp_two(base, base), log2e2 = lp_two(kLog2e, kLog2e);
+        auto terms = [&](auto apart) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const bool it = !out && v[e] == most;
-                out |= it;
-                if (it) v[e] = -INFINITY;
+            for (int e = 0; e < N; e += 2) {
+                float2 d = lp_halves(lp_add2(lp_two(v[e], e + 1 < N ? v[e + 1 < N ? e + 1 : e] : -INFINITY), base2));
+                d.x = lp_max_nan(d.x, -20000.f);   // finite: 0 times d
+                d.y = lp_max_nan(d.y, -20000.f);
+                const uint64_t d2 = lp_two(d.x, d.y);
+                const float2 y = lp_halves(lp_mul2(d2, log2e2));
+                float x0 = lp_ex2(y.x), x1 = lp_ex2(y.y);
+                if constexpr (decltype(apart)::value) {
+                    ones += (d.x == 0.f) + (d.y == 0.f);
+                    x0 = d.x == 0.f ? 0.f : x0;
+                    x1 = d.y == 0.f ? 0.f : x1;
+                }
+                const uint64_t x2 = lp_two(x0, x1);
+                r = lp_add2(r, x2);
+                s = lp_fma2(x2, d2, s);
             }
-        }
-        const float m = sum.m == -INFINITY ? 0.f : sum.m;
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            const float d = v[e] - m, x = lp_ex2(d * kLog2e);
-            sum.r += x;
-            sum.s = x == 0.f ? sum.s : fmaf(x, d, sum.s);
-        }
+        };
+        if (hit) terms(std::true_type{});   // the whole warp
+        else terms(std::false_type{});
     };
-    // Warp 0 takes in what has been pushed.
-    auto take = [&]() {
-        const int n = sh_n;
+    LpKey list = 0;            // the lane's of the warp's best so far
+    LpKey limit = 0;           // what may enter is above it
+    float below = -INFINITY;   // and its value above this
+    volatile int *gathered = &sh_n[warp];
+    volatile LpKey *threshold = &sh_t;
+    auto raise = [&](LpKey t) {
+        limit = max(limit, t);
+        const uint32_t hi = static_cast<uint32_t>(limit >> 32);
+        below = hi > 0x00800000u ? lp_value(static_cast<LpKey>(hi - 1) << 32) : -INFINITY;   // above -FLT_MAX: the next float down
+    };
+    auto push = [&](float x, int i) {
+        const LpKey k = lp_key(x, i);
+        if (k > limit) sh_push[warp][atomicAdd(&sh_n[warp], 1)] = k;
+    };
+    auto merge = [&](int n) {   // the warp's keys
 #pragma unroll 1
         for (int i = 0; i < n; i += 32) {
-            const LpKey x = i + lane < n ? sh_push[i + lane] : 0, last = __shfl_sync(0xffffffffu, list, top - 1);
+            const LpKey x = i + lane < n ? sh_push[warp][i + lane] : 0, last = __shfl_sync(0xffffffffu, list, top - 1);
             if (__any_sync(0xffffffffu, x > last)) list = lp_merge(list, lp_sort(x, lane), lane);
         }
-        __syncwarp();
         const LpKey last = __shfl_sync(0xffffffffu, list, top - 1);
         if (lane == 0) {
-            sh_t = last;
-            sh_n = 0;
+            *gathered = 0;
+            if (last > *threshold) atomicMax(&sh_t, last);
         }
+        __syncwarp();
     };
     __syncthreads();
 
-    bool begun = false;
 #pragma unroll 1
-    for (int base = v0; base < v1; base += kLpThreads * NV) {
+    for (int base = v0, stage = 0; base < v1; base += kLpThreads * NV, stage ^= 1) {
+        copy(base + kLpThreads * NV, stage ^ 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        uint4 w[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) w[k] = sh_ring[stage][k][tid];
+        if (base + kLpThreads * NV > v1) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if (base + k * kLpThreads + tid >= v1) sh_ring[stage][k][tid] = w[k] = make_uint4(kNone, kNone, kNone, kNone);
+        }
         float v[E];
-        float most = -INFINITY;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int at = base + k * kLpThreads + tid;
-            uint4 w;
-            if (at < v1) w = __ldcs(zv + at);
-            if constexpr (VEC == 4) {
-                v[4 * k] = __uint_as_float(w.x), v[4 * k + 1] = __uint_as_float(w.y), v[4 * k + 2] = __uint_as_float(w.z), v[4 * k + 3] = __uint_as_float(w.w);
-            } else {
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (VEC == 4) {
+                    v[4 * k + i] = __uint_as_float(u[i]);
+                } else {
                     v[8 * k + 2 * i] = __uint_as_float(u[i] << 16);
                     v[8 * k + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
                 }
             }
-            if (at >= v1) {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) v[VEC * k + i] = -INFINITY;
-            }
         }
+        float quad[E / 4], most = -INFINITY;   // largest of four, and of all; a NaN is none
 #pragma unroll
-        for (int e = 0; e < E; ++e) most = fmaxf(most, v[e]);   // a NaN is none
+        for (int q = 0; q < E / 4; ++q) quad[q] = fmaxf(lp_max3(v[4 * q], v[4 * q + 1], v[4 * q + 2]), v[4 * q + 3]);
+        most = lp_max3(lp_max3(most, quad[0], quad[1]), quad[2], quad[3]);
         if (top) {
-            auto index = [&](int e) { return head + (base + (e / VEC) * kLpThreads + tid) * VEC + e % VEC; };
-            LpKey t = 0;
-            if (!begun) {
-                // The warp's k-th largest of its lanes' largest keys; the largest of the warps' is the threshold.
-                LpKey mine = 0;
-#pragma unroll
-                for (int e = E - 1; e >= 0; --e)
-                    if (v[e] == most && most > -INFINITY) mine = lp_key(most, index(e));
-#pragma unroll 1
-                for (int i = 0; i < top; ++i) {
-                    const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(mine >> 32));
-                    const bool in = static_cast<uint32_t>(mine >> 32) == hi;
-                    const uint32_t lo = __reduce_max_sync(0xffffffffu, in ? static_cast<uint32_t>(mine) : 0u);
-                    t = static_cast<LpKey>(hi) << 32 | lo;
-                    if (mine == t) mine = 0;
+            if (base == v0) {
+                // lo: `top` threads or more reach it (or none is asked to), at first the
+                // warps' least k / 8-th; hi: fewer do
+                const uint32_t mine = most > -INFINITY ? order_key(most + 0.f) : 0u;
+                uint32_t rest = mine, lo = 0, hi = 0;
+                for (int i = 0; i < top; i += kLpWarps) {
+                    lo = __reduce_max_sync(0xffffffffu, rest);
+                    if (rest == lo) rest = 0;
+                    hi = max(hi, lo);
                 }
-                if (lane == 0) sh_first[warp] = t;
+                if (lane == 0) sh_first[warp] = make_uint2(lo, hi);
                 __syncthreads();
 #pragma unroll
-                for (int w = 0; w < kLpWarps; ++w) t = max(t, sh_first[w]);
-                begun = true;
+                for (int w = 0; w < kLpWarps; ++w) {
+                    lo = min(lo, sh_first[w].x);
+                    hi = max(hi, sh_first[w].y);
+                }
+                if (lo > 0 && top > 1) {
+                    ++hi;
+                    for (int i = 0; i < 5 && hi - lo > 1; ++i) {
+                        const uint32_t mid = lo + (hi - lo) / 2;
+                        if (__syncthreads_count(mine >= mid) >= top) lo = mid;
+                        else hi = mid;
+                    }
+                } else if (top == 1) {
+                    lo = hi;
+                }
+                raise(lo ? (static_cast<LpKey>(lo) << 32) - 1 : 0);
             } else {
-                t = sh_t ? sh_t + 1 : 0;
+                const LpKey t = *threshold;
+                if (t > limit) raise(t);
             }
-            const float least = t ? lp_value(t) : -INFINITY;
-            bool pushed = false;
-            if (most >= least && most > -INFINITY) {
+            if (__any_sync(0xffffffffu, most > below)) {
+                const int first = head + (base + tid) * VEC;
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    if (v[e] >= least && v[e] > -INFINITY) {
-                        const LpKey k = lp_key(v[e], index(e));
-                        if (k >= t) {
-                            sh_push[atomicAdd(&sh_n, 1)] = k;
-                            pushed = true;
+                for (int q = 0; q < E / 4; ++q) {
+                    if (quad[q] > below) {
+#pragma unroll
+                        for (int e = 4 * q; e < 4 * q + 4; ++e)
+                            if (v[e] > below) push(v[e], first + e / VEC * kLpThreads * VEC + e % VEC);
+                    }
+                    if (q & 1) {
+                        __syncwarp();
+                        const int n = *gathered;
+                        if (n >= kLpGather) {
+                            merge(n);
+                            const LpKey t = *threshold;
+                            if (t > limit) raise(t);
                         }
                     }
                 }
             }
-            if (__syncthreads_or(pushed)) {
-                if (warp == 0) take();
-                add(v, most);
-                __syncthreads();
-            } else {
-                add(v, most);
-            }
-        } else {
-            add(v, most);
         }
+        add(v, most);
     }
     if (rank == C - 1 && odd > 0) {   // the single elements
-        float v[1] = {-INFINITY};
         const int i = tid < head ? tid : tail + tid - head;
-        if (tid < odd) v[0] = to_f32<T>(z[i]);
-        if (top) {
-            __syncthreads();   // sh_t is the last pass's
-            const LpKey k = tid < odd && v[0] > -INFINITY ? lp_key(v[0], i) : 0;
-            if (k > sh_t) sh_push[atomicAdd(&sh_n, 1)] = k;
-            __syncthreads();
-            if (warp == 0) take();
-        }
-        add(v, isnan(v[0]) ? -INFINITY : v[0]);
+        float v[1] = {tid < odd ? to_f32<T>(z[i]) : -INFINITY};
+        if (top && tid < odd && v[0] > -INFINITY) push(v[0], i);
+        __syncwarp();
+        add(v, v[0] > -INFINITY ? v[0] : -INFINITY);   // a NaN is none
+    }
+    if (top) {
+        __syncwarp();
+        merge(*gathered);
+        sh_list[warp][lane] = list;
     }
 
     // The block's sums and list
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const LpSum y = {__shfl_xor_sync(0xffffffffu, sum.m, o), __shfl_xor_sync(0xffffffffu, sum.r, o), __shfl_xor_sync(0xffffffffu, sum.s, o)};
-        sum = lane & o ? lp_join(y, sum) : lp_join(sum, y);
+    LpSum sum;
+    {
+        const float2 y = lp_halves(r), z = lp_halves(s);
+        ones = __reduce_add_sync(0xffffffffu, ones);
+        sum = {m, warp_sum(y.x + y.y) + static_cast<float>(ones > 0 ? ones - 1 : 0), warp_sum(z.x + z.y)};
     }
     if (lane == 0) sh_sum[warp] = sum;
     __syncthreads();
+    if (top) {   // the warps' lists, two and two
+#pragma unroll 1
+        for (int o = kLpWarps / 2; o; o >>= 1) {
+            if (warp < o) sh_list[warp][lane] = list = lp_merge(list, sh_list[warp + o][lane], lane);
+            __syncthreads();
+        }
+    }
     if (warp == 0) {
         sum = sh_sum[0];
         for (int w = 1; w < kLpWarps; ++w) sum = lp_join(sum, sh_sum[w]);
         if (lane == 0) sh_block = sum;
-        sh_list[lane] = list;
     }
     if (C > 1) {
         cluster_sync_all();
         if (rank == 0 && warp == 0) {
-            for (int c = 1; c < C; ++c) {
+            LpSum sums[7];   // all on their way at once
+            LpKey keys[7];
+#pragma unroll
+            for (int c = 1; c < 8; ++c) {
+                if (c >= C) break;
                 const uint32_t at = mapa_shared(smem_u32(&sh_block), c);
-                sum = lp_join(sum, {ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)});
-                if (top) {
-                    LpKey k;
-                    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(k) : "r"(mapa_shared(smem_u32(&sh_list[lane]), c)) : "memory");
-                    list = lp_merge(list, k, lane);
-                }
+                sums[c - 1] = {ld_cluster_f32(at), ld_cluster_f32(at + 4), ld_cluster_f32(at + 8)};
+                asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(keys[c - 1]) : "r"(mapa_shared(smem_u32(&sh_list[0][lane]), c)) : "memory");
+            }
+#pragma unroll
+            for (int c = 1; c < 8; ++c) {
+                if (c >= C) break;
+                sum = lp_join(sum, sums[c - 1]);
+                if (top) list = lp_merge(list, keys[c - 1], lane);
             }
             if (lane == 0) sh_block = sum;
         }
@@ -335,10 +445,11 @@ cudaError_t logprobs_launch(const la_logprobs_args &a, int nsm, cudaStream_t s) 
     // Blocks of a row: while the rows leave SMs idle and each has a pass of its own
     const int pass = kLpThreads * kLpPass;
     p.blocks = 1;
-    while (p.blocks < 8 && static_cast<long long>(a.rows) * p.blocks * 2 <= 2 * nsm && a.vocab > p.blocks * pass) p.blocks *= 2;
+    while (p.blocks < 8 && static_cast<long long>(a.rows) * p.blocks * 2 <= nsm && a.vocab > p.blocks * pass) p.blocks *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * p.blocks);
     cfg.blockDim = dim3(kLpThreads);
+    cfg.dynamicSmemBytes = kLpStages * kLpThreads * kLpPass * (a.type == LA_F32 ? 4 : 2) + kLpWarps * kLpRoom * 8;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -348,6 +459,17 @@ cudaError_t logprobs_launch(const la_logprobs_args &a, int nsm, cudaStream_t s) 
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = p.blocks > 1 ? 2 : 1;
+    static std::atomic<unsigned long long> done{0};   // bit d: device d allows that much shared memory
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(done.load() >> dev & 1)) {
+        const int most = kLpStages * kLpThreads * kLpPass * 4 + kLpWarps * kLpRoom * 8;
+        e = cudaFuncSetAttribute(k_logprobs<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(k_logprobs<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) done.fetch_or(1ull << dev);
+    }
     return a.type == LA_F32 ? cudaLaunchKernelEx(&cfg, k_logprobs<float>, p) : cudaLaunchKernelEx(&cfg, k_logprobs<__nv_bfloat16>, p);
 }
 
