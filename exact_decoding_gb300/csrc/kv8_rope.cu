@@ -12,9 +12,20 @@
 // A block takes some rows and some of their heads.  Its threads find the rows'
 // positions and compute a row's sines and cosines once, for all of its heads,
 // into shared memory; then HD / 16 lanes share a head, 8 rotary pairs each, so
-// both halves of a pair are one lane's.
+// both halves of a pair are one lane's, 16 bytes a load, and the norm is one
+// reduction over 4 or 8 lanes.
+//
+// Memory bounds a prompt: 6144 rows of 72 heads of 128, bf16 (151 MB): 29.8 us,
+// 5.1 TB/s, 75 % of a copy's rate.  What is left: a block finds positions and
+// angles before its first load.  Hidden by other blocks of the SM, so registers
+// are held to 48 (five blocks; four 32.1 us, eight with spills 39.7) and a lane
+// has one head in flight (two: 30.7).  Up to 16 passes of heads a block (8:
+// 30.2, 4: 32.4) while that leaves four blocks for every SM.  Tables lie so that the lanes
+// of a head read 16 bytes side by side.  A single token (32 + 2 * 32 heads,
+// fp32): 3.6 us, latency.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "kv8.h"
 
@@ -50,6 +61,27 @@ __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, flo
         x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
 }
+// Two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float2 one_by_one(uint64_t v) {
+    float2 y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(y.x), "=f"(y.y) : "l"(v));
+    return y;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t y;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+    return y;
+}
 __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
     uint32_t w[4];
 #pragma unroll
@@ -61,15 +93,26 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
 }
 
 template <int HD, typename T>
-__global__ void __launch_bounds__(kRopeThreads) k_kv8_norm_rope(const __grid_constant__ RopeArgs p) {
+__global__ void __launch_bounds__(kRopeThreads, 5) k_kv8_norm_rope(const __grid_constant__ RopeArgs p) {
     constexpr int H2 = HD / 2, L = HD / 16, ITEMS = kRopeThreads / L;   // lanes of a head; heads at a time
     __shared__ int sh_pos[kRopeRows];
     __shared__ int sh_on[kRopeRows];
-    __shared__ __align__(16) float2 sh_cs[kRopeRows][H2];   // cos, sin; pair 8 j + 2 c (+ 1) of lane j at 2 (c L + j) (+ 1)
-    __shared__ __align__(16) float sh_w[2][HD];
+    // cos and sin of the pairs: pairs 8 j + 2 c and + 1 of lane j at [c][j]
+    __shared__ __align__(16) ulonglong2 sh_cs[kRopeRows][4][L];
+    // gains of q and of k: values 8 j + 2 c and + 1 of a head's two halves at [c][j]
+    __shared__ __align__(16) ulonglong2 sh_w[2][4][L];
     const la_kv8_qkv &a = p.a;
     const int tid = threadIdx.x, r0 = blockIdx.x * p.rows, nr = min(p.rows, a.n_rows - r0);
     const int h_all = a.n_heads + p.n_kv_heads * (a.v ? 2 : 1), h0 = blockIdx.y * p.heads, nh = min(p.heads, h_all - h0);
+    const int j = tid % L;
+    // The block's heads of q, of k and of v: heads h0 .. h0 + nh - 1 of them all in a row
+    auto part = [&](int from, int count, int &first) {
+        first = min(max(h0 - from, 0), count);
+        return max(min(h0 + nh - from, count), first) - first;
+    };
+    int q_first, k_first, v_first;
+    const int q_heads = part(0, a.n_heads, q_first), k_heads = part(a.n_heads, p.n_kv_heads, k_first),
+              v_heads = part(a.n_heads + p.n_kv_heads, a.v ? p.n_kv_heads : 0, v_first);
     pdl_trigger();
     pdl_wait();
     // Positions of the block's rows
@@ -106,7 +149,9 @@ __global__ void __launch_bounds__(kRopeThreads) k_kv8_norm_rope(const __grid_con
     for (int i = tid; i < 2 * HD; i += kRopeThreads) {
         const void *w = i < HD ? a.q_weight : a.k_weight;
         const int d = i & (HD - 1);
-        if (w) sh_w[i / HD][d] = a.weight_type == LA_F32 ? static_cast<const float *>(w)[d] : __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[d]);
+        const int e = d & 7, half = d / H2;
+        float *to = reinterpret_cast<float *>(&sh_w[i / HD][e >> 1][(d - half * H2) >> 3]) + 2 * half + (e & 1);
+        if (w) *to = a.weight_type == LA_F32 ? static_cast<const float *>(w)[d] : __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[d]);
     }
     __syncthreads();
     for (int i = tid; i < nr * H2; i += kRopeThreads) {
@@ -119,55 +164,71 @@ __global__ void __launch_bounds__(kRopeThreads) k_kv8_norm_rope(const __grid_con
         const uint64_t t = f * static_cast<uint64_t>(static_cast<int64_t>(sh_pos[r]));   // turns * 2^64, modulo 2^64
         float s, c;
         sincospif(static_cast<float>(static_cast<int>(t >> 32)) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns, -1 .. 1
-        const int j = k >> 3, e = k & 7;
-        sh_cs[r][2 * ((e >> 1) * L + j) + (e & 1)] = make_float2(c, s);
+        const int e = k & 7;
+        float *to = reinterpret_cast<float *>(&sh_cs[r][e >> 1][k >> 3]) + (e & 1);
+        to[0] = c;
+        to[2] = s;
     }
     __syncthreads();
 
-    const int j = tid % L;
-#pragma unroll 2
-    for (int i = tid / L; i < nr * nh; i += ITEMS) {   // whole groups of L lanes
-        const int r = i / nh, head = h0 + i % nh, row = r0 + r;
-        if (!sh_on[r]) continue;                       // rows of no slot stay as they are
-        const int kind = head < a.n_heads ? 0 : head < a.n_heads + p.n_kv_heads ? 1 : 2;
-        const int h = kind == 0 ? head : head - a.n_heads - (kind - 1) * p.n_kv_heads;
-        const T *src = static_cast<const T *>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + row * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + h * HD + 8 * j;
-        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(kind == 0 ? a.q_out : kind == 1 ? a.k_out : a.v_out) +
-                             row * (kind == 0 ? a.q_out_stride : kind == 1 ? a.k_out_stride : a.v_out_stride) + h * HD + 8 * j;
-        float x[8], y[8];
-        load8(src, x);
-        load8(src + H2, y);
-        if (kind < 2) {
-            if (kind == 0 ? a.q_weight : a.k_weight) {
-                float sum = 0.f;
+    // Heads of one kind: `heads` of every row from `first` on, a group of L lanes
+    // (whole in its warp) for each.
+    auto heads_of = [&](auto rotated, const T *src, __nv_bfloat16 *dst, long long src_stride, long long dst_stride, int heads, int first, const void *weight, int kind) {
+        if (heads < 1) return;
+        const float per_row = 1.f / static_cast<float>(heads);
+        src += r0 * src_stride + first * HD + 8 * j;
+        dst += r0 * dst_stride + first * HD + 8 * j;
+#pragma unroll 1
+        for (int i = tid / L; i < nr * heads; i += ITEMS) {
+            // i / heads: below 16 rows the quotient is off by less than the half that was added
+            const int r = static_cast<int>((static_cast<float>(i) + 0.5f) * per_row), at = (i - r * heads) * HD;
+            if (!sh_on[r]) continue;   // rows of no slot stay as they are
+            float x[8], y[8];
+            load8(src + r * src_stride + at, x);
+            load8(src + r * src_stride + at + H2, y);
+            if constexpr (decltype(rotated)::value) {
+                uint64_t x2[4], y2[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum = fmaf(x[e], x[e], fmaf(y[e], y[e], sum));
-                const unsigned lanes = (L == 8 ? 0xffu : 0xfu) << (tid & 31 & ~(L - 1));
+                for (int c = 0; c < 4; ++c) {
+                    x2[c] = two(x[2 * c], x[2 * c + 1]);
+                    y2[c] = two(y[2 * c], y[2 * c + 1]);
+                }
+                if (weight) {
+                    uint64_t s2 = mul2(x2[0], x2[0]);
 #pragma unroll
-                for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(lanes, sum, o);
-                const float n = rsqrtf(sum * (1.f / HD) + a.eps);
-                const float4 *w = reinterpret_cast<const float4 *>(sh_w[kind] + 8 * j), *u = reinterpret_cast<const float4 *>(sh_w[kind] + H2 + 8 * j);
-                const float4 w0 = w[0], w1 = w[1], u0 = u[0], u1 = u[1];
-                const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w}, uu[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+                    for (int c = 1; c < 4; ++c) s2 = fma2(x2[c], x2[c], s2);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[e] *= n * ww[e];
-                    y[e] *= n * uu[e];
+                    for (int c = 0; c < 4; ++c) s2 = fma2(y2[c], y2[c], s2);
+                    const float2 halves = one_by_one(s2);
+                    float sum = halves.x + halves.y;
+                    const unsigned lanes = (L == 8 ? 0xffu : 0xfu) << (tid & 31 & ~(L - 1));
+#pragma unroll
+                    for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(lanes, sum, o);
+                    const float n = rsqrtf(sum * (1.f / HD) + a.eps);
+                    const uint64_t n2 = two(n, n);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const ulonglong2 w = sh_w[kind][c][j];
+                        x2[c] = mul2(mul2(x2[c], n2), w.x);
+                        y2[c] = mul2(mul2(y2[c], n2), w.y);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const ulonglong2 t = sh_cs[r][c][j];   // cosines, sines
+                    const float2 p0 = one_by_one(fma2(y2[c], t.y ^ 0x8000000080000000ull, mul2(x2[c], t.x))),
+                                 p1 = one_by_one(fma2(x2[c], t.y, mul2(y2[c], t.x)));
+                    x[2 * c] = p0.x, x[2 * c + 1] = p0.y;
+                    y[2 * c] = p1.x, y[2 * c + 1] = p1.y;
                 }
             }
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float4 t = *reinterpret_cast<const float4 *>(&sh_cs[r][2 * (c * L + j)]);
-                const float a0 = x[2 * c], b0 = y[2 * c], a1 = x[2 * c + 1], b1 = y[2 * c + 1];
-                x[2 * c] = a0 * t.x - b0 * t.y;
-                y[2 * c] = b0 * t.x + a0 * t.y;
-                x[2 * c + 1] = a1 * t.z - b1 * t.w;
-                y[2 * c + 1] = b1 * t.z + a1 * t.w;
-            }
+            store8(dst + r * dst_stride + at, x);
+            store8(dst + r * dst_stride + at + H2, y);
         }
-        store8(dst, x);
-        store8(dst + H2, y);
-    }
+    };
+    heads_of(std::true_type{}, static_cast<const T *>(a.q), static_cast<__nv_bfloat16 *>(a.q_out), a.q_stride, a.q_out_stride, q_heads, q_first, a.q_weight, 0);
+    heads_of(std::true_type{}, static_cast<const T *>(a.k), static_cast<__nv_bfloat16 *>(a.k_out), a.k_stride, a.k_out_stride, k_heads, k_first, a.k_weight, 1);
+    heads_of(std::false_type{}, static_cast<const T *>(a.v), static_cast<__nv_bfloat16 *>(a.v_out), a.v_stride, a.v_out_stride, v_heads, v_first, nullptr, 0);
 }
 
 cudaError_t kv8_norm_rope_launch(const la_kv8_cache &c, const la_kv8_qkv &a, int nsm, cudaStream_t s) {
@@ -180,15 +241,20 @@ cudaError_t kv8_norm_rope_launch(const la_kv8_cache &c, const la_kv8_qkv &a, int
     p.n_kv_heads = c.n_kv_heads;
     p.room = static_cast<long long>(c.max_pages) * c.page;
     if (!a.inv_freq) {
-        // f_i = base^(-2 i / head_dim); in turns, its part below one
+        // f_i = base^(-2 i / head_dim), a power for i / 8 times one for i % 8 (a
+        // quarter of the powers, two roundings more); in turns, its part below one
+        double low[8], high = 1.;
         for (int i = 0; i < c.head_dim / 2; ++i) {
-            const double x = std::pow(static_cast<double>(a.rope_base), -2.0 * i / c.head_dim) * 0.15915494309189533577;
+            const auto power = [&](int n) { return std::pow(static_cast<double>(a.rope_base), -2.0 * n / c.head_dim); };
+            if (i < 8) low[i] = power(i) * 0.15915494309189533577;
+            if (i % 8 == 0 && i) high = power(i);
+            const double x = high * low[i % 8];
             const double t = (x - std::floor(x)) * 18446744073709551616.0;
             p.turn[i] = t < 18446744073709549568.0 ? static_cast<uint64_t>(t) : ~0ull;
         }
     }
     const int items = kRopeThreads / (c.head_dim / 16), h_all = a.n_heads + c.n_kv_heads * (a.v ? 2 : 1);
-    const long long all = static_cast<long long>(a.n_rows) * h_all, per = std::max<long long>(1, std::min<long long>(8, all / (static_cast<long long>(items) * nsm * 4)));
+    const long long all = static_cast<long long>(a.n_rows) * h_all, per = std::max<long long>(1, std::min<long long>(16, all / (static_cast<long long>(items) * nsm * 4)));
     // `per` passes of `items` heads for a block: as many rows as that takes, or a part of one row's heads
     p.rows = static_cast<int>(std::max<long long>(1, std::min<long long>(kRopeRows, per * items / h_all)));
     p.heads = p.rows > 1 || h_all <= per * items ? h_all : static_cast<int>(per * items);
