@@ -24,7 +24,10 @@
 // Short calls are bound by instruction fetches: code that runs once per call
 // comes from L2 a line at a time, about 50 instructions per microsecond.  So
 // what runs once is written as small loops, and only the loops over keys are
-// unrolled.
+// unrolled, with one exception: the join of a CTA's warps, whose reads would wait
+// for one another (0.4 us of a call).  Divisions by sizes known at run time are
+// shifts, and a unit's own loads go out before its copies (117 tokens of 32
+// heads: 8.5 us with neither, 7.1 with both).
 #include <algorithm>
 #include <atomic>
 
@@ -54,7 +57,8 @@ struct Kv8Args {
     int gq;            // query heads per KV head
     int page_log2;
     int q_tile;        // query vectors per unit
-    int k_tile, n_tile;   // cached tokens, new rows per key tile (0: the new rows are not counted in tiles)
+    int q_log2, k_log2;   // of q_tile and k_tile: a division by a number known at run time takes hundreds of cycles where nothing hides it
+    int k_tile, n_tile;   // cached tokens, new rows per key tile (the same, or 0: the new rows are not counted in tiles)
     int unit_cost;     // what a unit costs beside its key tiles, in tiles
     int snap;          // a share that begins within this many tiles of a unit's begin begins with the unit
     int whole;         // 1: worker w runs units w, w + workers, ... whole, and nothing is joined
@@ -95,20 +99,28 @@ struct Kv8Seq {
 // first, and tiles between the two that no row of the slot sees are left out of
 // the slot's tiles.  So a unit's work is what its rows see, but for tiles at the
 // two edges, in which keys are masked.
+//
+// Windows measured (floor: the window's bytes, or its products): the last 4096 of
+// 65413 tokens and 4 first ones, 64 heads over 8 KV heads, 14.0 us (the same
+// tokens without a window 12.0 in a cache of no more; 8.4 MB, latency); 64
+// sequences of up to 8192, window 1024, 38.5 us (130 MB: 3.4 TB/s); 121 rows of 32
+// heads, window 512, 32.3 us; 256 rows over 16k tokens, window 4096, 63.9 us
+// (115.7 without).  What a short unit costs beside its tiles bounds them: positions,
+// pages and queries are looked up one behind another before the first product.
 template <bool WIN>
 __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Args &p, int s) {
     Kv8Seq q;
     q.rows = kv8_rows(p.c, p.a.row_start, p.a.n_rows, s, &q.first);
     q.len = kv8_len(p.c, s);
-    q.qtiles = static_cast<int>((static_cast<long long>(q.rows) * p.gq + p.q_tile - 1) / p.q_tile);
-    q.ctiles = (q.len + p.k_tile - 1) / p.k_tile;
+    q.qtiles = static_cast<int>((static_cast<long long>(q.rows) * p.gq + p.q_tile - 1) >> p.q_log2);
+    q.ctiles = (q.len + p.k_tile - 1) >> p.k_log2;
     if constexpr (WIN) {
         const int first = min(max(q.len + (p.a.k && !p.a.vis ? 1 : 0) - p.window, 0), q.len);   // of the slot's earliest window
-        q.keep = (min(p.sinks, q.len) + p.k_tile - 1) / p.k_tile;
-        q.skip = max((first == q.len ? q.ctiles : first / p.k_tile) - q.keep, 0);
+        q.keep = (min(p.sinks, q.len) + p.k_tile - 1) >> p.k_log2;
+        q.skip = max((first == q.len ? q.ctiles : first >> p.k_log2) - q.keep, 0);
         q.ctiles -= q.skip;
     }
-    q.ntiles = p.a.k && p.n_tile ? (q.rows + p.n_tile - 1) / p.n_tile : 0;
+    q.ntiles = p.a.k && p.n_tile ? (q.rows + p.n_tile - 1) >> p.k_log2 : 0;
     q.ktiles = p.whole ? 1 : p.unit_cost + q.ctiles + q.ntiles;
     return q;
 }
@@ -203,7 +215,7 @@ __device__ __forceinline__ bool kv8_next(const Kv8Args &p, const long long *tile
     u.sq = kv8_seq<WIN>(p, u.s);
     const int kt = u.sq.ktiles;
     const long long in_slot = w.at - tiles[u.s];
-    const int unit = static_cast<int>(kv8_div(in_slot, kt));
+    const int unit = static_cast<int>(p.whole ? in_slot : kv8_div(in_slot, kt));
     if (p.whole) {
         u.k0 = 0;
         u.k1 = u.sq.ctiles + u.sq.ntiles;
@@ -218,8 +230,8 @@ __device__ __forceinline__ bool kv8_next(const Kv8Args &p, const long long *tile
         u.begins = v0 == 0;
         w.at += v1 - v0;
     }
-    u.head = unit / u.sq.qtiles;
-    u.qv0 = (unit % u.sq.qtiles) * p.q_tile;
+    u.head = u.sq.qtiles == 1 ? unit : unit / u.sq.qtiles;
+    u.qv0 = (unit - u.head * u.sq.qtiles) << p.q_log2;
     u.nqv = min(p.q_tile, u.sq.rows * p.gq - u.qv0);
     return true;
 }
@@ -231,7 +243,7 @@ __device__ __forceinline__ void kv8_note(const Kv8Args &p, const long long *tile
     x.inside = any && !u.begins;
     if (x.inside) {
         const int kt = u.sq.ktiles;
-        const int unit = u.head * u.sq.qtiles + u.qv0 / p.q_tile;
+        const int unit = u.head * u.sq.qtiles + (u.qv0 >> p.q_log2);
         x.t0 = tiles[u.s] + static_cast<long long>(unit) * kt;
         x.t1 = x.t0 + kt;
         x.first = u.sq.first;
@@ -314,7 +326,7 @@ __device__ __forceinline__ int fit_f16(float amax) { return max(exponent_of(amax
 // k_kv8_rows: 16 query vectors per unit (all heads of a KV head's group for
 // one row, or some rows).  Bound by the cache's bytes: every byte is read
 // once and meets 16 query vectors (64 sequences of up to 8192 tokens, 8 KV
-// heads: 548 MB in 97 us).  The warps of a CTA take the unit's tiles
+// heads: 548 MB in 94 us).  The warps of a CTA take the unit's tiles
 // (one page each) in turn, each with its own running softmax and its own ring
 // of page blocks in shared memory, so no barrier is met inside a unit; they
 // are joined through shared memory at the unit's end.  A block of K or V of
@@ -383,8 +395,9 @@ __device__ __forceinline__ uint32_t scaled_f16(uint32_t w, float f) { return pac
 // Online softmax of one piece: scores sc (columns: this lane's keys, `live`
 // of them) to the fp16 weights w16, with r, d, the sum l and O's factor.
 // reach: of O, for rows g and g + 8 (in shared memory: it is seldom asked for).
+// both: rows 8 .. 15 hold query vectors; else their weights are 0.
 template <int NJ, int NI>
-__device__ __forceinline__ void rows_softmax(float (&sc)[NJ][4], int live, float kf, const float (&qf)[2], int vx, float (&r)[2], float (&d)[2],
+__device__ __forceinline__ void rows_softmax(float (&sc)[NJ][4], bool both, int live, float kf, const float (&qf)[2], int vx, float (&r)[2], float (&d)[2],
                                              float (&l)[2], float *reach, float (&o)[NI][4], uint32_t (&w16)[NJ][2]) {
     if (live < 2 * NJ) {
 #pragma unroll
@@ -393,26 +406,37 @@ __device__ __forceinline__ void rows_softmax(float (&sc)[NJ][4], int live, float
             for (int e = 0; e < 4; ++e)
                 if (2 * j + (e & 1) >= live) sc[j][e] = -INFINITY;   // factors are positive
     }
+    // rows g (elements 0, 1 of a product) and g + 8 (2, 3)
+    float f[2] = {1.f, 1.f}, nr[2] = {r[0], r[1]}, nd[2] = {d[0], d[1]};
+    const float v = static_cast<float>(vx);
+    bool change = false;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {   // rows g (elements 0, 1 of a product) and g + 8 (2, 3)
-        const float f = factor(kf, qf[h]);
+    for (int h = 0; h < 2; ++h) {
+        if (h && !both) continue;
+        f[h] = factor(kf, qf[h]);
         float mx = -INFINITY;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) mx = fmaxf(mx, fmaxf(sc[j][2 * h], sc[j][2 * h + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float z = mx * f, v = static_cast<float>(vx);
+        const float z = mx * f[h];
         const bool grow = r[h] == -INFINITY ? z > -INFINITY : z - r[h] > kLazy;
         const bool shift = z > -INFINITY && (v - d[h] > kUnitHigh || v - d[h] < kUnitLow);
-        if (__any_sync(0xffffffffu, grow || shift)) {
-            const float nr = grow ? ceilf(z) : r[h], far = fmaxf(reach[8 * h], d[h] + kReach) - (grow ? nr - r[h] : 0.f);
-            const float nd = shift ? fmaxf(v - kUnit, far - kSpan) : d[h];
-            const float fl = grow ? ex2(r[h] - nr) : 1.f, fo = fl * ex2(d[h] - nd);
+        if (grow) nr[h] = ceilf(z);
+        if (shift) nd[h] = fmaxf(v - kUnit, fmaxf(reach[8 * h], d[h] + kReach) - (grow ? nr[h] - r[h] : 0.f) - kSpan);
+        change |= grow || shift;
+    }
+    if (__any_sync(0xffffffffu, change)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const bool grow = nr[h] != r[h];
+            const float far = fmaxf(reach[8 * h], d[h] + kReach) - (grow ? nr[h] - r[h] : 0.f);
+            const float fl = grow ? ex2(r[h] - nr[h]) : 1.f, fo = fl * ex2(d[h] - nd[h]);
             __syncwarp();
             reach[8 * h] = far;   // the quad's lanes write the same
             __syncwarp();
-            r[h] = nr;
-            d[h] = nd;
+            r[h] = nr[h];
+            d[h] = nd[h];
             l[h] *= fl;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
@@ -420,11 +444,19 @@ __device__ __forceinline__ void rows_softmax(float (&sc)[NJ][4], int live, float
                 o[i][2 * h + 1] *= fo;
             }
         }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (h && !both) {
+#pragma unroll
+            for (int j = 0; j < NJ; ++j) w16[j][h] = 0u;
+            continue;
+        }
         const float u = v - d[h], off = u - (r[h] == -INFINITY ? 0.f : r[h]);
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            const float a = ex2(fmaf(sc[j][2 * h], f, off)), b = ex2(fmaf(sc[j][2 * h + 1], f, off));
+            const float a = ex2(fmaf(sc[j][2 * h], f[h], off)), b = ex2(fmaf(sc[j][2 * h + 1], f[h], off));
             s0 += a;
             s1 += b;
             w16[j][h] = pack_f16(a, b);
@@ -475,7 +507,35 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
         const Kv8Seq sq = u.sq;
         // This warp's tiles: pages page0 + NW i, i = 0 .. nc - 1.
         const int page0 = u.k0 + warp, s = u.s, head = u.head;
+        // The first of its new rows.  Warp 0 has no fewer tiles than another; a window's rows begin with the last warp.
+        const int new0 = WIN ? NW - 1 - warp : warp;
         const int nc = ok && page0 < u.k1 ? (u.k1 - page0 + NW - 1) / NW : 0;
+        // q first, and the new row that this warp begins with: behind the copies of
+        // a full GPU they wait their turn (64 sequences of 1090 tokens, 8 KV heads:
+        // 7000 cycles for q alone).
+        constexpr int NP = HD / 64;   // 16-byte pieces of a thread's HD / 8 dims
+        uint4 q_raw[NP];
+        if (tid < 8 * kRowsQ) {
+            const int part = tid & 7, qv = u.qv0 + (tid >> 3);
+            const bool in = qv - u.qv0 < u.nqv;
+            const int row = in ? qv / p.gq : 0;
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.q) + (sq.first + row) * p.a.q_stride +
+                                                               (head * p.gq + (in ? qv - row * p.gq : 0)) * HD + part * (HD / 8));
+#pragma unroll
+            for (int i = 0; i < NP; ++i) q_raw[i] = in ? src[i] : make_uint4(0, 0, 0, 0);
+        }
+        uint4 kw[HD / 32];
+        uint32_t vw[NI];
+        auto load_new = [&](int j) {
+            const uint4 *kj = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.k) + (sq.first + j) * p.a.k_stride + head * HD + t * (HD / 4));
+            const uint32_t *vj = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + j) * p.a.v_stride + head * HD) + t;
+#pragma unroll
+            for (int i = 0; i < HD / 32; ++i) kw[i] = kj[i];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) vw[i] = vj[4 * i];
+        };
+        const int n_new = u.begins && p.a.k ? sq.rows : 0;
+        if (new0 < n_new) load_new(new0);
         // Block 2 i is K of tile i, block 2 i + 1 its V.  Page numbers and
         // scales are looked up 32 tiles at a time, lane i for tile 32 n + i
         // (last_*: the 32 tiles before, some of which may still be read).
@@ -513,21 +573,15 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
 
         // q as fp16, each vector scaled by a power of two to fit: 8 threads a row.
         if (tid < 8 * kRowsQ) {
-            constexpr int NP = HD / 64;   // 16-byte pieces of a thread's HD / 8 dims
-            const int r = tid >> 3, part = tid & 7, qv = u.qv0 + r;
-            const bool in = r < u.nqv;
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.q) + (sq.first + (in ? qv / p.gq : 0)) * p.a.q_stride +
-                                                               (head * p.gq + (in ? qv % p.gq : 0)) * HD + part * (HD / 8));
-            uint4 w[NP];
+            uint4 (&w)[NP] = q_raw;
             uint32_t top = 0;
-#pragma unroll
-            for (int i = 0; i < NP; ++i) w[i] = in ? src[i] : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int i = 0; i < NP; ++i) top = most2(most2(most2(most2(top, w[i].x), w[i].y), w[i].z), w[i].w);
 #pragma unroll
             for (int k = 1; k < 8; k <<= 1) top = most2(top, __shfl_xor_sync(0xffffffffu, top, k));
             const int qx = fit_pair(top);
             const float f = power_of(-qx);
+            const int r = tid >> 3, part = tid & 7;
             uint4 *dst = reinterpret_cast<uint4 *>(smem + Lay::q_off + r * Lay::q_row + (part >> 1) * Lay::q_piece + (part & 1) * (HD / 4));
 #pragma unroll
             for (int i = 0; i < NP; ++i) dst[i] = make_uint4(scaled_f16(w[i].x, f), scaled_f16(w[i].y, f), scaled_f16(w[i].z, f), scaled_f16(w[i].w, f));
@@ -547,24 +601,23 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
         if constexpr (WIN) {
 #pragma unroll 1
             for (int h = 0; h < 2; ++h)
-                from[h] = sq.len + kv8_seen(p, sq.first, sq.rows, min(u.qv0 + g + 8 * h, u.qv0 + u.nqv - 1) / p.gq) - p.window;
+            {
+                const int row = min(u.qv0 + g + 8 * h, u.qv0 + u.nqv - 1) / p.gq;
+                from[h] = sq.len + (p.a.vis ? kv8_seen(p, sq.first, sq.rows, row) : p.a.k ? row + 1 : 0) - p.window;
+            }
         }
 
         // ---- new rows, in the piece that begins the unit: one key at a time
-        if (u.begins && p.a.k) {
+        if (n_new > 0) {
             const int r0 = g < u.nqv ? (u.qv0 + g) / p.gq : -1, r1 = g + 8 < u.nqv ? (u.qv0 + g + 8) / p.gq : -1;
 #pragma unroll 1
-            for (int j = warp; j < sq.rows; j += NW) {
-                const uint4 *kj = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.k) + (sq.first + j) * p.a.k_stride + head * HD + t * (HD / 4));
-                const uint32_t *vj = reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + j) * p.a.v_stride + head * HD) + t;
-                uint4 kw[HD / 32];
-                uint32_t vw[NI];
-#pragma unroll
-                for (int i = 0; i < HD / 32; ++i) kw[i] = kj[i];
-#pragma unroll
-                for (int i = 0; i < NI; ++i) vw[i] = vj[4 * i];
+            for (int j = new0; j < n_new; j += NW) {
                 bool see[2];
-                if constexpr (WIN) {
+                if (WIN && !p.a.vis) {
+                    const int w0 = p.sinks - sq.len, w1 = p.window;
+                    see[0] = j <= r0 && (j < w0 || j > r0 - w1);
+                    see[1] = j <= r1 && (j < w0 || j > r1 - w1);
+                } else if constexpr (WIN) {
                     see[0] = r0 >= 0 && (kv8_window_new(p, sq.first, sq.rows, sq.len, r0, j & ~31) >> (j & 31) & 1u);
                     see[1] = r1 >= 0 && (kv8_window_new(p, sq.first, sq.rows, sq.len, r1, j & ~31) >> (j & 31) & 1u);
                 } else if (p.a.vis) {
@@ -618,6 +671,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
                         o[i][2 * h + 1] = fmaf(w[h], see[h] ? hi : 0.f, o[i][2 * h + 1] * alpha[h]);
                     }
                 }
+                if (j + NW < n_new) load_new(j + NW);
             }
             // Every lane of a quad has added the key: l is summed over the quad below.
             if (t != 0) l[0] = l[1] = 0.f;
@@ -690,7 +744,7 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
                     }
                 }
                 uint32_t w16[NJ][2];
-                rows_softmax<NJ, NI>(sc, live, kf, qf, vx, r, d, l, reach, o, w16);
+                rows_softmax<NJ, NI>(sc, u.nqv > 8, live, kf, qf, vx, r, d, l, reach, o, w16);
                 if (piece == 0) {   // V is the block behind K
                     const int vs = PAGE / KT == 1 ? out_slot : out_slot + 1 == NS ? 0 : out_slot + 1;
                     const uint32_t ph = PAGE / KT == 1 || out_slot + 1 < NS ? out_phase : out_phase ^ 1;
@@ -796,14 +850,14 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
         for (int i = tid; i < u.nqv * (HD / 4); i += 32 * NW) {
             const int r = i / (HD / 4), d = 4 * (i % (HD / 4));
             float R = -INFINITY, D = -INFINITY, L = 0.f;
-#pragma unroll 1
+#pragma unroll
             for (int w = 0; w < NW; ++w) {
                 const float4 x = sh_ml[w * kRowsQ + r];
                 R = fmaxf(R, x.x);
                 D = fmaxf(D, x.y);
             }
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
+#pragma unroll
             for (int w = 0; w < NW; ++w) {
                 const float4 ml = sh_ml[w * kRowsQ + r];
                 if (ml.z == 0.f) continue;   // saw no key
@@ -2201,7 +2255,10 @@ static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     using Lay = Rows<HD, PAGE>;
     static_assert(Lay::per_sm <= kRowsPerSm, "workspace");
     p.q_tile = kRowsQ;
+    p.q_log2 = 4;
     p.k_tile = PAGE;
+    p.k_log2 = p.page_log2;
+    static_assert(kRowsQ == 1 << 4, "shift");
     p.n_tile = 0;
     p.unit_cost = kRowsUnitCost;
     p.snap = p.unit_cost - 1;
@@ -2235,6 +2292,8 @@ static cudaError_t tiles_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     using Lay = Tiles<HD>;
     p.q_tile = kTileQ;
     p.k_tile = p.n_tile = kTileK;
+    p.q_log2 = p.k_log2 = 7;
+    static_assert(kTileQ == 1 << 7 && kTileK == 1 << 7, "shift");
     p.snap = 0;   // finding the unit costs more than an empty piece (121 rows over 2k tokens, 32 heads: 34.4 us against 33.1)
     // Whole against split: 121 rows of 32 heads, 6 tiles 24.2 us against 25.4, 9
     // tiles 29.9 against 25.4; four such sequences, which fill the SMs whole, 12
