@@ -17,7 +17,8 @@
 // operand (8 vectors).  A product is a sum over k, so any order of k will do as
 // long as both have the same one: lane (g, t) reads a quarter of a group of
 // outputs g and g + 8, GROUP / 8 consecutive bytes each, straight into registers,
-// some groups ahead, and the same places of vector g.
+// some groups ahead (groups of 32: through a ring in shared memory), and the same
+// places of vector g.
 //
 // A block's warps share 16 * MT * wm outputs and 8 / wm parts of k, the blocks of
 // a cluster share k further; the parts are added in a fixed order, through
@@ -37,10 +38,18 @@
 namespace la {
 
 constexpr int kW4Warps = 8, kW4Rows = 16;
-constexpr int kW4Block = 4;          // groups whose scales a quad's lanes load together
-constexpr int kW4Smem = 100 * 1024;  // most of a block, for its own operands
+constexpr int kW4Block = 4;          // groups whose scales a quad's lanes load together: a pass of the loop
+constexpr int kW4Smem = 100 * 1024;  // most of a block
 // Blocks of k_gemv_w4 on an SM
 constexpr int w4_per_sm(int group, int mt) { return mt == 1 && group < 128 ? 3 : 2; }
+// Groups of 32: a lane's part of a group is 4 bytes, and loads of 4 bytes of 8
+// outputs each cost the memory system four times what 16 bytes do.  So the bytes
+// come 16 at a time into a ring of passes for each warp, and the words from there:
+// 16 rows of 64 bytes, 80 apart, so that a warp reads 32 different banks
+// (8192 x 28672: 54.2 us with loads of 4 bytes, 43.5 so; four or five stages leave
+// room for fewer blocks and take longer at smaller sizes; groups of 64 gain nothing).
+constexpr int kW4RingRow = 80, kW4Stages = 3;
+constexpr int w4_ring(int group) { return group == 32 ? kW4Warps * kW4Stages * 16 * kW4RingRow : 0; }
 
 struct W4Args {
     const __nv_bfloat16 *x;
@@ -52,8 +61,9 @@ struct W4Args {
     int rows, out, groups;
     int wm;          // warps along the outputs
     int blocks;      // of a cluster, along k
-    int part_log2;   // parts of k, over all blocks of a cluster
+    int parts;       // of k, over all blocks of a cluster
     int longest;     // groups of the longest part
+    int ring;        // the ring's place in shared memory
 };
 
 __device__ __forceinline__ float w4_power(int e) { return __uint_as_float(static_cast<unsigned>(e + 127) << 23); }   // -126 .. 127
@@ -112,15 +122,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const float (&c)[4], uint
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
-// N words that are read once.
+// Words that are read once.
 template <int N>
 __device__ __forceinline__ void w4_load(const uint8_t *p, uint32_t (&w)[N]) {
     if constexpr (N == 4)
         asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
-    else if constexpr (N == 2)
-        asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
     else
-        asm volatile("ld.global.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));   // half of a 32-byte sector: the next group is the other
+        asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
 }
 
 // MT tiles of 16 outputs for a warp, up to 8 vectors.
@@ -137,7 +145,8 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
     const int wm = warp % p.wm, wk = warp / p.wm, parts = kW4Warps / p.wm;
     const int outs = 16 * MT * p.wm, o0 = static_cast<int>(blockIdx.x) / C * outs;
     const int rows = p.rows;
-    const int j0 = p.groups * (rank * parts + wk) >> p.part_log2, j1 = p.groups * (rank * parts + wk + 1) >> p.part_log2;
+    const int j0 = static_cast<int>(static_cast<unsigned>(p.groups * (rank * parts + wk)) / static_cast<unsigned>(p.parts)),
+              j1 = static_cast<int>(static_cast<unsigned>(p.groups * (rank * parts + wk + 1)) / static_cast<unsigned>(p.parts));
     pdl_trigger();
     pdl_wait();
 
@@ -148,18 +157,37 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const long long o = min(o0 + 16 * (MT * wm + m) + g + 8 * h, p.out - 1);   // past the last: not written
-            w[m][h] = p.w + (o * p.groups + j0) * (GROUP / 2) + t * (GROUP / 8);
+            w[m][h] = p.w + (o * p.groups + j0) * (GROUP / 2) + (GROUP == 32 ? 0 : t * (GROUP / 8));
             fs[m][h] = p.s + o * p.groups + j0 + t;
         }
-    uint32_t a[AHEAD][MT][2][NW];
+    constexpr bool RING = GROUP == 32;
+    constexpr int ROW = kW4RingRow, STAGES = kW4Stages, RUN = kW4Block * GROUP / 2;   // bytes of an output's pass
+    static_assert(!RING || MT == 1, "the ring's rows");
+    uint32_t a[RING ? 1 : AHEAD][MT][2][NW];
     int left = j1 - j0;        // groups from w on
-    auto load = [&](int u, int slot) {   // group u of the block at w
+    auto load = [&](int u, int slot) {   // group u of the pass at w
         if (u < left) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) w4_load<NW>(w[m][h] + u * (GROUP / 2), a[slot][m][h]);
+                for (int h = 0; h < 2; ++h) w4_load(w[m][h] + u * (GROUP / 2), a[slot][m][h]);
         }
+    };
+    const uint32_t ring = smem_u32(w4_smem) + p.ring + warp * STAGES * 16 * ROW + g * ROW;
+    const int run_bytes = (j1 - j0) * (GROUP / 2);
+    int to_load = 16 * t, load_slot = 0;   // byte of an output's run, slot of the next pass to load
+    auto load_pass = [&]() {
+        if constexpr (RING) {
+            static_assert(RUN == 64, "16 bytes for each lane of a quad");
+            if (to_load < run_bytes) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + load_slot * (16 * ROW) + h * (8 * ROW) + 16 * t), "l"(w[0][h] + to_load) : "memory");
+            }
+            to_load += RUN;
+            load_slot = load_slot + 1 == STAGES ? 0 : load_slot + 1;
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
     __nv_bfloat16 fn[MT][2];   // lane t: the scale of group t of the next block
     auto load_scales = [&]() {
@@ -169,8 +197,13 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
             for (int h = 0; h < 2; ++h)
                 if (t < left) fn[m][h] = *fs[m][h];
     };
+    if constexpr (RING) {
+#pragma unroll 1
+        for (int i = 0; i < STAGES - 1; ++i) load_pass();
+    } else {
 #pragma unroll
-    for (int u = 0; u < AHEAD; ++u) load(u, u);
+        for (int u = 0; u < AHEAD; ++u) load(u, u);
+    }
     load_scales();
 
     // This part's warps turn its vectors, 32 words at a time
@@ -210,6 +243,7 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
     for (int n = 0; n < NT; ++n) at[n] = min(8 * n + g, rows - 1) * 4;   // past the last vector: it again
     float acc[MT][NT][4] = {};
     const int n_groups = j1 - j0;
+    int slot = 0;
 #pragma unroll 1
     for (int j = 0; j < n_groups; j += kW4Block) {
         float f[MT][2];
@@ -224,11 +258,22 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
         left -= kW4Block;
         load_scales();
         left = now;
+        const uint32_t from = ring + slot * (16 * ROW) + t * (GROUP / 8);
+        if constexpr (RING) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+            __syncwarp();   // the pass is there, and all lanes are through with the one before
+            load_pass();
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
+        }
 #pragma unroll
         for (int u = 0; u < kW4Block; ++u) {
             if (u >= now) break;
             float d[MT][NT][4];
             float4 xf[NT];
+            if constexpr (RING) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a[0][0][h][0]) : "r"(from + h * (8 * ROW) + u * (GROUP / 2)) : "memory");
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) xf[n] = bf[u * 8 + 4 * n];
 #pragma unroll
@@ -238,7 +283,7 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
                 for (int n = 0; n < NT; ++n) v[n] = bx[(u * NW + i) * rows * 4 + at[n]];
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                    const uint32_t x = a[u % AHEAD][m][0][i], y = a[u % AHEAD][m][1][i], x8 = x >> 8, y8 = y >> 8;
+                    const uint32_t x = a[RING ? 0 : u % AHEAD][m][0][i], y = a[RING ? 0 : u % AHEAD][m][1][i], x8 = x >> 8, y8 = y >> 8;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         if (i == 0)
@@ -249,7 +294,7 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
                     }
                 }
             }
-            load(u + AHEAD, u % AHEAD);
+            if constexpr (!RING) load(u + AHEAD, u % AHEAD);
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 const float fa = __shfl_sync(0xffffffffu, f[m][0], u, 4), fb = __shfl_sync(0xffffffffu, f[m][1], u, 4);
@@ -265,10 +310,12 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
         left -= kW4Block;
         bx += kW4Block * NW * rows * 4;
         bf += kW4Block * 8;
+        if constexpr (!RING) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) w[m][h] += kW4Block * (GROUP / 2);
+                for (int h = 0; h < 2; ++h) w[m][h] += kW4Block * (GROUP / 2);
+        }
     }
     // The parts of k of this block, then those of the cluster's blocks
     __syncthreads();
@@ -649,9 +696,14 @@ W4Plan w4_plan(int rows, int out, int k, int group, int nsm) {
     W4Plan best{};
     const int groups = k / group, chunks = (k + 127) / 128, tiles = (out + 127) / 128, many = (rows + kW4Rows - 1) / kW4Rows;
     // k_gemv_w4: the split of outputs and k that fills most of the SMs in one round
-    // (11008 x 4096: 172 blocks 9.2 us, 344 12.1 us), with the most outputs for a
-    // block where two do alike (each block turns its vectors); with fewer than 128 only where k
-    // is in as many parts as there may be and SMs are idle.
+    // (11008 x 4096: 172 blocks 9.2 us, 258 in clusters of 6 8.9 us, 301 in clusters of 7, which
+    // take two rounds, 13.7 us), with the most outputs for a block where two do nearly
+    // alike (each block turns its vectors; 1 vector, groups of 64: 258 blocks of 256 outputs
+    // 10.5 us, 430 of 128 12.2 us); with fewer than 128 only where k is in as many parts
+    // as there may be and SMs are idle.
+    // Clusters of n blocks leave SMs over where an SM's neighbours do not make a whole
+    // one: the blocks that the occupancy query allows at a time, of those of single ones, at least.
+    static constexpr double kClusterRoom[8] = {1., 1., .95, .96, .95, .9, .87, .89};
     double most = 0.;
     bool idle = true;
     if (rows <= kFewVectors) {
@@ -660,13 +712,14 @@ W4Plan w4_plan(int rows, int out, int k, int group, int nsm) {
         } forms[] = {{2, 8}, {1, 8}, {1, 4}, {1, 2}, {1, 1}};
         for (const auto &f : forms) {
             if (f.wm < kW4Warps && !idle) break;
+            if (f.mt == 2 && group == 32) continue;   // its ring has the rows of one tile
             const int outs = 16 * f.mt * f.wm, count = (out + outs - 1) / outs, parts = kW4Warps / f.wm, slots = w4_per_sm(group, f.mt) * nsm;
             int blocks = 1;
-            while (blocks < 8 && static_cast<int64_t>(count) * blocks * 2 <= slots && blocks * 2 * parts <= groups) blocks *= 2;
+            while (blocks < 8 && static_cast<int64_t>(count) * (blocks + 1) <= static_cast<int64_t>(slots * kClusterRoom[blocks]) && (blocks + 1) * parts <= groups) ++blocks;
             const int64_t smem = static_cast<int64_t>(parts) * ((groups + blocks * parts - 1) / (blocks * parts)) * (group * rows * 2 + 128);
             const int64_t rounds = (static_cast<int64_t>(count) * blocks + slots - 1) / slots;
             const double fill = static_cast<double>(count) * blocks / (static_cast<double>(rounds) * slots);
-            if (smem > kW4Smem || parts > groups || fill <= most * 1.05) continue;
+            if (smem + w4_ring(group) > kW4Smem || parts > groups || fill <= most * 1.12) continue;
             idle = static_cast<int64_t>(count) * blocks * 2 <= slots;
             most = fill;
             best.mt = f.mt, best.wm = f.wm, best.blocks = blocks;
@@ -699,14 +752,17 @@ cudaError_t w4_few_launch(W4Args p, const W4Plan &plan, cudaStream_t s) {
     p.blocks = plan.blocks;
     const int parts = kW4Warps / p.wm, outs = 16 * MT * p.wm;
     p.longest = (p.groups + p.blocks * parts - 1) / (p.blocks * parts);
-    for (p.part_log2 = 0; 1 << p.part_log2 < p.blocks * parts;) ++p.part_log2;
-    const int smem = std::max(parts * p.longest * (GROUP * p.rows * 2 + 128), kW4Warps * MT * 8 * 20 * 4);
+    p.parts = p.blocks * parts;
+    p.ring = std::max(parts * p.longest * (GROUP * p.rows * 2 + 128), kW4Warps * MT * 8 * 20 * 4);
+    const int smem = p.ring + w4_ring(GROUP);
     return w4_clusters(k_gemv_w4<GROUP, MT>, dim3((p.out + outs - 1) / outs * p.blocks), 32 * kW4Warps, smem, p.blocks, s, p);
 }
 template <int GROUP>
 cudaError_t w4_launch(const W4Args &p, const W4Plan &plan, const CUtensorMap &map, cudaStream_t s) {
     if (plan.large) return p.rows > 8 ? w4_tiles_launch<GROUP, 2>(p, plan, map, s) : w4_tiles_launch<GROUP, 1>(p, plan, map, s);
-    return plan.mt == 2 ? w4_few_launch<GROUP, 2>(p, plan, s) : w4_few_launch<GROUP, 1>(p, plan, s);
+    if constexpr (GROUP != 32)
+        if (plan.mt == 2) return w4_few_launch<GROUP, 2>(p, plan, s);
+    return w4_few_launch<GROUP, 1>(p, plan, s);
 }
 
 int w4_sizes(int32_t rows, int32_t out, int32_t k, int32_t group) {
