@@ -153,3 +153,12 @@ def test_calls_at_once(lib):
             n = 16 if i % 2 else 5
             close(got, y[:n], tol[:n])
     lib.la_gemm_status()
+
+
+@pytest.mark.parametrize("rows,out,k,group", [
+    (1, 11008, 1024, 128), (2, 13800, 768, 128), (1, 24300, 384, 128), (1, 11008, 1056, 32), (3, 5000, 4128, 32), (4, 7100, 2240, 64),
+    (6, 1900, 3200, 128), (1, 2000, 8736, 32), (2, 100, 11232, 32)])
+def test_products_shared_unevenly(lib, rows, out, k, group):
+    """Numbers of outputs for which 3, 5, 6 or 8 blocks share k, whose groups do not divide evenly."""
+    x, w, s, y, tol = case(rows, out, k, group, seed=rows + out)
+    close(lib.W4Matrix(w, s).matvec(x), y, tol)
