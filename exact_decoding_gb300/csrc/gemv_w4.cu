@@ -3,14 +3,15 @@
 //
 // Bound by the matrix's bytes: every byte is read once and meets up to 16
 // vectors.  What the bytes cost are the instructions that unpack them, so there
-// are few: a nibble at the low end of 16 bits is the fp16 number q 2^-24 (a
-// subnormal one, which the tensor cores take as it is), one above it 16 q 2^-24.
-// A 32-bit word, 8 weights, is one shift and four masks: nibbles i and i + 4 of it
-// are a pair.  The vectors come as fp16 to match, in the same order of k, 16 times
-// smaller at the odd nibbles, each group of a vector times a power of two that
-// brings its largest value to 2^14 .. 2^15: 11 bits hold bf16's 8, and what is
-// too small for them is below 2^-35 of the largest.  The -8 is -8 times the sum of
-// the group's x, with which the products' sum begins.  A group's sum is multiplied
+// are few: a 32-bit word, 8 weights, is one shift and four times a mask with the
+// bits of fp16's 1024 put in, so that nibbles i and i + 4 are a pair 1024 + q, or
+// 1024 + 16 q where the nibble lies higher; one packed operation each makes it
+// q - 8, exactly.  (Without that one, with q as a subnormal number and -8 times the
+// sum of x added, products took 0.4 us less in 25 but were off by 3.6e-6 of the result's
+// 2-norm, as the tensor cores add with few bits below their largest term; so by
+// 9e-8.)  The vectors come as fp16, each group of a vector times
+// a power of two that brings its largest value to 2^14 .. 2^15: 11 bits hold bf16's 8, and what is
+// too small for them is below 2^-39 of the largest.  A group's sum is multiplied
 // by the vector's power and by its scale once, in fp32.
 //
 // The weights are the A operand of mma.m16n8k16 (16 outputs), the vectors its B
@@ -46,7 +47,7 @@ constexpr int w4_per_sm(int group, int mt) { return mt == 1 && group < 128 ? 3 :
 // outputs each cost the memory system four times what 16 bytes do.  So the bytes
 // come 16 at a time into a ring of passes for each warp, and the words from there:
 // 16 rows of 64 bytes, 80 apart, so that a warp reads 32 different banks
-// (8192 x 28672: 54.2 us with loads of 4 bytes, 43.5 so; four or five stages leave
+// (8192 x 28672: 54.2 us with loads of 4 bytes, 42.3 so; four or five stages leave
 // room for fewer blocks and take longer at smaller sizes; groups of 64 gain nothing).
 constexpr int kW4RingRow = 80, kW4Stages = 3;
 constexpr int w4_ring(int group) { return group == 32 ? kW4Warps * kW4Stages * 16 * kW4RingRow : 0; }
@@ -73,11 +74,10 @@ __device__ __forceinline__ uint32_t w4_most(uint32_t a, uint32_t b) {   // large
     return r;
 }
 // Eight consecutive values of a vector (bf16) as an operand: fp16 pairs (0, 4),
-// (1, 5), (2, 6), (3, 7), the odd ones times 1 / 16.  LANES lanes have a group
-// together; all lanes of the warp call it.  sum: of the group's values, at its power of two;
-// returns that power's exponent.
+// (1, 5), (2, 6), (3, 7).  LANES lanes have a group together; all lanes of the
+// warp call it.  Returns the exponent of the group's power of two.
 template <int LANES>
-__device__ __forceinline__ int w4_operand(const uint4 &x, uint4 &y, float &sum) {
+__device__ __forceinline__ int w4_operand(const uint4 &x, uint4 &y) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     constexpr uint32_t kAbs = 0x7fff7fffu;
     uint32_t top = w4_most(w4_most(w[0] & kAbs, w[1] & kAbs), w4_most(w[2] & kAbs, w[3] & kAbs));
@@ -96,25 +96,30 @@ __device__ __forceinline__ int w4_operand(const uint4 &x, uint4 &y, float &sum) 
         v[2 * i] = __uint_as_float(w[i] << 16);
         v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
-    sum = ((v[0] + v[4]) + (v[1] + v[5])) + ((v[2] + v[6]) + (v[3] + v[7]));
 #pragma unroll
-    for (int o = 1; o < LANES; o <<= 1) {
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
+    for (int o = 1; o < LANES; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const int e = min(14 + 127 - static_cast<int>(top >> 7), 126);   // the largest value, times 2^e, is in 2^14 .. 2^15
-    const float f = w4_power(e), f16 = w4_power(e - 4);
+    const float f = w4_power(e);
     uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(v[i] * (i & 1 ? f16 : f), v[i + 4] * (i & 1 ? f16 : f));
+        const __half2 h = __floats2half2_rn(v[i] * f, v[i + 4] * f);
         r[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
     y = make_uint4(r[0], r[1], r[2], r[3]);
-    sum *= f;
     return e;
 }
-
+// The weights of a word as pairs of fp16: nibbles i and i + 4, less 8.
+__device__ __forceinline__ uint32_t w4_low(uint32_t x) {   // i = 0, or 2 of a word shifted by 8
+    uint32_t r;
+    asm("{\n\t.reg .b32 a;\n\tlop3.b32 a, %1, 0x000f000f, 0x64006400, 0xea;\n\tadd.rn.f16x2 %0, a, %2;\n\t}" : "=r"(r) : "r"(x), "r"(0xe408e408u));   // - 1032
+    return r;
+}
+__device__ __forceinline__ uint32_t w4_high(uint32_t x) {   // i = 1, or 3
+    uint32_t r;
+    asm("{\n\t.reg .b32 a;\n\tlop3.b32 a, %1, 0x00f000f0, 0x64006400, 0xea;\n\tfma.rn.f16x2 %0, a, %2, %3;\n\t}" : "=r"(r) : "r"(x), "r"(0x2c002c00u), "r"(0xd480d480u));   // / 16, - 72
+    return r;
+}
 
 // D (16 x 8, fp32) = A (16 x 16, fp16) * B (16 x 8, fp16) + C.
 __device__ __forceinline__ void mma_f16(float (&d)[4], const float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -122,6 +127,23 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const float (&c)[4], uint
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t w4_two(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t w4_mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t w4_fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // Words that are read once.
 template <int N>
 __device__ __forceinline__ void w4_load(const uint8_t *p, uint32_t (&w)[N]) {
@@ -189,13 +211,18 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    __nv_bfloat16 fn[MT][2];   // lane t: the scale of group t of the next block
+    // Lane t: the scales of groups t, t + 4, ... of the next NF passes, on their way while 512 k or more are multiplied
+    // (groups of 32, 8192 x 28672: 53.8 us with NF = 1)
+    constexpr int NF = GROUP == 32 ? 4 : 1;
+    __nv_bfloat16 fn[MT][2][NF];
     auto load_scales = [&]() {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (t < left) fn[m][h] = *fs[m][h];
+#pragma unroll
+                for (int q = 0; q < NF; ++q)
+                    if (t + kW4Block * q < left) fn[m][h][q] = fs[m][h][kW4Block * q];
     };
     if constexpr (RING) {
 #pragma unroll 1
@@ -208,7 +235,7 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
 
     // This part's warps turn its vectors, 32 words at a time
     uint4 *to = reinterpret_cast<uint4 *>(w4_smem) + wk * p.longest * NW * rows * 4;
-    float2 *tf = reinterpret_cast<float2 *>(w4_smem + parts * p.longest * GROUP * rows * 2) + wk * p.longest * 16;
+    float *tf = reinterpret_cast<float *>(w4_smem + parts * p.longest * GROUP * rows * 2) + wk * p.longest * 8;
     const int per = (j1 - j0) * LANES;   // words of a vector
     for (int n = 0; n < rows; ++n) {
         const __nv_bfloat16 *xs = p.x + n * p.x_stride + static_cast<long long>(j0) * GROUP;
@@ -226,95 +253,99 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
                 const int i = i0 + b * 32 * p.wm + lane;
                 if (i - lane >= per) break;
                 uint4 y;
-                float sum;
-                const int e = w4_operand<LANES>(x[b], y, sum), j = i / LANES, li = i % LANES;
+                const int e = w4_operand<LANES>(x[b], y), j = i / LANES, li = i % LANES;
                 if (i < per) {
                     to[((j * NW + li % NW) * rows + n) * 4 + li / NW] = y;
-                    if (li == 0) tf[j * 16 + n] = make_float2(sum * -4.76837158203125e-7f, w4_power(-e));   // -8 * 2^-24
+                    if (li == 0) tf[j * 8 + n] = w4_power(-e);
                 }
             }
         }
     }
     __syncthreads();
     const uint4 *bx = to + t;
-    const float4 *bf = reinterpret_cast<const float4 *>(tf) + t;
+    const float2 *bf = reinterpret_cast<const float2 *>(tf) + t;
     int at[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) at[n] = min(8 * n + g, rows - 1) * 4;   // past the last vector: it again
-    float acc[MT][NT][4] = {};
+    uint64_t acc[MT][NT][2] = {};   // pairs of sums
     const int n_groups = j1 - j0;
     int slot = 0;
 #pragma unroll 1
-    for (int j = 0; j < n_groups; j += kW4Block) {
-        float f[MT][2];
+    for (int j = 0; j < n_groups; j += NF * kW4Block) {
+        float f[MT][2][NF];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                f[m][h] = __bfloat162float(fn[m][h]);
-                fs[m][h] += kW4Block;
+#pragma unroll
+                for (int q = 0; q < NF; ++q) f[m][h][q] = __bfloat162float(fn[m][h][q]);
+                fs[m][h] += NF * kW4Block;
             }
-        const int now = left;
-        left -= kW4Block;
+        const int now_all = left;
+        left -= NF * kW4Block;
         load_scales();
-        left = now;
-        const uint32_t from = ring + slot * (16 * ROW) + t * (GROUP / 8);
-        if constexpr (RING) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
-            __syncwarp();   // the pass is there, and all lanes are through with the one before
-            load_pass();
-            slot = slot + 1 == STAGES ? 0 : slot + 1;
-        }
+        left = now_all;
 #pragma unroll
-        for (int u = 0; u < kW4Block; ++u) {
-            if (u >= now) break;
-            float d[MT][NT][4];
-            float4 xf[NT];
+        for (int pass = 0; pass < NF; ++pass) {
+            const int now = left;
+            if (pass && now <= 0) break;
+            const uint8_t *from = w4_smem + p.ring + (warp * STAGES + slot) * (16 * ROW) + g * ROW + t * (GROUP / 8);
             if constexpr (RING) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(a[0][0][h][0]) : "r"(from + h * (8 * ROW) + u * (GROUP / 2)) : "memory");
+                asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+                __syncwarp();   // the pass is there, and all lanes are through with the one before
+                load_pass();
+                slot = slot + 1 == STAGES ? 0 : slot + 1;
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) xf[n] = bf[u * 8 + 4 * n];
+            for (int u = 0; u < kW4Block; ++u) {
+                if (u >= now) break;
+                float d[MT][NT][4];
+                float2 xf[NT];
+                if constexpr (RING) {
 #pragma unroll
-            for (int i = 0; i < NW; ++i) {
-                uint4 v[NT];
+                    for (int h = 0; h < 2; ++h) a[0][0][h][0] = *reinterpret_cast<const uint32_t *>(from + h * (8 * ROW) + u * (GROUP / 2));
+                }
 #pragma unroll
-                for (int n = 0; n < NT; ++n) v[n] = bx[(u * NW + i) * rows * 4 + at[n]];
+                for (int n = 0; n < NT; ++n) xf[n] = bf[u * 4];
+#pragma unroll
+                for (int i = 0; i < NW; ++i) {
+                    uint4 v[NT];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) v[n] = bx[(u * NW + i) * rows * 4 + at[n]];
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        const uint32_t x = a[RING ? 0 : u % AHEAD][m][0][i], y = a[RING ? 0 : u % AHEAD][m][1][i], x8 = x >> 8, y8 = y >> 8;
+                        const uint32_t xl = w4_low(x), yl = w4_low(y), xh = w4_high(x), yh = w4_high(y), xl8 = w4_low(x8), yl8 = w4_low(y8), xh8 = w4_high(x8), yh8 = w4_high(y8);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            float (&to)[4] = d[m][n];
+                            if (i == 0) mma_f16(to, {0.f, 0.f, 0.f, 0.f}, xl, yl, xh, yh, v[n].x, v[n].y);
+                            else mma_f16(to, to, xl, yl, xh, yh, v[n].x, v[n].y);
+                            mma_f16(to, to, xl8, yl8, xh8, yh8, v[n].z, v[n].w);
+                        }
+                    }
+                }
+                if constexpr (!RING) load(u + AHEAD, u % AHEAD);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                    const uint32_t x = a[RING ? 0 : u % AHEAD][m][0][i], y = a[RING ? 0 : u % AHEAD][m][1][i], x8 = x >> 8, y8 = y >> 8;
+                    const float fa = __shfl_sync(0xffffffffu, f[m][0][pass], u, 4), fb = __shfl_sync(0xffffffffu, f[m][1][pass], u, 4);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        if (i == 0)
-                            mma_f16(d[m][n], {xf[n].x, xf[n].z, xf[n].x, xf[n].z}, x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, v[n].x, v[n].y);
-                        else
-                            mma_f16(d[m][n], d[m][n], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u, v[n].x, v[n].y);
-                        mma_f16(d[m][n], d[m][n], x8 & 0x000f000fu, y8 & 0x000f000fu, x8 & 0x00f000f0u, y8 & 0x00f000f0u, v[n].z, v[n].w);
+                        const uint64_t xf2 = w4_two(xf[n].x, xf[n].y);
+                        acc[m][n][0] = w4_fma2(w4_mul2(w4_two(d[m][n][0], d[m][n][1]), xf2), w4_two(fa, fa), acc[m][n][0]);
+                        acc[m][n][1] = w4_fma2(w4_mul2(w4_two(d[m][n][2], d[m][n][3]), xf2), w4_two(fb, fb), acc[m][n][1]);
                     }
                 }
             }
-            if constexpr (!RING) load(u + AHEAD, u % AHEAD);
+            left -= kW4Block;
+            bx += kW4Block * NW * rows * 4;
+            bf += kW4Block * 4;
+            if constexpr (!RING) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const float fa = __shfl_sync(0xffffffffu, f[m][0], u, 4), fb = __shfl_sync(0xffffffffu, f[m][1], u, 4);
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    acc[m][n][0] = fmaf(d[m][n][0] * xf[n].y, fa, acc[m][n][0]);
-                    acc[m][n][1] = fmaf(d[m][n][1] * xf[n].w, fa, acc[m][n][1]);
-                    acc[m][n][2] = fmaf(d[m][n][2] * xf[n].y, fb, acc[m][n][2]);
-                    acc[m][n][3] = fmaf(d[m][n][3] * xf[n].w, fb, acc[m][n][3]);
-                }
+                    for (int h = 0; h < 2; ++h) w[m][h] += kW4Block * (GROUP / 2);
             }
-        }
-        left -= kW4Block;
-        bx += kW4Block * NW * rows * 4;
-        bf += kW4Block * 8;
-        if constexpr (!RING) {
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) w[m][h] += kW4Block * (GROUP / 2);
         }
     }
     // The parts of k of this block, then those of the cluster's blocks
@@ -326,7 +357,10 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sh[place(warp, 16 * m + g + 8 * (e >> 1), 8 * n + 2 * t + (e & 1))] = acc[m][n][e] * 16777216.f;
+            for (int h = 0; h < 2; ++h) {
+                sh[place(warp, 16 * m + g + 8 * h, 8 * n + 2 * t)] = __uint_as_float(static_cast<uint32_t>(acc[m][n][h]));
+                sh[place(warp, 16 * m + g + 8 * h, 8 * n + 2 * t + 1)] = __uint_as_float(static_cast<uint32_t>(acc[m][n][h] >> 32));
+            }
     __syncthreads();
     constexpr int OW = 16 * MT;   // outputs of a warp
     const int items = outs * rows, log = 31 - __clz(outs);
@@ -357,10 +391,9 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
 // ------------------------------------------------------------------ many bytes
 // k_w4_operands makes the vectors' operands once, in the form that k_w4_tiles
 // wants them in shared memory: for each chunk of 128 k 16 rows of fp16 (K-major,
-// 128-byte swizzle, two blocks of 64 k) and, per group, -8 * 2^-24 times the sums
-// and the powers of the 16 vectors.
+// 128-byte swizzle, two blocks of 64 k) and, per group, the powers of the 16 vectors.
 constexpr int kChunkB = 16 * 128 * 2;             // operand
-constexpr int kChunkF = 4 * 128;                  // [group][16] sums, [group][16] powers, for up to 4 groups
+constexpr int kChunkF = 4 * 64;                   // [group][16] powers, for up to 4 groups
 constexpr int kChunk = kChunkB + kChunkF;
 
 static __device__ unsigned g_w4_err;              // a bounded wait gave up
@@ -377,18 +410,13 @@ __global__ void __launch_bounds__(128) k_w4_operands(const __grid_constant__ W4A
     const int word = blockIdx.x * 128 + threadIdx.x, chunk = word >> 4;   // 8 k each
     uint4 x = make_uint4(0, 0, 0, 0), y;
     if (r0 + n < p.rows && word * 8 < p.groups * GROUP) x = *reinterpret_cast<const uint4 *>(p.x + (r0 + n) * p.x_stride + static_cast<long long>(word) * 8);
-    float sum;
-    const int e = w4_operand<LANES>(x, y, sum);   // behind the last group: zeros, as the products want them
+    const int e = w4_operand<LANES>(x, y);   // behind the last group: zeros, as the products want them
     const int chunks = (p.groups + PER - 1) / PER;
     if (chunk >= chunks) return;
     uint8_t *to = p.made + (static_cast<long long>(blockIdx.z) * chunks + chunk) * kChunk;
     const int w = word & 15;
     *reinterpret_cast<uint4 *>(to + (w >> 3) * 2048 + n * 128 + (((w & 7) ^ (n & 7)) << 4)) = y;
-    if (w % LANES == 0) {
-        float *f = reinterpret_cast<float *>(to + kChunkB) + w / LANES * 16 + n;
-        f[0] = sum * -4.76837158203125e-7f;   // -8 * 2^-24
-        f[PER * 16] = w4_power(-e);
-    }
+    if (w % LANES == 0) reinterpret_cast<float *>(to + kChunkB)[w / LANES * 16 + n] = w4_power(-e);
 }
 
 // k_w4_tiles: 128 outputs x 16 vectors on the tcgen05 tensor cores.  Per chunk of 128 k
@@ -420,28 +448,6 @@ __device__ __forceinline__ void w4_umma(uint32_t d, uint32_t a, uint64_t b, uint
                  "r"(accumulate)
                  : "memory");
 }
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t w4_two(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t w4_add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t w4_mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t w4_fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 // NT: tiles of 8 vectors in use.
 template <int GROUP, int NT>
 __global__ void __launch_bounds__(kTileThreads, 2) k_w4_tiles(const __grid_constant__ W4Args p, const __grid_constant__ CUtensorMap map) {
@@ -568,10 +574,10 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_w4_tiles(const __grid_const
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     const uint32_t x = w[q], x8 = x >> 8;
-                    v[4 * q] = x & 0x000f000fu;
-                    v[4 * q + 1] = x & 0x00f000f0u;
-                    v[4 * q + 2] = x8 & 0x000f000fu;
-                    v[4 * q + 3] = x8 & 0x00f000f0u;
+                    v[4 * q] = w4_low(x);
+                    v[4 * q + 1] = w4_high(x);
+                    v[4 * q + 2] = w4_low(x8);
+                    v[4 * q + 3] = w4_high(x8);
                 }
                 tmem_st_32x32b_x32(a + 32 * h, v);
             }
@@ -598,10 +604,10 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_w4_tiles(const __grid_const
                 const uint64_t f2 = w4_two(fs[u], fs[u]);
 #pragma unroll
                 for (int n = 0; n < 2 * NT; ++n) {
-                    const ulonglong2 c = reinterpret_cast<const ulonglong2 *>(table + u * 64)[n], e = reinterpret_cast<const ulonglong2 *>(table + (PER + u) * 64)[n];
+                    const ulonglong2 e = reinterpret_cast<const ulonglong2 *>(table + u * 64)[n];
                     const uint64_t x = w4_two(__uint_as_float(v[4 * n]), __uint_as_float(v[4 * n + 1])), y = w4_two(__uint_as_float(v[4 * n + 2]), __uint_as_float(v[4 * n + 3]));
-                    sums[2 * n] = w4_fma2(w4_mul2(w4_add2(x, c.x), e.x), f2, sums[2 * n]);
-                    sums[2 * n + 1] = w4_fma2(w4_mul2(w4_add2(y, c.y), e.y), f2, sums[2 * n + 1]);
+                    sums[2 * n] = w4_fma2(w4_mul2(x, e.x), f2, sums[2 * n]);
+                    sums[2 * n + 1] = w4_fma2(w4_mul2(y, e.y), f2, sums[2 * n + 1]);
                 }
             }
             tc_fence_before();
@@ -625,7 +631,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_w4_tiles(const __grid_const
     __syncthreads();
     if (warp < 4)
 #pragma unroll
-        for (int n = 0; n < 8 * NT; ++n) sh[n * LD + tid] = (acc[n] + sh[n * LD + tid]) * 16777216.f;
+        for (int n = 0; n < 8 * NT; ++n) sh[n * LD + tid] = acc[n] + sh[n * LD + tid];
     if (C > 1) cluster_sync_all();
     else __syncthreads();
     const int items = 128 * rows;
@@ -687,9 +693,10 @@ struct W4Plan {
 };
 
 // k_gemv_w4 up to 6 vectors, k_w4_tiles above (device us, k_gemv_w4 against
-// k_w4_tiles: 4096 x 4096 1 vector 5.6 and 7.8, 8 vectors 10.1 and 8.2; 13824 x 5120 5 vectors
-// 14.6 and 15.4; 32000 x 4096 8 vectors 20.3 and 18.4; 8192 x 28672 1 vector 24.4 and
-// 28.3, 4 vectors 27.3 and 28.4, 8 vectors 30.9 and 28.6).
+// k_w4_tiles, groups of 128 (13824: 64): 4096 x 4096 1 vector 5.7 and 7.8, 8 vectors 10.1 and 8.2; 13824 x 5120 5 vectors
+// 15.2 and 15.4; 32000 x 4096 8 vectors 20.3 and 18.4; 8192 x 28672 1 vector 25.0 and
+// 28.3, 4 vectors 27.3 and 28.4, 8 vectors 30.9 and 28.6; groups of 32: 8192 x 28672 1 vector
+// 42.3, 7 vectors 53.6 by tiles).
 constexpr int kFewVectors = 6;
 
 W4Plan w4_plan(int rows, int out, int k, int group, int nsm) {
@@ -716,7 +723,7 @@ W4Plan w4_plan(int rows, int out, int k, int group, int nsm) {
             const int outs = 16 * f.mt * f.wm, count = (out + outs - 1) / outs, parts = kW4Warps / f.wm, slots = w4_per_sm(group, f.mt) * nsm;
             int blocks = 1;
             while (blocks < 8 && static_cast<int64_t>(count) * (blocks + 1) <= static_cast<int64_t>(slots * kClusterRoom[blocks]) && (blocks + 1) * parts <= groups) ++blocks;
-            const int64_t smem = static_cast<int64_t>(parts) * ((groups + blocks * parts - 1) / (blocks * parts)) * (group * rows * 2 + 128);
+            const int64_t smem = static_cast<int64_t>(parts) * ((groups + blocks * parts - 1) / (blocks * parts)) * (group * rows * 2 + 32);
             const int64_t rounds = (static_cast<int64_t>(count) * blocks + slots - 1) / slots;
             const double fill = static_cast<double>(count) * blocks / (static_cast<double>(rounds) * slots);
             if (smem + w4_ring(group) > kW4Smem || parts > groups || fill <= most * 1.12) continue;
@@ -753,7 +760,7 @@ cudaError_t w4_few_launch(W4Args p, const W4Plan &plan, cudaStream_t s) {
     const int parts = kW4Warps / p.wm, outs = 16 * MT * p.wm;
     p.longest = (p.groups + p.blocks * parts - 1) / (p.blocks * parts);
     p.parts = p.blocks * parts;
-    p.ring = std::max(parts * p.longest * (GROUP * p.rows * 2 + 128), kW4Warps * MT * 8 * 20 * 4);
+    p.ring = std::max(parts * p.longest * (GROUP * p.rows * 2 + 32), kW4Warps * MT * 8 * 20 * 4);
     const int smem = p.ring + w4_ring(GROUP);
     return w4_clusters(k_gemv_w4<GROUP, MT>, dim3((p.out + outs - 1) / outs * p.blocks), 32 * kW4Warps, smem, p.blocks, s, p);
 }

@@ -162,3 +162,22 @@ def test_products_shared_unevenly(lib, rows, out, k, group):
     """Numbers of outputs for which 3, 5, 6 or 8 blocks share k, whose groups do not divide evenly."""
     x, w, s, y, tol = case(rows, out, k, group, seed=rows + out)
     close(lib.W4Matrix(w, s).matvec(x), y, tol)
+
+
+@pytest.mark.parametrize("rows,out,k,group", [(1, 2000, 4096, 128), (5, 900, 5120, 64), (2, 700, 2784, 32), (16, 512, 8192, 128), (9, 512, 4096, 32), (3, 256, 28672, 128)])
+def test_sums_keep_their_bits(lib, rows, out, k, group):
+    """Weights near 0, as they are in a model, and some strong channels: off by 2^-21 of the results' size at most.
+
+    Size: the 2-norm over the rows and outputs.  Terms of random sign add up like a random walk, whose mean square is
+    half of its end's, and a rounding to 2^-24 of a sum is 2^-24 / sqrt(3) of it in the mean square at most.  So n = k / group
+    + 64 <= 288 rounded additions are off by 2^-24 sqrt(n / 6) = 4.1e-7 together, and the products of a group, up to 8 after one
+    another at 2^-23, by 2^-23 sqrt(8 / 6) = 1.4e-7; both: 4.4e-7, below 2^-21."""
+    import torch
+    g = torch.Generator().manual_seed(k)
+    q = (torch.randn(out, k, generator=g) * 2.7).round().clamp(-8, 7)
+    w = (q + 8).to(torch.uint8)
+    s = (torch.exp(0.4 * torch.randn(out, k // group, generator=g)) * 0.007).to(torch.bfloat16)
+    x = (torch.randn(rows, k, generator=g) * (1 + 15 * (torch.rand(1, k, generator=g) < 0.01))).to(torch.bfloat16)
+    want = x.double() @ (q.double() * s.double().repeat_interleave(group, 1)).T
+    got = lib.W4Matrix((w[:, ::2] | w[:, 1::2] << 4).cuda(), s.cuda()).matvec(x.cuda()).cpu().double()
+    assert (got - want).norm() <= 2.0 ** -21 * want.norm()
