@@ -324,7 +324,7 @@ int la_gemm_bf16_noalloc(const void *x, const void *w, float *y, int32_t rows, i
  * half; scales device bf16 [out][k / group], group 32, 64 or 128, a divisor of
  * k; y device fp32, rows y_stride elements apart.  0 <= rows <= 256; the
  * matrix is read once for every 16 rows, so it is for a batch of single tokens.
- * x is exact to 2^-35 of the largest value of its group (of one row), the
+ * x is exact to 2^-39 of the largest value of its group (of one row), the
  * products' sums are fp32, and a group's sum meets its scale once; results are
  * deterministic.  A row with a value that is not finite is not finite at all.
  * Calls of many rows need a workspace: la_gemv_w4_workspace says how many bytes
@@ -530,8 +530,8 @@ typedef struct la_kv8_qkv {
 /* For each head x of q and of k: n = x / sqrt(mean(x^2) + eps) * weight (n = x
  * without a weight), then the rotation of the pairs (i, i + head_dim / 2) by
  * position * inv_freq[i]; v is only rounded.  All in fp32, rounded once to
- * bf16; the rotation's angles are exact to 2^-30 of a turn up to position
- * 2^20, and to 2^-24 for every position.  Of the cache it reads the sizes,
+ * bf16; the rotation's angles are within 2^-26 of a turn up to position
+ * 2^20, and within 2^-23 at every position.  Of the cache it reads the sizes,
  * lens and status alone, before the rows are appended.  Asynchronous, without
  * a workspace.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int la_kv8_norm_rope(const la_kv8_cache *c, const la_kv8_qkv *a, void *stream);

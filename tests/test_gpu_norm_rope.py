@@ -175,3 +175,24 @@ def test_zero_rows_zero_heads_and_streams(lib):
     for a, b in zip(again, other):
         assert torch.equal(a, b)
     close(again[1], *formula(k, None, [8, 13], 0, frequencies(10000.0, 128)))
+
+
+@pytest.mark.parametrize("base", [10000.0, 500000.0, 1.0, 0.25])
+def test_far_positions(lib, base):
+    """Angles by rope_base up to the largest position: off by 2^-23 of a turn at most, by 2^-26 up to position 2^20."""
+    import torch
+    c = cache(lib, 1, 2, 128, [0])
+    pos = [2 ** 20, 2 ** 20 - 1, 2 ** 31 - 1, -2 ** 31, 123456789]
+    q, k, _ = rows_of(5, 4, 2, 128, torch.float32, seed=3)
+    qo, _ = c.norm_rope(q, k, pos=ints(pos), rope_base=base)
+    c.status()
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60                                    # the angles in decimals: doubles end at 2^-53 of 2^31 turns
+    two_pi = Decimal("6.28318530717958647692528676655900576839433879875021164194988918")
+    f = [Decimal(base) ** (Decimal(-2 * i) / Decimal(128)) for i in range(64)]
+    for r, p in enumerate(pos):
+        angle = np.array([float((Decimal(p) * x / two_pi) % 1) for x in f]) * 2 * math.pi
+        y, tol = formula(q[r:r + 1], None, [1.0], 0, angle)
+        xd = np.abs(q[r:r + 1].cpu().double().numpy())
+        off = 2.0 ** -26 if abs(p) <= 2 ** 20 else 2.0 ** -23
+        close(qo[r:r + 1], y, tol + 2 * math.pi * off * np.concatenate([xd[..., :64] + xd[..., 64:]] * 2, -1))

@@ -17,14 +17,13 @@ def lib():
 def case(rows, out, k, group, seed=0, device="cuda"):
     """x, packed weights and scales on the GPU, with y and its tolerance in 64 bits.
 
-    Tolerance: products of a bf16 number and a whole number up to 15 are exact in
-    fp32 (x is, to 2^-35 of its group's largest value).  One matrix product adds 16
+    Tolerance: products of a bf16 number and a whole number of four bits are exact in
+    fp32 (x is, to 2^-39 of its group's largest value).  One matrix product adds 16
     of them to a sum and may cut each term at 2^-23 of the largest, so it is off
     by 17 * 2^-23 of the terms' magnitudes at most; a group takes group / 16 of
-    them, and 8 times the sum of its x, which rounds by (group + 8) * 2^-24 of
-    their magnitudes.  q - 8 is 1 in 16 times 0: terms with q and 8 x are bounded by
-    15 |x| and 8 |x|, so 23 times the group's |x| stands for the magnitudes.  Its
-    power is exact, its scale, the sum over the groups and over at most 64 parts
+    them.  q - 8 is 8 at most and 0 in one of 16 cases: 23 times the group's |x| bounds the
+    magnitudes, also for a kernel that adds q x and -8 times the sum of x, which
+    rounds by (group + 8) * 2^-24 of them.  The group's power is exact, its scale, the sum over the groups and over at most 64 parts
     of k round by 2^-24 each."""
     import torch
     g = np.random.default_rng(seed)
@@ -157,9 +156,10 @@ def test_calls_at_once(lib):
 
 @pytest.mark.parametrize("rows,out,k,group", [
     (1, 11008, 1024, 128), (2, 13800, 768, 128), (1, 24300, 384, 128), (1, 11008, 1056, 32), (3, 5000, 4128, 32), (4, 7100, 2240, 64),
-    (6, 1900, 3200, 128), (1, 2000, 8736, 32), (2, 100, 11232, 32)])
+    (6, 1900, 3200, 128), (1, 2000, 8736, 32), (2, 100, 11232, 32),
+    (16, 130, 32, 32), (7, 3, 64, 64)])
 def test_products_shared_unevenly(lib, rows, out, k, group):
-    """Numbers of outputs for which 3, 5, 6 or 8 blocks share k, whose groups do not divide evenly."""
+    """Numbers of outputs for which 3, 5, 6 or 8 blocks share k, whose groups do not divide evenly; matrices of one group."""
     x, w, s, y, tol = case(rows, out, k, group, seed=rows + out)
     close(lib.W4Matrix(w, s).matvec(x), y, tol)
 
