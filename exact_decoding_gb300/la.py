@@ -609,7 +609,7 @@ class Kv8Cache:
     def __init__(self, n_layers: int, n_pages: int, page: int, n_kv_heads: int, head_dim: int, n_seqs: int,
                  max_pages: int, device="cuda", tensors: Optional[dict] = None):
         import torch
-        self._torch = torch
+        self._torch, self._bf16, self._f32, self._i32 = torch, torch.bfloat16, torch.float32, torch.int32
         tensors = dict(tensors or {})
         given = next(iter(tensors.values()), None)
         dev = torch.device(given.device if given is not None else device)
@@ -672,13 +672,13 @@ class Kv8Cache:
 
     def _rows(self, t, name, heads, dtype=None):
         """bf16 (or `dtype`) [rows, heads, dim] with dense (heads, dim): rows, row stride."""
-        sh, st = t.shape, t.stride()
-        dtype = dtype or self._torch.bfloat16
-        if t.dtype is not dtype or t.get_device() != self._index or len(sh) != 3 or sh[2] != self.head_dim \
-                or (heads and sh[1] != heads) or st[2] != 1 or (st[1] != sh[2] and sh[1] > 1):
-            raise ValueError(f"{name} must be a {str(dtype)[6:]} tensor [rows, {heads or 'heads'}, {self.head_dim}] on {self.device} "
-                             f"with dense heads, not {t.dtype} {tuple(sh)} strides {st} on {t.device}")
-        return sh[0], st[0] if sh[0] > 1 else sh[1] * sh[2]
+        dtype, sh, st = dtype or self._bf16, t.shape, t.stride()
+        if len(sh) == 3:
+            (n, h, d), (row, head, one) = sh, st
+            if d == self.head_dim and one == 1 and (head == d or h == 1) and (h == heads or not heads) and t.dtype is dtype and t.get_device() == self._index:
+                return n, row if n > 1 else h * d
+        raise ValueError(f"{name} must be a {str(dtype)[6:]} tensor [rows, {heads or 'heads'}, {self.head_dim}] on {self.device} "
+                         f"with dense heads, not {t.dtype} {tuple(sh)} strides {st} on {t.device}")
 
     def _layers(self, t, name, rows):
         """bf16 [layers, rows, kv heads, dim] with dense (heads, dim): row and layer strides."""
@@ -754,40 +754,37 @@ class Kv8Cache:
         have nothing to do with the cache; depth [rows]: places of a tree's
         rows.  Returns (q, k) or (q, k, v), or writes to `out`, which may be
         the bfloat16 inputs themselves."""
-        torch = self._torch
-        dtype = q.dtype
-        if dtype not in (torch.float32, torch.bfloat16):
+        dtype, bf16, f32, heads, kv = q.dtype, self._bf16, self._f32, q.shape[1] if q.dim() == 3 else 0, self.n_kv_heads
+        if dtype is not f32 and dtype is not bf16:
             raise ValueError(f"q must be float32 or bfloat16, not {dtype}")
-        rows, qs = self._rows(q, "q", 0, dtype)
-        heads, ins = q.shape[1], (q, k) if v is None else (q, k, v)
-        strides = [qs]
-        for t, name in zip(ins[1:], "kv"):
-            n, st = self._rows(t, name, self.n_kv_heads, dtype)
-            if n != rows:
-                raise ValueError(f"{name} must have q's {rows} rows, not {n}")
-            strides.append(st)
+        n, qs = self._rows(q, "q", 0, dtype)
+        n_k, ks = self._rows(k, "k", kv, dtype)
+        n_v, vs = (n, 0) if v is None else self._rows(v, "v", kv, dtype)
+        if n_k != n or n_v != n:
+            raise ValueError(f"k and v must have q's {n} rows, not {n_k} and {n_v}")
         if out is None:
-            out = tuple(_empty(stream, *t.shape, dtype=torch.bfloat16, device=self.device) for t in ins)
-        elif len(out) != len(ins):
-            raise ValueError(f"out must be {len(ins)} tensors, as q, k{'' if v is None else ' and v'}")
-        out_strides = []
-        for t, name, h in zip(out, ("out's q", "out's k", "out's v"), (heads, self.n_kv_heads, self.n_kv_heads)):
-            n, st = self._rows(t, name, h)
-            if n != rows:
-                raise ValueError(f"{name} must have q's {rows} rows, not {n}")
-            out_strides.append(st)
-        kind = torch.bfloat16 if (q_weight is None and k_weight is None) else (k_weight if q_weight is None else q_weight).dtype
-        if kind not in (torch.float32, torch.bfloat16):
+            out = tuple([_empty(stream, *t.shape, dtype=bf16, device=self.device) for t in ((q, k) if v is None else (q, k, v))])
+        elif len(out) != (2 if v is None else 3):
+            raise ValueError(f"out must be {'q and k' if v is None else 'q, k and v'}, not {len(out)} tensors")
+        qo, ko, vo = out if v is not None else (*out, None)
+        m, qos = self._rows(qo, "out's q", heads)
+        m_k, kos = self._rows(ko, "out's k", kv)
+        m_v, vos = (n, 0) if vo is None else self._rows(vo, "out's v", kv)
+        if m != n or m_k != n or m_v != n:
+            raise ValueError(f"out must have q's {n} rows, not {m}, {m_k} and {m_v}")
+        weight = k_weight if q_weight is None else q_weight
+        kind = bf16 if weight is None else weight.dtype
+        if kind is not f32 and kind is not bf16:
             raise ValueError(f"q_weight and k_weight must be float32 or bfloat16, not {kind}")
-        vec = lambda t, name, dt, n: 0 if t is None else self._checked(t, name, dt, (n,))  # noqa: E731
-        none = [0] if v is None else []
-        args = _KV8_QKV.pack(heads, rows, LA_F32 if dtype is torch.float32 else LA_BF16, LA_F32 if kind is torch.float32 else LA_BF16, eps, rope_base,
-                             *strides, *none, *out_strides, *none, self._ints(row_start, "row_start", self.n_seqs + 1), self._ints(pos, "pos", rows),
-                             self._ints(depth, "depth", rows), *[t.data_ptr() for t in ins], *none, vec(q_weight, "q_weight", kind, self.head_dim),
-                             vec(k_weight, "k_weight", kind, self.head_dim), vec(inv_freq, "inv_freq", torch.float32, self.head_dim // 2),
-                             *[t.data_ptr() for t in out], *none)
+        dim = (self.head_dim,)
+        args = _KV8_QKV.pack(heads, n, LA_F32 if dtype is f32 else LA_BF16, LA_F32 if kind is f32 else LA_BF16, eps, rope_base, qs, ks, vs, qos, kos, vos,
+                             0 if row_start is None else self._ints(row_start, "row_start", self.n_seqs + 1), 0 if pos is None else self._ints(pos, "pos", n),
+                             0 if depth is None else self._ints(depth, "depth", n), q.data_ptr(), k.data_ptr(), 0 if v is None else v.data_ptr(),
+                             0 if q_weight is None else self._checked(q_weight, "q_weight", kind, dim), 0 if k_weight is None else self._checked(k_weight, "k_weight", kind, dim),
+                             0 if inv_freq is None else self._checked(inv_freq, "inv_freq", f32, (self.head_dim // 2,)),
+                             qo.data_ptr(), ko.data_ptr(), 0 if vo is None else vo.data_ptr())
         self._call(self._fn["la_kv8_norm_rope"], "la_kv8_norm_rope", args, stream=stream)
-        return tuple(out)
+        return out if type(out) is tuple else tuple(out)
 
     def append(self, k, v, row_start=None, row_idx=None, stored=None, max_rows: int = 0, workspace=None, stream=None):
         """Append the rows of k, v [layers, rows, kv heads, dim] (or the rows
