@@ -19,9 +19,15 @@
 // short search finds such a T that few more reach.  Lanes push such keys to shared memory; when 32 have
 // gathered the warp sorts them and merges.  The warps' lists are merged at the end.
 //
-// A row is one block's, or a cluster's: each block takes a run of it, and the
-// first joins their sums and keys through distributed shared memory.  So there
-// is one launch, no workspace, and results that do not depend on any order.
+// A row is one block's (of 1 to 8 warps, by its length), or a cluster's: each block
+// takes a run of it, and the first joins their sums and keys through distributed
+// shared memory.  So there is one launch, no workspace, and results that do not depend
+// on any order.
+//
+// Measured: 2048 rows of 32000 fp32 (262 MB) with 20 alternatives 60.6 us, 4.3 TB/s,
+// 64 % of a copy's rate; bound by instructions (68 % of the issue slots; without
+// alternatives 41.8 us, 93 %).  76 rows of 32016 bf16 with 20 alternatives 9.6 us, one
+// row of 32000 with 5 6.8 us: latency of a pass, the search for the threshold and the joins.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -33,7 +39,6 @@
 
 namespace la {
 
-constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
 constexpr int kLpPass = 16;       // elements of a thread's pass
 constexpr int kLpTop = 32;
 
@@ -150,20 +155,21 @@ __device__ __forceinline__ void lp_copy(uint32_t to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constant__ LpArgs p) {
+template <typename T, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) k_logprobs(const __grid_constant__ LpArgs p) {
+    constexpr int THREADS = 32 * WARPS;
     constexpr int VEC = LpType<T>::vec, E = kLpPass, NV = E / VEC;   // 16-byte loads of a pass
     constexpr float kLog2e = 1.4426950408889634f;
     constexpr uint32_t kNone = VEC == 4 ? 0xff800000u : 0xff80ff80u;  // -infinity
     extern __shared__ __align__(16) uint8_t lp_smem[];
-    uint4(*sh_ring)[NV][kLpThreads] = reinterpret_cast<uint4(*)[NV][kLpThreads]>(lp_smem);
-    LpKey(*sh_push)[kLpRoom] = reinterpret_cast<LpKey(*)[kLpRoom]>(lp_smem + kLpStages * NV * kLpThreads * 16);
-    __shared__ LpKey sh_list[kLpWarps][kLpTop];
-    __shared__ uint2 sh_first[kLpWarps];
-    __shared__ LpSum sh_sum[kLpWarps];
+    uint4(*sh_ring)[NV][THREADS] = reinterpret_cast<uint4(*)[NV][THREADS]>(lp_smem);
+    LpKey(*sh_push)[kLpRoom] = reinterpret_cast<LpKey(*)[kLpRoom]>(lp_smem + kLpStages * NV * THREADS * 16);
+    __shared__ LpKey sh_list[WARPS][kLpTop];
+    __shared__ uint2 sh_first[WARPS];
+    __shared__ LpSum sh_sum[WARPS];
     __shared__ LpSum sh_block;
     __shared__ LpKey sh_t;                       // the largest last key of a full list
-    __shared__ int sh_n[kLpWarps];               // keys that a warp has gathered
+    __shared__ int sh_n[WARPS];               // keys that a warp has gathered
     const la_logprobs_args &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, C = p.blocks, rank = C > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int row = blockIdx.x / C, top = a.n_top;
@@ -181,7 +187,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constan
     auto copy = [&](int base, int stage) {
         if (base < v1) {
 #pragma unroll
-            for (int k = 0; k < NV; ++k) lp_copy(smem_u32(&sh_ring[stage][k][tid]), zv + min(base + k * kLpThreads + tid, v1 - 1));
+            for (int k = 0; k < NV; ++k) lp_copy(smem_u32(&sh_ring[stage][k][tid]), zv + min(base + k * THREADS + tid, v1 - 1));
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -263,16 +269,16 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constan
     __syncthreads();
 
 #pragma unroll 1
-    for (int base = v0, stage = 0; base < v1; base += kLpThreads * NV, stage ^= 1) {
-        copy(base + kLpThreads * NV, stage ^ 1);
+    for (int base = v0, stage = 0; base < v1; base += THREADS * NV, stage ^= 1) {
+        copy(base + THREADS * NV, stage ^ 1);
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         uint4 w[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) w[k] = sh_ring[stage][k][tid];
-        if (base + kLpThreads * NV > v1) {
+        if (base + THREADS * NV > v1) {
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-                if (base + k * kLpThreads + tid >= v1) sh_ring[stage][k][tid] = w[k] = make_uint4(kNone, kNone, kNone, kNone);
+                if (base + k * THREADS + tid >= v1) sh_ring[stage][k][tid] = w[k] = make_uint4(kNone, kNone, kNone, kNone);
         }
         float v[E];
 #pragma unroll
@@ -298,7 +304,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constan
                 // warps' least k / 8-th; hi: fewer do
                 const uint32_t mine = most > -INFINITY ? order_key(most + 0.f) : 0u;
                 uint32_t rest = mine, lo = 0, hi = 0;
-                for (int i = 0; i < top; i += kLpWarps) {
+                for (int i = 0; i < top; i += WARPS) {
                     lo = __reduce_max_sync(0xffffffffu, rest);
                     if (rest == lo) rest = 0;
                     hi = max(hi, lo);
@@ -306,7 +312,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constan
                 if (lane == 0) sh_first[warp] = make_uint2(lo, hi);
                 __syncthreads();
 #pragma unroll
-                for (int w = 0; w < kLpWarps; ++w) {
+                for (int w = 0; w < WARPS; ++w) {
                     lo = min(lo, sh_first[w].x);
                     hi = max(hi, sh_first[w].y);
                 }
@@ -332,7 +338,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constan
                     if (quad[q] > below) {
 #pragma unroll
                         for (int e = 4 * q; e < 4 * q + 4; ++e)
-                            if (v[e] > below) push(v[e], first + e / VEC * kLpThreads * VEC + e % VEC);
+                            if (v[e] > below) push(v[e], first + e / VEC * THREADS * VEC + e % VEC);
                     }
                     if (q & 1) {
                         __syncwarp();
@@ -372,14 +378,14 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constan
     __syncthreads();
     if (top) {   // the warps' lists, two and two
 #pragma unroll 1
-        for (int o = kLpWarps / 2; o; o >>= 1) {
+        for (int o = WARPS / 2; o; o >>= 1) {
             if (warp < o) sh_list[warp][lane] = list = lp_merge(list, sh_list[warp + o][lane], lane);
             __syncthreads();
         }
     }
     if (warp == 0) {
         sum = sh_sum[0];
-        for (int w = 1; w < kLpWarps; ++w) sum = lp_join(sum, sh_sum[w]);
+        for (int w = 1; w < WARPS; ++w) sum = lp_join(sum, sh_sum[w]);
         if (lane == 0) sh_block = sum;
     }
     if (C > 1) {
@@ -412,9 +418,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) k_logprobs(const __grid_constan
     const bool none = all.m == -INFINITY && !isnan(all.r), bad = isnan(all.r) || all.m == INFINITY;
     auto out = [&](float x) { return bad ? NAN : none || x == -INFINITY ? -INFINITY : (x - all.m) - l; };
     if (a.tokens) {
-        for (int i = tid; i < a.n_tokens; i += kLpThreads) {
+        for (int i = tid; i < a.n_tokens; i += THREADS) {
             const long long at = static_cast<long long>(row) * a.n_tokens + i;
-            if (i >= kLpThreads) {
+            if (i >= THREADS) {
                 const int t = a.tokens[at];
                 given = t >= 0 && t < a.vocab ? to_f32<T>(z[t]) : -INFINITY;
             }
@@ -439,17 +445,30 @@ int lp_bad(const char *what, int code = LA_ERR_INVALID_ARG) {
 
 }  // namespace
 
-cudaError_t logprobs_launch(const la_logprobs_args &a, int nsm, cudaStream_t s) {
+// Warps of a block: a warp's pass is 512 logits, and what a row costs beside its
+// passes grows with them; with more rows than fit at a time fewer warps for each pay
+// sooner.  Device us with 8, 4, 2 and 1 warps (fp32, 20 alternatives): 1838 rows of 120: 30.9,
+// 16.1, 12.8, 8.0; 100 of 500: 7.8, 4.9, 4.7, 6.2; 2000 of 2288: 26.1, 17.5, 14.4, 20.3; 100 of 2288: 6.2,
+// 5.8, 8.2, 13.8; 300 of 8192: 9.1, 10.5, 15.7; 700 of 32000: 30.1, 35.1, 49.9; 2048 of 32000:
+// 63.8, 60.5, 62.0.
+static int lp_warps(const la_logprobs_args &a, int nsm) {
+    if (a.vocab <= 256) return 1;
+    if (a.vocab <= 1024 || (a.vocab <= 2560 && a.rows > 8 * nsm)) return 2;
+    return a.vocab <= 4096 || a.rows > 7 * nsm ? 4 : 8;
+}
+
+template <typename T, int WARPS>
+static cudaError_t logprobs_start(const la_logprobs_args &a, int nsm, cudaStream_t s) {
+    constexpr int pass = 32 * WARPS * kLpPass, smem = kLpStages * pass * static_cast<int>(sizeof(T)) + WARPS * kLpRoom * 8;
     LpArgs p{};
     p.a = a;
     // Blocks of a row: while the rows leave SMs idle and each has a pass of its own
-    const int pass = kLpThreads * kLpPass;
     p.blocks = 1;
     while (p.blocks < 8 && static_cast<long long>(a.rows) * p.blocks * 2 <= nsm && a.vocab > p.blocks * pass) p.blocks *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows) * p.blocks);
-    cfg.blockDim = dim3(kLpThreads);
-    cfg.dynamicSmemBytes = kLpStages * kLpThreads * kLpPass * (a.type == LA_F32 ? 4 : 2) + kLpWarps * kLpRoom * 8;
+    cfg.blockDim = dim3(32 * WARPS);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -464,13 +483,21 @@ cudaError_t logprobs_launch(const la_logprobs_args &a, int nsm, cudaStream_t s) 
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(done.load() >> dev & 1)) {
-        const int most = kLpStages * kLpThreads * kLpPass * 4 + kLpWarps * kLpRoom * 8;
-        e = cudaFuncSetAttribute(k_logprobs<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(k_logprobs<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        e = cudaFuncSetAttribute(k_logprobs<T, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         if (dev < 64) done.fetch_or(1ull << dev);
     }
-    return a.type == LA_F32 ? cudaLaunchKernelEx(&cfg, k_logprobs<float>, p) : cudaLaunchKernelEx(&cfg, k_logprobs<__nv_bfloat16>, p);
+    return cudaLaunchKernelEx(&cfg, k_logprobs<T, WARPS>, p);
+}
+
+template <typename T>
+static cudaError_t logprobs_launch(const la_logprobs_args &a, int nsm, cudaStream_t s) {
+    switch (lp_warps(a, nsm)) {
+    case 1: return logprobs_start<T, 1>(a, nsm, s);
+    case 2: return logprobs_start<T, 2>(a, nsm, s);
+    case 4: return logprobs_start<T, 4>(a, nsm, s);
+    default: return logprobs_start<T, 8>(a, nsm, s);
+    }
 }
 
 static int logprobs_body(const la_logprobs_args *args, void *stream) {
@@ -490,7 +517,8 @@ static int logprobs_body(const la_logprobs_args *args, void *stream) {
     int nsm = 0;
     const int rc = sm_count(&nsm);
     if (rc != LA_OK) return rc;
-    const cudaError_t e = logprobs_launch(a, nsm, static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = a.type == LA_F32 ? logprobs_launch<float>(a, nsm, s) : logprobs_launch<__nv_bfloat16>(a, nsm, s);
     return e == cudaSuccess ? LA_OK : lp_bad(cudaGetErrorString(e), LA_ERR_CUDA);
 }
 

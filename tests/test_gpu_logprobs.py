@@ -191,3 +191,21 @@ def test_forms_of_the_call(lib):
     for a, b, c in zip((lp, ent, ids, best), out, other):
         assert torch.equal(a, b) and torch.equal(a, c)
     assert lib.logprobs(z[:0], tokens[:0], top=2)[2].shape == (0, 2)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("rows,vocab,top", [(1300, 2050, 20), (1301, 5003, 32), (2500, 200, 7), (3000, 1024, 1)])
+def test_many_rows(lib, dtype, rows, vocab, top):
+    """More rows than the GPU holds at a time: some of them against the definition, all against the same rows in small calls."""
+    import torch
+    z = logits(rows, vocab, dtype, rows)
+    z[5] = z[6]
+    tokens = torch.from_numpy(np.random.default_rng(3).integers(0, vocab, (rows, 2)).astype(np.int32)).cuda()
+    got = lib.logprobs(z, tokens, top=top)
+    some = torch.tensor([0, 1, 5, 6, rows // 2, rows - 1], device="cuda")
+    agree([x[some] for x in got], *model(z[some].cpu().double().numpy(), tokens[some].cpu().numpy(), top))
+    for i in range(0, rows, 100):
+        part = lib.logprobs(z[i:i + 100], tokens[i:i + 100], top=top)
+        assert torch.equal(part[2], got[2][i:i + 100])
+        for a, b in zip(part, got):
+            torch.testing.assert_close(a, b[i:i + 100], rtol=1e-5, atol=1e-5)
