@@ -209,3 +209,13 @@ def test_many_rows(lib, dtype, rows, vocab, top):
         assert torch.equal(part[2], got[2][i:i + 100])
         for a, b in zip(part, got):
             torch.testing.assert_close(a, b[i:i + 100], rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.parametrize("rows,vocab", [(120, 32003), (3, 250001), (70, 60000)])
+def test_long_rows_in_parts(lib, rows, vocab):
+    """Rows that two to eight blocks share, some of them two on an SM."""
+    z = logits(rows, vocab, "bfloat16", 5)
+    got = lib.logprobs(z, top=32)
+    some = [0, rows // 2, rows - 1]
+    want, tols = model(z[some].cpu().double().numpy(), np.zeros((3, 0), np.int32), 32)
+    agree([z.new_zeros(3, 0), got[1][some], got[2][some], got[3][some]], want, tols)
