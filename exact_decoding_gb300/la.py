@@ -308,8 +308,8 @@ NOALLOC_SCRATCH_FLOATS = 4 * 1024 * 1024
 
 
 def la_gemm_status(stream: Optional[int] = None) -> None:
-    """Raise LaError(-5) if a bounded wait inside an earlier la_gemm_bf16 /
-    la_gemm_bf16_noalloc kernel on this device gave up; clears the status."""
+    """Raise LaError(-5) if a bounded wait inside an earlier la_gemm_bf16,
+    la_gemm_bf16_noalloc or la_gemv_w4 kernel on this device gave up; clears the status."""
     _check(load_library().la_gemm_status(stream), "la_gemm_status")
 
 
