@@ -479,30 +479,35 @@ def logprobs(logits, tokens=None, top: int = 0, out=None, stream=None):
     `stream` (default: torch's current one of the logits' device) and does not
     synchronise."""
     torch = _torch()
-    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16) or (logits.stride(1) != 1 and logits.shape[1] > 1):
-        raise ValueError(f"logits must be float32 or bfloat16 [rows, vocab] with dense rows, not {logits.dtype} {tuple(logits.shape)} "
-                         f"strides {logits.stride()}")
-    index = _cuda_index(logits, "logits")
-    rows, vocab = logits.shape
-    n = 0
+    f32, sh, st, kind = torch.float32, logits.shape, logits.stride(), logits.dtype
+    if len(sh) != 2 or (kind is not f32 and kind is not torch.bfloat16) or (st[1] != 1 and sh[1] > 1):
+        raise ValueError(f"logits must be float32 or bfloat16 [rows, vocab] with dense rows, not {kind} {tuple(sh)} strides {st}")
+    index = logits.get_device()
+    if index < 0:
+        _cuda_index(logits, "logits")
+    rows, vocab = sh
+    n, given = 0, None
     if tokens is not None:
-        if tokens.dtype is not torch.int32 or tokens.dim() not in (1, 2) or tokens.shape[0] != rows or not tokens.is_contiguous() or tokens.get_device() != index:
+        given = tokens.shape
+        if tokens.dtype is not torch.int32 or not 1 <= len(given) <= 2 or given[0] != rows or not tokens.is_contiguous() or tokens.get_device() != index:
             raise ValueError(f"tokens must be a contiguous int32 tensor [{rows}] or [{rows}, n] on {logits.device}, not {tokens.dtype} "
-                             f"{tuple(tokens.shape)} on {tokens.device}")
-        n = tokens.shape[1] if tokens.dim() == 2 else 1
+                             f"{tuple(given)} on {tokens.device}")
+        n = given[1] if len(given) == 2 else 1
     if out is None:
-        f = {"dtype": torch.float32, "device": logits.device}
-        out = (None if tokens is None else _empty(stream, *tokens.shape, **f), _empty(stream, rows, **f),
-               _empty(stream, rows, max(top, 0), dtype=torch.int32, device=logits.device), _empty(stream, rows, max(top, 0), **f))
+        f = {"dtype": f32, "device": logits.device}
+        lp, entropy = None if tokens is None else _empty(stream, *given, **f), _empty(stream, rows, **f)
+        ids, best = _empty(stream, rows, max(top, 0), dtype=torch.int32, device=logits.device), _empty(stream, rows, max(top, 0), **f)
+        out = lp, entropy, ids, best
     else:
-        want = ((None if tokens is None else tokens.shape, torch.float32), ((rows,), torch.float32), ((rows, top), torch.int32), ((rows, top), torch.float32))
-        for name, t, (shape, dtype) in zip(("logprob", "entropy", "ids", "top logprob"), out, want):
-            if (t is None) != (shape is None) or t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != index):
-                raise ValueError(f"out's {name} must be {'None' if shape is None else f'a contiguous {dtype} tensor {tuple(shape)} on {logits.device}'}")
-    lp, entropy, ids, best = out
-    args = _LOGPROBS.pack(rows, vocab, LA_F32 if logits.dtype is torch.float32 else LA_BF16, n, top, logits.stride(0) if rows > 1 else vocab,
-                          logits.data_ptr(), tokens.data_ptr() if n else 0, lp.data_ptr() if n else 0, entropy.data_ptr(),
-                          ids.data_ptr() if top > 0 else 0, best.data_ptr() if top > 0 else 0)
+        lp, entropy, ids, best = out
+        if (lp is None) != (given is None):
+            raise ValueError(f"out's logprob must be {'None' if given is None else f'a float32 tensor {tuple(given)}'}")
+        listed = (rows, top)
+        for name, t, shape, dtype in (("logprob", lp, given, f32), ("entropy", entropy, (rows,), f32), ("ids", ids, listed, torch.int32), ("top logprob", best, listed, f32)):
+            if t is not None and (t.shape != shape or t.dtype is not dtype or not t.is_contiguous() or t.get_device() != index) or t is None and name != "logprob":
+                raise ValueError(f"out's {name} must be a contiguous {dtype} tensor {tuple(shape)} on {logits.device}")
+    args = _LOGPROBS.pack(rows, vocab, LA_F32 if kind is f32 else LA_BF16, n, top, st[0] if rows > 1 else vocab, logits.data_ptr(), tokens.data_ptr() if n else 0,
+                          lp.data_ptr() if n else 0, entropy.data_ptr(), ids.data_ptr() if top > 0 else 0, best.data_ptr() if top > 0 else 0)
     _on(index, stream, load_library().la_logprobs, "la_logprobs", args)
     return out
 
