@@ -50,7 +50,7 @@ constexpr int w4_per_sm(int group, int mt) { return mt == 1 && group < 128 ? 3 :
 // (8192 x 28672: 54.2 us with loads of 4 bytes, 42.3 so; four or five stages leave
 // room for fewer blocks and take longer at smaller sizes; groups of 64 gain nothing).
 constexpr int kW4RingRow = 80, kW4Stages = 3;
-constexpr int w4_ring(int group) { return group == 32 ? kW4Warps * kW4Stages * 16 * kW4RingRow : 0; }
+constexpr int w4_ring_bytes(int group) { return group == 32 ? kW4Warps * kW4Stages * 16 * kW4RingRow : 0; }
 
 struct W4Args {
     const __nv_bfloat16 *x;
@@ -726,7 +726,7 @@ W4Plan w4_plan(int rows, int out, int k, int group, int nsm) {
             const int64_t smem = static_cast<int64_t>(parts) * ((groups + blocks * parts - 1) / (blocks * parts)) * (group * rows * 2 + 32);
             const int64_t rounds = (static_cast<int64_t>(count) * blocks + slots - 1) / slots;
             const double fill = static_cast<double>(count) * blocks / (static_cast<double>(rounds) * slots);
-            if (smem + w4_ring(group) > kW4Smem || parts > groups || fill <= most * 1.12) continue;
+            if (smem + w4_ring_bytes(group) > kW4Smem || parts > groups || fill <= most * 1.12) continue;
             idle = static_cast<int64_t>(count) * blocks * 2 <= slots;
             most = fill;
             best.mt = f.mt, best.wm = f.wm, best.blocks = blocks;
@@ -761,7 +761,7 @@ cudaError_t w4_few_launch(W4Args p, const W4Plan &plan, cudaStream_t s) {
     p.longest = (p.groups + p.blocks * parts - 1) / (p.blocks * parts);
     p.parts = p.blocks * parts;
     p.ring = std::max(parts * p.longest * (GROUP * p.rows * 2 + 32), kW4Warps * MT * 8 * 20 * 4);
-    const int smem = p.ring + w4_ring(GROUP);
+    const int smem = p.ring + w4_ring_bytes(GROUP);
     return w4_clusters(k_gemv_w4<GROUP, MT>, dim3((p.out + outs - 1) / outs * p.blocks), 32 * kW4Warps, smem, p.blocks, s, p);
 }
 template <int GROUP>

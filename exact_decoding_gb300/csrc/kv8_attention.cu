@@ -30,6 +30,7 @@
 // heads: 8.5 us with neither, 7.1 with both).
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kv8.h"
 
@@ -101,9 +102,8 @@ struct Kv8Seq {
 // two edges, in which keys are masked.
 //
 // Windows measured (floor: the window's bytes, or its products): the last 4096 of
-// 65413 tokens and 4 first ones, 64 heads over 8 KV heads, 14.0 us (the same
-// tokens without a window 12.0 in a cache of no more; 8.4 MB, latency); 64
-// sequences of up to 8192, window 1024, 38.5 us (130 MB: 3.4 TB/s); 121 rows of 32
+// 65413 tokens and 4 first ones, 64 heads over 8 KV heads, 13.5 us (8.4 MB, latency); 64
+// sequences of up to 8192, window 1024, 32.8 us (130 MB: 4.0 TB/s); 121 rows of 32
 // heads, window 512, 32.3 us; 256 rows over 16k tokens, window 4096, 63.9 us
 // (115.7 without).  What a short unit costs beside its tiles bounds them: positions,
 // pages and queries are looked up one behind another before the first product.
@@ -879,6 +879,498 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
             } else {
                 *reinterpret_cast<float4 *>(p.part + (static_cast<long long>(slot) * kRowsQ + r) * HD + d) = acc;
                 if (d == 0) *reinterpret_cast<float4 *>(p.part_ml + (static_cast<long long>(slot) * kRowsQ + r) * 4) = make_float4(R, D, L, 0.f);
+            }
+        }
+        fence_proxy_async_smem();   // these accesses before the next unit's bulk copies into the same bytes
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------ up to eight query vectors per KV head, with a window
+// k_kv8_few: k_kv8_rows for 8 query vectors, with the operands changed over: keys
+// are the rows of the first product (S^T = K Q^T, 16 keys x 8 vectors) and dims those of
+// the second (O^T = V^T P^T), so none of a product's rows is empty, and the scores and O
+// take half the registers.  That makes room for 12 warps on an SM, and for more of
+// a unit's tiles at a time: short units are bound by what a tile takes one warp (about
+// 2 us, most of it waiting for the instruction before).  Windows of 1024 and 4 first tokens, 64
+// sequences, 64 heads over 8 KV heads, pages of 64: 32.8 us, k_kv8_rows 38.6 (4 warps and
+// three blocks of ring each 34.0, three CTAs of 4 warps 37.2); 32 of them with pages of 128 27.2 and 35.9; 48
+// sequences, head_dim 64, 12 heads over 4, window 700 11.1 and 16.3; one window of 4096 13.5 and
+// 14.1.  Without a window k_kv8_rows stays: its sums have another order.
+//   S^T: rows g and g + 8 of product b are keys CH (g >> 1) + 4 b + (g & 1) and 2 more of
+//        the piece; lane (g, t) reads HD / 4 consecutive bytes of theirs, and has the
+//        scores of vectors 2 t and 2 t + 1.
+//   P^T: packed pairs turned by movmatrix: lane (g, t) has vector g's weights of keys
+//        CH t + 4 b .. + 3, whose bytes of V are those that it reads for dims 16 n + g, + 8.
+constexpr int kFewQ = 8;
+
+template <int HD, int PAGE>
+struct Few {
+    static constexpr int block = HD * PAGE;
+    static constexpr int warps = 6;
+    static constexpr int slots = block >= 8192 ? 2 : 4;
+    static constexpr int per_sm = block > 8192 ? 1 : 2;
+    static constexpr int ring = block * slots * warps;
+    static constexpr int join = warps * kFewQ * (HD + 4) * 4;
+    static constexpr int q_row = HD * 2 + 16;                                   // q in fp16
+    static constexpr int q_off = ring > join ? ring : join;
+    static constexpr int qf_off = q_off + kFewQ * q_row;
+    static constexpr int ml_off = qf_off + kFewQ * 4;
+    static constexpr int reach_off = ml_off + warps * kFewQ * 16;
+    static constexpr int bar_off = reach_off + warps * kFewQ * 4;
+    static constexpr int sum_off = bar_off + warps * slots * 8;
+    static constexpr int tiles_off = sum_off + warps * 8;
+    static size_t bytes(int n_seqs) { return tiles_off + (static_cast<size_t>(n_seqs) + 1) * 8; }
+};
+
+// The 8 x 8 matrix of 16-bit numbers whose rows the warp's lanes hold in pairs, turned.
+__device__ __forceinline__ uint32_t turned(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+template <int HD, int PAGE>
+__global__ void __launch_bounds__(32 * Few<HD, PAGE>::warps, Few<HD, PAGE>::per_sm) k_kv8_few(const __grid_constant__ Kv8Args p) {
+    using Lay = Few<HD, PAGE>;
+    constexpr int ND = HD / 16;                   // 16-dim groups
+    constexpr int KT = PAGE < 64 ? PAGE : 64;     // keys per piece
+    constexpr int CH = KT / 4, NB = KT / 16;      // of them, one lane's bytes of V; products
+    constexpr int NS = Lay::slots, NW = Lay::warps;
+    extern __shared__ __align__(128) uint8_t smem[];
+    float4 *sh_ml = reinterpret_cast<float4 *>(smem + Lay::ml_off);  // [warp][8] r, d, l
+    float *sh_o = reinterpret_cast<float *>(smem);                   // [warp][8][HD + 4], over the ring
+    float *sh_qf = reinterpret_cast<float *>(smem + Lay::qf_off);
+    long long *tiles = reinterpret_cast<long long *>(smem + Lay::tiles_off);
+    pdl_trigger();
+    const la_kv8_cache &c = p.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t ring = smem_u32(smem) + warp * NS * Lay::block, bars = smem_u32(smem + Lay::bar_off) + warp * NS * 8;
+    const uint8_t *my_ring = smem + warp * NS * Lay::block;
+    float *reach = reinterpret_cast<float *>(smem + Lay::reach_off) + warp * kFewQ + 2 * t;   // of this lane's two vectors
+    if (lane < NS) mbar_init(bars + lane * 8, 1);
+    fence_barrier_init();
+    pdl_wait();
+    kv8_plan<true>(p, tiles, reinterpret_cast<long long *>(smem + Lay::sum_off));
+    Kv8Walk walk = kv8_walk<true>(p, tiles);
+    Kv8Piece u;
+    int in_slot = 0, out_slot = 0;   // ring positions: the next block to load, the next to read
+    uint32_t out_phase = 0;
+    bool ok = true;                  // false once a wait gave up: this warp loads nothing more
+    bool noted = p.whole;
+
+    for (;;) {
+        const bool any = kv8_next<true>(p, tiles, walk, u);
+        auto note = [&]() {
+            if (!noted && tid == 0) kv8_note(p, tiles, any, u);
+            noted = true;
+        };
+        if (!any) {
+            note();
+            break;
+        }
+        const Kv8Seq sq = u.sq;
+        const int page0 = u.k0 + warp, s = u.s, head = u.head;
+        const int new0 = NW - 1 - warp;   // new rows begin with the last warp, which has no more tiles than another
+        const int nc = ok && page0 < u.k1 ? (u.k1 - page0 + NW - 1) / NW : 0;
+        // q and the first new row before the copies (see k_kv8_rows); 16 threads of the first four warps a vector
+        const int q_mine = tid >> 4, q_part = tid & 15;
+        uint4 q_raw = make_uint4(0, 0, 0, 0);
+        if (q_mine < u.nqv && 8 * q_part < HD) {
+            const int qv = u.qv0 + q_mine, its = qv / p.gq;
+            q_raw = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.q) + (sq.first + its) * p.a.q_stride + (head * p.gq + qv - its * p.gq) * HD + 8 * q_part);
+        }
+        uint4 kw[HD / 64];          // this lane's HD / 8 dims of a new key
+        uint16_t vw[2 * ND];        // and its dims 16 n + g, + 8 of the value
+        auto load_new = [&](int j) {
+            const uint4 *kj = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.k) + (sq.first + j) * p.a.k_stride + head * HD + g * (HD / 8));
+            const uint16_t *vj = reinterpret_cast<const uint16_t *>(static_cast<const __nv_bfloat16 *>(p.a.v) + (sq.first + j) * p.a.v_stride + head * HD) + g;
+#pragma unroll
+            for (int i = 0; i < HD / 64; ++i) kw[i] = kj[i];
+#pragma unroll
+            for (int i = 0; i < 2 * ND; ++i) vw[i] = vj[8 * i];
+        };
+        const int n_new = u.begins && p.a.k ? sq.rows : 0;
+        if (new0 < n_new) load_new(new0);
+        // Block 2 i is K of tile i, block 2 i + 1 its V: as in k_kv8_rows
+        int my_page = -1, last_page = -1, issued = 0;
+        float my_kf = 0.f, last_kf = 0.f, my_vs = 0.f, last_vs = 0.f;
+        auto issue = [&]() {
+            const int i = issued >> 1;
+            if ((issued & 63) == 0) {
+                last_page = my_page;
+                last_vs = my_vs;
+                last_kf = my_kf;
+                my_page = i + lane < nc ? kv8_page(c, s, kv8_tile<true>(sq, page0 + NW * (i + lane))) : -1;
+                const long long blk = kv8_block(c, p.a.layer, max(my_page, 0), head);
+                my_kf = c.k_scale[blk];
+                my_vs = c.v_scale[blk];
+            }
+            const int pg = __shfl_sync(0xffffffffu, my_page, i & 31);
+            if (lane == 0) {
+                const uint32_t bar = bars + in_slot * 8;
+                if (pg >= 0) {
+                    mbar_arrive_expect_tx(bar, Lay::block);
+                    bulk_load(ring + in_slot * Lay::block,
+                              static_cast<const uint8_t *>(issued & 1 ? c.v : c.k) + kv8_block(c, p.a.layer, pg, head) * Lay::block, Lay::block, bar);
+                } else {
+                    mbar_arrive_expect_tx(bar, 0);   // a page number outside the cache: nothing is loaded, no key counts
+                }
+            }
+            __syncwarp();
+            in_slot = in_slot + 1 == NS ? 0 : in_slot + 1;
+            ++issued;
+        };
+#pragma unroll 1
+        while (issued < min(NS, 2 * nc)) issue();
+        note();   // while the first copies are on their way
+
+        // q as fp16, each vector scaled by a power of two to fit
+        if (q_mine < kFewQ) {   // whole warps
+            const uint4 w = q_raw;
+            uint32_t top = most2(most2(most2(most2(0u, w.x), w.y), w.z), w.w);
+#pragma unroll
+            for (int k = 1; k < 16; k <<= 1) top = most2(top, __shfl_xor_sync(0xffffffffu, top, k));
+            const int qx = fit_pair(top);
+            const float f = power_of(-qx);
+            if (8 * q_part < HD)
+                *reinterpret_cast<uint4 *>(smem + Lay::q_off + q_mine * Lay::q_row + 16 * q_part) = make_uint4(scaled_f16(w.x, f), scaled_f16(w.y, f), scaled_f16(w.z, f), scaled_f16(w.w, f));
+            if (q_part == 0) sh_qf[q_mine] = factor(power_of(qx), p.scale_log2);
+        }
+        __syncthreads();
+        uint32_t q[HD / 8];   // the first product's operand: vector g, dims t HD / 4 on
+#pragma unroll
+        for (int i = 0; i < HD / 32; ++i) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(smem + Lay::q_off + g * Lay::q_row + t * (HD / 2) + 16 * i);
+            q[4 * i] = x.x, q[4 * i + 1] = x.y, q[4 * i + 2] = x.z, q[4 * i + 3] = x.w;
+        }
+        const float qf[2] = {sh_qf[2 * t], sh_qf[2 * t + 1]};
+
+        // Of vectors 2 t and 2 t + 1
+        float r[2] = {-INFINITY, -INFINITY}, d[2] = {kRowsUnit, kRowsUnit}, l[2] = {0.f, 0.f};
+        float far[2] = {-INFINITY, -INFINITY};   // reach of O, of the new rows
+        float o[ND][4];                          // dims 16 n + g (0, 1) and + 8 (2, 3)
+#pragma unroll
+        for (int i = 0; i < ND; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        int row[2], from[2];                     // their new rows, and where those' windows begin
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int mine = 2 * t + e < u.nqv ? (u.qv0 + 2 * t + e) / p.gq : -1, there = max(mine, 0);
+            row[e] = mine;
+            from[e] = sq.len + (p.a.vis ? kv8_seen(p, sq.first, sq.rows, there) : p.a.k ? there + 1 : 0) - p.window;
+        }
+
+        // ---- new rows, in the piece that begins the unit: one key at a time
+        if (n_new > 0) {
+#pragma unroll 1
+            for (int j = new0; j < n_new; j += NW) {
+                bool see[2];
+                float z[2] = {0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (p.a.vis) see[e] = row[e] >= 0 && (kv8_window_new(p, sq.first, sq.rows, sq.len, row[e], j & ~31) >> (j & 31) & 1u);
+                    else see[e] = j <= row[e] && (j < p.sinks - sq.len || j > row[e] - p.window);
+                    const uint8_t *at = smem + Lay::q_off + (2 * t + e) * Lay::q_row + g * (HD / 4);
+#pragma unroll
+                    for (int i = 0; i < HD / 64; ++i) {
+                        const uint4 a = *reinterpret_cast<const uint4 *>(at + 16 * i);
+                        const uint32_t x[4] = {kw[i].x, kw[i].y, kw[i].z, kw[i].w}, y[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 qa = __half22float2(*reinterpret_cast<const __half2 *>(&y[k]));
+                            z[e] = fmaf(qa.x, bf16_bits(x[k] & 0xffffu), fmaf(qa.y, __uint_as_float(x[k] & 0xffff0000u), z[e]));
+                        }
+                    }
+                }
+                uint32_t top = 0;   // V's largest magnitude: what it reaches in O may raise d
+#pragma unroll
+                for (int i = 0; i < 2 * ND; ++i) top = max(top, vw[i] & 0x7fffu);
+#pragma unroll
+                for (int k = 4; k < 32; k <<= 1) {
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, k));
+                    z[0] += __shfl_xor_sync(0xffffffffu, z[0], k);
+                    z[1] += __shfl_xor_sync(0xffffffffu, z[1], k);
+                }
+                const int ve = exponent_of(bf16_bits(top));   // 128: a NaN or infinity, which hides its neighbours' size
+                float w[2], alpha[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float x = see[e] ? z[e] * qf[e] : -INFINITY, nr = x > r[e] ? ceilf(x) : r[e], base = nr == -INFINITY ? 0.f : nr;
+                    const float fl = ex2(r[e] - base);
+                    far[e] = fmaxf(far[e] - (base - r[e]), (x - base) + static_cast<float>(ve == 128 ? 0 : ve + 1));
+                    const float nd = fmaxf(d[e], far[e] - kSpan);
+                    alpha[e] = fl * ex2(d[e] - nd);
+                    r[e] = nr;
+                    d[e] = nd;
+                    l[e] = l[e] * fl + ex2(x - base);
+                    w[e] = ex2((x - base) - nd);
+                }
+#pragma unroll
+                for (int i = 0; i < ND; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float v = bf16_bits(vw[2 * i + h]);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)   // what a row does not see never meets it, not even times 0
+                            o[i][2 * h + e] = fmaf(w[e], see[e] ? v : 0.f, o[i][2 * h + e] * alpha[e]);
+                    }
+                if (j + NW < n_new) load_new(j + NW);
+            }
+            // Every lane g has added the key: l is summed over them below.
+            if (g != 0) l[0] = l[1] = 0.f;
+        }
+        reach[0] = far[0];
+        reach[1] = far[1];
+
+        // ---- cached tokens
+        auto landed = [&]() {   // the next block to read is there
+            ok = __all_sync(0xffffffffu, bar_wait(bars + out_slot * 8, out_phase, c.status, LA_KV8_TIMEOUT));
+            return ok;
+        };
+        auto next = [&]() {     // it has been read: its slot takes the next block to load
+            __syncwarp();
+            if (++out_slot == NS) {
+                out_slot = 0;
+                out_phase ^= 1;
+            }
+            if (issued < 2 * nc) issue();
+        };
+        int read = 0;           // blocks read
+#pragma unroll 1
+        for (int i = 0; i < nc; ++i) {
+            if (!landed()) break;
+            const bool old = i >> 5 != (issued - 1) >> 6;   // issue() is in the next 32 tiles already
+            const int pg = __shfl_sync(0xffffffffu, old ? last_page : my_page, i & 31);
+            const float kf_ = __shfl_sync(0xffffffffu, old ? last_kf : my_kf, i & 31), kf = pg < 0 ? 1.f : kf_;
+            const float vs_ = __shfl_sync(0xffffffffu, old ? last_vs : my_vs, i & 31);
+            const float v = static_cast<float>(pg < 0 ? 0 : exponent_of(vs_));
+            const int key0 = kv8_tile<true>(sq, page0 + NW * i) * PAGE, left = pg < 0 ? 0 : sq.len - key0;   // keys of this page that count
+            const bool edge = kv8_edge(p, sq, (u.qv0 + u.nqv - 1) / p.gq, key0, PAGE);
+            const uint8_t *kblk = my_ring + out_slot * Lay::block, *vblk = nullptr;
+#pragma unroll 1
+            for (int piece = 0; piece < PAGE / KT; ++piece) {
+                float sc[NB][4];
+#pragma unroll
+                for (int b = 0; b < NB; ++b) sc[b][0] = sc[b][1] = sc[b][2] = sc[b][3] = 0.f;
+                const int mine = CH * (g >> 1) + (g & 1);   // this lane's first key of the piece
+                const uint8_t *krow = kblk + (piece * KT + mine) * HD + t * (HD / 4);
+#pragma unroll
+                for (int x = 0; x < HD / 64; ++x) {   // steps outside, products inside: their sums do not wait on one another
+                    uint4 w[NB][2];
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) w[b][h] = *reinterpret_cast<const uint4 *>(krow + (4 * b + 2 * h) * HD + 16 * x);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            auto word = [&](const uint4 &y) { return k == 0 ? y.x : k == 1 ? y.y : k == 2 ? y.z : y.w; };
+                            uint32_t a[4];
+                            e4m3x4_f16(word(w[b][0]), a[0], a[2]);
+                            e4m3x4_f16(word(w[b][1]), a[1], a[3]);
+                            mma_f16(sc[b], a, q[8 * x + 2 * k], q[8 * x + 2 * k + 1]);
+                        }
+                }
+                if (piece == PAGE / KT - 1) {
+                    next();
+                    ++read;
+                }
+                const int live = left - piece * KT;   // keys of the piece that count
+                if (live < KT || edge) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int at = mine + 4 * b + 2 * (e >> 1), key = key0 + piece * KT + at;
+                            if (at >= live || (key >= p.sinks && key < from[e & 1])) sc[b][e] = -INFINITY;   // factors are positive
+                        }
+                }
+                // Online softmax, as in k_kv8_rows
+                float f[2], nr[2] = {r[0], r[1]}, nd[2] = {d[0], d[1]};
+                bool change = false;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    f[e] = factor(kf, qf[e]);
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) mx = fmaxf(mx, fmaxf(sc[b][e], sc[b][2 + e]));
+#pragma unroll
+                    for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+                    const float z = mx * f[e];
+                    const bool grow = r[e] == -INFINITY ? z > -INFINITY : z - r[e] > kLazy;
+                    const bool shift = z > -INFINITY && (v - d[e] > kUnitHigh || v - d[e] < kUnitLow);
+                    if (grow) nr[e] = ceilf(z);
+                    if (shift) nd[e] = fmaxf(v - kUnit, fmaxf(reach[e], d[e] + kReach) - (grow ? nr[e] - r[e] : 0.f) - kSpan);
+                    change |= grow || shift;
+                }
+                if (__any_sync(0xffffffffu, change)) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const bool grow = nr[e] != r[e];
+                        const float to = fmaxf(reach[e], d[e] + kReach) - (grow ? nr[e] - r[e] : 0.f);
+                        const float fl = grow ? ex2(r[e] - nr[e]) : 1.f, fo = fl * ex2(d[e] - nd[e]);
+                        __syncwarp();
+                        reach[e] = to;   // the lanes of a vector write the same
+                        __syncwarp();
+                        r[e] = nr[e];
+                        d[e] = nd[e];
+                        l[e] *= fl;
+#pragma unroll
+                        for (int n = 0; n < ND; ++n) {
+                            o[n][e] *= fo;
+                            o[n][2 + e] *= fo;
+                        }
+                    }
+                }
+                uint32_t w16[NB][2];   // the second product's operand
+                float off[2], sum[2] = {0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) off[e] = (v - d[e]) - (r[e] == -INFINITY ? 0.f : r[e]);
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float x = ex2(fmaf(sc[b][2 * h], f[0], off[0])), y = ex2(fmaf(sc[b][2 * h + 1], f[1], off[1]));
+                        sum[0] += x;
+                        sum[1] += y;
+                        w16[b][h] = turned(pack_f16(x, y));
+                    }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) l[e] += sum[e] * ex2(d[e] - v);
+                if (piece == 0) {   // V is the block behind K
+                    const int vs = PAGE / KT == 1 ? out_slot : out_slot + 1 == NS ? 0 : out_slot + 1;
+                    const uint32_t ph = PAGE / KT == 1 || out_slot + 1 < NS ? out_phase : out_phase ^ 1;
+                    ok = __all_sync(0xffffffffu, bar_wait(bars + vs * 8, ph, c.status, LA_KV8_TIMEOUT));
+                    if (!ok) break;
+                    vblk = my_ring + vs * Lay::block;
+                }
+                const uint8_t *col = vblk + g * PAGE + piece * KT + CH * t;
+                const int kept = min(max(live - CH * t, 0), CH);   // of this lane's bytes
+                constexpr int NG = 4;   // output groups in flight together
+                uint32_t odd = 0;       // an edge's bytes that are NaN
+#pragma unroll
+                for (int n0 = 0; n0 < ND; n0 += NG) {
+                    uint32_t w[NG][2][NB];
+#pragma unroll
+                    for (int n = 0; n < NG; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint8_t *at = col + (16 * (n0 + n) + 8 * h) * PAGE;
+                            if constexpr (NB == 4) {
+                                const uint4 x = *reinterpret_cast<const uint4 *>(at);
+                                w[n][h][0] = x.x, w[n][h][1] = x.y, w[n][h][2] = x.z, w[n][h][3] = x.w;
+                            } else {
+                                const uint2 x = *reinterpret_cast<const uint2 *>(at);
+                                w[n][h][0] = x.x, w[n][h][1] = x.y;
+                            }
+                        }
+                    if (live < KT) {   // bytes behind the last token may be anything
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            const int k = kept - 4 * b;
+                            const uint32_t mask = k >= 4 ? 0xffffffffu : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
+#pragma unroll
+                            for (int n = 0; n < NG; ++n) w[n][0][b] &= mask, w[n][1][b] &= mask;
+                        }
+                    }
+                    if (edge) {   // a NaN counts 0 here: a row that does not see it has a weight of 0
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+#pragma unroll
+                            for (int n = 0; n < NG; ++n)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const uint32_t nan = __vcmpeq4(w[n][h][b] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                    odd |= nan;
+                                    w[n][h][b] &= ~nan;
+                                }
+                    }
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int n = 0; n < NG; ++n) {
+                            uint32_t a[4];
+                            e4m3x4_f16(w[n][0][b], a[0], a[2]);
+                            e4m3x4_f16(w[n][1][b], a[1], a[3]);
+                            mma_f16(o[n0 + n], a, w16[b][0], w16[b][1]);
+                        }
+                }
+                if (edge && __any_sync(0xffffffffu, odd != 0)) {   // and is added for the rows that do
+#pragma unroll 1
+                    for (int j = 0; j < min(live, KT); ++j) {
+                        const int key = key0 + piece * KT + j;
+                        const uint8_t *at = vblk + g * PAGE + piece * KT + j;
+#pragma unroll
+                        for (int n = 0; n < ND; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if ((at[(16 * n + 8 * (e >> 1)) * PAGE] & 0x7f) == 0x7f && (key < p.sinks || key >= from[e & 1])) o[n][e] = NAN;
+                    }
+                }
+            }
+            if (!ok) break;
+            next();
+            ++read;
+        }
+        if (!ok) {   // void: wait (bounded) for what is still in flight
+            for (; read < issued; ++read) {
+                bar_wait(bars + out_slot * 8, out_phase, c.status, LA_KV8_TIMEOUT);
+                if (++out_slot == NS) {
+                    out_slot = 0;
+                    out_phase ^= 1;
+                }
+            }
+        }
+
+        // ---- join the warps at the largest r and d of those that saw a key, in warp order
+        __syncthreads();   // the rings are free
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int at = warp * kFewQ + 2 * t + e;
+#pragma unroll
+            for (int k = 4; k < 32; k <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], k);
+            if (g == 0) sh_ml[at] = make_float4(r[e], l[e] == 0.f ? -INFINITY : d[e], l[e], 0.f);
+#pragma unroll
+            for (int n = 0; n < ND; ++n) {
+                sh_o[at * (HD + 4) + 16 * n + g] = o[n][e];
+                sh_o[at * (HD + 4) + 16 * n + 8 + g] = o[n][2 + e];
+            }
+        }
+        __syncthreads();
+        const int slot = 2 * blockIdx.x + (u.begins ? 1 : 0);
+#pragma unroll 1
+        for (int i = tid; i < u.nqv * (HD / 4); i += 32 * NW) {
+            const int qi = i / (HD / 4), dim = 4 * (i % (HD / 4));
+            float R = -INFINITY, D = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float4 x = sh_ml[w * kFewQ + qi];
+                R = fmaxf(R, x.x);
+                D = fmaxf(D, x.y);
+            }
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float4 ml = sh_ml[w * kFewQ + qi];
+                if (ml.z == 0.f) continue;   // saw no key
+                const float fl = ex2(ml.x - R), fw = ex2((ml.x - R) + (ml.y - D));
+                const float4 x = *reinterpret_cast<const float4 *>(sh_o + (w * kFewQ + qi) * (HD + 4) + dim);
+                L += fl * ml.z;
+                acc.x += fw * x.x;
+                acc.y += fw * x.y;
+                acc.z += fw * x.z;
+                acc.w += fw * x.w;
+            }
+            if (u.all) {
+                const float inv = L == 0.f ? 0.f : ex2(D) / L;
+                const int qv = u.qv0 + qi;
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) + (sq.first + qv / p.gq) * p.a.out_stride + (head * p.gq + qv % p.gq) * HD + dim;
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+                *reinterpret_cast<uint2 *>(out) = make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+            } else {
+                *reinterpret_cast<float4 *>(p.part + (static_cast<long long>(slot) * kFewQ + qi) * HD + dim) = acc;
+                if (dim == 0) *reinterpret_cast<float4 *>(p.part_ml + (static_cast<long long>(slot) * kFewQ + qi) * 4) = make_float4(R, D, L, 0.f);
             }
         }
         fence_proxy_async_smem();   // these accesses before the next unit's bulk copies into the same bytes
@@ -2250,15 +2742,20 @@ static bool keep_whole(const Kv8Args &p, long long units, long long tiles, int c
     return tiles <= most && rounds * tiles - units * (tiles + p.unit_cost) / p.workers <= cost;
 }
 
-template <int HD, int PAGE, bool WIN>
+// FEW: k_kv8_few, of 8 query vectors a unit, else k_kv8_rows, of 16.
+template <int HD, int PAGE, bool WIN, bool FEW>
 static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
-    using Lay = Rows<HD, PAGE>;
+    using Lay = std::conditional_t<FEW, Few<HD, PAGE>, Rows<HD, PAGE>>;
+    const auto kernel = [] {
+        if constexpr (FEW) return k_kv8_few<HD, PAGE>;
+        else return k_kv8_rows<HD, PAGE, WIN>;
+    }();
     static_assert(Lay::per_sm <= kRowsPerSm, "workspace");
-    p.q_tile = kRowsQ;
-    p.q_log2 = 4;
+    p.q_tile = FEW ? kFewQ : kRowsQ;
+    p.q_log2 = FEW ? 3 : 4;
     p.k_tile = PAGE;
     p.k_log2 = p.page_log2;
-    static_assert(kRowsQ == 1 << 4, "shift");
+    static_assert(kRowsQ == 1 << 4 && kFewQ == 1 << 3, "shift");
     p.n_tile = 0;
     p.unit_cost = kRowsUnitCost;
     p.snap = p.unit_cost - 1;
@@ -2276,12 +2773,12 @@ static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     static std::atomic<unsigned long long> configured{0};
     unsigned long long bit = 0;
     if (attrs_needed(configured, &bit)) {
-        cudaError_t e = cudaFuncSetAttribute(k_kv8_rows<HD, PAGE, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(Lay::bytes(LA_KV8_MAX_SEQS)));
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
-    cudaError_t e = launch_k(k_kv8_rows<HD, PAGE, WIN>, dim3(p.workers), dim3(32 * Lay::warps), Lay::bytes(p.c.n_seqs), s, p);
+    cudaError_t e = launch_k(kernel, dim3(p.workers), dim3(32 * Lay::warps), Lay::bytes(p.c.n_seqs), s, p);
     if (e != cudaSuccess || p.whole) return e;
     if (p.workers < 2) return cudaSuccess;
     return launch_k(k_kv8_join<HD, 4>, dim3(p.workers - 1), dim3(kJoinThreads), 0, s, p);
@@ -2329,9 +2826,16 @@ constexpr int kFewVectors = 32;
 template <int HD, bool WIN>
 static cudaError_t attention_launch_hd(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     if (static_cast<long long>(p.a.max_rows) * p.gq > kFewVectors) return tiles_launch<HD, WIN>(p, nsm, ws, s);
-    if (p.c.page == 32) return rows_launch<HD, 32, WIN>(p, nsm, ws, s);
-    if (p.c.page == 64) return rows_launch<HD, 64, WIN>(p, nsm, ws, s);
-    return rows_launch<HD, 128, WIN>(p, nsm, ws, s);
+    if constexpr (WIN) {
+        if (static_cast<long long>(p.a.max_rows) * p.gq <= kFewQ) {
+            if (p.c.page == 32) return rows_launch<HD, 32, WIN, true>(p, nsm, ws, s);
+            if (p.c.page == 64) return rows_launch<HD, 64, WIN, true>(p, nsm, ws, s);
+            return rows_launch<HD, 128, WIN, true>(p, nsm, ws, s);
+        }
+    }
+    if (p.c.page == 32) return rows_launch<HD, 32, WIN, false>(p, nsm, ws, s);
+    if (p.c.page == 64) return rows_launch<HD, 64, WIN, false>(p, nsm, ws, s);
+    return rows_launch<HD, 128, WIN, false>(p, nsm, ws, s);
 }
 
 cudaError_t kv8_attention_launch(const la_kv8_cache &c, const la_kv8_attn &a, int window, int sinks, void *ws, int nsm, cudaStream_t s,

@@ -262,3 +262,42 @@ def test_pages_in_the_gap_are_not_read(lib):
     out = cache.attention(q, k, v, window=200, sinks=4)
     cache.status()
     close(out, *want)
+
+
+@pytest.mark.parametrize("hd,page,heads,kv,lens,rows,window,sinks", [
+    (64, 32, 8, 2, [300, 0, 33, 64, 700], [1, 1, 2, 0, 2], 50, 4), (64, 64, 8, 1, [2100, 5, 640], [1] * 3, 300, 1), (128, 32, 2, 1, [900, 31], [4, 3], 129, 40),
+    (64, 64, 3, 3, [70, 200], [8, 5], 6, 0), (128, 64, 2, 2, [1000], [8], 4, 900), (64, 128, 7, 1, [5000], [1], 3333, 0), (128, 128, 5, 1, [130, 128, 127, 1] * 9, [1] * 36, 100, 30),
+    (128, 64, 8, 1, [4000] * 20, [1] * 20, 1000, 4), (64, 32, 1, 1, [20000], [1], 15000, 64), (128, 64, 16, 2, list(range(0, 640, 5)), [1] * 128, 64, 2)])
+def test_few_vectors(lib, hd, page, heads, kv, lens, rows, window, sinks):
+    """Up to eight query vectors for each KV head and sequence, all pages and dims, with and without new keys."""
+    cache = build(lib, lens, hd, page, kv, seed=hd + page)
+    n = sum(rows)
+    q, k, v = normal((n, heads, hd), 1, 1.5), normal((n, kv, hd), 2), normal((n, kv, hd), 3)
+    hints = dict(max_rows=max(rows), max_len=max(lens))
+    out = cache.attention(q, k, v, row_start=starts(rows), window=window, sinks=sinks, **hints)
+    cache.status()
+    close(out, *model(cache, q, k, v, rows, window, sinks))
+    assert (out == cache.attention(q, k, v, row_start=starts(rows), window=window, sinks=sinks, **hints)).all()
+    alone = cache.attention(q, row_start=starts(rows), window=window, sinks=sinks, **hints)
+    cache.status()
+    close(alone, *model(cache, q, None, None, rows, window, sinks))
+
+
+def test_few_vectors_of_a_tree(lib):
+    """Rows of a small tree, whose ancestors count towards their windows; NaN in the keys and values that some do not see."""
+    import torch
+    rows, window, sinks = 7, 20, 3
+    see = [[0], [0, 1], [0, 2], [0, 1, 3], [0, 2, 4], [5], [0, 1, 3, 6]]
+    words = np.zeros((rows, 8), np.int32)
+    for r, seen in enumerate(see):
+        words[r, 0] = sum(1 << j for j in seen)
+    cache = build(lib, [90], 128, 32, 2, seed=6)
+    q, k, v = normal((rows, 2, 128), 1), normal((rows, 2, 128), 2), normal((rows, 2, 128), 3)
+    table = cache.table.cpu().numpy()
+    for place in (60, 71, 72, 73, 5):                          # windows begin at 71 .. 74
+        cache.v[0, int(table[0, place // 32]), 0, place, place % 32] = 0x7F
+    want, tol = model(cache, q, k, v, [rows], window, sinks, see=lambda s, r: see[r])
+    assert np.isnan(want).any() and not np.isnan(want).all()
+    out = cache.attention(q, k, v, row_start=starts([rows]), vis=torch.from_numpy(words).cuda(), window=window, sinks=sinks, max_rows=rows)
+    cache.status()
+    same(out, want, tol)
