@@ -236,28 +236,28 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
     // This part's warps turn its vectors, 32 words at a time
     uint4 *to = reinterpret_cast<uint4 *>(w4_smem) + wk * p.longest * NW * rows * 4;
     float *tf = reinterpret_cast<float *>(w4_smem + parts * p.longest * GROUP * rows * 2) + wk * p.longest * 8;
-    const int per = (j1 - j0) * LANES;   // words of a vector
-    for (int n = 0; n < rows; ++n) {
-        const __nv_bfloat16 *xs = p.x + n * p.x_stride + static_cast<long long>(j0) * GROUP;
-        constexpr int B = 4;             // in flight
+    const int per = (j1 - j0) * LANES, words = rows * per;   // 8 values each: of a vector, of all in a row
+    constexpr int B = 4;                                     // in flight
 #pragma unroll 1
-        for (int i0 = wm * 32; i0 < per; i0 += B * 32 * p.wm) {
-            uint4 x[B];
+    for (int f0 = wm * 32; f0 < words; f0 += B * 32 * p.wm) {
+        uint4 x[B];
+        int n[B], i[B];
 #pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const int i = i0 + b * 32 * p.wm + lane;
-                x[b] = i < per ? *reinterpret_cast<const uint4 *>(xs + 8 * i) : make_uint4(0, 0, 0, 0);
-            }
+        for (int b = 0; b < B; ++b) {
+            const int f = f0 + b * 32 * p.wm + lane;
+            n[b] = rows == 1 ? 0 : static_cast<int>(static_cast<unsigned>(f) / static_cast<unsigned>(per));
+            i[b] = f - n[b] * per;
+            x[b] = f < words ? *reinterpret_cast<const uint4 *>(p.x + n[b] * p.x_stride + static_cast<long long>(j0) * GROUP + 8 * i[b]) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const int i = i0 + b * 32 * p.wm + lane;
-                if (i - lane >= per) break;
-                uint4 y;
-                const int e = w4_operand<LANES>(x[b], y), j = i / LANES, li = i % LANES;
-                if (i < per) {
-                    to[((j * NW + li % NW) * rows + n) * 4 + li / NW] = y;
-                    if (li == 0) tf[j * 8 + n] = w4_power(-e);
-                }
+        for (int b = 0; b < B; ++b) {
+            const int f = f0 + b * 32 * p.wm + lane;
+            if (f - lane >= words) break;
+            uint4 y;
+            const int e = w4_operand<LANES>(x[b], y), j = i[b] / LANES, li = i[b] % LANES;
+            if (f < words) {
+                to[((j * NW + li % NW) * rows + n[b]) * 4 + li / NW] = y;
+                if (li == 0) tf[j * 8 + n[b]] = w4_power(-e);
             }
         }
     }

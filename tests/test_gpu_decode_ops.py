@@ -133,3 +133,22 @@ def test_steps_from_a_graph(lib):
     for x, y in zip(want, got):
         assert all(torch.equal(s, t) for s, t in zip(x, y))
     assert torch.equal(a.cache.lens, b.cache.lens)
+
+
+def test_two_models_at_once(lib):
+    """Steps of two models on two streams, none waiting for the other: the bits of the same steps one after another."""
+    import torch
+    shapes = [([63, 0, 30], 40, 4), ([700, 90], 300, 0)]
+    want = [[m.step() for _ in range(4)] for m in (Model(lib, *s) for s in shapes)]
+    models, streams = [Model(lib, *s) for s in shapes], [torch.cuda.Stream() for _ in shapes]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for m, stream, steps in zip(models, streams, got):
+            with torch.cuda.stream(stream):
+                steps.append(m.step())
+    torch.cuda.synchronize()
+    for m, w, g in zip(models, want, got):
+        m.cache.status()
+        for x, y in zip(w, g):
+            assert all(torch.equal(s, t) for s, t in zip(x, y))
