@@ -40,7 +40,8 @@ namespace la {
 
 constexpr int kW4Warps = 8, kW4Rows = 16;
 constexpr int kW4Block = 4;          // groups whose scales a quad's lanes load together: a pass of the loop
-constexpr int kW4Smem = 100 * 1024;  // most of a block
+constexpr int kW4Smem = 100 * 1024;  // most of a block; of three on an SM:
+constexpr int kW4SmemOf3 = 60 * 1024;   // more leaves the scales too little of the L1 cache (8 vectors of 28672 x 8192, groups of 64: 53 us with 66 KB, 38 so)
 // Blocks of k_gemv_w4 on an SM
 constexpr int w4_per_sm(int group, int mt) { return mt == 1 && group < 128 ? 3 : 2; }
 // Groups of 32: a lane's part of a group is 4 bytes, and loads of 4 bytes of 8
@@ -692,12 +693,11 @@ struct W4Plan {
     int64_t bytes;   // of workspace
 };
 
-// k_gemv_w4 up to 6 vectors, k_w4_tiles above (device us, k_gemv_w4 against
-// k_w4_tiles, groups of 128 (13824: 64): 4096 x 4096 1 vector 5.7 and 7.8, 8 vectors 10.1 and 8.2; 13824 x 5120 5 vectors
-// 15.2 and 15.4; 32000 x 4096 8 vectors 20.3 and 18.4; 8192 x 28672 1 vector 25.0 and
-// 28.3, 4 vectors 27.3 and 28.4, 8 vectors 30.9 and 28.6; groups of 32: 8192 x 28672 1 vector
-// 42.3, 7 vectors 53.6 by tiles).
-constexpr int kFewVectors = 6;
+// k_gemv_w4 up to 8 vectors, k_w4_tiles above.  Device us of 8 vectors, k_gemv_w4 against
+// k_w4_tiles, groups of 128: 512 x 512 3.7 and 4.9, 4096 x 4096 6.7 and 8.2, 13824 x 5120 12.5 and 15.2,
+// 32000 x 4096 19.4 and 19.2, 8192 x 28672 30.1 and 29.6; groups of 32: 4096 x 4096 9.3 and 9.8, 5120 x 13824
+// 20.9 and 24.9, 8192 x 28672 53.7 both.
+constexpr int kFewVectors = 8;
 
 W4Plan w4_plan(int rows, int out, int k, int group, int nsm) {
     W4Plan best{};
@@ -726,7 +726,7 @@ W4Plan w4_plan(int rows, int out, int k, int group, int nsm) {
             const int64_t smem = static_cast<int64_t>(parts) * ((groups + blocks * parts - 1) / (blocks * parts)) * (group * rows * 2 + 32);
             const int64_t rounds = (static_cast<int64_t>(count) * blocks + slots - 1) / slots;
             const double fill = static_cast<double>(count) * blocks / (static_cast<double>(rounds) * slots);
-            if (smem + w4_ring_bytes(group) > kW4Smem || parts > groups || fill <= most * 1.12) continue;
+            if (smem + w4_ring_bytes(group) > (w4_per_sm(group, f.mt) == 3 ? kW4SmemOf3 : kW4Smem) || parts > groups || fill <= most * 1.12) continue;
             idle = static_cast<int64_t>(count) * blocks * 2 <= slots;
             most = fill;
             best.mt = f.mt, best.wm = f.wm, best.blocks = blocks;
