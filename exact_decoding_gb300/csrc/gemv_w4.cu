@@ -23,9 +23,14 @@
 //
 // A block's warps share 16 * MT * wm outputs and 8 / wm parts of k, the blocks of
 // a cluster share k further; the parts are added in a fixed order, through
-// shared and distributed shared memory.  With many vectors or a long k
-// k_w4_operands makes the vectors' operand once for all blocks (MADE); else each
-// block makes its own in shared memory, which saves a launch.
+// shared and distributed shared memory.  Each block makes the vectors' operand for its
+// part of k in shared memory, which saves a launch; for more than 8 vectors, or a k
+// that does not fit, k_w4_operands makes it once for k_w4_tiles.
+//
+// Measured, groups of 128: 1 vector of 4096 x 4096 5.8 us (8.7 MB, latency), of 8192 x 28672
+// 24.9 us (119 MB at 4.8 TB/s; loads alone take 22.8 to 24), 16 vectors 31.0 us (4.0 TB/s:
+// the ALU pipe and the waits between a chunk's roles); 5 vectors of 13824 x 5120, groups of 64,
+// 13.8 us (2.8 TB/s, latency).
 #include <algorithm>
 #include <atomic>
 #include <cstdio>
@@ -41,7 +46,7 @@ namespace la {
 constexpr int kW4Warps = 8, kW4Rows = 16;
 constexpr int kW4Block = 4;          // groups whose scales a quad's lanes load together: a pass of the loop
 constexpr int kW4Smem = 100 * 1024;  // most of a block; of three on an SM:
-constexpr int kW4SmemOf3 = 60 * 1024;   // more leaves the scales too little of the L1 cache (8 vectors of 28672 x 8192, groups of 64: 53 us with 66 KB, 38 so)
+constexpr int kW4SmemOf3 = 60 * 1024;   // more leaves the scales too little of the L1 cache (8 vectors of 28672 x 8192, groups of 64: 53 us with 66 KB, 42 so)
 // Blocks of k_gemv_w4 on an SM
 constexpr int w4_per_sm(int group, int mt) { return mt == 1 && group < 128 ? 3 : 2; }
 // Groups of 32: a lane's part of a group is 4 bytes, and loads of 4 bytes of 8

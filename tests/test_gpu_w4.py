@@ -181,3 +181,33 @@ def test_sums_keep_their_bits(lib, rows, out, k, group):
     want = x.double() @ (q.double() * s.double().repeat_interleave(group, 1)).T
     got = lib.W4Matrix((w[:, ::2] | w[:, 1::2] << 4).cuda(), s.cuda()).matvec(x.cuda()).cpu().double()
     assert (got - want).norm() <= 2.0 ** -21 * want.norm()
+
+
+def test_two_graphs_with_workspaces(lib):
+    """Calls of many rows in two captured graphs, replayed in turn and on two streams at once: each has a workspace of its own."""
+    import torch
+    cases = [case(16, 700, 2048, 128, seed=1), case(40, 900, 1024, 64, seed=2)]
+    assert all(lib.la_gemv_w4_workspace(x.shape[0], w.shape[0], x.shape[1], 2 * w.shape[1] // s.shape[1]) > 0 for x, w, s, _, _ in cases)
+    matrices = [lib.W4Matrix(w, s) for _, w, s, _, _ in cases]
+    want = [m.matvec(c[0]) for m, c in zip(matrices, cases)]
+    torch.cuda.synchronize()
+    inputs, graphs, outs = [torch.zeros_like(c[0]) for c in cases], [], []
+    for m, x in zip(matrices, inputs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(m.matvec(x))
+    for x, c in zip(inputs, cases):
+        x.copy_(c[0])
+    for g in (0, 1, 1, 0):
+        graphs[g].replay()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(5):
+        for g, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                g.replay()
+    torch.cuda.synchronize()
+    for out, w, c in zip(outs, want, cases):
+        assert torch.equal(out, w)
+        close(out, c[3], c[4])
+    lib.la_gemm_status()
