@@ -241,13 +241,12 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) k_logprobs(const __gri
     };
     LpKey list = 0;            // the lane's of the warp's best so far
     LpKey limit = 0;           // what may enter is above it
-    float below = -INFINITY;   // and its value above this
+    float least = -3.40282347e38f;   // and its value this or more: an equal one may enter, by its index
     volatile int *gathered = &sh_n[warp];
     volatile LpKey *threshold = &sh_t;
     auto raise = [&](LpKey t) {
         limit = max(limit, t);
-        const uint32_t hi = static_cast<uint32_t>(limit >> 32);
-        below = hi > 0x00800000u ? lp_value(static_cast<LpKey>(hi - 1) << 32) : -INFINITY;   // above -FLT_MAX: the next float down
+        least = lp_value(limit);
     };
     auto push = [&](float x, int i) {
         const LpKey k = lp_key(x, i);
@@ -326,19 +325,19 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) k_logprobs(const __gri
                 } else if (top == 1) {
                     lo = hi;
                 }
-                raise(lo ? (static_cast<LpKey>(lo) << 32) - 1 : 0);
+                if (lo) raise((static_cast<LpKey>(lo) << 32) - 1);
             } else {
                 const LpKey t = *threshold;
                 if (t > limit) raise(t);
             }
-            if (__any_sync(0xffffffffu, most > below)) {
+            if (__any_sync(0xffffffffu, most >= least)) {
                 const int first = head + (base + tid) * VEC;
 #pragma unroll
                 for (int q = 0; q < E / 4; ++q) {
-                    if (quad[q] > below) {
+                    if (quad[q] >= least) {
 #pragma unroll
                         for (int e = 4 * q; e < 4 * q + 4; ++e)
-                            if (v[e] > below) push(v[e], first + e / VEC * THREADS * VEC + e % VEC);
+                            if (v[e] >= least) push(v[e], first + e / VEC * THREADS * VEC + e % VEC);
                     }
                     if (q & 1) {
                         __syncwarp();

@@ -219,3 +219,35 @@ def test_long_rows_in_parts(lib, rows, vocab):
     some = [0, rows // 2, rows - 1]
     want, tols = model(z[some].cpu().double().numpy(), np.zeros((3, 0), np.int32), 32)
     agree([z.new_zeros(3, 0), got[1][some], got[2][some], got[3][some]], want, tols)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("top", [1, 5, 32])
+@pytest.mark.parametrize("rows,vocab,warps", [(160, 20000, 8), (1200, 20000, 4), (1300, 2500, 2)])
+def test_zeros_that_tie_behind_the_first_pass(lib, dtype, top, rows, vocab, warps):
+    """Zeros of both signs as a row's best, none of them in the first pass of a block's warps: the lowest indices whatever
+    warp is ahead.  In each row one warp has more to sort in the first pass, so that it comes late to the lowest zeros, and
+    the others have many."""
+    import torch
+    vec, lanes = 128 // torch.finfo(getattr(torch, dtype)).bits, 32
+    first = 16 * lanes * warps                                # elements of a pass: 16 of each thread, `vec` at a time
+    g = torch.Generator().manual_seed(top + warps)
+    z = -10 - torch.rand(rows, vocab, generator=g)
+    zero = torch.zeros(rows, vocab, dtype=torch.bool)
+    index = torch.arange(vocab)
+    owner, part = index // vec // lanes % warps, index // vec // (lanes * warps) % (16 // vec)
+    for r in range(rows):
+        late = warps - 1 - r % min(warps, 4) if warps > 1 else 0
+        busy = (index < first) & (owner == late)
+        z[r, busy] = torch.linspace(-1, -0.9, int(busy.sum()))
+        few = (index >= first) & (index < 2 * first) & (owner == late) & (part == 0)
+        zero[r] = few & (torch.rand(vocab, generator=g) < 0.05) | (index >= first) & (part > 0) & (owner != late) & (torch.rand(vocab, generator=g) < 0.5)
+    signs = torch.where(torch.rand(rows, vocab, generator=g) < 0.5, 0.0, -0.0)
+    z = torch.where(zero, signs, z).to(getattr(torch, dtype))
+    assert int(zero.sum(1).min()) >= 32
+    want = torch.where(zero, index, vocab).sort(1).values[:, :top].int()
+    z = z.cuda()
+    for _ in range(5):
+        ids = lib.logprobs(z, top=top)[2].cpu()
+        wrong = (ids != want).any(1)
+        assert not wrong.any(), f"{int(wrong.sum())} of {rows} rows, the first {int(wrong.nonzero()[0])}: {ids[wrong][0].tolist()} for {want[wrong][0].tolist()}"
