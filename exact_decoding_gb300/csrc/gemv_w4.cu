@@ -11,8 +11,10 @@
 // 2-norm, as the tensor cores add with few bits below their largest term; so by
 // 9e-8.)  The vectors come as fp16, each group of a vector times
 // a power of two that brings its largest value to 2^14 .. 2^15: 11 bits hold bf16's 8, and what is
-// too small for them is below 2^-39 of the largest.  A group's sum is multiplied
-// by the vector's power and by its scale once, in fp32.
+// too small for them is below 2^-39 of the largest.  A group's sum, in fp32, is multiplied
+// by one number, the vector's power times the scale.  That is exact where the largest value
+// times the scale is 2^-127 or more, and infinite only where it is above 2^141 (the sum times
+// the power alone is infinite for x near 2^127, whatever the scale).
 //
 // The weights are the A operand of mma.m16n8k16 (16 outputs), the vectors its B
 // operand (8 vectors).  A product is a sum over k, so any order of k will do as
@@ -338,8 +340,8 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const uint64_t xf2 = w4_two(xf[n].x, xf[n].y);
-                        acc[m][n][0] = w4_fma2(w4_mul2(w4_two(d[m][n][0], d[m][n][1]), xf2), w4_two(fa, fa), acc[m][n][0]);
-                        acc[m][n][1] = w4_fma2(w4_mul2(w4_two(d[m][n][2], d[m][n][3]), xf2), w4_two(fb, fb), acc[m][n][1]);
+                        acc[m][n][0] = w4_fma2(w4_two(d[m][n][0], d[m][n][1]), w4_mul2(xf2, w4_two(fa, fa)), acc[m][n][0]);
+                        acc[m][n][1] = w4_fma2(w4_two(d[m][n][2], d[m][n][3]), w4_mul2(xf2, w4_two(fb, fb)), acc[m][n][1]);
                     }
                 }
             }
@@ -612,8 +614,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_w4_tiles(const __grid_const
                 for (int n = 0; n < 2 * NT; ++n) {
                     const ulonglong2 e = reinterpret_cast<const ulonglong2 *>(table + u * 64)[n];
                     const uint64_t x = w4_two(__uint_as_float(v[4 * n]), __uint_as_float(v[4 * n + 1])), y = w4_two(__uint_as_float(v[4 * n + 2]), __uint_as_float(v[4 * n + 3]));
-                    sums[2 * n] = w4_fma2(w4_mul2(x, e.x), f2, sums[2 * n]);
-                    sums[2 * n + 1] = w4_fma2(w4_mul2(y, e.y), f2, sums[2 * n + 1]);
+                    sums[2 * n] = w4_fma2(x, w4_mul2(e.x, f2), sums[2 * n]);
+                    sums[2 * n + 1] = w4_fma2(y, w4_mul2(e.y, f2), sums[2 * n + 1]);
                 }
             }
             tc_fence_before();

@@ -326,7 +326,10 @@ int la_gemm_bf16_noalloc(const void *x, const void *w, float *y, int32_t rows, i
  * matrix is read once for every 16 rows, so it is for a batch of single tokens.
  * x is exact to 2^-39 of the largest value of its group (of one row), the
  * products' sums are fp32, and a group's sum meets its scale once; results are
- * deterministic.  A row with a value that is not finite is not finite at all.
+ * deterministic.  They are finite where x is and the results, and each group's
+ * largest x times its scale, are within fp32's range (where that product is
+ * below 2^-127 a group loses bits).  A row with a value that is not finite is
+ * not finite at all.
  * Calls of many rows need a workspace: la_gemv_w4_workspace says how many bytes
  * on the current device (0: none), 16-byte aligned device memory with any
  * contents; calls that overlap need one each.  Asynchronous: a bounded wait that

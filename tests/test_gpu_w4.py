@@ -211,3 +211,40 @@ def test_two_graphs_with_workspaces(lib):
         assert torch.equal(out, w)
         close(out, c[3], c[4])
     lib.la_gemm_status()
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("rows", [1, 8, 9, 17])
+@pytest.mark.parametrize("x_least,x_most,s_least,s_most", [(110, 127, -60, -24), (-133, -126, 20, 60), (100, 127, -126, -100), (-120, -100, 80, 100)])
+def test_extreme_values(lib, group, rows, x_least, x_most, s_least, s_most):
+    """bf16's largest and smallest values with scales that bring the results back: every group to the bits of its own size,
+    though its sum before the scale may be far outside fp32's range.  Tolerance: as in case(), of these rows alone."""
+    import torch
+    g = np.random.default_rng(rows + group)
+    k, out = 8 * group, 50
+    x = g.choice([-1.0, 1.0], (rows, k)) * 2.0 ** g.integers(x_least, x_most + 1, (rows, k)) * (1 if x_least < -126 else g.integers(128, 256, (rows, k)) / 128)
+    x = torch.from_numpy(x).to(torch.bfloat16)
+    q = g.integers(0, 16, (out, k), dtype=np.uint8)
+    q[0], q[1] = 0, np.where(x[0].double().numpy() > 0, 15, 0)          # sums that nothing takes back
+    s = torch.from_numpy(2.0 ** g.integers(s_least, s_most + 1, (out, k // group)).astype(np.float64)).to(torch.bfloat16)
+    w = torch.from_numpy(q[:, ::2] | (q[:, 1::2] << 4))
+    m = (q.astype(np.float64) - 8) * np.repeat(s.double().numpy(), group, 1)
+    xd = x.double().numpy()
+    assert np.isfinite(xd).all()
+    size = np.abs(xd) @ np.repeat(s.double().numpy(), group, 1).T
+    tol = 23 * size * (group / 16 * 17 * 2.0 ** -23 + (group + 8) * 2.0 ** -24) + np.abs(xd) @ np.abs(m).T * (k // group + 68) * 2.0 ** -24
+    close(lib.W4Matrix(w.cuda(), s.cuda()).matvec(x.cuda()), xd @ m.T, tol)
+
+
+def test_one_large_value(lib):
+    """x = 2^126 times -8: infinity before its scale of 2^-7, -2^122 behind it; groups of opposite sign take each other back."""
+    import torch
+    for rows in (1, 16):
+        x = torch.zeros(rows, 256, dtype=torch.bfloat16, device="cuda")
+        x[:, 5], x[:, 133] = 2.0 ** 126, -2.0 ** 126
+        w = torch.full((2, 128), 0x88, dtype=torch.uint8, device="cuda")
+        w[:, 2] = 0x08                                       # column 5: 0, column 4: 8
+        w[1, 66] = 0x08                                      # column 133 likewise
+        s = torch.full((2, 2), 2.0 ** -7, dtype=torch.bfloat16, device="cuda")
+        y = lib.W4Matrix(w, s).matvec(x)
+        assert torch.all(y[:, 0] == -2.0 ** 122) and torch.all(y[:, 1] == 0)
