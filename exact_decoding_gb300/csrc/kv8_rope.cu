@@ -33,6 +33,9 @@ namespace la {
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeRows = 16;   // most rows of a block
+// Means of squares (with eps) between these are sums of fp32 squares that lose nothing: HD of
+// them stay below 2^127, and a square that is not a normal number is below 2^-26 of them all.
+constexpr float kLeastMean = 7.888609052210118e-31f, kMostMean = 1.329227995784916e36f;   // 2^-100, 2^120
 
 struct RopeArgs {
     la_kv8_qkv a;
@@ -91,6 +94,9 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
     }
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+// 2^-e for x >= 0 in 2^e .. 2^(e + 1), within fp32's normal numbers
+__device__ __forceinline__ float power_below(float x) { return __uint_as_float(min(max(254 - static_cast<int>(__float_as_uint(x) >> 23), 1), 254) << 23); }
 
 template <int HD, typename T>
 __global__ void __launch_bounds__(kRopeThreads, 5) k_kv8_norm_rope(const __grid_constant__ RopeArgs p) {
@@ -204,7 +210,33 @@ __global__ void __launch_bounds__(kRopeThreads, 5) k_kv8_norm_rope(const __grid_
                     const unsigned lanes = (L == 8 ? 0xffu : 0xfu) << (tid & 31 & ~(L - 1));
 #pragma unroll
                     for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(lanes, sum, o);
-                    const float n = rsqrtf(sum * (1.f / HD) + a.eps);
+                    float mean = sum * (1.f / HD) + a.eps;
+                    if (!(mean > kLeastMean && mean < kMostMean)) {
+                        // The squares leave fp32's range: all by a power of two that brings the
+                        // largest value, or the root of eps, near 1.  (A NaN or infinity stays one.)
+                        float top = 0.f;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const float2 u = one_by_one(x2[c]), v = one_by_one(y2[c]);
+                            top = fmaxf(fmaxf(top, fmaxf(fabsf(u.x), fabsf(u.y))), fmaxf(fabsf(v.x), fabsf(v.y)));
+                        }
+#pragma unroll
+                        for (int o = 1; o < L; o <<= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, o));
+                        const float f = power_below(fmaxf(top, sqrtf(a.eps)));
+                        const uint64_t f2 = two(f, f);
+                        sum = 0.f;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            x2[c] = mul2(x2[c], f2);
+                            y2[c] = mul2(y2[c], f2);
+                            const float2 s = one_by_one(fma2(x2[c], x2[c], mul2(y2[c], y2[c])));
+                            sum += s.x + s.y;
+                        }
+#pragma unroll
+                        for (int o = 1; o < L; o <<= 1) sum += __shfl_xor_sync(lanes, sum, o);
+                        mean = sum * (1.f / HD) + a.eps * f * f;
+                    }
+                    const float n = rsqrtf(mean);
                     const uint64_t n2 = two(n, n);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {

@@ -196,3 +196,23 @@ def test_far_positions(lib, base):
         xd = np.abs(q[r:r + 1].cpu().double().numpy())
         off = 2.0 ** -26 if abs(p) <= 2 ** 20 else 2.0 ** -23
         close(qo[r:r + 1], y, tol + 2 * math.pi * off * np.concatenate([xd[..., :64] + xd[..., 64:]] * 2, -1))
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("eps", [0.0, 1e-5, 1e30])
+def test_heads_whose_squares_leave_fp32(lib, dtype, hd, eps):
+    """Heads near 2^-120 .. 2^120: the mean of their squares is 0 or infinity in fp32, their norm is not."""
+    import torch
+    c = cache(lib, 1, 2, hd, [11])
+    q, k, _ = rows_of(9, 4, 2, hd, torch.float32, seed=8)
+    size = torch.tensor([2.0 ** e for e in (-120, -80, -65, -50, 0, 60, 64, 90, 120)], device="cuda")
+    q, k = ((x * size[:, None, None]).to(getattr(torch, dtype)).contiguous() for x in (q, k))
+    q[:, 1, 3:] *= 2.0 ** -6                                  # one large value
+    w = (1 + torch.rand(hd, generator=torch.Generator().manual_seed(2))).cuda()
+    pos = 11 + np.arange(9)
+    qo, ko = c.norm_rope(q, k, q_weight=w, k_weight=w, eps=eps, row_start=ints([0, 9]))
+    c.status()
+    eps = float(np.float32(eps))
+    close(qo, *formula(q, w, pos, eps, frequencies(10000.0, hd)))
+    close(ko, *formula(k, w, pos, eps, frequencies(10000.0, hd)))
