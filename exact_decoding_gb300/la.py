@@ -746,6 +746,8 @@ class Kv8Cache:
         if window == 0 and sinks == 0:
             self._call(self._fn["la_kv8_attention"], "la_kv8_attention", args, ws, wb, stream=stream)
         else:
+            if abs(window) >> 31 or abs(sinks) >> 31:   # ctypes would cut them
+                raise ValueError(f"window must be 1 .. 2^30 and sinks 0 .. 2^30, not {window} and {sinks}")
             self._call(self._fn["la_kv8_attention_window"], "la_kv8_attention_window", args, window, sinks, ws, wb, stream=stream)
         return out
 

@@ -301,3 +301,13 @@ def test_few_vectors_of_a_tree(lib):
     out = cache.attention(q, k, v, row_start=starts([rows]), vis=torch.from_numpy(words).cuda(), window=window, sinks=sinks, max_rows=rows)
     cache.status()
     same(out, want, tol)
+
+
+@pytest.mark.parametrize("window,sinks", [(2 ** 32 + 8, 0), (2 ** 32, 4), (8, 2 ** 32), (8, -2 ** 32), (-2 ** 32 + 8, 0)])
+def test_numbers_of_more_than_32_bits(lib, window, sinks):
+    """Refused, not cut to their low 32 bits."""
+    import torch
+    c = lib.Kv8Cache(1, 4, 64, 2, 128, 1, 4)
+    q = torch.zeros(1, 4, 128, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises((ValueError, lib.LaError), match="window"):
+        c.attention(q, window=window, sinks=sinks)
