@@ -2764,9 +2764,18 @@ static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     // tiles 17.7 against 19.7, 32 tiles 24.4 against 22.5; 48 sequences, head_dim
     // 64, 4 KV heads, pages of 32, 16 tiles 10.7 against 13.5, 47 tiles 19.6
     // against 16.4.
+    // k_kv8_few counts tokens: its six warps take pages of any size at about the same rate.
+    // Whole against split, windows of 512, 1024 and 2048: one row of 64 heads over 8 KV heads, pages
+    // of 64 8.9, 11.3, 16.4 against 11.1, 11.4, 11.6, pages of 128 9.2, 11.7, 15.7 against 12.0, 12.1,
+    // 12.5; of 32 heads over 4, pages of 32 9.3, 13.1, 20.8 against 10.5, 11.2, 11.5; 16 sequences, pages of
+    // 64 10.8, 13.6, 20.3 against 14.8, 16.6, 19.6; 64 of them 22.0, 33.0, 51.6 against 26.9, 37.3,
+    // 55.7; 48, head_dim 64, 4 KV heads, pages of 32 9.2, 12.8, 19.2 against 14.5, 17.0, 20.5.  A window
+    // of 4096, different lengths: 64 sequences 76.2 against 77.8, 32 with pages of 128 53.6 against
+    // 51.0.  A unit_cost of 8 or 22 does neither better nor worse than 14.
+    constexpr int kCost = FEW ? 896 / PAGE : 8, kMost = FEW ? 2304 / PAGE : 32;
     const long long tiles = (p.a.max_len + PAGE - 1) / PAGE;
     p.workers = nsm * Lay::per_sm;
-    if (keep_whole(p, unit_bound(p), tiles, 8, 32)) p.whole = 1, p.workers = static_cast<int>(std::min<long long>(unit_bound(p), 1 << 20));
+    if (keep_whole(p, unit_bound(p), tiles, kCost, kMost)) p.whole = 1, p.workers = static_cast<int>(std::min<long long>(unit_bound(p), 1 << 20));
     p.part = static_cast<float *>(ws);
     p.part_ml = p.part + static_cast<long long>(nsm) * kRowsPerSm * 2 * kRowsQ * HD;
     p.split = reinterpret_cast<Kv8Split *>(p.part_ml + static_cast<long long>(nsm) * kRowsPerSm * 2 * kRowsQ * 4);

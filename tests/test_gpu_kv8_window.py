@@ -311,3 +311,18 @@ def test_numbers_of_more_than_32_bits(lib, window, sinks):
     q = torch.zeros(1, 4, 128, dtype=torch.bfloat16, device="cuda")
     with pytest.raises((ValueError, lib.LaError), match="window"):
         c.attention(q, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("hd,page,heads,kv,lens,window,sinks", [
+    (64, 32, 8, 4, [3000, 1801, 40, 0] + [100 * i for i in range(1, 29)], 1800, 4), (128, 64, 8, 2, [2000, 5, 700, 1500], 750, 0), (128, 64, 8, 2, [2000, 5, 700], 1000, 70),
+    (128, 128, 4, 4, [1100] * 3, 700, 130), (128, 32, 5, 5, [400, 1000], 600, 1)])
+def test_units_of_some_pages(lib, hd, page, heads, kv, lens, window, sinks):
+    """Single rows whose windows are long enough to be split among blocks, and few or short enough to stay whole, with each bound on the lengths."""
+    cache = build(lib, lens, hd, page, kv, seed=heads)
+    n = len(lens)
+    q, k, v = normal((n, heads, hd), 1, 1.5), normal((n, kv, hd), 2), normal((n, kv, hd), 3)
+    want = model(cache, q, k, v, [1] * n, window, sinks)
+    for most in (0, max(lens), 64):
+        out = cache.attention(q, k, v, max_len=most, window=window, sinks=sinks)
+        cache.status()
+        close(out, *want)
