@@ -167,7 +167,6 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
     constexpr int NW = GROUP / 32;             // words of a lane, of each output's group
     constexpr int LANES = GROUP / 8;           // lanes that turn a group of a vector
     constexpr int AHEAD = MT == 2 ? 2 : 4;     // groups on their way
-    constexpr int NT = 1;                      // tiles of 8 vectors
     constexpr int LD = 20;                     // of the sums in shared memory: lanes write different banks
     extern __shared__ __align__(128) uint8_t w4_smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -272,10 +271,8 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
     __syncthreads();
     const uint4 *bx = to + t;
     const float2 *bf = reinterpret_cast<const float2 *>(tf) + t;
-    int at[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) at[n] = min(8 * n + g, rows - 1) * 4;   // past the last vector: it again
-    uint64_t acc[MT][NT][2] = {};   // pairs of sums
+    const int at = min(g, rows - 1) * 4;   // past the last vector: it again
+    uint64_t acc[MT][2] = {};   // pairs of sums
     const int n_groups = j1 - j0;
     int slot = 0;
 #pragma unroll 1
@@ -307,42 +304,32 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
 #pragma unroll
             for (int u = 0; u < kW4Block; ++u) {
                 if (u >= now) break;
-                float d[MT][NT][4];
-                float2 xf[NT];
+                float d[MT][4];
                 if constexpr (RING) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) a[0][0][h][0] = *reinterpret_cast<const uint32_t *>(from + h * (8 * ROW) + u * (GROUP / 2));
                 }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) xf[n] = bf[u * 4];
+                const float2 xf = bf[u * 4];
 #pragma unroll
                 for (int i = 0; i < NW; ++i) {
-                    uint4 v[NT];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) v[n] = bx[(u * NW + i) * rows * 4 + at[n]];
+                    const uint4 v = bx[(u * NW + i) * rows * 4 + at];
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
                         const uint32_t x = a[RING ? 0 : u % AHEAD][m][0][i], y = a[RING ? 0 : u % AHEAD][m][1][i], x8 = x >> 8, y8 = y >> 8;
                         const uint32_t xl = w4_low(x), yl = w4_low(y), xh = w4_high(x), yh = w4_high(y), xl8 = w4_low(x8), yl8 = w4_low(y8), xh8 = w4_high(x8), yh8 = w4_high(y8);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            float (&to)[4] = d[m][n];
-                            if (i == 0) mma_f16(to, {0.f, 0.f, 0.f, 0.f}, xl, yl, xh, yh, v[n].x, v[n].y);
-                            else mma_f16(to, to, xl, yl, xh, yh, v[n].x, v[n].y);
-                            mma_f16(to, to, xl8, yl8, xh8, yh8, v[n].z, v[n].w);
-                        }
+                        float (&to)[4] = d[m];
+                        if (i == 0) mma_f16(to, {0.f, 0.f, 0.f, 0.f}, xl, yl, xh, yh, v.x, v.y);
+                        else mma_f16(to, to, xl, yl, xh, yh, v.x, v.y);
+                        mma_f16(to, to, xl8, yl8, xh8, yh8, v.z, v.w);
                     }
                 }
                 if constexpr (!RING) load(u + AHEAD, u % AHEAD);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     const float fa = __shfl_sync(0xffffffffu, f[m][0][pass], u, 4), fb = __shfl_sync(0xffffffffu, f[m][1][pass], u, 4);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const uint64_t xf2 = w4_two(xf[n].x, xf[n].y);
-                        acc[m][n][0] = w4_fma2(w4_two(d[m][n][0], d[m][n][1]), w4_mul2(xf2, w4_two(fa, fa)), acc[m][n][0]);
-                        acc[m][n][1] = w4_fma2(w4_two(d[m][n][2], d[m][n][3]), w4_mul2(xf2, w4_two(fb, fb)), acc[m][n][1]);
-                    }
+                    const uint64_t xf2 = w4_two(xf.x, xf.y);
+                    acc[m][0] = w4_fma2(w4_two(d[m][0], d[m][1]), w4_mul2(xf2, w4_two(fa, fa)), acc[m][0]);
+                    acc[m][1] = w4_fma2(w4_two(d[m][2], d[m][3]), w4_mul2(xf2, w4_two(fb, fb)), acc[m][1]);
                 }
             }
             left -= kW4Block;
@@ -359,16 +346,14 @@ __global__ void __launch_bounds__(32 * kW4Warps, w4_per_sm(GROUP, MT)) k_gemv_w4
     // The parts of k of this block, then those of the cluster's blocks
     __syncthreads();
     float *sh = reinterpret_cast<float *>(w4_smem);   // [warp][m][vector][LD]
-    auto place = [&](int wp, int o, int n) { return ((wp * MT + o / 16) * (NT * 8) + n) * LD + o % 16; };
+    auto place = [&](int wp, int o, int n) { return ((wp * MT + o / 16) * 8 + n) * LD + o % 16; };
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                sh[place(warp, 16 * m + g + 8 * h, 8 * n + 2 * t)] = __uint_as_float(static_cast<uint32_t>(acc[m][n][h]));
-                sh[place(warp, 16 * m + g + 8 * h, 8 * n + 2 * t + 1)] = __uint_as_float(static_cast<uint32_t>(acc[m][n][h] >> 32));
-            }
+        for (int h = 0; h < 2; ++h) {
+            sh[place(warp, 16 * m + g + 8 * h, 2 * t)] = __uint_as_float(static_cast<uint32_t>(acc[m][h]));
+            sh[place(warp, 16 * m + g + 8 * h, 2 * t + 1)] = __uint_as_float(static_cast<uint32_t>(acc[m][h] >> 32));
+        }
     __syncthreads();
     constexpr int OW = 16 * MT;   // outputs of a warp
     const int items = outs * rows, log = 31 - __clz(outs);

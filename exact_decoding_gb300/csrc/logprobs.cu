@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(32 * WARPS, 32 / WARPS) k_logprobs(const __gri
         if (base + THREADS * NV > v1) {
 #pragma unroll
             for (int k = 0; k < NV; ++k)
-                if (base + k * THREADS + tid >= v1) sh_ring[stage][k][tid] = w[k] = make_uint4(kNone, kNone, kNone, kNone);
+                if (base + k * THREADS + tid >= v1) w[k] = make_uint4(kNone, kNone, kNone, kNone);
         }
         float v[E];
 #pragma unroll
