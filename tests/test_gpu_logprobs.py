@@ -251,3 +251,16 @@ def test_zeros_that_tie_behind_the_first_pass(lib, dtype, top, rows, vocab, warp
         ids = lib.logprobs(z, top=top)[2].cpu()
         wrong = (ids != want).any(1)
         assert not wrong.any(), f"{int(wrong.sum())} of {rows} rows, the first {int(wrong.nonzero()[0])}: {ids[wrong][0].tolist()} for {want[wrong][0].tolist()}"
+
+
+def test_more_logits_than_31_bits_count(lib):
+    """The last of 2^31 + 2^18 logits, bf16, in rows at a stride: rows at both ends of it as by themselves."""
+    import torch
+    rows, vocab, stride = 8194, 262000, 262144
+    z = torch.full((rows, stride), -3.0, dtype=torch.bfloat16, device="cuda")[:, :vocab]
+    some = [0, 4097, rows - 2, rows - 1]
+    z[some] = logits(4, vocab, "bfloat16", 9)
+    tokens = torch.full((rows, 1), vocab - 1, dtype=torch.int32, device="cuda")
+    got = lib.logprobs(z, tokens, top=8)
+    agree([x[some] for x in got], *model(z[some].cpu().double().numpy(), tokens[some].cpu().numpy(), 8))
+    assert torch.all(got[2][1:4097] == torch.arange(8, device="cuda", dtype=torch.int32))

@@ -248,3 +248,40 @@ def test_one_large_value(lib):
         s = torch.full((2, 2), 2.0 ** -7, dtype=torch.bfloat16, device="cuda")
         y = lib.W4Matrix(w, s).matvec(x)
         assert torch.all(y[:, 0] == -2.0 ** 122) and torch.all(y[:, 1] == 0)
+
+
+def test_a_stride_that_is_refused(lib):
+    """Rows 300 apart: no multiple of 8."""
+    import torch
+    x, w, s, _, _ = case(6, 70, 256, 64)
+    wide = torch.zeros(6, 300, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(lib.LaError, match="x_stride"):
+        lib.W4Matrix(w, s).matvec(wide[:, 8:264])
+
+
+@pytest.mark.parametrize("rows,out,k,group", [(41, 200, 512, 64), (64, 129, 1024, 128), (100, 70, 4160, 64), (121, 500, 2048, 128), (129, 33, 96, 32), (255, 140, 640, 128)])
+def test_rows_between(lib, rows, out, k, group):
+    """A step's rows and other numbers between 40 and 256, ragged in the last sixteen."""
+    x, w, s, y, tol = case(rows, out, k, group, seed=rows)
+    close(lib.W4Matrix(w, s).matvec(x), y, tol)
+    lib.la_gemm_status()
+
+
+@pytest.mark.parametrize("rows", [1, 16])
+def test_more_bytes_than_31_bits_count(lib, rows):
+    """A matrix of 2.2 GB: its first, middle and last outputs against the same rows as a matrix of their own."""
+    import torch
+    out, k, group = 131100, 32768, 128
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.randint(0, 256, (out, k // 2), dtype=torch.uint8, device="cuda", generator=g)
+    s = (torch.rand(out, k // group, device="cuda", generator=g) * 0.01).to(torch.bfloat16)
+    x = torch.randn(rows, k, device="cuda", generator=g).to(torch.bfloat16)
+    assert w.numel() > 1 << 31
+    got = lib.W4Matrix(w, s).matvec(x)
+    xd = x.double()
+    for a in (0, 65500, out - 60):
+        part, scales = w[a:a + 60], s[a:a + 60].double().repeat_interleave(group, 1)
+        q = torch.stack([part & 15, part >> 4], 2).view(60, k).double() - 8
+        want, size = xd @ (q * scales).T, xd.abs() @ scales.T
+        assert torch.all((got[:, a:a + 60].double() - want).abs() <= 23 * size * (group / 16 * 17 * 2.0 ** -23 + (group + 8) * 2.0 ** -24 + (k // group + 68) * 2.0 ** -24))
+    lib.la_gemm_status()
