@@ -591,17 +591,19 @@ __global__ void __launch_bounds__(kTileThreads, 2) k_w4_tiles(const __grid_const
                 if (PER > 1 && (c0 + i) * PER + u > last) break;   // the matrix ends inside the chunk
                 uint32_t v[16];
                 tmem_ld_32x32b_x16(d + 16 * u, v);
-                tmem_ld_wait();
-#pragma unroll
-                for (int n = 0; n < 16; ++n) asm volatile("" : "+r"(v[n]));
                 const uint64_t f2 = w4_two(fs[u], fs[u]);
+                uint64_t both[4 * NT];   // powers times scale, while the sums are on their way
 #pragma unroll
                 for (int n = 0; n < 2 * NT; ++n) {
                     const ulonglong2 e = reinterpret_cast<const ulonglong2 *>(table + u * 64)[n];
-                    const uint64_t x = w4_two(__uint_as_float(v[4 * n]), __uint_as_float(v[4 * n + 1])), y = w4_two(__uint_as_float(v[4 * n + 2]), __uint_as_float(v[4 * n + 3]));
-                    sums[2 * n] = w4_fma2(x, w4_mul2(e.x, f2), sums[2 * n]);
-                    sums[2 * n + 1] = w4_fma2(y, w4_mul2(e.y, f2), sums[2 * n + 1]);
+                    both[2 * n] = w4_mul2(e.x, f2);
+                    both[2 * n + 1] = w4_mul2(e.y, f2);
                 }
+                tmem_ld_wait();
+#pragma unroll
+                for (int n = 0; n < 16; ++n) asm volatile("" : "+r"(v[n]));
+#pragma unroll
+                for (int n = 0; n < 4 * NT; ++n) sums[n] = w4_fma2(w4_two(__uint_as_float(v[2 * n]), __uint_as_float(v[2 * n + 1])), both[n], sums[n]);
             }
             tc_fence_before();
             __syncwarp();
