@@ -4,7 +4,7 @@
 // Bound by the matrix's bytes: every byte is read once and meets up to 16
 // vectors.  What the bytes cost are the instructions that unpack them, so there
 // are few: a 32-bit word, 8 weights, is one shift and four times a mask with the
-// bits of fp16's 1024 put in, so that nibbles i and i + 4 are a pair 1024 + q, or
+// bits of fp16's 1024 put in (the known way to make small whole numbers floating), so that nibbles i and i + 4 are a pair 1024 + q, or
 // 1024 + 16 q where the nibble lies higher; one packed operation each makes it
 // q - 8, exactly.  (Without that one, with q as a subnormal number and -8 times the
 // sum of x added, products took 0.4 us less in 25 but were off by 3.6e-6 of the result's
@@ -30,9 +30,9 @@
 // that does not fit, k_w4_operands makes it once for k_w4_tiles.
 //
 // Measured, groups of 128: 1 vector of 4096 x 4096 5.8 us (8.7 MB, latency), of 8192 x 28672
-// 24.9 us (119 MB at 4.8 TB/s; loads alone take 22.8 to 24), 16 vectors 31.0 us (4.0 TB/s:
-// the ALU pipe and the waits between a chunk's roles); 5 vectors of 13824 x 5120, groups of 64,
-// 13.8 us (2.8 TB/s, latency).
+// 24.9 us (119 MB at 4.8 TB/s; loads alone take 22.8 to 24), 16 vectors 31.0 us (4.0 TB/s),
+// 121 vectors, for which k_w4_tiles reads it eight times, 197 us; 5 vectors of 13824 x 5120,
+// groups of 64, 13.8 us (2.8 TB/s, latency).
 #include <algorithm>
 #include <atomic>
 #include <cstdio>
@@ -422,6 +422,10 @@ __global__ void __launch_bounds__(128) k_w4_operands(const __grid_constant__ W4A
 //   the group's scale and the vectors' powers.
 // mma.sync would need a fifth of the instructions more, and its operand's loads
 // fill the shared memory's bandwidth at 16 vectors.
+// A block's 55 thousand cycles for 16 vectors of 8192 x 28672, groups of 128 (two blocks on an SM): 4
+// until the first bytes, 44 in the loop, and 7 until the cluster's last block is through and its sums are
+// joined.  A group of warps has 28 chunks, each 1550 cycles: unpacking 460, the product 620 and the sums 235, one
+// behind another, the next bytes 135, 100 between them.  256 blocks have 148 SMs, 40 of them one alone.
 constexpr int kTileStages = 7, kTileStage = 13 * 1024;   // weights 8 KB, chunk
 constexpr int kTileThreads = 320;
 constexpr int kTileBars = kTileStages * kTileStage, kTileSmem = kTileBars + 256;

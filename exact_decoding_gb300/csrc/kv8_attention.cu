@@ -9,7 +9,7 @@
 //   O = sum_j w_j V8_j,      o = O 2^d / L.
 // r follows the maximum of z lazily (z_j - r <= kLazy), d follows vx so that u
 // stays within kUnitLow .. kUnitHigh: weights are at most 2^15, and those
-// below 2^-14 are off by 2^-25 at most, 2^(-25 - kUnitLow) of the largest key's
+// below 2^-14 are off by 2^-25 at most, 2^(-24 - kUnitLow) of the largest key's
 // weight, whatever scales other pages have.  Were one number (a maximum of
 // z + vx) to follow both, a page of large scale would leave no bits of the
 // others, even where it has no weight.
@@ -103,8 +103,8 @@ struct Kv8Seq {
 //
 // Windows measured (floor: the window's bytes, or its products): the last 4096 of
 // 65413 tokens and 4 first ones, 64 heads over 8 KV heads, 13.5 us (8.4 MB, latency); 64
-// sequences of up to 8192, window 1024, 32.8 us (130 MB: 4.0 TB/s); 121 rows of 32
-// heads, window 512, 32.3 us; 256 rows over 16k tokens, window 4096, 63.9 us
+// sequences of up to 8192, window 1024, 32.9 us (130 MB: 3.9 TB/s); 121 rows of 32
+// heads, window 512, 32.2 us; 256 rows over 16k tokens, window 4096, 63.9 us
 // (115.7 without).  What a short unit costs beside its tiles bounds them: positions,
 // pages and queries are looked up one behind another before the first product.
 template <bool WIN>
@@ -890,10 +890,11 @@ __global__ void __launch_bounds__(32 * Rows<HD, PAGE>::warps, Rows<HD, PAGE>::pe
 // k_kv8_few: k_kv8_rows for 8 query vectors, with the operands changed over: keys
 // are the rows of the first product (S^T = K Q^T, 16 keys x 8 vectors) and dims those of
 // the second (O^T = V^T P^T), so none of a product's rows is empty, and the scores and O
-// take half the registers.  That makes room for 12 warps on an SM, and for more of
+// take half the registers.  That makes room for six warps in a block and 12 on an SM (with
+// head_dim 128 and pages of 128 their rings leave room for one block), and for more of
 // a unit's tiles at a time: short units are bound by what a tile takes one warp (about
 // 2 us, most of it waiting for the instruction before).  Windows of 1024 and 4 first tokens, 64
-// sequences, 64 heads over 8 KV heads, pages of 64: 32.8 us, k_kv8_rows 38.6 (4 warps and
+// sequences, 64 heads over 8 KV heads, pages of 64: 32.9 us, k_kv8_rows 38.6 (4 warps and
 // three blocks of ring each 34.0, three CTAs of 4 warps 37.2); 32 of them with pages of 128 27.2 and 35.9; 48
 // sequences, head_dim 64, 12 heads over 4, window 700 11.1 and 16.3; one window of 4096 13.5 and
 // 14.1.  Without a window k_kv8_rows stays: its sums have another order.

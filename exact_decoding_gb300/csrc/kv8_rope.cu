@@ -15,14 +15,15 @@
 // both halves of a pair are one lane's, 16 bytes a load, and the norm is one
 // reduction over 4 or 8 lanes.
 //
-// Memory bounds a prompt: 6144 rows of 72 heads of 128, bf16 (151 MB): 29.8 us,
-// 5.1 TB/s, 75 % of a copy's rate.  What is left: a block finds positions and
+// Memory bounds a prompt: 4096 rows of 72 heads of 128, bf16 (151 MB): 30.2 us,
+// 5.0 TB/s, 74 % of a copy's rate (29.8 without the check of the mean); fp32 (226 MB)
+// 39.9 us, 84 %.  What is left: a block finds positions and
 // angles before its first load.  Hidden by other blocks of the SM, so registers
 // are held to 48 (five blocks; four 32.1 us, eight with spills 39.7) and a lane
 // has one head in flight (two: 30.7).  Up to 16 passes of heads a block (8:
 // 30.2, 4: 32.4) while that leaves four blocks for every SM.  Tables lie so that the lanes
 // of a head read 16 bytes side by side.  A single token (32 + 2 * 32 heads,
-// fp32): 3.6 us, latency.
+// fp32): 3.7 us, latency.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>

@@ -24,10 +24,11 @@
 // shared memory.  So there is one launch, no workspace, and results that do not depend
 // on any order.
 //
-// Measured: 2048 rows of 32000 fp32 (262 MB) with 20 alternatives 60.6 us, 4.3 TB/s,
-// 64 % of a copy's rate; bound by instructions (68 % of the issue slots; without
-// alternatives 41.8 us, 93 %).  76 rows of 32016 bf16 with 20 alternatives 9.6 us, one
-// row of 32000 with 5 6.8 us: latency of a pass, the search for the threshold and the joins.
+// Measured: 2048 rows of 32000 fp32 (262 MB) with 20 alternatives 60.4 us, 4.3 TB/s,
+// 64 % of a copy's rate; bound by instructions (71 % of the issue slots; without
+// alternatives 41.6 us, 93 %).  76 rows of 32016 bf16 with 20 alternatives 9.4 us, where most
+// logits are masked 9.7; one row of 32000 with 5 6.7 us: latency of a pass, the search for the
+// threshold and the joins.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -462,8 +463,8 @@ static cudaError_t logprobs_start(const la_logprobs_args &a, int nsm, cudaStream
     LpArgs p{};
     p.a = a;
     // Blocks of a row: while the rows leave SMs idle and each has a pass of its own, or, two
-    // on an SM, 3.5 passes (76 rows of 32016: 2 blocks 9.4 us, 4 11.1; 152 of 32000: 1
-    // 14.0, 2 11.5; 100 of 128000: 1 34.7, 2 23.6).
+    // on an SM, 3.5 passes (bf16, 20 alternatives, 76 rows of 32016: 1 block 13.3 us, 2 9.4, 4 11.3;
+    // 152 of 32000: 1 13.6, 2 11.1, 4 16.2; 100 of 128000: 1 35.0, 2 23.3, 4 21.9).
     p.blocks = 1;
     while (p.blocks < 8 && a.vocab > p.blocks * pass && static_cast<long long>(a.rows) * p.blocks * 2 <= (a.vocab / 7 >= p.blocks * pass ? 2 * nsm : nsm)) p.blocks *= 2;
     cudaLaunchConfig_t cfg = {};

@@ -475,9 +475,9 @@ int la_kv8_workspace(const la_kv8_cache *c, int64_t *bytes);
  * where the keys are the lens[s] cached tokens of its sequence and its visible
  * new rows.  Sums and the softmax are fp32; the products' operands are fp16
  * with power-of-two factors: e4m3 values are exact in them, q and new rows to
- * 2^-23 of their largest value, the softmax weights are rounded to 11 bits or
- * to 2^-19 of the row's largest weight, whatever the sizes of the values that
- * they meet.  (New rows that lie within 128 of one another and differ by more
+ * 2^-23 of their largest value (or to 2^-85, where that is more), the softmax
+ * weights are rounded to 11 bits or to 2^-19 of the row's largest weight,
+ * whatever the sizes of the values that they meet.  (New rows that lie within 128 of one another and differ by more
  * than 2^16 in size: to 2^-24 of the largest product of a weight and a value that
  * the row sees.)  Sums past fp32's range become infinite; out is rounded once to
  * bf16.  A row that sees nothing gives 0.  Values of keys that a row does not see, and
@@ -533,10 +533,11 @@ typedef struct la_kv8_qkv {
 /* For each head x of q and of k: n = x / sqrt(mean(x^2) + eps) * weight (n = x
  * without a weight), then the rotation of the pairs (i, i + head_dim / 2) by
  * position * inv_freq[i]; v is only rounded.  All in fp32, rounded once to
- * bf16; the rotation's angles are within 2^-26 of a turn up to position
- * 2^20, and within 2^-23 at every position.  Of the cache it reads the sizes,
- * lens and status alone, before the rows are appended.  Asynchronous, without
- * a workspace.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+ * bf16; for frequencies up to 1 (rope_base 1 or more) the rotation's angles are
+ * within 2^-26 of a turn up to position 2^20 and within 2^-23 at every position
+ * (above 1: times the frequency).  Of the cache it reads the sizes, lens and
+ * status alone, before the rows are appended.  Asynchronous, without a
+ * workspace.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int la_kv8_norm_rope(const la_kv8_cache *c, const la_kv8_qkv *a, void *stream);
 
 /* Rows to append, all layers at once. */
