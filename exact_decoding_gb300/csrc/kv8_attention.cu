@@ -2765,7 +2765,8 @@ static cudaError_t rows_launch(Kv8Args &p, int nsm, void *ws, cudaStream_t s) {
     // tiles 17.7 against 19.7, 32 tiles 24.4 against 22.5; 48 sequences, head_dim
     // 64, 4 KV heads, pages of 32, 16 tiles 10.7 against 13.5, 47 tiles 19.6
     // against 16.4.
-    // k_kv8_few counts tokens: its six warps take pages of any size at about the same rate.
+    // k_kv8_few counts tokens, as its six warps take pages of any size at about the same rate:
+    // units of up to 2304 stay whole where that costs less than 896 tokens' time.
     // Whole against split, windows of 512, 1024 and 2048: one row of 64 heads over 8 KV heads, pages
     // of 64 8.9, 11.3, 16.4 against 11.1, 11.4, 11.6, pages of 128 9.2, 11.7, 15.7 against 12.0, 12.1,
     // 12.5; of 32 heads over 4, pages of 32 9.3, 13.1, 20.8 against 10.5, 11.2, 11.5; 16 sequences, pages of

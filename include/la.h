@@ -326,10 +326,10 @@ int la_gemm_bf16_noalloc(const void *x, const void *w, float *y, int32_t rows, i
  * matrix is read once for every 16 rows, so it is for a batch of single tokens.
  * x is exact to 2^-39 of the largest value of its group (of one row), the
  * products' sums are fp32, and a group's sum meets its scale once; results are
- * deterministic.  They are finite where x is and the results, and each group's
- * largest x times its scale, are within fp32's range (where that product is
- * below 2^-127 a group loses bits).  A row with a value that is not finite is
- * not finite at all.
+ * deterministic.  Finite values give finite results where the results, and each
+ * group's largest x times its scale, are within fp32's range (a group where that
+ * product is below 2^-127 loses bits).  A row with a value that is not finite
+ * is not finite at all.
  * Calls of many rows need a workspace: la_gemv_w4_workspace says how many bytes
  * on the current device (0: none), 16-byte aligned device memory with any
  * contents; calls that overlap need one each.  Asynchronous: a bounded wait that
@@ -477,9 +477,9 @@ int la_kv8_workspace(const la_kv8_cache *c, int64_t *bytes);
  * with power-of-two factors: e4m3 values are exact in them, q and new rows to
  * 2^-23 of their largest value (or to 2^-85, where that is more), the softmax
  * weights are rounded to 11 bits or to 2^-19 of the row's largest weight,
- * whatever the sizes of the values that they meet.  (New rows that lie within 128 of one another and differ by more
- * than 2^16 in size: to 2^-24 of the largest product of a weight and a value that
- * the row sees.)  Sums past fp32's range become infinite; out is rounded once to
+ * whatever the sizes of the values that they meet.  (New rows that lie within
+ * 128 of one another and differ by more than 2^16 in size: to 2^-24 of the
+ * largest product of a weight and a value that the row sees.)  Sums past fp32's range become infinite; out is rounded once to
  * bf16.  A row that sees nothing gives 0.  Values of keys that a row does not see, and
  * bytes behind a sequence's last token, never reach it, NaN and infinities
  * included.  Results do not depend on other sequences' contents but may
